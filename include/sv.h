@@ -84,7 +84,13 @@ enum {
   SV_DEV_BAD_ALPHA = 1u << 5,       /* confidence outside [0, 1] or NaN              */
   SV_DEV_BAD_DRAFT_LEN = 1u << 6,   /* draft_len outside [0, Dmax]                   */
   SV_DEV_TIMEOUT = 1u << 7,         /* a bounded wait inside a kernel ran out        */
-  SV_DEV_BAD_PARENT = 1u << 8       /* tree node whose parent is not an earlier node */
+  SV_DEV_BAD_PARENT = 1u << 8,      /* tree node whose parent is not an earlier node */
+  SV_DEV_BAD_LOGIT = 1u << 9,       /* sampling: a row with a NaN or +inf logit      */
+  SV_DEV_BAD_FILTER = 1u << 10,     /* sampling: top_k, top_p, min_p or a uniform out of range */
+  SV_DEV_BAD_PAGE = 1u << 11,       /* cache: a needed page_table entry names no page, or a page was given back too often */
+  SV_DEV_OUT_OF_PAGES = 1u << 12,   /* cache: the pool has too few free pages        */
+  SV_DEV_BAD_SEQ = 1u << 13,        /* cache: length, row number or path out of range */
+  SV_DEV_BAD_NODES = 1u << 14       /* attention / cache: node_offsets out of range  */
 };
 
 /* per-request bits of out_flags */
@@ -366,6 +372,155 @@ sv_status sv_verify_sample_noalloc(const void* target, int64_t t_row_stride, con
                                    int32_t* out_tokens, int32_t* out_accept_len, float* out_p,
                                    float* out_q, uint8_t* out_flags, void* stream);
 
+/*
+ * Operators of the round around verification: drawing drafted tokens, a paged key/value cache
+ * and the attention of a token tree over it.  ([release] "Why one universal drafter
+ * underperforms": the drafter proposes, one target pass verifies; [explainer] "D-cut", Figure 3.)
+ * A round: sv_cache_reserve, per layer sv_cache_append and sv_tree_attention, sv_verify_tree,
+ * sv_cache_commit of the accepted path; the drafter's tokens come from sv_sample_rows.
+ */
+
+/*
+ * sv_sample_rows -- draws tokens from logit rows with temperature, top-k, top-p and min-p, from
+ * given uniforms, and can write the rows with every token that cannot be drawn set to -inf.
+ * Verification is lossless for the distribution of the rows that it is given: a drafter that
+ * samples from cut rows passes the cut rows (out_rows) to sv_verify_*, and a target with a cut
+ * distribution has its rows cut first.
+ *
+ * Row r (0 <= r < R): V logits x_v at logits + r * row_stride, T = temperature[r], k = top_k[r],
+ * p = top_p[r], q = min_p[r] (device arrays; a NULL array switches its filter off, and so do
+ * k = 0, p = 1, q = 0), M uniforms u_j = uniforms[r * M + j] in [0, 1).
+ *   m = max x;  s = log2(e) / T;  y_v = (x_v - m) s  (each float32 operation rounded once)
+ *   w_v = 2^y_v rounded to a multiple of 2^-40, held as the integer w_v 2^40: every sum below is
+ *         exact, so no result depends on the order of additions
+ *   kept tokens, in the order (x desc, index asc), logits of -inf never:
+ *     top-k: the first k;  top-p: those with (weights before them) < max(1, floor(p W)), W the
+ *     top-k's weights (p rounded to a multiple of 2^-24);  min-p: y_v >= log2(q)
+ *   draw j: t = floor(u_j Z), Z the kept weights (u_j cut to a multiple of 2^-24); the first kept v
+ *   in vocabulary order whose running sum of kept weights exceeds t
+ * T == 0: the first argmax, probability 1, whatever the filters and uniforms.
+ * Outputs: out_tokens [R, M] int32; out_probs [R, M] float32 (nullable): w_v / Z;  out_rows
+ * (nullable, dtype dt, row stride out_stride >= V; may equal logits with its stride): x_v where kept, else
+ * -inf.  A row of nothing but -inf gives tokens -1 and probabilities 0.  A row with a NaN or +inf
+ * logit (SV_DEV_BAD_LOGIT), a bad temperature (SV_DEV_BAD_TEMPERATURE) or a filter or uniform out of range
+ * (k < 0, p outside (0, 1], q outside [0, 1], SV_DEV_BAD_FILTER) gives tokens -1, probabilities
+ * NaN and a row of -inf.
+ * Limits: 0 <= R <= SV_MAX_SAMPLE_ROWS, 1 <= V <= SV_MAX_SAMPLE_VOCAB, 0 <= M <= SV_MAX_SAMPLE_DRAWS.
+ * R == 0 is a no-op.  Workspace: SV_STATUS_BYTES, zero-filled before the first use (the status word).
+ */
+#define SV_STATUS_BYTES 256
+#define SV_MAX_SAMPLE_ROWS (1 << 20)
+#define SV_MAX_SAMPLE_VOCAB (1 << 18)
+#define SV_MAX_SAMPLE_DRAWS 1024
+sv_status sv_sample_rows(const void* logits, int64_t row_stride, sv_dtype dt, int R, int V, const float* temperature,
+                         const int32_t* top_k, const float* top_p, const float* min_p, const float* uniforms, int M,
+                         int32_t* out_tokens, float* out_probs, void* out_rows, int64_t out_stride, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
+ * A paged key/value cache.  k and v are pools of bf16 elements: layer l, page g, slot s, key/value
+ * head h, dimension d lies at l * layer_stride + g * page_stride + s * slot_stride + h * head_stride + d
+ * (elements, the same for both pools; strides multiples of 8, bases 16-byte aligned).  A sequence is a
+ * row of page_table ([rows, table_width] int32, row stride table_width): entry e names the page of its
+ * slots [e page_size, (e + 1) page_size), -1 = none.  The entries that a row holds come first.
+ * page_refs [pages] int32 counts the rows that hold a page; a page with count 0 is free.  Slots of held pages that lie
+ * past a sequence's length may hold anything, NaN included.
+ * Limits: page_size a power of two in [8, 1024], head_dim 64 or 128, 1 <= kv_heads <= 1024, 1 <= pages <= SV_MAX_PAGES,
+ * table_width <= SV_MAX_TABLE_WIDTH, rows (B, n) <= SV_MAX_BATCH.
+ * The struct is read during the call only.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t layer_stride, page_stride, slot_stride, head_stride;
+  int32_t layers, pages, page_size, kv_heads, head_dim;
+  int32_t* page_refs;
+} sv_cache;
+#define SV_MAX_PAGES (1 << 22)
+#define SV_MAX_TABLE_WIDTH (1 << 20)
+/* Workspace of the sv_cache_* calls (zero-filled once before its first use). */
+#define SV_CACHE_WORKSPACE_BYTES (SV_STATUS_BYTES + 8 * SV_MAX_BATCH)
+
+/*
+ * sv_cache_reserve -- pages for slots [0, seq_len[i] + extra[i]) of each row i < B.  Entries that
+ * the row lacks get the lowest-numbered free pages, rows in order, entries in order.  Row i is
+ * served iff the pages that rows 0..i lack are no more than the free pages (else it gets none,
+ * out_ok[i] = 0 and SV_DEV_OUT_OF_PAGES).  out_ok [B] (nullable).  A negative length or extra, or more
+ * slots than table_width pages hold: out_ok[i] = 0, SV_DEV_BAD_SEQ.
+ */
+sv_status sv_cache_reserve(const sv_cache* c, int32_t* page_table, int table_width, const int32_t* seq_len,
+                           const int32_t* extra, int B, int32_t* out_ok, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * sv_cache_append -- writes new keys and values of `layers` layers from `layer` on: request i's
+ * node c (row node_offsets[i] + c, 0 <= c < N_i = node_offsets[i+1] - node_offsets[i]) to slot
+ * seq_len[i] + c.  k_new / v_new: bf16 [layers, n_rows, kv_heads, head_dim] with new_layer_stride and
+ * new_row_stride (elements, multiples of 8; the last two dimensions contiguous; 16-byte aligned
+ * bases).  node_offsets [B+1] device int32.  A row whose slot has no page is
+ * left out (SV_DEV_BAD_PAGE), a request whose rows do not lie in [0, n_rows) too (SV_DEV_BAD_NODES).
+ */
+sv_status sv_cache_append(const sv_cache* c, int layer, int layers, const int32_t* page_table, int table_width,
+                          const int32_t* seq_len, const int32_t* node_offsets, int64_t n_rows, const void* k_new,
+                          const void* v_new, int64_t new_layer_stride, int64_t new_row_stride, int B, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * sv_cache_commit -- after sv_verify_tree: keeps the accepted path and gives back the rest.  Request
+ * i's node path[i * Nmax + j] (0 <= j < a = accept_len[i]; nodes strictly increasing in [1, N_i), N_i from
+ * node_offsets [B+1]) moves from slot seq_len[i] + path to slot seq_len[i] + 1 + j in every layer; node 0 stays at slot
+ * seq_len[i].  out_len[i] = seq_len[i] + 1 + a; a < 0 (a request that verification rejected as invalid) or N_i = 0 with
+ * a <= 0 (no tree this round): seq_len[i].
+ * Pages past ceil(out_len / page_size) leave the row.  out_len may be seq_len.  A bad path or length: nothing
+ * moves, no page is given back, out_len[i] = seq_len[i], SV_DEV_BAD_SEQ; a slot without a page: SV_DEV_BAD_PAGE, that node
+ * does not move.  Tail pages that another row shares stay with it.
+ */
+sv_status sv_cache_commit(const sv_cache* c, int32_t* page_table, int table_width, const int32_t* seq_len,
+                          const int32_t* node_offsets, const int32_t* path, const int32_t* accept_len, int B, int Nmax,
+                          int32_t* out_len, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * sv_cache_fork -- row dst[j] becomes a copy of row src[j] (0 <= j < n): it shares the full pages and
+ * gets the lowest free page (pairs in order) for the partly filled last one, whose used slots are copied in every
+ * layer; seq_len[dst] = seq_len[src].  Lengths are read before any is written.  rows = rows of
+ * page_table and seq_len.  dst rows must be empty and differ from each other (else SV_DEV_BAD_SEQ and out_ok[j] = 0); a
+ * pair for which no page is left stays undone (SV_DEV_OUT_OF_PAGES, out_ok[j] = 0).  out_ok [n] nullable.
+ */
+sv_status sv_cache_fork(const sv_cache* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
+                        const int32_t* src, const int32_t* dst, int n, int32_t* out_ok, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* sv_cache_release -- gives the pages of rows seqs[0..n) back and empties them (seq_len = 0). */
+sv_status sv_cache_release(const sv_cache* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
+                           const int32_t* seqs, int n, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * sv_tree_attention -- attention of every request's token tree over its cached sequence, one layer.
+ *
+ * Request i has L_i = seq_len[i] cached slots and N_i = node_offsets[i+1] - node_offsets[i] nodes
+ * (0 <= N_i <= Nmax), whose keys and values lie at slots L_i + c (sv_cache_append).  parent[node_offsets[i]
+ * + c] is node c's parent, 0 <= parent < c (the entry of node 0 is not read); parent NULL = every tree
+ * is a chain.  Node c sees slots [0, L_i) and the slots of its ancestors and itself.  A cached slot
+ * s has position s, node a has L_i + depth(a).  window > 0: node c sees only positions < sinks or >
+ * L_i + depth(c) - window.
+ *   o[c, h] = sum_s softmax_s(scale q[c, h] . k[s, g]) v[s, g],  g = h / (q_heads / kv_heads)
+ *   lse[c, h] = log sum_s exp(scale q[c, h] . k[s, g])
+ * q, out: bf16, row node_offsets[i] + c at row * row_stride + h * head_stride (elements; q strides multiples of 8
+ * and q 16-byte aligned; out strides multiples of 8 and out 16-byte aligned); n_rows rows.  out_lse (nullable): float32
+ * [n_rows, q_heads].  q_heads a multiple of kv_heads.  Products of bf16 are summed in float32; softmax weights are rounded to bf16
+ * for the product with v, their sum is not.
+ * The keys and values of visible slots must be finite; slots of other requests, past the tree or outside
+ * every node's window may hold anything.  A request whose rows do not lie in [0, n_rows), with N_i
+ * outside [0, Nmax] or L_i < 0 or L_i + N_i slots beyond its row (SV_DEV_BAD_NODES / SV_DEV_BAD_SEQ) or a visible slot without a page
+ * (SV_DEV_BAD_PAGE) or a bad parent (SV_DEV_BAD_PARENT): outputs 0, lse -inf for its rows in [0, n_rows).
+ * Workspace: sv_attention_workspace_size(c, q_heads), zero-filled once before its first use.
+ */
+size_t sv_attention_workspace_size(const sv_cache* c, int q_heads);
+sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            int q_heads, const int32_t* page_table, int table_width, const int32_t* seq_len,
+                            const int32_t* node_offsets, int64_t n_rows, const int32_t* parent, int B, int Nmax,
+                            float scale, int window, int sinks, void* out, int64_t out_row_stride,
+                            int64_t out_head_stride, float* out_lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Testing hook for the bounded waits.  The next verification call (any entry
  * point, on any thread) runs with every wait of its streaming kernel limited to
  * wait_limit_ms (instead of about 2 s), and the producer of that kernel's first
@@ -402,10 +557,18 @@ enum {
   SV_KERNEL_MASS = 3,      /* per-chunk draw weights for long requests                    */
   SV_KERNEL_PICK = 4,      /* inverse-CDF draw                                            */
   SV_KERNEL_TREE_WALK = 5, /* tree verification: the walk from the root                   */
-  SV_NUM_KERNELS = 6
+  SV_NUM_KERNELS = 6,      /* the kernels that sv_profile_collect reports                 */
+  SV_KERNEL_SAMPLE = 6,    /* sv_sample_rows                                              */
+  SV_KERNEL_CACHE_PAGES = 7, /* page bookkeeping of the cache calls                       */
+  SV_KERNEL_CACHE_ROWS = 8,  /* key/value rows written, moved or copied                   */
+  SV_KERNEL_ATTENTION = 9,   /* tree attention: tiles of the cache                        */
+  SV_KERNEL_ATTENTION_JOIN = 10, /* tree attention: partial results joined                */
+  SV_NUM_KERNEL_IDS = 11
 };
 void sv_profile_enable(int on);
 sv_status sv_profile_collect(double* total_ms, int64_t* launches);
+/* The same for the kernel ids [0, n), n <= SV_NUM_KERNEL_IDS (arrays of n). */
+sv_status sv_profile_collect_ids(double* total_ms, int64_t* launches, int n);
 void sv_profile_reset(void);
 int64_t sv_launch_count(void);
 

@@ -8,8 +8,8 @@ every call raises.
 
 The ``sv_*`` functions mirror the C ABI in ``include/sv.h`` one to one (tensors in place of
 pointers, ``None`` for NULL).  The lower-case helpers (``verify_greedy``, ``verify_sample``,
-``verify_ragged``, ``schedule_depth``) derive sizes and strides from the tensors and allocate
-outputs and workspaces.
+``verify_ragged``, ``verify_tree``, ``schedule_depth``, ``sample``, ``tree_attention``) and ``PagedCache``
+derive sizes and strides from the tensors and allocate outputs and workspaces.
 """
 from __future__ import annotations
 
@@ -29,11 +29,18 @@ SV_OP_VERIFY, SV_OP_SCHEDULE, SV_OP_TREE = 0, 1, 2
 SV_OBJ_THROUGHPUT, SV_OBJ_NET = 0, 1
 SV_PHASE_STATS, SV_PHASE_ACCEPT, SV_PHASE_WEIGHTS, SV_PHASE_PICK = range(4)
 (SV_DEV_BAD_TOKEN, SV_DEV_BAD_TEMPERATURE, SV_DEV_BAD_KEEP_LEN, SV_DEV_BAD_OFFSETS, SV_DEV_NO_DRAFT_ROWS,
- SV_DEV_BAD_ALPHA, SV_DEV_BAD_DRAFT_LEN, SV_DEV_TIMEOUT, SV_DEV_BAD_PARENT) = (1 << b for b in range(9))
+ SV_DEV_BAD_ALPHA, SV_DEV_BAD_DRAFT_LEN, SV_DEV_TIMEOUT, SV_DEV_BAD_PARENT, SV_DEV_BAD_LOGIT, SV_DEV_BAD_FILTER,
+ SV_DEV_BAD_PAGE, SV_DEV_OUT_OF_PAGES, SV_DEV_BAD_SEQ, SV_DEV_BAD_NODES) = (1 << b for b in range(15))
+SV_STATUS_BYTES, SV_MAX_BATCH = 256, 4096
+SV_CACHE_WORKSPACE_BYTES = SV_STATUS_BYTES + 8 * SV_MAX_BATCH
 SV_FLAG_Q_ZERO, SV_FLAG_Z_ZERO, SV_FLAG_INVALID = 1, 2, 4
 (SV_KERNEL_ROW_STATS, SV_KERNEL_COMBINE, SV_KERNEL_SCHEDULE, SV_KERNEL_MASS, SV_KERNEL_PICK, SV_KERNEL_TREE_WALK,
  SV_NUM_KERNELS) = range(7)
 KERNEL_NAMES = ("row_stats", "combine", "schedule", "mass", "pick", "tree_walk")
+# kernels of the round's other operators (sv_profile_collect_ids reports them too)
+(SV_KERNEL_SAMPLE, SV_KERNEL_CACHE_PAGES, SV_KERNEL_CACHE_ROWS, SV_KERNEL_ATTENTION, SV_KERNEL_ATTENTION_JOIN,
+ SV_NUM_KERNEL_IDS) = range(6, 12)
+OPERATOR_KERNEL_NAMES = KERNEL_NAMES + ("sample", "cache_pages", "cache_rows", "attention", "attention_join")
 
 _c = ctypes
 _vp, _i32, _i64, _u32, _u64, _f32, _sz = (_c.c_void_p, _c.c_int32, _c.c_int64, _c.c_uint32, _c.c_uint64,
@@ -64,17 +71,36 @@ _SIGS = {
     "sv_verify_sample_phase": (_c.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _u64, _u32, _vp, _c.c_int, _c.c_int,
                                           _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _vp, _vp, _vp, _vp,
                                           _vp, _vp, _sz, _vp]),
+    "sv_sample_rows": (_c.c_int, [_vp, _i64, _c.c_int, _c.c_int, _c.c_int, _vp, _vp, _vp, _vp, _vp, _c.c_int, _vp, _vp,
+                                  _vp, _i64, _vp, _sz, _vp]),
+    "sv_cache_reserve": (_c.c_int, [_vp, _vp, _c.c_int, _vp, _vp, _c.c_int, _vp, _vp, _sz, _vp]),
+    "sv_cache_append": (_c.c_int, [_vp, _c.c_int, _c.c_int, _vp, _c.c_int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _c.c_int,
+                                   _vp, _sz, _vp]),
+    "sv_cache_commit": (_c.c_int, [_vp, _vp, _c.c_int, _vp, _vp, _vp, _vp, _c.c_int, _c.c_int, _vp, _vp, _sz, _vp]),
+    "sv_cache_fork": (_c.c_int, [_vp, _vp, _c.c_int, _c.c_int, _vp, _vp, _vp, _c.c_int, _vp, _vp, _sz, _vp]),
+    "sv_cache_release": (_c.c_int, [_vp, _vp, _c.c_int, _c.c_int, _vp, _vp, _c.c_int, _vp, _sz, _vp]),
+    "sv_attention_workspace_size": (_sz, [_vp, _c.c_int]),
+    "sv_tree_attention": (_c.c_int, [_vp, _c.c_int, _vp, _i64, _i64, _c.c_int, _vp, _c.c_int, _vp, _vp, _i64, _vp, _c.c_int,
+                                     _c.c_int, _f32, _c.c_int, _c.c_int, _vp, _i64, _i64, _vp, _vp, _sz, _vp]),
     "sv_test_stall_next_verify": (None, [_c.c_int]),
     "sv_query_status": (_c.c_int, [_vp, _vp, _c.POINTER(_u32)]),
     "sv_status_string": (_c.c_char_p, [_c.c_int]),
     "sv_last_error_string": (_c.c_char_p, []),
     "sv_profile_enable": (None, [_c.c_int]),
     "sv_profile_collect": (_c.c_int, [_c.POINTER(_c.c_double), _c.POINTER(_i64)]),
+    "sv_profile_collect_ids": (_c.c_int, [_c.POINTER(_c.c_double), _c.POINTER(_i64), _c.c_int]),
     "sv_profile_reset": (None, []),
     "sv_launch_count": (_i64, []),
 }
 
 _lib = None
+
+
+class sv_cache(_c.Structure):
+    """The C struct of the same name: a paged key/value cache (see include/sv.h)."""
+    _fields_ = [("k", _vp), ("v", _vp), ("layer_stride", _i64), ("page_stride", _i64), ("slot_stride", _i64),
+                ("head_stride", _i64), ("layers", _i32), ("pages", _i32), ("page_size", _i32), ("kv_heads", _i32),
+                ("head_dim", _i32), ("page_refs", _vp)]
 
 
 class SVError(RuntimeError):
@@ -359,6 +385,97 @@ def sv_verify_sample_phase(target, t_row_stride, draft, d_row_stride, draft_toke
                                         _p(out_q), _p(out_flags), _p(ws), _ws_bytes(ws), _stream(stream)))
 
 
+def sv_sample_rows(logits, row_stride, dt, R, V, temperature, top_k, top_p, min_p, uniforms, M, out_tokens, out_probs,
+                   out_rows, out_stride, ws, stream=None) -> None:
+    if R > 0:
+        _need_rows(logits, "logits", dt, R, row_stride, V)
+        _need(temperature, "temperature", torch.float32, R)
+        _need(top_k, "top_k", torch.int32, R)
+        _need(top_p, "top_p", torch.float32, R)
+        _need(min_p, "min_p", torch.float32, R)
+        _need(uniforms, "uniforms", torch.float32, R * M)
+        _need(out_tokens, "out_tokens", torch.int32, R * M)
+        _need(out_probs, "out_probs", torch.float32, R * M)
+        _need_rows(out_rows, "out_rows", dt, R, out_stride, V)
+    _check(lib().sv_sample_rows(_p(logits), row_stride, dt, R, V, _p(temperature), _p(top_k), _p(top_p), _p(min_p),
+                                _p(uniforms), M, _p(out_tokens), _p(out_probs), _p(out_rows), out_stride, _p(ws),
+                                _ws_bytes(ws), _stream(stream)))
+
+
+def _need_table(page_table, table_width: int, rows: int, **per_row) -> None:
+    _need(page_table, "page_table", torch.int32, rows * table_width if table_width > 0 else 0)
+    for name, t in per_row.items():
+        _need(t, name, torch.int32, rows)
+
+
+def sv_cache_reserve(cache, page_table, table_width, seq_len, extra, B, out_ok, ws, stream=None) -> None:
+    if B > 0:
+        _need_table(page_table, table_width, B, seq_len=seq_len, extra=extra, out_ok=out_ok)
+    _check(lib().sv_cache_reserve(_c.addressof(cache), _p(page_table), table_width, _p(seq_len), _p(extra), B, _p(out_ok),
+                                  _p(ws), _ws_bytes(ws), _stream(stream)))
+
+
+def sv_cache_append(cache, layer, layers, page_table, table_width, seq_len, node_offsets, n_rows, k_new, v_new,
+                    new_layer_stride, new_row_stride, B, ws, stream=None) -> None:
+    if B > 0 and layers > 0 and n_rows > 0:
+        _need_table(page_table, table_width, B, seq_len=seq_len)
+        _need(node_offsets, "node_offsets", torch.int32, B + 1)
+        last = (layers - 1) * new_layer_stride + (n_rows - 1) * new_row_stride + cache.kv_heads * cache.head_dim
+        _need(k_new, "k_new", torch.bfloat16, last)
+        _need(v_new, "v_new", torch.bfloat16, last)
+    _check(lib().sv_cache_append(_c.addressof(cache), layer, layers, _p(page_table), table_width, _p(seq_len),
+                                 _p(node_offsets), n_rows, _p(k_new), _p(v_new), new_layer_stride, new_row_stride, B,
+                                 _p(ws), _ws_bytes(ws), _stream(stream)))
+
+
+def sv_cache_commit(cache, page_table, table_width, seq_len, node_offsets, path, accept_len, B, Nmax, out_len, ws,
+                    stream=None) -> None:
+    if B > 0:
+        _need_table(page_table, table_width, B, seq_len=seq_len, accept_len=accept_len, out_len=out_len)
+        _need(node_offsets, "node_offsets", torch.int32, B + 1)
+        _need(path, "path", torch.int32, B * Nmax)
+    _check(lib().sv_cache_commit(_c.addressof(cache), _p(page_table), table_width, _p(seq_len), _p(node_offsets), _p(path),
+                                 _p(accept_len), B, Nmax, _p(out_len), _p(ws), _ws_bytes(ws), _stream(stream)))
+
+
+def sv_cache_fork(cache, page_table, table_width, rows, seq_len, src, dst, n, out_ok, ws, stream=None) -> None:
+    if n > 0:
+        _need_table(page_table, table_width, rows, seq_len=seq_len)
+        _need(src, "src", torch.int32, n)
+        _need(dst, "dst", torch.int32, n)
+        _need(out_ok, "out_ok", torch.int32, n)
+    _check(lib().sv_cache_fork(_c.addressof(cache), _p(page_table), table_width, rows, _p(seq_len), _p(src), _p(dst), n,
+                               _p(out_ok), _p(ws), _ws_bytes(ws), _stream(stream)))
+
+
+def sv_cache_release(cache, page_table, table_width, rows, seq_len, seqs, n, ws, stream=None) -> None:
+    if n > 0:
+        _need_table(page_table, table_width, rows, seq_len=seq_len)
+        _need(seqs, "seqs", torch.int32, n)
+    _check(lib().sv_cache_release(_c.addressof(cache), _p(page_table), table_width, rows, _p(seq_len), _p(seqs), n, _p(ws),
+                                  _ws_bytes(ws), _stream(stream)))
+
+
+def sv_attention_workspace_size(cache, q_heads: int) -> int:
+    return int(lib().sv_attention_workspace_size(_c.addressof(cache), q_heads))
+
+
+def sv_tree_attention(cache, layer, q, q_row_stride, q_head_stride, q_heads, page_table, table_width, seq_len,
+                      node_offsets, n_rows, parent, B, Nmax, scale, window, sinks, out, out_row_stride,
+                      out_head_stride, out_lse, ws, stream=None) -> None:
+    if B > 0 and n_rows > 0:
+        _need_table(page_table, table_width, B, seq_len=seq_len)
+        _need(node_offsets, "node_offsets", torch.int32, B + 1)
+        _need(parent, "parent", torch.int32, n_rows)
+        _need(q, "q", torch.bfloat16, (n_rows - 1) * q_row_stride + (q_heads - 1) * q_head_stride + cache.head_dim)
+        _need(out, "out", torch.bfloat16, (n_rows - 1) * out_row_stride + (q_heads - 1) * out_head_stride + cache.head_dim)
+        _need(out_lse, "out_lse", torch.float32, n_rows * q_heads)
+    _check(lib().sv_tree_attention(_c.addressof(cache), layer, _p(q), q_row_stride, q_head_stride, q_heads,
+                                   _p(page_table), table_width, _p(seq_len), _p(node_offsets), n_rows, _p(parent), B,
+                                   Nmax, scale, window, sinks, _p(out), out_row_stride, out_head_stride, _p(out_lse),
+                                   _p(ws), _ws_bytes(ws), _stream(stream)))
+
+
 def sv_test_stall_next_verify(wait_limit_ms: int) -> None:
     lib().sv_test_stall_next_verify(int(wait_limit_ms))
 
@@ -380,6 +497,13 @@ def sv_profile_collect() -> tuple[list[float], list[int]]:
     n = (ctypes.c_int64 * SV_NUM_KERNELS)()
     _check(lib().sv_profile_collect(ms, n))
     return list(ms), list(n)
+
+
+def sv_profile_collect_ids(n: int = SV_NUM_KERNEL_IDS) -> tuple[list[float], list[int]]:
+    ms = (ctypes.c_double * n)()
+    launches = (ctypes.c_int64 * n)()
+    _check(lib().sv_profile_collect_ids(ms, launches, n))
+    return list(ms), list(launches)
 
 
 def sv_profile_reset() -> None:
@@ -513,3 +637,186 @@ def schedule_depth(alpha, cost_a, cost_b, budget, *, draft_len=None, ratios=None
         sv_schedule_depth(alpha, alpha.stride(0), draft_len, B, Dmax, cost_a, cost_b, budget, ratios, objective,
                           *out, ws, stream)
     return out
+
+
+# ------------------------------------------------------------------------------------------
+# the round around verification: sampling, the paged cache, tree attention
+# ------------------------------------------------------------------------------------------
+
+def _zeros(nbytes: int, device, stream) -> torch.Tensor:
+    """A zero-filled workspace whose fill is ordered before the call on `stream`."""
+    if stream is None:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def sample_workspace(rows: int, vocab: int, device="cuda") -> torch.Tensor:
+    """Workspace of sample() for that many rows (its first word is the device status word)."""
+    return torch.zeros(SV_STATUS_BYTES, dtype=torch.uint8, device=device)
+
+
+def sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None, probs=True, filtered=None, out=None,
+           ws=None, stream=None):
+    """Draws from rows of logits.  logits [R, V] (bf16 or float32; rows may be strided); temperature [R]
+    float32; uniforms [R, M] float32 in [0, 1); top_k [R] int32, top_p / min_p [R] float32 or None.  filtered: None,
+    True, or a tensor like logits (it may be logits itself) that receives the rows with everything that cannot be
+    drawn set to -inf: these are the rows to verify with.  Returns (tokens [R, M] int32, probs [R, M] float32 or None,
+    filtered or None); out = (tokens, probs) takes the place of new tensors."""
+    if logits.dim() != 2 or uniforms.dim() != 2 or uniforms.shape[0] != logits.shape[0]:
+        raise ValueError("sample() takes logits [R, V] and uniforms [R, M]")
+    if not uniforms.is_contiguous():
+        raise ValueError("uniforms must be contiguous")
+    R, V = logits.shape
+    M = uniforms.shape[1]
+    dt = _dt(logits)
+    dev = logits.device
+    if out is None:
+        out = (torch.empty((R, M), dtype=torch.int32, device=dev),
+               torch.empty((R, M), dtype=torch.float32, device=dev) if probs else None)
+    if filtered is True:
+        filtered = torch.empty((R, V), dtype=logits.dtype, device=dev)
+    if filtered is not None and filtered.shape != logits.shape:
+        raise ValueError("filtered must have the shape of logits")
+    if ws is None:
+        ws = _zeros(SV_STATUS_BYTES, dev, stream)
+    sv_sample_rows(logits, _rows(logits)[1] if R > 1 else V, dt, R, V, temperature, top_k, top_p, min_p, uniforms, M,
+                   out[0], out[1], filtered, V if filtered is None or R <= 1 else _rows(filtered)[1], ws, stream)
+    return out[0], out[1], filtered
+
+
+class PagedCache:
+    """A paged key/value cache on the device (the C struct sv_cache and the sequences' page table).
+
+    k, v        [layers, pages, page_size, kv_heads, head_dim] bf16, the same strides, the last
+                dimension contiguous (so [..., kv_heads, page_size, ...] pools come as transposed views)
+    page_refs   [pages] int32, how many sequences hold a page (0 = free)
+    page_table  [sequences, entries] int32, contiguous: a sequence's pages in order, then -1
+
+    The methods take the sequences' lengths as a device tensor; they work on the table's first B rows, B
+    from their arguments.  Everything stays on the device and on `stream`; errors that only the device sees go
+    to the status word of `ws` (sv_query_status(cache.ws)).  One cache belongs to one stream at a time.
+    """
+
+    def __init__(self, k, v, page_refs, page_table, ws=None):
+        if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be [layers, pages, page_size, kv_heads, head_dim] alike")
+        _need(k, "k", torch.bfloat16)
+        if k.stride(4) != 1:
+            raise ValueError("the head dimension must be contiguous")
+        _need(page_refs, "page_refs", torch.int32, k.shape[1])
+        _need(page_table, "page_table", torch.int32)
+        if page_table.dim() != 2 or not page_table.is_contiguous() or not page_refs.is_contiguous():
+            raise ValueError("page_table [sequences, entries] and page_refs must be contiguous")
+        self.k, self.v, self.page_refs, self.page_table = k, v, page_refs, page_table
+        self.rows, self.width = page_table.shape
+        L, P, S, H, D = k.shape
+        # a dimension of size 1 is never stepped along: its stride only has to be a valid one
+        st = [k.stride(i) if k.shape[i] > 1 else max(8, D) for i in range(4)]
+        self.c = sv_cache(k=_p(k), v=_p(v), layer_stride=st[0], page_stride=st[1], slot_stride=st[2], head_stride=st[3],
+                          layers=L, pages=P, page_size=S, kv_heads=H, head_dim=D, page_refs=_p(page_refs))
+        self.ws = torch.zeros(SV_CACHE_WORKSPACE_BYTES, dtype=torch.uint8, device=k.device) if ws is None else ws
+
+    @classmethod
+    def empty(cls, layers, pages, page_size, kv_heads, head_dim, sequences, entries, device="cuda"):
+        """A cache of free pages and empty sequences."""
+        shape = (layers, pages, page_size, kv_heads, head_dim)
+        return cls(torch.zeros(shape, dtype=torch.bfloat16, device=device),
+                   torch.zeros(shape, dtype=torch.bfloat16, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device),
+                   torch.full((sequences, entries), -1, dtype=torch.int32, device=device))
+
+    def _batch(self, B: int) -> int:
+        if B > self.rows:
+            raise ValueError(f"{B} requests, but the page table has {self.rows} rows")
+        return B
+
+    def reserve(self, seq_len, extra, *, ok=None, stream=None):
+        """Pages for slots [0, seq_len + extra) of rows 0..B-1, B = extra.numel().  Returns ok [B] int32: 1 where
+        served."""
+        B = self._batch(extra.numel())
+        if ok is None:
+            ok = torch.empty(B, dtype=torch.int32, device=extra.device)
+        sv_cache_reserve(self.c, self.page_table, self.width, seq_len, extra, B, ok, self.ws, stream)
+        return ok
+
+    def append(self, k_new, v_new, seq_len, node_offsets, layer=0, *, stream=None):
+        """Writes the nodes' keys and values, [layers, rows, kv_heads, head_dim] from `layer` on or [rows, kv_heads,
+        head_dim] for one layer: node c of request i (row node_offsets[i] + c) to slot seq_len[i] + c."""
+        if k_new.dim() == 3:
+            k_new, v_new = k_new.unsqueeze(0), v_new.unsqueeze(0)
+        if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[2:] != self.k.shape[3:]:
+            raise ValueError("k_new and v_new must be [layers, rows, kv_heads, head_dim] of this cache's heads")
+        L, n, H, D = k_new.shape
+        if k_new.numel() and (k_new.stride() != v_new.stride() or k_new.stride(3) != 1 or (H > 1 and k_new.stride(2) != D)):
+            raise ValueError("k_new and v_new need the same strides and contiguous [kv_heads, head_dim]")
+        sv_cache_append(self.c, layer, L, self.page_table, self.width, seq_len, node_offsets, n, k_new, v_new,
+                        k_new.stride(0) if L > 1 else 0, k_new.stride(1) if n > 1 else H * D,
+                        self._batch(node_offsets.numel() - 1), self.ws, stream)
+
+    def commit(self, seq_len, node_offsets, path, accept_len, *, out_len=None, stream=None):
+        """Keeps the accepted path (verify_tree's outputs path [B, Nmax] and accept_len [B]) in every layer and gives
+        the pages past it back.  Returns the new lengths (written to out_len; it may be seq_len)."""
+        if path.dim() != 2 or not path.is_contiguous():
+            raise ValueError("path must be contiguous [B, Nmax]")
+        B = self._batch(path.shape[0])
+        if out_len is None:
+            out_len = torch.empty(B, dtype=torch.int32, device=path.device)
+        sv_cache_commit(self.c, self.page_table, self.width, seq_len, node_offsets, path, accept_len, B, path.shape[1],
+                        out_len, self.ws, stream)
+        return out_len
+
+    def fork(self, seq_len, src, dst, *, ok=None, stream=None):
+        """Rows dst become copies of rows src (full pages shared); seq_len is updated.  Returns ok [n] int32."""
+        n = src.numel()
+        if dst.numel() != n or seq_len.numel() < self.rows:
+            raise ValueError("src and dst must have one length, seq_len an entry per row of the page table")
+        if ok is None:
+            ok = torch.empty(n, dtype=torch.int32, device=src.device)
+        sv_cache_fork(self.c, self.page_table, self.width, self.rows, seq_len, src, dst, n, ok, self.ws, stream)
+        return ok
+
+    def release(self, seq_len, seqs, *, stream=None):
+        """Gives the pages of rows seqs back and empties them (seq_len = 0)."""
+        if seq_len.numel() < self.rows:
+            raise ValueError("seq_len needs an entry per row of the page table")
+        sv_cache_release(self.c, self.page_table, self.width, self.rows, seq_len, seqs, seqs.numel(), self.ws, stream)
+
+
+def attention_workspace(cache: PagedCache, q_heads: int) -> torch.Tensor:
+    """Workspace of tree_attention() on this cache (its first word is the device status word)."""
+    n = sv_attention_workspace_size(cache.c, q_heads)
+    if n == 0:
+        raise ValueError(lib().sv_last_error_string().decode() or "invalid sizes for sv_attention_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def tree_attention(q, cache: PagedCache, layer, seq_len, node_offsets, parent, Nmax, *, scale=None, window=0, sinks=0,
+                   out=None, lse=True, ws=None, stream=None):
+    """Attention of every request's token tree over its cached sequence in one layer.  q [rows, q_heads, head_dim]
+    bf16, row node_offsets[i] + c for node c of request i, whose keys and values are in the cache at slot seq_len[i] +
+    c (cache.append); parent [rows] int32 as in verify_tree, or None for chains; at most Nmax nodes a request.  window,
+    sinks: a sliding window of that many positions and the first positions that stay visible.  Returns (out like q,
+    lse [rows, q_heads] float32, or None with lse=False)."""
+    if q.dim() != 3 or q.shape[2] != cache.k.shape[4]:
+        raise ValueError("q must be [rows, q_heads, head_dim] of the cache's head_dim")
+    n, H, D = q.shape
+    if q.numel() and q.stride(2) != 1:
+        raise ValueError("the head dimension of q must be contiguous")
+    if out is None:
+        out = torch.empty((n, H, D), dtype=torch.bfloat16, device=q.device)
+    if out.shape != q.shape or (out.numel() and out.stride(2) != 1):
+        raise ValueError("out must have q's shape and a contiguous head dimension")
+    if lse is True:
+        lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
+    if ws is None:
+        ws = _zeros(sv_attention_workspace_size(cache.c, H), q.device, stream)
+    step = lambda t, d, least: t.stride(d) if t.shape[d] > 1 else least  # noqa: E731
+    sv_tree_attention(cache.c, layer, q, step(q, 0, H * D), step(q, 1, D), H, cache.page_table, cache.width, seq_len,
+                      node_offsets, n, parent, cache._batch(node_offsets.numel() - 1), Nmax,
+                      D ** -0.5 if scale is None else scale, window, sinks, out, step(out, 0, H * D), step(out, 1, D),
+                      lse, ws, stream)
+    return out, lse

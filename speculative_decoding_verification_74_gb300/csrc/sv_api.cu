@@ -55,7 +55,7 @@ std::mutex g_prof_mu;
 bool g_prof_on = false;
 std::vector<ProfRec> g_prof;
 std::vector<cudaEvent_t> g_event_pool;
-cudaEvent_t g_pending_start[SV_NUM_KERNELS];
+cudaEvent_t g_pending_start[SV_NUM_KERNEL_IDS];
 std::atomic<int64_t> g_launches{0};
 
 cudaEvent_t take_event() {
@@ -532,11 +532,17 @@ void sv_profile_enable(int on) {
 }
 
 sv_status sv_profile_collect(double* total_ms, int64_t* launches) {
+  return sv_profile_collect_ids(total_ms, launches, SV_NUM_KERNELS);
+}
+
+sv_status sv_profile_collect_ids(double* total_ms, int64_t* launches, int n) {
   if (total_ms == nullptr || launches == nullptr) return fail(SV_ERR_INVALID_ARG, "NULL argument");
+  if (n < 0 || n > SV_NUM_KERNEL_IDS) return fail(SV_ERR_INVALID_ARG, "n=%d outside [0, %d]", n, SV_NUM_KERNEL_IDS);
   std::lock_guard<std::mutex> lk(g_prof_mu);
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "profile sync");
   for (const ProfRec& r : g_prof) {
+    if (r.id >= n) continue;
     float ms = 0.0f;
     if (cudaEventElapsedTime(&ms, r.a, r.b) == cudaSuccess) {
       total_ms[r.id] += ms;

@@ -155,7 +155,11 @@ __global__ void __launch_bounds__(kPageThreads) reserve_kernel(Pool p, int32_t* 
       lack = -1;  // not served
     } else {
       first = static_cast<int>(need);
-      for (int64_t e0 = len >> p.shift; e0 < need; e0 += 32) {
+      // the held entries come first; those before the length's page need no look unless the row
+      // is short of pages for the slots that it already has
+      int64_t e0 = len >> p.shift;
+      if (e0 > 0 && table[static_cast<int64_t>(i) * width + e0 - 1] < 0) e0 = 0;
+      for (; e0 < need; e0 += 32) {
         const int64_t e = e0 + lane;
         const unsigned none = __ballot_sync(0xFFFFFFFFu, e < need && table[static_cast<int64_t>(i) * width + e] < 0);
         if (none != 0) {

@@ -1,11 +1,21 @@
 // sv_sample_rows: draws from logit rows with temperature, top-k, top-p and min-p.
 //
-// One thread-block cluster per row; each CTA keeps a contiguous slice of the row in shared memory,
-// so the row is read from memory once.  Weights are integers (multiples of 2^-40), so every sum
-// is exact and the result does not depend on how the row is split.  The filters keep a prefix of
-// the order (x desc, index asc): the boundary logit is found by a radix descent on the
-// order-preserving integer image of x, 8 bits a step, with histograms of counts and weights that the
-// cluster's CTAs add up through distributed shared memory.
+// One thread-block cluster per row; each CTA keeps a contiguous slice of the row in shared memory, so the row is
+// read from memory once.  Weights are integers (multiples of 2^-40), so every sum is exact and the result does not
+// depend on how the row is split.  The filters keep a prefix of the order (x desc, index asc), so they come down to a
+// boundary logit and how many of its equals are kept:
+//   1. a bound below the boundary, from little work:
+//        top-k   each thread's largest logit is one of a group; the k-th largest of these maxima (rounded down to
+//                one of 512 steps) is at or below the k-th largest logit
+//        top-p   logits whose weight is below (1 - p) W / V add up to less than (1 - p) W
+//        min-p   its own threshold
+//   2. the logits at or above the bound are listed, in vocabulary order, a list per warp (2 bytes each);
+//   3. a histogram of the listed logits (512 steps between the bound and the top; counts, and weights in three
+//      14-bit limbs, which 32-bit atomics add without overflow) is summed over the cluster and gives the step that holds the
+//      boundary, and the count and weight above it;
+//   4. that step's few logits are exchanged, and each CTA ranks them all.
+// Where a step holds more logits than the exchange takes (long runs of equals), the boundary is found by a
+// radix descent on the integer image of x instead.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,9 +30,12 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 256;
+constexpr int kSteps = kThreads;        // histogram steps: one per thread
 constexpr int kMaxCluster = 8;
-constexpr int kPieces = 4;  // bulk copies (and barriers) per slice
+constexpr int kPieces = 4;              // bulk copies (and barriers) per slice
+constexpr int kListPerWarp = 384;       // listed logits per warp; a warp with more walks its run instead
+constexpr int kExchange = kThreads;     // logits of one step that the cluster exchanges: one per thread
+constexpr int kLimb = 14;
 
 struct SampleParams {
   const void* logits;
@@ -40,22 +53,30 @@ struct SampleParams {
   int32_t R, V, M, slice;  // slice: elements per CTA, a multiple of 8
 };
 
-// What the cluster's CTAs read from one another.
+// Per-CTA state; the parts that peers read are written before a cluster barrier.
 struct Shared {
-  uint64_t weight[kBins];
-  uint32_t count[kBins];
-  uint64_t z;          // kept weights of the slice
-  float top;           // largest logit of the slice
+  uint32_t count[kSteps];
+  uint32_t limb[3][kSteps];
+  uint32_t mine[kExchange];            // this CTA's keys of the exchanged step
+  uint32_t all[kExchange];             // the cluster's
+  uint64_t all_w[kExchange];
+  uint16_t list[kWarps][kListPerWarp];
+  uint64_t z;                          // a sum of the slice
+  float top, low;                      // largest logit; smallest group maximum
+  uint32_t mine_n;
   uint64_t bar[kPieces];
   uint64_t seg[kWarps];
   uint32_t ties[kWarps];
   uint64_t scan_w[kWarps];
   uint32_t scan_c[kWarps];
-  // result of a descent step
-  uint32_t bin, above_c, here_c;
-  uint64_t above_w, here_w;
-  uint32_t cut;        // first tie (vocabulary index) that is left out
-  float red[kWarps];
+  uint32_t from[kMaxCluster + 1];      // where each CTA's keys begin in `all`
+  uint32_t step, above_c, here_c;      // the step that holds a boundary
+  uint64_t above_w;
+  uint32_t key, key_above_c, key_equal_c;
+  uint64_t key_above_w;
+  uint32_t equal_before, equal_here;
+  uint32_t cut;                        // first equal (vocabulary index) that is left out
+  float red[2][kWarps];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -84,6 +105,7 @@ __device__ __forceinline__ uint64_t peer_u64(const void* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer_addr(p, rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ float peer_f32(const void* p, uint32_t rank) { return __uint_as_float(peer_u32(p, rank)); }
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -104,6 +126,25 @@ __device__ __forceinline__ float exponent_of(float x, float top, float steep) {
 }
 // 2^y as a multiple of 2^-40.
 __device__ __forceinline__ uint64_t weight_of(float y) { return __float2ull_rn(ex2_approx(y) * 0x1p40f); }
+
+// A running sum of weights, for up to 4096 terms: adding 1.5 2^3 leaves 2^y rounded to a multiple of 2^-20 in the
+// low bits, adding 1.5 2^-17 to what is left does the same for 2^-40; both images are summed as integers.
+struct WeightSum {
+  uint32_t hi = 0, lo = 0, n = 0;
+  __device__ __forceinline__ void add(float y) {
+    const float e = ex2_approx(y);
+    const float t = __fadd_rn(e, 12.0f);
+    const float rest = __fsub_rn(e, __fsub_rn(t, 12.0f));
+    hi += __float_as_uint(t);
+    lo += __float_as_uint(__fadd_rn(rest, 0x1.8p-17f));
+    ++n;
+  }
+  __device__ __forceinline__ uint64_t total() const {
+    const uint32_t h = hi - n * __float_as_uint(12.0f);
+    const int32_t l = static_cast<int32_t>(lo - n * __float_as_uint(0x1.8p-17f));
+    return (static_cast<uint64_t>(h) << 20) + static_cast<uint64_t>(static_cast<int64_t>(l));
+  }
+};
 
 // floor(total * part / 2^24), part <= 2^24, total < 2^62.
 __device__ __forceinline__ uint64_t share_of(uint64_t total, uint32_t part) {
@@ -131,39 +172,114 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 }
 
 // One slice of a row in shared memory: 16-byte vectors, the first `phase` elements and those past
-// the slice padded with -inf.
+// the slice padded with -inf.  A warp owns a contiguous run of vectors.
 template <int DT>
 struct Slice {
   static constexpr int kElems = Vec<DT>::kElems;
   using Elem = typename std::conditional<DT == SV_BF16, uint16_t, uint32_t>::type;
   unsigned char* data;
   int phase, n, vecs;
-  int64_t first;  // vocabulary index of element 0 of the slice
+  int run_a, run_z;  // this warp's vectors
+  int64_t first;     // vocabulary index of element 0 of the slice
 
   __device__ __forceinline__ uint4 vec(int i) const { return lds128(data + static_cast<size_t>(i) * 16); }
-  __device__ __forceinline__ int index(int vec, int e) const { return static_cast<int>(first) + vec * kElems + e - phase; }
+  // by position in the padded slice
+  __device__ __forceinline__ float at(int pos) const {
+    if constexpr (DT == SV_BF16) return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(data)[pos]) << 16);
+    else return reinterpret_cast<const float*>(data)[pos];
+  }
+  __device__ __forceinline__ int index_of(int pos) const { return static_cast<int>(first) + pos - phase; }
 };
 
-// Radix descent over the whole row for the boundary of a prefix of (x desc): the smallest prefix whose count
-// reaches `want` (by count) or whose weight does.  Returns the boundary key, the count and weight above
-// it, and how often the key occurs (in the row, and in the CTAs before this one).
+// Boundary of a prefix of the order (x desc): the smallest one whose count, or weight, reaches what is asked for.
+// key 0: none, everything lies above.
 struct Boundary {
   uint32_t key, above_c, equal_c, equal_before, equal_here;
   uint64_t above_w;
 };
+
+// Adds a weight to a histogram step in limbs.
+__device__ __forceinline__ void add_limbs(Shared& sh, int step, uint64_t w) {
+  const uint32_t mask = (1u << kLimb) - 1u;
+  const uint32_t a = static_cast<uint32_t>(w) & mask, b = static_cast<uint32_t>(w >> kLimb) & mask,
+                 c = static_cast<uint32_t>(w >> (2 * kLimb));
+  if (a) atomicAdd(&sh.limb[0][step], a);
+  if (b) atomicAdd(&sh.limb[1][step], b);
+  if (c) atomicAdd(&sh.limb[2][step], c);
+}
+__device__ __forceinline__ uint64_t limbs_of(uint64_t a, uint64_t b, uint64_t c) { return a + (b << kLimb) + (c << (2 * kLimb)); }
+
+__device__ __forceinline__ void clear_histogram(Shared& sh) {
+  const int t = threadIdx.x;
+  sh.count[t] = sh.limb[0][t] = sh.limb[1][t] = sh.limb[2][t] = 0;
+}
+
+// The cluster's count and weight of one histogram step.
+__device__ __forceinline__ void merged_step(const Shared& sh, int step, bool weights, uint32_t* c, uint64_t* w) {
+  const uint32_t cs = cluster_size();
+  uint32_t n = 0;
+  uint64_t l0 = 0, l1 = 0, l2 = 0;
+  for (uint32_t r = 0; r < cs; ++r) {
+    n += peer_u32(&sh.count[step], r);
+    if (weights) {
+      l0 += peer_u32(&sh.limb[0][step], r);
+      l1 += peer_u32(&sh.limb[1][step], r);
+      l2 += peer_u32(&sh.limb[2][step], r);
+    }
+  }
+  *c = n;
+  *w = limbs_of(l0, l1, l2);
+}
+
+// Finds the first thread, in thread order, at which base + the running sum of c (or w) reaches `want`; writes
+// step = its index, above_c / above_w = the sums before it, here_c to shared memory; step = 0xFFFFFFFF if none does.
+template <bool kByWeight>
+__device__ void find_step(Shared& sh, uint32_t c, uint64_t w, uint64_t want, uint32_t base_c, uint64_t base_w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t ci = c;
+  uint64_t wi = w;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t cu = __shfl_up_sync(0xFFFFFFFFu, ci, d);
+    const uint64_t wu = __shfl_up_sync(0xFFFFFFFFu, wi, d);
+    if (lane >= d) {
+      ci += cu;
+      wi += wu;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    sh.scan_c[warp] = ci;
+    sh.scan_w[warp] = wi;
+  }
+  if (threadIdx.x == 0) sh.step = 0xFFFFFFFFu;
+  __syncthreads();
+  ci += base_c;
+  wi += base_w;
+  for (int i = 0; i < warp; ++i) {
+    ci += sh.scan_c[i];
+    wi += sh.scan_w[i];
+  }
+  if (c > 0 && (kByWeight ? wi >= want && wi - w < want : ci >= want && ci - c < want)) {
+    sh.step = threadIdx.x;
+    sh.above_c = ci - c;
+    sh.above_w = wi - w;
+    sh.here_c = c;
+  }
+  __syncthreads();
+}
+
+// Radix descent over the whole row, 8 bits of the key a level.
 template <int DT, bool kByWeight>
 __device__ Boundary descend(const Slice<DT>& s, Shared& sh, uint64_t want, float top, float steep) {
   constexpr int kLevels = DT == SV_BF16 ? 2 : 4;
-  const uint32_t cs = cluster_size(), rank = cluster_rank();
+  const uint32_t rank = cluster_rank();
   uint32_t prefix = 0, above_c = 0;
   uint64_t above_w = 0;
   Boundary b = {};
   for (int level = 0; level < kLevels; ++level) {
     const int shift = 24 - 8 * level;
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      sh.count[i] = 0;
-      sh.weight[i] = 0;
-    }
+    clear_histogram(sh);
     __syncthreads();
     for (int v = threadIdx.x; v < s.vecs; v += kThreads) {
       const Vec<DT> x(s.vec(v));
@@ -171,78 +287,156 @@ __device__ Boundary descend(const Slice<DT>& s, Shared& sh, uint64_t want, float
       for (int e = 0; e < Vec<DT>::kElems; ++e) {
         const uint32_t key = key_of(x.x[e]);
         if (x.x[e] != -INFINITY && (level == 0 || (key >> (shift + 8)) == prefix)) {
-          const uint32_t bin = (key >> shift) & 255u;
-          atomicAdd(&sh.count[bin], 1u);
-          if (kByWeight) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.weight[bin]), weight_of(exponent_of(x.x[e], top, steep)));
+          const uint32_t step = 255u - ((key >> shift) & 255u);  // large logits first
+          atomicAdd(&sh.count[step], 1u);
+          if (kByWeight) add_limbs(sh, step, weight_of(exponent_of(x.x[e], top, steep)));
         }
       }
     }
     cluster_sync();  // every slice's histogram is complete
-    // thread t of the first 256 takes bin 255 - t: a scan over threads goes from large to small logits
-    const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
-    uint32_t c = 0;
-    uint64_t w = 0;
-    if (bin >= 0)
-      for (uint32_t r = 0; r < cs; ++r) {
-        c += peer_u32(&sh.count[bin], r);
-        if (kByWeight) w += peer_u64(&sh.weight[bin], r);
-      }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t ci = c;
-    uint64_t wi = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t cu = __shfl_up_sync(0xFFFFFFFFu, ci, d);
-      const uint64_t wu = __shfl_up_sync(0xFFFFFFFFu, wi, d);
-      if (lane >= d) {
-        ci += cu;
-        wi += wu;
-      }
-    }
-    if (lane == 31) {
-      sh.scan_c[warp] = ci;
-      sh.scan_w[warp] = wi;
-    }
-    if (threadIdx.x == 0) sh.bin = 0xFFFFFFFFu;
-    __syncthreads();
-    for (int i = 0; i < warp; ++i) {
-      ci += sh.scan_c[i];
-      wi += sh.scan_w[i];
-    }
-    ci += above_c;
-    wi += above_w;
-    const bool reaches = bin >= 0 && c > 0 && (kByWeight ? wi >= want && wi - w < want : ci >= want && ci - c < want);
-    if (reaches) {
-      sh.bin = bin;
-      sh.above_c = ci - c;
-      sh.above_w = wi - w;
-      sh.here_c = c;
-    }
-    __syncthreads();
-    if (sh.bin == 0xFFFFFFFFu) {  // fewer than `want`: everything is kept (the caller's want is at most the total by weight)
-      b.key = 0;
+    uint32_t c;
+    uint64_t w;
+    merged_step(sh, threadIdx.x, kByWeight, &c, &w);
+    find_step<kByWeight>(sh, c, w, want, above_c, above_w);
+    if (sh.step == 0xFFFFFFFFu) {  // fewer than `want`: everything is kept
       cluster_sync();
       return b;
     }
     above_c = sh.above_c;
     above_w = sh.above_w;
-    prefix = level == 0 ? sh.bin : (prefix << 8) | sh.bin;
+    const uint32_t digit = 255u - sh.step;
+    prefix = level == 0 ? digit : (prefix << 8) | digit;
     if (level == kLevels - 1) {
       b.equal_c = sh.here_c;
-      b.equal_here = sh.count[sh.bin];
-      for (uint32_t r = 0; r < rank; ++r) b.equal_before += peer_u32(&sh.count[sh.bin], r);
+      b.equal_here = sh.count[sh.step];
+      for (uint32_t r = 0; r < rank; ++r) b.equal_before += peer_u32(&sh.count[sh.step], r);
     }
     cluster_sync();  // the peers have read this histogram
   }
-  // bf16 keys: the low half of a key is 0x8000 or more exactly for negative logits (all ones), else 0
+  // a bf16 key's low half is all ones for a negative logit, else 0
   b.key = DT == SV_BF16 ? ((prefix << 16) | ((prefix & 0x8000u) ? 0u : 0xFFFFu)) : prefix;
   b.above_c = above_c;
   b.above_w = above_w;
   return b;
 }
 
+// Calls f(position, x) for this warp's logits at or above `bound`, in vocabulary order and by whole warps: lanes
+// without one get position -1.  listed >= 0: from the warp's list.
+template <int DT, typename F>
+__device__ __forceinline__ void for_candidates(const Slice<DT>& s, const Shared& sh, int listed, float bound, F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (listed >= 0) {
+    for (int i = lane; i - lane < listed; i += 32) {
+      const int pos = i < listed ? sh.list[warp][i] : -1;
+      f(pos, pos >= 0 ? s.at(pos) : -INFINITY);
+    }
+  } else {
+    for (int p0 = s.run_a * Slice<DT>::kElems; p0 < s.run_z * Slice<DT>::kElems; p0 += 32) {
+      const int pos = p0 + lane;
+      const float x = pos < s.run_z * Slice<DT>::kElems ? s.at(pos) : -INFINITY;
+      const bool in = x >= bound && x != -INFINITY;
+      if (__any_sync(0xFFFFFFFFu, in)) f(in ? pos : -1, in ? x : -INFINITY);
+    }
+  }
+}
+
+// Steps of the candidates' histogram: equal widths between the top and the bound, the last one open.
+struct Scale {
+  float top, inv;
+  static __device__ __forceinline__ Scale over(float top, float range) {
+    return {top, range > 0.0f ? fminf(static_cast<float>(kSteps - 1) / range, FLT_MAX) : 0.0f};
+  }
+  __device__ __forceinline__ int step(float x) const {
+    return static_cast<int>(fminf(__fmul_rn(__fsub_rn(top, x), inv), static_cast<float>(kSteps - 1)));
+  }
+};
+
+// The logits of one step, exchanged over the cluster and ranked: the boundary by count or weight, given the sums
+// above the step.
+template <int DT, bool kByWeight>
+__device__ Boundary rank_step(const Slice<DT>& s, Shared& sh, int listed, float bound, const Scale& scale, int step,
+                              uint64_t want, uint32_t above_c, uint64_t above_w, float top, float steep) {
+  const uint32_t cs = cluster_size(), rank = cluster_rank();
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    sh.mine_n = 0;
+    sh.equal_before = sh.equal_here = 0;
+  }
+  __syncthreads();
+  for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
+    if (pos >= 0 && scale.step(x) == step) sh.mine[atomicAdd(&sh.mine_n, 1u)] = key_of(x);
+  });
+  cluster_sync();
+  if (tid <= static_cast<int>(cs)) {
+    uint32_t n = 0;
+    for (int r = 0; r < tid; ++r) n += peer_u32(&sh.mine_n, r);
+    sh.from[tid] = n;
+  }
+  __syncthreads();
+  const uint32_t n = sh.from[cs];
+  uint32_t key = 0;
+  uint64_t w = 0;
+  if (tid < static_cast<int>(n)) {
+    uint32_t r = 0;
+    while (sh.from[r + 1] <= static_cast<uint32_t>(tid)) ++r;
+    key = peer_u32(&sh.mine[tid - sh.from[r]], r);
+    w = weight_of(exponent_of(logit_of_key(key), top, steep));
+    sh.all[tid] = key;
+    sh.all_w[tid] = w;
+  }
+  __syncthreads();
+  if (tid < static_cast<int>(n)) {
+    uint32_t more = 0, equal = 0;
+    uint64_t more_w = 0;
+    for (uint32_t i = 0; i < n; ++i) {
+      const uint32_t k = sh.all[i];
+      more += k > key;
+      equal += k == key;
+      if (kByWeight) more_w += k > key ? sh.all_w[i] : 0;
+    }
+    const bool here = kByWeight ? above_w + more_w < want && above_w + more_w + equal * w >= want
+                                : above_c + more < want && above_c + more + equal >= want;
+    if (here) {  // every holder of the key writes the same
+      if (!kByWeight)
+        for (uint32_t i = 0; i < n; ++i) more_w += sh.all[i] > key ? sh.all_w[i] : 0;
+      sh.key = key;
+      sh.key_above_c = above_c + more;
+      sh.key_above_w = above_w + more_w;
+      sh.key_equal_c = equal;
+      if (tid < static_cast<int>(sh.from[rank])) atomicAdd(&sh.equal_before, 1u);
+      else if (tid < static_cast<int>(sh.from[rank + 1])) atomicAdd(&sh.equal_here, 1u);
+    }
+  }
+  __syncthreads();
+  Boundary b;
+  b.key = sh.key;
+  b.above_c = sh.key_above_c;
+  b.above_w = sh.key_above_w;
+  b.equal_c = sh.key_equal_c;
+  b.equal_before = sh.equal_before;
+  b.equal_here = sh.equal_here;
+  return b;
+}
+
+// Sum of one value per thread over the cluster (one cluster barrier; a second one before sh.z may be written again).
+__device__ uint64_t cluster_total(Shared& sh, uint64_t v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_sum(v);
+  if (lane == 0) sh.seg[warp] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint64_t z = 0;
+    for (int i = 0; i < kWarps; ++i) z += sh.seg[i];
+    sh.z = z;
+  }
+  cluster_sync();
+  uint64_t total = 0;
+  for (uint32_t r = 0; r < cluster_size(); ++r) total += peer_u64(&sh.z, r);
+  return total;
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleParams p) {
   using Elem = typename Slice<DT>::Elem;
   constexpr int kElems = Vec<DT>::kElems;
   extern __shared__ __align__(128) unsigned char dyn[];
@@ -258,15 +452,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
   const Elem* src = x_row + s.first;
   s.phase = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(Elem));
   s.vecs = s.n > 0 ? (s.phase + s.n + kElems - 1) / kElems : 0;
+  const int run = (s.vecs + kWarps - 1) / kWarps;
+  s.run_a = min(s.vecs, warp * run);
+  s.run_z = min(s.vecs, s.run_a + run);
   if (tid == 0) {
     for (int i = 0; i < kPieces; ++i) mbar_init(&sh.bar[i], 1);
     fence_proxy_async_smem();
   }
   __syncthreads();
   pdl_wait();
-  // whole 16-byte vectors by bulk copy, the row's ragged ends element by element
+  // whole 16-byte vectors by bulk copy, the slice's ragged ends element by element
   const int v0 = s.phase > 0 ? 1 : 0, v1 = (s.phase + s.n) / kElems;
-  const int per_piece = v1 > v0 ? (v1 - v0 + kPieces - 1) / kPieces : 0;
+  const int per_piece = max(1, v1 > v0 ? (v1 - v0 + kPieces - 1) / kPieces : 0);
   if (tid == 0)
     for (int i = 0; i < kPieces; ++i) {
       const int a = min(v1, v0 + i * per_piece), b = min(v1, a + per_piece);
@@ -278,181 +475,291 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
       }
     }
   const Elem none = DT == SV_BF16 ? static_cast<Elem>(0xFF80u) : static_cast<Elem>(0xFF800000u);
-  for (int i = tid; i < s.vecs * kElems; i += kThreads) {
-    if (i >= v0 * kElems && v1 > v0 && i < v1 * kElems) {
-      i += ((v1 * kElems - i - 1) / kThreads) * kThreads;  // skip the copied vectors
-      continue;
+  // the ragged ends: at most two vectors
+  if (tid < 2 * kElems) {
+    const int v = tid < kElems ? 0 : s.vecs - 1;
+    const int pos = v * kElems + (tid % kElems);
+    if (s.vecs > 0 && (tid < kElems || s.vecs > 1) && !(v >= v0 && v < v1)) {
+      const int e = pos - s.phase;
+      reinterpret_cast<Elem*>(dyn)[pos] = e >= 0 && e < s.n ? src[e] : none;
     }
-    const int e = i - s.phase;
-    reinterpret_cast<Elem*>(dyn)[i] = e >= 0 && e < s.n ? src[e] : none;
   }
-  float T = p.temperature[row];
+  const float T = p.temperature[row];
   const int k_in = p.top_k != nullptr ? p.top_k[row] : 0;
   const float p_in = p.top_p != nullptr ? p.top_p[row] : 1.0f;
   const float q_in = p.min_p != nullptr ? p.min_p[row] : 0.0f;
   uint32_t bad = 0;
   if (!(T >= 0.0f) || T == INFINITY) bad |= SV_DEV_BAD_TEMPERATURE;
   if (k_in < 0 || !(p_in > 0.0f && p_in <= 1.0f) || !(q_in >= 0.0f && q_in <= 1.0f)) bad |= SV_DEV_BAD_FILTER;
-  for (int j = 0; j < p.M; ++j) {
+  bool bad_uniform = false;
+  for (int j = tid; j < p.M; j += kThreads) {
     const float u = p.uniforms[row * p.M + j];
-    if (!(u >= 0.0f && u < 1.0f)) bad |= SV_DEV_BAD_FILTER;
+    bad_uniform |= !(u >= 0.0f && u < 1.0f);
   }
-  __syncthreads();
-  for (int i = 0; i < kPieces; ++i) mbar_wait(&sh.bar[i], 0, p.status);
-  // ---- the largest logit --------------------------------------------------------------------
-  float top = -INFINITY;
-  for (int v = tid; v < s.vecs; v += kThreads) {
+  const bool greedy = T == 0.0f;
+  const float steep = greedy ? 1.0f : fminf(__fdiv_rn(1.44269504088896341f, T), FLT_MAX);
+  const int k = greedy ? 1 : (k_in == 0 ? p.V : k_in);
+  const bool by_count = k < p.V;
+  const bool nucleus = !greedy && p_in < 1.0f;
+  const bool floor_on = !greedy && q_in > 0.0f;
+  const bool cuts = by_count || nucleus || floor_on;
+  const float least = floor_on ? log2f(q_in) : -INFINITY;  // of y
+  const uint32_t p24 = static_cast<uint32_t>(rintf(p_in * 16777216.0f));
+  // The cut row is -inf but for what is kept: filled while the logits are on their way (a row cut in place only
+  // after they have arrived), and the kept logits follow at the end.
+  Elem* out_row = p.out_rows != nullptr ? static_cast<Elem*>(p.out_rows) + row * p.out_stride + s.first : nullptr;
+  const bool in_place = p.out_rows == p.logits;
+  auto fill_row = [&]() {
+    const int head = min(s.n, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(out_row) & 15u)) & 15u) / sizeof(Elem)));
+    const int vecs = (s.n - head) / kElems;
+    const uint32_t w = DT == SV_BF16 ? 0xFF80FF80u : 0xFF800000u;
+    for (int i = tid; i < vecs; i += kThreads) reinterpret_cast<uint4*>(out_row + head)[i] = make_uint4(w, w, w, w);
+    for (int i = tid; i < s.n - vecs * kElems; i += kThreads) out_row[i < head ? i : i + vecs * kElems] = none;
+  };
+  if (out_row != nullptr && !in_place) fill_row();
+  if (__syncthreads_or(bad_uniform)) bad |= SV_DEV_BAD_FILTER;
+  // ---- the largest logit, of the row and of each thread's group ------------------------------
+  // a warp waits for the copies that hold its run only
+  for (int i = 0; i < kPieces; ++i) {
+    const int a = v0 + i * per_piece;
+    if (a < s.run_z && min(v1, a + per_piece) > s.run_a) mbar_wait(&sh.bar[i], 0, p.status);
+  }
+  float group = -INFINITY;
+#pragma unroll 4
+  for (int v = s.run_a + lane; v < s.run_z; v += 32) {
     const Vec<DT> x(s.vec(v));
 #pragma unroll
-    for (int e = 0; e < kElems; ++e) top = max_nan(top, x.x[e]);
+    for (int e = 0; e < kElems; ++e) group = max_nan(group, x.x[e]);
   }
+  float top = group, low = group == -INFINITY ? INFINITY : group;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  if (lane == 0) sh.red[warp] = top;
+  for (int d = 16; d > 0; d >>= 1) {
+    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, d));
+  }
+  if (lane == 0) {
+    sh.red[0][warp] = top;
+    sh.red[1][warp] = low;
+  }
+  clear_histogram(sh);
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) top = max_nan(top, sh.red[w]);
+    for (int w = 1; w < kWarps; ++w) {
+      top = max_nan(top, sh.red[0][w]);
+      low = fminf(low, sh.red[1][w]);
+    }
     sh.top = top;
+    sh.low = low;
   }
   cluster_sync();
   top = -INFINITY;
-  for (uint32_t r = 0; r < cs; ++r) top = max_nan(top, __uint_as_float(peer_u32(&sh.top, r)));
+  low = INFINITY;
+  for (uint32_t r = 0; r < cs; ++r) {
+    top = max_nan(top, peer_f32(&sh.top, r));
+    low = fminf(low, peer_f32(&sh.low, r));
+  }
   if (!(top < INFINITY)) bad |= SV_DEV_BAD_LOGIT;
-  const bool empty = top == -INFINITY;
-  if (bad != 0 || empty) {  // the same in every CTA of the cluster
+  if (out_row != nullptr && in_place) {  // the whole slice is here: every warp has waited for its run
+    fill_row();
+    __syncthreads();
+  }
+  if (bad != 0 || top == -INFINITY) {  // the same in every CTA of the cluster
     if (bad != 0 && rank == 0 && tid == 0) atomicOr(p.status, bad);
     if (rank == 0)
       for (int j = tid; j < p.M; j += kThreads) {
         p.out_tokens[row * p.M + j] = -1;
         if (p.out_probs != nullptr) p.out_probs[row * p.M + j] = bad != 0 ? NAN : 0.0f;
       }
-    if (p.out_rows != nullptr)
-      for (int i = tid; i < s.n; i += kThreads) static_cast<Elem*>(p.out_rows)[row * p.out_stride + s.first + i] = none;
     cluster_sync();  // no CTA leaves while a peer may still read its shared memory
     return;
   }
-  const bool greedy = T == 0.0f;
-  const float steep = greedy ? 1.0f : fminf(__fdiv_rn(1.44269504088896341f, T), FLT_MAX);
-  const int k = greedy ? 1 : (k_in == 0 ? p.V : k_in);
-  const float least = greedy ? -INFINITY : log2f(q_in);
-  const uint32_t p24 = greedy ? 1u << 24 : static_cast<uint32_t>(rintf(p_in * 16777216.0f));
-  // ---- the filters' boundary ----------------------------------------------------------------
-  Boundary b = {};          // key 0: every logit lies above
-  uint32_t ties_kept = 0;   // how many of the boundary's equals are kept, lowest indexes first
-  uint64_t total = 0;
-  if (k < p.V) {
-    b = descend<DT, false>(s, sh, k, top, steep);
-    ties_kept = b.key == 0 ? 0 : k - b.above_c;
-  }
-  const bool nucleus = !greedy && p_in < 1.0f;
-  if (nucleus) {
-    // W: weights of the top-k
-    uint64_t w = 0;
-    for (int v = tid; v < s.vecs; v += kThreads) {
+  // ---- 1. a bound below the boundary ----------------------------------------------------------
+  float bound = -INFINITY;
+  uint64_t total = 0;  // W, where it is known
+  if (by_count) {
+    const Scale groups = Scale::over(top, __fsub_rn(top, low));
+    if (group != -INFINITY) atomicAdd(&sh.count[groups.step(group)], 1u);
+    cluster_sync();
+    uint32_t c;
+    uint64_t w;
+    merged_step(sh, tid, false, &c, &w);
+    find_step<false>(sh, c, 0, k, 0, 0);
+    // a step's lower end, a little lower than the roundings of step() may put it
+    if (sh.step != 0xFFFFFFFFu)
+      bound = groups.inv > 0.0f ? __fsub_rd(top, __fmul_ru(static_cast<float>(sh.step + 1) / groups.inv, 1.00001f)) : top;
+    cluster_sync();  // the peers have read this histogram
+    clear_histogram(sh);
+  } else if (nucleus) {
+    WeightSum sum;
+#pragma unroll 2
+    for (int v = s.run_a + lane; v < s.run_z; v += 32) {
       const Vec<DT> x(s.vec(v));
 #pragma unroll
-      for (int e = 0; e < kElems; ++e)
-        if (key_of(x.x[e]) > b.key) w += weight_of(exponent_of(x.x[e], top, steep));
+      for (int e = 0; e < kElems; ++e) sum.add(exponent_of(x.x[e], top, steep));
     }
-    w = warp_sum(w);
-    if (lane == 0) sh.seg[warp] = w;
-    __syncthreads();
-    if (tid == 0) {
-      uint64_t z = 0;
-      for (int i = 0; i < kWarps; ++i) z += sh.seg[i];
-      sh.z = z;
-    }
-    cluster_sync();
-    for (uint32_t r = 0; r < cs; ++r) total += peer_u64(&sh.z, r);
-    if (b.key != 0) total += static_cast<uint64_t>(ties_kept) * weight_of(exponent_of(logit_of_key(b.key), top, steep));
-    cluster_sync();
-    const uint64_t limit = max(share_of(total, p24), uint64_t(1));
-    b = descend<DT, true>(s, sh, limit, top, steep);
-    const uint64_t each = weight_of(exponent_of(logit_of_key(b.key), top, steep));
-    ties_kept = each == 0 ? 0 : static_cast<uint32_t>((limit - b.above_w + each - 1) / each);
+    total = cluster_total(sh, sum.total());
+    // V weights of at most this (and half a unit of rounding each) stay below (1 - p) W; 1e-3 covers ex2 and log2
+    const float each = static_cast<float>(total) * (static_cast<float>((1u << 24) - p24) * 0x1p-24f) / static_cast<float>(p.V) - 0.5f;
+    if (each > 0.0f) bound = __fadd_rd(top, __fdiv_rd(log2f(each) - 40.0f - 1e-3f, steep));
   }
-  // ties of this slice that are kept: those before vocabulary index `cut`
+  // Below min-p's threshold nothing is kept.  The boundary may then lie below the bound: it is not found, and everything
+  // above the bound is kept.  Only the top-k's own weight needs all of the top-k.
+  if (floor_on && !(by_count && nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(least * 1.000001f, steep)));
+  if (!(bound < top)) bound = bound >= top ? top : -INFINITY;
+  // ---- 2. the logits at or above the bound, by warp and in order -------------------------------
+  int listed = -1;
+  if (cuts) {
+    int n = 0;
+    for (int vb = s.run_a; vb < s.run_z; vb += 32) {
+      const int v = vb + lane;
+      uint32_t mask = 0;
+      if (v < s.run_z) {
+        const Vec<DT> x(s.vec(v));
+#pragma unroll
+        for (int e = 0; e < kElems; ++e) mask |= (x.x[e] >= bound && x.x[e] != -INFINITY ? 1u : 0u) << e;
+      }
+      if (__any_sync(0xFFFFFFFFu, mask != 0)) {
+        const int c = __popc(mask);
+        int incl = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+          if (lane >= d) incl += u;
+        }
+        int at = n + incl - c;
+        n += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        if (n <= kListPerWarp)
+          for (uint32_t m = mask; m != 0; m &= m - 1) sh.list[warp][at++] = static_cast<uint16_t>(v * kElems + __ffs(m) - 1);
+      }
+    }
+    if (n <= kListPerWarp) listed = n;
+    __syncwarp();
+  }
+  // ---- 3. and 4. the boundary ---------------------------------------------------------------------
+  Boundary b = {};
+  uint32_t ties_kept = 0;  // how many of the boundary's equals are kept, lowest indexes first
+  if (by_count || nucleus) {
+    const Scale scale = Scale::over(top, bound == -INFINITY ? 64.0f / steep : __fsub_rn(top, bound));
+    __syncthreads();  // the histogram is clear
+    for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
+      if (pos >= 0) {
+        const int step = scale.step(x);
+        atomicAdd(&sh.count[step], 1u);
+        if (nucleus) add_limbs(sh, step, weight_of(exponent_of(x, top, steep)));
+      }
+    });
+    cluster_sync();
+    uint32_t c;
+    uint64_t w;
+    merged_step(sh, tid, nucleus, &c, &w);
+    bool found = true, crowded = false;
+    uint32_t step = 0;
+    if (by_count) {
+      find_step<false>(sh, c, w, k, 0, 0);
+      step = sh.step;
+      found = step != 0xFFFFFFFFu;  // else fewer than k logits: all are kept
+      crowded = found && sh.here_c > kExchange;
+      if (found && !crowded)
+        b = rank_step<DT, false>(s, sh, listed, bound, scale, step, k, sh.above_c, sh.above_w, top, steep);
+      if (crowded) {
+        cluster_sync();  // the peers have read the histogram
+        b = descend<DT, false>(s, sh, k, top, steep);
+      }
+      ties_kept = found ? k - b.above_c : 0;
+    }
+    if (nucleus) {
+      if (by_count) {
+        // W: what lies above the boundary, and its kept equals
+        if (found && !crowded) {
+          total = b.above_w;
+        } else {
+          WeightSum sum;
+          for (int v = s.run_a + lane; v < s.run_z; v += 32) {
+            const Vec<DT> x(s.vec(v));
+#pragma unroll
+            for (int e = 0; e < kElems; ++e)
+              if (key_of(x.x[e]) > b.key) sum.add(exponent_of(x.x[e], top, steep));
+          }
+          total = cluster_total(sh, sum.total());
+        }
+        if (found) total += static_cast<uint64_t>(ties_kept) * weight_of(exponent_of(logit_of_key(b.key), top, steep));
+      }
+      const uint64_t limit = max(share_of(total, p24), uint64_t(1));
+      if (crowded) {
+        b = descend<DT, true>(s, sh, limit, top, steep);
+      } else {
+        find_step<true>(sh, c, w, limit, 0, 0);
+        const bool inside = sh.step != 0xFFFFFFFFu;
+        if (inside ? sh.here_c > kExchange : !floor_on) {
+          cluster_sync();  // the peers have read the histogram
+          b = descend<DT, true>(s, sh, limit, top, steep);
+        } else if (inside) {
+          if (by_count) cluster_sync();  // the peers have read the keys exchanged before
+          b = rank_step<DT, true>(s, sh, listed, bound, scale, sh.step, limit, sh.above_c, sh.above_w, top, steep);
+        } else {
+          b = Boundary{};
+        }
+      }
+      if (b.key != 0) {
+        const uint64_t each = weight_of(exponent_of(logit_of_key(b.key), top, steep));
+        ties_kept = each == 0 ? 0 : static_cast<uint32_t>((limit - b.above_w + each - 1) / each);
+      }
+    }
+  }
+  // equals of this slice that are kept: those before vocabulary index `cut`
   uint32_t cut = 0xFFFFFFFFu;
   {
     const uint32_t quota = ties_kept > b.equal_before ? min(ties_kept - b.equal_before, b.equal_here) : 0;
-    if (b.key == 0) {
-      cut = 0;
-    } else if (quota == 0) {
+    if (b.key == 0 || quota == 0) {
       cut = 0;
     } else if (quota < b.equal_here) {
-      // the quota-th tie of the slice, in order: warps own contiguous runs of vectors
-      const int run = (s.vecs + kWarps - 1) / kWarps;
-      const int a = min(s.vecs, warp * run), z = min(s.vecs, a + run);
       uint32_t c = 0;
-      for (int v = a + lane; v < z; v += 32) {
-        const Vec<DT> x(s.vec(v));
-#pragma unroll
-        for (int e = 0; e < kElems; ++e) c += key_of(x.x[e]) == b.key;
-      }
+      for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) { c += pos >= 0 && key_of(x) == b.key; });
       c = __reduce_add_sync(0xFFFFFFFFu, c);
       if (lane == 0) sh.ties[warp] = c;
       __syncthreads();
       uint32_t before = 0;
       for (int i = 0; i < warp; ++i) before += sh.ties[i];
-      if (before < quota && before + c >= quota) {
-        for (int v0r = a; v0r < z; v0r += 32) {
-          const int v = v0r + lane;
-          uint32_t mask = 0;
-          if (v < z) {
-            const Vec<DT> x(s.vec(v));
-#pragma unroll
-            for (int e = 0; e < kElems; ++e) mask |= (key_of(x.x[e]) == b.key ? 1u : 0u) << e;
-          }
-          uint32_t incl = __popc(mask);
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-            if (lane >= d) incl += u;
-          }
-          const uint32_t excl = incl - __popc(mask);
-          if (before + excl < quota && before + incl >= quota) {
-            uint32_t left = quota - before - excl;  // the left-th set bit of mask
-            while (--left > 0) mask &= mask - 1;
-            sh.cut = static_cast<uint32_t>(s.index(v, __ffs(mask) - 1)) + 1;
-          }
-          before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-        }
-      }
+      if (before < quota && before + c >= quota)
+        for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
+          const bool equal = pos >= 0 && key_of(x) == b.key;
+          const uint32_t set = __ballot_sync(0xFFFFFFFFu, equal);
+          if (equal && before + __popc(set & ((1u << lane) - 1u)) == quota - 1) sh.cut = static_cast<uint32_t>(s.index_of(pos)) + 1;
+          before += __popc(set);
+        });
       __syncthreads();
       cut = sh.cut;
     }
   }
-  // kept weight of an element (0 = cut or no weight)
-  auto keeps = [&](float x, int index) {
+  auto keeps = [&](int pos, float x) {
     const uint32_t key = key_of(x);
-    return x != -INFINITY && (key > b.key || (key == b.key && static_cast<uint32_t>(index) < cut)) &&
-           exponent_of(x, top, steep) >= least;
+    return (key > b.key || (key == b.key && static_cast<uint32_t>(s.index_of(pos)) < cut)) && exponent_of(x, top, steep) >= least;
   };
-  // ---- kept weights by warp runs, the row's total, the draws -----------------------------------
-  const int run = (s.vecs + kWarps - 1) / kWarps;
-  const int run_a = min(s.vecs, warp * run), run_z = min(s.vecs, run_a + run);
+  // ---- kept weights by warp, the row's total, the kept logits ------------------------------------
   {
     uint64_t w = 0;
-    for (int v = run_a + lane; v < run_z; v += 32) {
-      const Vec<DT> x(s.vec(v));
-      float kept[kElems];
-#pragma unroll
-      for (int e = 0; e < kElems; ++e) {
-        const bool keep = keeps(x.x[e], s.index(v, e));
-        kept[e] = keep ? x.x[e] : -INFINITY;
-        if (keep) w += weight_of(exponent_of(x.x[e], top, steep));
-      }
-      if (p.out_rows != nullptr) {
-        Elem* out = static_cast<Elem*>(p.out_rows) + row * p.out_stride;
-#pragma unroll
-        for (int e = 0; e < kElems; ++e) {
-          const int64_t i = s.index(v, e);
-          if (i >= s.first && i < s.first + s.n)
-            out[i] = DT == SV_BF16 ? static_cast<Elem>(__float_as_uint(kept[e]) >> 16) : static_cast<Elem>(__float_as_uint(kept[e]));
+    if (cuts) {
+      for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
+        if (pos >= 0 && keeps(pos, x)) {
+          w += weight_of(exponent_of(x, top, steep));
+          if (out_row != nullptr) out_row[pos - s.phase] = reinterpret_cast<const Elem*>(dyn)[pos];
         }
+      });
+    } else {
+      WeightSum sum;
+#pragma unroll 2
+      for (int v = s.run_a + lane; v < s.run_z; v += 32) {
+        const Vec<DT> x(s.vec(v));
+#pragma unroll
+        for (int e = 0; e < kElems; ++e) sum.add(exponent_of(x.x[e], top, steep));
       }
+      w = sum.total();
+      if (out_row != nullptr)
+        for (int pos = s.run_a * kElems + lane; pos < s.run_z * kElems; pos += 32)
+          if (pos >= s.phase && pos < s.phase + s.n) out_row[pos - s.phase] = reinterpret_cast<const Elem*>(dyn)[pos];
     }
     w = warp_sum(w);
+    if (by_count && nucleus) cluster_sync();  // sh.z may be written again
     if (lane == 0) sh.seg[warp] = w;
     __syncthreads();
     if (tid == 0) {
@@ -469,28 +776,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
     if (r == rank) mine = zr;
     z += zr;
   }
-  for (int j = warp; j < p.M; j += kWarps) {
+  // ---- the draws: the CTA that holds a draw's crossing, its warp, its logit -----------------------
+  for (int j = 0; j < p.M; ++j) {
     const uint32_t u24 = static_cast<uint32_t>(p.uniforms[row * p.M + j] * 16777216.0f);
     uint64_t t = share_of(z, u24);
-    if (t < before || t >= before + mine) continue;  // another CTA's
+    if (t < before || t >= before + mine) continue;
     t -= before;
-    int seg = 0;
-    while (seg < kWarps - 1 && t >= sh.seg[seg]) t -= sh.seg[seg++];
-    const int a = min(s.vecs, seg * run), b_end = min(s.vecs, a + run);
-    for (int vb = a; vb < b_end; vb += 32) {
-      const int v = vb + lane;
-      uint64_t each[kElems], sum = 0;
-#pragma unroll
-      for (int e = 0; e < kElems; ++e) each[e] = 0;
-      if (v < b_end) {
-        const Vec<DT> x(s.vec(v));
-#pragma unroll
-        for (int e = 0; e < kElems; ++e) {
-          if (keeps(x.x[e], s.index(v, e))) each[e] = weight_of(exponent_of(x.x[e], top, steep));
-          sum += each[e];
-        }
-      }
-      uint64_t incl = sum;
+    uint64_t ahead = 0;
+    for (int i = 0; i < warp; ++i) ahead += sh.seg[i];
+    if (t < ahead || t >= ahead + sh.seg[warp]) continue;  // the warp that owns the run draws
+    t -= ahead;
+    bool open = true;
+    auto look = [&](int pos, float x) {
+      if (!open) return;
+      const uint64_t w = pos >= 0 && (!cuts || keeps(pos, x)) ? weight_of(exponent_of(x, top, steep)) : 0;
+      uint64_t incl = w;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -498,25 +798,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
       }
       const uint64_t all = __shfl_sync(0xFFFFFFFFu, incl, 31);
       if (t < all) {
-        if (t < incl && t >= incl - sum) {
-          uint64_t left = t - (incl - sum);
-          int e = 0;
-#pragma unroll
-          for (int i = 0; i < kElems - 1; ++i)
-            if (e == i && left >= each[i]) {
-              left -= each[i];
-              e = i + 1;
-            }
-          uint64_t w = 0;
-#pragma unroll
-          for (int i = 0; i < kElems; ++i) w = e == i ? each[i] : w;
-          p.out_tokens[row * p.M + j] = s.index(v, e);
+        if (t < incl && t >= incl - w) {
+          p.out_tokens[row * p.M + j] = s.index_of(pos);
           if (p.out_probs != nullptr) p.out_probs[row * p.M + j] = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(z));
         }
-        break;
+        open = false;
       }
       t -= all;
-    }
+    };
+    for_candidates<DT>(s, sh, listed, bound, look);
   }
   cluster_sync();  // no CTA leaves while a peer may still read its shared memory
 }

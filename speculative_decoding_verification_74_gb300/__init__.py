@@ -155,7 +155,7 @@ def _need(t, name: str, dtype, count: int = 0) -> None:
         return
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if count > 0:
+    if count > 0 and not (count <= t.numel() and t.is_contiguous()):  # (a contiguous tensor holds its elements)
         avail = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
         if avail < count:
             raise ValueError(f"{name} holds {avail} elements from its data pointer, the call reads {count}")
@@ -174,8 +174,13 @@ def _ws_bytes(ws) -> int:
     return 0 if ws is None else ws.numel() * ws.element_size()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():  # without building a Stream object
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -643,6 +648,20 @@ def schedule_depth(alpha, cost_a, cost_b, budget, *, draft_len=None, ratios=None
 # the round around verification: sampling, the paged cache, tree attention
 # ------------------------------------------------------------------------------------------
 
+def _array(t, name: str, dtype, count: int) -> int | None:
+    """Pointer of a contiguous device array of at least `count` elements (None = NULL)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= count:
+        return t.data_ptr()
+    _need(t, name, dtype, count)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < count:
+        raise ValueError(f"{name} holds {t.numel()} elements, the call reads {count}")
+    return _p(t)
+
+
 def _zeros(nbytes: int, device, stream) -> torch.Tensor:
     """A zero-filled workspace whose fill is ordered before the call on `stream`."""
     if stream is None:
@@ -666,8 +685,6 @@ def sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None,
     filtered or None); out = (tokens, probs) takes the place of new tensors."""
     if logits.dim() != 2 or uniforms.dim() != 2 or uniforms.shape[0] != logits.shape[0]:
         raise ValueError("sample() takes logits [R, V] and uniforms [R, M]")
-    if not uniforms.is_contiguous():
-        raise ValueError("uniforms must be contiguous")
     R, V = logits.shape
     M = uniforms.shape[1]
     dt = _dt(logits)
@@ -675,14 +692,23 @@ def sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None,
     if out is None:
         out = (torch.empty((R, M), dtype=torch.int32, device=dev),
                torch.empty((R, M), dtype=torch.float32, device=dev) if probs else None)
-    if filtered is True:
-        filtered = torch.empty((R, V), dtype=logits.dtype, device=dev)
-    if filtered is not None and filtered.shape != logits.shape:
-        raise ValueError("filtered must have the shape of logits")
+    row_stride = _rows(logits)[1] if R > 1 else V
+    out_stride = V
+    if filtered is not None:
+        if filtered is True:
+            filtered = torch.empty((R, V), dtype=logits.dtype, device=dev)
+        if filtered.shape != logits.shape or filtered.dtype != logits.dtype:
+            raise ValueError("filtered must have the shape and type of logits")
+        out_stride = _rows(filtered)[1] if R > 1 else V
     if ws is None:
         ws = _zeros(SV_STATUS_BYTES, dev, stream)
-    sv_sample_rows(logits, _rows(logits)[1] if R > 1 else V, dt, R, V, temperature, top_k, top_p, min_p, uniforms, M,
-                   out[0], out[1], filtered, V if filtered is None or R <= 1 else _rows(filtered)[1], ws, stream)
+    n = R * M
+    f32, i32 = torch.float32, torch.int32
+    _check((_lib or lib()).sv_sample_rows(
+        _p(logits), row_stride, dt, R, V, _array(temperature, "temperature", f32, R), _array(top_k, "top_k", i32, R),
+        _array(top_p, "top_p", f32, R), _array(min_p, "min_p", f32, R), _array(uniforms, "uniforms", f32, n), M,
+        _array(out[0], "tokens", i32, n), _array(out[1], "probs", f32, n), _p(filtered), out_stride, _p(ws), _ws_bytes(ws),
+        _stream(stream)))
     return out[0], out[1], filtered
 
 
@@ -705,18 +731,22 @@ class PagedCache:
         _need(k, "k", torch.bfloat16)
         if k.stride(4) != 1:
             raise ValueError("the head dimension must be contiguous")
-        _need(page_refs, "page_refs", torch.int32, k.shape[1])
-        _need(page_table, "page_table", torch.int32)
-        if page_table.dim() != 2 or not page_table.is_contiguous() or not page_refs.is_contiguous():
-            raise ValueError("page_table [sequences, entries] and page_refs must be contiguous")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [sequences, entries]")
         self.k, self.v, self.page_refs, self.page_table = k, v, page_refs, page_table
         self.rows, self.width = page_table.shape
         L, P, S, H, D = k.shape
         # a dimension of size 1 is never stepped along: its stride only has to be a valid one
         st = [k.stride(i) if k.shape[i] > 1 else max(8, D) for i in range(4)]
+        self.kv_heads, self.head_dim = H, D
         self.c = sv_cache(k=_p(k), v=_p(v), layer_stride=st[0], page_stride=st[1], slot_stride=st[2], head_stride=st[3],
-                          layers=L, pages=P, page_size=S, kv_heads=H, head_dim=D, page_refs=_p(page_refs))
+                          layers=L, pages=P, page_size=S, kv_heads=H, head_dim=D,
+                          page_refs=_array(page_refs, "page_refs", torch.int32, P))
         self.ws = torch.zeros(SV_CACHE_WORKSPACE_BYTES, dtype=torch.uint8, device=k.device) if ws is None else ws
+        # what every call passes: the struct, the table, the workspace
+        self._c = _c.addressof(self.c)
+        self._table = _array(page_table, "page_table", torch.int32, self.rows * self.width)
+        self._ws, self._ws_bytes = _p(self.ws), _ws_bytes(self.ws)
 
     @classmethod
     def empty(cls, layers, pages, page_size, kv_heads, head_dim, sequences, entries, device="cuda"):
@@ -736,9 +766,12 @@ class PagedCache:
         """Pages for slots [0, seq_len + extra) of rows 0..B-1, B = extra.numel().  Returns ok [B] int32: 1 where
         served."""
         B = self._batch(extra.numel())
+        i32 = torch.int32
         if ok is None:
-            ok = torch.empty(B, dtype=torch.int32, device=extra.device)
-        sv_cache_reserve(self.c, self.page_table, self.width, seq_len, extra, B, ok, self.ws, stream)
+            ok = torch.empty(B, dtype=i32, device=extra.device)
+        _check((_lib or lib()).sv_cache_reserve(
+            self._c, self._table, self.width, _array(seq_len, "seq_len", i32, B), _array(extra, "extra", i32, B), B,
+            _array(ok, "ok", i32, B), self._ws, self._ws_bytes, _stream(stream)))
         return ok
 
     def append(self, k_new, v_new, seq_len, node_offsets, layer=0, *, stream=None):
@@ -746,42 +779,57 @@ class PagedCache:
         head_dim] for one layer: node c of request i (row node_offsets[i] + c) to slot seq_len[i] + c."""
         if k_new.dim() == 3:
             k_new, v_new = k_new.unsqueeze(0), v_new.unsqueeze(0)
-        if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[2:] != self.k.shape[3:]:
+        if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.shape[2] != self.kv_heads or k_new.shape[3] != self.head_dim:
             raise ValueError("k_new and v_new must be [layers, rows, kv_heads, head_dim] of this cache's heads")
         L, n, H, D = k_new.shape
-        if k_new.numel() and (k_new.stride() != v_new.stride() or k_new.stride(3) != 1 or (H > 1 and k_new.stride(2) != D)):
+        st = k_new.stride()
+        if L * n and (st != v_new.stride() or st[3] != 1 or (H > 1 and st[2] != D)):
             raise ValueError("k_new and v_new need the same strides and contiguous [kv_heads, head_dim]")
-        sv_cache_append(self.c, layer, L, self.page_table, self.width, seq_len, node_offsets, n, k_new, v_new,
-                        k_new.stride(0) if L > 1 else 0, k_new.stride(1) if n > 1 else H * D,
-                        self._batch(node_offsets.numel() - 1), self.ws, stream)
+        if k_new.dtype is not torch.bfloat16 or v_new.dtype is not torch.bfloat16:
+            raise ValueError("k_new and v_new must be torch.bfloat16")
+        B = self._batch(node_offsets.numel() - 1)
+        i32 = torch.int32
+        _check((_lib or lib()).sv_cache_append(
+            self._c, layer, L, self._table, self.width, _array(seq_len, "seq_len", i32, B),
+            _array(node_offsets, "node_offsets", i32, B + 1), n, _p(k_new), _p(v_new), st[0] if L > 1 else 0,
+            st[1] if n > 1 else H * D, B, self._ws, self._ws_bytes, _stream(stream)))
 
     def commit(self, seq_len, node_offsets, path, accept_len, *, out_len=None, stream=None):
         """Keeps the accepted path (verify_tree's outputs path [B, Nmax] and accept_len [B]) in every layer and gives
         the pages past it back.  Returns the new lengths (written to out_len; it may be seq_len)."""
-        if path.dim() != 2 or not path.is_contiguous():
-            raise ValueError("path must be contiguous [B, Nmax]")
-        B = self._batch(path.shape[0])
+        if path.dim() != 2:
+            raise ValueError("path must be [B, Nmax]")
+        B, Nmax = path.shape
+        self._batch(B)
+        i32 = torch.int32
         if out_len is None:
-            out_len = torch.empty(B, dtype=torch.int32, device=path.device)
-        sv_cache_commit(self.c, self.page_table, self.width, seq_len, node_offsets, path, accept_len, B, path.shape[1],
-                        out_len, self.ws, stream)
+            out_len = torch.empty(B, dtype=i32, device=path.device)
+        _check((_lib or lib()).sv_cache_commit(
+            self._c, self._table, self.width, _array(seq_len, "seq_len", i32, B),
+            _array(node_offsets, "node_offsets", i32, B + 1), _array(path, "path", i32, B * Nmax),
+            _array(accept_len, "accept_len", i32, B), B, Nmax, _array(out_len, "out_len", i32, B), self._ws, self._ws_bytes,
+            _stream(stream)))
         return out_len
 
     def fork(self, seq_len, src, dst, *, ok=None, stream=None):
         """Rows dst become copies of rows src (full pages shared); seq_len is updated.  Returns ok [n] int32."""
         n = src.numel()
-        if dst.numel() != n or seq_len.numel() < self.rows:
-            raise ValueError("src and dst must have one length, seq_len an entry per row of the page table")
+        i32 = torch.int32
         if ok is None:
-            ok = torch.empty(n, dtype=torch.int32, device=src.device)
-        sv_cache_fork(self.c, self.page_table, self.width, self.rows, seq_len, src, dst, n, ok, self.ws, stream)
+            ok = torch.empty(n, dtype=i32, device=src.device)
+        _check((_lib or lib()).sv_cache_fork(
+            self._c, self._table, self.width, self.rows, _array(seq_len, "seq_len", i32, self.rows),
+            _array(src, "src", i32, n), _array(dst, "dst", i32, n), n, _array(ok, "ok", i32, n), self._ws, self._ws_bytes,
+            _stream(stream)))
         return ok
 
     def release(self, seq_len, seqs, *, stream=None):
         """Gives the pages of rows seqs back and empties them (seq_len = 0)."""
-        if seq_len.numel() < self.rows:
-            raise ValueError("seq_len needs an entry per row of the page table")
-        sv_cache_release(self.c, self.page_table, self.width, self.rows, seq_len, seqs, seqs.numel(), self.ws, stream)
+        n = seqs.numel()
+        i32 = torch.int32
+        _check((_lib or lib()).sv_cache_release(
+            self._c, self._table, self.width, self.rows, _array(seq_len, "seq_len", i32, self.rows),
+            _array(seqs, "seqs", i32, n), n, self._ws, self._ws_bytes, _stream(stream)))
 
 
 def attention_workspace(cache: PagedCache, q_heads: int) -> torch.Tensor:
@@ -799,24 +847,31 @@ def tree_attention(q, cache: PagedCache, layer, seq_len, node_offsets, parent, N
     c (cache.append); parent [rows] int32 as in verify_tree, or None for chains; at most Nmax nodes a request.  window,
     sinks: a sliding window of that many positions and the first positions that stay visible.  Returns (out like q,
     lse [rows, q_heads] float32, or None with lse=False)."""
-    if q.dim() != 3 or q.shape[2] != cache.k.shape[4]:
+    bf16, i32 = torch.bfloat16, torch.int32
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError("q must be [rows, q_heads, head_dim] of the cache's head_dim")
     n, H, D = q.shape
-    if q.numel() and q.stride(2) != 1:
-        raise ValueError("the head dimension of q must be contiguous")
     if out is None:
-        out = torch.empty((n, H, D), dtype=torch.bfloat16, device=q.device)
-    if out.shape != q.shape or (out.numel() and out.stride(2) != 1):
-        raise ValueError("out must have q's shape and a contiguous head dimension")
+        out = torch.empty((n, H, D), dtype=bf16, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if q.dtype is not bf16 or out.dtype is not bf16:
+        raise ValueError("q and out must be torch.bfloat16")
     if lse is True:
         lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
     elif lse is False:
         lse = None
     if ws is None:
         ws = _zeros(sv_attention_workspace_size(cache.c, H), q.device, stream)
-    step = lambda t, d, least: t.stride(d) if t.shape[d] > 1 else least  # noqa: E731
-    sv_tree_attention(cache.c, layer, q, step(q, 0, H * D), step(q, 1, D), H, cache.page_table, cache.width, seq_len,
-                      node_offsets, n, parent, cache._batch(node_offsets.numel() - 1), Nmax,
-                      D ** -0.5 if scale is None else scale, window, sinks, out, step(out, 0, H * D), step(out, 1, D),
-                      lse, ws, stream)
+    qs, os = q.stride(), out.stride()
+    if n * H and (qs[2] != 1 or os[2] != 1):
+        raise ValueError("the head dimension of q and out must be contiguous")
+    B = cache._batch(node_offsets.numel() - 1)
+    # a dimension of size 1 is never stepped along: its stride only has to be a valid one
+    _check((_lib or lib()).sv_tree_attention(
+        cache._c, layer, _p(q), qs[0] if n > 1 else H * D, qs[1] if H > 1 else D, H, cache._table, cache.width,
+        _array(seq_len, "seq_len", i32, B), _array(node_offsets, "node_offsets", i32, B + 1), n,
+        _array(parent, "parent", i32, n), B, Nmax, D ** -0.5 if scale is None else scale, window, sinks, _p(out),
+        os[0] if n > 1 else H * D, os[1] if H > 1 else D, _array(lse, "lse", torch.float32, n * H), _p(ws), _ws_bytes(ws),
+        _stream(stream)))
     return out, lse

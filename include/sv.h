@@ -506,7 +506,7 @@ sv_status sv_cache_release(const sv_cache* c, int32_t* page_table, int table_wid
  *   lse[c, h] = log sum_s exp(scale q[c, h] . k[s, g])
  * q, out: bf16, row node_offsets[i] + c at row * row_stride + h * head_stride (elements; q strides multiples of 8
  * and q 16-byte aligned; out strides multiples of 8 and out 16-byte aligned); n_rows rows.  out_lse (nullable): float32
- * [n_rows, q_heads].  q_heads a multiple of kv_heads.  Products of bf16 are summed in float32; softmax weights are rounded to bf16
+ * [n_rows, q_heads].  q_heads a multiple of kv_heads, at most 128 times it.  Products of bf16 are summed in float32; softmax weights are rounded to bf16
  * for the product with v, their sum is not.
  * The keys and values of visible slots must be finite; slots of other requests, past the tree or outside
  * every node's window may hold anything.  A request whose rows do not lie in [0, n_rows), with N_i

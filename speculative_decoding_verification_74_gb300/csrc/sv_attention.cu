@@ -1,20 +1,26 @@
 // sv_tree_attention: a token tree's queries against a paged cache.
 //
-// Rows and tiles.  A request's query rows of one key/value head (its nodes times the query heads that
-// share the head) form tiles of 128 rows, the height of a tcgen05 product; the cache is read in tiles of
-// 128 slots.  For a tile of rows, with c = scale log2(e) and running maximum m:
+// Rows and tiles.  The query heads that share a key/value head, for as many nodes as fit into 128 rows (the height of
+// a tcgen05 product), form a row tile; the cache is read in tiles of 128 slots.  For a row tile, with c = scale
+// log2(e) and running maximum m:
 //   S = Q K^T          [128 x 128], accumulated in tensor memory
 //   P = 2^(c S - m)    bf16, written back to tensor memory over S
-//   O = O + P V        in tensor memory; l = l + row sums of P (float32, before P's rounding)
-// and at the end o = O / l, lse = (m + log2 l) ln 2.  O is scaled by 2^(m - m') only when some row's maximum has
-// grown by more than 8 (P stays below 2^8, so float32 sums and bf16's range are far from their ends).
+//   O = O + P V        in tensor memory
+// and at the end o = O / (sum of the rounded P), lse = (m + log2 sum P) ln 2.  O is scaled by 2^(m - m') only when some
+// row's maximum has grown by more than 8 (P stays below 2^8, so float32 sums and bf16's range are far from their ends).
 //
 // Work split.  All (row tile, cache tile) pairs of the batch lie on one line; CTA c of C takes the c-th part of
-// it (a persistent CTA per SM).  A row tile whose line part crosses CTAs leaves partial (O, m, l) in the workspace,
-// and join_kernel adds them.  So one long context and many short ones load the SMs alike.
+// it (a persistent CTA per SM), in segments: stretches of one row tile.  A row tile that crosses CTAs leaves partial (O, m,
+// sums) in the workspace, and join_kernel adds them.  So one long context and many short ones load the SMs alike.
 //
-// Roles in a CTA: warp 0 copies tiles (TMA, page by page, through a ring of stages); one thread of warp 1 issues the
-// products; warps 2 to 5 own a row per thread: they load Q, turn S into P and read O.
+// Few rows.  A row of S belongs to one lane of tensor memory, and a quarter of its lanes to one of the SM's four
+// schedulers.  So a tile of at most 64 (32) rows is multiplied with Q's rows two (four) times over, one copy per half (quarter)
+// of the lanes, and each copy takes the exponentials of its half (quarter) of the slots; P is 0 elsewhere.  The copies' (O,
+// m, sums) are added at the end of a segment, like those of the two groups.
+//
+// Roles in a CTA: warps 0 and 11 copy K and V page by page through a ring of stages (TMA; one warp alone needs 1.1 us a
+// tile for it); one thread of warp 1 issues the products; warp 10 brings each segment's description, parents and Q; two groups of four warps take the tiles in turn (a
+// thread has a row), each with its own S and O, so one group's exponentials run beside the other's products.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -30,30 +36,33 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 128;                 // rows of Q, and slots of the cache, in a tile
-constexpr int kSoftThreads = 128;
-constexpr int kThreads = 64 + kSoftThreads;
+constexpr int kGroupThreads = 128;
+constexpr int kSoftThreads = 2 * kGroupThreads;
+constexpr int kThreads = 128 + kSoftThreads;
+constexpr int kWarpK = 0, kWarpMma = 1, kWarpQ = 10, kWarpV = 11;  // 2 to 9: the two groups
 constexpr int kHalfBytes = kTile * 128;    // 128 slots of 64 bf16: one swizzled column block
 constexpr int kTmemColumns = 512;
-constexpr int kColS = 0, kColO = 256;      // S / P buffers at columns 0 and 128, O at 256
+// Tensor memory by group: S at columns 0 and 128, O from 256 on.  With 128 dimensions P lies over S, so a group's next
+// S waits for its product P V; with 64 there is room for P, and S only waits until the softmax has read it.
+template <int D>
+struct Columns {
+  static constexpr bool kOwnP = D == 64;
+  static __device__ __forceinline__ constexpr uint32_t s(uint32_t g) { return g * 128; }
+  static __device__ __forceinline__ constexpr uint32_t o(uint32_t g) { return 256 + g * D; }
+  static __device__ __forceinline__ constexpr uint32_t p(uint32_t g) { return kOwnP ? 384 + g * 64 : g * 128; }
+};
 constexpr float kLazyGrowth = 8.0f;        // log2 units by which a maximum may grow without a rescale of O
 constexpr int kJoinRows = 16;              // rows per CTA of the join
-
-// Stages of 32 KB (D = 128) or 16 KB: five tiles' halves in flight keep about 160 KB on the way per SM.
-template <int D>
-struct Shape {
-  static constexpr int kHalves = D / 64;
-  static constexpr int kStageBytes = kHalves * kHalfBytes;
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kQBytes = kHalves * kHalfBytes;
-};
+constexpr int kMaxStages = 12;
+constexpr int kMaxCtas = 152;              // SMs of the GPU: one CTA each
+constexpr int kSmemMax = 232448;           // shared memory that a CTA can have
 
 struct alignas(16) Job {  // a row tile that several CTAs worked on: parts of CTAs `first` to `last`
   int32_t valid, request, head, mtile, rows, first, last, pad;
 };
 
 struct AttendParams {
-  const __nv_bfloat16* q;
-  int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+  int64_t out_row_stride, out_head_stride;
   const int32_t *table, *seq_len, *node_offsets, *parent;
   __nv_bfloat16* out;
   float* lse;
@@ -64,12 +73,15 @@ struct AttendParams {
   float* parts;       // [2 grid] partial results
   int64_t n_rows;
   int32_t width, B, Nmax, pages, shift, q_heads, kv_heads, group, window, sinks;
+  int32_t tile_nodes;  // nodes of a row tile
+  uint32_t over_group; // ceil(2^16 / group)
+  int32_t stages;
   float scale;
 };
 
-// Floats of one partial result: O as [D / 4][128 rows][4], then m and l per row.
+// Floats of one partial result: O as [D / 4][128 rows][4], then m and the two sums per row.
 template <int D>
-constexpr int part_floats() { return kTile * D + 2 * kTile; }
+constexpr int part_floats() { return kTile * D + 3 * kTile; }
 
 // ---- tcgen05 -----------------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst) {
@@ -110,6 +122,13 @@ constexpr uint32_t instr_desc(int n, bool b_rows_are_k) {
          (static_cast<uint32_t>(kTile >> 4) << 24);
 }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 #define SV_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
 #define SV_I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
 // 32 columns of this warp's 32 rows: lane r holds row r.
@@ -128,8 +147,35 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* x) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// After the wait, loaded registers may be used: the empty statements keep their uses behind it.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&x)[N]) {
+  tmem_wait_load();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i]));
+}
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : SV_R8(x, 0), SV_R8(x, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::SV_I8(x, 0),
+      SV_I8(x, 8), "r"(addr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
@@ -152,7 +198,7 @@ struct Request {
   int32_t mtiles;      // row tiles per key/value head
   uint32_t bad;        // SV_DEV_* bits
 };
-__device__ __forceinline__ Request request_of(const AttendParams& a, int i) {
+__device__ __noinline__ Request request_of(const AttendParams& a, int i) {
   Request r = {};
   const int64_t first = a.node_offsets[i], last = a.node_offsets[i + 1];
   const int64_t len = a.seq_len[i], nodes = last - first;
@@ -175,7 +221,7 @@ __device__ __forceinline__ Request request_of(const AttendParams& a, int i) {
     r.sink_tiles = min(static_cast<int>((static_cast<int64_t>(min(a.sinks, lo)) + kTile - 1) / kTile), r.near_tile);
   }
   r.tiles = r.sink_tiles + all - r.near_tile;
-  r.mtiles = (r.nodes * a.group + kTile - 1) / kTile;
+  r.mtiles = (r.nodes + a.tile_nodes - 1) / a.tile_nodes;
   return r;
 }
 
@@ -184,7 +230,7 @@ struct Segment {
   Request r;
   int32_t request, head, mtile, kv0, kv1;
 };
-__device__ __forceinline__ Segment segment_at(const AttendParams& a, const uint32_t* before, uint32_t t, uint32_t end) {
+__device__ __noinline__ Segment segment_at(const AttendParams& a, const uint32_t* before, uint32_t t, uint32_t end) {
   int lo = 0, hi = a.B;  // the last request whose tiles begin at or before t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -203,9 +249,17 @@ __device__ __forceinline__ Segment segment_at(const AttendParams& a, const uint3
 __device__ __forceinline__ int tile_slot(const Request& r, int j) {
   return (j < r.sink_tiles ? j : r.near_tile + (j - r.sink_tiles)) * kTile;
 }
-__device__ __forceinline__ uint32_t part_begin(uint32_t total, uint32_t c, uint32_t n) {
+__device__ __noinline__ uint32_t part_begin(uint32_t total, uint32_t c, uint32_t n) {
   return static_cast<uint32_t>(static_cast<uint64_t>(total) * c / n);
 }
+// The CTA (of n) whose part of the line holds tile `at`.
+__device__ __noinline__ int part_of(uint32_t total, uint32_t at, uint32_t n) {
+  uint32_t c = static_cast<uint32_t>(static_cast<uint64_t>(at) * n / total);
+  while (part_begin(total, c + 1, n) <= at) ++c;
+  return static_cast<int>(c);
+}
+// row / group for row < 128, group <= 128: over = ceil(2^16 / group).
+__device__ __forceinline__ int over_group(int row, uint32_t over) { return static_cast<int>((row * over) >> 16); }
 
 // Bits [lo, hi) of a 32-bit word whose bit 0 stands for position `at`.
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int at) {
@@ -214,27 +268,46 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int at) {
   return (b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-template <int D>
+// The part of shared memory with a fixed size; then come the tiles before each request [B], the parents of two segments'
+// trees [2][Nmax] and, 1024-byte aligned, Q and the ring.
 struct Smem {
-  alignas(1024) unsigned char q[Shape<D>::kQBytes];
-  alignas(1024) unsigned char stage[Shape<D>::kStages][Shape<D>::kStageBytes];
-  alignas(16) uint64_t full[Shape<D>::kStages];
-  uint64_t empty[Shape<D>::kStages];
-  uint64_t s_full[2], p_full[2], pv_done, q_full;
+  Segment seg[2];              // by the segment's parity
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t q_full[2];          // by the segment's parity: its Q and description are there
+  uint64_t q_free;             // once per segment: its last S is complete
+  uint64_t seg_free[2];        // every softmax thread is done with a description
+  uint64_t s_full[2], p_full[2], pv_done[2];  // by group
+  uint64_t sums_full, o_free;  // once per segment: the groups' sums are there; every thread has read O
+  uint64_t mix_full[2], mix_free[2];  // by group: copies' columns written, read
+  float m[2][2][kTile], l[2][2][kTile], lr[2][2][kTile];  // by the segment's parity and group
+  float4 mix[2][4 * kGroupThreads];   // by group: columns of every copy's rows, four columns of all rows together
+  uint32_t scan[kThreads / 32];
   uint32_t tmem;
   volatile int32_t dead;       // a wait ran out: everyone leaves
-  uint32_t scan[kThreads / 32 + 1];
-  int32_t parent[SV_MAX_DRAFT + 1];
-  uint32_t before[1];          // [B + 1] tiles of the requests before
 };
 
-__device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
-  if (*dead) return false;
-  if (mbar_wait(bar, parity, status)) return true;
+// Bounded wait (about 2 s), polling: the waits between products and softmax are a fraction of a microsecond each, and
+// a suspended try_wait oversleeps them.  The loop is not inlined: with it at every wait the kernel's code does not
+// stay in the instruction cache.
+__device__ __noinline__ bool still_waiting(uint64_t* began, volatile int32_t* dead, uint32_t* status) {
+  const uint64_t now = globaltimer_ns();
+  if (*began == 0) *began = now;
+  if (!*dead && now - *began <= kWaitLimitNs) return true;
+  atomicOr(status, SV_DEV_TIMEOUT);
   *dead = 1;
   return false;
 }
-
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
+  uint64_t began = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (it >= 16) __nanosleep(40);
+    if (mbar_test_wait(bar, parity)) return true;
+    if ((it & 255u) == 0 && !still_waiting(&began, dead, status)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
+  return mbar_test_wait(bar, parity) || wait_slow(bar, parity, dead, status);
+}
 // The same by a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
   return __all_sync(0xFFFFFFFFu, wait_or_leave(bar, parity, dead, status));
@@ -246,41 +319,67 @@ __device__ __forceinline__ void mark_bad(const AttendParams& a, int request, uin
   atomicOr(a.status, bits);
 }
 
-template <int D>
+// A place in the ring of stages and the parity of its present round.
+struct Ring {
+  uint32_t stage = 0, parity = 0;
+  __device__ __forceinline__ void step(uint32_t stages) {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+template <int D, int kCopies>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_kernel(const AttendParams a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-  using Sh = Shape<D>;
+    attend_kernel(const AttendParams a, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map) {
+  using Col = Columns<D>;
+  constexpr int kHalves = D / 64;
+  constexpr int kStageBytes = kHalves * kHalfBytes;
   extern __shared__ unsigned char dyn[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ Smem sm;
+  uint32_t* before = reinterpret_cast<uint32_t*>(dyn);           // [B]
+  int32_t* parents = reinterpret_cast<int32_t*>(dyn) + a.B;      // [2][Nmax]
+  unsigned char* q_buf = dyn + 4 * (a.B + 2 * a.Nmax);
+  q_buf += (1024u - (smem_u32(q_buf) & 1023u)) & 1023u;
+  unsigned char* ring = q_buf + kHalves * kHalfBytes;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (known to be the same in all lanes)
   if (tid == 0) {
-    for (int i = 0; i < Sh::kStages; ++i) {
+    for (int i = 0; i < a.stages; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
+    mbar_init(&sm.q_free, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.seg_free[i], kSoftThreads);
+      mbar_init(&sm.mix_full[i], kGroupThreads);
+      mbar_init(&sm.mix_free[i], kGroupThreads);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kSoftThreads);
+      mbar_init(&sm.p_full[i], kGroupThreads);
+      mbar_init(&sm.pv_done[i], 1);
     }
-    mbar_init(&sm.pv_done, 1);
-    mbar_init(&sm.q_full, kSoftThreads);
+    mbar_init(&sm.sums_full, kSoftThreads);
+    mbar_init(&sm.o_free, kSoftThreads);
     sm.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == 1) tmem_alloc(&sm.tmem);
+  if (warp == kWarpMma) tmem_alloc(&sm.tmem);
   pdl_wait();
   pdl_trigger();
   // tiles before each request
   uint32_t total;
   {
     const int per = (a.B + kThreads - 1) / kThreads;
-    const int i0 = tid * per, i1 = min(a.B, i0 + per);
+    const int i0 = min(a.B, tid * per), i1 = min(a.B, i0 + per);
     uint32_t sum = 0;
     for (int i = i0; i < i1; ++i) {
       const Request r = request_of(a, i);
       if (r.bad != 0 && blockIdx.x == 0) mark_bad(a, i, r.bad);
-      sm.before[i] = sum;
+      before[i] = sum;
       sum += static_cast<uint32_t>(r.tiles) * r.mtiles * a.kv_heads;
     }
     uint32_t x = sum;
@@ -299,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) at += sm.scan[w];
       total += sm.scan[w];
     }
-    for (int i = i0; i < i1; ++i) sm.before[i] += at;
+    for (int i = i0; i < i1; ++i) before[i] += at;
     __syncthreads();
   }
   const uint32_t tmem = sm.tmem;
@@ -307,314 +406,510 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t parts = min(gridDim.x, total);
   const uint32_t t0 = blockIdx.x < parts ? part_begin(total, blockIdx.x, parts) : total;
   const uint32_t t1 = blockIdx.x < parts ? part_begin(total, blockIdx.x + 1, parts) : total;
-  uint32_t loaded = 0;  // stages that the producer filled
+  const uint32_t stages = a.stages;
+  uint32_t loaded = 0, segments = 0;  // stages and Q's that were asked for
 
-  if (warp == 0) {
+  if (warp == kWarpK || warp == kWarpV) {
     // ---- copies -----------------------------------------------------------------------------------
-    const int box = min(kTile, 1 << a.shift), chunks = kTile / box;  // pages (or one part of a page) per tile
+    const int box_shift = min(7, a.shift), box = 1 << box_shift;  // slots per copy: a page, or 128 slots of one
+    const int chunks = kTile >> box_shift;
     bool go = true;
+    const uint32_t second = warp == kWarpV;  // K's and V's stages alternate
+    const CUtensorMap* map = second ? &v_map : &k_map;
+    Ring at;
+    if (second) at.step(stages);
+    loaded = second;
+    // page numbers of 32 copies at a time (a copy's page: lane = its number in the block), one block ahead
+    auto pages_of = [&](const Segment& s, int block) {
+      const int64_t slot = (static_cast<int64_t>(block) * 32 + lane) << box_shift;
+      return slot < s.r.len + s.r.nodes ? a.table[static_cast<int64_t>(s.request) * a.width + (slot >> a.shift)] : -1;
+    };
+    Segment s = {}, next = {};  // the next segment and its first pages are looked up while the ring is full
+    int block = 0, page_now = -1, page_next = -1, next_block = 0, next_now = -1;
+    if (t0 < t1) {
+      s = segment_at(a, before, t0, t1);
+      block = tile_slot(s.r, s.kv0) >> (box_shift + 5);
+      page_now = pages_of(s, block);
+    }
     for (uint32_t t = t0; t < t1 && go;) {
-      const Segment s = segment_at(a, sm.before, t, t1);
       const int end = s.r.len + s.r.nodes, lo = a.window > 0 ? max(0, s.r.len - a.window + 1) : 0;
-      const int32_t* row = a.table + static_cast<int64_t>(s.request) * a.width;
+      const uint32_t after = t + (s.kv1 - s.kv0);
+      page_next = pages_of(s, block + 1);
       for (int j = s.kv0; j < s.kv1 && go; ++j) {
         const int s0 = tile_slot(s.r, j);
-        // lane x < chunks looks its page up; a page without a visible slot is left out
-        int page = -1;
-        bool wanted = false;
-        if (lane < chunks) {
-          const int at = s0 + lane * box;
-          wanted = at < end && (a.window <= 0 || at < a.sinks || at + box > lo);
-          if (wanted) {
-            page = row[at >> a.shift];
-            if (page < 0 || page >= a.pages) {
-              mark_bad(a, s.request, SV_DEV_BAD_PAGE);
-              page = a.pages;  // outside the tensor: the copy fills zeros
-            }
-          }
+        const int need = s0 >> (box_shift + 5);
+        if (need != block) {
+          page_now = need == block + 1 ? page_next : pages_of(s, need);
+          block = need;
+          page_next = pages_of(s, block + 1);
         }
-        const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, wanted)) * Sh::kHalves * box * 128;
-        for (int kv = 0; kv < 2; ++kv, ++loaded) {
-          const uint32_t st = loaded % Sh::kStages, round = loaded / Sh::kStages;
-          if (round > 0) go = warp_wait(&sm.empty[st], (round - 1) & 1, &sm.dead, a.status);
-          if (!go) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], bytes);
-          __syncwarp();
-          if (wanted) {
+        // lane x < chunks copies the x-th page's part; a page without a visible slot is left out
+        const int slot = s0 + (lane << box_shift);
+        int page = __shfl_sync(0xFFFFFFFFu, page_now, ((s0 >> box_shift) + lane) & 31);
+        const bool wanted = lane < chunks && slot < end && (a.window <= 0 || slot < a.sinks || slot + box > lo);
+        if (wanted && (page < 0 || page >= a.pages)) {
+          mark_bad(a, s.request, SV_DEV_BAD_PAGE);
+          page = a.pages;  // outside the tensor: the copy fills zeros
+        }
+        const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, wanted)) * kHalves * box * 128;
+        if (loaded >= stages) go = warp_wait(&sm.empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
+        if (!go) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.stage], bytes);
+        __syncwarp();
+        if (wanted) {
 #pragma unroll
-            for (int h = 0; h < Sh::kHalves; ++h)
-              tma_load_4d(sm.stage[st] + h * kHalfBytes + lane * box * 128, kv ? &v_map : &k_map, h * 64, s.head,
-                          (s0 + lane * box) & ((1 << a.shift) - 1), page, &sm.full[st]);
-          }
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_4d(ring + at.stage * kStageBytes + h * kHalfBytes + (lane << box_shift) * 128, map, h * 64, s.head,
+                        slot & ((1 << a.shift) - 1), page, &sm.full[at.stage]);
         }
+        loaded += 2;
+        at.step(stages);
+        at.step(stages);
+        if (j == max(s.kv0, s.kv1 - 2) && after < t1) {
+          next = segment_at(a, before, after, t1);
+          next_block = tile_slot(next.r, next.kv0) >> (box_shift + 5);
+          next_now = pages_of(next, next_block);
+        }
+      }
+      t = after;
+      s = next;
+      block = next_block;
+      page_now = next_now;
+    }
+  } else if (warp == kWarpQ) {
+    // ---- segments: description, parents, Q --------------------------------------------------------
+    constexpr int rows_apart = kTile / kCopies;
+    for (uint32_t t = t0; t < t1; ++segments) {
+      const Segment s = segment_at(a, before, t, t1);
+      const int b = segments & 1;
+      if (segments >= 2 && !warp_wait(&sm.seg_free[b], ((segments >> 1) - 1) & 1, &sm.dead, a.status)) break;
+      if (a.parent != nullptr)
+        for (int x = lane; x < s.r.nodes; x += 32) parents[b * a.Nmax + x] = a.parent[s.r.first + x];
+      if (lane == 0) sm.seg[b] = s;
+      if (segments >= 1 && !warp_wait(&sm.q_free, (segments - 1) & 1, &sm.dead, a.status)) break;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full[b], kCopies * kHalves * a.tile_nodes * a.group * 128);
+        for (int copy = 0; copy < kCopies; ++copy)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_3d(q_buf + h * kHalfBytes + copy * rows_apart * 128, &q_map, h * 64, s.head * a.group,
+                        static_cast<int>(s.r.first) + s.mtile * a.tile_nodes, &sm.q_full[b]);
       }
       t += s.kv1 - s.kv0;
     }
-  } else if (warp == 1) {
+  } else if (warp == kWarpMma) {
     // ---- products ---------------------------------------------------------------------------------
-    if (lane == 0) {
+    // The whole warp runs the loop, so counters and descriptors stay in uniform registers, which tcgen05.mma takes its
+    // operands from; one elected thread issues.
+    if (t0 < t1) {
+      const bool elected = elect_one();
+      auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
       constexpr uint32_t kDescS = instr_desc(kTile, false), kDescO = instr_desc(D, true);
-      const uint32_t q_addr = smem_u32(sm.q);
-      auto scores = [&](uint32_t n) {  // S of the n-th tile of this CTA
-        const uint32_t st = (2 * n) % Sh::kStages, round = (2 * n) / Sh::kStages;
-        if (!wait_or_leave(&sm.full[st], round & 1, &sm.dead, a.status)) return;
-        tc_after_sync();
-        const uint32_t k_addr = smem_u32(sm.stage[st]);
+      const uint32_t count = t1 - t0;
+      // descriptors by addition: their low words count 16-byte units of shared memory
+      const uint64_t q_desc0 = smem_desc(smem_u32(q_buf), 16, 1024), k_desc0 = smem_desc(smem_u32(ring), 16, 1024),
+                     v_desc0 = smem_desc(smem_u32(ring), kHalfBytes, 1024);
+      Ring ks, vs;  // K's and V's stages alternate
+      vs.step(stages);
+      uint32_t s_seg = 0, p_seg = 0;      // segments of the next S and the next P V
+      int s_left = 0, p_tiles = 0, p_j = 0;
+      uint32_t n = 0, i = 0;  // tiles of the next S and the next P V: whichever is ready is issued, so neither waits
+                              // behind the other's barriers
+      uint32_t idle = 0;
+      uint64_t began = 0;
+      while (i < count) {
+        bool issued = false;
+        if (n < count) {
+          if (s_left == 0 && ready(&sm.q_full[s_seg & 1], (s_seg >> 1) & 1))
+            s_left = __shfl_sync(0xFFFFFFFFu, sm.seg[s_seg & 1].kv1 - sm.seg[s_seg & 1].kv0, 0);
+          // the group's S was last read by the softmax, or by the product P V, of tile n - 2
+          if (s_left > 0 && ready(&sm.full[ks.stage], ks.parity) &&
+              (n < 2 || ready(Col::kOwnP ? &sm.p_full[n & 1] : &sm.pv_done[n & 1], ((n - 2) >> 1) & 1))) {
+            tc_after_sync();
+            const uint64_t k_desc = k_desc0 + ks.stage * (kStageBytes >> 4);
+            const uint32_t d = tmem + Col::s(n & 1);
+            --s_left;
+            if (elected) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * kHalfBytes + (k % 4) * 32;
-          mma_ss(tmem + kColS + (n & 1) * kTile, smem_desc(q_addr + off, 16, 1024), smem_desc(k_addr + off, 16, 1024), kDescS, k > 0);
-        }
-        tc_commit(&sm.s_full[n & 1]);
-        tc_commit(&sm.empty[st]);
-      };
-      uint32_t n = 0, seg = 0;
-      for (uint32_t t = t0; t < t1 && !sm.dead; ++seg) {
-        const Segment s = segment_at(a, sm.before, t, t1);
-        const int tiles = s.kv1 - s.kv0;
-        if (!wait_or_leave(&sm.q_full, seg & 1, &sm.dead, a.status)) break;
-        // S's buffer of tile n was last read by the product P V of tile n - 2 (and the barrier can
-        // only be asked about its latest phase)
-        if (n >= 1 && !wait_or_leave(&sm.pv_done, (n - 1) & 1, &sm.dead, a.status)) break;
-        scores(n);
-        for (int j = 0; j < tiles && !sm.dead; ++j, ++n) {
-          if (j + 1 < tiles) {
-            if (n >= 1 && !wait_or_leave(&sm.pv_done, (n - 1) & 1, &sm.dead, a.status)) break;
-            scores(n + 1);
+              for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ss(d, q_desc0 + h * (kHalfBytes >> 4) + 2 * k, k_desc + h * (kHalfBytes >> 4) + 2 * k, kDescS, h + k > 0);
+              tc_commit(&sm.s_full[n & 1]);
+              tc_commit(&sm.empty[ks.stage]);
+              if (s_left == 0) tc_commit(&sm.q_free);
+            }
+            ks.step(stages);
+            ks.step(stages);
+            s_seg += s_left == 0;
+            ++n;
+            issued = true;
           }
-          const uint32_t st = (2 * n + 1) % Sh::kStages, round = (2 * n + 1) / Sh::kStages;
-          if (!wait_or_leave(&sm.full[st], round & 1, &sm.dead, a.status)) break;
-          if (!wait_or_leave(&sm.p_full[n & 1], (n >> 1) & 1, &sm.dead, a.status)) break;
-          tc_after_sync();
-          const uint32_t v_addr = smem_u32(sm.stage[st]);
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem + kColO, tmem + kColS + (n & 1) * kTile + k * 8, smem_desc(v_addr + k * 2048, kHalfBytes, 1024), kDescO,
-                   j > 0 || k > 0);
-          tc_commit(&sm.pv_done);
-          tc_commit(&sm.empty[st]);
         }
-        t += tiles;
+        if (i < n) {
+          if (p_j == p_tiles) {
+            p_tiles = __shfl_sync(0xFFFFFFFFu, sm.seg[p_seg & 1].kv1 - sm.seg[p_seg & 1].kv0, 0);
+            p_j = 0;
+            ++p_seg;
+          }
+          // (at a segment's first tile both groups' O of the segment before have been read)
+          if (ready(&sm.p_full[i & 1], (i >> 1) & 1) && ready(&sm.full[vs.stage], vs.parity) &&
+              (p_j > 0 || p_seg < 2 || ready(&sm.o_free, (p_seg - 2) & 1))) {
+            tc_after_sync();
+            const uint64_t v_desc = v_desc0 + vs.stage * (kStageBytes >> 4);
+            const uint32_t d = tmem + Col::o(i & 1), p = tmem + Col::p(i & 1);
+            const uint32_t more = p_j > 1;
+            if (elected) {
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k) mma_ts(d, p + 8 * k, v_desc + k * (2048 >> 4), kDescO, k > 0 ? 1u : more);
+              tc_commit(&sm.pv_done[i & 1]);
+              tc_commit(&sm.empty[vs.stage]);
+            }
+            vs.step(stages);
+            vs.step(stages);
+            ++p_j;
+            ++i;
+            issued = true;
+          }
+        }
+        idle = issued ? 0 : idle + 1;
+        if ((idle & 1023u) == 1023u && !__all_sync(0xFFFFFFFFu, still_waiting(&began, &sm.dead, a.status))) break;
+        if (issued) began = 0;
       }
     }
     __syncwarp();
   } else {
-    // ---- softmax: thread r has row r of the tile ---------------------------------------------------
+    // ---- softmax: thread r of a group has row r of the tile: row `row_in` of copy `copy` -----------
+    const int group = (warp - 2) >> 2;
     const int r = (warp & 3) * 32 + lane;
+    constexpr int rows_apart = kTile / kCopies;
+    const int row_in = r & (rows_apart - 1), copy = r / rows_apart;
+    constexpr int kWide = kCopies == 4 ? 32 : 64;           // slots whose scores are in registers at once
+    constexpr int kSteps = kTile / kCopies / kWide;          // of a copy's slots: 2 with one copy, else 1
+    const int slot0 = copy * (kTile / kCopies);              // first slot of a tile that this thread's copy takes
     const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_addr = my + Col::s(group), o_addr = my + Col::o(group), p_addr = my + Col::p(group);
+    float4* mix = sm.mix[group];
     const float c = a.scale * 1.44269504088896341f;
-    uint32_t n = 0;
-    // Q's rows of a segment, in the swizzled layout of its product, and the tree's parents
-    auto load_q = [&](const Segment& s) {
-      const int rows = min(kTile, s.r.nodes * a.group - s.mtile * kTile);
-      // neighbouring threads take neighbouring 16-byte pieces of a row
-      for (int x = tid - 64; x < rows * (D / 8); x += kSoftThreads) {
-        const int row = x / (D / 8), piece = x % (D / 8);
-        const int at = s.mtile * kTile + row, node = at / a.group, g = at - node * a.group;
-        const uint4 v = *reinterpret_cast<const uint4*>(a.q + (s.r.first + node) * a.q_row_stride +
-                                                        (s.head * a.group + g) * a.q_head_stride + piece * 8);
-        *reinterpret_cast<uint4*>(sm.q + (piece >> 3) * kHalfBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
-      }
-      if (a.parent != nullptr)
-        for (int x = tid - 64; x < s.r.nodes; x += kSoftThreads) sm.parent[x] = a.parent[s.r.first + x];
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.q_full);
-    };
-    auto parent_of = [&](int node) { return a.parent != nullptr ? sm.parent[node] : node - 1; };
-    Segment s;
-    if (r == 0) a.jobs[blockIdx.x].valid = 0;
-    if (t0 < t1) {
-      s = segment_at(a, sm.before, t0, t1);
-      load_q(s);
-    }
-    uint32_t seg = 0;
+    if (tid == 64) a.jobs[blockIdx.x].valid = 0;
+    uint32_t n0 = 0, seg = 0, mixes = 0, frees = 0;  // the segment's first tile in this CTA's count
     for (uint32_t t = t0; t < t1; ++seg) {
-      if (!warp_wait(&sm.q_full, seg & 1, &sm.dead, a.status)) break;  // the parents are there for every thread
-      const int rows = min(kTile, s.r.nodes * a.group - s.mtile * kTile);
-      const bool active = (warp & 3) * 32 < rows;  // some row of this warp exists
-      const int at = s.mtile * kTile + r;
-      const int node = r < rows ? at / a.group : 0;
+      const int b = seg & 1;
+      if (!warp_wait(&sm.q_full[b], (seg >> 1) & 1, &sm.dead, a.status)) break;
+      const Segment& s = sm.seg[b];
+      const int32_t* tree = parents + b * a.Nmax;
+      auto parent_of = [&](int node) { return a.parent != nullptr ? tree[node] : node - 1; };
+      const int rows = min(a.tile_nodes, s.r.nodes - s.mtile * a.tile_nodes) * a.group;
+      const bool active = (((warp & 3) * 32) & (rows_apart - 1)) < rows;  // some row of this warp exists
+      const int node = s.mtile * a.tile_nodes + (row_in < rows ? over_group(row_in, a.over_group) : 0);
       const int len = s.r.len, end = len + s.r.nodes;
       const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0;  // before it (and past the sinks) no node sees a slot
-      // depth, and a check of the path
       int depth = 0;
-      if (r < rows)
-        for (int p = node; p > 0; ++depth) {
-          const int up = parent_of(p);
-          if (up < 0 || up >= p) {
-            mark_bad(a, s.request, SV_DEV_BAD_PARENT);
-            break;
+      if (a.window > 0) {
+        if (a.parent == nullptr) depth = node;
+        else
+          for (int p = node; p > 0; ++depth) {
+            const int up = tree[p];
+            if (up < 0 || up >= p) break;  // reported where the node's own tile is masked
+            p = up;
           }
-          p = up;
-        }
+      }
       const int near = a.window > 0 ? len + depth - a.window + 1 : 0;  // first position of the window
-      float m = -INFINITY, l = 0.0f;
-      for (int j = s.kv0; j < s.kv1; ++j, ++n) {
-        if (!warp_wait(&sm.s_full[n & 1], (n >> 1) & 1, &sm.dead, a.status)) break;
+      const int tiles = s.kv1 - s.kv0;
+      float m = -INFINITY, l = 0.0f, lr = 0.0f;  // maximum, sum of P, sum of the rounded P
+      bool left = false;
+      for (int j = (group + n0) & 1; j < tiles; j += 2) {
+        const uint32_t n = n0 + j;
+        if (left = !warp_wait(&sm.s_full[group], (n >> 1) & 1, &sm.dead, a.status); left) break;
         tc_after_sync();
-        const int s0 = tile_slot(s.r, j);
+        const int s0 = tile_slot(s.r, s.kv0 + j);
         const bool whole = s0 + kTile <= len && (a.window <= 0 || s0 + kTile <= a.sinks || s0 >= len + s.r.nodes - a.window);
         if (!whole && (s0 + kTile > end || (a.window > 0 && s0 < lo && s0 + kTile > a.sinks))) {
           // slots that no node sees may hold anything: 0 times it has to be 0
-          const uint32_t v = 2 * n + 1, st = v % Sh::kStages;
-          if (!warp_wait(&sm.full[st], (v / Sh::kStages) & 1, &sm.dead, a.status)) break;
+          const uint32_t v = 2 * n + 1, st = v % stages;
+          if (left = !warp_wait(&sm.full[st], (v / stages) & 1, &sm.dead, a.status); left) break;
           const int slot = s0 + r;
           if (slot >= end || (slot < lo && slot >= a.sinks)) {
-#pragma unroll
+#pragma unroll 4
             for (int x = 0; x < D / 8; ++x)
-              *reinterpret_cast<uint4*>(sm.stage[st] + (x >> 3) * kHalfBytes + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(ring + st * kStageBytes + (x >> 3) * kHalfBytes + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
         if (active) {
-          uint32_t x[kTile];
-          const uint32_t s_addr = my + kColS + (n & 1) * kTile;
+          // With one copy S is read in two halves, the first half twice (for the maximum and for P); P's columns
+          // lie over columns that were read before.
+          uint32_t x[kWide];
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int k = 0; k < kSteps; ++k) {
+            const int col = slot0 + k * kWide;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_load32(s_addr + 32 * i, x + 32 * i);
-          tmem_wait_load();
-          if (!whole) {
-            uint32_t see[4];
+            for (int i = 0; i < kWide; i += 32) tmem_load32(s_addr + col + i, x + i);
+            uint32_t see[kWide / 32];
+            if (!whole) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int p = s0 + 32 * w;
-              see[w] = range_bits(near, len, p) | (a.window > 0 ? range_bits(0, min(a.sinks, len), p) : 0u);
-            }
-            if (s0 + kTile > len && r < rows) {
-              int d = depth;
-              for (int up = node;; --d) {
-                const int b = len + up - s0;
-                if (b >= 0 && b < kTile && (len + d >= near || len + d < a.sinks)) {
-#pragma unroll
-                  for (int w = 0; w < 4; ++w)
-                    if ((b >> 5) == w) see[w] |= 1u << (b & 31);
+              for (int w = 0; w < kWide / 32; ++w)
+                see[w] = range_bits(near, len, s0 + col + 32 * w) | (a.window > 0 ? range_bits(0, min(a.sinks, len), s0 + col + 32 * w) : 0u);
+              if (s0 + col + kWide > len && row_in < rows) {
+                int d = depth;
+                for (int up = node;; --d) {
+                  const int bit = len + up - s0 - col;
+                  if (bit >= 0 && bit < kWide && (a.window <= 0 || len + d >= near || len + d < a.sinks)) {
+                    if (kWide == 32 || bit < 32) see[0] |= 1u << (bit & 31);
+                    else see[kWide / 32 - 1] |= 1u << (bit & 31);
+                  }
+                  if (up <= 0 || bit < 0) break;
+                  const int p = parent_of(up);
+                  if (p < 0 || p >= up) {
+                    mark_bad(a, s.request, SV_DEV_BAD_PARENT);
+                    break;
+                  }
+                  up = p;
                 }
-                if (up <= 0 || d <= 0 || b < 0) break;
-                up = parent_of(up);
+              }
+            }
+            tmem_loaded(x);
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < kWide; ++i)
+                if (!((see[i >> 5] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
+              if (kSteps > 1 && k == 0) {  // masked, for the second reading
+#pragma unroll
+                for (int i = 0; i < kWide; i += 32) tmem_store32(s_addr + col + i, x + i);
               }
             }
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if (!((see[i >> 5] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
+            for (int i = 0; i < kWide; i += 8)  // four chains, three operands a step
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                top4[e] = fmaxf(fmaxf(top4[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + 4 + e]));
           }
-          float top = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) top = fmaxf(top, __uint_as_float(x[i]));
-          top *= c;  // c > 0
-          const bool grow = top > m + kLazyGrowth || (m == -INFINITY && top > -INFINITY);
-          if (j == s.kv0) {
+          if (!whole) tmem_wait_store();
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;  // c > 0
+          if (j < 2) {
             m = top;
-          } else if (__any_sync(0xFFFFFFFFu, grow)) {
-            const float keep = grow ? (m == -INFINITY ? 0.0f : ex2_approx(m - top)) : 1.0f;
-            if (grow) m = top;
-            l *= keep;
-            // O is complete up to the tile before
-            if (!warp_wait(&sm.pv_done, (n - 1) & 1, &sm.dead, a.status)) break;
-            tc_after_sync();
+          } else {
+            const bool grow = top > m + kLazyGrowth || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+              const float keep = grow ? (m == -INFINITY ? 0.0f : ex2_approx(m - top)) : 1.0f;
+              if (grow) m = top;
+              l *= keep;
+              lr *= keep;
+              // the group's O is complete up to its tile before
+              if (left = !warp_wait(&sm.pv_done[group], ((n - 2) >> 1) & 1, &sm.dead, a.status); left) break;
+              tc_after_sync();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tmem_load16(o_addr + i, o);
+                tmem_loaded(o);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t o[32];
-              tmem_load32(my + kColO + 32 * i, o);
-              tmem_wait_load();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-              tmem_store32(my + kColO + 32 * i, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                tmem_store16(o_addr + i, o);
+              }
             }
           }
-          const float off = m == -INFINITY ? 0.0f : -m;
-          float sum0 = 0.0f, sum1 = 0.0f;
-          const f32x2 c2 = f2_pack(c, c), off2 = f2_pack(off, off);
-#pragma unroll
-          for (int i = 0; i < kTile; i += 2) {
-            float e0, e1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, off2), e0, e1);
-            e0 = ex2_approx(e0);
-            e1 = ex2_approx(e1);
-            sum0 += e0;
-            sum1 += e1;
-            x[i >> 1] = pack_bf16(e0, e1);
+          if (Col::kOwnP && j >= 2) {  // the product of the group's tile before has read P
+            if (left = !warp_wait(&sm.pv_done[group], ((n - 2) >> 1) & 1, &sm.dead, a.status); left) break;
+            tc_after_sync();
           }
-          l += sum0 + sum1;
-          tmem_store32(s_addr, x);
-          tmem_store32(s_addr + 32, x + 32);
+          const float off = m == -INFINITY ? 0.0f : -m;
+          const f32x2 c2 = f2_pack(c, c), off2 = f2_pack(off, off);
+          f32x2 sum[2] = {0, 0}, sumr[2] = {0, 0};
+          [[maybe_unused]] uint32_t later[kSteps > 1 ? 32 : 1];
+#pragma unroll 1
+          for (int k = kSteps - 1; k >= 0; --k) {  // the last step's scores are still there
+            const int col = slot0 + k * kWide;
+            if (k < kSteps - 1) {
+#pragma unroll
+              for (int i = 0; i < kWide; i += 32) tmem_load32(s_addr + col + i, x + i);
+              tmem_loaded(x);
+            }
+#pragma unroll
+            for (int i = 0; i < kWide; i += 2) {
+              float e0, e1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, off2), e0, e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              const uint32_t w = pack_bf16(e0, e1);
+              sum[(i >> 1) & 1] = f2_add(sum[(i >> 1) & 1], f2_pack(e0, e1));
+              sumr[(i >> 1) & 1] = f2_add(sumr[(i >> 1) & 1], f2_pack(bf16_lo(w), bf16_hi(w)));
+              x[i >> 1] = w;
+            }
+            if constexpr (kSteps > 1) {
+              if (k > 0) {  // this half's P lies over the half of S that is still to be read
+#pragma unroll
+                for (int i = 0; i < 32; ++i) later[i] = x[i];
+              } else {
+                tmem_store32(p_addr, x);
+                tmem_store32(p_addr + 32, later);
+              }
+            } else if constexpr (kWide == 64) {
+              tmem_store32(p_addr + col / 2, x);
+            } else {
+              tmem_store16(p_addr + col / 2, x);
+            }
+          }
+          if constexpr (kCopies > 1) {
+            uint32_t zero[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k)
+              if (32 * k < slot0 || 32 * k >= slot0 + kTile / kCopies) tmem_store16(p_addr + 16 * k, zero);
+          }
+          float e0, e1;
+          f2_unpack(f2_add(sum[0], sum[1]), e0, e1);
+          l += e0 + e1;
+          f2_unpack(f2_add(sumr[0], sumr[1]), e0, e1);
+          lr += e0 + e1;
           tmem_wait_store();
         }
         tc_before_sync();
-        mbar_arrive(&sm.p_full[n & 1]);
+        mbar_arrive(&sm.p_full[group]);
       }
-      // the next segment's Q can go in: every product with this one's is complete
-      const Segment done = s;
-      t += s.kv1 - s.kv0;
-      // every thread has arrived with its last tile: none still reads the parents
-      if (!warp_wait(&sm.p_full[(n - 1) & 1], ((n - 1) >> 1) & 1, &sm.dead, a.status)) break;
-      if (t < t1) {
-        s = segment_at(a, sm.before, t, t1);
-        load_q(s);
+      if (left) break;
+      // ---- the segment's end: the sums of groups and copies, then half of the columns per group --------
+      sm.m[b][group][r] = m;
+      sm.l[b][group][r] = l;
+      sm.lr[b][group][r] = lr;
+      mbar_arrive(&sm.sums_full);
+      if (!warp_wait(&sm.sums_full, seg & 1, &sm.dead, a.status)) break;
+      float top = -INFINITY, sum = 0.0f, sumr = 0.0f;
+      for (int x = row_in; x < kTile; x += rows_apart) top = fmaxf(top, fmaxf(sm.m[b][0][x], sm.m[b][1][x]));
+      for (int x = row_in; x < kTile; x += rows_apart)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float w = sm.m[b][g][x] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][g][x] - top);
+          sum += w * sm.l[b][g][x];
+          sumr += w * sm.lr[b][g][x];
+        }
+      const bool complete = s.kv0 == 0 && s.kv1 == s.r.tiles;
+      const float inv = complete && sumr > 0.0f ? 1.0f / sumr : 1.0f;
+      // (a group without a tile in the segment has m = -inf: its O is not used, whatever it holds)
+      const float w0 = sm.m[b][0][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][0][r] - top) * inv;
+      const float w1 = sm.m[b][1][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][1][r] - top) * inv;
+      const int head = s.head * a.group;
+      float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (s.kv0 == 0)) * part_floats<D>();
+      // four columns of this thread's row: to the output, or to this CTA's partial result
+      __nv_bfloat16* out_row = a.out + (s.r.first + node) * a.out_row_stride +
+                               (head + row_in - over_group(row_in, a.over_group) * a.group) * a.out_head_stride;
+      float* part_row = part + row_in * 4;
+      auto emit4 = [&](int column, float4 v) {
+        if (complete) *reinterpret_cast<uint2*>(out_row + column) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        else *reinterpret_cast<float4*>(part_row + column * kTile) = v;
+      };
+      if (group == 0 && copy == 0 && row_in < rows) {
+        if (!complete) {
+          part[kTile * D + row_in] = top;
+          part[kTile * D + kTile + row_in] = sum;
+          part[kTile * D + 2 * kTile + row_in] = sumr;
+        } else if (a.lse != nullptr) {
+          a.lse[(s.r.first + node) * a.q_heads + head + row_in - over_group(row_in, a.over_group) * a.group] = (top + log2f(sum)) * 0.693147180559945309f;
+        }
       }
-      if (!warp_wait(&sm.pv_done, (n - 1) & 1, &sm.dead, a.status)) break;
+      if (tid == 64 && s.kv0 == 0 && !complete) {
+        // the CTA in which the row tile ends
+        const uint32_t ends = t + s.r.tiles - 1;
+        const Job job = {1, s.request, s.head, s.mtile, rows, static_cast<int32_t>(blockIdx.x), part_of(total, ends, parts), 0};
+        a.jobs[blockIdx.x] = job;
+      }
+      // the last tile of each parity: its product is the last into that group's O
+      const uint32_t last = n0 + tiles - 1;
+      bool ok = warp_wait(&sm.pv_done[last & 1], (last >> 1) & 1, &sm.dead, a.status);
+      if (ok && tiles > 1) ok = warp_wait(&sm.pv_done[(last - 1) & 1], ((last - 1) >> 1) & 1, &sm.dead, a.status);
+      if (!ok) break;
       tc_after_sync();
-      const bool complete = done.kv0 == 0 && done.kv1 == done.r.tiles;
-      if (active) {
-        if (complete) {
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          const int g = at - node * a.group;
-          const int64_t row = done.r.first + node;
-          const int head = done.head * a.group + g;
-          __nv_bfloat16* out = a.out + row * a.out_row_stride + head * a.out_head_stride;
+      // this thread's 16 columns from `column` on, both groups' O's together
+      auto read_o = [&](int column, float (&f)[16]) {
+        uint32_t x[16], y[16];
+        tmem_load16(my + Col::o(0) + column, x);
+        tmem_load16(my + Col::o(1) + column, y);
+        tmem_loaded(x);
+        tmem_loaded(y);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_load32(my + kColO + 32 * i, o);
-            tmem_wait_load();
-            if (r < rows) {
+        for (int e = 0; e < 16; ++e)
+          f[e] = (w0 != 0.0f ? w0 * __uint_as_float(x[e]) : 0.0f) + (w1 != 0.0f ? w1 * __uint_as_float(y[e]) : 0.0f);
+      };
+      const int col0 = group * (D / 2), col1 = col0 + D / 2;
+      if constexpr (kCopies == 1) {
+        if (active) {
+#pragma unroll 1
+          for (int i = col0; i < col1; i += 16) {
+            float f[16];
+            read_o(i, f);
+            if (row_in < rows) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint4 w;
-                w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                *reinterpret_cast<uint4*>(out + 32 * i + e) = w;
+              for (int q = 0; q < 4; ++q) emit4(i + 4 * q, make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]));
+            }
+          }
+        }
+      } else {
+        // The copies' sum through shared memory, in rounds of as many columns as fit: every copy writes its own, then
+        // each adds and writes out every kCopies-th four columns.  (Loops, not unrolled: this code runs once a segment
+        // and comes from behind the instruction cache.)
+        const int kept_rows = (rows + 7) & ~7, all_rows = kCopies * kept_rows;
+        const int round = min(D / 2, (4 * kGroupThreads / all_rows * 4) & ~15);
+#pragma unroll 1
+        for (int i0 = col0; i0 < col1; i0 += round) {
+          const int i1 = min(i0 + round, col1);
+#pragma unroll 1
+          for (int i = i0; i < i1 && active; i += 16) {
+            float f[16];
+            read_o(i, f);
+            float4* to = mix + ((i - i0) >> 2) * all_rows + copy * kept_rows + row_in;
+            if (row_in < rows) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) to[q * all_rows] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+            }
+          }
+          mbar_arrive(&sm.mix_full[group]);
+          if (left = !warp_wait(&sm.mix_full[group], mixes & 1, &sm.dead, a.status); left) break;
+          ++mixes;
+          if (row_in < rows) {
+#pragma unroll 1
+            for (int i = i0 + 4 * copy; i < i1; i += 4 * kCopies) {
+              const float4* from = mix + ((i - i0) >> 2) * all_rows + row_in;
+              float4 v = from[0];
+#pragma unroll
+              for (int o = 1; o < kCopies; ++o) {
+                const float4 w = from[o * kept_rows];
+                v.x += w.x;
+                v.y += w.y;
+                v.z += w.z;
+                v.w += w.w;
               }
+              emit4(i, v);
             }
           }
-          if (r < rows && a.lse != nullptr) a.lse[row * a.q_heads + head] = (m + log2f(l)) * 0.693147180559945309f;
-        } else {
-          float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (done.kv0 == 0)) * part_floats<D>();
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_load32(my + kColO + 32 * i, o);
-            tmem_wait_load();
-            if (r < rows) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(part + ((8 * i + e / 4) * kTile + r) * 4) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
-          }
-          if (r < rows) {
-            part[kTile * D + r] = m;
-            part[kTile * D + kTile + r] = l;
+          if (i1 < col1) {  // the buffer is written again
+            mbar_arrive(&sm.mix_free[group]);
+            if (left = !warp_wait(&sm.mix_free[group], frees & 1, &sm.dead, a.status); left) break;
+            ++frees;
           }
         }
       }
+      if (left) break;
       tc_before_sync();
-      if (r == 0 && done.kv0 == 0 && !complete) {
-        // the CTA in which the row tile ends
-        const uint32_t last = t - 1 + (done.r.tiles - done.kv1);
-        uint32_t e = static_cast<uint32_t>(static_cast<uint64_t>(last) * parts / total);
-        while (part_begin(total, e + 1, parts) <= last) ++e;
-        Job job = {1, done.request, done.head, done.mtile, rows, static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(e), 0};
-        a.jobs[blockIdx.x] = job;
-      }
+      mbar_arrive(&sm.o_free);
+      mbar_arrive(&sm.seg_free[b]);
+      t += tiles;
+      n0 += tiles;
     }
   }
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
-  if (sm.dead && warp == 0)  // copies in flight land before the CTA leaves
-    for (uint32_t x = loaded > Sh::kStages ? loaded - Sh::kStages : 0; x < loaded; ++x)
-      mbar_wait(&sm.full[x % Sh::kStages], (x / Sh::kStages) & 1, a.status);
-  if (warp == 1) tmem_free(tmem);
+  if (sm.dead) {  // copies in flight land before the CTA leaves
+    if (warp == kWarpK || warp == kWarpV)  // its last fills: every second place of the ring's line
+      for (uint32_t x = loaded > stages + 1 ? loaded - ((stages + 1) & ~1u) : (warp == kWarpV); x < loaded; x += 2)
+        mbar_wait(&sm.full[x % stages], (x / stages) & 1, a.status);
+    if (warp == kWarpQ && segments > 0) mbar_wait(&sm.q_full[(segments - 1) & 1], ((segments - 1) >> 1) & 1, a.status);
+    __syncthreads();
+  }
+  if (warp == kWarpMma) tmem_free(tmem);
 }
 
 // Adds the partial results of row tile `jobs[x]`: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
@@ -630,7 +925,7 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendParams a) {
     for (int x = threadIdx.x; x < kJoinRows * kPieces; x += 128) {
       const int r = row0 + x % kJoinRows, piece = x / kJoinRows;
       if (r >= job.rows) continue;
-      float M = -INFINITY, L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float M = -INFINITY, L = 0.0f, R = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int i = 0; i < n; ++i) {
         const float* part = a.parts + static_cast<int64_t>(2 * (job.first + i) + (i == 0)) * part_floats<D>();
         M = fmaxf(M, part[kTile * D + r]);
@@ -641,13 +936,14 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendParams a) {
         const float w = m == -INFINITY ? 0.0f : ex2_approx(m - M);
         const float4 v = *reinterpret_cast<const float4*>(part + (piece * kTile + r) * 4);
         L += w * part[kTile * D + kTile + r];
+        R += w * part[kTile * D + 2 * kTile + r];
         o[0] += w * v.x;
         o[1] += w * v.y;
         o[2] += w * v.z;
         o[3] += w * v.w;
       }
-      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-      const int at = job.mtile * kTile + r, node = at / a.group, head = job.head * a.group + (at - node * a.group);
+      const float inv = R > 0.0f ? 1.0f / R : 0.0f;
+      const int node = job.mtile * a.tile_nodes + r / a.group, head = job.head * a.group + r % a.group;
       const int64_t row = a.node_offsets[job.request] + node;
       uint2 w;
       w.x = pack_bf16(o[0] * inv, o[1] * inv);
@@ -700,8 +996,6 @@ Layout layout_of(int ctas, int head_dim) {
   L.total = L.parts + sizeof(float) * (head_dim == 128 ? part_floats<128>() : part_floats<64>()) * 2 * ctas;
   return L;
 }
-constexpr int kMaxCtas = 152;  // SMs of the GPU: one CTA each
-
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -733,14 +1027,34 @@ bool encode_pool(CUtensorMap* map, const sv_cache* c, const void* base) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-cudaError_t launch_attention(const AttendParams& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int ctas, void* stream) {
-  const size_t dyn = sizeof(Smem<D>) + sizeof(uint32_t) * a.B + 1024;
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dyn));
+// The query rows as (dimension, head, row); a copy takes 64 dimensions of a head group's rows of a tile.
+bool encode_queries(CUtensorMap* map, const void* q, int64_t row_stride, int64_t head_stride, int head_dim, int heads,
+                    int64_t rows, int group, int tile_nodes) {
+  const EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tile_nodes)};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int kCopies>
+cudaError_t launch_attention(AttendParams& a, const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                             int ctas, void* stream) {
+  // the ring gets what Q, the tables and the fixed part leave of the shared memory: at least 4 stages
+  constexpr int kStageBytes = D / 64 * kHalfBytes;
+  const int fixed = 4 * (a.B + 2 * a.Nmax) + 1024 + kStageBytes;
+  const int room = kSmemMax - static_cast<int>(sizeof(Smem)) - 64 - fixed;
+  a.stages = std::min(kMaxStages, room / kStageBytes);
+  const size_t dyn = static_cast<size_t>(fixed) + static_cast<size_t>(a.stages) * kStageBytes;
+  cudaError_t e = allow_smem<attend_kernel<D, kCopies>>(kSmemMax - sizeof(Smem) - 64);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attend_kernel<D>, dim3(ctas), kThreads, dyn, stream, SV_KERNEL_ATTENTION, 1, a, k_map, v_map);
+  e = launch_dependent(attend_kernel<D, kCopies>, dim3(ctas), kThreads, dyn, stream, SV_KERNEL_ATTENTION, 1, a, q_map, k_map, v_map);
   if (e != cudaSuccess) return e;
-  const int groups = (std::min(kTile, a.Nmax * a.group) + kJoinRows - 1) / kJoinRows;
+  const int groups = (a.tile_nodes * a.group + kJoinRows - 1) / kJoinRows;
   return launch_dependent(join_kernel<D>, dim3(ctas, groups), 128, 0, stream, SV_KERNEL_ATTENTION_JOIN, 1, a);
 }
 
@@ -752,7 +1066,7 @@ using namespace sv;
 extern "C" {
 
 size_t sv_attention_workspace_size(const sv_cache* c, int q_heads) {
-  if (check_cache(c) != SV_OK || q_heads < 1 || q_heads % c->kv_heads != 0) return 0;
+  if (check_cache(c) != SV_OK || q_heads < 1 || q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > kTile) return 0;
   return layout_of(kMaxCtas, c->head_dim).total;
 }
 
@@ -764,8 +1078,8 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   sv_status s;
   if ((s = check_cache(c)) != SV_OK || (s = check_table(page_table, table_width, seq_len, B)) != SV_OK) return s;
   if (layer < 0 || layer >= c->layers) return set_error(SV_ERR_INVALID_ARG, "layer=%d outside [0, %d)", layer, c->layers);
-  if (q_heads < 1 || q_heads % c->kv_heads != 0)
-    return set_error(SV_ERR_INVALID_ARG, "q_heads=%d is no multiple of kv_heads=%d", q_heads, c->kv_heads);
+  if (q_heads < 1 || q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > kTile)
+    return set_error(SV_ERR_INVALID_ARG, "q_heads=%d: 1 to %d times kv_heads=%d are needed", q_heads, kTile, c->kv_heads);
   if (Nmax < 1 || Nmax > SV_MAX_DRAFT + 1) return set_error(SV_ERR_INVALID_ARG, "Nmax=%d outside [1, %d]", Nmax, SV_MAX_DRAFT + 1);
   if (n_rows < 0 || n_rows > static_cast<int64_t>(SV_MAX_BATCH) * (SV_MAX_DRAFT + 1))
     return set_error(SV_ERR_INVALID_ARG, "n_rows=%lld", (long long)n_rows);
@@ -778,27 +1092,26 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
       q_head_stride < c->head_dim || out_head_stride < c->head_dim || q_row_stride < 0 || out_row_stride < 0)
     return set_error(SV_ERR_INVALID_ARG, "q / out: 16-byte aligned rows of head_dim elements are needed");
   if ((s = check_workspace(ws, ws_bytes, sv_attention_workspace_size(c, q_heads))) != SV_OK) return s;
+  const int group = q_heads / c->kv_heads, tile_nodes = std::min(kTile / group, Nmax);
   // the line of work is counted in 32 bits
   const int64_t tiles = ((static_cast<int64_t>(table_width) * c->page_size + kTile - 1) / kTile + 1) *
-                        ((static_cast<int64_t>(Nmax) * (q_heads / c->kv_heads) + kTile - 1) / kTile);
+                        ((Nmax + tile_nodes - 1) / tile_nodes);
   if (tiles > INT_MAX || tiles * c->kv_heads > INT_MAX || tiles * c->kv_heads * B > INT_MAX)
     return set_error(SV_ERR_INVALID_ARG, "B=%d requests of up to %lld tiles a head are too many for one call", B, (long long)tiles);
   const size_t offset = static_cast<size_t>(layer) * c->layer_stride * 2;
-  CUtensorMap k_map, v_map;
+  CUtensorMap q_map, k_map, v_map;
+  if (!encode_queries(&q_map, q, q_row_stride, q_head_stride, c->head_dim, q_heads, n_rows, group, tile_nodes))
+    return set_error(SV_ERR_CUDA, "the query rows' strides or sizes cannot be described to the copy engine");
   if (!encode_pool(&k_map, c, static_cast<const unsigned char*>(c->k) + offset) ||
       !encode_pool(&v_map, c, static_cast<const unsigned char*>(c->v) + offset))
     return set_error(SV_ERR_CUDA, "the cache's strides or sizes cannot be described to the copy engine");
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return launch_status(e, "device");
   const int ctas = std::min(sms, kMaxCtas);
   const Layout L = layout_of(kMaxCtas, c->head_dim);
   unsigned char* w = static_cast<unsigned char*>(ws);
   AttendParams a = {};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_row_stride = q_row_stride;
-  a.q_head_stride = q_head_stride;
   a.out_row_stride = out_row_stride;
   a.out_head_stride = out_head_stride;
   a.table = page_table;
@@ -821,13 +1134,20 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   while ((1 << a.shift) < c->page_size) ++a.shift;
   a.q_heads = q_heads;
   a.kv_heads = c->kv_heads;
-  a.group = q_heads / c->kv_heads;
+  a.group = group;
+  a.tile_nodes = tile_nodes;
+  a.over_group = (65536 + group - 1) / group;
   a.window = window;
   a.sinks = sinks;
   a.scale = scale;
-  return launch_status(c->head_dim == 128 ? launch_attention<128>(a, k_map, v_map, ctas, stream)
-                                          : launch_attention<64>(a, k_map, v_map, ctas, stream),
-                       "attention");
+  const int tile_rows = tile_nodes * group;
+  const auto launch = c->head_dim == 128 ? (tile_rows <= 32   ? launch_attention<128, 4>
+                                            : tile_rows <= 64 ? launch_attention<128, 2>
+                                                              : launch_attention<128, 1>)
+                                         : (tile_rows <= 32   ? launch_attention<64, 4>
+                                            : tile_rows <= 64 ? launch_attention<64, 2>
+                                                              : launch_attention<64, 1>);
+  return launch_status(launch(a, q_map, k_map, v_map, ctas, stream), "attention");
 }
 
 }  // extern "C"

@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -25,6 +26,33 @@ sv_status check_table(const int32_t* page_table, int table_width, const int32_t*
 
 inline sv_status launch_status(cudaError_t e, const char* what) {
   return e == cudaSuccess ? SV_OK : set_error(SV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// Dynamic shared memory of a kernel, raised once per device (and again only for more).
+constexpr int kMaxDevices = 64;
+template <auto kKernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<size_t> allowed[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && dev < kMaxDevices) allowed[dev].store(bytes, std::memory_order_relaxed);
+  return e;
+}
+
+// Multiprocessors of the current device, looked up once per device.
+inline cudaError_t sm_count(int* out) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *out = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*out > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < kMaxDevices) known[dev].store(*out, std::memory_order_relaxed);
+  return e;
 }
 
 // Launch behind the stream's previous kernel with programmatic dependent launch: the launch

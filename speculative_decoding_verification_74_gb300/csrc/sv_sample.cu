@@ -818,7 +818,7 @@ cudaError_t launch_sample(SampleParams p, void* stream) {
   while (cs < kMaxCluster && static_cast<int64_t>(p.V) * kElt > cs * 32768) cs *= 2;
   p.slice = ((p.V + cs - 1) / cs + 7) & ~7;
   const size_t dyn = static_cast<size_t>(p.slice) * kElt + 32;
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dyn));
+  const cudaError_t e = allow_smem<sample_kernel<DT>>(dyn);
   if (e != cudaSuccess) return e;
   return launch_dependent(sample_kernel<DT>, dim3(static_cast<unsigned>(p.R) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
 }

@@ -10,13 +10,15 @@
 //        top-p   logits whose weight is below (1 - p) W / V add up to less than (1 - p) W
 //        min-p   its own threshold
 //   2. the logits at or above the bound are listed in vocabulary order;
-//   3. up to 2048 of them are gathered by the cluster's first CTA, sorted, and summed up: the prefix's end, its weight
-//      and the draws follow from scans of that list.  The other CTAs are done.
-// Longer lists (flat rows under top-p alone, large k) stay with their CTAs (cut_wide): a histogram of the listed logits
-// (512 steps between bound and top; counts, and weights in three 14-bit limbs, which 32-bit atomics add without
-// overflow), summed over the cluster, gives the step that holds the boundary, and that step's logits are exchanged and
-// ranked by every CTA.  Where a step holds more logits than the exchange takes (long runs of equals), the boundary is
-// found by a radix descent on the integer image of x instead.
+//   3. up to 2048 of them are gathered by the cluster's first CTA, which finds the prefix's end and draws; the other CTAs
+//      are done.  Up to 128 are ranked by counting; more go into a histogram (512 steps between bound and top; counts,
+//      and weights in three 14-bit limbs, which 32-bit atomics add without overflow), whose step that holds the end
+//      is ranked; a step of more than 128 (long runs of equals) is sorted out by sorting the list.
+// Longer lists (flat rows under top-p alone, large k) stay with their CTAs (cut_wide): a histogram of counts, summed over
+// the cluster, gives the step that holds the boundary (for top-p by the weight of each step's middle, then checked
+// against the exact weights of the steps around it), and that step's logits are exchanged and ranked by every CTA.
+// Where a step holds more logits than the exchange takes, the boundary is found by a radix descent on the integer image
+// of x instead.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -40,6 +42,7 @@ constexpr int kLimb = 14;
 constexpr int kGather = 2048;           // logits that one CTA sorts
 constexpr int kGatherK = 1024;          // largest k that goes that way
 constexpr int kRanks = 8;               // order statistics of a CTA's groups that it publishes
+constexpr int kShort = 128;             // a gathered list this short is ranked by counting, a longer one sorted
 
 struct SampleParams {
   const void* logits;
@@ -71,8 +74,11 @@ struct Shared {
   uint32_t count[kSteps];
   uint16_t list[kWarps][kListPerWarp];
   uint64_t z;                          // a sum of the slice
-  float top;                           // largest logit of the slice
-  float rank_at[kRanks];               // a logit at or below the ranks()[j]-th largest group maximum
+  uint32_t top;                        // image of the slice's largest logit
+  float rank_at[kRanks];               // a logit at or below the rank_n[j]-th largest group maximum
+  float rank_all[kMaxCluster * kRanks];  // the cluster's
+  uint32_t rank_n[kRanks];
+  uint32_t bound;                      // image of the bound, 0 = none
   uint32_t mine_n;                     // logits in `gather` (more than kGather: too many), or of the exchanged step
   uint64_t bar[kPieces];
   uint64_t seg[kWarps];
@@ -84,9 +90,10 @@ struct Shared {
   uint64_t above_w;
   uint32_t key, key_above_c, key_equal_c;
   uint64_t key_above_w;
+  uint64_t end[2];                     // the prefix's last logit, and the weight up to it
   uint32_t equal_before, equal_here;
   uint32_t cut;                        // first equal (vocabulary index) that is left out; entries of the sorted prefix
-  float red[2][kWarps];
+  uint32_t red[2][kWarps];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -138,20 +145,34 @@ __device__ __forceinline__ float exponent_of(float x, float top, float steep) {
 __device__ __forceinline__ uint64_t weight_of(float y) { return __float2ull_rn(ex2_approx(y) * 0x1p40f); }
 
 // A running sum of weights, for up to 4096 terms: adding 1.5 2^3 leaves 2^y rounded to a multiple of 2^-20 in the
-// low bits, adding 1.5 2^-17 to what is left does the same for 2^-40; both images are summed as integers.
+// low bits, adding 1.5 2^-17 to what is left does the same for 2^-40; both images are summed as integers.  Two logits
+// at a time in packed arithmetic, each half rounded like the scalar operation.  A logit of -inf adds nothing.
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 struct WeightSum {
-  uint32_t hi = 0, lo = 0, n = 0;
-  __device__ __forceinline__ void add(float y) {
-    const float e = ex2_approx(y);
-    const float t = __fadd_rn(e, 12.0f);
-    const float rest = __fsub_rn(e, __fsub_rn(t, 12.0f));
-    hi += __float_as_uint(t);
-    lo += __float_as_uint(__fadd_rn(rest, 0x1.8p-17f));
-    ++n;
+  uint32_t hi = 0, lo = 0;
+  f32x2 minus_top, steep;
+  __device__ __forceinline__ WeightSum(float top, float s) : minus_top(f2_pack(-top, -top)), steep(f2_pack(s, s)) {}
+  __device__ __forceinline__ void add(float x0, float x1) {
+    float y0, y1, t0, t1, r0, r1;
+    f2_unpack(f2_mul(f2_add(f2_pack(x0, x1), minus_top), steep), y0, y1);
+    const f32x2 e = f2_pack(ex2_approx(y0), ex2_approx(y1));
+    const f32x2 t = f2_add(e, f2_pack(12.0f, 12.0f));
+    f2_unpack(t, t0, t1);
+    const f32x2 high = f2_add(t, f2_pack(-12.0f, -12.0f));
+    float h0, h1;
+    f2_unpack(high, h0, h1);
+    f2_unpack(f2_add(f2_add(e, f2_pack(-h0, -h1)), f2_pack(0x1.8p-17f, 0x1.8p-17f)), r0, r1);
+    hi += __float_as_uint(t0) + __float_as_uint(t1);
+    lo += __float_as_uint(r0) + __float_as_uint(r1);
   }
-  __device__ __forceinline__ uint64_t total() const {
-    const uint32_t h = hi - n * __float_as_uint(12.0f);
-    const int32_t l = static_cast<int32_t>(lo - n * __float_as_uint(0x1.8p-17f));
+  // after n additions (of two)
+  __device__ __forceinline__ uint64_t total(uint32_t n) const {
+    const uint32_t h = hi - 2 * n * __float_as_uint(12.0f);
+    const int32_t l = static_cast<int32_t>(lo - 2 * n * __float_as_uint(0x1.8p-17f));
     return (static_cast<uint64_t>(h) << 20) + static_cast<uint64_t>(static_cast<int64_t>(l));
   }
 };
@@ -201,6 +222,22 @@ struct Slice {
   __device__ __forceinline__ int index_of(int pos) const { return static_cast<int>(first) + pos - phase; }
 };
 
+// This warp's weights of the logits above `last` (each lane its share; any order).
+template <int DT>
+__device__ __forceinline__ uint64_t weights_above(const Slice<DT>& s, float last, float top, float steep) {
+  const int lane = threadIdx.x & 31;
+  WeightSum sum(top, steep);
+  uint32_t n = 0;
+#pragma unroll 2
+  for (int v = s.run_a + lane; v < s.run_z; v += 32, ++n) {
+    const Vec<DT> x(s.vec(v));
+#pragma unroll
+    for (int e = 0; e < Vec<DT>::kElems; e += 2)
+      sum.add(x.x[e] > last ? x.x[e] : -INFINITY, x.x[e + 1] > last ? x.x[e + 1] : -INFINITY);
+  }
+  return sum.total(n * (Vec<DT>::kElems / 2));
+}
+
 // Boundary of a prefix of the order (x desc): the smallest one whose count, or weight, reaches what is asked for.
 // key 0: none, everything lies above.
 struct Boundary {
@@ -224,7 +261,22 @@ __device__ __forceinline__ void clear_histogram(Shared& sh) {
   sh.count[t] = sh.limb[0][t] = sh.limb[1][t] = sh.limb[2][t] = 0;
 }
 
-// Sum over the threads before this one (exclusive) of a 64-bit value.
+// Sum over the threads before this one (exclusive).
+__device__ uint32_t block_scan32(Shared& sh, uint32_t v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh.scan_c[warp] = x;
+  __syncthreads();
+  const uint32_t ahead = lane < warp ? sh.scan_c[lane] : 0;  // (warp <= 16: the lanes cover it)
+  return x - v + __reduce_add_sync(0xFFFFFFFFu, ahead);
+}
+// The same for 64 bits.
 __device__ uint64_t block_scan(Shared& sh, uint64_t v) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t x = v;
@@ -347,31 +399,18 @@ __device__ __noinline__ Boundary descend(const Slice<DT>& s, Shared& sh, uint64_
   return b;
 }
 
-// Calls f(position, x) for this warp's logits at or above `bound`, in vocabulary order and by whole warps: lanes
-// without one get position -1.  listed >= 0: from the warp's list.
-template <int DT, typename F>
-__device__ __forceinline__ void for_candidates(const Slice<DT>& s, const Shared& sh, int listed, float bound, F f) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (listed >= 0) {
-    for (int i = lane; i - lane < listed; i += 32) {
-      const int pos = i < listed ? sh.list[warp][i] : -1;
-      f(pos, pos >= 0 ? s.at(pos) : -INFINITY);
-    }
-  } else {
-    for (int p0 = s.run_a * Slice<DT>::kElems; p0 < s.run_z * Slice<DT>::kElems; p0 += 32) {
-      const int pos = p0 + lane;
-      const float x = pos < s.run_z * Slice<DT>::kElems ? s.at(pos) : -INFINITY;
-      const bool in = x >= bound && x != -INFINITY;
-      if (__any_sync(0xFFFFFFFFu, in)) f(in ? pos : -1, in ? x : -INFINITY);
-    }
-  }
-}
-
 // Steps of the candidates' histogram: equal widths between the top and the bound, the last one open.
 struct Scale {
   float top, inv;
   static __device__ __forceinline__ Scale over(float top, float range) {
     return {top, range > 0.0f ? fminf(static_cast<float>(kSteps - 1) / range, FLT_MAX) : 0.0f};
+  }
+  // a logit surely above the steps from `step` on, and one surely below those up to it (step() rounds a little)
+  __device__ __forceinline__ float above(int step) const {
+    return inv > 0.0f && step > 0 ? __fadd_ru(top, __fmul_ru(-(step / inv), 0.99999f)) : INFINITY;
+  }
+  __device__ __forceinline__ float below(int step) const {
+    return inv > 0.0f && step < kSteps - 1 ? __fadd_rd(top, __fmul_rd(-((step + 1) / inv), 1.00001f)) : -INFINITY;
   }
   __device__ __forceinline__ int step(float x) const {
     return static_cast<int>(fminf(__fmul_rn(__fsub_rn(top, x), inv), static_cast<float>(kSteps - 1)));
@@ -381,8 +420,8 @@ struct Scale {
 // The logits of one step, exchanged over the cluster and ranked: the boundary by count or weight, given the sums
 // above the step.
 template <int DT, bool kByWeight>
-__device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, int listed, float bound, const Scale& scale, int step,
-                              uint64_t want, uint32_t above_c, uint64_t above_w, float top, float steep) {
+__device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, float bound, const Scale& scale, int step, uint64_t want,
+                              uint32_t above_c, uint64_t above_w, float top, float steep) {
   const uint32_t cs = cluster_size(), rank = cluster_rank();
   const int tid = threadIdx.x;
   if (tid == 0) {
@@ -390,9 +429,15 @@ __device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, int l
     sh.equal_before = sh.equal_here = 0;
   }
   __syncthreads();
-  for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
-    if (pos >= 0 && scale.step(x) == step) sh.mine[atomicAdd(&sh.mine_n, 1u)] = key_of(x);
-  });
+  const float hi = scale.above(step), lo = fmaxf(scale.below(step), bound);
+#pragma unroll 2
+  for (int v = s.run_a + (tid & 31); v < s.run_z; v += 32) {
+    const Vec<DT> x(s.vec(v));
+#pragma unroll
+    for (int e = 0; e < Vec<DT>::kElems; ++e)
+      if (x.x[e] >= lo && x.x[e] <= hi && x.x[e] != -INFINITY && scale.step(x.x[e]) == step)
+        sh.mine[atomicAdd(&sh.mine_n, 1u)] = key_of(x.x[e]);
+  }
   cluster_sync();
   if (tid <= static_cast<int>(cs)) {
     uint32_t n = 0;
@@ -477,17 +522,222 @@ struct Ask {
 // Up to 128 KB of shared memory is on its way at once: waits of microseconds, not inlined.
 __device__ __noinline__ void wait_piece(uint64_t* bar, uint32_t* status) { mbar_wait(bar, 0, status); }
 
-// Draws from the weights of `gather` (vocabulary order) at or above `last`, whose sum is z; thread t looks at its run
-// of `per` entries.
-__device__ __forceinline__ void draw_gathered(Shared& sh, const Ask& ask, const uint64_t* g, int n, uint64_t last, uint64_t z) {
+// Bitonic sort, descending, of `size` (a power of two) entries.
+__device__ __noinline__ void sort_descending(uint64_t* x, int size) {
+#pragma unroll 1
+  for (int block = 2; block <= size; block *= 2)
+#pragma unroll 1
+    for (int stride = block / 2; stride > 0; stride /= 2) {
+      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
+        const uint64_t a = x[lo], b = x[hi];
+        if ((a < b) == ((lo & block) == 0)) {
+          x[lo] = b;
+          x[hi] = a;
+        }
+      }
+      // a warp's pairs of a stride up to 32 lie in 64 entries that only this warp touches until the next longer stride
+      if (stride > 32 || (stride == 1 && block >= 64)) __syncthreads(); else __syncwarp();
+    }
+  __syncthreads();
+}
+
+// Step 3 for at most kShort gathered logits: thread t has the t-th, counts those before it in the order, and adds
+// their weights.
+template <int DT>
+__device__ __noinline__ void finish_short(Shared& sh, const Ask& ask, int n, uint64_t* weights) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t g = 0, w = 0;
+  float y = -INFINITY;
+  if (tid < n) {
+    g = sh.gather[tid];
+    y = exponent_of(logit_of_key(static_cast<uint32_t>(g >> 32)), ask.top, ask.steep);
+    w = weight_of(y);
+    weights[tid] = w;
+  }
+  __syncthreads();
+  uint32_t more = 0;
+  uint64_t above = 0;
+  if (warp * 32 < n)
+#pragma unroll 4
+    for (int i = 0; i < n; ++i)
+      if (sh.gather[i] > g) {
+        ++more;
+        above += weights[i];
+      }
+  const bool in_k = tid < n && (!ask.by_count || more < static_cast<uint32_t>(ask.k));
+  uint64_t total = ask.total;
+  if (ask.by_count && ask.nucleus) {  // the top-k's weight
+    const uint64_t part = warp_sum(in_k ? w : 0);
+    if (lane == 0) sh.scan_w[warp] = part;
+    __syncthreads();
+    total = 0;
+    for (int i = 0; i < kShort / 32; ++i) total += sh.scan_w[i];
+  }
+  const bool keep = in_k && (!ask.nucleus || above < max(share_of(total, ask.p24), uint64_t(1))) && y >= ask.least;
+  if (keep && ask.out_row != nullptr) {
+    using Elem = typename Slice<DT>::Elem;
+    const uint32_t bits = __float_as_uint(logit_of_key(static_cast<uint32_t>(g >> 32)));
+    static_cast<Elem*>(ask.out_row)[~static_cast<uint32_t>(g)] = DT == SV_BF16 ? static_cast<Elem>(bits >> 16) : static_cast<Elem>(bits);
+  }
+  if (!keep) w = 0;
+  // draws: the list is in vocabulary order
+  uint64_t incl = w;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += u;
+  }
+  if (lane == 31) sh.seg[warp] = incl;
+  __syncthreads();
+  uint64_t before = incl - w, z = 0;
+  for (int i = 0; i < kShort / 32; ++i) {
+    if (i < warp) before += sh.seg[i];
+    z += sh.seg[i];
+  }
+  const SampleParams& p = *ask.p;
+  if (w != 0)
+    for (int j = 0; j < p.M; ++j) {
+      const uint64_t t = share_of(z, static_cast<uint32_t>(p.uniforms[ask.row * p.M + j] * 16777216.0f));
+      if (t >= before && t < before + w) {
+        p.out_tokens[ask.row * p.M + j] = static_cast<int32_t>(~static_cast<uint32_t>(g));
+        if (p.out_probs != nullptr) p.out_probs[ask.row * p.M + j] = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(z));
+      }
+    }
+}
+
+// Among the gathered logits of one histogram step: the entry up to which the prefix goes, by count (the want-th
+// of all) or by weight (the one that makes the weight reach want), and the weight up to it inclusive; `few` has room
+// for kShort, `weights` for all.
+struct End {
+  uint64_t entry, weight;
+};
+template <bool kByWeight>
+__device__ __noinline__ End end_in_step(Shared& sh, const Ask& ask, const Scale& scale, int n, uint64_t want, uint64_t* sorted) {
+  const int tid = threadIdx.x;
+  const uint32_t step = sh.step;
+  const uint32_t here = sh.here_c, above_c = sh.above_c;
+  const uint64_t above_w = sh.above_w;
+  __syncthreads();
+  auto weight = [&](uint64_t g) { return weight_of(exponent_of(logit_of_key(static_cast<uint32_t>(g >> 32)), ask.top, ask.steep)); };
+  if (here > kShort) {  // many equals: sort everything (rare)
+    int size = 32;
+    while (size < n) size *= 2;
+    for (int i = tid; i < size; i += kThreads) sorted[i] = i < n ? sh.gather[i] : 0;
+    __syncthreads();
+    sort_descending(sorted, size);
+    const int per = (n + kThreads - 1) / kThreads, a = min(n, tid * per), b = min(n, a + per);
+    uint64_t sum = 0;
+    for (int i = a; i < b; ++i) sum += weight(sorted[i]);
+    uint64_t at = block_scan(sh, sum);
+    for (int i = a; i < b; ++i) {
+      const uint64_t w = weight(sorted[i]);
+      if (kByWeight ? at < want && at + w >= want : i + 1 == static_cast<int>(want)) {
+        sh.end[0] = sorted[i];
+        sh.end[1] = at + w;
+      }
+      at += w;
+    }
+    __syncthreads();
+  } else {
+    if (tid == 0) sh.mine_n = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t g = sh.gather[i];
+      if (scale.step(logit_of_key(static_cast<uint32_t>(g >> 32))) == static_cast<int>(step)) sorted[atomicAdd(&sh.mine_n, 1u)] = g;
+    }
+    __syncthreads();
+    if (tid < static_cast<int>(here)) {
+      const uint64_t g = sorted[tid], w = weight(g);
+      uint32_t more = above_c;
+      uint64_t at = above_w;
+      for (uint32_t i = 0; i < here; ++i)
+        if (sorted[i] > g) {
+          ++more;
+          at += weight(sorted[i]);
+        }
+      if (kByWeight ? at < want && at + w >= want : more + 1 == want) {
+        sh.end[0] = g;
+        sh.end[1] = at + w;
+      }
+    }
+    __syncthreads();
+  }
+  const End end = {sh.end[0], sh.end[1]};
+  __syncthreads();
+  return end;
+}
+
+// Step 3 in the cluster's first CTA, which holds the n > kShort gathered logits in vocabulary order (the histogram's limbs
+// and the ends lie in `more`, and so does room for sorting).
+template <int DT>
+__device__ __noinline__ void finish_gathered(Shared& sh, const Ask& ask, int n, uint64_t* more) {
+  const int tid = threadIdx.x;
+  uint32_t* limb = reinterpret_cast<uint32_t*>(more + kGather);  // [3][kSteps]
+  const Scale scale = Scale::over(ask.top, ask.bound == -INFINITY ? 64.0f / ask.steep : __fsub_rn(ask.top, ask.bound));
+  uint64_t last = 0;
+  if (ask.by_count || ask.nucleus) {
+    sh.count[tid] = 0;
+    for (int l = 0; l < 3; ++l) limb[l * kSteps + tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const float x = logit_of_key(static_cast<uint32_t>(sh.gather[i] >> 32));
+      const int step = scale.step(x);
+      const uint64_t w = weight_of(exponent_of(x, ask.top, ask.steep));
+      atomicAdd(&sh.count[step], 1u);
+      for (int l = 0; l < 3; ++l) {
+        const uint32_t part = static_cast<uint32_t>(w >> (l * kLimb)) & ((1u << kLimb) - 1u);
+        if (part) atomicAdd(&limb[l * kSteps + step], part);
+      }
+    }
+    __syncthreads();
+    const uint32_t c = sh.count[tid];
+    const uint64_t w = limbs_of(limb[tid], limb[kSteps + tid], limb[2 * kSteps + tid]);
+    uint64_t total = ask.total;
+    if (ask.by_count) {
+      find_step<false>(sh, c, w, ask.k, 0, 0);
+      if (sh.step != 0xFFFFFFFFu) {
+        const End end = end_in_step<false>(sh, ask, scale, n, ask.k, more);
+        last = end.entry;
+        total = end.weight;
+      } else {  // fewer than k logits: all are kept
+        __syncthreads();
+        const uint64_t before = block_scan(sh, w);
+        if (tid == kThreads - 1) sh.z = before + w;
+        __syncthreads();
+        total = sh.z;
+      }
+    }
+    if (ask.nucleus) {
+      const uint64_t limit = max(share_of(total, ask.p24), uint64_t(1));
+      find_step<true>(sh, c, w, limit, 0, 0);
+      if (sh.step != 0xFFFFFFFFu) last = max(last, end_in_step<true>(sh, ask, scale, n, limit, more).entry);
+    }
+  }
+  // the kept logits are those at or above `last` and min-p's threshold; thread t has a run of the list
   const int per = (n + kThreads - 1) / kThreads;
-  const int a = min(n, static_cast<int>(threadIdx.x) * per), b = min(n, a + per);
+  const int a = min(n, tid * per), b = min(n, a + per);
   auto weight = [&](int i) {
-    return g[i] >= last ? weight_of(exponent_of(logit_of_key(static_cast<uint32_t>(g[i] >> 32)), ask.top, ask.steep)) : 0;
+    const uint64_t g = sh.gather[i];
+    const float y = exponent_of(logit_of_key(static_cast<uint32_t>(g >> 32)), ask.top, ask.steep);
+    return g >= last && y >= ask.least ? weight_of(y) : 0;
   };
   uint64_t sum = 0;
-  for (int i = a; i < b; ++i) sum += weight(i);
+  for (int i = a; i < b; ++i) {
+    sum += weight(i);
+    if (ask.out_row != nullptr) {  // the first CTA's part begins the row
+      const uint64_t g = sh.gather[i];
+      const float x = logit_of_key(static_cast<uint32_t>(g >> 32));
+      using Elem = typename Slice<DT>::Elem;
+      if (g >= last && exponent_of(x, ask.top, ask.steep) >= ask.least)
+        static_cast<Elem*>(ask.out_row)[~static_cast<uint32_t>(g)] =
+            DT == SV_BF16 ? static_cast<Elem>(__float_as_uint(x) >> 16) : static_cast<Elem>(__float_as_uint(x));
+    }
+  }
   const uint64_t before = block_scan(sh, sum);
+  if (tid == kThreads - 1) sh.z = before + sum;
+  __syncthreads();
+  const uint64_t z = sh.z;
   const SampleParams& p = *ask.p;
   for (int j = 0; j < p.M; ++j) {
     const uint64_t t = share_of(z, static_cast<uint32_t>(p.uniforms[ask.row * p.M + j] * 16777216.0f));
@@ -496,7 +746,7 @@ __device__ __forceinline__ void draw_gathered(Shared& sh, const Ask& ask, const 
     for (int i = a; i < b; ++i) {
       const uint64_t w = weight(i);
       if (t < at + w) {
-        p.out_tokens[ask.row * p.M + j] = static_cast<int32_t>(~static_cast<uint32_t>(g[i]));
+        p.out_tokens[ask.row * p.M + j] = static_cast<int32_t>(~static_cast<uint32_t>(sh.gather[i]));
         if (p.out_probs != nullptr) p.out_probs[ask.row * p.M + j] = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(z));
         break;
       }
@@ -505,253 +755,12 @@ __device__ __forceinline__ void draw_gathered(Shared& sh, const Ask& ask, const 
   }
 }
 
-// Step 3 in the cluster's first CTA, which holds the n gathered logits in vocabulary order; `sorted`: room for as many
-// (a power of two, at most kGather).
-template <int DT>
-__device__ __noinline__ void finish_gathered(Shared& sh, const Ask& ask, int n, uint64_t* sorted) {
-  const int tid = threadIdx.x;
-  int size = 32;
-  while (size < n) size *= 2;
-  for (int i = tid; i < size; i += kThreads) sorted[i] = i < n ? sh.gather[i] : 0;
-  __syncthreads();
-  // bitonic, descending: by logit, then by index
-#pragma unroll 1
-  for (int block = 2; block <= size; block *= 2)
-#pragma unroll 1
-    for (int stride = block / 2; stride > 0; stride /= 2) {
-      for (int i = tid; i < size / 2; i += kThreads) {
-        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
-        const uint64_t x = sorted[lo], y = sorted[hi];
-        if ((x < y) == ((lo & block) == 0)) {
-          sorted[lo] = y;
-          sorted[hi] = x;
-        }
-      }
-      // a warp's pairs of a stride up to 32 lie in 64 entries that only this warp touches until the next longer stride
-      if (stride > 32 || (stride == 1 && block >= 64)) __syncthreads(); else __syncwarp();
-    }
-  __syncthreads();
-  const int per = (n + kThreads - 1) / kThreads;
-  const int a = min(n, tid * per), b = min(n, a + per);
-  auto exponent = [&](int i) { return exponent_of(logit_of_key(static_cast<uint32_t>(sorted[i] >> 32)), ask.top, ask.steep); };
-  // how many entries are kept: the top-k, the top-p of their weight, those above min-p
-  int kept = ask.by_count ? min(ask.k, n) : n;
-  uint64_t sum = 0;
-  for (int i = a; i < min(b, kept); ++i) sum += weight_of(exponent(i));
-  const uint64_t before = block_scan(sh, sum);
-  uint64_t total = ask.total;
-  if (ask.by_count) {
-    __syncthreads();
-    if (tid == kThreads - 1) sh.z = before + sum;
-    __syncthreads();
-    total = sh.z;
-  }
-  if (tid == 0) sh.cut = kept;
-  __syncthreads();
-  if (ask.nucleus || ask.floor_on) {
-    const uint64_t limit = ask.nucleus ? max(share_of(total, ask.p24), uint64_t(1)) : ~uint64_t(0);
-    uint64_t at = before;
-    for (int i = a; i < min(b, kept); ++i) {
-      const float y = exponent(i);
-      if (at >= limit || y < ask.least) {  // the first entry of this thread that is left out
-        atomicMin(&sh.cut, static_cast<uint32_t>(i));
-        break;
-      }
-      at += weight_of(y);
-    }
-    __syncthreads();
-  }
-  kept = static_cast<int>(sh.cut);
-  const uint64_t last = sorted[kept - 1];  // (the largest logit is always kept)
-  uint64_t mine = 0;
-  for (int i = a; i < min(b, kept); ++i) mine += weight_of(exponent(i));
-  mine = warp_sum(mine);
-  if ((tid & 31) == 0) sh.seg[tid >> 5] = mine;
-  __syncthreads();
-  uint64_t z = 0;
-  for (int w = 0; w < kWarps; ++w) z += sh.seg[w];
-  if (ask.out_row != nullptr) {  // the first CTA's part begins the row
-    using Elem = typename Slice<DT>::Elem;
-    Elem* out = static_cast<Elem*>(ask.out_row);
-    for (int i = tid; i < kept; i += kThreads) {
-      const uint32_t bits = __float_as_uint(logit_of_key(static_cast<uint32_t>(sorted[i] >> 32)));
-      out[~static_cast<uint32_t>(sorted[i])] = DT == SV_BF16 ? static_cast<Elem>(bits >> 16) : static_cast<Elem>(bits);
-    }
-  }
-  draw_gathered(sh, ask, sh.gather, n, last, z);
-}
-
-// Steps 3 and 4 with the lists where they are.
-template <int DT>
-__device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask& ask, int listed) {
-  using Elem = typename Slice<DT>::Elem;
-  constexpr int kElems = Slice<DT>::kElems;
-  const SampleParams& p = *ask.p;
-  const uint32_t cs = cluster_size(), rank = cluster_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float top = ask.top, steep = ask.steep, bound = ask.bound;
-  uint64_t total = ask.total;
-  Boundary b = {};
-  uint32_t ties_kept = 0;  // how many of the boundary's equals are kept, lowest indexes first
-  if (ask.by_count || ask.nucleus) {
-    clear_histogram(sh);
-    const Scale scale = Scale::over(top, bound == -INFINITY ? 64.0f / steep : __fsub_rn(top, bound));
-    __syncthreads();
-    for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
-      if (pos >= 0) {
-        const int step = scale.step(x);
-        atomicAdd(&sh.count[step], 1u);
-        if (ask.nucleus) add_limbs(sh, step, weight_of(exponent_of(x, top, steep)));
-      }
-    });
-    cluster_sync();
-    uint32_t c;
-    uint64_t w;
-    merged_step(sh, tid, ask.nucleus, &c, &w);
-    bool found = true, crowded = false;
-    if (ask.by_count) {
-      find_step<false>(sh, c, w, ask.k, 0, 0);
-      found = sh.step != 0xFFFFFFFFu;  // else fewer than k logits: all are kept
-      crowded = found && sh.here_c > kExchange;
-      const int step = sh.step;
-      const uint32_t above_c = sh.above_c;
-      const uint64_t above_w = sh.above_w;
-      cluster_sync();  // the peers have read the histogram (the exchange's arrays are beside it)
-      if (crowded) b = descend<DT, false>(s, sh, ask.k, top, steep);
-      else if (found) b = rank_step<DT, false>(s, sh, listed, bound, scale, step, ask.k, above_c, above_w, top, steep);
-      ties_kept = found ? ask.k - b.above_c : 0;
-    }
-    if (ask.nucleus) {
-      if (ask.by_count) {
-        // W: what lies above the boundary, and its kept equals
-        if (found && !crowded) {
-          total = b.above_w;
-        } else {
-          WeightSum sum;
-          for (int v = s.run_a + lane; v < s.run_z; v += 32) {
-            const Vec<DT> x(s.vec(v));
-#pragma unroll
-            for (int e = 0; e < kElems; ++e)
-              if (key_of(x.x[e]) > b.key) sum.add(exponent_of(x.x[e], top, steep));
-          }
-          total = cluster_total(sh, sum.total());
-        }
-        if (found) total += static_cast<uint64_t>(ties_kept) * weight_of(exponent_of(logit_of_key(b.key), top, steep));
-      }
-      const uint64_t limit = max(share_of(total, ask.p24), uint64_t(1));
-      if (crowded) {
-        b = descend<DT, true>(s, sh, limit, top, steep);
-      } else {
-        find_step<true>(sh, c, w, limit, 0, 0);
-        const int step = sh.step;
-        const uint32_t here_c = sh.here_c, above_c = sh.above_c;
-        const uint64_t above_w = sh.above_w;
-        const bool inside = sh.step != 0xFFFFFFFFu;
-        cluster_sync();  // the peers have read the histogram, or the keys exchanged before
-        // (a bound at min-p's threshold may lie above the boundary: then everything above the bound is kept)
-        if (inside ? here_c > kExchange : !ask.floor_on) b = descend<DT, true>(s, sh, limit, top, steep);
-        else if (inside) b = rank_step<DT, true>(s, sh, listed, bound, scale, step, limit, above_c, above_w, top, steep);
-        else b = Boundary{};
-      }
-      if (b.key != 0) {
-        const uint64_t each = weight_of(exponent_of(logit_of_key(b.key), top, steep));
-        ties_kept = each == 0 ? 0 : static_cast<uint32_t>((limit - b.above_w + each - 1) / each);
-      }
-    }
-  }
-  // equals of this slice that are kept: those before vocabulary index `cut`
-  uint32_t cut = 0xFFFFFFFFu;
-  {
-    const uint32_t quota = ties_kept > b.equal_before ? min(ties_kept - b.equal_before, b.equal_here) : 0;
-    if (b.key == 0 || quota == 0) {
-      cut = 0;
-    } else if (quota < b.equal_here) {
-      uint32_t c = 0;
-      for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) { c += pos >= 0 && key_of(x) == b.key; });
-      c = __reduce_add_sync(0xFFFFFFFFu, c);
-      if (lane == 0) sh.ties[warp] = c;
-      __syncthreads();
-      uint32_t before = 0;
-      for (int i = 0; i < warp; ++i) before += sh.ties[i];
-      if (before < quota && before + c >= quota)
-        for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
-          const bool equal = pos >= 0 && key_of(x) == b.key;
-          const uint32_t set = __ballot_sync(0xFFFFFFFFu, equal);
-          if (equal && before + __popc(set & ((1u << lane) - 1u)) == quota - 1) sh.cut = static_cast<uint32_t>(s.index_of(pos)) + 1;
-          before += __popc(set);
-        });
-      __syncthreads();
-      cut = sh.cut;
-    }
-  }
-  auto keeps = [&](int pos, float x) {
-    const uint32_t key = key_of(x);
-    return (key > b.key || (key == b.key && static_cast<uint32_t>(s.index_of(pos)) < cut)) && exponent_of(x, top, steep) >= ask.least;
-  };
-  // kept weights by warp, the row's total, the kept logits
-  Elem* out_row = static_cast<Elem*>(ask.out_row);
-  uint64_t w = 0;
-  for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
-    if (pos >= 0 && keeps(pos, x)) {
-      w += weight_of(exponent_of(x, top, steep));
-      if (out_row != nullptr) out_row[pos - s.phase] = reinterpret_cast<const Elem*>(s.data)[pos];
-    }
-  });
-  w = warp_sum(w);
-  cluster_sync();  // sh.z may be written again
-  if (lane == 0) sh.seg[warp] = w;
-  __syncthreads();
-  if (tid == 0) {
-    uint64_t z = 0;
-    for (int i = 0; i < kWarps; ++i) z += sh.seg[i];
-    sh.z = z;
-  }
-  cluster_sync();
-  uint64_t before = 0, z = 0, mine = 0;
-  for (uint32_t r = 0; r < cs; ++r) {
-    const uint64_t zr = peer_u64(&sh.z, r);
-    if (r < rank) before += zr;
-    if (r == rank) mine = zr;
-    z += zr;
-  }
-  // the draws: the CTA that holds a draw's crossing, its warp, its logit
-  for (int j = 0; j < p.M; ++j) {
-    const uint32_t u24 = static_cast<uint32_t>(p.uniforms[ask.row * p.M + j] * 16777216.0f);
-    uint64_t t = share_of(z, u24);
-    if (t < before || t >= before + mine) continue;
-    t -= before;
-    uint64_t ahead = 0;
-    for (int i = 0; i < warp; ++i) ahead += sh.seg[i];
-    if (t < ahead || t >= ahead + sh.seg[warp]) continue;  // the warp that owns the run draws
-    t -= ahead;
-    bool open = true;
-    for_candidates<DT>(s, sh, listed, bound, [&](int pos, float x) {
-      if (!open) return;
-      const uint64_t we = pos >= 0 && keeps(pos, x) ? weight_of(exponent_of(x, top, steep)) : 0;
-      uint64_t incl = we;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += u;
-      }
-      const uint64_t all = __shfl_sync(0xFFFFFFFFu, incl, 31);
-      if (t < all) {
-        if (t < incl && t >= incl - we) {
-          p.out_tokens[ask.row * p.M + j] = s.index_of(pos);
-          if (p.out_probs != nullptr) p.out_probs[ask.row * p.M + j] = __fdiv_rn(__ull2float_rn(we), __ull2float_rn(z));
-        }
-        open = false;
-      }
-      t -= all;
-    });
-  }
-  cluster_sync();  // no CTA leaves while a peer may still read its shared memory
-}
-
-// No filter: every logit's weight.  A lane sums a contiguous stretch of its warp's run (an odd number of vectors, so
-// that a quarter warp's 16-byte loads fall on different banks): a draw then looks into one lane's stretch.
-template <int DT>
-__device__ __noinline__ void draw_all(const Slice<DT>& s, Shared& sh, const Ask& ask) {
+// Kept weights, the row's total, the draws and the kept logits, with every slice where it is.  A logit is kept if it lies
+// above the boundary, or equals it and has an index below `cut`.  A lane sums a
+// contiguous stretch of its warp's run (an odd number of vectors, so that a quarter warp's 16-byte loads fall on
+// different banks): a draw then looks into one lane's stretch.
+template <int DT, bool kAll>
+__device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const Ask& ask, uint32_t boundary, uint32_t cut) {
   using Elem = typename Slice<DT>::Elem;
   constexpr int kElems = Slice<DT>::kElems;
   const SampleParams& p = *ask.p;
@@ -759,23 +768,35 @@ __device__ __noinline__ void draw_all(const Slice<DT>& s, Shared& sh, const Ask&
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int stretch = (s.run_z - s.run_a + 31) / 32 | 1;
   const int va = min(s.run_z, s.run_a + lane * stretch), vz = min(s.run_z, va + stretch);
-  WeightSum sum;
-  for (int v = va; v < vz; ++v) {
+  const float last = kAll || boundary == 0 ? -INFINITY : logit_of_key(boundary);
+  // (logits compare as their images do: -0 and +0 are one value in both)
+  auto kept = [&](float x, int pos) {
+    return kAll || x > last || (x == last && x != -INFINITY && static_cast<uint32_t>(s.index_of(pos)) < cut) ? x : -INFINITY;
+  };
+  Elem* out_row = static_cast<Elem*>(ask.out_row);
+  WeightSum sum(ask.top, ask.steep);
+  uint32_t adds = 0;
+#pragma unroll 2
+  for (int v = va; v < vz; ++v, ++adds) {
     const Vec<DT> x(s.vec(v));
 #pragma unroll
-    for (int e = 0; e < kElems; ++e) sum.add(exponent_of(x.x[e], ask.top, ask.steep));
+    for (int e = 0; e < kElems; e += 2) {
+      const float x0 = kept(x.x[e], v * kElems + e), x1 = kept(x.x[e + 1], v * kElems + e + 1);
+      sum.add(x0, x1);
+      if (out_row != nullptr) {
+        if (x0 != -INFINITY) out_row[v * kElems + e - s.phase] = reinterpret_cast<const Elem*>(s.data)[v * kElems + e];
+        if (x1 != -INFINITY) out_row[v * kElems + e + 1 - s.phase] = reinterpret_cast<const Elem*>(s.data)[v * kElems + e + 1];
+      }
+    }
   }
-  if (ask.out_row != nullptr)
-    for (int pos = s.run_a * kElems + lane; pos < s.run_z * kElems; pos += 32)
-      if (pos >= s.phase && pos < s.phase + s.n)
-        static_cast<Elem*>(ask.out_row)[pos - s.phase] = reinterpret_cast<const Elem*>(s.data)[pos];
-  const uint64_t w = sum.total();
+  const uint64_t w = sum.total(adds * (kElems / 2));
   uint64_t incl = w;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
     if (lane >= d) incl += u;
   }
+  cluster_sync();  // sh.z may be written again
   if (lane == 31) sh.seg[warp] = incl;
   __syncthreads();
   if (tid == 0) {
@@ -798,10 +819,10 @@ __device__ __noinline__ void draw_all(const Slice<DT>& s, Shared& sh, const Ask&
     const uint32_t owner = __ballot_sync(0xFFFFFFFFu, t >= incl - w && t < incl);
     const int from = __ffs(owner) - 1;
     uint64_t left = t - __shfl_sync(0xFFFFFFFFu, incl - w, from);
-    const int first = (s.run_a + from * stretch) * kElems, last = min(s.run_z, s.run_a + (from + 1) * stretch) * kElems;
-    for (int base = first; base < last; base += 32) {
+    const int first = (s.run_a + from * stretch) * kElems, end = min(s.run_z, s.run_a + (from + 1) * stretch) * kElems;
+    for (int base = first; base < end; base += 32) {
       const int pos = base + lane;
-      const uint64_t we = pos < last ? weight_of(exponent_of(s.at(pos), ask.top, ask.steep)) : 0;
+      const uint64_t we = pos < end ? weight_of(exponent_of(kept(s.at(pos), pos), ask.top, ask.steep)) : 0;
       uint64_t in = we;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -820,6 +841,189 @@ __device__ __noinline__ void draw_all(const Slice<DT>& s, Shared& sh, const Ask&
     }
   }
   cluster_sync();  // no CTA leaves while a peer may still read its shared memory
+}
+
+// The cluster's exact weight of the steps before `step` - 1, and of `step` - 1, `step` and `step` + 1.
+template <int DT>
+__device__ __noinline__ void weights_around(const Slice<DT>& s, Shared& sh, const Ask& ask, const Scale& scale, int step,
+                                            uint64_t (&out)[4]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 9) sh.limb[tid / 3][tid % 3] = 0;
+  __syncthreads();
+  // surely above: the packed sum; surely below: nothing; the few between, by their step
+  const float hi = scale.above(step - 1), lo = fmaxf(scale.below(step + 1), ask.bound);
+  const uint64_t high = warp_sum(weights_above<DT>(s, hi, ask.top, ask.steep));
+  uint64_t rest = 0;  // of those between: before step - 1
+#pragma unroll 2
+  for (int v = s.run_a + lane; v < s.run_z; v += 32) {
+    const Vec<DT> x(s.vec(v));
+#pragma unroll
+    for (int e = 0; e < Vec<DT>::kElems; ++e)
+      if (x.x[e] >= lo && x.x[e] <= hi && x.x[e] != -INFINITY) {
+        const int d = scale.step(x.x[e]) - step + 1;
+        const uint64_t w = weight_of(exponent_of(x.x[e], ask.top, ask.steep));
+        if (d < 0) {
+          rest += w;
+        } else if (d <= 2) {
+          for (int l = 0; l < 3; ++l) {
+            const uint32_t part = static_cast<uint32_t>(w >> (l * kLimb)) & ((1u << kLimb) - 1u);
+            if (part) atomicAdd(&sh.limb[l][d], part);
+          }
+        }
+      }
+  }
+  rest = warp_sum(rest);
+  if (lane == 0) sh.all_w[warp] = high + rest;
+  __syncthreads();
+  if (tid == 0) {
+    uint64_t t = 0;
+    for (int w = 0; w < kWarps; ++w) t += sh.all_w[w];
+    sh.all_w[kWarps] = t;
+  } else if (tid <= 3) {
+    sh.all_w[kWarps + tid] = limbs_of(sh.limb[0][tid - 1], sh.limb[1][tid - 1], sh.limb[2][tid - 1]);
+  }
+  cluster_sync();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[i] = 0;
+    for (uint32_t r = 0; r < cluster_size(); ++r) out[i] += peer_u64(&sh.all_w[kWarps + i], r);
+  }
+  cluster_sync();  // the peers have read them
+}
+
+// The image of the smallest logit whose exponent reaches `least` (<= 0): min-p's threshold, exactly.
+__device__ __noinline__ uint32_t floor_key(float top, float steep, float least) {
+  uint32_t lo = key_of(-INFINITY), hi = key_of(top);  // lo does not reach it, hi does
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (exponent_of(logit_of_key(mid), top, steep) >= least) hi = mid; else lo = mid;
+  }
+  return hi;
+}
+
+// Step 3 for long lists.
+template <int DT>
+__device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask& ask) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float top = ask.top, steep = ask.steep, bound = ask.bound;
+  uint64_t total = ask.total;
+  Boundary b = {};
+  uint32_t ties_kept = 0;  // how many of the boundary's equals are kept, lowest indexes first
+  if (ask.by_count || ask.nucleus) {
+    sh.count[tid] = 0;
+    const Scale scale = Scale::over(top, bound == -INFINITY ? 64.0f / steep : __fsub_rn(top, bound));
+    __syncthreads();
+#pragma unroll 2
+    for (int v = s.run_a + lane; v < s.run_z; v += 32) {
+      const Vec<DT> x(s.vec(v));
+#pragma unroll
+      for (int e = 0; e < Vec<DT>::kElems; ++e)
+        if (x.x[e] >= bound && x.x[e] != -INFINITY) atomicAdd(&sh.count[scale.step(x.x[e])], 1u);
+    }
+    cluster_sync();
+    uint32_t c;
+    uint64_t none;
+    merged_step(sh, tid, false, &c, &none);
+    // a step's weight by its middle, in units of 2^-30: good to a part in a few hundred
+    const float middle = scale.inv > 0.0f ? -(tid + 0.5f) / scale.inv * steep : 0.0f;
+    const uint64_t about = static_cast<uint64_t>(static_cast<float>(c) * ex2_approx(middle) * 0x1p30f);
+    uint64_t near[4];
+    bool by_radix = false;
+    if (ask.by_count) {
+      find_step<false>(sh, c, 0, ask.k, 0, 0);
+      const uint32_t step = sh.step, here = sh.here_c, above_c = sh.above_c;
+      cluster_sync();  // the peers have read the histogram
+      if (step != 0xFFFFFFFFu) {
+        by_radix = here > kExchange;
+        uint64_t above_w = 0;
+        if (ask.nucleus) {
+          weights_around<DT>(s, sh, ask, scale, step, near);
+          above_w = near[0] + near[1];
+        }
+        if (by_radix) b = descend<DT, false>(s, sh, ask.k, top, steep);
+        else b = rank_step<DT, false>(s, sh, bound, scale, step, ask.k, above_c, above_w, top, steep);
+        ties_kept = ask.k - b.above_c;
+      }  // else fewer than k logits: all are kept
+      if (ask.nucleus) {  // W: what lies above the boundary, and its kept equals
+        if (step != 0xFFFFFFFFu && !by_radix) {
+          total = b.above_w;
+        } else {
+          total = cluster_total(sh, weights_above<DT>(s, b.key == 0 ? -INFINITY : logit_of_key(b.key), top, steep));
+        }
+        if (step != 0xFFFFFFFFu) total += static_cast<uint64_t>(ties_kept) * weight_of(exponent_of(logit_of_key(b.key), top, steep));
+      }
+    }
+    if (ask.nucleus) {
+      const uint64_t limit = max(share_of(total, ask.p24), uint64_t(1));
+      // the step whose weight makes the sum reach the limit, about; its neighbours are weighed with it
+      find_step<true>(sh, c, about, max(limit >> 10, uint64_t(1)), 0, 0);
+      uint32_t step = sh.step;
+      cluster_sync();  // the peers have read the histogram, or the keys exchanged before
+      bool inside = false;
+      uint64_t above_w = 0;
+      if (!by_radix) {
+        weights_around<DT>(s, sh, ask, scale, min(step, static_cast<uint32_t>(kSteps - 1)), near);
+        step = min(step, static_cast<uint32_t>(kSteps - 1)) - 1;
+        above_w = near[0];
+        for (int i = 1; i < 4 && !inside; ++i) {
+          if (above_w < limit && above_w + near[i] >= limit) inside = true;
+          else {
+            above_w += near[i];
+            ++step;
+          }
+        }
+      }
+      // (a bound at min-p's threshold may lie above the boundary: then everything above the bound is kept, and so it is
+      // where the descent finds the boundary below the bound)
+      uint32_t here = 0;
+      if (inside) {
+        // how many logits the step holds, from the thread that has it
+        if (tid == static_cast<int>(step)) sh.here_c = c;
+        __syncthreads();
+        here = sh.here_c;
+      }
+      if (inside && here <= kExchange) b = rank_step<DT, true>(s, sh, bound, scale, step, limit, 0, above_w, top, steep);
+      else b = descend<DT, true>(s, sh, limit, top, steep);
+      if (b.key != 0) {
+        const uint64_t each = weight_of(exponent_of(logit_of_key(b.key), top, steep));
+        ties_kept = each == 0 ? 0 : static_cast<uint32_t>((limit - b.above_w + each - 1) / each);
+      }
+    }
+  }
+  // equals of this slice that are kept: those before vocabulary index `cut`
+  uint32_t cut = 0xFFFFFFFFu;
+  const uint32_t quota = ties_kept > b.equal_before ? min(ties_kept - b.equal_before, b.equal_here) : 0;
+  if (b.key == 0 || quota == 0) {
+    cut = 0;
+  } else if (quota < b.equal_here) {
+    const int first = s.run_a * Vec<DT>::kElems, end = s.run_z * Vec<DT>::kElems;
+    uint32_t c = 0;
+    for (int pos = first + lane; pos < end; pos += 32) c += key_of(s.at(pos)) == b.key;
+    c = __reduce_add_sync(0xFFFFFFFFu, c);
+    if (lane == 0) sh.ties[warp] = c;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int i = 0; i < warp; ++i) before += sh.ties[i];
+    if (before < quota && before + c >= quota)
+      for (int base = first; base < end; base += 32) {
+        const bool equal = base + lane < end && key_of(s.at(base + lane)) == b.key;
+        const uint32_t set = __ballot_sync(0xFFFFFFFFu, equal);
+        if (equal && before + __popc(set & ((1u << lane) - 1u)) == quota - 1) sh.cut = static_cast<uint32_t>(s.index_of(base + lane)) + 1;
+        before += __popc(set);
+      }
+    __syncthreads();
+    cut = sh.cut;
+  }
+  // min-p as a boundary of its own: everything above the logit just below its threshold
+  uint32_t last = b.key;
+  if (ask.floor_on) {
+    const uint32_t under = floor_key(top, steep, ask.least) - 1;
+    if (under > last) {
+      last = under;
+      cut = 0;
+    }
+  }
+  draw_slices<DT, false>(s, sh, ask, last, cut);
 }
 
 template <int DT>
@@ -930,53 +1134,52 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
     for (int e = 0; e < kElems; ++e) group = max_nan(group, x.x[e]);
   }
-  float top = group, low = group == -INFINITY ? INFINITY : group;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, d));
-  }
-  if (lane == 0) {
-    sh.red[0][warp] = top;
-    sh.red[1][warp] = low;
-  }
-  __syncthreads();
+  // reductions on integer images (a NaN's lies above that of +inf)
+  const uint32_t none_key = key_of(-INFINITY), inf_key = key_of(INFINITY);
   {
-    top = lane < kWarps ? sh.red[0][lane] : -INFINITY;
-    low = lane < kWarps ? sh.red[1][lane] : INFINITY;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, d));
+    const uint32_t key = key_of(group);
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, key);
+    const uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, key > none_key ? key : 0xFFFFFFFFu);
+    if (lane == 0) {
+      sh.red[0][warp] = hi;
+      sh.red[1][warp] = lo;
     }
   }
-  if (tid == 0) sh.top = top;
+  __syncthreads();
+  const uint32_t top_key = __reduce_max_sync(0xFFFFFFFFu, sh.red[0][lane & (kWarps - 1)]);
+  const uint32_t low_key = __reduce_min_sync(0xFFFFFFFFu, sh.red[1][lane & (kWarps - 1)]);
+  if (tid == 0) sh.top = top_key;
   // ---- 1. a bound ---------------------------------------------------------------------------------
-  // the CTA vouches for ranks(j) logits at or above rank_at[j]: from an even share of k to all of it
-  auto rank_of = [&](int j) { return static_cast<uint32_t>(ceilf(static_cast<float>(ask.k) * exp2f(-3.0f + 3.0f * j / (kRanks - 1)))); };
+  // the CTA vouches for rank_n[j] logits at or above rank_at[j]: from an even share of k to all of it
   if (ask.by_count) {
-    if (tid < kRanks) sh.rank_at[tid] = -INFINITY;
-    const Scale groups = Scale::over(top, __fsub_rn(top, low));
-    if (group > -INFINITY && top < INFINITY) atomicAdd(&sh.count[groups.step(group)], 1u);
+    if (tid < kRanks) {
+      sh.rank_at[tid] = -INFINITY;
+      sh.rank_n[tid] = static_cast<uint32_t>(ceilf(static_cast<float>(ask.k) * exp2f(-3.0f + 3.0f * tid / (kRanks - 1))));
+    }
+    if (tid == 0) sh.bound = 0;
+    const float own = logit_of_key(top_key);
+    const bool counts = top_key < inf_key && low_key != 0xFFFFFFFFu;
+    const Scale groups = Scale::over(own, counts ? __fsub_rn(own, logit_of_key(low_key)) : 0.0f);
+    if (counts && group > -INFINITY) atomicAdd(&sh.count[groups.step(group)], 1u);
     __syncthreads();
     const uint32_t c = sh.count[tid];
-    const uint32_t before = static_cast<uint32_t>(block_scan(sh, c));
-#pragma unroll
-    for (int j = 0; j < kRanks; ++j) {
-      const uint32_t want = rank_of(j);
+    const uint32_t before = block_scan32(sh, c);
+    if (c > 0) {
       // a step's lower end, a little lower than the roundings of step() may put it
-      if (before < want && before + c >= want)
-        sh.rank_at[j] = groups.inv > 0.0f ? __fsub_rd(top, __fmul_ru(static_cast<float>(tid + 1) / groups.inv, 1.00001f)) : top;
+      const float at = groups.inv > 0.0f ? __fsub_rd(own, __fmul_ru(static_cast<float>(tid + 1) / groups.inv, 1.00001f)) : own;
+#pragma unroll 1
+      for (int j = 0; j < kRanks; ++j) {
+        const uint32_t want = sh.rank_n[j];
+        if (before < want && before + c >= want) sh.rank_at[j] = at;
+      }
     }
   }
   cluster_sync();
-  top = lane < static_cast<int>(cs) ? peer_f32(&sh.top, lane) : -INFINITY;
-#pragma unroll
-  for (int d = kMaxCluster / 2; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  top = __shfl_sync(0xFFFFFFFFu, top, 0);
+  const uint32_t row_top = __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(cs) ? peer_u32(&sh.top, lane) : 0u);
+  const float top = logit_of_key(row_top);
   ask.top = top;
-  if (!(top < INFINITY)) bad |= SV_DEV_BAD_LOGIT;
-  if (bad != 0 || top == -INFINITY) {  // the same in every CTA of the cluster
+  if (row_top >= inf_key) bad |= SV_DEV_BAD_LOGIT;
+  if (bad != 0 || row_top <= none_key) {  // the same in every CTA of the cluster
     if (bad != 0 && rank == 0 && tid == 0) atomicOr(p.status, bad);
     if (rank == 0)
       for (int j = tid; j < p.M; j += kThreads) {
@@ -987,50 +1190,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     return;
   }
   if (!ask.by_count && !ask.nucleus && !ask.floor_on) {
-    draw_all<DT>(s, sh, ask);
+    draw_slices<DT, true>(s, sh, ask, 0, 0);
     return;
   }
   float bound = -INFINITY;
   if (ask.by_count) {
-    // the largest published logit above which the CTAs together vouch for k: lane l tries the l-th and the (l + 32)-th
-    // (CTA, order statistic)
-    if (warp == 0) {
-      float at[2];
-      int sure[2] = {0, 0};
-      for (int h = 0; h < 2; ++h) {
-        const int i = lane + 32 * h;
-        at[h] = i < static_cast<int>(cs) * kRanks ? peer_f32(&sh.rank_at[i % kRanks], i / kRanks) : -INFINITY;
-      }
-      const int mine = static_cast<int>(rank_of(lane % kRanks));
-      for (uint32_t r = 0; r < cs; ++r) {
-        int most[2] = {0, 0};
-        for (int j = 0; j < kRanks; ++j) {
-          const int i = r * kRanks + j;
-          const float v = __shfl_sync(0xFFFFFFFFu, i < 32 ? at[0] : at[1], i & 31);
-          const int vouched = __shfl_sync(0xFFFFFFFFu, mine, j);
-          if (v >= at[0]) most[0] = vouched;
-          if (v >= at[1]) most[1] = vouched;
-        }
-        sure[0] += most[0];
-        sure[1] += most[1];
-      }
-      for (int h = 0; h < 2; ++h)
-        if (at[h] > -INFINITY && sure[h] >= ask.k) bound = fmaxf(bound, at[h]);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) bound = fmaxf(bound, __shfl_xor_sync(0xFFFFFFFFu, bound, d));
-      if (lane == 0) sh.red[0][0] = bound;
-    }
+    // the largest published logit above which the CTAs together vouch for k: thread t asks CTA t % 8 about the
+    // (t / 8)-th published one
+    if (tid < kMaxCluster * kRanks)
+      sh.rank_all[tid] = tid < static_cast<int>(cs) * kRanks ? peer_f32(&sh.rank_at[tid % kRanks], tid / kRanks) : -INFINITY;
     __syncthreads();
-    bound = sh.red[0][0];
+    const float at = sh.rank_all[tid / kMaxCluster];
+    uint32_t sure = 0;
+#pragma unroll 1
+    for (int j = 0; j < kRanks; ++j)
+      if (sh.rank_all[(tid % kMaxCluster) * kRanks + j] >= at) sure = sh.rank_n[j];
+    sure += __shfl_xor_sync(0xFFFFFFFFu, sure, 1);
+    sure += __shfl_xor_sync(0xFFFFFFFFu, sure, 2);
+    sure += __shfl_xor_sync(0xFFFFFFFFu, sure, 4);
+    const uint32_t good = __reduce_max_sync(0xFFFFFFFFu, at > -INFINITY && sure >= static_cast<uint32_t>(ask.k) ? key_of(at) : 0u);
+    if (lane == 0 && good != 0) atomicMax(&sh.bound, good);
+    __syncthreads();
+    if (sh.bound != 0) bound = logit_of_key(sh.bound);
   } else if (ask.nucleus) {
-    WeightSum sum;
-#pragma unroll 2
-    for (int v = s.run_a + lane; v < s.run_z; v += 32) {
-      const Vec<DT> x(s.vec(v));
-#pragma unroll
-      for (int e = 0; e < kElems; ++e) sum.add(exponent_of(x.x[e], top, ask.steep));
-    }
-    ask.total = cluster_total(sh, sum.total());
+    ask.total = cluster_total(sh, weights_above<DT>(s, -INFINITY, top, ask.steep));
     // V weights of at most this (and half a unit of rounding each) stay below (1 - p) W; 1e-3 covers ex2 and log2
     const float each = static_cast<float>(ask.total) * (static_cast<float>((1u << 24) - ask.p24) * 0x1p-24f) / static_cast<float>(p.V) - 0.5f;
     if (each > 0.0f) bound = __fadd_rd(top, __fdiv_rd(log2f(each) - 40.0f - 1e-3f, ask.steep));
@@ -1042,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   ask.bound = bound;
   // ---- 2. the logits at or above the bound, by warp and in order -------------------------------
   int n = 0;
-#pragma unroll 1
+#pragma unroll 2
   for (int vb = s.run_a; vb < s.run_z; vb += 32) {
     const int v = vb + lane;
     uint32_t mask = 0;
@@ -1070,11 +1253,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const bool few = __syncthreads_and(listed >= 0) && (!ask.by_count || ask.k <= kGatherK);
   if (lane == 0) sh.ties[warp] = n;
   __syncthreads();
-  uint32_t at = 0, all = 0;
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) at += sh.ties[i];
-    all += sh.ties[i];
-  }
+  const uint32_t warp_n = lane < kWarps ? sh.ties[lane] : 0;
+  const uint32_t at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_n : 0), all = __reduce_add_sync(0xFFFFFFFFu, warp_n);
   const bool fits = few && all <= kGather;
   if (fits)
     for (int i = lane; i < listed; i += 32) {
@@ -1083,33 +1263,54 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
   if (tid == 0) sh.mine_n = fits ? all : kGather + 1;
   cluster_sync();
-  uint32_t gathered = 0;
-  for (uint32_t r = 0; r < cs; ++r) gathered += peer_u32(&sh.mine_n, r);
+  const uint32_t peer_n = lane < static_cast<int>(cs) ? peer_u32(&sh.mine_n, lane) : 0;
+  const uint32_t gathered = __reduce_add_sync(0xFFFFFFFFu, peer_n);
   if (gathered > kGather) {  // the same in every CTA
     cluster_sync();          // everyone has read the counts
-    cut_wide<DT>(s, sh, ask, listed);
+    cut_wide<DT>(s, sh, ask);
     return;
   }
   if (rank == 0) {
-    uint32_t to = all;
-    for (uint32_t r = 1; r < cs; ++r) {
-      const uint32_t m = peer_u32(&sh.mine_n, r);
-      for (uint32_t i = tid; i < m; i += kThreads) sh.gather[to + i] = peer_u64(&sh.gather[i], r);
-      to += m;
+    uint32_t from = peer_n;  // where lane l's CTA's logits end in the list
+#pragma unroll
+    for (int d = 1; d < kMaxCluster; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, from, d);
+      if (lane >= d) from += u;
+    }
+    for (uint32_t i0 = all; i0 < gathered; i0 += kThreads) {
+      const uint32_t i = i0 + tid;
+      uint32_t r = 0, begin = 0;
+#pragma unroll
+      for (int l = 0; l < kMaxCluster - 1; ++l) {
+        const uint32_t end = __shfl_sync(0xFFFFFFFFu, from, l);
+        if (i >= end && l + 1 < static_cast<int>(cs)) {
+          r = l + 1;
+          begin = end;
+        }
+      }
+      if (i < gathered) sh.gather[i] = peer_u64(&sh.gather[i - begin], r);
     }
   }
   cluster_sync();  // the first CTA has everything: the others leave
-  if (rank == 0) finish_gathered<DT>(sh, ask, static_cast<int>(gathered), reinterpret_cast<uint64_t*>(dyn));
+  if (rank == 0) {
+    if (gathered <= kShort) finish_short<DT>(sh, ask, static_cast<int>(gathered), reinterpret_cast<uint64_t*>(dyn));
+    else finish_gathered<DT>(sh, ask, static_cast<int>(gathered), reinterpret_cast<uint64_t*>(dyn));
+  }
 }
 
 template <int DT>
 cudaError_t launch_sample(SampleParams p, void* stream) {
   constexpr int kElt = DT == SV_BF16 ? 2 : 4;
-  int cs = 1;  // slices of about 32 KB: a row's CTAs share its passes
-  while (cs < kMaxCluster && static_cast<int64_t>(p.V) * kElt > cs * 32768) cs *= 2;
+  // CTAs per row: slices of at most 80 KB (two CTAs an SM), and smaller ones while all rows' CTAs are on the GPU at
+  // once (two of 512 threads an SM)
+  int cs = 1, sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int64_t bytes = static_cast<int64_t>(p.V) * kElt;
+  while (cs < kMaxCluster && (bytes > cs * 81920 || (bytes > cs * 16384 && 2 * static_cast<int64_t>(cs) * p.R <= 2 * sms))) cs *= 2;
   p.slice = ((p.V + cs - 1) / cs + 7) & ~7;
-  const size_t dyn = std::max(static_cast<size_t>(p.slice) * kElt + 32, sizeof(uint64_t) * kGather);  // (the sort's room too)
-  const cudaError_t e = allow_smem<sample_kernel<DT>>(dyn);
+  const size_t dyn = std::max(static_cast<size_t>(p.slice) * kElt + 32, sizeof(uint64_t) * kGather + sizeof(uint32_t) * 3 * kSteps);  // (the first CTA's room too)
+  e = allow_smem<sample_kernel<DT>>(dyn);
   if (e != cudaSuccess) return e;
   return launch_dependent(sample_kernel<DT>, dim3(static_cast<unsigned>(p.R) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
 }

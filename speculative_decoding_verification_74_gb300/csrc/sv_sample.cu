@@ -66,9 +66,8 @@ struct Shared {
     uint64_t gather[kGather];          // this CTA's listed logits: integer image << 32 | ~index; the first CTA's: everybody's
     struct {                           // cut_wide
       uint32_t limb[3][kSteps];
-      uint32_t all[kExchange];         // the cluster's keys of the exchanged step
-      uint64_t all_w[kExchange];
-      uint32_t mine[kExchange];        // this CTA's
+      uint32_t mine[kExchange];        // this CTA's keys of the exchanged step
+      uint64_t all_w[kExchange];       // the cluster's, sorted; weights
     };
   };
   uint32_t count[kSteps];
@@ -88,10 +87,9 @@ struct Shared {
   uint32_t from[kMaxCluster + 1];      // where each CTA's logits begin in the cluster's list
   uint32_t step, above_c, here_c;      // the step that holds a boundary
   uint64_t above_w;
-  uint32_t key, key_above_c, key_equal_c;
+  uint32_t key, key_above_c;
   uint64_t key_above_w;
   uint64_t end[2];                     // the prefix's last logit, and the weight up to it
-  uint32_t equal_before, equal_here;
   uint32_t cut;                        // first equal (vocabulary index) that is left out; entries of the sorted prefix
   uint32_t red[2][kWarps];
 };
@@ -417,6 +415,26 @@ struct Scale {
   }
 };
 
+// Bitonic sort, descending, of `size` (a power of two) entries.
+__device__ __noinline__ void sort_descending(uint64_t* x, int size) {
+#pragma unroll 1
+  for (int block = 2; block <= size; block *= 2)
+#pragma unroll 1
+    for (int stride = block / 2; stride > 0; stride /= 2) {
+      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
+        const uint64_t a = x[lo], b = x[hi];
+        if ((a < b) == ((lo & block) == 0)) {
+          x[lo] = b;
+          x[hi] = a;
+        }
+      }
+      // a warp's pairs of a stride up to 32 lie in 64 entries that only this warp touches until the next longer stride
+      if (stride > 32 || (stride == 1 && block >= 64)) __syncthreads(); else __syncwarp();
+    }
+  __syncthreads();
+}
+
 // The logits of one step, exchanged over the cluster and ranked: the boundary by count or weight, given the sums
 // above the step.
 template <int DT, bool kByWeight>
@@ -424,10 +442,7 @@ __device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, float
                               uint32_t above_c, uint64_t above_w, float top, float steep) {
   const uint32_t cs = cluster_size(), rank = cluster_rank();
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    sh.mine_n = 0;
-    sh.equal_before = sh.equal_here = 0;
-  }
+  if (tid == 0) sh.mine_n = 0;
   __syncthreads();
   const float hi = scale.above(step), lo = fmaxf(scale.below(step), bound);
 #pragma unroll 2
@@ -447,46 +462,35 @@ __device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, float
   __syncthreads();
   const uint32_t n = sh.from[cs];
   uint32_t key = 0;
-  uint64_t w = 0;
   if (tid < static_cast<int>(n)) {
     uint32_t r = 0;
     while (sh.from[r + 1] <= static_cast<uint32_t>(tid)) ++r;
     key = peer_u32(&sh.mine[tid - sh.from[r]], r);
-    w = weight_of(exponent_of(logit_of_key(key), top, steep));
-    sh.all[tid] = key;
-    sh.all_w[tid] = w;
   }
+  sh.all_w[tid] = key;  // (a logit's image is never 0)
   __syncthreads();
-  if (tid < static_cast<int>(n)) {
-    uint32_t more = 0, equal = 0;
-    uint64_t more_w = 0;
-    for (uint32_t i = 0; i < n; ++i) {
-      const uint32_t k = sh.all[i];
-      more += k > key;
-      equal += k == key;
-      if (kByWeight) more_w += k > key ? sh.all_w[i] : 0;
-    }
-    const bool here = kByWeight ? above_w + more_w < want && above_w + more_w + equal * w >= want
-                                : above_c + more < want && above_c + more + equal >= want;
-    if (here) {  // every holder of the key writes the same
-      if (!kByWeight)
-        for (uint32_t i = 0; i < n; ++i) more_w += sh.all[i] > key ? sh.all_w[i] : 0;
-      sh.key = key;
-      sh.key_above_c = above_c + more;
-      sh.key_above_w = above_w + more_w;
-      sh.key_equal_c = equal;
-      if (tid < static_cast<int>(sh.from[rank])) atomicAdd(&sh.equal_before, 1u);
-      else if (tid < static_cast<int>(sh.from[rank + 1])) atomicAdd(&sh.equal_here, 1u);
-    }
-  }
+  int size = 32;
+  while (size < static_cast<int>(n)) size *= 2;
+  sort_descending(sh.all_w, size);
+  // thread t has the t-th largest; runs of equals are one boundary
+  const uint32_t mine = static_cast<uint32_t>(sh.all_w[tid]);
+  const bool first = tid < static_cast<int>(n) && (tid == 0 || sh.all_w[tid - 1] != mine);
+  const uint64_t w = tid < static_cast<int>(n) ? weight_of(exponent_of(logit_of_key(mine), top, steep)) : 0;
+  const uint64_t at = above_w + block_scan(sh, w);
+  if (tid < static_cast<int>(n) && (kByWeight ? at < want && at + w >= want : above_c + tid + 1 == want)) sh.key = mine;
   __syncthreads();
   Boundary b;
   b.key = sh.key;
+  if (first && mine == b.key) {
+    sh.key_above_c = above_c + tid;
+    sh.key_above_w = at;
+  }
+  const bool equal = key == b.key && tid < static_cast<int>(n);
+  b.equal_c = __syncthreads_count(equal);
+  b.equal_before = __syncthreads_count(equal && tid < static_cast<int>(sh.from[rank]));
+  b.equal_here = __syncthreads_count(equal && tid >= static_cast<int>(sh.from[rank]) && tid < static_cast<int>(sh.from[rank + 1]));
   b.above_c = sh.key_above_c;
   b.above_w = sh.key_above_w;
-  b.equal_c = sh.key_equal_c;
-  b.equal_before = sh.equal_before;
-  b.equal_here = sh.equal_here;
   return b;
 }
 
@@ -519,28 +523,12 @@ struct Ask {
   bool by_count, nucleus, floor_on;
 };
 
+__device__ __forceinline__ Scale scale_of(const Ask& ask) {
+  return Scale::over(ask.top, ask.bound == -INFINITY ? 64.0f / ask.steep : __fsub_rn(ask.top, ask.bound));
+}
+
 // Up to 128 KB of shared memory is on its way at once: waits of microseconds, not inlined.
 __device__ __noinline__ void wait_piece(uint64_t* bar, uint32_t* status) { mbar_wait(bar, 0, status); }
-
-// Bitonic sort, descending, of `size` (a power of two) entries.
-__device__ __noinline__ void sort_descending(uint64_t* x, int size) {
-#pragma unroll 1
-  for (int block = 2; block <= size; block *= 2)
-#pragma unroll 1
-    for (int stride = block / 2; stride > 0; stride /= 2) {
-      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-        const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
-        const uint64_t a = x[lo], b = x[hi];
-        if ((a < b) == ((lo & block) == 0)) {
-          x[lo] = b;
-          x[hi] = a;
-        }
-      }
-      // a warp's pairs of a stride up to 32 lie in 64 entries that only this warp touches until the next longer stride
-      if (stride > 32 || (stride == 1 && block >= 64)) __syncthreads(); else __syncwarp();
-    }
-  __syncthreads();
-}
 
 // Step 3 for at most kShort gathered logits: thread t has the t-th, counts those before it in the order, and adds
 // their weights.
@@ -674,7 +662,7 @@ template <int DT>
 __device__ __noinline__ void finish_gathered(Shared& sh, const Ask& ask, int n, uint64_t* more) {
   const int tid = threadIdx.x;
   uint32_t* limb = reinterpret_cast<uint32_t*>(more + kGather);  // [3][kSteps]
-  const Scale scale = Scale::over(ask.top, ask.bound == -INFINITY ? 64.0f / ask.steep : __fsub_rn(ask.top, ask.bound));
+  const Scale scale = scale_of(ask);
   uint64_t last = 0;
   if (ask.by_count || ask.nucleus) {
     sh.count[tid] = 0;
@@ -848,45 +836,47 @@ template <int DT>
 __device__ __noinline__ void weights_around(const Slice<DT>& s, Shared& sh, const Ask& ask, const Scale& scale, int step,
                                             uint64_t (&out)[4]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < 9) sh.limb[tid / 3][tid % 3] = 0;
-  __syncthreads();
   // surely above: the packed sum; surely below: nothing; the few between, by their step
   const float hi = scale.above(step - 1), lo = fmaxf(scale.below(step + 1), ask.bound);
-  const uint64_t high = warp_sum(weights_above<DT>(s, hi, ask.top, ask.steep));
-  uint64_t rest = 0;  // of those between: before step - 1
+  WeightSum sum(ask.top, ask.steep);
+  uint32_t adds = 0;
+  uint64_t part[4] = {0, 0, 0, 0};  // of those between, by step (in registers: atomics on four addresses would queue up)
 #pragma unroll 2
-  for (int v = s.run_a + lane; v < s.run_z; v += 32) {
+  for (int v = s.run_a + lane; v < s.run_z; v += 32, ++adds) {
     const Vec<DT> x(s.vec(v));
+    uint32_t between = 0;
 #pragma unroll
-    for (int e = 0; e < Vec<DT>::kElems; ++e)
-      if (x.x[e] >= lo && x.x[e] <= hi && x.x[e] != -INFINITY) {
-        const int d = scale.step(x.x[e]) - step + 1;
-        const uint64_t w = weight_of(exponent_of(x.x[e], ask.top, ask.steep));
-        if (d < 0) {
-          rest += w;
-        } else if (d <= 2) {
-          for (int l = 0; l < 3; ++l) {
-            const uint32_t part = static_cast<uint32_t>(w >> (l * kLimb)) & ((1u << kLimb) - 1u);
-            if (part) atomicAdd(&sh.limb[l][d], part);
-          }
-        }
-      }
+    for (int e = 0; e < Vec<DT>::kElems; e += 2) {
+      sum.add(x.x[e] > hi ? x.x[e] : -INFINITY, x.x[e + 1] > hi ? x.x[e + 1] : -INFINITY);
+      between |= (x.x[e] >= lo && x.x[e] <= hi ? 1u : 0u) << e | (x.x[e + 1] >= lo && x.x[e + 1] <= hi ? 2u : 0u) << e;
+    }
+#pragma unroll 1
+    for (; between != 0; between &= between - 1) {
+      const float xe = s.at(v * Vec<DT>::kElems + __ffs(between) - 1);
+      const int d = scale.step(xe) - step + 1;
+      const uint64_t w = weight_of(exponent_of(xe, ask.top, ask.steep));  // (0 for -inf)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[i] += (i == 0 ? d < 0 : d == i - 1) ? w : 0;
+    }
   }
-  rest = warp_sum(rest);
-  if (lane == 0) sh.all_w[warp] = high + rest;
+  const uint64_t high = warp_sum(sum.total(adds * (Vec<DT>::kElems / 2)));
   __syncthreads();
-  if (tid == 0) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = warp_sum(part[i]) + (i == 0 ? high : 0);
+    if (lane == 0) sh.all_w[4 * warp + i] = t;
+  }
+  __syncthreads();
+  if (tid < 4) {
     uint64_t t = 0;
-    for (int w = 0; w < kWarps; ++w) t += sh.all_w[w];
-    sh.all_w[kWarps] = t;
-  } else if (tid <= 3) {
-    sh.all_w[kWarps + tid] = limbs_of(sh.limb[0][tid - 1], sh.limb[1][tid - 1], sh.limb[2][tid - 1]);
+    for (int w = 0; w < kWarps; ++w) t += sh.all_w[4 * w + tid];
+    sh.all_w[4 * kWarps + tid] = t;
   }
   cluster_sync();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     out[i] = 0;
-    for (uint32_t r = 0; r < cluster_size(); ++r) out[i] += peer_u64(&sh.all_w[kWarps + i], r);
+    for (uint32_t r = 0; r < cluster_size(); ++r) out[i] += peer_u64(&sh.all_w[4 * kWarps + i], r);
   }
   cluster_sync();  // the peers have read them
 }
@@ -901,29 +891,37 @@ __device__ __noinline__ uint32_t floor_key(float top, float steep, float least) 
   return hi;
 }
 
-// Step 3 for long lists.
+// The cluster's counts of the logits at or above the bound: thread t's step.
 template <int DT>
-__device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask& ask) {
+__device__ __noinline__ uint32_t count_steps(const Slice<DT>& s, Shared& sh, const Ask& ask) {
+  const Scale scale = scale_of(ask);
+  const float bound = ask.bound;
+  sh.count[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 2
+  for (int v = s.run_a + (threadIdx.x & 31); v < s.run_z; v += 32) {
+    const Vec<DT> x(s.vec(v));
+#pragma unroll
+    for (int e = 0; e < Vec<DT>::kElems; ++e)
+      if (x.x[e] >= bound && x.x[e] != -INFINITY) atomicAdd(&sh.count[scale.step(x.x[e])], 1u);
+  }
+  cluster_sync();
+  uint32_t c;
+  uint64_t none;
+  merged_step(sh, threadIdx.x, false, &c, &none);
+  return c;
+}
+
+// Step 3 for long lists; c: this thread's step of the histogram.
+template <int DT>
+__device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask& ask, uint32_t c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float top = ask.top, steep = ask.steep, bound = ask.bound;
   uint64_t total = ask.total;
   Boundary b = {};
   uint32_t ties_kept = 0;  // how many of the boundary's equals are kept, lowest indexes first
   if (ask.by_count || ask.nucleus) {
-    sh.count[tid] = 0;
-    const Scale scale = Scale::over(top, bound == -INFINITY ? 64.0f / steep : __fsub_rn(top, bound));
-    __syncthreads();
-#pragma unroll 2
-    for (int v = s.run_a + lane; v < s.run_z; v += 32) {
-      const Vec<DT> x(s.vec(v));
-#pragma unroll
-      for (int e = 0; e < Vec<DT>::kElems; ++e)
-        if (x.x[e] >= bound && x.x[e] != -INFINITY) atomicAdd(&sh.count[scale.step(x.x[e])], 1u);
-    }
-    cluster_sync();
-    uint32_t c;
-    uint64_t none;
-    merged_step(sh, tid, false, &c, &none);
+    const Scale scale = scale_of(ask);
     // a step's weight by its middle, in units of 2^-30: good to a part in a few hundred
     const float middle = scale.inv > 0.0f ? -(tid + 0.5f) / scale.inv * steep : 0.0f;
     const uint64_t about = static_cast<uint64_t>(static_cast<float>(c) * ex2_approx(middle) * 0x1p30f);
@@ -996,20 +994,39 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
   if (b.key == 0 || quota == 0) {
     cut = 0;
   } else if (quota < b.equal_here) {
-    const int first = s.run_a * Vec<DT>::kElems, end = s.run_z * Vec<DT>::kElems;
+    const float last = logit_of_key(b.key);
     uint32_t c = 0;
-    for (int pos = first + lane; pos < end; pos += 32) c += key_of(s.at(pos)) == b.key;
+#pragma unroll 2
+    for (int v = s.run_a + lane; v < s.run_z; v += 32) {
+      const Vec<DT> x(s.vec(v));
+#pragma unroll
+      for (int e = 0; e < Vec<DT>::kElems; ++e) c += x.x[e] == last;
+    }
     c = __reduce_add_sync(0xFFFFFFFFu, c);
     if (lane == 0) sh.ties[warp] = c;
     __syncthreads();
     uint32_t before = 0;
     for (int i = 0; i < warp; ++i) before += sh.ties[i];
     if (before < quota && before + c >= quota)
-      for (int base = first; base < end; base += 32) {
-        const bool equal = base + lane < end && key_of(s.at(base + lane)) == b.key;
-        const uint32_t set = __ballot_sync(0xFFFFFFFFu, equal);
-        if (equal && before + __popc(set & ((1u << lane) - 1u)) == quota - 1) sh.cut = static_cast<uint32_t>(s.index_of(base + lane)) + 1;
-        before += __popc(set);
+      for (int vb = s.run_a; vb < s.run_z && before < quota; vb += 32) {
+        uint32_t mask = 0;
+        if (vb + lane < s.run_z) {
+          const Vec<DT> x(s.vec(vb + lane));
+#pragma unroll
+          for (int e = 0; e < Vec<DT>::kElems; ++e) mask |= (x.x[e] == last ? 1u : 0u) << e;
+        }
+        uint32_t incl = __popc(mask);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+          if (lane >= d) incl += u;
+        }
+        const uint32_t excl = incl - __popc(mask);
+        if (before + excl < quota && before + incl >= quota) {
+          for (uint32_t left = quota - before - excl; left > 1; --left) mask &= mask - 1;
+          sh.cut = static_cast<uint32_t>(s.index_of((vb + lane) * Vec<DT>::kElems + __ffs(mask) - 1)) + 1;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
       }
     __syncthreads();
     cut = sh.cut;
@@ -1223,6 +1240,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(ask.least * 1.000001f, ask.steep)));
   if (!(bound < top)) bound = bound >= top ? top : -INFINITY;
   ask.bound = bound;
+  if (ask.nucleus && !ask.by_count) {  // top-p alone: its list may be long, which the counts tell for less than listing
+    const uint32_t c = count_steps<DT>(s, sh, ask);
+    const uint32_t before = block_scan32(sh, c);
+    if (tid == kThreads - 1) sh.here_c = before + c;
+    __syncthreads();
+    const uint32_t all = sh.here_c;
+    if (all > kGather) {
+      cut_wide<DT>(s, sh, ask, c);
+      return;
+    }
+  }
   // ---- 2. the logits at or above the bound, by warp and in order -------------------------------
   int n = 0;
 #pragma unroll 2
@@ -1267,7 +1295,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const uint32_t gathered = __reduce_add_sync(0xFFFFFFFFu, peer_n);
   if (gathered > kGather) {  // the same in every CTA
     cluster_sync();          // everyone has read the counts
-    cut_wide<DT>(s, sh, ask);
+    cut_wide<DT>(s, sh, ask, count_steps<DT>(s, sh, ask));
     return;
   }
   if (rank == 0) {

@@ -406,12 +406,14 @@ sv_status sv_verify_sample_noalloc(const void* target, int64_t t_row_stride, con
  * (k < 0, p outside (0, 1], q outside [0, 1], SV_DEV_BAD_FILTER) gives tokens -1, probabilities
  * NaN and a row of -inf.
  * Limits: 0 <= R <= SV_MAX_SAMPLE_ROWS, 1 <= V <= SV_MAX_SAMPLE_VOCAB, 0 <= M <= SV_MAX_SAMPLE_DRAWS.
- * R == 0 is a no-op.  Workspace: SV_STATUS_BYTES, zero-filled before the first use (the status word).
+ * R == 0 is a no-op.  Workspace: sv_sample_workspace_size(R, V) bytes, its first SV_STATUS_BYTES zero-filled before the
+ * first use (the status word).
  */
 #define SV_STATUS_BYTES 256
 #define SV_MAX_SAMPLE_ROWS (1 << 20)
 #define SV_MAX_SAMPLE_VOCAB (1 << 18)
 #define SV_MAX_SAMPLE_DRAWS 1024
+size_t sv_sample_workspace_size(int R, int V); /* 0 for invalid sizes */
 sv_status sv_sample_rows(const void* logits, int64_t row_stride, sv_dtype dt, int R, int V, const float* temperature,
                          const int32_t* top_k, const float* top_p, const float* min_p, const float* uniforms, int M,
                          int32_t* out_tokens, float* out_probs, void* out_rows, int64_t out_stride, void* ws,

@@ -71,6 +71,7 @@ _SIGS = {
     "sv_verify_sample_phase": (_c.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _u64, _u32, _vp, _c.c_int, _c.c_int,
                                           _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _vp, _vp, _vp, _vp,
                                           _vp, _vp, _sz, _vp]),
+    "sv_sample_workspace_size": (_sz, [_c.c_int, _c.c_int]),
     "sv_sample_rows": (_c.c_int, [_vp, _i64, _c.c_int, _c.c_int, _c.c_int, _vp, _vp, _vp, _vp, _vp, _c.c_int, _vp, _vp,
                                   _vp, _i64, _vp, _sz, _vp]),
     "sv_cache_reserve": (_c.c_int, [_vp, _vp, _c.c_int, _vp, _vp, _c.c_int, _vp, _vp, _sz, _vp]),
@@ -390,6 +391,10 @@ def sv_verify_sample_phase(target, t_row_stride, draft, d_row_stride, draft_toke
                                         _p(out_q), _p(out_flags), _p(ws), _ws_bytes(ws), _stream(stream)))
 
 
+def sv_sample_workspace_size(R: int, V: int) -> int:
+    return int(lib().sv_sample_workspace_size(R, V))
+
+
 def sv_sample_rows(logits, row_stride, dt, R, V, temperature, top_k, top_p, min_p, uniforms, M, out_tokens, out_probs,
                    out_rows, out_stride, ws, stream=None) -> None:
     if R > 0:
@@ -662,18 +667,25 @@ def _array(t, name: str, dtype, count: int) -> int | None:
     return _p(t)
 
 
-def _zeros(nbytes: int, device, stream) -> torch.Tensor:
-    """A zero-filled workspace whose fill is ordered before the call on `stream`."""
-    if stream is None:
+def _workspace(nbytes: int, device, stream=None, zeros=False) -> torch.Tensor:
+    """A workspace whose first SV_STATUS_BYTES (or all) are zero, the fill ordered before a call on `stream`."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
+        with torch.cuda.stream(s):
+            return _workspace(nbytes, device, zeros=zeros)
+    if zeros:
         return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
-    with torch.cuda.stream(s):
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:SV_STATUS_BYTES] = 0
+    return ws
 
 
 def sample_workspace(rows: int, vocab: int, device="cuda") -> torch.Tensor:
     """Workspace of sample() for that many rows (its first word is the device status word)."""
-    return torch.zeros(SV_STATUS_BYTES, dtype=torch.uint8, device=device)
+    n = sv_sample_workspace_size(rows, vocab)
+    if n == 0:
+        raise ValueError("invalid sizes for sv_sample_workspace_size")
+    return _workspace(n, device)
 
 
 def sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None, probs=True, filtered=None, out=None,
@@ -701,7 +713,7 @@ def sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None,
             raise ValueError("filtered must have the shape and type of logits")
         out_stride = _rows(filtered)[1] if R > 1 else V
     if ws is None:
-        ws = _zeros(SV_STATUS_BYTES, dev, stream)
+        ws = _workspace(sv_sample_workspace_size(R, V), dev, stream)
     n = R * M
     f32, i32 = torch.float32, torch.int32
     _check((_lib or lib()).sv_sample_rows(
@@ -834,10 +846,14 @@ class PagedCache:
 
 def attention_workspace(cache: PagedCache, q_heads: int) -> torch.Tensor:
     """Workspace of tree_attention() on this cache (its first word is the device status word)."""
+    return _workspace(attention_workspace_size(cache, q_heads), cache.k.device, zeros=True)
+
+
+def attention_workspace_size(cache: PagedCache, q_heads: int) -> int:
     n = sv_attention_workspace_size(cache.c, q_heads)
     if n == 0:
         raise ValueError(lib().sv_last_error_string().decode() or "invalid sizes for sv_attention_workspace_size")
-    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+    return n
 
 
 def tree_attention(q, cache: PagedCache, layer, seq_len, node_offsets, parent, Nmax, *, scale=None, window=0, sinks=0,
@@ -862,7 +878,7 @@ def tree_attention(q, cache: PagedCache, layer, seq_len, node_offsets, parent, N
     elif lse is False:
         lse = None
     if ws is None:
-        ws = _zeros(sv_attention_workspace_size(cache.c, H), q.device, stream)
+        ws = _workspace(attention_workspace_size(cache, H), q.device, stream, zeros=True)
     qs, os = q.stride(), out.stride()
     if n * H and (qs[2] != 1 or os[2] != 1):
         raise ValueError("the head dimension of q and out must be contiguous")

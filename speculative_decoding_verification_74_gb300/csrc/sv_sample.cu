@@ -19,6 +19,11 @@
 // against the exact weights of the steps around it), and that step's logits are exchanged and ranked by every CTA.
 // Where a step holds more logits than the exchange takes, the boundary is found by a radix descent on the integer image
 // of x instead.
+//
+// Many rows with a top-k (or min-p alone): the latency of a cluster's steps, not memory, bounds the above.  Such rows go
+// another way: maxima_kernel streams them once, in no order, and keeps the largest logit of every 128 bytes; select_kernel
+// (a CTA per row) takes the bound from these maxima, reads again only the 128-byte groups that reach it (about k of them)
+// and goes on with step 3.  Rows that it leaves (no top-k, bad input, too long a list) are marked for the clusters.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -57,7 +62,10 @@ struct SampleParams {
   void* out_rows;
   int64_t out_stride;
   uint32_t* status;
+  int32_t* left;           // [1 + R] the rows that select_kernel leaves to the clusters, after their number; or NULL: all
+  float* maxima;           // [R][groups]
   int32_t R, V, M, slice;  // slice: elements per CTA, a multiple of 8
+  int32_t groups, segments;
 };
 
 // Per-CTA state; the parts that peers read are written before a cluster barrier.
@@ -523,12 +531,39 @@ struct Ask {
   bool by_count, nucleus, floor_on;
 };
 
+// The row's parameters; SV_DEV_* bits of those that are out of range.
+__device__ __forceinline__ uint32_t read_ask(const SampleParams& p, int64_t row, Ask& ask) {
+  const float T = p.temperature[row];
+  const int k_in = p.top_k != nullptr ? p.top_k[row] : 0;
+  const float p_in = p.top_p != nullptr ? p.top_p[row] : 1.0f;
+  const float q_in = p.min_p != nullptr ? p.min_p[row] : 0.0f;
+  uint32_t bad = 0;
+  if (!(T >= 0.0f) || T == INFINITY) bad |= SV_DEV_BAD_TEMPERATURE;
+  if (k_in < 0 || !(p_in > 0.0f && p_in <= 1.0f) || !(q_in >= 0.0f && q_in <= 1.0f)) bad |= SV_DEV_BAD_FILTER;
+  const bool greedy = T == 0.0f;
+  ask.p = &p;
+  ask.row = row;
+  ask.total = 0;
+  ask.steep = greedy ? 1.0f : fminf(__fdiv_rn(1.44269504088896341f, T), FLT_MAX);
+  ask.k = greedy ? 1 : (k_in == 0 ? p.V : k_in);
+  ask.by_count = ask.k < p.V;
+  ask.nucleus = !greedy && p_in < 1.0f;
+  ask.floor_on = !greedy && q_in > 0.0f;
+  ask.least = ask.floor_on ? log2f(q_in) : -INFINITY;  // of y
+  ask.p24 = static_cast<uint32_t>(rintf(p_in * 16777216.0f));
+  return bad;
+}
+// Rows for maxima_kernel and select_kernel: their prefix's end follows from few logits.
+__device__ __forceinline__ bool by_maxima(const Ask& ask, uint32_t bad) {
+  return bad == 0 && (ask.by_count ? ask.k <= kGatherK : ask.floor_on && !ask.nucleus);
+}
+
 __device__ __forceinline__ Scale scale_of(const Ask& ask) {
   return Scale::over(ask.top, ask.bound == -INFINITY ? 64.0f / ask.steep : __fsub_rn(ask.top, ask.bound));
 }
 
 // Up to 128 KB of shared memory is on its way at once: waits of microseconds, not inlined.
-__device__ __noinline__ void wait_piece(uint64_t* bar, uint32_t* status) { mbar_wait(bar, 0, status); }
+__device__ __noinline__ void wait_piece(uint64_t* bar, uint32_t parity, uint32_t* status) { mbar_wait(bar, parity, status); }
 
 // Step 3 for at most kShort gathered logits: thread t has the t-th, counts those before it in the order, and adds
 // their weights.
@@ -957,7 +992,7 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
       find_step<true>(sh, c, about, max(limit >> 10, uint64_t(1)), 0, 0);
       uint32_t step = sh.step;
       cluster_sync();  // the peers have read the histogram, or the keys exchanged before
-      bool inside = false;
+      bool inside = false, all = false;
       uint64_t above_w = 0;
       if (!by_radix) {
         weights_around<DT>(s, sh, ask, scale, min(step, static_cast<uint32_t>(kSteps - 1)), near);
@@ -970,9 +1005,10 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
             ++step;
           }
         }
+        // a bound at min-p's threshold may lie above the boundary: then everything above the bound is kept (and so it is
+        // where the descent finds the boundary below the bound)
+        all = !inside && step == kSteps + 1 && above_w < limit;
       }
-      // (a bound at min-p's threshold may lie above the boundary: then everything above the bound is kept, and so it is
-      // where the descent finds the boundary below the bound)
       uint32_t here = 0;
       if (inside) {
         // how many logits the step holds, from the thread that has it
@@ -981,7 +1017,7 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
         here = sh.here_c;
       }
       if (inside && here <= kExchange) b = rank_step<DT, true>(s, sh, bound, scale, step, limit, 0, above_w, top, steep);
-      else b = descend<DT, true>(s, sh, limit, top, steep);
+      else if (!all) b = descend<DT, true>(s, sh, limit, top, steep);
       if (b.key != 0) {
         const uint64_t each = weight_of(exponent_of(logit_of_key(b.key), top, steep));
         ties_kept = each == 0 ? 0 : static_cast<uint32_t>((limit - b.above_w + each - 1) / each);
@@ -1043,14 +1079,12 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
   draw_slices<DT, false>(s, sh, ask, last, cut);
 }
 
+// One row by the cluster; `parity` of the copies' barriers.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+__device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, unsigned char* dyn, Shared& sh, uint32_t parity) {
   using Elem = typename Slice<DT>::Elem;
   constexpr int kElems = Vec<DT>::kElems;
-  extern __shared__ __align__(128) unsigned char dyn[];
-  __shared__ Shared sh;
   const uint32_t cs = cluster_size(), rank = cluster_rank();
-  const int64_t row = blockIdx.x / cs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Elem* x_row = static_cast<const Elem*>(p.logits) + row * p.row_stride;
   Slice<DT> s;
@@ -1063,13 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int run = (s.vecs + kWarps - 1) / kWarps;
   s.run_a = min(s.vecs, warp * run);
   s.run_z = min(s.vecs, s.run_a + run);
-  if (tid == 0) {
-    for (int i = 0; i < kPieces; ++i) mbar_init(&sh.bar[i], 1);
-    fence_proxy_async_smem();
-  }
   sh.count[tid] = 0;
-  __syncthreads();
-  pdl_wait();
   // whole 16-byte vectors by bulk copy, the slice's ragged ends element by element
   const int v0 = s.phase > 0 ? 1 : 0, v1 = (s.phase + s.n) / kElems;
   const int per_piece = max(1, v1 > v0 ? (v1 - v0 + kPieces - 1) / kPieces : 0);
@@ -1094,29 +1122,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
   }
   Ask ask;
-  const float T = p.temperature[row];
-  const int k_in = p.top_k != nullptr ? p.top_k[row] : 0;
-  const float p_in = p.top_p != nullptr ? p.top_p[row] : 1.0f;
-  const float q_in = p.min_p != nullptr ? p.min_p[row] : 0.0f;
-  uint32_t bad = 0;
-  if (!(T >= 0.0f) || T == INFINITY) bad |= SV_DEV_BAD_TEMPERATURE;
-  if (k_in < 0 || !(p_in > 0.0f && p_in <= 1.0f) || !(q_in >= 0.0f && q_in <= 1.0f)) bad |= SV_DEV_BAD_FILTER;
+  uint32_t bad = read_ask(p, row, ask);
   bool bad_uniform = false;
   for (int j = tid; j < p.M; j += kThreads) {
     const float u = p.uniforms[row * p.M + j];
     bad_uniform |= !(u >= 0.0f && u < 1.0f);
   }
-  const bool greedy = T == 0.0f;
-  ask.p = &p;
-  ask.row = row;
-  ask.total = 0;
-  ask.steep = greedy ? 1.0f : fminf(__fdiv_rn(1.44269504088896341f, T), FLT_MAX);
-  ask.k = greedy ? 1 : (k_in == 0 ? p.V : k_in);
-  ask.by_count = ask.k < p.V;
-  ask.nucleus = !greedy && p_in < 1.0f;
-  ask.floor_on = !greedy && q_in > 0.0f;
-  ask.least = ask.floor_on ? log2f(q_in) : -INFINITY;  // of y
-  ask.p24 = static_cast<uint32_t>(rintf(p_in * 16777216.0f));
   // The cut row is -inf but for what is kept: filled while the logits are on their way (a row cut in place only
   // after they have arrived), and the kept logits follow at the end.
   Elem* out_row = p.out_rows != nullptr ? static_cast<Elem*>(p.out_rows) + row * p.out_stride + s.first : nullptr;
@@ -1127,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (__syncthreads_or(bad_uniform)) bad |= SV_DEV_BAD_FILTER;
       if (!in_place) break;
       // every copy of the slice has landed before its place is overwritten
-      for (int i = 0; i < kPieces; ++i) wait_piece(&sh.bar[i], p.status);
+      for (int i = 0; i < kPieces; ++i) wait_piece(&sh.bar[i], parity, p.status);
       __syncthreads();
     }
     if (out_row != nullptr && in_place == (pass == 1)) {
@@ -1142,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // a warp waits for the copies that hold its run only
   for (int i = 0; i < kPieces; ++i) {
     const int a = v0 + i * per_piece;
-    if (a < s.run_z && min(v1, a + per_piece) > s.run_a) wait_piece(&sh.bar[i], p.status);
+    if (a < s.run_z && min(v1, a + per_piece) > s.run_a) wait_piece(&sh.bar[i], parity, p.status);
   }
   float group = -INFINITY;
 #pragma unroll 4
@@ -1326,6 +1337,241 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
 }
 
+// A cluster per row, or (kListed) resident clusters for the rows that select_kernel has left, in turn.
+template <int DT, bool kListed>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ Shared sh;
+  const int cluster = blockIdx.x / cluster_size(), clusters = gridDim.x / cluster_size();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPieces; ++i) mbar_init(&sh.bar[i], 1);
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  pdl_wait();
+  if (!kListed) {
+    sample_row<DT>(p, cluster, dyn, sh, 0);
+    return;
+  }
+  const int rows = p.left[0];
+  uint32_t parity = 0;
+#pragma unroll 1
+  for (int i = cluster; i < rows; i += clusters) {  // (a row's end has synchronised the cluster)
+    sample_row<DT>(p, p.left[1 + i], dyn, sh, parity);
+    parity ^= 1;
+    __syncthreads();
+    fence_proxy_async_smem();  // the next row's copies overwrite what this one has read and written
+  }
+}
+
+// ---- many rows: maxima of 128-byte groups, then a CTA per row ----------------------------------------
+constexpr int kMaxThreads = 256;
+constexpr int kMaxLoads = 4;                             // 16-byte loads of a thread at a time, and as many in flight
+constexpr int kSegmentVecs = kMaxThreads * kMaxLoads;    // 16 KB of a row
+constexpr int kMaxCtas = 4;                              // per SM
+constexpr int kGroupVecs = 8;
+constexpr int kSelectCtas = 3;                           // per SM
+constexpr int64_t kStreamBytes = 64 << 20;
+
+// 16 bytes of a row from its vector v on (vectors lie on 16-byte boundaries; -inf outside the row).
+template <int DT>
+__device__ __forceinline__ uint4 row_vec(const typename Slice<DT>::Elem* x_row, int phase, int V, int v) {
+  using Elem = typename Slice<DT>::Elem;
+  constexpr int kElems = Vec<DT>::kElems;
+  const int e0 = v * kElems - phase;
+  if (e0 >= 0 && e0 + kElems <= V) return __ldg(reinterpret_cast<const uint4*>(x_row + e0));
+  uint4 w;
+  Elem* e = reinterpret_cast<Elem*>(&w);
+#pragma unroll
+  for (int i = 0; i < kElems; ++i)
+    e[i] = e0 + i >= 0 && e0 + i < V ? x_row[e0 + i] : (DT == SV_BF16 ? static_cast<Elem>(0xFF80u) : static_cast<Elem>(0xFF800000u));
+  return w;
+}
+
+// Resident CTAs take 16 KB segments of rows in turn, the next one's loads in flight while one's maxima are taken.  Bound by
+// memory: nothing but loads, maxima and one float per 128 bytes written (and the cut row's -inf).
+template <int DT>
+__global__ void __launch_bounds__(kMaxThreads, kMaxCtas) maxima_kernel(const SampleParams p) {
+  using Elem = typename Slice<DT>::Elem;
+  constexpr int kElems = Vec<DT>::kElems;
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.left[0] = 0;
+  const uint32_t items = static_cast<uint32_t>(p.R) * p.segments;
+  auto wanted = [&](uint32_t item) {
+    Ask ask;
+    return item < items && by_maxima(ask, read_ask(p, item / p.segments, ask));
+  };
+  auto load = [&](uint32_t item, uint4 (&w)[kMaxLoads]) {
+    const uint32_t row = item / p.segments;
+    const Elem* x_row = static_cast<const Elem*>(p.logits) + row * p.row_stride;
+    const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(x_row) & 15u) / sizeof(Elem));
+    const int vecs = (phase + p.V + kElems - 1) / kElems;
+    const int v0 = static_cast<int>(item - row * p.segments) * kSegmentVecs + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kMaxLoads; ++i) {
+      const int v = v0 + i * kMaxThreads;
+      const uint32_t none = DT == SV_BF16 ? 0xFF80FF80u : 0xFF800000u;
+      w[i] = v < vecs ? row_vec<DT>(x_row, phase, p.V, v) : make_uint4(none, none, none, none);
+    }
+  };
+  uint4 w[kMaxLoads], w_next[kMaxLoads];
+  uint32_t item = blockIdx.x;
+  bool want = wanted(item), want_next = wanted(item + gridDim.x);
+  if (want) load(item, w);
+#pragma unroll 1
+  for (; item < items; item += gridDim.x) {
+    if (want_next) load(item + gridDim.x, w_next);
+    const bool want_later = wanted(item + 2 * gridDim.x);
+    const uint32_t row = item / p.segments;
+    const int segment = static_cast<int>(item - row * p.segments);
+    if (want && p.out_rows != nullptr) {  // (never the rows themselves: those are left to the clusters)
+      const int e0 = segment * kSegmentVecs * kElems;
+      const int n = max(0, min(kSegmentVecs * kElems, p.V - e0));
+      Elem* out = static_cast<Elem*>(p.out_rows) + row * p.out_stride + e0;
+      const Elem none = DT == SV_BF16 ? static_cast<Elem>(0xFF80u) : static_cast<Elem>(0xFF800000u);
+      const int head = min(n, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / sizeof(Elem)));
+      const int whole = (n - head) / kElems;
+      const uint32_t ninf = DT == SV_BF16 ? 0xFF80FF80u : 0xFF800000u;
+      for (int i = threadIdx.x; i < whole; i += kMaxThreads) reinterpret_cast<uint4*>(out + head)[i] = make_uint4(ninf, ninf, ninf, ninf);
+      for (int i = threadIdx.x; i < n - whole * kElems; i += kMaxThreads) out[i < head ? i : i + whole * kElems] = none;
+    }
+    if (want) {
+#pragma unroll
+      for (int i = 0; i < kMaxLoads; ++i) {
+        const Vec<DT> x(w[i]);
+        float m = x.x[0];
+#pragma unroll
+        for (int e = 1; e < kElems; ++e) m = max_nan(m, x.x[e]);
+#pragma unroll
+        for (int d = 1; d < kGroupVecs; d <<= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        const int g = (segment * kSegmentVecs + i * kMaxThreads + threadIdx.x) / kGroupVecs;
+        if ((threadIdx.x & (kGroupVecs - 1)) == 0 && g < p.groups) p.maxima[row * static_cast<int64_t>(p.groups) + g] = m;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxLoads; ++i) w[i] = w_next[i];
+    want = want_next;
+    want_next = want_later;
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const SampleParams p) {
+  using Elem = typename Slice<DT>::Elem;
+  constexpr int kElems = Vec<DT>::kElems;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ Shared sh;
+  uint64_t* more = reinterpret_cast<uint64_t*>(dyn);                                     // step 3's room
+  float* maxima = reinterpret_cast<float*>(dyn + sizeof(uint64_t) * kGather + sizeof(uint32_t) * 3 * kSteps);
+  uint16_t* groups = &sh.list[0][0];
+  constexpr int kMost = kWarps * kListPerWarp;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x;
+  sh.count[tid] = 0;
+  pdl_wait();
+  Ask ask;
+  const uint32_t bad = read_ask(p, row, ask);
+  bool bad_uniform = false;
+  for (int j = tid; j < p.M; j += kThreads) {
+    const float u = p.uniforms[row * p.M + j];
+    bad_uniform |= !(u >= 0.0f && u < 1.0f);
+  }
+  const bool mine = !__syncthreads_or(bad_uniform) && by_maxima(ask, bad);
+  const Elem* x_row = static_cast<const Elem*>(p.logits) + row * p.row_stride;
+  const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(x_row) & 15u) / sizeof(Elem));
+  const int vecs = (phase + p.V + kElems - 1) / kElems, n_groups = (vecs + kGroupVecs - 1) / kGroupVecs;
+  const uint32_t none_key = key_of(-INFINITY), inf_key = key_of(INFINITY);
+  uint32_t hi = 0, lo = 0xFFFFFFFFu;
+  if (mine)
+#pragma unroll 4
+    for (int g = tid; g < n_groups; g += kThreads) {
+      const float m = p.maxima[row * p.groups + g];
+      maxima[g] = m;
+      const uint32_t key = key_of(m);
+      hi = max(hi, key);
+      if (key > none_key) lo = min(lo, key);
+    }
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  if (lane == 0) {
+    sh.red[0][warp] = hi;
+    sh.red[1][warp] = lo;
+  }
+  __syncthreads();
+  const uint32_t top_key = __reduce_max_sync(0xFFFFFFFFu, sh.red[0][lane & (kWarps - 1)]);
+  const uint32_t low_key = __reduce_min_sync(0xFFFFFFFFu, sh.red[1][lane & (kWarps - 1)]);
+  if (!mine || top_key >= inf_key || top_key <= none_key) {
+    if (tid == 0) p.left[1 + atomicAdd(p.left, 1)] = static_cast<int>(row);  // (in any order: rows do not depend on it)
+    return;
+  }
+  const float top = logit_of_key(top_key);
+  ask.top = top;
+  // the bound: the k-th largest maximum has k logits at or above it (a step's lower end, a little lower than the
+  // roundings of step() may put it)
+  float bound = -INFINITY;
+  if (ask.by_count) {
+    const Scale scale = Scale::over(top, __fsub_rn(top, logit_of_key(low_key)));
+    for (int g = tid; g < n_groups; g += kThreads)
+      if (maxima[g] > -INFINITY) atomicAdd(&sh.count[scale.step(maxima[g])], 1u);
+    __syncthreads();
+    find_step<false>(sh, sh.count[tid], 0, ask.k, 0, 0);
+    if (sh.step != 0xFFFFFFFFu)
+      bound = scale.inv > 0.0f ? __fsub_rd(top, __fmul_ru(static_cast<float>(sh.step + 1) / scale.inv, 1.00001f)) : top;
+  }
+  if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(ask.least * 1.000001f, ask.steep)));
+  if (!(bound < top)) bound = bound >= top ? top : -INFINITY;
+  ask.bound = bound;
+  ask.out_row = p.out_rows != nullptr ? static_cast<Elem*>(p.out_rows) + row * p.out_stride : nullptr;
+  // the groups that reach it, in order: thread t looks at a stretch
+  const int per = (n_groups + kThreads - 1) / kThreads, a = min(n_groups, tid * per), b = min(n_groups, a + per);
+  uint32_t c = 0;
+  for (int g = a; g < b; ++g) c += maxima[g] >= bound && maxima[g] > -INFINITY;
+  uint32_t at = block_scan32(sh, c);
+  if (tid == kThreads - 1) sh.here_c = at + c;
+  for (int g = a; g < b; ++g)
+    if (maxima[g] >= bound && maxima[g] > -INFINITY) {
+      if (at < kMost) groups[at] = static_cast<uint16_t>(g);
+      ++at;
+    }
+  __syncthreads();
+  const int listed = static_cast<int>(sh.here_c);
+  __syncthreads();
+  // their logits at or above the bound, in order: eight threads a group
+  int n = 0;
+  bool too_many = listed > kMost;
+  for (int g0 = 0; g0 < listed && !too_many; g0 += kThreads / kGroupVecs) {
+    const int g = g0 + tid / kGroupVecs;
+    const int v = g < listed ? groups[g] * kGroupVecs + tid % kGroupVecs : vecs;
+    uint32_t mask = 0;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (v < vecs) w = row_vec<DT>(x_row, phase, p.V, v);
+    const Vec<DT> x(w);
+    if (v < vecs)
+#pragma unroll
+      for (int e = 0; e < kElems; ++e) mask |= (x.x[e] >= bound && x.x[e] != -INFINITY ? 1u : 0u) << e;
+    const uint32_t count = __popc(mask);
+    uint32_t to = n + block_scan32(sh, count);
+    if (tid == kThreads - 1) sh.here_c = to + count;
+    __syncthreads();
+    n = static_cast<int>(sh.here_c);
+    too_many = n > kGather;
+    if (!too_many)
+#pragma unroll
+      for (int e = 0; e < kElems; ++e)
+        if ((mask >> e) & 1u) sh.gather[to++] = static_cast<uint64_t>(key_of(x.x[e])) << 32 | static_cast<uint32_t>(~(v * kElems + e - phase));
+    __syncthreads();
+  }
+  if (too_many) {
+    if (tid == 0) p.left[1 + atomicAdd(p.left, 1)] = static_cast<int>(row);
+    return;
+  }
+  if (n <= kShort) finish_short<DT>(sh, ask, n, more);
+  else finish_gathered<DT>(sh, ask, n, more);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+int groups_of(int V) { return (V + 2 * 4) / (4 * kGroupVecs) + 1; }  // float32 rows have the most
+
 template <int DT>
 cudaError_t launch_sample(SampleParams p, void* stream) {
   constexpr int kElt = DT == SV_BF16 ? 2 : 4;
@@ -1338,15 +1584,32 @@ cudaError_t launch_sample(SampleParams p, void* stream) {
   while (cs < kMaxCluster && (bytes > cs * 81920 || (bytes > cs * 16384 && 2 * static_cast<int64_t>(cs) * p.R <= 2 * sms))) cs *= 2;
   p.slice = ((p.V + cs - 1) / cs + 7) & ~7;
   const size_t dyn = std::max(static_cast<size_t>(p.slice) * kElt + 32, sizeof(uint64_t) * kGather + sizeof(uint32_t) * 3 * kSteps);  // (the first CTA's room too)
-  e = allow_smem<sample_kernel<DT>>(dyn);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(sample_kernel<DT>, dim3(static_cast<unsigned>(p.R) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
+  if (p.left != nullptr) {
+    p.segments = ((p.V + 2 * (16 / kElt)) / (16 / kElt) + kSegmentVecs) / kSegmentVecs;
+    const int64_t items = static_cast<int64_t>(p.R) * p.segments;
+    e = launch_dependent(maxima_kernel<DT>, dim3(static_cast<unsigned>(std::min<int64_t>(items, kMaxCtas * sms))), kMaxThreads, 0, stream, SV_KERNEL_SAMPLE, 1, p);
+    if (e != cudaSuccess) return e;
+    const size_t room = sizeof(uint64_t) * kGather + sizeof(uint32_t) * 3 * kSteps + sizeof(float) * p.groups;
+    if ((e = allow_smem<select_kernel<DT>>(room)) != cudaSuccess) return e;
+    e = launch_dependent(select_kernel<DT>, dim3(p.R), kThreads, room, stream, SV_KERNEL_SAMPLE, 1, p);
+    if (e != cudaSuccess) return e;
+    if ((e = allow_smem<sample_kernel<DT, true>>(dyn)) != cudaSuccess) return e;
+    const int clusters = std::min(p.R, std::max(1, 2 * sms / cs));
+    return launch_dependent(sample_kernel<DT, true>, dim3(static_cast<unsigned>(clusters) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
+  }
+  if ((e = allow_smem<sample_kernel<DT, false>>(dyn)) != cudaSuccess) return e;
+  return launch_dependent(sample_kernel<DT, false>, dim3(static_cast<unsigned>(p.R) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
 }
 
 }  // namespace
 }  // namespace sv
 
 using namespace sv;
+
+extern "C" size_t sv_sample_workspace_size(int R, int V) {
+  if (R < 0 || R > SV_MAX_SAMPLE_ROWS || V < 1 || V > SV_MAX_SAMPLE_VOCAB) return 0;
+  return SV_STATUS_BYTES + round256(sizeof(int32_t) * (1 + R)) + sizeof(float) * static_cast<size_t>(R) * groups_of(V);
+}
 
 extern "C" sv_status sv_sample_rows(const void* logits, int64_t row_stride, sv_dtype dt, int R, int V,
                                     const float* temperature, const int32_t* top_k, const float* top_p,
@@ -1368,7 +1631,7 @@ extern "C" sv_status sv_sample_rows(const void* logits, int64_t row_stride, sv_d
     return set_error(SV_ERR_INVALID_ARG, "row stride below V = %d", V);
   if (out_rows == logits && out_stride != row_stride)
     return set_error(SV_ERR_INVALID_ARG, "rows cut in place keep their stride");
-  sv_status st = check_workspace(ws, ws_bytes, SV_STATUS_BYTES);
+  sv_status st = check_workspace(ws, ws_bytes, sv_sample_workspace_size(R, V));
   if (st != SV_OK) return st;
   SampleParams p = {};
   p.logits = logits;
@@ -1386,5 +1649,11 @@ extern "C" sv_status sv_sample_rows(const void* logits, int64_t row_stride, sv_d
   p.R = R;
   p.V = V;
   p.M = M;
+  p.groups = groups_of(V);
+  p.maxima = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + SV_STATUS_BYTES + round256(sizeof(int32_t) * (1 + R)));
+  // by the maxima where rows may have a top-k or min-p and there is enough to stream (below, the clusters' one launch is
+  // quicker); rows cut in place are not: their logits are needed again after the fill
+  if ((top_k != nullptr || min_p != nullptr) && static_cast<int64_t>(R) * V * static_cast<int64_t>(elt) >= kStreamBytes && out_rows != logits)
+    p.left = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + SV_STATUS_BYTES);
   return launch_status(dt == SV_BF16 ? launch_sample<SV_BF16>(p, stream) : launch_sample<SV_F32>(p, stream), "sample");
 }

@@ -42,10 +42,11 @@ constexpr int kSteps = kThreads;        // histogram steps: one per thread
 constexpr int kMaxCluster = 8;
 constexpr int kPieces = 4;              // bulk copies (and barriers) per slice
 constexpr int kListPerWarp = 384;       // listed logits per warp; a warp with more walks its run instead
-constexpr int kExchange = kThreads;     // logits of one step that the cluster exchanges: one per thread
+constexpr int kExchange = 2 * kThreads; // logits of one step that the cluster exchanges: two per thread
 constexpr int kLimb = 14;
 constexpr int kGather = 2048;           // logits that one CTA sorts
 constexpr int kGatherK = 1024;          // largest k that goes that way
+constexpr int kTries = 8;               // estimates of the step that holds a top-p boundary, before a radix descent
 constexpr int kRanks = 8;               // order statistics of a CTA's groups that it publishes
 constexpr int kShort = 128;             // a gathered list this short is ranked by counting, a longer one sorted
 
@@ -443,23 +444,43 @@ __device__ __noinline__ void sort_descending(uint64_t* x, int size) {
   __syncthreads();
 }
 
+// Adds the marked logits of vector v (a lane's bits) to the warp's list, in order; n: how many it has, or would have.
+template <int kElems>
+__device__ __forceinline__ void list_marked(Shared& sh, int& n, uint32_t marked, int v) {
+  const int lane = threadIdx.x & 31, c = __popc(marked);
+  int incl = c;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += u;
+  }
+  int at = n + incl - c;
+  n += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  if (n <= kListPerWarp)
+    for (uint32_t m = marked; m != 0; m &= m - 1) sh.list[threadIdx.x >> 5][at++] = static_cast<uint16_t>(v * kElems + __ffs(m) - 1);
+}
+
 // The logits of one step, exchanged over the cluster and ranked: the boundary by count or weight, given the sums
-// above the step.
+// above the step, and how many logits the warp has listed among which they are (-1: none).
 template <int DT, bool kByWeight>
 __device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, float bound, const Scale& scale, int step, uint64_t want,
-                              uint32_t above_c, uint64_t above_w, float top, float steep) {
+                              uint32_t above_c, uint64_t above_w, float top, float steep, int listed) {
   const uint32_t cs = cluster_size(), rank = cluster_rank();
   const int tid = threadIdx.x;
   if (tid == 0) sh.mine_n = 0;
   __syncthreads();
   const float hi = scale.above(step), lo = fmaxf(scale.below(step), bound);
+  auto exchange = [&](float x) {
+    if (x >= lo && x <= hi && x != -INFINITY && scale.step(x) == step) sh.mine[atomicAdd(&sh.mine_n, 1u)] = key_of(x);
+  };
+#pragma unroll 1
+  for (int i = tid & 31; i < listed; i += 32) exchange(s.at(sh.list[tid >> 5][i]));
+  if (listed < 0)
 #pragma unroll 2
   for (int v = s.run_a + (tid & 31); v < s.run_z; v += 32) {
     const Vec<DT> x(s.vec(v));
 #pragma unroll
-    for (int e = 0; e < Vec<DT>::kElems; ++e)
-      if (x.x[e] >= lo && x.x[e] <= hi && x.x[e] != -INFINITY && scale.step(x.x[e]) == step)
-        sh.mine[atomicAdd(&sh.mine_n, 1u)] = key_of(x.x[e]);
+    for (int e = 0; e < Vec<DT>::kElems; ++e) exchange(x.x[e]);
   }
   cluster_sync();
   if (tid <= static_cast<int>(cs)) {
@@ -468,35 +489,54 @@ __device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, float
     sh.from[tid] = n;
   }
   __syncthreads();
-  const uint32_t n = sh.from[cs];
-  uint32_t key = 0;
-  if (tid < static_cast<int>(n)) {
-    uint32_t r = 0;
-    while (sh.from[r + 1] <= static_cast<uint32_t>(tid)) ++r;
-    key = peer_u32(&sh.mine[tid - sh.from[r]], r);
+  const int n = static_cast<int>(sh.from[cs]);
+  uint32_t key[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = tid + j * kThreads;
+    key[j] = 0;  // (a logit's image is never 0)
+    if (i < n) {
+      uint32_t r = 0;
+      while (sh.from[r + 1] <= static_cast<uint32_t>(i)) ++r;
+      key[j] = peer_u32(&sh.mine[i - sh.from[r]], r);
+    }
+    sh.all_w[i] = key[j];
   }
-  sh.all_w[tid] = key;  // (a logit's image is never 0)
   __syncthreads();
   int size = 32;
-  while (size < static_cast<int>(n)) size *= 2;
+  while (size < n) size *= 2;
   sort_descending(sh.all_w, size);
-  // thread t has the t-th largest; runs of equals are one boundary
-  const uint32_t mine = static_cast<uint32_t>(sh.all_w[tid]);
-  const bool first = tid < static_cast<int>(n) && (tid == 0 || sh.all_w[tid - 1] != mine);
-  const uint64_t w = tid < static_cast<int>(n) ? weight_of(exponent_of(logit_of_key(mine), top, steep)) : 0;
-  const uint64_t at = above_w + block_scan(sh, w);
-  if (tid < static_cast<int>(n) && (kByWeight ? at < want && at + w >= want : above_c + tid + 1 == want)) sh.key = mine;
+  // thread t has the 2t-th largest and the next; runs of equals are one boundary
+  uint32_t mine[2];
+  uint64_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    mine[j] = static_cast<uint32_t>(sh.all_w[2 * tid + j]);
+    w[j] = mine[j] != 0 ? weight_of(exponent_of(logit_of_key(mine[j]), top, steep)) : 0;
+  }
+  uint64_t at[2];
+  at[0] = above_w + block_scan(sh, w[0] + w[1]);
+  at[1] = at[0] + w[0];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (mine[j] != 0 && (kByWeight ? at[j] < want && at[j] + w[j] >= want : above_c + 2 * tid + j + 1 == want)) sh.key = mine[j];
   __syncthreads();
   Boundary b;
   b.key = sh.key;
-  if (first && mine == b.key) {
-    sh.key_above_c = above_c + tid;
-    sh.key_above_w = at;
+  b.equal_c = b.equal_before = b.equal_here = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = 2 * tid + j;
+    if (mine[j] == b.key && (i == 0 || static_cast<uint32_t>(sh.all_w[i - 1]) != b.key)) {
+      sh.key_above_c = above_c + i;
+      sh.key_above_w = at[j];
+    }
+    const int own = tid + j * kThreads;
+    const bool equal = key[j] == b.key;
+    b.equal_c += __syncthreads_count(equal);
+    b.equal_before += __syncthreads_count(equal && own < static_cast<int>(sh.from[rank]));
+    b.equal_here += __syncthreads_count(equal && own >= static_cast<int>(sh.from[rank]) && own < static_cast<int>(sh.from[rank + 1]));
   }
-  const bool equal = key == b.key && tid < static_cast<int>(n);
-  b.equal_c = __syncthreads_count(equal);
-  b.equal_before = __syncthreads_count(equal && tid < static_cast<int>(sh.from[rank]));
-  b.equal_here = __syncthreads_count(equal && tid >= static_cast<int>(sh.from[rank]) && tid < static_cast<int>(sh.from[rank + 1]));
   b.above_c = sh.key_above_c;
   b.above_w = sh.key_above_w;
   return b;
@@ -866,32 +906,50 @@ __device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const A
   cluster_sync();  // no CTA leaves while a peer may still read its shared memory
 }
 
-// The cluster's exact weight of the steps before `step` - 1, and of `step` - 1, `step` and `step` + 1.
+// The cluster's exact weight of the steps before `step` - 1, and of `step` - 1, `step` and `step` + 1.  Returns how many
+// logits the warp has listed that may lie in these three, or -1 for too many.
 template <int DT>
-__device__ __noinline__ void weights_around(const Slice<DT>& s, Shared& sh, const Ask& ask, const Scale& scale, int step,
-                                            uint64_t (&out)[4]) {
+__device__ __noinline__ int weights_around(const Slice<DT>& s, Shared& sh, const Ask& ask, const Scale& scale, int step,
+                                           uint64_t (&out)[4]) {
+  constexpr int kElems = Vec<DT>::kElems;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // surely above: the packed sum; surely below: nothing; the few between, by their step
+  // surely above: the packed sum; surely below: nothing; the few between are listed and weighed by their step (in
+  // registers: atomics on four addresses would queue up)
   const float hi = scale.above(step - 1), lo = fmaxf(scale.below(step + 1), ask.bound);
   WeightSum sum(ask.top, ask.steep);
   uint32_t adds = 0;
-  uint64_t part[4] = {0, 0, 0, 0};  // of those between, by step (in registers: atomics on four addresses would queue up)
+  int n = 0;
 #pragma unroll 2
-  for (int v = s.run_a + lane; v < s.run_z; v += 32, ++adds) {
-    const Vec<DT> x(s.vec(v));
+  for (int vb = s.run_a; vb < s.run_z; vb += 32) {
+    const int v = vb + lane;
     uint32_t between = 0;
+    if (v < s.run_z) {
+      const Vec<DT> x(s.vec(v));
 #pragma unroll
-    for (int e = 0; e < Vec<DT>::kElems; e += 2) {
-      sum.add(x.x[e] > hi ? x.x[e] : -INFINITY, x.x[e + 1] > hi ? x.x[e + 1] : -INFINITY);
-      between |= (x.x[e] >= lo && x.x[e] <= hi ? 1u : 0u) << e | (x.x[e + 1] >= lo && x.x[e + 1] <= hi ? 2u : 0u) << e;
+      for (int e = 0; e < kElems; e += 2) {
+        sum.add(x.x[e] > hi ? x.x[e] : -INFINITY, x.x[e + 1] > hi ? x.x[e + 1] : -INFINITY);
+        between |= (x.x[e] >= lo && x.x[e] <= hi ? 1u : 0u) << e | (x.x[e + 1] >= lo && x.x[e + 1] <= hi ? 2u : 0u) << e;
+      }
+      ++adds;
     }
-#pragma unroll 1
-    for (; between != 0; between &= between - 1) {
-      const float xe = s.at(v * Vec<DT>::kElems + __ffs(between) - 1);
-      const int d = scale.step(xe) - step + 1;
-      const uint64_t w = weight_of(exponent_of(xe, ask.top, ask.steep));  // (0 for -inf)
+    if (__any_sync(0xFFFFFFFFu, between != 0)) list_marked<kElems>(sh, n, between, v);
+  }
+  uint64_t part[4] = {0, 0, 0, 0};
+  auto weigh = [&](float x) {
+    const int d = scale.step(x) - step + 1;
+    const uint64_t w = weight_of(exponent_of(x, ask.top, ask.steep));  // (0 for -inf)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[i] += (i == 0 ? d < 0 : d == i - 1) ? w : 0;
+    for (int i = 0; i < 4; ++i) part[i] += (i == 0 ? d < 0 : d == i - 1) ? w : 0;
+  };
+  __syncwarp();
+  if (n <= kListPerWarp) {
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) weigh(s.at(sh.list[warp][i]));
+  } else {
+#pragma unroll 1
+    for (int pos = s.run_a * kElems + lane; pos < s.run_z * kElems; pos += 32) {
+      const float x = s.at(pos);
+      if (x >= lo && x <= hi) weigh(x);
     }
   }
   const uint64_t high = warp_sum(sum.total(adds * (Vec<DT>::kElems / 2)));
@@ -914,6 +972,7 @@ __device__ __noinline__ void weights_around(const Slice<DT>& s, Shared& sh, cons
     for (uint32_t r = 0; r < cluster_size(); ++r) out[i] += peer_u64(&sh.all_w[4 * kWarps + i], r);
   }
   cluster_sync();  // the peers have read them
+  return n <= kListPerWarp ? n : -1;
 }
 
 // The image of the smallest logit whose exponent reaches `least` (<= 0): min-p's threshold, exactly.
@@ -961,6 +1020,7 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
     const float middle = scale.inv > 0.0f ? -(tid + 0.5f) / scale.inv * steep : 0.0f;
     const uint64_t about = static_cast<uint64_t>(static_cast<float>(c) * ex2_approx(middle) * 0x1p30f);
     uint64_t near[4];
+    int listed = -1;
     bool by_radix = false;
     if (ask.by_count) {
       find_step<false>(sh, c, 0, ask.k, 0, 0);
@@ -970,11 +1030,11 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
         by_radix = here > kExchange;
         uint64_t above_w = 0;
         if (ask.nucleus) {
-          weights_around<DT>(s, sh, ask, scale, step, near);
+          listed = weights_around<DT>(s, sh, ask, scale, step, near);
           above_w = near[0] + near[1];
         }
         if (by_radix) b = descend<DT, false>(s, sh, ask.k, top, steep);
-        else b = rank_step<DT, false>(s, sh, bound, scale, step, ask.k, above_c, above_w, top, steep);
+        else b = rank_step<DT, false>(s, sh, bound, scale, step, ask.k, above_c, above_w, top, steep, listed);
         ties_kept = ask.k - b.above_c;
       }  // else fewer than k logits: all are kept
       if (ask.nucleus) {  // W: what lies above the boundary, and its kept equals
@@ -988,35 +1048,52 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
     }
     if (ask.nucleus) {
       const uint64_t limit = max(share_of(total, ask.p24), uint64_t(1));
-      // the step whose weight makes the sum reach the limit, about; its neighbours are weighed with it
-      find_step<true>(sh, c, about, max(limit >> 10, uint64_t(1)), 0, 0);
-      uint32_t step = sh.step;
       cluster_sync();  // the peers have read the histogram, or the keys exchanged before
+      // The step whose weight makes the sum reach the limit, about; it is weighed with its neighbours, exactly, and if it
+      // is not one of them, the estimate is set right there and another step chosen (few heavy logits make it that far
+      // off).
+      const uint64_t ahead = by_radix ? 0 : block_scan(sh, about);
+      uint64_t want = max(limit >> 10, uint64_t(1));
       bool inside = false, all = false;
       uint64_t above_w = 0;
-      if (!by_radix) {
-        weights_around<DT>(s, sh, ask, scale, min(step, static_cast<uint32_t>(kSteps - 1)), near);
-        step = min(step, static_cast<uint32_t>(kSteps - 1)) - 1;
+      int step = kSteps - 1;
+#pragma unroll 1
+      for (int tries = 0; tries < kTries && !by_radix && !inside && !all; ++tries) {
+        const int last = step;
+        const bool below = tries > 0 && near[0] >= limit;  // the boundary lies before the weighed steps
+        if (tid == 0) sh.step = kSteps - 1;
+        __syncthreads();
+        if (ahead < want && ahead + about >= want) sh.step = tid;
+        __syncthreads();
+        step = sh.step;
+        if (tries > 0) step = below ? min(step, last - 3) : max(step, last + 3);
+        step = max(0, min(step, kSteps - 1));
+        listed = weights_around<DT>(s, sh, ask, scale, step, near);
         above_w = near[0];
+        int in = step - 1;
         for (int i = 1; i < 4 && !inside; ++i) {
           if (above_w < limit && above_w + near[i] >= limit) inside = true;
           else {
             above_w += near[i];
-            ++step;
+            ++in;
           }
         }
         // a bound at min-p's threshold may lie above the boundary: then everything above the bound is kept (and so it is
         // where the descent finds the boundary below the bound)
-        all = !inside && step == kSteps + 1 && above_w < limit;
+        all = !inside && step == kSteps - 1 && above_w < limit;
+        if (tid == max(step - 1, 0)) sh.above_w = ahead;
+        __syncthreads();
+        want = max(static_cast<int64_t>((limit >> 10) + sh.above_w - (near[0] >> 10)), int64_t(1));
+        if (inside) step = in;
       }
       uint32_t here = 0;
       if (inside) {
         // how many logits the step holds, from the thread that has it
-        if (tid == static_cast<int>(step)) sh.here_c = c;
+        if (tid == step) sh.here_c = c;
         __syncthreads();
         here = sh.here_c;
       }
-      if (inside && here <= kExchange) b = rank_step<DT, true>(s, sh, bound, scale, step, limit, 0, above_w, top, steep);
+      if (inside && here <= kExchange) b = rank_step<DT, true>(s, sh, bound, scale, step, limit, 0, above_w, top, steep, listed);
       else if (!all) b = descend<DT, true>(s, sh, limit, top, steep);
       if (b.key != 0) {
         const uint64_t each = weight_of(exponent_of(logit_of_key(b.key), top, steep));
@@ -1273,19 +1350,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
 #pragma unroll
       for (int e = 0; e < kElems; ++e) mask |= (x.x[e] >= bound && x.x[e] != -INFINITY ? 1u : 0u) << e;
     }
-    if (__any_sync(0xFFFFFFFFu, mask != 0)) {
-      const int c = __popc(mask);
-      int incl = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += u;
-      }
-      int at = n + incl - c;
-      n += __shfl_sync(0xFFFFFFFFu, incl, 31);
-      if (n <= kListPerWarp)
-        for (uint32_t m = mask; m != 0; m &= m - 1) sh.list[warp][at++] = static_cast<uint16_t>(v * kElems + __ffs(m) - 1);
-    }
+    if (__any_sync(0xFFFFFFFFu, mask != 0)) list_marked<kElems>(sh, n, mask, v);
   }
   const int listed = n <= kListPerWarp ? n : -1;
   // ---- 3. gathered by the first CTA, if they are few -----------------------------------------------
@@ -1575,13 +1640,13 @@ int groups_of(int V) { return (V + 2 * 4) / (4 * kGroupVecs) + 1; }  // float32 
 template <int DT>
 cudaError_t launch_sample(SampleParams p, void* stream) {
   constexpr int kElt = DT == SV_BF16 ? 2 : 4;
-  // CTAs per row: slices of at most 80 KB (two CTAs an SM), and smaller ones while all rows' CTAs are on the GPU at
+  // CTAs per row: slices of at most 78 KB (two CTAs an SM), and smaller ones while all rows' CTAs are on the GPU at
   // once (two of 512 threads an SM)
   int cs = 1, sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int64_t bytes = static_cast<int64_t>(p.V) * kElt;
-  while (cs < kMaxCluster && (bytes > cs * 81920 || (bytes > cs * 16384 && 2 * static_cast<int64_t>(cs) * p.R <= 2 * sms))) cs *= 2;
+  while (cs < kMaxCluster && (bytes > cs * 79872 || (bytes > cs * 16384 && 2 * static_cast<int64_t>(cs) * p.R <= 2 * sms))) cs *= 2;
   p.slice = ((p.V + cs - 1) / cs + 7) & ~7;
   const size_t dyn = std::max(static_cast<size_t>(p.slice) * kElt + 32, sizeof(uint64_t) * kGather + sizeof(uint32_t) * 3 * kSteps);  // (the first CTA's room too)
   if (p.left != nullptr) {

@@ -18,6 +18,11 @@
 // of the lanes, and each copy takes the exponentials of its half (quarter) of the slots; P is 0 elsewhere.  The copies' (O,
 // m, sums) are added at the end of a segment, like those of the two groups.
 //
+// Pairs of heads.  With 64 dimensions a slot of one head is 128 bytes, and the next lies kv_heads * 128 bytes on: too short
+// a piece for memory's pace (4.5 of 6.8 TB/s measured).  So two neighbouring heads make one tile of 128 dimensions: Q's rows
+// of the first in the lower half of the (copy's) rows and the lower 64 dimensions, those of the second in the upper ones,
+// zeros elsewhere; of O each row's own 64 columns count.  The products do the work of 128 dimensions on as many bytes.
+//
 // Roles in a CTA: warps 0 and 11 copy K and V page by page through a ring of stages (TMA; one warp alone needs 1.1 us a
 // tile for it); one thread of warp 1 issues the products; warp 10 brings each segment's description, parents and Q; two groups of four warps take the tiles in turn (a
 // thread has a row), each with its own S and O, so one group's exponentials run beside the other's products.
@@ -73,6 +78,8 @@ struct AttendParams {
   float* parts;       // [2 grid] partial results
   int64_t n_rows;
   int32_t width, B, Nmax, pages, shift, q_heads, kv_heads, group, window, sinks;
+  int32_t units;       // key/value heads, or pairs of them
+  int32_t half_rows;   // rows of a copy that one head takes
   int32_t tile_nodes;  // nodes of a row tile
   uint32_t over_group; // ceil(2^16 / group)
   int32_t stages;
@@ -330,12 +337,14 @@ struct Ring {
   }
 };
 
-template <int D, int kCopies>
+template <int D, bool kPair, int kCopies>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const AttendParams a, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map) {
-  using Col = Columns<D>;
-  constexpr int kHalves = D / 64;
+  constexpr int W = kPair ? 2 * D : D;  // dimensions of a tile
+  using Col = Columns<W>;
+  constexpr int kHalves = W / 64;
+  constexpr int kHalfRows = kTile / kCopies / (kPair ? 2 : 1);
   constexpr int kStageBytes = kHalves * kHalfBytes;
   extern __shared__ unsigned char dyn[];
   __shared__ Smem sm;
@@ -367,6 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
+  if constexpr (kPair) {  // the other head's dimensions: never written again
+    for (int i = tid; i < kHalves * kHalfBytes / 16; i += kThreads) reinterpret_cast<uint4*>(q_buf)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
   if (warp == kWarpMma) tmem_alloc(&sm.tmem);
   pdl_wait();
   pdl_trigger();
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Request r = request_of(a, i);
       if (r.bad != 0 && blockIdx.x == 0) mark_bad(a, i, r.bad);
       before[i] = sum;
-      sum += static_cast<uint32_t>(r.tiles) * r.mtiles * a.kv_heads;
+      sum += static_cast<uint32_t>(r.tiles) * r.mtiles * a.units;
     }
     uint32_t x = sum;
 #pragma unroll
@@ -459,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (wanted) {
 #pragma unroll
           for (int h = 0; h < kHalves; ++h)
-            tma_load_4d(ring + at.stage * kStageBytes + h * kHalfBytes + (lane << box_shift) * 128, map, h * 64, s.head,
+            tma_load_4d(ring + at.stage * kStageBytes + h * kHalfBytes + (lane << box_shift) * 128, map, kPair ? 0 : h * 64,
+                        kPair ? 2 * s.head + h : s.head,
                         slot & ((1 << a.shift) - 1), page, &sm.full[at.stage]);
         }
         loaded += 2;
@@ -493,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int copy = 0; copy < kCopies; ++copy)
 #pragma unroll
           for (int h = 0; h < kHalves; ++h)
-            tma_load_3d(q_buf + h * kHalfBytes + copy * rows_apart * 128, &q_map, h * 64, s.head * a.group,
+            tma_load_3d(q_buf + h * kHalfBytes + (copy * rows_apart + (kPair ? h * kHalfRows : 0)) * 128, &q_map,
+                        kPair ? 0 : h * 64, (kPair ? 2 * s.head + h : s.head) * a.group,
                         static_cast<int>(s.r.first) + s.mtile * a.tile_nodes, &sm.q_full[b]);
       }
       t += s.kv1 - s.kv0;
@@ -505,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (t0 < t1) {
       const bool elected = elect_one();
       auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
-      constexpr uint32_t kDescS = instr_desc(kTile, false), kDescO = instr_desc(D, true);
+      constexpr uint32_t kDescS = instr_desc(kTile, false), kDescO = instr_desc(W, true);
       const uint32_t count = t1 - t0;
       // descriptors by addition: their low words count 16-byte units of shared memory
       const uint64_t q_desc0 = smem_desc(smem_u32(q_buf), 16, 1024), k_desc0 = smem_desc(smem_u32(ring), 16, 1024),
@@ -585,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     constexpr int rows_apart = kTile / kCopies;
     const int row_in = r & (rows_apart - 1), copy = r / rows_apart;
+    const int half = kPair ? row_in / kHalfRows : 0, local = row_in & (kHalfRows - 1);  // its head of the pair, its row there
     constexpr int kWide = kCopies == 4 ? 32 : 64;           // slots whose scores are in registers at once
     constexpr int kSteps = kTile / kCopies / kWide;          // of a copy's slots: 2 with one copy, else 1
     const int slot0 = copy * (kTile / kCopies);              // first slot of a tile that this thread's copy takes
@@ -601,8 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* tree = parents + b * a.Nmax;
       auto parent_of = [&](int node) { return a.parent != nullptr ? tree[node] : node - 1; };
       const int rows = min(a.tile_nodes, s.r.nodes - s.mtile * a.tile_nodes) * a.group;
-      const bool active = (((warp & 3) * 32) & (rows_apart - 1)) < rows;  // some row of this warp exists
-      const int node = s.mtile * a.tile_nodes + (row_in < rows ? over_group(row_in, a.over_group) : 0);
+      const bool active = (((warp & 3) * 32) & (kHalfRows - 1)) < rows;  // some row of this warp exists
+      const bool exists = local < rows;
+      const int local_node = exists ? over_group(local, a.over_group) : 0, node = s.mtile * a.tile_nodes + local_node;
       const int len = s.r.len, end = len + s.r.nodes;
       const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0;  // before it (and past the sinks) no node sees a slot
       int depth = 0;
@@ -632,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = s0 + r;
           if (slot >= end || (slot < lo && slot >= a.sinks)) {
 #pragma unroll 4
-            for (int x = 0; x < D / 8; ++x)
+            for (int x = 0; x < W / 8; ++x)
               *reinterpret_cast<uint4*>(ring + st * kStageBytes + (x >> 3) * kHalfBytes + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -652,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int w = 0; w < kWide / 32; ++w)
                 see[w] = range_bits(near, len, s0 + col + 32 * w) | (a.window > 0 ? range_bits(0, min(a.sinks, len), s0 + col + 32 * w) : 0u);
-              if (s0 + col + kWide > len && row_in < rows) {
+              if (s0 + col + kWide > len && exists) {
                 int d = depth;
                 for (int up = node;; --d) {
                   const int bit = len + up - s0 - col;
@@ -701,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (left = !warp_wait(&sm.pv_done[group], ((n - 2) >> 1) & 1, &sm.dead, a.status); left) break;
               tc_after_sync();
 #pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
+              for (int i = 0; i < W; i += 16) {
                 uint32_t o[16];
                 tmem_load16(o_addr + i, o);
                 tmem_loaded(o);
@@ -791,23 +808,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a group without a tile in the segment has m = -inf: its O is not used, whatever it holds)
       const float w0 = sm.m[b][0][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][0][r] - top) * inv;
       const float w1 = sm.m[b][1][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][1][r] - top) * inv;
-      const int head = s.head * a.group;
+      const int head = ((kPair ? 2 * s.head + half : s.head) - local_node) * a.group + local;  // (of an existing row)
       float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (s.kv0 == 0)) * part_floats<D>();
       // four columns of this thread's row: to the output, or to this CTA's partial result
       __nv_bfloat16* out_row = a.out + (s.r.first + node) * a.out_row_stride +
-                               (head + row_in - over_group(row_in, a.over_group) * a.group) * a.out_head_stride;
-      float* part_row = part + row_in * 4;
+                               head * a.out_head_stride - (kPair ? half * D : 0);
+      float* part_row = part + row_in * 4 - (kPair ? half * D * kTile : 0);
       auto emit4 = [&](int column, float4 v) {
         if (complete) *reinterpret_cast<uint2*>(out_row + column) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         else *reinterpret_cast<float4*>(part_row + column * kTile) = v;
       };
-      if (group == 0 && copy == 0 && row_in < rows) {
+      if (group == 0 && copy == 0 && exists) {
         if (!complete) {
           part[kTile * D + row_in] = top;
           part[kTile * D + kTile + row_in] = sum;
           part[kTile * D + 2 * kTile + row_in] = sumr;
         } else if (a.lse != nullptr) {
-          a.lse[(s.r.first + node) * a.q_heads + head + row_in - over_group(row_in, a.over_group) * a.group] = (top + log2f(sum)) * 0.693147180559945309f;
+          a.lse[(s.r.first + node) * a.q_heads + head] = (top + log2f(sum)) * 0.693147180559945309f;
         }
       }
       if (tid == 64 && s.kv0 == 0 && !complete) {
@@ -833,14 +850,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 16; ++e)
           f[e] = (w0 != 0.0f ? w0 * __uint_as_float(x[e]) : 0.0f) + (w1 != 0.0f ? w1 * __uint_as_float(y[e]) : 0.0f);
       };
-      const int col0 = group * (D / 2), col1 = col0 + D / 2;
+      // (of a pair each group writes one head's)
+      const int col0 = group * (W / 2), col1 = col0 + W / 2;
+      const bool writes = exists && (!kPair || half == group);
       if constexpr (kCopies == 1) {
         if (active) {
 #pragma unroll 1
           for (int i = col0; i < col1; i += 16) {
             float f[16];
             read_o(i, f);
-            if (row_in < rows) {
+            if (writes) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) emit4(i + 4 * q, make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]));
             }
@@ -851,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // each adds and writes out every kCopies-th four columns.  (Loops, not unrolled: this code runs once a segment
         // and comes from behind the instruction cache.)
         const int kept_rows = (rows + 7) & ~7, all_rows = kCopies * kept_rows;
-        const int round = min(D / 2, (4 * kGroupThreads / all_rows * 4) & ~15);
+        const int round = min(W / 2, (4 * kGroupThreads / all_rows * 4) & ~15);
 #pragma unroll 1
         for (int i0 = col0; i0 < col1; i0 += round) {
           const int i1 = min(i0 + round, col1);
@@ -859,8 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = i0; i < i1 && active; i += 16) {
             float f[16];
             read_o(i, f);
-            float4* to = mix + ((i - i0) >> 2) * all_rows + copy * kept_rows + row_in;
-            if (row_in < rows) {
+            float4* to = mix + ((i - i0) >> 2) * all_rows + copy * kept_rows + local;
+            if (writes) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) to[q * all_rows] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
             }
@@ -868,10 +887,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sm.mix_full[group]);
           if (left = !warp_wait(&sm.mix_full[group], mixes & 1, &sm.dead, a.status); left) break;
           ++mixes;
-          if (row_in < rows) {
+          if (writes) {
 #pragma unroll 1
             for (int i = i0 + 4 * copy; i < i1; i += 4 * kCopies) {
-              const float4* from = mix + ((i - i0) >> 2) * all_rows + row_in;
+              const float4* from = mix + ((i - i0) >> 2) * all_rows + local;
               float4 v = from[0];
 #pragma unroll
               for (int o = 1; o < kCopies; ++o) {
@@ -918,13 +937,17 @@ template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const AttendParams a) {
   pdl_wait();
   const Job job = a.jobs[blockIdx.x];
-  const int row0 = blockIdx.y * kJoinRows;
-  if (job.valid != 0 && row0 < job.rows && !a.bad[job.request]) {
+  const int row0 = blockIdx.y * kJoinRows, heads = a.kv_heads / a.units;
+  if (job.valid != 0 && row0 < heads * job.rows && !a.bad[job.request]) {
     constexpr int kPieces = D / 4;
     const int n = job.last - job.first + 1;
     for (int x = threadIdx.x; x < kJoinRows * kPieces; x += 128) {
-      const int r = row0 + x % kJoinRows, piece = x / kJoinRows;
-      if (r >= job.rows) continue;
+      const int piece = x / kJoinRows;
+      int local = row0 + x % kJoinRows;
+      if (local >= heads * job.rows) continue;
+      const int half = local >= job.rows;
+      local -= half * job.rows;
+      const int r = half * a.half_rows + local;
       float M = -INFINITY, L = 0.0f, R = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int i = 0; i < n; ++i) {
         const float* part = a.parts + static_cast<int64_t>(2 * (job.first + i) + (i == 0)) * part_floats<D>();
@@ -943,7 +966,7 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendParams a) {
         o[3] += w * v.w;
       }
       const float inv = R > 0.0f ? 1.0f / R : 0.0f;
-      const int node = job.mtile * a.tile_nodes + r / a.group, head = job.head * a.group + r % a.group;
+      const int node = job.mtile * a.tile_nodes + local / a.group, head = (heads * job.head + half) * a.group + local % a.group;
       const int64_t row = a.node_offsets[job.request] + node;
       uint2 w;
       w.x = pack_bf16(o[0] * inv, o[1] * inv);
@@ -1041,20 +1064,20 @@ bool encode_queries(CUtensorMap* map, const void* q, int64_t row_stride, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kCopies>
+template <int D, bool kPair, int kCopies>
 cudaError_t launch_attention(AttendParams& a, const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
                              int ctas, void* stream) {
   // the ring gets what Q, the tables and the fixed part leave of the shared memory: at least 4 stages
-  constexpr int kStageBytes = D / 64 * kHalfBytes;
+  constexpr int kStageBytes = (kPair ? 2 : 1) * D / 64 * kHalfBytes;
   const int fixed = 4 * (a.B + 2 * a.Nmax) + 1024 + kStageBytes;
   const int room = kSmemMax - static_cast<int>(sizeof(Smem)) - 64 - fixed;
   a.stages = std::min(kMaxStages, room / kStageBytes);
   const size_t dyn = static_cast<size_t>(fixed) + static_cast<size_t>(a.stages) * kStageBytes;
-  cudaError_t e = allow_smem<attend_kernel<D, kCopies>>(kSmemMax - sizeof(Smem) - 64);
+  cudaError_t e = allow_smem<attend_kernel<D, kPair, kCopies>>(kSmemMax - sizeof(Smem) - 64);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attend_kernel<D, kCopies>, dim3(ctas), kThreads, dyn, stream, SV_KERNEL_ATTENTION, 1, a, q_map, k_map, v_map);
+  e = launch_dependent(attend_kernel<D, kPair, kCopies>, dim3(ctas), kThreads, dyn, stream, SV_KERNEL_ATTENTION, 1, a, q_map, k_map, v_map);
   if (e != cudaSuccess) return e;
-  const int groups = (a.tile_nodes * a.group + kJoinRows - 1) / kJoinRows;
+  const int groups = ((kPair ? 2 : 1) * a.tile_nodes * a.group + kJoinRows - 1) / kJoinRows;
   return launch_dependent(join_kernel<D>, dim3(ctas, groups), 128, 0, stream, SV_KERNEL_ATTENTION_JOIN, 1, a);
 }
 
@@ -1092,7 +1115,10 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
       q_head_stride < c->head_dim || out_head_stride < c->head_dim || q_row_stride < 0 || out_row_stride < 0)
     return set_error(SV_ERR_INVALID_ARG, "q / out: 16-byte aligned rows of head_dim elements are needed");
   if ((s = check_workspace(ws, ws_bytes, sv_attention_workspace_size(c, q_heads))) != SV_OK) return s;
-  const int group = q_heads / c->kv_heads, tile_nodes = std::min(kTile / group, Nmax);
+  // two heads at a time where they lie side by side and all nodes' rows of both fit into a tile
+  const int group = q_heads / c->kv_heads;
+  const bool pair = c->head_dim == 64 && c->head_stride == 64 && c->kv_heads % 2 == 0 && 2 * Nmax * group <= kTile;
+  const int tile_nodes = std::min(kTile / group, Nmax);
   // the line of work is counted in 32 bits
   const int64_t tiles = ((static_cast<int64_t>(table_width) * c->page_size + kTile - 1) / kTile + 1) *
                         ((Nmax + tile_nodes - 1) / tile_nodes);
@@ -1134,19 +1160,24 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   while ((1 << a.shift) < c->page_size) ++a.shift;
   a.q_heads = q_heads;
   a.kv_heads = c->kv_heads;
+  a.units = pair ? c->kv_heads / 2 : c->kv_heads;
   a.group = group;
   a.tile_nodes = tile_nodes;
   a.over_group = (65536 + group - 1) / group;
   a.window = window;
   a.sinks = sinks;
   a.scale = scale;
-  const int tile_rows = tile_nodes * group;
-  const auto launch = c->head_dim == 128 ? (tile_rows <= 32   ? launch_attention<128, 4>
-                                            : tile_rows <= 64 ? launch_attention<128, 2>
-                                                              : launch_attention<128, 1>)
-                                         : (tile_rows <= 32   ? launch_attention<64, 4>
-                                            : tile_rows <= 64 ? launch_attention<64, 2>
-                                                              : launch_attention<64, 1>);
+  const int tile_rows = tile_nodes * group * (pair ? 2 : 1), copies = tile_rows <= 32 ? 4 : tile_rows <= 64 ? 2 : 1;
+  a.half_rows = kTile / copies / (pair ? 2 : 1);
+  const auto launch = pair                 ? (copies == 4   ? launch_attention<64, true, 4>
+                                              : copies == 2 ? launch_attention<64, true, 2>
+                                                            : launch_attention<64, true, 1>)
+                      : c->head_dim == 128 ? (copies == 4   ? launch_attention<128, false, 4>
+                                              : copies == 2 ? launch_attention<128, false, 2>
+                                                            : launch_attention<128, false, 1>)
+                                           : (copies == 4   ? launch_attention<64, false, 4>
+                                              : copies == 2 ? launch_attention<64, false, 2>
+                                                            : launch_attention<64, false, 1>);
   return launch_status(launch(a, q_map, k_map, v_map, ctas, stream), "attention");
 }
 

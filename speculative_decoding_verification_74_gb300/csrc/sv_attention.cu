@@ -9,9 +9,10 @@
 // and at the end o = O / (sum of the rounded P), lse = (m + log2 sum P) ln 2.  O is scaled by 2^(m - m') only when some
 // row's maximum has grown by more than 8 (P stays below 2^8, so float32 sums and bf16's range are far from their ends).
 //
-// Work split.  All (row tile, cache tile) pairs of the batch lie on one line; CTA c of C takes the c-th part of
-// it (a persistent CTA per SM), in segments: stretches of one row tile.  A row tile that crosses CTAs leaves partial (O, m,
-// sums) in the workspace, and join_kernel adds them.  So one long context and many short ones load the SMs alike.
+// Work split.  All (row tile, cache tile) pairs of the batch lie on one line, and before each row tile a few places for what
+// beginning and ending it costs; CTA c of C takes the c-th part of the line (a persistent CTA per SM), in segments:
+// stretches of one row tile.  A row tile that crosses CTAs leaves partial (O, m, sums) in the workspace, and join_kernel
+// adds them.  So one long context and many short ones load the SMs alike.
 //
 // Few rows.  A row of S belongs to one lane of tensor memory, and a quarter of its lanes to one of the SM's four
 // schedulers.  So a tile of at most 64 (32) rows is multiplied with Q's rows two (four) times over, one copy per half (quarter)
@@ -58,6 +59,9 @@ struct Columns {
 };
 constexpr float kLazyGrowth = 8.0f;        // log2 units by which a maximum may grow without a rescale of O
 constexpr int kJoinRows = 16;              // rows per CTA of the join
+// What a row tile costs besides its cache tiles, in those: its masked tiles and its end (2.5 us with few rows, 5 with many,
+// against 1.5 a tile; 64 trees 142 us at 0, 134 at 1, 127 at 2, 123 at 3, 121 at 4 and 5).
+constexpr int kExtra = 4, kExtraFewRows = 3;
 constexpr int kMaxStages = 12;
 constexpr int kMaxCtas = 152;              // SMs of the GPU: one CTA each
 constexpr int kSmemMax = 232448;           // shared memory that a CTA can have
@@ -80,6 +84,7 @@ struct AttendParams {
   int32_t width, B, Nmax, pages, shift, q_heads, kv_heads, group, window, sinks;
   int32_t units;       // key/value heads, or pairs of them
   int32_t half_rows;   // rows of a copy that one head takes
+  int32_t extra;       // places before a row tile's cache tiles
   int32_t tile_nodes;  // nodes of a row tile
   uint32_t over_group; // ceil(2^16 / group)
   int32_t stages;
@@ -236,6 +241,7 @@ __device__ __noinline__ Request request_of(const AttendParams& a, int i) {
 struct Segment {
   Request r;
   int32_t request, head, mtile, kv0, kv1;
+  uint32_t begin, next;  // places of the line: the row tile's first, and the one after this stretch
 };
 __device__ __noinline__ Segment segment_at(const AttendParams& a, const uint32_t* before, uint32_t t, uint32_t end) {
   int lo = 0, hi = a.B;  // the last request whose tiles begin at or before t
@@ -246,9 +252,12 @@ __device__ __noinline__ Segment segment_at(const AttendParams& a, const uint32_t
   Segment s;
   s.request = lo;
   s.r = request_of(a, lo);
-  const uint32_t local = t - before[lo], unit = local / static_cast<uint32_t>(s.r.tiles);
-  s.kv0 = static_cast<int>(local - unit * s.r.tiles);
-  s.kv1 = static_cast<int>(min(static_cast<uint32_t>(s.r.tiles), s.kv0 + (end - t)));
+  const uint32_t places = s.r.tiles + a.extra, local = t - before[lo], unit = local / places, at = local - unit * places;
+  const uint32_t to = min(places, at + (end - t));
+  s.begin = t - at;
+  s.next = s.begin + to;
+  s.kv0 = max(static_cast<int>(at) - a.extra, 0);
+  s.kv1 = max(static_cast<int>(to) - a.extra, 0);  // (kv0: the part ends among the places before the tiles)
   s.head = static_cast<int>(unit / s.r.mtiles);   // a head's row tiles are neighbours: they share its tiles in L2
   s.mtile = static_cast<int>(unit - static_cast<uint32_t>(s.head) * s.r.mtiles);
   return s;
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Request r = request_of(a, i);
       if (r.bad != 0 && blockIdx.x == 0) mark_bad(a, i, r.bad);
       before[i] = sum;
-      sum += static_cast<uint32_t>(r.tiles) * r.mtiles * a.units;
+      sum += static_cast<uint32_t>(r.tiles + a.extra) * r.mtiles * a.units;
     }
     uint32_t x = sum;
 #pragma unroll
@@ -415,10 +424,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const uint32_t tmem = sm.tmem;
-  // every part holds a tile: with fewer tiles than CTAs the last CTAs have none
+  // with fewer places than CTAs the last CTAs have none
   const uint32_t parts = min(gridDim.x, total);
   const uint32_t t0 = blockIdx.x < parts ? part_begin(total, blockIdx.x, parts) : total;
   const uint32_t t1 = blockIdx.x < parts ? part_begin(total, blockIdx.x + 1, parts) : total;
+  Segment opening = {};
+  if (t0 < t1) opening = segment_at(a, before, t0, t1);
+  const bool some = opening.kv0 < opening.kv1;
+  // a part's stretches but the first begin a row tile; the last may hold none of its cache tiles
+  auto stretch_at = [&](uint32_t t) { return t == t0 ? some : t + a.extra < t1; };
   const uint32_t stages = a.stages;
   uint32_t loaded = 0, segments = 0;  // stages and Q's that were asked for
 
@@ -439,14 +453,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Segment s = {}, next = {};  // the next segment and its first pages are looked up while the ring is full
     int block = 0, page_now = -1, page_next = -1, next_block = 0, next_now = -1;
-    if (t0 < t1) {
-      s = segment_at(a, before, t0, t1);
+    if (some) {
+      s = opening;
       block = tile_slot(s.r, s.kv0) >> (box_shift + 5);
       page_now = pages_of(s, block);
     }
-    for (uint32_t t = t0; t < t1 && go;) {
+    for (uint32_t t = t0; stretch_at(t) && go;) {
       const int end = s.r.len + s.r.nodes, lo = a.window > 0 ? max(0, s.r.len - a.window + 1) : 0;
-      const uint32_t after = t + (s.kv1 - s.kv0);
+      const uint32_t after = s.next;
       page_next = pages_of(s, block + 1);
       for (int j = s.kv0; j < s.kv1 && go; ++j) {
         const int s0 = tile_slot(s.r, j);
@@ -479,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         loaded += 2;
         at.step(stages);
         at.step(stages);
-        if (j == max(s.kv0, s.kv1 - 2) && after < t1) {
+        if (j == max(s.kv0, s.kv1 - 2) && stretch_at(after)) {
           next = segment_at(a, before, after, t1);
           next_block = tile_slot(next.r, next.kv0) >> (box_shift + 5);
           next_now = pages_of(next, next_block);
@@ -493,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpQ) {
     // ---- segments: description, parents, Q --------------------------------------------------------
     constexpr int rows_apart = kTile / kCopies;
-    for (uint32_t t = t0; t < t1; ++segments) {
-      const Segment s = segment_at(a, before, t, t1);
+    for (uint32_t t = t0; stretch_at(t); ++segments) {
+      const Segment s = t == t0 ? opening : segment_at(a, before, t, t1);
       const int b = segments & 1;
       if (segments >= 2 && !warp_wait(&sm.seg_free[b], ((segments >> 1) - 1) & 1, &sm.dead, a.status)) break;
       if (a.parent != nullptr)
@@ -511,17 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kPair ? 0 : h * 64, (kPair ? 2 * s.head + h : s.head) * a.group,
                         static_cast<int>(s.r.first) + s.mtile * a.tile_nodes, &sm.q_full[b]);
       }
-      t += s.kv1 - s.kv0;
+      t = s.next;
     }
   } else if (warp == kWarpMma) {
     // ---- products ---------------------------------------------------------------------------------
     // The whole warp runs the loop, so counters and descriptors stay in uniform registers, which tcgen05.mma takes its
     // operands from; one elected thread issues.
-    if (t0 < t1) {
+    if (some) {
       const bool elected = elect_one();
       auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
       constexpr uint32_t kDescS = instr_desc(kTile, false), kDescO = instr_desc(W, true);
-      const uint32_t count = t1 - t0;
+      bool more = true;                   // S's are left
       // descriptors by addition: their low words count 16-byte units of shared memory
       const uint64_t q_desc0 = smem_desc(smem_u32(q_buf), 16, 1024), k_desc0 = smem_desc(smem_u32(ring), 16, 1024),
                      v_desc0 = smem_desc(smem_u32(ring), kHalfBytes, 1024);
@@ -533,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                               // behind the other's barriers
       uint32_t idle = 0;
       uint64_t began = 0;
-      while (i < count) {
+      while (more || i < n) {
         bool issued = false;
-        if (n < count) {
+        if (more) {
           if (s_left == 0 && ready(&sm.q_full[s_seg & 1], (s_seg >> 1) & 1))
             s_left = __shfl_sync(0xFFFFFFFFu, sm.seg[s_seg & 1].kv1 - sm.seg[s_seg & 1].kv0, 0);
           // the group's S was last read by the softmax, or by the product P V, of tile n - 2
@@ -557,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ks.step(stages);
             ks.step(stages);
+            if (s_left == 0) more = stretch_at(__shfl_sync(0xFFFFFFFFu, sm.seg[s_seg & 1].next, 0));
             s_seg += s_left == 0;
             ++n;
             issued = true;
@@ -610,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale * 1.44269504088896341f;
     if (tid == 64) a.jobs[blockIdx.x].valid = 0;
     uint32_t n0 = 0, seg = 0, mixes = 0, frees = 0;  // the segment's first tile in this CTA's count
-    for (uint32_t t = t0; t < t1; ++seg) {
+    for (uint32_t t = t0; stretch_at(t); ++seg) {
       const int b = seg & 1;
       if (!warp_wait(&sm.q_full[b], (seg >> 1) & 1, &sm.dead, a.status)) break;
       const Segment& s = sm.seg[b];
@@ -829,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tid == 64 && s.kv0 == 0 && !complete) {
         // the CTA in which the row tile ends
-        const uint32_t ends = t + s.r.tiles - 1;
+        const uint32_t ends = s.begin + a.extra + s.r.tiles - 1;
         const Job job = {1, s.request, s.head, s.mtile, rows, static_cast<int32_t>(blockIdx.x), part_of(total, ends, parts), 0};
         a.jobs[blockIdx.x] = job;
       }
@@ -912,9 +927,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (left) break;
       tc_before_sync();
+      t = s.next;
       mbar_arrive(&sm.o_free);
       mbar_arrive(&sm.seg_free[b]);
-      t += tiles;
       n0 += tiles;
     }
   }
@@ -932,48 +947,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Adds the partial results of row tile `jobs[x]`: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// grid (CTAs of the attention, row groups).  Then the outputs of bad requests become 0.
+// grid (CTAs of the attention, row groups); a thread has four columns of a row.  Then the outputs of bad requests become 0.
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const AttendParams a) {
+__global__ void __launch_bounds__(kJoinRows * D / 4) join_kernel(const AttendParams a) {
+  constexpr int kJoinThreads = kJoinRows * D / 4;
   pdl_wait();
   const Job job = a.jobs[blockIdx.x];
-  const int row0 = blockIdx.y * kJoinRows, heads = a.kv_heads / a.units;
-  if (job.valid != 0 && row0 < heads * job.rows && !a.bad[job.request]) {
-    constexpr int kPieces = D / 4;
+  const int heads = a.kv_heads / a.units, piece = threadIdx.x / kJoinRows;
+  int local = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;
+  if (job.valid != 0 && local < heads * job.rows && !a.bad[job.request]) {
+    const int half = local >= job.rows;
+    local -= half * job.rows;
+    const int r = half * a.half_rows + local;
     const int n = job.last - job.first + 1;
-    for (int x = threadIdx.x; x < kJoinRows * kPieces; x += 128) {
-      const int piece = x / kJoinRows;
-      int local = row0 + x % kJoinRows;
-      if (local >= heads * job.rows) continue;
-      const int half = local >= job.rows;
-      local -= half * job.rows;
-      const int r = half * a.half_rows + local;
-      float M = -INFINITY, L = 0.0f, R = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int i = 0; i < n; ++i) {
-        const float* part = a.parts + static_cast<int64_t>(2 * (job.first + i) + (i == 0)) * part_floats<D>();
-        M = fmaxf(M, part[kTile * D + r]);
-      }
-      for (int i = 0; i < n; ++i) {
-        const float* part = a.parts + static_cast<int64_t>(2 * (job.first + i) + (i == 0)) * part_floats<D>();
-        const float m = part[kTile * D + r];
-        const float w = m == -INFINITY ? 0.0f : ex2_approx(m - M);
-        const float4 v = *reinterpret_cast<const float4*>(part + (piece * kTile + r) * 4);
-        L += w * part[kTile * D + kTile + r];
-        R += w * part[kTile * D + 2 * kTile + r];
-        o[0] += w * v.x;
-        o[1] += w * v.y;
-        o[2] += w * v.z;
-        o[3] += w * v.w;
-      }
-      const float inv = R > 0.0f ? 1.0f / R : 0.0f;
-      const int node = job.mtile * a.tile_nodes + local / a.group, head = (heads * job.head + half) * a.group + local % a.group;
-      const int64_t row = a.node_offsets[job.request] + node;
-      uint2 w;
-      w.x = pack_bf16(o[0] * inv, o[1] * inv);
-      w.y = pack_bf16(o[2] * inv, o[3] * inv);
-      *reinterpret_cast<uint2*>(a.out + row * a.out_row_stride + head * a.out_head_stride + piece * 4) = w;
-      if (piece == 0 && a.lse != nullptr) a.lse[row * a.q_heads + head] = (M + log2f(L)) * 0.693147180559945309f;
+    // part i > 0 is its CTA's first, part 0 its CTA's second
+    const float* first = a.parts + static_cast<int64_t>(2 * job.first + 1) * part_floats<D>();
+    const float* others = a.parts + static_cast<int64_t>(2 * job.first) * part_floats<D>();
+    float M = -INFINITY, L = 0.0f, R = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) M = fmaxf(M, (i == 0 ? first : others + static_cast<int64_t>(2 * i) * part_floats<D>())[kTile * D + r]);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* part = i == 0 ? first : others + static_cast<int64_t>(2 * i) * part_floats<D>();
+      const float m = part[kTile * D + r];
+      const float w = m == -INFINITY ? 0.0f : ex2_approx(m - M);
+      const float4 v = *reinterpret_cast<const float4*>(part + (piece * kTile + r) * 4);
+      L += w * part[kTile * D + kTile + r];
+      R += w * part[kTile * D + 2 * kTile + r];
+      o[0] += w * v.x;
+      o[1] += w * v.y;
+      o[2] += w * v.z;
+      o[3] += w * v.w;
     }
+    const float inv = R > 0.0f ? 1.0f / R : 0.0f;
+    const int node = job.mtile * a.tile_nodes + local / a.group, head = (heads * job.head + half) * a.group + local % a.group;
+    const int64_t row = a.node_offsets[job.request] + node;
+    uint2 w;
+    w.x = pack_bf16(o[0] * inv, o[1] * inv);
+    w.y = pack_bf16(o[2] * inv, o[3] * inv);
+    *reinterpret_cast<uint2*>(a.out + row * a.out_row_stride + head * a.out_head_stride + piece * 4) = w;
+    if (piece == 0 && a.lse != nullptr) a.lse[row * a.q_heads + head] = (M + log2f(L)) * 0.693147180559945309f;
   }
   if (*a.any_bad != 0) {
     const int blocks = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
@@ -982,11 +995,11 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendParams a) {
       const int64_t first = max(int64_t(0), static_cast<int64_t>(a.node_offsets[i]));
       const int64_t last = min(a.n_rows, static_cast<int64_t>(a.node_offsets[i + 1]));
       for (int64_t row = first; row < last; ++row) {
-        for (int x = threadIdx.x; x < a.q_heads * (D / 8); x += 128)
+        for (int x = threadIdx.x; x < a.q_heads * (D / 8); x += kJoinThreads)
           *reinterpret_cast<uint4*>(a.out + row * a.out_row_stride + (x / (D / 8)) * a.out_head_stride + (x % (D / 8)) * 8) =
               make_uint4(0, 0, 0, 0);
         if (a.lse != nullptr)
-          for (int x = threadIdx.x; x < a.q_heads; x += 128) a.lse[row * a.q_heads + x] = -INFINITY;
+          for (int x = threadIdx.x; x < a.q_heads; x += kJoinThreads) a.lse[row * a.q_heads + x] = -INFINITY;
       }
     }
     // the last CTA clears the marks for the next call
@@ -998,7 +1011,7 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendParams a) {
     }
     __syncthreads();
     if (last_one) {
-      for (int i = threadIdx.x; i < a.B; i += 128) a.bad[i] = 0;
+      for (int i = threadIdx.x; i < a.B; i += kJoinThreads) a.bad[i] = 0;
       if (threadIdx.x == 0) {
         a.any_bad[0] = 0;
         a.any_bad[1] = 0;
@@ -1078,7 +1091,7 @@ cudaError_t launch_attention(AttendParams& a, const CUtensorMap& q_map, const CU
   e = launch_dependent(attend_kernel<D, kPair, kCopies>, dim3(ctas), kThreads, dyn, stream, SV_KERNEL_ATTENTION, 1, a, q_map, k_map, v_map);
   if (e != cudaSuccess) return e;
   const int groups = ((kPair ? 2 : 1) * a.tile_nodes * a.group + kJoinRows - 1) / kJoinRows;
-  return launch_dependent(join_kernel<D>, dim3(ctas, groups), 128, 0, stream, SV_KERNEL_ATTENTION_JOIN, 1, a);
+  return launch_dependent(join_kernel<D>, dim3(ctas, groups), kJoinRows * D / 4, 0, stream, SV_KERNEL_ATTENTION_JOIN, 1, a);
 }
 
 }  // namespace
@@ -1120,7 +1133,7 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   const bool pair = c->head_dim == 64 && c->head_stride == 64 && c->kv_heads % 2 == 0 && 2 * Nmax * group <= kTile;
   const int tile_nodes = std::min(kTile / group, Nmax);
   // the line of work is counted in 32 bits
-  const int64_t tiles = ((static_cast<int64_t>(table_width) * c->page_size + kTile - 1) / kTile + 1) *
+  const int64_t tiles = ((static_cast<int64_t>(table_width) * c->page_size + kTile - 1) / kTile + 1 + kExtra) *
                         ((Nmax + tile_nodes - 1) / tile_nodes);
   if (tiles > INT_MAX || tiles * c->kv_heads > INT_MAX || tiles * c->kv_heads * B > INT_MAX)
     return set_error(SV_ERR_INVALID_ARG, "B=%d requests of up to %lld tiles a head are too many for one call", B, (long long)tiles);
@@ -1169,6 +1182,7 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   a.scale = scale;
   const int tile_rows = tile_nodes * group * (pair ? 2 : 1), copies = tile_rows <= 32 ? 4 : tile_rows <= 64 ? 2 : 1;
   a.half_rows = kTile / copies / (pair ? 2 : 1);
+  a.extra = tile_rows <= 16 ? kExtraFewRows : kExtra;
   const auto launch = pair                 ? (copies == 4   ? launch_attention<64, true, 4>
                                               : copies == 2 ? launch_attention<64, true, 2>
                                                             : launch_attention<64, true, 1>)

@@ -593,9 +593,15 @@ __device__ __forceinline__ uint32_t read_ask(const SampleParams& p, int64_t row,
   ask.p24 = static_cast<uint32_t>(rintf(p_in * 16777216.0f));
   return bad;
 }
-// Rows for maxima_kernel and select_kernel: their prefix's end follows from few logits.
+// Rows for maxima_kernel and select_kernel: their prefix's end follows from few logits (and W, which top-p alone needs).
 __device__ __forceinline__ bool by_maxima(const Ask& ask, uint32_t bad) {
-  return bad == 0 && (ask.by_count ? ask.k <= kGatherK : ask.floor_on && !ask.nucleus);
+  return bad == 0 && (ask.by_count ? ask.k <= kGatherK : ask.floor_on);
+}
+// Top-p alone: V weights below this logit (and half a unit of rounding each) stay below (1 - p) W; 1e-3 covers ex2 and
+// log2.
+__device__ __forceinline__ float nucleus_bound(const Ask& ask, int V) {
+  const float each = static_cast<float>(ask.total) * (static_cast<float>((1u << 24) - ask.p24) * 0x1p-24f) / static_cast<float>(V) - 0.5f;
+  return each > 0.0f ? __fadd_rd(ask.top, __fdiv_rd(log2f(each) - 40.0f - 1e-3f, ask.steep)) : -INFINITY;
 }
 
 __device__ __forceinline__ Scale scale_of(const Ask& ask) {
@@ -1319,9 +1325,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
     if (sh.bound != 0) bound = logit_of_key(sh.bound);
   } else if (ask.nucleus) {
     ask.total = cluster_total(sh, weights_above<DT>(s, -INFINITY, top, ask.steep));
-    // V weights of at most this (and half a unit of rounding each) stay below (1 - p) W; 1e-3 covers ex2 and log2
-    const float each = static_cast<float>(ask.total) * (static_cast<float>((1u << 24) - ask.p24) * 0x1p-24f) / static_cast<float>(p.V) - 0.5f;
-    if (each > 0.0f) bound = __fadd_rd(top, __fdiv_rd(log2f(each) - 40.0f - 1e-3f, ask.steep));
+    bound = nucleus_bound(ask, p.V);
   }
   // Below min-p's threshold nothing is kept.  The boundary may then lie below the bound: it is not found, and everything
   // above the bound is kept.  Only the top-k's own weight needs all of the top-k.
@@ -1582,6 +1586,21 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
     find_step<false>(sh, sh.count[tid], 0, ask.k, 0, 0);
     if (sh.step != 0xFFFFFFFFu)
       bound = scale.inv > 0.0f ? __fsub_rd(top, __fmul_ru(static_cast<float>(sh.step + 1) / scale.inv, 1.00001f)) : top;
+  }
+  if (ask.nucleus && !ask.by_count) {  // W, over the whole row (its second reading)
+    WeightSum sum(top, ask.steep);
+    uint32_t adds = 0;
+#pragma unroll 4
+    for (int v = tid; v < vecs; v += kThreads, ++adds) {
+      const Vec<DT> x(row_vec<DT>(x_row, phase, p.V, v));
+#pragma unroll
+      for (int e = 0; e < kElems; e += 2) sum.add(x.x[e], x.x[e + 1]);
+    }
+    const uint64_t w = warp_sum(sum.total(adds * (kElems / 2)));
+    if (lane == 0) sh.seg[warp] = w;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) ask.total += sh.seg[i];
+    bound = nucleus_bound(ask, p.V);
   }
   if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(ask.least * 1.000001f, ask.steep)));
   if (!(bound < top)) bound = bound >= top ? top : -INFINITY;

@@ -208,6 +208,15 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
   return v;
 }
+// The cluster's sum of one value per CTA, by every warp for itself: a lane per CTA (reads of peers one after the other take
+// 0.25 us each).
+__device__ __forceinline__ uint64_t peers_sum(const uint64_t* value) {
+  const uint32_t r = threadIdx.x % kMaxCluster;
+  uint64_t v = r < cluster_size() ? peer_u64(value, r) : 0;
+#pragma unroll
+  for (int d = kMaxCluster / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
 
 // One slice of a row in shared memory: 16-byte vectors, the first `phase` elements and those past
 // the slice padded with -inf.  A warp owns a contiguous run of vectors.
@@ -303,16 +312,18 @@ __device__ uint64_t block_scan(Shared& sh, uint64_t v) {
 // The cluster's count and weight of one histogram step.
 __device__ __noinline__ void merged_step(const Shared& sh, int step, bool weights, uint32_t* c, uint64_t* w) {
   const uint32_t cs = cluster_size();
-  uint32_t n = 0;
+  uint32_t n = 0, part[kMaxCluster];
   uint64_t l0 = 0, l1 = 0, l2 = 0;
-  for (uint32_t r = 0; r < cs; ++r) {
-    n += peer_u32(&sh.count[step], r);
-    if (weights) {
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) part[r] = r < cs ? peer_u32(&sh.count[step], r) : 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) n += part[r];
+  if (weights)
+    for (uint32_t r = 0; r < cs; ++r) {
       l0 += peer_u32(&sh.limb[0][step], r);
       l1 += peer_u32(&sh.limb[1][step], r);
       l2 += peer_u32(&sh.limb[2][step], r);
     }
-  }
   *c = n;
   *w = limbs_of(l0, l1, l2);
 }
@@ -483,10 +494,14 @@ __device__ __noinline__ Boundary rank_step(const Slice<DT>& s, Shared& sh, float
     for (int e = 0; e < Vec<DT>::kElems; ++e) exchange(x.x[e]);
   }
   cluster_sync();
-  if (tid <= static_cast<int>(cs)) {
-    uint32_t n = 0;
-    for (int r = 0; r < tid; ++r) n += peer_u32(&sh.mine_n, r);
-    sh.from[tid] = n;
+  if (tid < 32) {
+    uint32_t n = tid > 0 && tid <= static_cast<int>(cs) ? peer_u32(&sh.mine_n, tid - 1) : 0;
+#pragma unroll
+    for (int d = 1; d <= kMaxCluster; d <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, n, d);
+      if (tid >= d) n += u;
+    }
+    if (tid <= kMaxCluster) sh.from[tid] = n;  // (the same from cs on)
   }
   __syncthreads();
   const int n = static_cast<int>(sh.from[cs]);
@@ -554,9 +569,7 @@ __device__ __noinline__ uint64_t cluster_total(Shared& sh, uint64_t v) {
     sh.z = z;
   }
   cluster_sync();
-  uint64_t total = 0;
-  for (uint32_t r = 0; r < cluster_size(); ++r) total += peer_u64(&sh.z, r);
-  return total;
+  return peers_sum(&sh.z);
 }
 
 // What a row asks for, the same in every CTA of its cluster.
@@ -874,11 +887,13 @@ __device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const A
     sh.z = z;
   }
   cluster_sync();
-  uint64_t before = 0, z = 0;
-  for (uint32_t r = 0; r < cs; ++r) {
-    const uint64_t zr = peer_u64(&sh.z, r);
-    if (r < rank) before += zr;
-    z += zr;
+  const uint32_t peer = lane % kMaxCluster;
+  const uint64_t zr = peer < cs ? peer_u64(&sh.z, peer) : 0;
+  uint64_t z = zr, before = peer < rank ? zr : 0;
+#pragma unroll
+  for (int d = kMaxCluster / 2; d > 0; d >>= 1) {
+    z += __shfl_xor_sync(0xFFFFFFFFu, z, d);
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
   }
   for (int i = 0; i < warp; ++i) before += sh.seg[i];
   for (int j = 0; j < p.M; ++j) {
@@ -972,11 +987,10 @@ __device__ __noinline__ int weights_around(const Slice<DT>& s, Shared& sh, const
     sh.all_w[4 * kWarps + tid] = t;
   }
   cluster_sync();
+  static_assert(4 * kMaxCluster == 32, "a lane per CTA and value");
+  uint64_t sums = peers_sum(&sh.all_w[4 * kWarps + lane / kMaxCluster]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    out[i] = 0;
-    for (uint32_t r = 0; r < cluster_size(); ++r) out[i] += peer_u64(&sh.all_w[4 * kWarps + i], r);
-  }
+  for (int i = 0; i < 4; ++i) out[i] = __shfl_sync(0xFFFFFFFFu, sums, i * kMaxCluster);
   cluster_sync();  // the peers have read them
   return n <= kListPerWarp ? n : -1;
 }

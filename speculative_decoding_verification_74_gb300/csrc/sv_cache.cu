@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kPageThreads) fork_kernel(Pool p, int32_t* tab
     for (int j = kPerThread - 1; j >= 0; --j)
       if (split[j]) {
         --r;
-        pair_of[r] = ok[j] ? threadIdx.x * kPerThread + j : -1;
+        pair_of[r] = ok[j] ? static_cast<int>(threadIdx.x) * kPerThread + j : -1;
       }
   }
   __syncthreads();
@@ -487,7 +487,10 @@ struct CopyParams {
   const int32_t* done;  // [n] pairs that were forked
 };
 
-// grid (pieces of [layer][k, v][slot][piece], pairs): the used slots of each forked pair's last page.
+// grid (pieces of [layer][k, v][slot][piece], pairs): the used slots of each forked pair's last page.  I: an unsigned type
+// that counts a pair's pieces (64-bit divisions per piece cost more than its copy).
+constexpr int kInFlight = 4;
+template <typename I>
 __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(CopyParams a) {
   pdl_wait();
   const int j = blockIdx.y;
@@ -498,16 +501,24 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(CopyParams a) {
   const int32_t from = a.table[static_cast<int64_t>(from_row) * a.width + e0];
   const int32_t to = a.table[static_cast<int64_t>(to_row) * a.width + e0];
   if (from < 0 || from >= a.r.pages || to < 0 || to >= a.r.pages) return;
-  const int per_side = part * a.r.pieces;
-  const int64_t items = static_cast<int64_t>(a.layers) * 2 * per_side;
-#pragma unroll 4
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; x < items;
-       x += static_cast<int64_t>(gridDim.x) * kRowThreads) {
-    const int side = static_cast<int>(x / per_side);
-    const int y = static_cast<int>(x - static_cast<int64_t>(side) * per_side);
-    const int slot = y / a.r.pieces, e = y - slot * a.r.pieces;
-    __nv_bfloat16* base = ((side & 1) ? a.v : a.k) + (side >> 1) * a.r.layer_stride + slot * a.r.slot_stride + piece_offset(a.r, e);
-    *reinterpret_cast<int4*>(base + to * a.r.page_stride) = *reinterpret_cast<const int4*>(base + from * a.r.page_stride);
+  const I pieces = static_cast<I>(a.r.pieces), per_side = part * pieces, items = static_cast<I>(a.layers) * 2 * per_side;
+  const I step = static_cast<I>(gridDim.x) * kRowThreads;
+  for (I x0 = static_cast<I>(blockIdx.x) * kRowThreads + threadIdx.x; x0 < items; x0 += kInFlight * step) {
+    int4 w[kInFlight];
+    __nv_bfloat16* at[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const I x = x0 + u * step;
+      at[u] = nullptr;
+      if (x >= items) continue;
+      const I side = x / per_side, y = x - side * per_side, slot = y / pieces;
+      at[u] = ((side & 1) ? a.v : a.k) + static_cast<int64_t>(side >> 1) * a.r.layer_stride + static_cast<int64_t>(slot) * a.r.slot_stride +
+              piece_offset(a.r, static_cast<int>(y - slot * pieces));
+      w[u] = *reinterpret_cast<const int4*>(at[u] + from * a.r.page_stride);
+    }
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u)
+      if (at[u] != nullptr) *reinterpret_cast<int4*>(at[u] + to * a.r.page_stride) = w[u];
   }
 }
 
@@ -659,7 +670,8 @@ sv_status sv_cache_fork(const sv_cache* c, int32_t* page_table, int table_width,
   a.done = done;
   const int64_t items = static_cast<int64_t>(c->layers) * 2 * c->page_size * a.r.pieces;
   const int64_t groups = std::min<int64_t>(std::max(1, 1824 / n), (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
-  return launch_status(launch_dependent(fork_rows_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, groups)), n),
+  const auto kernel = items <= INT_MAX ? fork_rows_kernel<uint32_t> : fork_rows_kernel<uint64_t>;
+  return launch_status(launch_dependent(kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, groups)), n),
                                         kRowThreads, 0, stream, SV_KERNEL_CACHE_ROWS, 1, a),
                        "fork rows");
 }

@@ -70,9 +70,16 @@ struct alignas(16) Job {  // a row tile that several CTAs worked on: parts of CT
   int32_t valid, request, head, mtile, rows, first, last, pad;
 };
 
-struct AttendParams {
+struct Line {  // what the line of work follows from
+  const int32_t *seq_len, *node_offsets;
+  int64_t n_rows;
+  int32_t B, Nmax, width, shift, window, sinks;
+  int32_t tile_nodes;  // nodes of a row tile
+  int32_t extra;       // places before a row tile's cache tiles
+};
+struct AttendParams : Line {
   int64_t out_row_stride, out_head_stride;
-  const int32_t *table, *seq_len, *node_offsets, *parent;
+  const int32_t *table, *parent;
   __nv_bfloat16* out;
   float* lse;
   uint32_t* status;
@@ -80,12 +87,9 @@ struct AttendParams {
   uint8_t* bad;       // [SV_MAX_BATCH] requests whose outputs become 0
   Job* jobs;          // [grid]
   float* parts;       // [2 grid] partial results
-  int64_t n_rows;
-  int32_t width, B, Nmax, pages, shift, q_heads, kv_heads, group, window, sinks;
+  int32_t pages, q_heads, kv_heads, group;
   int32_t units;       // key/value heads, or pairs of them
   int32_t half_rows;   // rows of a copy that one head takes
-  int32_t extra;       // places before a row tile's cache tiles
-  int32_t tile_nodes;  // nodes of a row tile
   uint32_t over_group; // ceil(2^16 / group)
   int32_t stages;
   float scale;
@@ -210,7 +214,7 @@ struct Request {
   int32_t mtiles;      // row tiles per key/value head
   uint32_t bad;        // SV_DEV_* bits
 };
-__device__ __noinline__ Request request_of(const AttendParams& a, int i) {
+__device__ __forceinline__ Request request_of(const Line& a, int i) {
   Request r = {};
   const int64_t first = a.node_offsets[i], last = a.node_offsets[i + 1];
   const int64_t len = a.seq_len[i], nodes = last - first;
@@ -243,7 +247,8 @@ struct Segment {
   int32_t request, head, mtile, kv0, kv1;
   uint32_t begin, next;  // places of the line: the row tile's first, and the one after this stretch
 };
-__device__ __noinline__ Segment segment_at(const AttendParams& a, const uint32_t* before, uint32_t t, uint32_t end) {
+// (a: in shared memory; a kernel parameter passed by reference is read through global memory, 0.3 us a field)
+__device__ __noinline__ Segment segment_at(const Line& a, const uint32_t* before, uint32_t t, uint32_t end) {
   int lo = 0, hi = a.B;  // the last request whose tiles begin at or before t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -265,15 +270,18 @@ __device__ __noinline__ Segment segment_at(const AttendParams& a, const uint32_t
 __device__ __forceinline__ int tile_slot(const Request& r, int j) {
   return (j < r.sink_tiles ? j : r.near_tile + (j - r.sink_tiles)) * kTile;
 }
-__device__ __noinline__ uint32_t part_begin(uint32_t total, uint32_t c, uint32_t n) {
-  return static_cast<uint32_t>(static_cast<uint64_t>(total) * c / n);
-}
-// The CTA (of n) whose part of the line holds tile `at`.
-__device__ __noinline__ int part_of(uint32_t total, uint32_t at, uint32_t n) {
-  uint32_t c = static_cast<uint32_t>(static_cast<uint64_t>(at) * n / total);
-  while (part_begin(total, c + 1, n) <= at) ++c;
-  return static_cast<int>(c);
-}
+// The line in n parts as equal as can be: the first `longer` have a place more.  (32-bit arithmetic: a 64-bit division is
+// a page of code, and at a call's start code comes from behind the instruction cache.)
+struct Parts {
+  uint32_t length, longer;
+  __device__ __forceinline__ Parts(uint32_t total, uint32_t n) : length(total / n), longer(total - length * n) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * length + min(c, longer); }
+  // the part that holds place `at`
+  __device__ __forceinline__ int of(uint32_t at) const {
+    const uint32_t first = longer * (length + 1);
+    return static_cast<int>(at < first ? at / (length + 1) : longer + (at - first) / length);
+  }
+};
 // row / group for row < 128, group <= 128: over = ceil(2^16 / group).
 __device__ __forceinline__ int over_group(int row, uint32_t over) { return static_cast<int>((row * over) >> 16); }
 
@@ -287,6 +295,7 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int at) {
 // The part of shared memory with a fixed size; then come the tiles before each request [B], the parents of two segments'
 // trees [2][Nmax] and, 1024-byte aligned, Q and the ring.
 struct Smem {
+  Line line;
   Segment seg[2];              // by the segment's parity
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t q_full[2];          // by the segment's parity: its Q and description are there
@@ -382,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.sums_full, kSoftThreads);
     mbar_init(&sm.o_free, kSoftThreads);
     sm.dead = 0;
+    sm.line = a;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -425,11 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = sm.tmem;
   // with fewer places than CTAs the last CTAs have none
-  const uint32_t parts = min(gridDim.x, total);
-  const uint32_t t0 = blockIdx.x < parts ? part_begin(total, blockIdx.x, parts) : total;
-  const uint32_t t1 = blockIdx.x < parts ? part_begin(total, blockIdx.x + 1, parts) : total;
+  const Parts parts(total, max(1u, min(gridDim.x, total)));
+  const uint32_t t0 = min(parts.begin(blockIdx.x), total), t1 = min(parts.begin(blockIdx.x + 1), total);
   Segment opening = {};
-  if (t0 < t1) opening = segment_at(a, before, t0, t1);
+  if (t0 < t1) opening = segment_at(sm.line, before, t0, t1);
   const bool some = opening.kv0 < opening.kv1;
   // a part's stretches but the first begin a row tile; the last may hold none of its cache tiles
   auto stretch_at = [&](uint32_t t) { return t == t0 ? some : t + a.extra < t1; };
@@ -494,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.step(stages);
         at.step(stages);
         if (j == max(s.kv0, s.kv1 - 2) && stretch_at(after)) {
-          next = segment_at(a, before, after, t1);
+          next = segment_at(sm.line, before, after, t1);
           next_block = tile_slot(next.r, next.kv0) >> (box_shift + 5);
           next_now = pages_of(next, next_block);
         }
@@ -508,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- segments: description, parents, Q --------------------------------------------------------
     constexpr int rows_apart = kTile / kCopies;
     for (uint32_t t = t0; stretch_at(t); ++segments) {
-      const Segment s = t == t0 ? opening : segment_at(a, before, t, t1);
+      const Segment s = t == t0 ? opening : segment_at(sm.line, before, t, t1);
       const int b = segments & 1;
       if (segments >= 2 && !warp_wait(&sm.seg_free[b], ((segments >> 1) - 1) & 1, &sm.dead, a.status)) break;
       if (a.parent != nullptr)
@@ -845,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid == 64 && s.kv0 == 0 && !complete) {
         // the CTA in which the row tile ends
         const uint32_t ends = s.begin + a.extra + s.r.tiles - 1;
-        const Job job = {1, s.request, s.head, s.mtile, rows, static_cast<int32_t>(blockIdx.x), part_of(total, ends, parts), 0};
+        const Job job = {1, s.request, s.head, s.mtile, rows, static_cast<int32_t>(blockIdx.x), parts.of(ends), 0};
         a.jobs[blockIdx.x] = job;
       }
       // the last tile of each parity: its product is the last into that group's O

@@ -88,6 +88,8 @@ struct Shared {
   uint32_t rank_n[kRanks];
   uint32_t bound;                      // image of the bound, 0 = none
   uint32_t mine_n;                     // logits in `gather` (more than kGather: too many), or of the exchanged step
+  SampleParams params;                 // for functions that are not inlined: a kernel parameter behind a pointer is read
+                                       // through global memory
   uint64_t bar[kPieces];
   uint64_t seg[kWarps];
   uint32_t ties[kWarps];
@@ -594,7 +596,6 @@ __device__ __forceinline__ uint32_t read_ask(const SampleParams& p, int64_t row,
   if (!(T >= 0.0f) || T == INFINITY) bad |= SV_DEV_BAD_TEMPERATURE;
   if (k_in < 0 || !(p_in > 0.0f && p_in <= 1.0f) || !(q_in >= 0.0f && q_in <= 1.0f)) bad |= SV_DEV_BAD_FILTER;
   const bool greedy = T == 0.0f;
-  ask.p = &p;
   ask.row = row;
   ask.total = 0;
   ask.steep = greedy ? 1.0f : fminf(__fdiv_rn(1.44269504088896341f, T), FLT_MAX);
@@ -1220,6 +1221,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
   }
   Ask ask;
   uint32_t bad = read_ask(p, row, ask);
+  ask.p = &sh.params;
   bool bad_uniform = false;
   for (int j = tid; j < p.M; j += kThreads) {
     const float u = p.uniforms[row * p.M + j];
@@ -1427,6 +1429,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   __shared__ Shared sh;
   const int cluster = blockIdx.x / cluster_size(), clusters = gridDim.x / cluster_size();
   if (threadIdx.x == 0) {
+    sh.params = p;
     for (int i = 0; i < kPieces; ++i) mbar_init(&sh.bar[i], 1);
     fence_proxy_async_smem();
   }
@@ -1551,9 +1554,11 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x;
   sh.count[tid] = 0;
+  if (tid == 0) sh.params = p;
   pdl_wait();
   Ask ask;
   const uint32_t bad = read_ask(p, row, ask);
+  ask.p = &sh.params;
   bool bad_uniform = false;
   for (int j = tid; j < p.M; j += kThreads) {
     const float u = p.uniforms[row * p.M + j];

@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "sv_device.cuh"
 #include "sv_ops.h"
@@ -62,6 +63,7 @@ constexpr int kJoinRows = 16;              // rows per CTA of the join
 // What a row tile costs besides its cache tiles, in those: its masked tiles and its end (2.5 us with few rows, 5 with many,
 // against 1.5 a tile; 64 trees 142 us at 0, 134 at 1, 127 at 2, 123 at 3, 121 at 4 and 5).
 constexpr int kExtra = 4, kExtraFewRows = 3;
+constexpr int kMixFloat4 = 768;            // (a fifth stage still fits)
 constexpr int kMaxStages = 12;
 constexpr int kMaxCtas = 152;              // SMs of the GPU: one CTA each
 constexpr int kSmemMax = 232448;           // shared memory that a CTA can have
@@ -177,6 +179,9 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* x) {
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : SV_R8(x, 0), SV_R8(x, 8)
       : "r"(addr));
+}
+__device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : SV_R8(x, 0) : "r"(addr));
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* x) {
   asm volatile(
@@ -305,7 +310,7 @@ struct Smem {
   uint64_t sums_full, o_free;  // once per segment: the groups' sums are there; every thread has read O
   uint64_t mix_full[2], mix_free[2];  // by group: copies' columns written, read
   float m[2][2][kTile], l[2][2][kTile], lr[2][2][kTile];  // by the segment's parity and group
-  float4 mix[2][4 * kGroupThreads];   // by group: columns of every copy's rows, four columns of all rows together
+  float4 mix[2][kMixFloat4];   // by group: columns that the copies exchange, four columns of all rows together
   uint32_t scan[kThreads / 32];
   uint32_t tmem;
   volatile int32_t dead;       // a wait ran out: everyone leaves
@@ -863,18 +868,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && tiles > 1) ok = warp_wait(&sm.pv_done[(last - 1) & 1], ((last - 1) >> 1) & 1, &sm.dead, a.status);
       if (!ok) break;
       tc_after_sync();
-      // this thread's 16 columns from `column` on, both groups' O's together
-      auto read_o = [&](int column, float (&f)[16]) {
-        uint32_t x[16], y[16];
-        tmem_load16(my + Col::o(0) + column, x);
-        tmem_load16(my + Col::o(1) + column, y);
+      // P of this thread's columns from `column` on, both groups' O's together
+      auto read_o = [&](int column, auto& f) {
+        constexpr int P = sizeof(f) / sizeof(float);
+        uint32_t x[P], y[P];
+        if constexpr (P == 16) {
+          tmem_load16(my + Col::o(0) + column, x);
+          tmem_load16(my + Col::o(1) + column, y);
+        } else {
+          tmem_load8(my + Col::o(0) + column, x);
+          tmem_load8(my + Col::o(1) + column, y);
+        }
         tmem_loaded(x);
         tmem_loaded(y);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < P; ++e)
           f[e] = (w0 != 0.0f ? w0 * __uint_as_float(x[e]) : 0.0f) + (w1 != 0.0f ? w1 * __uint_as_float(y[e]) : 0.0f);
       };
-      // (of a pair each group writes one head's)
       const int col0 = group * (W / 2), col1 = col0 + W / 2;
       const bool writes = exists && (!kPair || half == group);
       if constexpr (kCopies == 1) {
@@ -890,49 +900,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        // The copies' sum through shared memory, in rounds of as many columns as fit: every copy writes its own, then
-        // each adds and writes out every kCopies-th four columns.  (Loops, not unrolled: this code runs once a segment
-        // and comes from behind the instruction cache.)
-        const int kept_rows = (rows + 7) & ~7, all_rows = kCopies * kept_rows;
-        const int round = min(W / 2, (4 * kGroupThreads / all_rows * 4) & ~15);
+        // The copies' sum through shared memory: in a round every copy takes P columns, to which the others send theirs.
+        // Rounds of as many columns as fit: each costs 0.8 us, most of it latency.  (Loops, not unrolled: this code runs
+        // once a segment and comes from behind the instruction cache.)
+        const int kept_rows = (rows + 7) & ~7;
+        auto mixed = [&](auto width) {
+          constexpr int P = decltype(width)::value;
 #pragma unroll 1
-        for (int i0 = col0; i0 < col1; i0 += round) {
-          const int i1 = min(i0 + round, col1);
+          for (int i0 = col0; i0 < col1; i0 += kCopies * P) {
+            float f[P];
+            if (active) {
 #pragma unroll 1
-          for (int i = i0; i < i1 && active; i += 16) {
-            float f[16];
-            read_o(i, f);
-            float4* to = mix + ((i - i0) >> 2) * all_rows + copy * kept_rows + local;
-            if (writes) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) to[q * all_rows] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
-            }
-          }
-          mbar_arrive(&sm.mix_full[group]);
-          if (left = !warp_wait(&sm.mix_full[group], mixes & 1, &sm.dead, a.status); left) break;
-          ++mixes;
-          if (writes) {
-#pragma unroll 1
-            for (int i = i0 + 4 * copy; i < i1; i += 4 * kCopies) {
-              const float4* from = mix + ((i - i0) >> 2) * all_rows + local;
-              float4 v = from[0];
-#pragma unroll
               for (int o = 1; o < kCopies; ++o) {
-                const float4 w = from[o * kept_rows];
-                v.x += w.x;
-                v.y += w.y;
-                v.z += w.z;
-                v.w += w.w;
+                const int to = (copy + o) % kCopies;
+                read_o(i0 + to * P, f);
+                float4* at = mix + (to * (kCopies - 1) + o - 1) * (P / 4) * kept_rows + local;
+                if (writes) {
+#pragma unroll
+                  for (int q = 0; q < P / 4; ++q) at[q * kept_rows] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                }
               }
-              emit4(i, v);
+              read_o(i0 + copy * P, f);
+            }
+            mbar_arrive(&sm.mix_full[group]);
+            if (!warp_wait(&sm.mix_full[group], mixes & 1, &sm.dead, a.status)) return false;
+            ++mixes;
+            if (writes) {
+              const float4* from = mix + copy * (kCopies - 1) * (P / 4) * kept_rows + local;
+#pragma unroll
+              for (int q = 0; q < P / 4; ++q) {
+                float4 v = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+#pragma unroll
+                for (int o = 0; o < kCopies - 1; ++o) {
+                  const float4 w = from[(o * (P / 4) + q) * kept_rows];
+                  v.x += w.x;
+                  v.y += w.y;
+                  v.z += w.z;
+                  v.w += w.w;
+                }
+                emit4(i0 + copy * P + 4 * q, v);
+              }
+            }
+            if (i0 + kCopies * P < col1) {  // the buffer is written again
+              mbar_arrive(&sm.mix_free[group]);
+              if (!warp_wait(&sm.mix_free[group], frees & 1, &sm.dead, a.status)) return false;
+              ++frees;
             }
           }
-          if (i1 < col1) {  // the buffer is written again
-            mbar_arrive(&sm.mix_free[group]);
-            if (left = !warp_wait(&sm.mix_free[group], frees & 1, &sm.dead, a.status); left) break;
-            ++frees;
-          }
-        }
+          return true;
+        };
+        // (kept_rows copies (copies - 1) P floats; a half of 32 columns goes over four copies by 8)
+        static_assert(64 * 2 * 16 <= 4 * kMixFloat4 && 16 * 4 * 3 * 16 <= 4 * kMixFloat4 && 32 * 4 * 3 * 8 <= 4 * kMixFloat4, "mix");
+        using Sixteen = std::integral_constant<int, 16>;
+        using Eight = std::integral_constant<int, 8>;
+        if constexpr (kCopies == 2) left = !mixed(Sixteen());
+        else if constexpr (W == 64) left = !mixed(Eight());
+        else left = kept_rows <= 16 ? !mixed(Sixteen()) : !mixed(Eight());
       }
       if (left) break;
       tc_before_sync();

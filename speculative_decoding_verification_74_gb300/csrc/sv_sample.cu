@@ -1456,22 +1456,38 @@ constexpr int kMaxLoads = 4;                             // 16-byte loads of a t
 constexpr int kSegmentVecs = kMaxThreads * kMaxLoads;    // 16 KB of a row
 constexpr int kMaxCtas = 4;                              // per SM
 constexpr int kGroupVecs = 8;
+constexpr int kSumLoads = 4;                             // the same, where a CTA sums a whole row
 constexpr int kSelectCtas = 3;                           // per SM
 constexpr int64_t kStreamBytes = 64 << 20;
 
-// 16 bytes of a row from its vector v on (vectors lie on 16-byte boundaries; -inf outside the row).
-template <int DT>
-__device__ __forceinline__ uint4 row_vec(const typename Slice<DT>::Elem* x_row, int phase, int V, int v) {
+// N vectors of 16 bytes of a row, from v on and kMaxThreads or kThreads (`apart`) from each other; vectors lie on 16-byte
+// boundaries, and outside the row is -inf.  The loads of whole vectors are all in flight before the (at most two) ragged
+// ones are put together.
+template <int DT, int N>
+__device__ __forceinline__ void row_vecs(const typename Slice<DT>::Elem* x_row, int phase, int V, int v, int apart, uint4 (&w)[N]) {
   using Elem = typename Slice<DT>::Elem;
   constexpr int kElems = Vec<DT>::kElems;
-  const int e0 = v * kElems - phase;
-  if (e0 >= 0 && e0 + kElems <= V) return __ldg(reinterpret_cast<const uint4*>(x_row + e0));
-  uint4 w;
-  Elem* e = reinterpret_cast<Elem*>(&w);
+  constexpr uint32_t kNone = DT == SV_BF16 ? 0xFF80FF80u : 0xFF800000u;
+  const uint4* vecs = reinterpret_cast<const uint4*>(x_row - phase);
+  const int whole_a = phase > 0 ? 1 : 0, whole_z = (phase + V) / kElems, all = (phase + V + kElems - 1) / kElems;
 #pragma unroll
-  for (int i = 0; i < kElems; ++i)
-    e[i] = e0 + i >= 0 && e0 + i < V ? x_row[e0 + i] : (DT == SV_BF16 ? static_cast<Elem>(0xFF80u) : static_cast<Elem>(0xFF800000u));
-  return w;
+  for (int i = 0; i < N; ++i) {
+    const int u = v + i * apart;
+    w[i] = make_uint4(kNone, kNone, kNone, kNone);
+    if (u >= whole_a && u < whole_z) w[i] = __ldg(vecs + u);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int u = v + i * apart;
+    if (u < all && (u < whole_a || u >= whole_z)) {
+      Elem* e = reinterpret_cast<Elem*>(&w[i]);
+#pragma unroll
+      for (int x = 0; x < kElems; ++x) {
+        const int at = u * kElems - phase + x;
+        if (at >= 0 && at < V) e[x] = x_row[at];
+      }
+    }
+  }
 }
 
 // Resident CTAs take 16 KB segments of rows in turn, the next one's loads in flight while one's maxima are taken.  Bound by
@@ -1491,14 +1507,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxCtas) maxima_kernel(const Sam
     const uint32_t row = item / p.segments;
     const Elem* x_row = static_cast<const Elem*>(p.logits) + row * p.row_stride;
     const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(x_row) & 15u) / sizeof(Elem));
-    const int vecs = (phase + p.V + kElems - 1) / kElems;
-    const int v0 = static_cast<int>(item - row * p.segments) * kSegmentVecs + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < kMaxLoads; ++i) {
-      const int v = v0 + i * kMaxThreads;
-      const uint32_t none = DT == SV_BF16 ? 0xFF80FF80u : 0xFF800000u;
-      w[i] = v < vecs ? row_vec<DT>(x_row, phase, p.V, v) : make_uint4(none, none, none, none);
-    }
+    row_vecs<DT>(x_row, phase, p.V, static_cast<int>(item - row * p.segments) * kSegmentVecs + static_cast<int>(threadIdx.x), kMaxThreads, w);
   };
   uint4 w[kMaxLoads], w_next[kMaxLoads];
   uint32_t item = blockIdx.x;
@@ -1609,11 +1618,17 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
   if (ask.nucleus && !ask.by_count) {  // W, over the whole row (its second reading)
     WeightSum sum(top, ask.steep);
     uint32_t adds = 0;
-#pragma unroll 4
-    for (int v = tid; v < vecs; v += kThreads, ++adds) {
-      const Vec<DT> x(row_vec<DT>(x_row, phase, p.V, v));
+#pragma unroll 1
+    for (int v = tid; v < vecs; v += kSumLoads * kThreads) {
+      uint4 w[kSumLoads];
+      row_vecs<DT>(x_row, phase, p.V, v, kThreads, w);
 #pragma unroll
-      for (int e = 0; e < kElems; e += 2) sum.add(x.x[e], x.x[e + 1]);
+      for (int i = 0; i < kSumLoads; ++i) {
+        const Vec<DT> x(w[i]);
+#pragma unroll
+        for (int e = 0; e < kElems; e += 2) sum.add(x.x[e], x.x[e + 1]);
+      }
+      adds += kSumLoads;
     }
     const uint64_t w = warp_sum(sum.total(adds * (kElems / 2)));
     if (lane == 0) sh.seg[warp] = w;
@@ -1646,9 +1661,9 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
     const int g = g0 + tid / kGroupVecs;
     const int v = g < listed ? groups[g] * kGroupVecs + tid % kGroupVecs : vecs;
     uint32_t mask = 0;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (v < vecs) w = row_vec<DT>(x_row, phase, p.V, v);
-    const Vec<DT> x(w);
+    uint4 w[1];
+    row_vecs<DT>(x_row, phase, p.V, v, 0, w);
+    const Vec<DT> x(w[0]);
     if (v < vecs)
 #pragma unroll
       for (int e = 0; e < kElems; ++e) mask |= (x.x[e] >= bound && x.x[e] != -INFINITY ? 1u : 0u) << e;

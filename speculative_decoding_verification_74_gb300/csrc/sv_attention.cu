@@ -24,9 +24,18 @@
 // of the first in the lower half of the (copy's) rows and the lower 64 dimensions, those of the second in the upper ones,
 // zeros elsewhere; of O each row's own 64 columns count.  The products do the work of 128 dimensions on as many bytes.
 //
-// Roles in a CTA: warps 0 and 11 copy K and V page by page through a ring of stages (TMA; one warp alone needs 1.1 us a
-// tile for it); one thread of warp 1 issues the products; warp 10 brings each segment's description, parents and Q; two groups of four warps take the tiles in turn (a
-// thread has a row), each with its own S and O, so one group's exponentials run beside the other's products.
+// Measured (GB300, 32 query and 8 key/value heads of 128, graph replay; a copy of the cache's bytes in brackets): 64 requests
+// of one token over 6k to 8k slots 281 to 287 us (275), 64 trees of up to 16 nodes over 512 to 4096 slots 114 us (92), four
+// chains of 17 over 99k to 131k slots 286 to 293 us (278); a window of 1024 with 16 heads of 64, 33 trees 41 us (19); four
+// requests of one token and up to 130 slots 11.5 us.  Long contexts are bound by memory.  A row tile's masked tiles and
+// end cost about 4 us besides its tiles (1.5 us each), which short contexts feel; a call's launches, first tile and join
+// about 11 us.
+//
+// Roles in a CTA: warps 0 and 11 copy K and V page by page through a ring of stages (TMA; one warp alone needs
+// 1.1 us a tile for it); one thread of warp 1 issues the products; warp 10 brings each segment's description, parents and
+// Q; two groups of four warps take the tiles in turn (a thread has a row), each with its own S and O, so one group's
+// exponentials run beside the other's products.  P is rounded to bf16, the products' type; o is divided by the sum of
+// the rounded P, so its weights add up to 1, and lse takes the sum before rounding.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -60,9 +69,9 @@ struct Columns {
 };
 constexpr float kLazyGrowth = 8.0f;        // log2 units by which a maximum may grow without a rescale of O
 constexpr int kJoinRows = 16;              // rows per CTA of the join
-// What a row tile costs besides its cache tiles, in those: its masked tiles and its end (2.5 us with few rows, 5 with many,
-// against 1.5 a tile; 64 trees 142 us at 0, 134 at 1, 127 at 2, 123 at 3, 121 at 4 and 5).
-constexpr int kExtra = 4, kExtraFewRows = 3;
+// What a row tile costs besides its cache tiles, in those: its masked tiles and its end, about 4 us against 1.5 a tile
+// (64 trees over 512 to 4096 slots 126 us at 0, 114 at 2, 3 and 4; the window's 33 trees 55.5, 40.7, 40.6 and 41.2).
+constexpr int kExtra = 3;
 constexpr int kMixFloat4 = 768;            // (a fifth stage still fits)
 constexpr int kMaxStages = 12;
 constexpr int kMaxCtas = 152;              // SMs of the GPU: one CTA each
@@ -1160,7 +1169,8 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
       q_head_stride < c->head_dim || out_head_stride < c->head_dim || q_row_stride < 0 || out_row_stride < 0)
     return set_error(SV_ERR_INVALID_ARG, "q / out: 16-byte aligned rows of head_dim elements are needed");
   if ((s = check_workspace(ws, ws_bytes, sv_attention_workspace_size(c, q_heads))) != SV_OK) return s;
-  // two heads at a time where they lie side by side and all nodes' rows of both fit into a tile
+  // two heads at a time where they lie side by side and all nodes' rows of both fit into a tile (else a tile would be
+  // read once for each of their row tiles; 64 contexts of 8192, 16 heads of 64, one node: 322 us against 504 one by one; the window's 33 trees 41 against 50)
   const int group = q_heads / c->kv_heads;
   const bool pair = c->head_dim == 64 && c->head_stride == 64 && c->kv_heads % 2 == 0 && 2 * Nmax * group <= kTile;
   const int tile_nodes = std::min(kTile / group, Nmax);
@@ -1212,9 +1222,11 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   a.window = window;
   a.sinks = sinks;
   a.scale = scale;
+  // as many copies of a row tile as its height leaves room for (window's 33 trees, 32 rows: 41 us with four, 43 with two, 45
+  // with one; 64 trees of 64 rows: 114 with two, 121 with one; 64 contexts of 1000, 4 rows: 57, 58, 60)
   const int tile_rows = tile_nodes * group * (pair ? 2 : 1), copies = tile_rows <= 32 ? 4 : tile_rows <= 64 ? 2 : 1;
   a.half_rows = kTile / copies / (pair ? 2 : 1);
-  a.extra = tile_rows <= 16 ? kExtraFewRows : kExtra;
+  a.extra = kExtra;
   const auto launch = pair                 ? (copies == 4   ? launch_attention<64, true, 4>
                                               : copies == 2 ? launch_attention<64, true, 2>
                                                             : launch_attention<64, true, 1>)

@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (slot >= end || (slot < lo && slot >= a.sinks)) {
 #pragma unroll 4
             for (int x = 0; x < W / 8; ++x)
-              *reinterpret_cast<uint4*>(ring + st * kStageBytes + (x >> 3) * kHalfBytes + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(ring + st * kStageBytes + (x >> 3) * kHalfBytes + r * 128 + ((x + r) & 7) * 16) = make_uint4(0, 0, 0, 0);  // (neighbours in different banks)
           }
           fence_proxy_async_smem();
         }

@@ -119,6 +119,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// cluster_sync in two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
@@ -888,7 +891,7 @@ __device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const A
     const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
     if (lane >= d) incl += u;
   }
-  cluster_sync();  // sh.z may be written again
+  __syncthreads();  // (no peer still reads sh.z: a cluster barrier lies between cluster_total and here)
   if (lane == 31) sh.seg[warp] = incl;
   __syncthreads();
   if (tid == 0) {
@@ -905,6 +908,7 @@ __device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const A
     z += __shfl_xor_sync(0xFFFFFFFFu, z, d);
     before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
   }
+  cluster_arrive();  // this CTA has read its peers' sums
   for (int i = 0; i < warp; ++i) before += sh.seg[i];
   for (int j = 0; j < p.M; ++j) {
     const uint64_t t0 = share_of(z, static_cast<uint32_t>(p.uniforms[ask.row * p.M + j] * 16777216.0f));
@@ -934,14 +938,15 @@ __device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const A
       left -= all;
     }
   }
-  cluster_sync();  // no CTA leaves while a peer may still read its shared memory
+  cluster_wait();  // no CTA leaves while a peer may still read its shared memory
 }
 
-// The cluster's exact weight of the steps before `step` - 1, and of `step` - 1, `step` and `step` + 1.  Returns how many
+// The cluster's exact weight of the steps before `step` - 1, and of `step` - 1, `step` and `step` + 1 (turn: 0 and 1 in
+// turn, so a call's sums are not written while a peer reads the call's before).  Returns how many
 // logits the warp has listed that may lie in these three, or -1 for too many.
 template <int DT>
 __device__ __noinline__ int weights_around(const Slice<DT>& s, Shared& sh, const Ask& ask, const Scale& scale, int step,
-                                           uint64_t (&out)[4]) {
+                                           uint32_t turn, uint64_t (&out)[4]) {
   constexpr int kElems = Vec<DT>::kElems;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // surely above: the packed sum; surely below: nothing; the few between are listed and weighed by their step (in
@@ -984,24 +989,24 @@ __device__ __noinline__ int weights_around(const Slice<DT>& s, Shared& sh, const
     }
   }
   const uint64_t high = warp_sum(sum.total(adds * (Vec<DT>::kElems / 2)));
+  uint64_t* sums_at = sh.all_w + (turn & 1) * 4 * (kWarps + 1);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint64_t t = warp_sum(part[i]) + (i == 0 ? high : 0);
-    if (lane == 0) sh.all_w[4 * warp + i] = t;
+    if (lane == 0) sums_at[4 * warp + i] = t;
   }
   __syncthreads();
   if (tid < 4) {
     uint64_t t = 0;
-    for (int w = 0; w < kWarps; ++w) t += sh.all_w[4 * w + tid];
-    sh.all_w[4 * kWarps + tid] = t;
+    for (int w = 0; w < kWarps; ++w) t += sums_at[4 * w + tid];
+    sums_at[4 * kWarps + tid] = t;
   }
   cluster_sync();
   static_assert(4 * kMaxCluster == 32, "a lane per CTA and value");
-  uint64_t sums = peers_sum(&sh.all_w[4 * kWarps + lane / kMaxCluster]);
+  uint64_t sums = peers_sum(&sums_at[4 * kWarps + lane / kMaxCluster]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) out[i] = __shfl_sync(0xFFFFFFFFu, sums, i * kMaxCluster);
-  cluster_sync();  // the peers have read them
   return n <= kListPerWarp ? n : -1;
 }
 
@@ -1060,7 +1065,7 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
         by_radix = here > kExchange;
         uint64_t above_w = 0;
         if (ask.nucleus) {
-          listed = weights_around<DT>(s, sh, ask, scale, step, near);
+          listed = weights_around<DT>(s, sh, ask, scale, step, 0, near);
           above_w = near[0] + near[1];
         }
         if (by_radix) b = descend<DT, false>(s, sh, ask.k, top, steep);
@@ -1078,7 +1083,7 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
     }
     if (ask.nucleus) {
       const uint64_t limit = max(share_of(total, ask.p24), uint64_t(1));
-      cluster_sync();  // the peers have read the histogram, or the keys exchanged before
+      if (by_radix) cluster_sync();  // the peers have read the last histogram (else weights_around's barrier sees to it)
       // The step whose weight makes the sum reach the limit, about; it is weighed with its neighbours, exactly, and if it
       // is not one of them, the estimate is set right there and another step chosen (few heavy logits make it that far
       // off).
@@ -1098,7 +1103,7 @@ __device__ __noinline__ void cut_wide(const Slice<DT>& s, Shared& sh, const Ask&
         step = sh.step;
         if (tries > 0) step = below ? min(step, last - 3) : max(step, last + 3);
         step = max(0, min(step, kSteps - 1));
-        listed = weights_around<DT>(s, sh, ask, scale, step, near);
+        listed = weights_around<DT>(s, sh, ask, scale, step, tries, near);
         above_w = near[0];
         int in = step - 1;
         for (int i = 1; i < 4 && !inside; ++i) {

@@ -1292,7 +1292,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
   if (tid == 0) sh.top = top_key;
   // ---- 1. a bound ---------------------------------------------------------------------------------
   // the CTA vouches for rank_n[j] logits at or above rank_at[j]: from an even share of k to all of it
-  if (ask.by_count) {
+  if (ask.by_count && ask.k > 1) {  // (one: the largest is the bound)
     if (tid < kRanks) {
       sh.rank_at[tid] = -INFINITY;
       sh.rank_n[tid] = static_cast<uint32_t>(ceilf(static_cast<float>(ask.k) * exp2f(-3.0f + 3.0f * tid / (kRanks - 1))));
@@ -1335,7 +1335,9 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
     return;
   }
   float bound = -INFINITY;
-  if (ask.by_count) {
+  if (ask.by_count && ask.k == 1) {
+    bound = top;
+  } else if (ask.by_count) {
     // the largest published logit above which the CTAs together vouch for k: thread t asks CTA t % 8 about the
     // (t / 8)-th published one
     if (tid < kMaxCluster * kRanks)
@@ -1360,7 +1362,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
   // Below min-p's threshold nothing is kept.  The boundary may then lie below the bound: it is not found, and everything
   // above the bound is kept.  Only the top-k's own weight needs all of the top-k.
   if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(ask.least * 1.000001f, ask.steep)));
-  if (!(bound < top)) bound = bound >= top ? top : -INFINITY;
+  if (!(bound < top)) bound = bound >= top ? top : -INFINITY;  // (a NaN: no bound)
   ask.bound = bound;
   if (ask.nucleus && !ask.by_count) {  // top-p alone: its list may be long, which the counts tell for less than listing
     const uint32_t c = count_steps<DT>(s, sh, ask);
@@ -1621,8 +1623,8 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
   ask.top = top;
   // the bound: the k-th largest maximum has k logits at or above it (a step's lower end, a little lower than the
   // roundings of step() may put it)
-  float bound = -INFINITY;
-  if (ask.by_count) {
+  float bound = ask.k == 1 ? top : -INFINITY;
+  if (ask.by_count && ask.k > 1) {
     const Scale scale = Scale::over(top, __fsub_rn(top, logit_of_key(low_key)));
     for (int g = tid; g < n_groups; g += kThreads)
       if (maxima[g] > -INFINITY) atomicAdd(&sh.count[scale.step(maxima[g])], 1u);
@@ -1653,7 +1655,7 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
     bound = nucleus_bound(ask, p.V);
   }
   if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(ask.least * 1.000001f, ask.steep)));
-  if (!(bound < top)) bound = bound >= top ? top : -INFINITY;
+  if (!(bound < top)) bound = bound >= top ? top : -INFINITY;  // (a NaN: no bound)
   ask.bound = bound;
   ask.out_row = p.out_rows != nullptr ? static_cast<Elem*>(p.out_rows) + row * p.out_stride : nullptr;
   // the groups that reach it, in order: thread t looks at a stretch

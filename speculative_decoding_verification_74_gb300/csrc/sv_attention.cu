@@ -25,9 +25,9 @@
 // zeros elsewhere; of O each row's own 64 columns count.  The products do the work of 128 dimensions on as many bytes.
 //
 // Measured (GB300, 32 query and 8 key/value heads of 128, graph replay; a copy of the cache's bytes in brackets): 64 requests
-// of one token over 6k to 8k slots 281 to 287 us (275), 64 trees of up to 16 nodes over 512 to 4096 slots 114 us (92), four
-// chains of 17 over 99k to 131k slots 286 to 293 us (278); a window of 1024 with 16 heads of 64, 33 trees 41 us (19); four
-// requests of one token and up to 130 slots 11.5 us.  Long contexts are bound by memory.  A row tile's masked tiles and
+// of one token over 6k to 8k slots 281 to 287 us (275), 64 trees of up to 16 nodes over 512 to 4096 slots 113 us (92), four
+// chains of 17 over 99k to 131k slots 286 to 293 us (278); a window of 1024 with 16 heads of 64, 33 trees 38 us (19); four
+// requests of one token and up to 130 slots 10.9 us.  Long contexts are bound by memory.  A row tile's masked tiles and
 // end cost about 4 us besides its tiles (1.5 us each), which short contexts feel; a call's launches, first tile and join
 // about 11 us.
 //

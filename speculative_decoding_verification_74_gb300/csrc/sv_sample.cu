@@ -27,12 +27,12 @@
 // are listed for the clusters, which take them in turn.
 //
 // Measured (GB300, 151936 logits a row; a copy of the same bytes takes 97.5 us for 1088 float32 rows): 1088 rows float32
-// plain 340 us, top-k 50 160 us (maxima 100, select 55), min-p alone 150 us, top-p 0.9 alone 730 us (peaked rows) to
-// 1300 us (flat ones); mixed filters with the cut rows written 388 us (maxima with the cut rows' -inf 200, 195 being
-// their copy's; select 80; clusters for the 50 rows with top-p alone 97).  64 rows bf16: plain 15 us, top-k 50 18 us,
-// top-p alone 57 to 62 us, mixed 44 to 50 us.  Four rows of 32000: 6.8 us, the latency of one launch and seven barriers.
+// plain 324 us, greedy 313 us, top-k 50 163 us (maxima 100, select 55), min-p alone 155 us, top-p 0.9 alone 720 us (peaked
+// rows) to 1250 us (flat ones); mixed filters with the cut rows written 381 us (maxima with the cut rows' -inf 200, 195
+// being their copy's; select 80; clusters for the 50 rows with top-p alone 95).  64 rows bf16: plain 15 us, top-k 50 18
+// us, top-p alone 55 to 61 us, mixed 42 to 48 us.  Four rows of 32000: 6.5 us, the latency of one launch and its barriers.
 // What bounds it now: with few rows the chain of barriers and passes of the slowest row (a flat row under top-p alone
-// takes six passes over its slices and fourteen cluster barriers: 36 us by itself), with many the reading.
+// takes six passes over its slices and ten cluster barriers: 34 us by itself), with many the reading.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -5,7 +5,7 @@
 // threads run.  A page's state is its reference count alone: there is no free list to keep in step.
 //
 // Measured (GB300): a turn of 64 trees of up to 16 nodes in 32 layers (8 heads of 128) 63 us: reserve 4 us, append 45 us
-// (its bytes copied: 40 us), commit 10 us; 16 prompts to 48 beams (the partly filled pages of 32 layers copied) 73 us (59
+// (its bytes copied: 40 us), commit 10 us; 16 prompts to 48 beams (the partly filled pages of 32 layers copied) 72 us (59
 // us).  The rows are bound by memory; the bookkeeping by the latency of one CTA's scans, and small calls by their launches
 // (a turn of four requests: five launches, 11 us).
 #include <cuda_bf16.h>
@@ -674,7 +674,8 @@ sv_status sv_cache_fork(const sv_cache* c, int32_t* page_table, int table_width,
   a.layers = c->layers;
   a.done = done;
   const int64_t items = static_cast<int64_t>(c->layers) * 2 * c->page_size * a.r.pieces;
-  const int64_t groups = std::min<int64_t>(std::max(1, 1824 / n), (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
+  // one wave of eight CTAs an SM (half as many again 73.5 us against 72.0 for 16 prompts to 48 beams)
+  const int64_t groups = std::min<int64_t>(std::max(1, 8 * 152 / n), (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
   const auto kernel = items <= INT_MAX ? fork_rows_kernel<uint32_t> : fork_rows_kernel<uint64_t>;
   return launch_status(launch_dependent(kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, groups)), n),
                                         kRowThreads, 0, stream, SV_KERNEL_CACHE_ROWS, 1, a),

@@ -109,3 +109,80 @@ def test_the_same_in_smaller_calls_and_again():
         part = sv.sample(x[s], T[s], u[s], top_k=k[s], top_p=p[s], min_p=q[s], filtered=True)
         for a, b in zip(first, part):
             assert torch.equal(a[s], b)
+
+
+# ---- some rows with top-p and no top-k beside others: 64 rows, clusters of 4 and of 8 -------------------------------
+@pytest.mark.parametrize("dtype,V", [(torch.bfloat16, 151936), (torch.float32, 50021)])
+@pytest.mark.parametrize("kind", ["normal", "ties", "wide", "masked"])
+@pytest.mark.parametrize("apart", [0, 1, 10, 38, 39, 64])
+def test_rows_apart(apart, kind, dtype, V):
+    R = 64
+    x, u = rows(kind, R, V, dtype, apart), uniforms(R, 3, 4)
+    T, k, p, q = params(R, 13, "kpq")
+    T = torch.where(T == 0, 0.8, T)
+    k = torch.where(k == 0, 20, k.clamp(max=1000)).to(torch.int32)
+    where = torch.randperm(R, generator=torch.Generator().manual_seed(apart))[:apart].cuda()
+    k[where] = 0
+    p[where] = torch.where(p[where] >= 1, 0.95, p[where])
+    ws = sv.sample_workspace(R, V)
+    for _ in range(2):
+        tok, prob, cut = sv.sample(x, T, u, top_k=k, top_p=p, min_p=q, filtered=True, ws=ws)
+        a, b, c = defined(x, T, u, k, p, q)
+        assert torch.equal(cut, c) and torch.equal(tok, a) and torch.equal(prob, b)
+    assert sv.sv_query_status(ws) == (sv.SV_OK, 0)
+
+
+def test_bad_rows_apart():
+    R, V = 64, 50021
+    x, u = rows("normal", R, V, torch.float32, 8), uniforms(R, 1, 6)
+    T, k, p, q = (torch.full((R,), 0.9, device="cuda"), torch.full((R,), 30, dtype=torch.int32, device="cuda"),
+                  torch.full((R,), 0.9, device="cuda"), torch.zeros(R, device="cuda"))
+    k[::5] = 0
+    good = sv.sample(x, T, u, top_k=k, top_p=p, min_p=q, filtered=True)
+    x[5, 3], x[10, 3], x[6, 4] = math.nan, math.inf, math.nan
+    p[15], u[20, 0], T[25], k[31] = 1.5, 1.0, math.inf, -1
+    x[30] = -math.inf
+    ws = sv.sample_workspace(R, V)
+    tok, prob, cut = sv.sample(x, T, u, top_k=k, top_p=p, min_p=q, filtered=True, ws=ws)
+    bad = [5, 6, 10, 15, 20, 25, 31]
+    others = [r for r in range(R) if r not in bad + [30]]
+    assert bool((tok[bad + [30]] == -1).all()) and bool(prob[bad].isnan().all()) and bool((cut[bad + [30]] == -math.inf).all())
+    for a, b in zip((tok, prob, cut), good):
+        assert torch.equal(a[others], b[others])
+    assert sv.sv_query_status(ws)[1] == sv.SV_DEV_BAD_LOGIT | sv.SV_DEV_BAD_TEMPERATURE | sv.SV_DEV_BAD_FILTER
+
+
+def test_rows_apart_on_a_stream_and_in_a_graph():
+    # the calls' own order: what fills the logits before, what reads the tokens after
+    R, V = 64, 50021
+    base, u = rows("normal", R, V, torch.float32, 9), uniforms(R, 1, 7)
+    T, k, p, q = params(R, 17, "kpq")
+    k[::6], p[::6] = 0, 0.9
+    ws = sv.sample_workspace(R, V)
+    x = torch.empty_like(base)
+    out = (torch.empty(R, 1, dtype=torch.int32, device="cuda"), torch.empty(R, 1, device="cuda"))
+    after = torch.empty_like(out[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step(scale):
+        torch.mul(base, scale, out=x)
+        sv.sample(x, T, u, top_k=k, top_p=p, min_p=q, out=out, ws=ws)
+        after.copy_(out[0])
+
+    with torch.cuda.stream(side):
+        for i in range(20):
+            step(1.0 + i)
+            a = defined(base * (1.0 + i), T, u, k, p, q)[0]
+            assert torch.equal(after, a)
+    graph = torch.cuda.CUDAGraph()
+    scale = torch.ones((), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            step(scale)
+    for i in range(5):
+        scale.fill_(1.0 + i)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(after, defined(base * (1.0 + i), T, u, k, p, q)[0])

@@ -7,7 +7,7 @@
 // Measured (GB300): a turn of 64 trees of up to 16 nodes in 32 layers (8 heads of 128) 63 us: reserve 4 us, append 45 us
 // (its bytes copied: 40 us), commit 10 us; 16 prompts to 48 beams (the partly filled pages of 32 layers copied) 72 us (59
 // us).  The rows are bound by memory; the bookkeeping by the latency of one CTA's scans, and small calls by their launches
-// (a turn of four requests: five launches, 11 us).
+// (a turn of four requests: three launches, 11 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -28,19 +28,16 @@ inline sv_status launch_status(cudaError_t e, const char* what) {
   return e == cudaSuccess ? SV_OK : set_error(SV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Dynamic shared memory of a kernel, raised once per device (and again only for more).  largest: the kernel shall run beside
-// others, with as much of an SM's memory shared as can be.
+// Dynamic shared memory of a kernel, raised once per device (and again only for more).
 constexpr int kMaxDevices = 64;
 template <auto kKernel>
-cudaError_t allow_smem(size_t bytes, bool largest = false) {
+cudaError_t allow_smem(size_t bytes) {
   static std::atomic<size_t> allowed[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < kMaxDevices && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && largest)
-    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess && dev < kMaxDevices) allowed[dev].store(bytes, std::memory_order_relaxed);
   return e;
 }

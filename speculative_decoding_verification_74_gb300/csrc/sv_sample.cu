@@ -30,7 +30,7 @@
 // plain 324 us, greedy 313 us, top-k 50 163 us (maxima 100, select 55), min-p alone 155 us, top-p 0.9 alone 720 us (peaked
 // rows) to 1250 us (flat ones); mixed filters with the cut rows written 381 us (maxima with the cut rows' -inf 200, 195
 // being their copy's; select 80; clusters for the 50 rows with top-p alone 95).  64 rows bf16: plain 15 us, top-k 50 18
-// us, top-p alone 55 to 61 us, mixed 41 us.  Four rows of 32000: 6.5 us, the latency of one launch and its barriers.
+// us, top-p alone 55 to 61 us, mixed 42 to 48 us.  Four rows of 32000: 6.5 us, the latency of one launch and its barriers.
 // What bounds it now: with few rows the chain of barriers and passes of the slowest row (a flat row under top-p alone
 // takes six passes over its slices and ten cluster barriers: 34 us by itself), with many the reading.
 #include <cuda_bf16.h>
@@ -76,7 +76,6 @@ struct SampleParams {
   float* maxima;           // [R][groups]
   int32_t R, V, M, slice;  // slice: elements per CTA, a multiple of 8
   int32_t groups, segments;
-  int32_t apart;           // up to so many rows go by larger clusters beside the others'
 };
 
 // Per-CTA state; the parts that peers read are written before a cluster barrier.
@@ -1439,61 +1438,31 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
   }
 }
 
-// A cluster per row (kEvery); larger clusters for a few rows with top-p and no top-k (kApart) beside a cluster for each of
-// the others (kOthers); or resident clusters that take the rows that select_kernel has left, in turn (kListed).
-enum RowsOf { kEvery, kApart, kOthers, kListed };
-constexpr int kApartRows = 2 * kThreads;  // rows of a call that kApart looks at
-template <int DT, RowsOf kRows>
+// A cluster per row, or (kListed) resident clusters for the rows that select_kernel has left, in turn.
+template <int DT, bool kListed>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ Shared sh;
-  __shared__ int16_t mine[kRows == kApart ? kApartRows : 1];
-  const int tid = threadIdx.x;
   const int cluster = blockIdx.x / cluster_size(), clusters = gridDim.x / cluster_size();
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     sh.params = p;
     for (int i = 0; i < kPieces; ++i) mbar_init(&sh.bar[i], 1);
     fence_proxy_async_smem();
   }
   __syncthreads();
-  auto apart = [&](int row) {
-    Ask ask;
-    return row < p.R && read_ask(p, row, ask) == 0 && ask.nucleus && !ask.by_count;
-  };
-  if constexpr (kRows == kEvery) {
-    pdl_wait();
+  pdl_wait();
+  if (!kListed) {
     sample_row<DT>(p, cluster, dyn, sh, 0);
-  } else if constexpr (kRows == kOthers) {
-    // (nothing to wait for at the start: the kernel before only lets this one start when all before it is complete, and
-    // works on other rows)
-    int n = 0;
-    if (apart(cluster))
-      for (int r0 = 0; r0 < p.R; r0 += kThreads) n += __syncthreads_count(apart(r0 + tid));
-    if (n == 0 || n > p.apart) sample_row<DT>(p, cluster, dyn, sh, 0);
-    pdl_wait();  // so that what follows this kernel follows the one before, too
-  } else {
-    pdl_wait();
-    int rows = 0;
-    if constexpr (kRows == kListed) {
-      rows = p.left[0];
-    } else {
-      pdl_trigger();
-      for (int r0 = 0; r0 < p.R; r0 += kThreads) {
-        const bool is = apart(r0 + tid);
-        const int at = rows + static_cast<int>(block_scan32(sh, is));
-        if (is) mine[at] = static_cast<int16_t>(r0 + tid);
-        rows += __syncthreads_count(is);
-      }
-      if (rows > p.apart) return;
-    }
-    uint32_t parity = 0;
+    return;
+  }
+  const int rows = p.left[0];
+  uint32_t parity = 0;
 #pragma unroll 1
-    for (int i = cluster; i < rows; i += clusters) {  // (a row's end has synchronised the cluster)
-      sample_row<DT>(p, kRows == kListed ? p.left[1 + i] : mine[i], dyn, sh, parity);
-      parity ^= 1;
-      __syncthreads();
-      fence_proxy_async_smem();  // the next row's copies overwrite what this one has read and written
-    }
+  for (int i = cluster; i < rows; i += clusters) {  // (a row's end has synchronised the cluster)
+    sample_row<DT>(p, p.left[1 + i], dyn, sh, parity);
+    parity ^= 1;
+    __syncthreads();
+    fence_proxy_async_smem();  // the next row's copies overwrite what this one has read and written
   }
 }
 
@@ -1760,28 +1729,12 @@ cudaError_t launch_sample(SampleParams p, void* stream) {
     if ((e = allow_smem<select_kernel<DT>>(room)) != cudaSuccess) return e;
     e = launch_dependent(select_kernel<DT>, dim3(p.R), kThreads, room, stream, SV_KERNEL_SAMPLE, 1, p);
     if (e != cudaSuccess) return e;
-    if ((e = allow_smem<sample_kernel<DT, kListed>>(dyn)) != cudaSuccess) return e;
+    if ((e = allow_smem<sample_kernel<DT, true>>(dyn)) != cudaSuccess) return e;
     const int clusters = std::min(p.R, std::max(1, 2 * sms / cs));
-    return launch_dependent(sample_kernel<DT, kListed>, dim3(static_cast<unsigned>(clusters) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
+    return launch_dependent(sample_kernel<DT, true>, dim3(static_cast<unsigned>(clusters) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
   }
-  // Top-p without top-k takes several times as long as the other filters: where rows may differ in that and clusters may
-  // be larger, a few such rows are sampled by larger ones beside the others (64 rows of 151936 bf16, mixed filters: 41 us
-  // against 48; where no row or every row is such, the second launch costs 2 to 3 us: top-k 50 with top-p 21 against 18).
-  // Both kernels ask for the same division of an SM's memory, without which they do not run side by side (57 us).
-  if (p.top_p != nullptr && (p.top_k != nullptr || p.min_p != nullptr) && cs < kMaxCluster && p.R <= kApartRows && bytes > kMaxCluster * 16384) {
-    p.apart = 2 * sms / kMaxCluster;
-    SampleParams q = p;
-    q.slice = ((p.V + kMaxCluster - 1) / kMaxCluster + 7) & ~7;
-    const size_t room = std::max(static_cast<size_t>(q.slice) * kElt + 32, sizeof(uint64_t) * kGather + sizeof(uint32_t) * 3 * kSteps);
-    if ((e = allow_smem<sample_kernel<DT, kApart>>(room, true)) != cudaSuccess) return e;
-    e = launch_dependent(sample_kernel<DT, kApart>, dim3(static_cast<unsigned>(std::min(p.R, p.apart)) * kMaxCluster), kThreads, room, stream,
-                         SV_KERNEL_SAMPLE, kMaxCluster, q);
-    if (e != cudaSuccess) return e;
-    if ((e = allow_smem<sample_kernel<DT, kOthers>>(dyn, true)) != cudaSuccess) return e;
-    return launch_dependent(sample_kernel<DT, kOthers>, dim3(static_cast<unsigned>(p.R) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
-  }
-  if ((e = allow_smem<sample_kernel<DT, kEvery>>(dyn)) != cudaSuccess) return e;
-  return launch_dependent(sample_kernel<DT, kEvery>, dim3(static_cast<unsigned>(p.R) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
+  if ((e = allow_smem<sample_kernel<DT, false>>(dyn)) != cudaSuccess) return e;
+  return launch_dependent(sample_kernel<DT, false>, dim3(static_cast<unsigned>(p.R) * cs), kThreads, dyn, stream, SV_KERNEL_SAMPLE, cs, p);
 }
 
 }  // namespace

@@ -111,7 +111,7 @@ def test_the_same_in_smaller_calls_and_again():
             assert torch.equal(a[s], b)
 
 
-# ---- some rows with top-p and no top-k beside others: 64 rows, clusters of 4 and of 8 -------------------------------
+# ---- 64 rows (clusters of four), some with top-p and no top-k -------------------------------------------------------
 @pytest.mark.parametrize("dtype,V", [(torch.bfloat16, 151936), (torch.float32, 50021)])
 @pytest.mark.parametrize("kind", ["normal", "ties", "wide", "masked"])
 @pytest.mark.parametrize("apart", [0, 1, 10, 38, 39, 64])

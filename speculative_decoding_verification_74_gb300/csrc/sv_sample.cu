@@ -27,10 +27,10 @@
 // are listed for the clusters, which take them in turn.
 //
 // Measured (GB300, 151936 logits a row; a copy of the same bytes takes 97.5 us for 1088 float32 rows): 1088 rows float32
-// plain 324 us, greedy 313 us, top-k 50 163 us (maxima 100, select 55), min-p alone 155 us, top-p 0.9 alone 720 us (peaked
-// rows) to 1250 us (flat ones); mixed filters with the cut rows written 381 us (maxima with the cut rows' -inf 200, 195
+// plain 297 us, greedy 313 us, top-k 50 163 us (maxima 100, select 55), min-p alone 155 us, top-p 0.9 alone 720 us (peaked
+// rows) to 1230 us (flat ones); mixed filters with the cut rows written 377 us (maxima with the cut rows' -inf 200, 195
 // being their copy's; select 80; clusters for the 50 rows with top-p alone 95).  64 rows bf16: plain 15 us, top-k 50 18
-// us, top-p alone 55 to 61 us, mixed 42 to 48 us.  Four rows of 32000: 6.5 us, the latency of one launch and its barriers.
+// us, top-p alone 54 to 60 us, mixed 40 to 46 us.  Four rows of 32000: 6.3 us, the latency of one launch and its barriers.
 // What bounds it now: with few rows the chain of barriers and passes of the slowest row (a flat row under top-p alone
 // takes six passes over its slices and ten cluster barriers: 34 us by itself), with many the reading.
 #include <cuda_bf16.h>
@@ -868,7 +868,31 @@ __device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const A
   auto kept = [&](float x, int pos) {
     return kAll || x > last || (x == last && x != -INFINITY && static_cast<uint32_t>(s.index_of(pos)) < cut) ? x : -INFINITY;
   };
-  Elem* out_row = static_cast<Elem*>(ask.out_row);
+  // the cut row: a warp's vectors side by side, those without a kept logit left as they are
+  if (Elem* out_row = static_cast<Elem*>(ask.out_row); out_row != nullptr) {
+    const bool aligned = ((reinterpret_cast<uintptr_t>(out_row) - s.phase * sizeof(Elem)) & 15u) == 0;
+#pragma unroll 1
+    for (int v = s.run_a + lane; v < s.run_z; v += 32) {
+      uint4 w = s.vec(v);
+      const Vec<DT> x(w);
+      Elem* raw = reinterpret_cast<Elem*>(&w);
+      uint32_t keep = 0;
+#pragma unroll
+      for (int e = 0; e < kElems; ++e) keep |= (kept(x.x[e], v * kElems + e) != -INFINITY ? 1u : 0u) << e;
+      if (keep == 0) continue;
+      const int at = v * kElems - s.phase;
+      if (aligned && at >= 0 && at + kElems <= s.n) {
+#pragma unroll
+        for (int e = 0; e < kElems; ++e)
+          if (!((keep >> e) & 1u)) raw[e] = DT == SV_BF16 ? static_cast<Elem>(0xFF80u) : static_cast<Elem>(0xFF800000u);
+        *reinterpret_cast<uint4*>(out_row + at) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kElems; ++e)
+          if ((keep >> e) & 1u) out_row[at + e] = raw[e];
+      }
+    }
+  }
   WeightSum sum(ask.top, ask.steep);
   uint32_t adds = 0;
 #pragma unroll 2
@@ -878,10 +902,6 @@ __device__ __noinline__ void draw_slices(const Slice<DT>& s, Shared& sh, const A
     for (int e = 0; e < kElems; e += 2) {
       const float x0 = kept(x.x[e], v * kElems + e), x1 = kept(x.x[e + 1], v * kElems + e + 1);
       sum.add(x0, x1);
-      if (out_row != nullptr) {
-        if (x0 != -INFINITY) out_row[v * kElems + e - s.phase] = reinterpret_cast<const Elem*>(s.data)[v * kElems + e];
-        if (x1 != -INFINITY) out_row[v * kElems + e + 1 - s.phase] = reinterpret_cast<const Elem*>(s.data)[v * kElems + e + 1];
-      }
     }
   }
   const uint64_t w = sum.total(adds * (kElems / 2));

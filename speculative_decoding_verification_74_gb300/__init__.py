@@ -680,6 +680,15 @@ def _workspace(nbytes: int, device, stream=None, zeros=False) -> torch.Tensor:
     return ws
 
 
+def _row_stride(x: torch.Tensor) -> int:
+    """Row stride of logits [R, V].  A row's logits have to lie side by side however many rows there are; a dimension of
+    size 1 is never stepped along, and its stride may be any."""
+    R, V = x.shape
+    if V > 1 and R > 0 and x.stride(1) != 1:
+        raise ValueError("logit rows must be contiguous")
+    return x.stride(0) if R > 1 else V
+
+
 def sample_workspace(rows: int, vocab: int, device="cuda") -> torch.Tensor:
     """Workspace of sample() for that many rows (its first word is the device status word)."""
     n = sv_sample_workspace_size(rows, vocab)
@@ -704,14 +713,14 @@ def sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None,
     if out is None:
         out = (torch.empty((R, M), dtype=torch.int32, device=dev),
                torch.empty((R, M), dtype=torch.float32, device=dev) if probs else None)
-    row_stride = _rows(logits)[1] if R > 1 else V
+    row_stride = _row_stride(logits)
     out_stride = V
     if filtered is not None:
         if filtered is True:
             filtered = torch.empty((R, V), dtype=logits.dtype, device=dev)
         if filtered.shape != logits.shape or filtered.dtype != logits.dtype:
             raise ValueError("filtered must have the shape and type of logits")
-        out_stride = _rows(filtered)[1] if R > 1 else V
+        out_stride = _row_stride(filtered)
     if ws is None:
         ws = _workspace(sv_sample_workspace_size(R, V), dev, stream)
     n = R * M

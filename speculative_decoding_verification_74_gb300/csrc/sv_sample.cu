@@ -444,6 +444,12 @@ struct Scale {
   __device__ __forceinline__ float below(int step) const {
     return inv > 0.0f && step < kSteps - 1 ? __fadd_rd(top, __fmul_rd(-((step + 1) / inv), 1.00001f)) : -INFINITY;
   }
+  // A logit at or below every one of the steps up to `step`, a little lower than the roundings of step() may put it; `range`
+  // as given to over().  A range past the largest float (finite logits of 2e38 beside -2e38) leaves one step for all:
+  // its lower end is not known.
+  __device__ __forceinline__ float lower_end(int step, float range) const {
+    return inv > 0.0f ? __fsub_rd(top, __fmul_ru(static_cast<float>(step + 1) / inv, 1.00001f)) : range > 0.0f ? -INFINITY : top;
+  }
   __device__ __forceinline__ int step(float x) const {
     return static_cast<int>(fminf(__fmul_rn(__fsub_rn(top, x), inv), static_cast<float>(kSteps - 1)));
   }
@@ -1320,14 +1326,14 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
     if (tid == 0) sh.bound = 0;
     const float own = logit_of_key(top_key);
     const bool counts = top_key < inf_key && low_key != 0xFFFFFFFFu;
-    const Scale groups = Scale::over(own, counts ? __fsub_rn(own, logit_of_key(low_key)) : 0.0f);
+    const float range = counts ? __fsub_rn(own, logit_of_key(low_key)) : 0.0f;
+    const Scale groups = Scale::over(own, range);
     if (counts && group > -INFINITY) atomicAdd(&sh.count[groups.step(group)], 1u);
     __syncthreads();
     const uint32_t c = sh.count[tid];
     const uint32_t before = block_scan32(sh, c);
     if (c > 0) {
-      // a step's lower end, a little lower than the roundings of step() may put it
-      const float at = groups.inv > 0.0f ? __fsub_rd(own, __fmul_ru(static_cast<float>(tid + 1) / groups.inv, 1.00001f)) : own;
+      const float at = groups.lower_end(tid, range);
 #pragma unroll 1
       for (int j = 0; j < kRanks; ++j) {
         const uint32_t want = sh.rank_n[j];
@@ -1641,17 +1647,16 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
   }
   const float top = logit_of_key(top_key);
   ask.top = top;
-  // the bound: the k-th largest maximum has k logits at or above it (a step's lower end, a little lower than the
-  // roundings of step() may put it)
+  // the bound: the k-th largest maximum has k logits at or above it
   float bound = ask.k == 1 ? top : -INFINITY;
   if (ask.by_count && ask.k > 1) {
-    const Scale scale = Scale::over(top, __fsub_rn(top, logit_of_key(low_key)));
+    const float range = __fsub_rn(top, logit_of_key(low_key));
+    const Scale scale = Scale::over(top, range);
     for (int g = tid; g < n_groups; g += kThreads)
       if (maxima[g] > -INFINITY) atomicAdd(&sh.count[scale.step(maxima[g])], 1u);
     __syncthreads();
     find_step<false>(sh, sh.count[tid], 0, ask.k, 0, 0);
-    if (sh.step != 0xFFFFFFFFu)
-      bound = scale.inv > 0.0f ? __fsub_rd(top, __fmul_ru(static_cast<float>(sh.step + 1) / scale.inv, 1.00001f)) : top;
+    if (sh.step != 0xFFFFFFFFu) bound = scale.lower_end(sh.step, range);
   }
   if (ask.nucleus && !ask.by_count) {  // W, over the whole row (its second reading)
     WeightSum sum(top, ask.steep);

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "sv_internal.h"
 
@@ -28,17 +29,22 @@ inline sv_status launch_status(cudaError_t e, const char* what) {
   return e == cudaSuccess ? SV_OK : set_error(SV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Dynamic shared memory of a kernel, raised once per device (and again only for more).
+// Dynamic shared memory of a kernel, raised once per device (and again only for more).  Setting the limit and noting it are
+// one step for all host threads: set by one and noted by another in between, the note could stay above the limit, and
+// every launch of that size would fail from then on.
 constexpr int kMaxDevices = 64;
 template <auto kKernel>
 cudaError_t allow_smem(size_t bytes) {
   static std::atomic<size_t> allowed[kMaxDevices];
+  static std::mutex raising;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && allowed[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  const std::lock_guard<std::mutex> lock(raising);
   if (dev < kMaxDevices && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && dev < kMaxDevices) allowed[dev].store(bytes, std::memory_order_relaxed);
+  if (e == cudaSuccess && dev < kMaxDevices) allowed[dev].store(bytes, std::memory_order_release);
   return e;
 }
 

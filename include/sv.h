@@ -485,7 +485,8 @@ sv_status sv_cache_commit(const sv_cache* c, int32_t* page_table, int table_widt
  * gets the lowest free page (pairs in order) for the partly filled last one, whose used slots are copied in every
  * layer; seq_len[dst] = seq_len[src].  Lengths are read before any is written.  rows = rows of
  * page_table and seq_len.  dst rows must be empty and differ from each other (else SV_DEV_BAD_SEQ and out_ok[j] = 0); a
- * pair for which no page is left stays undone (SV_DEV_OUT_OF_PAGES, out_ok[j] = 0).  out_ok [n] nullable.
+ * pair whose src row lacks a page for one of its seq_len slots (SV_DEV_BAD_PAGE, out_ok[j] = 0; it takes no page), or for
+ * which no page is left (SV_DEV_OUT_OF_PAGES, out_ok[j] = 0), stays undone.  out_ok [n] nullable.
  */
 sv_status sv_cache_fork(const sv_cache* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
                         const int32_t* src, const int32_t* dst, int n, int32_t* out_ok, void* ws, size_t ws_bytes,

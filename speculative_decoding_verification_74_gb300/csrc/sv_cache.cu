@@ -245,6 +245,21 @@ __global__ void __launch_bounds__(kPageThreads) fork_kernel(Pool p, int32_t* tab
     len[j] = l < 0 ? -1 : static_cast<int32_t>(l);
   }
   __syncthreads();
+  // a row that lacks a page for a slot of its own has nothing to copy there: one warp per pair looks its entries through
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j = warp; j < n; j += kPageThreads / 32) {
+    if (len[j] <= 0) continue;
+    const int32_t* from = table + static_cast<int64_t>(src[j]) * width;
+    const int held = ((len[j] - 1) >> p.shift) + 1;
+    bool lacks = false;
+#pragma unroll 4
+    for (int e = lane; e < held; e += 32) lacks |= static_cast<uint32_t>(from[e]) >= static_cast<uint32_t>(p.pages);
+    if (__any_sync(0xFFFFFFFFu, lacks) && lane == 0) {
+      atomicOr(status, SV_DEV_BAD_PAGE);
+      len[j] = -1;
+    }
+  }
+  __syncthreads();
   const int part_mask = (1 << p.shift) - 1;
   int split[kPerThread], sum = 0;
 #pragma unroll
@@ -293,19 +308,14 @@ __global__ void __launch_bounds__(kPageThreads) fork_kernel(Pool p, int32_t* tab
   });
   __syncthreads();
   // the full pages are shared: one warp per pair
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = warp; i < n; i += kPageThreads / 32) {
     const int full = len[i] < 0 ? 0 : len[i] >> p.shift;
     const int32_t* from = table + static_cast<int64_t>(len[i] < 0 ? 0 : src[i]) * width;
     int32_t* row = table + static_cast<int64_t>(len[i] < 0 ? 0 : dst[i]) * width;
     for (int e = lane; e < full; e += 32) {
       const int page = from[e];
-      if (page >= 0 && page < p.pages) {
-        atomicAdd(p.refs + page, 1);
-        row[e] = page;
-      } else {
-        atomicOr(status, SV_DEV_BAD_PAGE);
-      }
+      atomicAdd(p.refs + page, 1);
+      row[e] = page;
     }
   }
 }
@@ -504,8 +514,7 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(CopyParams a) {
   const int len = a.seq_len[to_row], part = len & ((1 << a.r.shift) - 1), e0 = len >> a.r.shift;
   if (part == 0) return;
   const int32_t from = a.table[static_cast<int64_t>(from_row) * a.width + e0];
-  const int32_t to = a.table[static_cast<int64_t>(to_row) * a.width + e0];
-  if (from < 0 || from >= a.r.pages || to < 0 || to >= a.r.pages) return;
+  const int32_t to = a.table[static_cast<int64_t>(to_row) * a.width + e0];  // (both name pages: fork_kernel has seen to it)
   const I pieces = static_cast<I>(a.r.pieces), per_side = part * pieces, items = static_cast<I>(a.layers) * 2 * per_side;
   const I step = static_cast<I>(gridDim.x) * kRowThreads;
   for (I x0 = static_cast<I>(blockIdx.x) * kRowThreads + threadIdx.x; x0 < items; x0 += kInFlight * step) {

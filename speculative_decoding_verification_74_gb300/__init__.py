@@ -528,12 +528,43 @@ def sv_launch_count() -> int:
 # convenience wrappers
 # ------------------------------------------------------------------------------------------
 
-def workspace(op: int, B: int, Kmax: int, V: int, dt: int, device="cuda") -> torch.Tensor:
-    """Zero-filled workspace (torch allocations are 512-byte aligned)."""
+def _side_stream(stream, device) -> torch.cuda.Stream:
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
+
+
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A new tensor for a call on `stream` to write.  It comes from that stream's memory, so whatever the block was used for
+    before is done when the call runs (a block of the current stream's may still be waited for there), and it goes back
+    only when the current stream, on which the caller may read it, is done with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s, now = _side_stream(stream, device), torch.cuda.current_stream(device)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if s != now:
+        t.record_stream(now)
+    return t
+
+
+def _workspace(nbytes: int, device, stream=None, zeros=False) -> torch.Tensor:
+    """A workspace whose first SV_STATUS_BYTES (or all) are zero, from the memory of `stream` and the fill ordered before a
+    call on it."""
+    if stream is not None:
+        with torch.cuda.stream(_side_stream(stream, device)):
+            return _workspace(nbytes, device, zeros=zeros)
+    if zeros:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:SV_STATUS_BYTES] = 0
+    return ws
+
+
+def workspace(op: int, B: int, Kmax: int, V: int, dt: int, device="cuda", stream=None) -> torch.Tensor:
+    """Zero-filled workspace (torch allocations are 512-byte aligned) for calls on `stream` (None: the current one)."""
     n = sv_workspace_size(op, B, Kmax, V, dt)
     if n == 0:
         raise ValueError("invalid sizes for sv_workspace_size")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return _workspace(n, device, stream, zeros=True)
 
 
 def _rows(x: torch.Tensor):
@@ -557,10 +588,10 @@ def verify_greedy(target, K, *, draft=None, draft_tokens=None, ws=None, stream=N
     dt = _dt(target)
     _, ts = _rows(target)
     ds = _rows(draft)[1] if draft is not None else V
-    out_tok = torch.empty((B, K + 1), dtype=torch.int32, device=target.device)
-    out_len = torch.empty(B, dtype=torch.int32, device=target.device)
+    out_tok = _empty((B, K + 1), torch.int32, target.device, stream)
+    out_len = _empty(B, torch.int32, target.device, stream)
     if ws is None:
-        ws = workspace(SV_OP_VERIFY, B, K, V, dt, target.device)
+        ws = workspace(SV_OP_VERIFY, B, K, V, dt, target.device, stream)
     sv_verify_greedy(target, ts, draft, ds, draft_tokens, dt, B, K, V, out_tok, out_len, ws, stream)
     return out_tok, out_len
 
@@ -571,13 +602,13 @@ def verify_sample(target, draft, draft_tokens, temperature, K, *, seed=0, round_
     B = target.numel() // V // (K + 1)
     dt = _dt(target)
     dev = target.device
-    out_tok = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
-    out_len = torch.empty(B, dtype=torch.int32, device=dev)
-    out_p = torch.empty((B, K), dtype=torch.float32, device=dev) if want_pq else None
-    out_q = torch.empty((B, K), dtype=torch.float32, device=dev) if want_pq else None
-    out_f = torch.empty(B, dtype=torch.uint8, device=dev)
+    out_tok = _empty((B, K + 1), torch.int32, dev, stream)
+    out_len = _empty(B, torch.int32, dev, stream)
+    out_p = _empty((B, K), torch.float32, dev, stream) if want_pq else None
+    out_q = _empty((B, K), torch.float32, dev, stream) if want_pq else None
+    out_f = _empty(B, torch.uint8, dev, stream)
     if ws is None:
-        ws = workspace(SV_OP_VERIFY, B, K, V, dt, dev)
+        ws = workspace(SV_OP_VERIFY, B, K, V, dt, dev, stream)
     ds = _rows(draft)[1] if draft is not None else V
     sv_verify_sample(target, _rows(target)[1], draft, ds, draft_tokens, temperature, seed, round_, request_ids,
                      dt, B, K, V, out_tok, out_len, out_p, out_q, out_f, ws, stream)
@@ -594,12 +625,12 @@ def verify_tree(target, draft, node_offsets, parent, tokens, temperature, Nmax, 
     dt = _dt(target)
     dev = target.device
     if out is None:
-        out = (torch.empty((B, Nmax), dtype=torch.int32, device=dev),
-               torch.empty((B, Nmax), dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.uint8, device=dev))
+        out = (_empty((B, Nmax), torch.int32, dev, stream),
+               _empty((B, Nmax), torch.int32, dev, stream),
+               _empty(B, torch.int32, dev, stream),
+               _empty(B, torch.uint8, dev, stream))
     if ws is None:
-        ws = workspace(SV_OP_TREE, B, Nmax, V, dt, dev)
+        ws = workspace(SV_OP_TREE, B, Nmax, V, dt, dev, stream)
     ds = _rows(draft)[1] if draft is not None else V
     sv_verify_tree(target, _rows(target)[1], draft, ds, node_offsets, num_rows(target), parent, tokens, temperature,
                    seed, round_, request_ids, dt, B, Nmax, V, *out, ws, stream)
@@ -613,13 +644,13 @@ def verify_ragged(target, t_row_offsets, draft, d_row_offsets, draft_tokens, kee
     dt = _dt(target)
     dev = target.device
     if out is None:
-        out = (torch.empty((B, Kmax + 1), dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev),
-               torch.empty((B, Kmax), dtype=torch.float32, device=dev) if want_pq else None,
-               torch.empty((B, Kmax), dtype=torch.float32, device=dev) if want_pq else None,
-               torch.empty(B, dtype=torch.uint8, device=dev))
+        out = (_empty((B, Kmax + 1), torch.int32, dev, stream),
+               _empty(B, torch.int32, dev, stream),
+               _empty((B, Kmax), torch.float32, dev, stream) if want_pq else None,
+               _empty((B, Kmax), torch.float32, dev, stream) if want_pq else None,
+               _empty(B, torch.uint8, dev, stream))
     if ws is None:
-        ws = workspace(SV_OP_VERIFY, B, Kmax, V, dt, dev)
+        ws = workspace(SV_OP_VERIFY, B, Kmax, V, dt, dev, stream)
     ds = _rows(draft)[1] if draft is not None else V
     ts_ = draft_tokens.stride(0) if draft_tokens is not None else Kmax
     sv_verify_ragged(target, _rows(target)[1], t_row_offsets, num_rows(target), draft, ds, d_row_offsets,
@@ -636,10 +667,10 @@ def schedule_depth(alpha, cost_a, cost_b, budget, *, draft_len=None, ratios=None
     B, Dmax = alpha.shape
     dev = alpha.device
     if out is None:
-        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B + 1, dtype=torch.int32, device=dev),
-               torch.empty(1, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int64, device=dev))
+        out = (_empty(B, torch.int32, dev, stream), _empty(B + 1, torch.int32, dev, stream),
+               _empty(1, torch.int32, dev, stream), _empty(1, torch.int64, dev, stream))
     if ws is None:
-        ws = workspace(SV_OP_SCHEDULE, B, Dmax, 1, SV_F32, dev)
+        ws = workspace(SV_OP_SCHEDULE, B, Dmax, 1, SV_F32, dev, stream)
     if cost_table is not None:
         sv_schedule_depth_table(alpha, alpha.stride(0), draft_len, B, Dmax, cost_table[0], cost_table[1], budget,
                                 ratios, objective, *out, ws, stream)
@@ -665,19 +696,6 @@ def _array(t, name: str, dtype, count: int) -> int | None:
     if t.numel() < count:
         raise ValueError(f"{name} holds {t.numel()} elements, the call reads {count}")
     return _p(t)
-
-
-def _workspace(nbytes: int, device, stream=None, zeros=False) -> torch.Tensor:
-    """A workspace whose first SV_STATUS_BYTES (or all) are zero, the fill ordered before a call on `stream`."""
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
-        with torch.cuda.stream(s):
-            return _workspace(nbytes, device, zeros=zeros)
-    if zeros:
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    ws[:SV_STATUS_BYTES] = 0
-    return ws
 
 
 def _row_stride(x: torch.Tensor) -> int:
@@ -711,13 +729,13 @@ def sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None,
     dt = _dt(logits)
     dev = logits.device
     if out is None:
-        out = (torch.empty((R, M), dtype=torch.int32, device=dev),
-               torch.empty((R, M), dtype=torch.float32, device=dev) if probs else None)
+        out = (_empty((R, M), torch.int32, dev, stream),
+               _empty((R, M), torch.float32, dev, stream) if probs else None)
     row_stride = _row_stride(logits)
     out_stride = V
     if filtered is not None:
         if filtered is True:
-            filtered = torch.empty((R, V), dtype=logits.dtype, device=dev)
+            filtered = _empty((R, V), logits.dtype, dev, stream)
         if filtered.shape != logits.shape or filtered.dtype != logits.dtype:
             raise ValueError("filtered must have the shape and type of logits")
         out_stride = _row_stride(filtered)
@@ -789,7 +807,7 @@ class PagedCache:
         B = self._batch(extra.numel())
         i32 = torch.int32
         if ok is None:
-            ok = torch.empty(B, dtype=i32, device=extra.device)
+            ok = _empty(B, i32, extra.device, stream)
         _check((_lib or lib()).sv_cache_reserve(
             self._c, self._table, self.width, _array(seq_len, "seq_len", i32, B), _array(extra, "extra", i32, B), B,
             _array(ok, "ok", i32, B), self._ws, self._ws_bytes, _stream(stream)))
@@ -824,7 +842,7 @@ class PagedCache:
         self._batch(B)
         i32 = torch.int32
         if out_len is None:
-            out_len = torch.empty(B, dtype=i32, device=path.device)
+            out_len = _empty(B, i32, path.device, stream)
         _check((_lib or lib()).sv_cache_commit(
             self._c, self._table, self.width, _array(seq_len, "seq_len", i32, B),
             _array(node_offsets, "node_offsets", i32, B + 1), _array(path, "path", i32, B * Nmax),
@@ -837,7 +855,7 @@ class PagedCache:
         n = src.numel()
         i32 = torch.int32
         if ok is None:
-            ok = torch.empty(n, dtype=i32, device=src.device)
+            ok = _empty(n, i32, src.device, stream)
         _check((_lib or lib()).sv_cache_fork(
             self._c, self._table, self.width, self.rows, _array(seq_len, "seq_len", i32, self.rows),
             _array(src, "src", i32, n), _array(dst, "dst", i32, n), n, _array(ok, "ok", i32, n), self._ws, self._ws_bytes,
@@ -877,13 +895,13 @@ def tree_attention(q, cache: PagedCache, layer, seq_len, node_offsets, parent, N
         raise ValueError("q must be [rows, q_heads, head_dim] of the cache's head_dim")
     n, H, D = q.shape
     if out is None:
-        out = torch.empty((n, H, D), dtype=bf16, device=q.device)
+        out = _empty((n, H, D), bf16, q.device, stream)
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     if q.dtype is not bf16 or out.dtype is not bf16:
         raise ValueError("q and out must be torch.bfloat16")
     if lse is True:
-        lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
+        lse = _empty((n, H), torch.float32, q.device, stream)
     elif lse is False:
         lse = None
     if ws is None:

@@ -121,14 +121,22 @@ def vocab_parallel_verify_sample(target_local, draft_local, draft_tokens, temper
     [B*(K+1), V_r] and draft_local [B*K, V_r] hold this rank's columns: chunks
     chunk_ranges(nchunks, world)[rank] of the library's tiling (sv_vocab_chunks), i.e. columns
     [c0 * chunk_len, min(V, c1 * chunk_len)).  Returns (tokens, accept_len, p, q, flags), the same
-    on every rank."""
+    on every rank.  stream: where the steps and the exchanges run (None: the current stream)."""
     import torch.distributed as dist
-    from . import (sv_vocab_chunks, sv_verify_regions, sv_verify_sample_phase, workspace, _dt, _rows,
+    from . import (sv_vocab_chunks, sv_verify_regions, sv_verify_sample_phase, workspace, _dt, _rows, _side_stream,
                    SV_OP_VERIFY, SV_PHASE_STATS, SV_PHASE_ACCEPT, SV_PHASE_WEIGHTS, SV_PHASE_PICK)
+    dev = target_local.device
+    if stream is not None:  # fills, steps and the exchanges between them are one sequence: all of it on that stream
+        now = torch.cuda.current_stream(dev)
+        with torch.cuda.stream(_side_stream(stream, dev)):
+            out = vocab_parallel_verify_sample(target_local, draft_local, draft_tokens, temperature, K, V, seed=seed, round_=round_,
+                                               request_ids=request_ids, ws=ws, group=group)
+        for t in out:
+            t.record_stream(now)
+        return out
     rank, world = dist.get_rank(group), dist.get_world_size(group)
     dt = _dt(target_local)
     B = temperature.numel()
-    dev = target_local.device
     cl, nc = sv_vocab_chunks(V, dt)
     ranges = chunk_ranges(nc, world)
     c0, c1 = ranges[rank]

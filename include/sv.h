@@ -512,7 +512,8 @@ sv_status sv_cache_release(const sv_cache* c, int32_t* page_table, int table_wid
  * [n_rows, q_heads].  q_heads a multiple of kv_heads, at most 128 times it.  Products of bf16 are summed in
  * float32; softmax weights are rounded to bf16 for the product with v, and o is divided by the sum of the rounded ones;
  * lse takes the sum before rounding.
- * The keys and values of visible slots must be finite; slots of other requests, past the tree or outside
+ * The keys and values of visible slots must be finite (a q row that is not, with NaN among its scores or nothing but -inf,
+ * has no softmax: its o is NaN); slots of other requests, past the tree or outside
  * every node's window may hold anything.  A request whose rows do not lie in [0, n_rows), with N_i
  * outside [0, Nmax] or L_i < 0 or L_i + N_i slots beyond its row (SV_DEV_BAD_NODES / SV_DEV_BAD_SEQ) or a visible slot without a page
  * (SV_DEV_BAD_PAGE) or a bad parent (SV_DEV_BAD_PARENT): outputs 0, lse -inf for its rows in [0, n_rows).

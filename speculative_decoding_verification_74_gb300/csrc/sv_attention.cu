@@ -842,10 +842,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           sumr += w * sm.lr[b][g][x];
         }
       const bool complete = s.kv0 == 0 && s.kv1 == s.r.tiles;
-      const float inv = complete && sumr > 0.0f ? 1.0f / sumr : 1.0f;
+      // Every row sees its own node's slot, so a sum that is not above 0 is that of a row without a softmax: NaN among its
+      // scores (which the maximum passes over), or nothing but -inf.  Its outputs are NaN; the parts' sums tell the join.
+      const float inv = !complete ? 1.0f : sumr > 0.0f ? 1.0f / sumr : NAN;
       // (a group without a tile in the segment has m = -inf: its O is not used, whatever it holds)
-      const float w0 = sm.m[b][0][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][0][r] - top) * inv;
-      const float w1 = sm.m[b][1][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][1][r] - top) * inv;
+      const float w0 = (sm.m[b][0][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][0][r] - top)) * inv;
+      const float w1 = (sm.m[b][1][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][1][r] - top)) * inv;
       const int head = ((kPair ? 2 * s.head + half : s.head) - local_node) * a.group + local;  // (of an existing row)
       float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (s.kv0 == 0)) * part_floats<D>();
       // four columns of this thread's row: to the output, or to this CTA's partial result
@@ -1020,7 +1022,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) join_kernel(const AttendPar
       o[2] += w * v.z;
       o[3] += w * v.w;
     }
-    const float inv = R > 0.0f ? 1.0f / R : 0.0f;
+    const float inv = R > 0.0f ? 1.0f / R : NAN;  // (not above 0: NaN among the row's scores, or nothing but -inf)
     const int node = job.mtile * a.tile_nodes + local / a.group, head = (heads * job.head + half) * a.group + local % a.group;
     const int64_t row = a.node_offsets[job.request] + node;
     uint2 w;

@@ -473,8 +473,8 @@ sv_status sv_cache_append(const sv_cache* c, int layer, int layers, const int32_
  * seq_len[i].  out_len[i] = seq_len[i] + 1 + a; a < 0 (a request that verification rejected as invalid) or N_i = 0 with
  * a <= 0 (no tree this round): seq_len[i].
  * Pages past ceil(out_len / page_size) leave the row.  out_len may be seq_len.  A bad path or length: nothing
- * moves, no page is given back, out_len[i] = seq_len[i], SV_DEV_BAD_SEQ; a slot without a page: SV_DEV_BAD_PAGE, that node
- * does not move.  Tail pages that another row shares stay with it.
+ * moves, no page is given back, out_len[i] = seq_len[i], SV_DEV_BAD_SEQ; a kept node (node 0 too) whose slot has no page:
+ * SV_DEV_BAD_PAGE, it does not move, and out_len counts it all the same.  Tail pages that another row shares stay with it.
  */
 sv_status sv_cache_commit(const sv_cache* c, int32_t* page_table, int table_width, const int32_t* seq_len,
                           const int32_t* node_offsets, const int32_t* path, const int32_t* accept_len, int B, int Nmax,

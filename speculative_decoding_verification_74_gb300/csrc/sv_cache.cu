@@ -451,6 +451,9 @@ __global__ void __launch_bounds__(kRowThreads) commit_kernel(CommitParams a) {
       moves[2 * j + 1] = to;
     }
   }
+  // node 0 stays, but in a slot that has a page
+  if (keep >= 0 && blockIdx.x == 0 && threadIdx.x == kRowThreads - 1 && slot_offset(a.r, row, a.width, len) < 0)
+    atomicOr(a.status, SV_DEV_BAD_PAGE);
   __syncthreads();
   const bool invalid = wrong || bad != 0;
   if (invalid && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, SV_DEV_BAD_SEQ);

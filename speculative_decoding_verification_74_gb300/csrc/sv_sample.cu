@@ -636,6 +636,12 @@ __device__ __forceinline__ float nucleus_bound(const Ask& ask, int V) {
   return each > 0.0f ? __fadd_rd(ask.top, __fdiv_rd(log2f(each) - 40.0f - 1e-3f, ask.steep)) : -INFINITY;
 }
 
+// Min-p: no logit below this one reaches the threshold.  An exponent is rounded twice (a part in 2^23), and one that
+// underflows to a multiple of 2^-149: at q = 1 all those that round to -0 reach 0.
+__device__ __forceinline__ float floor_bound(const Ask& ask) {
+  return __fadd_rd(ask.top, __fdiv_rd(__fmaf_rd(ask.least, 1.000001f, -0x1p-148f), ask.steep));
+}
+
 __device__ __forceinline__ Scale scale_of(const Ask& ask) {
   return Scale::over(ask.top, ask.bound == -INFINITY ? 64.0f / ask.steep : __fsub_rn(ask.top, ask.bound));
 }
@@ -1387,7 +1393,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, int64_t row, u
   }
   // Below min-p's threshold nothing is kept.  The boundary may then lie below the bound: it is not found, and everything
   // above the bound is kept.  Only the top-k's own weight needs all of the top-k.
-  if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(ask.least * 1.000001f, ask.steep)));
+  if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, floor_bound(ask));
   if (!(bound < top)) bound = bound >= top ? top : -INFINITY;  // (a NaN: no bound)
   ask.bound = bound;
   if (ask.nucleus && !ask.by_count) {  // top-p alone: its list may be long, which the counts tell for less than listing
@@ -1679,7 +1685,7 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) select_kernel(const Sam
     for (int i = 0; i < kWarps; ++i) ask.total += sh.seg[i];
     bound = nucleus_bound(ask, p.V);
   }
-  if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, __fadd_rd(top, __fdiv_rd(ask.least * 1.000001f, ask.steep)));
+  if (ask.floor_on && !(ask.by_count && ask.nucleus)) bound = fmaxf(bound, floor_bound(ask));
   if (!(bound < top)) bound = bound >= top ? top : -INFINITY;  // (a NaN: no bound)
   ask.bound = bound;
   ask.out_row = p.out_rows != nullptr ? static_cast<Elem*>(p.out_rows) + row * p.out_stride : nullptr;

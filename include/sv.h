@@ -398,7 +398,7 @@ sv_status sv_verify_sample_noalloc(const void* target, int64_t t_row_stride, con
  *     top-k's weights (p rounded to a multiple of 2^-24);  min-p: y_v >= log2(q)
  *   draw j: t = floor(u_j Z), Z the kept weights (u_j cut to a multiple of 2^-24); the first kept v
  *   in vocabulary order whose running sum of kept weights exceeds t
- * T == 0: the first argmax, probability 1, whatever the filters and uniforms.
+ * T == 0: the first argmax, probability 1, whatever the filters and uniforms are (they have to be in range all the same).
  * Outputs: out_tokens [R, M] int32; out_probs [R, M] float32 (nullable): w_v / Z;  out_rows
  * (nullable, dtype dt, row stride out_stride >= V; may equal logits with its stride): x_v where kept, else
  * -inf.  A row of nothing but -inf gives tokens -1 and probabilities 0.  A row with a NaN or +inf

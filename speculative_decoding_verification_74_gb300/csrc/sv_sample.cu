@@ -28,9 +28,10 @@
 //
 // Measured (GB300, 151936 logits a row; a copy of the same bytes takes 97.5 us for 1088 float32 rows): 1088 rows float32
 // plain 297 us, greedy 313 us, top-k 50 163 us (maxima 100, select 55), min-p alone 155 us, top-p 0.9 alone 720 us (peaked
-// rows) to 1230 us (flat ones); mixed filters with the cut rows written 377 us (maxima with the cut rows' -inf 200, 195
+// rows) to 1230 us (flat ones); mixed filters with the cut rows written 377 to 396 us (maxima with the cut rows' -inf 200, 195
 // being their copy's; select 80; clusters for the 50 rows with top-p alone 95).  64 rows bf16: plain 15 us, top-k 50 18
-// us, top-p alone 54 to 60 us, mixed 40 to 46 us.  Four rows of 32000: 6.3 us, the latency of one launch and its barriers.
+// us, top-p alone 54 to 60 us, mixed 39 to 63 us by the rows.  Four rows of 32000: 6.3 to 6.7 us, the latency of one launch
+// and its barriers.
 // What bounds it now: with few rows the chain of barriers and passes of the slowest row (a flat row under top-p alone
 // takes six passes over its slices and ten cluster barriers: 34 us by itself), with many the reading.
 #include <cuda_bf16.h>

@@ -90,7 +90,8 @@ enum {
   SV_DEV_BAD_PAGE = 1u << 11,       /* cache: a needed page_table entry names no page, or a page was given back too often */
   SV_DEV_OUT_OF_PAGES = 1u << 12,   /* cache: the pool has too few free pages        */
   SV_DEV_BAD_SEQ = 1u << 13,        /* cache: length, row number or path out of range */
-  SV_DEV_BAD_NODES = 1u << 14       /* attention / cache: node_offsets out of range  */
+  SV_DEV_BAD_NODES = 1u << 14,      /* attention / cache: node_offsets out of range  */
+  SV_DEV_BAD_VALUE = 1u << 15       /* 4-bit cache: a new key or value that is not finite */
 };
 
 /* per-request bits of out_flags */
@@ -376,6 +377,7 @@ sv_status sv_verify_sample_noalloc(const void* target, int64_t t_row_stride, con
  * Operators of the round around verification: drawing drafted tokens, a paged key/value cache
  * and the attention of a token tree over it.  ([release] "Why one universal drafter
  * underperforms": the drafter proposes, one target pass verifies; [explainer] "D-cut", Figure 3.)
+ * Beam search: sv_beam_select picks the beams, sv_cache_reorder moves the cache along.
  * A round: sv_cache_reserve, per layer sv_cache_append and sv_tree_attention, sv_verify_tree,
  * sv_cache_commit of the accepted path; the drafter's tokens come from sv_sample_rows.
  */
@@ -497,6 +499,63 @@ sv_status sv_cache_release(const sv_cache* c, int32_t* page_table, int table_wid
                            const int32_t* seqs, int n, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * sv_cache_reorder -- row j becomes a copy of row src[j] as it was (0 <= j < rows; rows = rows of page_table and seq_len):
+ * after a beam search step, beam j goes on from src[j] (sv_beam_select's out_rows).  src[j] = -1 empties row j.
+ * Several rows may name one row.  Full pages are shared.  Of the rows that name row p, row p itself, if it does, else the
+ * first one keeps p's partly filled last page and the pages that p holds past its length; each other one gets the lowest
+ * free page for it (rows in order), into which its used slots are copied in every layer.  Pages of rows that no row names
+ * are free before that.  All or nothing: with fewer free pages than copies (SV_DEV_OUT_OF_PAGES), an entry of src outside
+ * [-1, rows) or a named row's length outside its table row (SV_DEV_BAD_SEQ), or a named row that lacks a page
+ * for one of its slots (SV_DEV_BAD_PAGE), nothing changes and out_ok[0] = 0, else 1 (out_ok nullable).
+ */
+sv_status sv_cache_reorder(const sv_cache* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
+                           const int32_t* src, int32_t* out_ok, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A paged key/value cache held in 4 bits: 9 bits for two elements, against 32 in sv_cache.  Sixteen neighbouring dimensions
+ * of a token's key (or value) in one head share a scale s: with t = x g' (g' = 1 / k_scale or 1 / v_scale in float32, the
+ * product rounded to float32), s = max|t| * (1/6) (float32) rounded to e4m3, at most 448, and a code is t / s (float32)
+ * rounded to e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives; ties to the even code, at most 6), 0 where s = 0.  The
+ * element stands for code * s * k_scale (v_scale).  k_scale and v_scale bring a pool's values into e4m3's range: best
+ * results where max|t| of most groups lies in [2^-4, 2688].
+ * pool: layer l, page g, key/value head h begin at byte l * layer_stride + g * page_stride + h * head_stride (strides and
+ * base multiples of 16) and hold page_size / 8 groups of eight slots, 9 head_dim bytes each (D = head_dim):
+ *   4 D bytes  key codes: slot i's at i D / 2, dimension d in byte d / 2 (d even: low half)
+ *   D / 2      key scales: slot i's at i D / 16, dimension d's is byte d / 16
+ *   4 D        value codes: eighth e of the dimensions, pair p of slots at (4 e + p) D / 8: the even slot's D / 16 bytes,
+ *              then the odd slot's, each in dimension order as above
+ *   D / 2      value scales: dimension d of slot i at (d / 16) * 8 + i
+ * (the order in which sv_tree_attention4's tensor-core fragments read them).  page_table, page_refs, limits and workspace as
+ * in sv_cache.  The sv_cache4_* calls are those of sv_cache_* with the same name, and:
+ *   append takes bf16 rows and quantises them; one that is not finite reports SV_DEV_BAD_VALUE (its group's stored values
+ *     are finite, but otherwise unspecified);
+ *   fork and reorder copy the used slots of a partly filled page in whole groups of eight.
+ */
+typedef struct {
+  void* pool;
+  int64_t layer_stride, page_stride, head_stride;
+  int32_t layers, pages, page_size, kv_heads, head_dim;
+  int32_t* page_refs;
+  float k_scale, v_scale; /* finite and > 0, and so are their float32 reciprocals */
+} sv_cache4;
+sv_status sv_cache4_reserve(const sv_cache4* c, int32_t* page_table, int table_width, const int32_t* seq_len,
+                            const int32_t* extra, int B, int32_t* out_ok, void* ws, size_t ws_bytes, void* stream);
+sv_status sv_cache4_append(const sv_cache4* c, int layer, int layers, const int32_t* page_table, int table_width,
+                           const int32_t* seq_len, const int32_t* node_offsets, int64_t n_rows, const void* k_new,
+                           const void* v_new, int64_t new_layer_stride, int64_t new_row_stride, int B, void* ws,
+                           size_t ws_bytes, void* stream);
+sv_status sv_cache4_commit(const sv_cache4* c, int32_t* page_table, int table_width, const int32_t* seq_len,
+                           const int32_t* node_offsets, const int32_t* path, const int32_t* accept_len, int B, int Nmax,
+                           int32_t* out_len, void* ws, size_t ws_bytes, void* stream);
+sv_status sv_cache4_fork(const sv_cache4* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
+                         const int32_t* src, const int32_t* dst, int n, int32_t* out_ok, void* ws, size_t ws_bytes,
+                         void* stream);
+sv_status sv_cache4_release(const sv_cache4* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
+                            const int32_t* seqs, int n, void* ws, size_t ws_bytes, void* stream);
+sv_status sv_cache4_reorder(const sv_cache4* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
+                            const int32_t* src, int32_t* out_ok, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * sv_tree_attention -- attention of every request's token tree over its cached sequence, one layer.
  *
  * Request i has L_i = seq_len[i] cached slots and N_i = node_offsets[i+1] - node_offsets[i] nodes
@@ -525,6 +584,41 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
                             const int32_t* node_offsets, int64_t n_rows, const int32_t* parent, int B, int Nmax,
                             float scale, int window, int sinks, void* out, int64_t out_row_stride,
                             int64_t out_head_stride, float* out_lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * sv_tree_attention4 -- sv_tree_attention over a cache held in 4 bits: the same arguments, masks, errors and outputs, with the
+ * values that the pool's codes stand for as keys and values (they have at most six significant bits, and enter the products
+ * exactly).  Slots past a sequence's length, or outside every node's window, may hold anything, scales that are NaN included.
+ * Workspace: sv_attention4_workspace_size(c, q_heads), zero-filled once before its first use.
+ */
+size_t sv_attention4_workspace_size(const sv_cache4* c, int q_heads);
+sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                             int q_heads, const int32_t* page_table, int table_width, const int32_t* seq_len,
+                             const int32_t* node_offsets, int64_t n_rows, const int32_t* parent, int B, int Nmax,
+                             float scale, int window, int sinks, void* out, int64_t out_row_stride,
+                             int64_t out_head_stride, float* out_lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * sv_beam_select -- one step of beam search: the K best continuations of each request over its W beams and the vocabulary.
+ * Row i W + w of logits (V entries at logits + row * row_stride, dtype dt) belongs to beam w of request i (0 <= i < B), whose
+ * sum of log-probabilities so far is scores[i W + w].
+ *   total(w, v) = scores[w] + (x_wv - log sum_u exp x_wu);  a beam with finished[i W + w] != 0 (finished nullable) has one
+ *   candidate instead, the token `pad` at total = scores[w] (its logits are not looked at)
+ * Totals of -inf are no candidates.  Outputs, K per request, in the order (total desc, beam asc, token asc), as if in exact
+ * arithmetic but for totals that 64 bits cannot tell apart; within a beam the order is that of the logits:
+ * out_scores float32, out_rows int32 (i W + w, what sv_cache_reorder takes for K = W), out_tokens int32.  Places past the last
+ * candidate get -inf, -1, -1.  A NaN or +inf among the scores of a request, or the logits of a beam that is not finished and whose
+ * score is not -inf: the request's outputs are NaN, -1, -1 (SV_DEV_BAD_LOGIT).
+ * Limits: 0 <= B, 1 <= W <= SV_MAX_BEAMS, B W <= SV_MAX_BEAM_ROWS, 1 <= V <= SV_MAX_SAMPLE_VOCAB, 1 <= K <= SV_MAX_BEAM_CANDIDATES,
+ * 0 <= pad.  Workspace: sv_beam_workspace_size(B W, V, K), its first SV_STATUS_BYTES zero-filled before its first use.
+ */
+#define SV_MAX_BEAMS 64
+#define SV_MAX_BEAM_ROWS (1 << 16)
+#define SV_MAX_BEAM_CANDIDATES 128
+size_t sv_beam_workspace_size(int rows, int V, int K); /* 0 for invalid sizes */
+sv_status sv_beam_select(const void* logits, int64_t row_stride, sv_dtype dt, int B, int W, int V, const float* scores,
+                         const int32_t* finished, int pad, int K, float* out_scores, int32_t* out_rows,
+                         int32_t* out_tokens, void* ws, size_t ws_bytes, void* stream);
 
 /* Testing hook for the bounded waits.  The next verification call (any entry
  * point, on any thread) runs with every wait of its streaming kernel limited to
@@ -568,7 +662,9 @@ enum {
   SV_KERNEL_CACHE_ROWS = 8,  /* key/value rows written, moved or copied                   */
   SV_KERNEL_ATTENTION = 9,   /* tree attention: tiles of the cache                        */
   SV_KERNEL_ATTENTION_JOIN = 10, /* tree attention: partial results joined                */
-  SV_NUM_KERNEL_IDS = 11
+  SV_KERNEL_BEAM = 11,       /* sv_beam_select: the pass over the logits                  */
+  SV_KERNEL_BEAM_MERGE = 12, /* sv_beam_select: the beams' candidates merged              */
+  SV_NUM_KERNEL_IDS = 13
 };
 void sv_profile_enable(int on);
 sv_status sv_profile_collect(double* total_ms, int64_t* launches);

@@ -82,6 +82,41 @@ class Cache:
             ok.append(1)
         return np.asarray(ok)
 
+    def reorder(self, lens, src):
+        """Rows become copies of rows src; 1 if that could be done."""
+        R, old, before = len(src), self.table.copy(), lens.copy()
+        refs = self.refs.copy()
+        for j in range(R):
+            if j not in list(src):
+                for e in range(self.table.shape[1]):
+                    if old[j, e] >= 0:
+                        refs[old[j, e]] -= 1
+        free, copies = [g for g in range(len(refs)) if refs[g] == 0], []
+        rows = np.full_like(old, -1)
+        for j, s in enumerate(src):
+            if s < 0:
+                continue
+            keeper = s if src[s] == s else list(src).index(s)
+            if j == keeper:
+                rows[j] = old[s]
+                continue
+            full, part = before[s] // self.ps, before[s] % self.ps
+            rows[j, :full] = old[s, :full]
+            for e in range(full):
+                refs[old[s, e]] += 1
+            if part:
+                if not free:
+                    return 0
+                rows[j, full] = free.pop(0)
+                refs[rows[j, full]] = 1
+                copies.append((rows[j, full], old[s, full], part))
+        for to, of, part in copies:
+            self.k[:, to, :part] = self.k[:, of, :part]
+            self.v[:, to, :part] = self.v[:, of, :part]
+        self.table[:], self.refs[:] = rows, refs
+        lens[:] = [before[s] if s >= 0 else 0 for s in src]
+        return 1
+
     def release(self, lens, seqs):
         for i in seqs:
             self._drop(i, 0)

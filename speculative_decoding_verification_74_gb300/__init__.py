@@ -8,12 +8,13 @@ every call raises.
 
 The ``sv_*`` functions mirror the C ABI in ``include/sv.h`` one to one (tensors in place of
 pointers, ``None`` for NULL).  The lower-case helpers (``verify_greedy``, ``verify_sample``,
-``verify_ragged``, ``verify_tree``, ``schedule_depth``, ``sample``, ``tree_attention``) and ``PagedCache``
-derive sizes and strides from the tensors and allocate outputs and workspaces.
+``verify_ragged``, ``verify_tree``, ``schedule_depth``, ``sample``, ``tree_attention``, ``beam_select``) and
+``PagedCache`` / ``PagedCache4`` derive sizes and strides from the tensors and allocate outputs and workspaces.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -30,7 +31,7 @@ SV_OBJ_THROUGHPUT, SV_OBJ_NET = 0, 1
 SV_PHASE_STATS, SV_PHASE_ACCEPT, SV_PHASE_WEIGHTS, SV_PHASE_PICK = range(4)
 (SV_DEV_BAD_TOKEN, SV_DEV_BAD_TEMPERATURE, SV_DEV_BAD_KEEP_LEN, SV_DEV_BAD_OFFSETS, SV_DEV_NO_DRAFT_ROWS,
  SV_DEV_BAD_ALPHA, SV_DEV_BAD_DRAFT_LEN, SV_DEV_TIMEOUT, SV_DEV_BAD_PARENT, SV_DEV_BAD_LOGIT, SV_DEV_BAD_FILTER,
- SV_DEV_BAD_PAGE, SV_DEV_OUT_OF_PAGES, SV_DEV_BAD_SEQ, SV_DEV_BAD_NODES) = (1 << b for b in range(15))
+ SV_DEV_BAD_PAGE, SV_DEV_OUT_OF_PAGES, SV_DEV_BAD_SEQ, SV_DEV_BAD_NODES, SV_DEV_BAD_VALUE) = (1 << b for b in range(16))
 SV_STATUS_BYTES, SV_MAX_BATCH = 256, 4096
 SV_CACHE_WORKSPACE_BYTES = SV_STATUS_BYTES + 8 * SV_MAX_BATCH
 SV_FLAG_Q_ZERO, SV_FLAG_Z_ZERO, SV_FLAG_INVALID = 1, 2, 4
@@ -39,8 +40,9 @@ SV_FLAG_Q_ZERO, SV_FLAG_Z_ZERO, SV_FLAG_INVALID = 1, 2, 4
 KERNEL_NAMES = ("row_stats", "combine", "schedule", "mass", "pick", "tree_walk")
 # kernels of the round's other operators (sv_profile_collect_ids reports them too)
 (SV_KERNEL_SAMPLE, SV_KERNEL_CACHE_PAGES, SV_KERNEL_CACHE_ROWS, SV_KERNEL_ATTENTION, SV_KERNEL_ATTENTION_JOIN,
- SV_NUM_KERNEL_IDS) = range(6, 12)
-OPERATOR_KERNEL_NAMES = KERNEL_NAMES + ("sample", "cache_pages", "cache_rows", "attention", "attention_join")
+ SV_KERNEL_BEAM, SV_KERNEL_BEAM_MERGE, SV_NUM_KERNEL_IDS) = range(6, 14)
+OPERATOR_KERNEL_NAMES = KERNEL_NAMES + ("sample", "cache_pages", "cache_rows", "attention", "attention_join", "beam",
+                                         "beam_merge")
 
 _c = ctypes
 _vp, _i32, _i64, _u32, _u64, _f32, _sz = (_c.c_void_p, _c.c_int32, _c.c_int64, _c.c_uint32, _c.c_uint64,
@@ -80,9 +82,14 @@ _SIGS = {
     "sv_cache_commit": (_c.c_int, [_vp, _vp, _c.c_int, _vp, _vp, _vp, _vp, _c.c_int, _c.c_int, _vp, _vp, _sz, _vp]),
     "sv_cache_fork": (_c.c_int, [_vp, _vp, _c.c_int, _c.c_int, _vp, _vp, _vp, _c.c_int, _vp, _vp, _sz, _vp]),
     "sv_cache_release": (_c.c_int, [_vp, _vp, _c.c_int, _c.c_int, _vp, _vp, _c.c_int, _vp, _sz, _vp]),
+    "sv_cache_reorder": (_c.c_int, [_vp, _vp, _c.c_int, _c.c_int, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sv_beam_workspace_size": (_sz, [_c.c_int, _c.c_int, _c.c_int]),
+    "sv_beam_select": (_c.c_int, [_vp, _i64, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _vp, _vp, _c.c_int, _c.c_int, _vp, _vp,
+                                  _vp, _vp, _sz, _vp]),
     "sv_attention_workspace_size": (_sz, [_vp, _c.c_int]),
     "sv_tree_attention": (_c.c_int, [_vp, _c.c_int, _vp, _i64, _i64, _c.c_int, _vp, _c.c_int, _vp, _vp, _i64, _vp, _c.c_int,
                                      _c.c_int, _f32, _c.c_int, _c.c_int, _vp, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "sv_attention4_workspace_size": (_sz, [_vp, _c.c_int]),
     "sv_test_stall_next_verify": (None, [_c.c_int]),
     "sv_query_status": (_c.c_int, [_vp, _vp, _c.POINTER(_u32)]),
     "sv_status_string": (_c.c_char_p, [_c.c_int]),
@@ -94,6 +101,11 @@ _SIGS = {
     "sv_launch_count": (_i64, []),
 }
 
+# the same calls on a cache held in 4 bits
+for _name in ("reserve", "append", "commit", "fork", "release", "reorder"):
+    _SIGS["sv_cache4_" + _name] = _SIGS["sv_cache_" + _name]
+_SIGS["sv_tree_attention4"] = _SIGS["sv_tree_attention"]
+
 _lib = None
 
 
@@ -102,6 +114,13 @@ class sv_cache(_c.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("layer_stride", _i64), ("page_stride", _i64), ("slot_stride", _i64),
                 ("head_stride", _i64), ("layers", _i32), ("pages", _i32), ("page_size", _i32), ("kv_heads", _i32),
                 ("head_dim", _i32), ("page_refs", _vp)]
+
+
+class sv_cache4(_c.Structure):
+    """The C struct of the same name: a paged key/value cache held in 4 bits (see include/sv.h)."""
+    _fields_ = [("pool", _vp), ("layer_stride", _i64), ("page_stride", _i64), ("head_stride", _i64), ("layers", _i32),
+                ("pages", _i32), ("page_size", _i32), ("kv_heads", _i32), ("head_dim", _i32), ("page_refs", _vp),
+                ("k_scale", _f32), ("v_scale", _f32)]
 
 
 class SVError(RuntimeError):
@@ -418,52 +437,89 @@ def _need_table(page_table, table_width: int, rows: int, **per_row) -> None:
         _need(t, name, torch.int32, rows)
 
 
-def sv_cache_reserve(cache, page_table, table_width, seq_len, extra, B, out_ok, ws, stream=None) -> None:
+def sv_cache_reserve(cache, page_table, table_width, seq_len, extra, B, out_ok, ws, stream=None, _f="sv_cache_reserve") -> None:
     if B > 0:
         _need_table(page_table, table_width, B, seq_len=seq_len, extra=extra, out_ok=out_ok)
-    _check(lib().sv_cache_reserve(_c.addressof(cache), _p(page_table), table_width, _p(seq_len), _p(extra), B, _p(out_ok),
+    _check(getattr(lib(), _f)(_c.addressof(cache), _p(page_table), table_width, _p(seq_len), _p(extra), B, _p(out_ok),
                                   _p(ws), _ws_bytes(ws), _stream(stream)))
 
 
 def sv_cache_append(cache, layer, layers, page_table, table_width, seq_len, node_offsets, n_rows, k_new, v_new,
-                    new_layer_stride, new_row_stride, B, ws, stream=None) -> None:
+                    new_layer_stride, new_row_stride, B, ws, stream=None, _f="sv_cache_append") -> None:
     if B > 0 and layers > 0 and n_rows > 0:
         _need_table(page_table, table_width, B, seq_len=seq_len)
         _need(node_offsets, "node_offsets", torch.int32, B + 1)
         last = (layers - 1) * new_layer_stride + (n_rows - 1) * new_row_stride + cache.kv_heads * cache.head_dim
         _need(k_new, "k_new", torch.bfloat16, last)
         _need(v_new, "v_new", torch.bfloat16, last)
-    _check(lib().sv_cache_append(_c.addressof(cache), layer, layers, _p(page_table), table_width, _p(seq_len),
+    _check(getattr(lib(), _f)(_c.addressof(cache), layer, layers, _p(page_table), table_width, _p(seq_len),
                                  _p(node_offsets), n_rows, _p(k_new), _p(v_new), new_layer_stride, new_row_stride, B,
                                  _p(ws), _ws_bytes(ws), _stream(stream)))
 
 
 def sv_cache_commit(cache, page_table, table_width, seq_len, node_offsets, path, accept_len, B, Nmax, out_len, ws,
-                    stream=None) -> None:
+                    stream=None, _f="sv_cache_commit") -> None:
     if B > 0:
         _need_table(page_table, table_width, B, seq_len=seq_len, accept_len=accept_len, out_len=out_len)
         _need(node_offsets, "node_offsets", torch.int32, B + 1)
         _need(path, "path", torch.int32, B * Nmax)
-    _check(lib().sv_cache_commit(_c.addressof(cache), _p(page_table), table_width, _p(seq_len), _p(node_offsets), _p(path),
+    _check(getattr(lib(), _f)(_c.addressof(cache), _p(page_table), table_width, _p(seq_len), _p(node_offsets), _p(path),
                                  _p(accept_len), B, Nmax, _p(out_len), _p(ws), _ws_bytes(ws), _stream(stream)))
 
 
-def sv_cache_fork(cache, page_table, table_width, rows, seq_len, src, dst, n, out_ok, ws, stream=None) -> None:
+def sv_cache_fork(cache, page_table, table_width, rows, seq_len, src, dst, n, out_ok, ws, stream=None, _f="sv_cache_fork") -> None:
     if n > 0:
         _need_table(page_table, table_width, rows, seq_len=seq_len)
         _need(src, "src", torch.int32, n)
         _need(dst, "dst", torch.int32, n)
         _need(out_ok, "out_ok", torch.int32, n)
-    _check(lib().sv_cache_fork(_c.addressof(cache), _p(page_table), table_width, rows, _p(seq_len), _p(src), _p(dst), n,
+    _check(getattr(lib(), _f)(_c.addressof(cache), _p(page_table), table_width, rows, _p(seq_len), _p(src), _p(dst), n,
                                _p(out_ok), _p(ws), _ws_bytes(ws), _stream(stream)))
 
 
-def sv_cache_release(cache, page_table, table_width, rows, seq_len, seqs, n, ws, stream=None) -> None:
+def sv_cache_release(cache, page_table, table_width, rows, seq_len, seqs, n, ws, stream=None, _f="sv_cache_release") -> None:
     if n > 0:
         _need_table(page_table, table_width, rows, seq_len=seq_len)
         _need(seqs, "seqs", torch.int32, n)
-    _check(lib().sv_cache_release(_c.addressof(cache), _p(page_table), table_width, rows, _p(seq_len), _p(seqs), n, _p(ws),
+    _check(getattr(lib(), _f)(_c.addressof(cache), _p(page_table), table_width, rows, _p(seq_len), _p(seqs), n, _p(ws),
                                   _ws_bytes(ws), _stream(stream)))
+
+
+def sv_cache_reorder(cache, page_table, table_width, rows, seq_len, src, out_ok, ws, stream=None, _f="sv_cache_reorder") -> None:
+    if rows > 0:
+        _need_table(page_table, table_width, rows, seq_len=seq_len, src=src)
+        _need(out_ok, "out_ok", torch.int32, 1)
+    _check(getattr(lib(), _f)(_c.addressof(cache), _p(page_table), table_width, rows, _p(seq_len), _p(src), _p(out_ok), _p(ws),
+                              _ws_bytes(ws), _stream(stream)))
+
+
+sv_cache4_reserve = functools.partial(sv_cache_reserve, _f="sv_cache4_reserve")
+sv_cache4_append = functools.partial(sv_cache_append, _f="sv_cache4_append")
+sv_cache4_commit = functools.partial(sv_cache_commit, _f="sv_cache4_commit")
+sv_cache4_fork = functools.partial(sv_cache_fork, _f="sv_cache4_fork")
+sv_cache4_release = functools.partial(sv_cache_release, _f="sv_cache4_release")
+sv_cache4_reorder = functools.partial(sv_cache_reorder, _f="sv_cache4_reorder")
+
+
+def sv_beam_workspace_size(rows: int, V: int, K: int) -> int:
+    return int(lib().sv_beam_workspace_size(rows, V, K))
+
+
+def sv_beam_select(logits, row_stride, dt, B, W, V, scores, finished, pad, K, out_scores, out_rows, out_tokens, ws,
+                   stream=None) -> None:
+    if B > 0 and W > 0 and K > 0:
+        _need_rows(logits, "logits", dt, B * W, row_stride, V)
+        _need(scores, "scores", torch.float32, B * W)
+        _need(finished, "finished", torch.int32, B * W)
+        _need(out_scores, "out_scores", torch.float32, B * K)
+        _need(out_rows, "out_rows", torch.int32, B * K)
+        _need(out_tokens, "out_tokens", torch.int32, B * K)
+    _check(lib().sv_beam_select(_p(logits), row_stride, dt, B, W, V, _p(scores), _p(finished), pad, K, _p(out_scores),
+                                _p(out_rows), _p(out_tokens), _p(ws), _ws_bytes(ws), _stream(stream)))
+
+
+def sv_attention4_workspace_size(cache, q_heads: int) -> int:
+    return int(lib().sv_attention4_workspace_size(_c.addressof(cache), q_heads))
 
 
 def sv_attention_workspace_size(cache, q_heads: int) -> int:
@@ -472,7 +528,7 @@ def sv_attention_workspace_size(cache, q_heads: int) -> int:
 
 def sv_tree_attention(cache, layer, q, q_row_stride, q_head_stride, q_heads, page_table, table_width, seq_len,
                       node_offsets, n_rows, parent, B, Nmax, scale, window, sinks, out, out_row_stride,
-                      out_head_stride, out_lse, ws, stream=None) -> None:
+                      out_head_stride, out_lse, ws, stream=None, _f="sv_tree_attention") -> None:
     if B > 0 and n_rows > 0:
         _need_table(page_table, table_width, B, seq_len=seq_len)
         _need(node_offsets, "node_offsets", torch.int32, B + 1)
@@ -480,10 +536,13 @@ def sv_tree_attention(cache, layer, q, q_row_stride, q_head_stride, q_heads, pag
         _need(q, "q", torch.bfloat16, (n_rows - 1) * q_row_stride + (q_heads - 1) * q_head_stride + cache.head_dim)
         _need(out, "out", torch.bfloat16, (n_rows - 1) * out_row_stride + (q_heads - 1) * out_head_stride + cache.head_dim)
         _need(out_lse, "out_lse", torch.float32, n_rows * q_heads)
-    _check(lib().sv_tree_attention(_c.addressof(cache), layer, _p(q), q_row_stride, q_head_stride, q_heads,
+    _check(getattr(lib(), _f)(_c.addressof(cache), layer, _p(q), q_row_stride, q_head_stride, q_heads,
                                    _p(page_table), table_width, _p(seq_len), _p(node_offsets), n_rows, _p(parent), B,
                                    Nmax, scale, window, sinks, _p(out), out_row_stride, out_head_stride, _p(out_lse),
                                    _p(ws), _ws_bytes(ws), _stream(stream)))
+
+
+sv_tree_attention4 = functools.partial(sv_tree_attention, _f="sv_tree_attention4")
 
 
 def sv_test_stall_next_verify(wait_limit_ms: int) -> None:
@@ -763,6 +822,10 @@ class PagedCache:
     from their arguments.  Everything stays on the device and on `stream`; errors that only the device sees go
     to the status word of `ws` (sv_query_status(cache.ws)).  One cache belongs to one stream at a time.
     """
+    _calls = "sv_cache_"
+
+    def _call(self, name):
+        return getattr(_lib or lib(), self._calls + name)
 
     def __init__(self, k, v, page_refs, page_table, ws=None):
         if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
@@ -772,16 +835,20 @@ class PagedCache:
             raise ValueError("the head dimension must be contiguous")
         if page_table.dim() != 2:
             raise ValueError("page_table must be [sequences, entries]")
-        self.k, self.v, self.page_refs, self.page_table = k, v, page_refs, page_table
-        self.rows, self.width = page_table.shape
+        self.k, self.v = k, v
         L, P, S, H, D = k.shape
         # a dimension of size 1 is never stepped along: its stride only has to be a valid one
         st = [k.stride(i) if k.shape[i] > 1 else max(8, D) for i in range(4)]
-        self.kv_heads, self.head_dim = H, D
         self.c = sv_cache(k=_p(k), v=_p(v), layer_stride=st[0], page_stride=st[1], slot_stride=st[2], head_stride=st[3],
                           layers=L, pages=P, page_size=S, kv_heads=H, head_dim=D,
                           page_refs=_array(page_refs, "page_refs", torch.int32, P))
-        self.ws = torch.zeros(SV_CACHE_WORKSPACE_BYTES, dtype=torch.uint8, device=k.device) if ws is None else ws
+        self._keep(k.device, H, D, page_refs, page_table, ws)
+
+    def _keep(self, device, kv_heads, head_dim, page_refs, page_table, ws):
+        self.device, self.kv_heads, self.head_dim = device, kv_heads, head_dim
+        self.page_refs, self.page_table = page_refs, page_table
+        self.rows, self.width = page_table.shape
+        self.ws = torch.zeros(SV_CACHE_WORKSPACE_BYTES, dtype=torch.uint8, device=device) if ws is None else ws
         # what every call passes: the struct, the table, the workspace
         self._c = _c.addressof(self.c)
         self._table = _array(page_table, "page_table", torch.int32, self.rows * self.width)
@@ -808,7 +875,7 @@ class PagedCache:
         i32 = torch.int32
         if ok is None:
             ok = _empty(B, i32, extra.device, stream)
-        _check((_lib or lib()).sv_cache_reserve(
+        _check(self._call("reserve")(
             self._c, self._table, self.width, _array(seq_len, "seq_len", i32, B), _array(extra, "extra", i32, B), B,
             _array(ok, "ok", i32, B), self._ws, self._ws_bytes, _stream(stream)))
         return ok
@@ -828,7 +895,7 @@ class PagedCache:
             raise ValueError("k_new and v_new must be torch.bfloat16")
         B = self._batch(node_offsets.numel() - 1)
         i32 = torch.int32
-        _check((_lib or lib()).sv_cache_append(
+        _check(self._call("append")(
             self._c, layer, L, self._table, self.width, _array(seq_len, "seq_len", i32, B),
             _array(node_offsets, "node_offsets", i32, B + 1), n, _p(k_new), _p(v_new), st[0] if L > 1 else 0,
             st[1] if n > 1 else H * D, B, self._ws, self._ws_bytes, _stream(stream)))
@@ -843,7 +910,7 @@ class PagedCache:
         i32 = torch.int32
         if out_len is None:
             out_len = _empty(B, i32, path.device, stream)
-        _check((_lib or lib()).sv_cache_commit(
+        _check(self._call("commit")(
             self._c, self._table, self.width, _array(seq_len, "seq_len", i32, B),
             _array(node_offsets, "node_offsets", i32, B + 1), _array(path, "path", i32, B * Nmax),
             _array(accept_len, "accept_len", i32, B), B, Nmax, _array(out_len, "out_len", i32, B), self._ws, self._ws_bytes,
@@ -856,7 +923,7 @@ class PagedCache:
         i32 = torch.int32
         if ok is None:
             ok = _empty(n, i32, src.device, stream)
-        _check((_lib or lib()).sv_cache_fork(
+        _check(self._call("fork")(
             self._c, self._table, self.width, self.rows, _array(seq_len, "seq_len", i32, self.rows),
             _array(src, "src", i32, n), _array(dst, "dst", i32, n), n, _array(ok, "ok", i32, n), self._ws, self._ws_bytes,
             _stream(stream)))
@@ -866,18 +933,106 @@ class PagedCache:
         """Gives the pages of rows seqs back and empties them (seq_len = 0)."""
         n = seqs.numel()
         i32 = torch.int32
-        _check((_lib or lib()).sv_cache_release(
+        _check(self._call("release")(
             self._c, self._table, self.width, self.rows, _array(seq_len, "seq_len", i32, self.rows),
             _array(seqs, "seqs", i32, n), n, self._ws, self._ws_bytes, _stream(stream)))
+
+    def reorder(self, seq_len, src, *, ok=None, stream=None):
+        """Every row j of the table becomes a copy of row src[j] as it was (src [rows] int32, -1 = empty), as a beam search
+        step asks for: full pages are shared, partly filled ones copied for all but one of the rows that name the same
+        source; seq_len follows.  Returns ok [1] int32: 0 where nothing was changed (too few free pages, a bad src)."""
+        i32 = torch.int32
+        if src.numel() != self.rows:
+            raise ValueError(f"src must name a row for each of the page table's {self.rows}")
+        if ok is None:
+            ok = _empty(1, i32, src.device, stream)
+        _check(self._call("reorder")(
+            self._c, self._table, self.width, self.rows, _array(seq_len, "seq_len", i32, self.rows),
+            _array(src, "src", i32, self.rows), _array(ok, "ok", i32, 1), self._ws, self._ws_bytes, _stream(stream)))
+        return ok
+
+
+class PagedCache4(PagedCache):
+    """A paged key/value cache held in 4 bits (the C struct sv_cache4): sixteen dimensions share an e4m3 scale, every element is
+    an e2m1 code, 9 bits for two elements.  The methods are PagedCache's; append quantises.
+
+    pool        [layers, pages, kv_heads, page_size * 9 * head_dim / 8] uint8, the last dimension contiguous, its
+                layout as in include/sv.h
+    page_refs, page_table   as in PagedCache
+    k_scale, v_scale        what the stored keys and values are multiplied by: new ones are divided by it before they
+                            are rounded, so that their sixteens' largest values fit e4m3's range (best in [2^-4, 2688])
+    """
+    _calls = "sv_cache4_"
+
+    def __init__(self, pool, page_refs, page_table, page_size, head_dim, *, k_scale=1.0, v_scale=1.0, ws=None):
+        if pool.dim() != 4 or pool.shape[3] != page_size * 9 * head_dim // 8:
+            raise ValueError("pool must be [layers, pages, kv_heads, page_size * 9 * head_dim / 8]")
+        _need(pool, "pool", torch.uint8)
+        if pool.stride(3) != 1:
+            raise ValueError("a head's page must be contiguous")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [sequences, entries]")
+        self.pool, self.k_scale, self.v_scale, self.page_size = pool, k_scale, v_scale, page_size
+        L, P, H, n = pool.shape
+        # a dimension of size 1 is never stepped along: its stride only has to be a valid one
+        st = [pool.stride(i) if pool.shape[i] > 1 else n for i in range(3)]
+        self.c = sv_cache4(pool=_p(pool), layer_stride=st[0], page_stride=st[1], head_stride=st[2], layers=L, pages=P,
+                           page_size=page_size, kv_heads=H, head_dim=head_dim,
+                           page_refs=_array(page_refs, "page_refs", torch.int32, P), k_scale=k_scale, v_scale=v_scale)
+        self._keep(pool.device, H, head_dim, page_refs, page_table, ws)
+
+    @classmethod
+    def empty(cls, layers, pages, page_size, kv_heads, head_dim, sequences, entries, device="cuda", *, k_scale=1.0, v_scale=1.0):
+        """A cache of free pages and empty sequences."""
+        return cls(torch.zeros((layers, pages, kv_heads, page_size * 9 * head_dim // 8), dtype=torch.uint8, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device),
+                   torch.full((sequences, entries), -1, dtype=torch.int32, device=device), page_size, head_dim,
+                   k_scale=k_scale, v_scale=v_scale)
+
+
+def beam_workspace(rows: int, vocab: int, candidates: int, device="cuda") -> torch.Tensor:
+    """Workspace of beam_select() for that many rows of logits (its first word is the device status word)."""
+    n = sv_beam_workspace_size(rows, vocab, candidates)
+    if n == 0:
+        raise ValueError("invalid sizes for sv_beam_workspace_size")
+    return _workspace(n, device)
+
+
+def beam_select(logits, scores, candidates, *, finished=None, pad=0, out=None, ws=None, stream=None):
+    """One step of beam search: the `candidates` best continuations of each request over its beams and the vocabulary.
+    logits [requests * beams, V] (bf16 or float32; rows may be strided); scores [requests, beams] float32, the beams' sums of
+    log-probabilities (-inf: no beam); finished [requests, beams] int32 or None: a finished beam stays as it is, with the token
+    `pad`.  Returns (scores [requests, candidates] float32, rows [requests, candidates] int32: the row of logits that a
+    candidate goes on from, tokens [requests, candidates] int32), best first; places without a candidate hold -inf, -1, -1.
+    With candidates = beams, rows.flatten() is what PagedCache.reorder takes.  out = (scores, rows, tokens) takes the place of
+    new tensors."""
+    if logits.dim() != 2 or scores.dim() != 2 or scores.numel() != logits.shape[0]:
+        raise ValueError("beam_select() takes logits [requests * beams, V] and scores [requests, beams]")
+    B, W = scores.shape
+    V, K, dev = logits.shape[1], candidates, logits.device
+    if finished is not None and finished.shape != scores.shape:
+        raise ValueError("finished must have the shape of scores")
+    f32, i32 = torch.float32, torch.int32
+    dt = _dt(logits)
+    if out is None:
+        out = (_empty((B, K), f32, dev, stream), _empty((B, K), i32, dev, stream), _empty((B, K), i32, dev, stream))
+    if ws is None:
+        ws = _workspace(sv_beam_workspace_size(B * W, V, K), dev, stream)
+    n = B * K
+    _check((_lib or lib()).sv_beam_select(
+        _p(logits), _row_stride(logits), dt, B, W, V, _array(scores, "scores", f32, B * W),
+        _array(finished, "finished", i32, B * W), pad, K, _array(out[0], "scores", f32, n), _array(out[1], "rows", i32, n),
+        _array(out[2], "tokens", i32, n), _p(ws), _ws_bytes(ws), _stream(stream)))
+    return out
 
 
 def attention_workspace(cache: PagedCache, q_heads: int) -> torch.Tensor:
     """Workspace of tree_attention() on this cache (its first word is the device status word)."""
-    return _workspace(attention_workspace_size(cache, q_heads), cache.k.device, zeros=True)
+    return _workspace(attention_workspace_size(cache, q_heads), cache.device, zeros=True)
 
 
 def attention_workspace_size(cache: PagedCache, q_heads: int) -> int:
-    n = sv_attention_workspace_size(cache.c, q_heads)
+    n = (sv_attention4_workspace_size if isinstance(cache, PagedCache4) else sv_attention_workspace_size)(cache.c, q_heads)
     if n == 0:
         raise ValueError(lib().sv_last_error_string().decode() or "invalid sizes for sv_attention_workspace_size")
     return n
@@ -886,7 +1041,7 @@ def attention_workspace_size(cache: PagedCache, q_heads: int) -> int:
 def tree_attention(q, cache: PagedCache, layer, seq_len, node_offsets, parent, Nmax, *, scale=None, window=0, sinks=0,
                    out=None, lse=True, ws=None, stream=None):
     """Attention of every request's token tree over its cached sequence in one layer.  q [rows, q_heads, head_dim]
-    bf16, row node_offsets[i] + c for node c of request i, whose keys and values are in the cache at slot seq_len[i] +
+    bf16 on a PagedCache or a PagedCache4, row node_offsets[i] + c for node c of request i, whose keys and values are in the cache at slot seq_len[i] +
     c (cache.append); parent [rows] int32 as in verify_tree, or None for chains; at most Nmax nodes a request.  window,
     sinks: a sliding window of that many positions and the first positions that stay visible.  Returns (out like q,
     lse [rows, q_heads] float32, or None with lse=False)."""
@@ -911,7 +1066,8 @@ def tree_attention(q, cache: PagedCache, layer, seq_len, node_offsets, parent, N
         raise ValueError("the head dimension of q and out must be contiguous")
     B = cache._batch(node_offsets.numel() - 1)
     # a dimension of size 1 is never stepped along: its stride only has to be a valid one
-    _check((_lib or lib()).sv_tree_attention(
+    call = _lib or lib()
+    _check((call.sv_tree_attention4 if isinstance(cache, PagedCache4) else call.sv_tree_attention)(
         cache._c, layer, _p(q), qs[0] if n > 1 else H * D, qs[1] if H > 1 else D, H, cache._table, cache.width,
         _array(seq_len, "seq_len", i32, B), _array(node_offsets, "node_offsets", i32, B + 1), n,
         _array(parent, "parent", i32, n), B, Nmax, D ** -0.5 if scale is None else scale, window, sinks, _p(out),

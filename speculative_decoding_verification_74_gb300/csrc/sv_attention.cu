@@ -46,12 +46,12 @@
 #include <type_traits>
 
 #include "sv_device.cuh"
+#include "sv_line.cuh"
 #include "sv_ops.h"
 
 namespace sv {
 namespace {
 
-constexpr int kTile = 128;                 // rows of Q, and slots of the cache, in a tile
 constexpr int kGroupThreads = 128;
 constexpr int kSoftThreads = 2 * kGroupThreads;
 constexpr int kThreads = 128 + kSoftThreads;
@@ -74,31 +74,12 @@ constexpr int kJoinRows = 16;              // rows per CTA of the join
 constexpr int kExtra = 3;
 constexpr int kMixFloat4 = 768;            // (a fifth stage still fits)
 constexpr int kMaxStages = 12;
-constexpr int kMaxCtas = 152;              // SMs of the GPU: one CTA each
-constexpr int kSmemMax = 232448;           // shared memory that a CTA can have
-
-struct alignas(16) Job {  // a row tile that several CTAs worked on: parts of CTAs `first` to `last`
-  int32_t valid, request, head, mtile, rows, first, last, pad;
-};
-
-struct Line {  // what the line of work follows from
-  const int32_t *seq_len, *node_offsets;
-  int64_t n_rows;
-  int32_t B, Nmax, width, shift, window, sinks;
-  int32_t tile_nodes;  // nodes of a row tile
-  int32_t extra;       // places before a row tile's cache tiles
-};
-struct AttendParams : Line {
-  int64_t out_row_stride, out_head_stride;
+struct AttendParams : Line, Marks, Outputs {
   const int32_t *table, *parent;
-  __nv_bfloat16* out;
-  float* lse;
-  uint32_t* status;
-  int32_t* any_bad;   // [2]: some request is bad; CTAs of the join that are done with that
-  uint8_t* bad;       // [SV_MAX_BATCH] requests whose outputs become 0
   Job* jobs;          // [grid]
   float* parts;       // [2 grid] partial results
-  int32_t pages, q_heads, kv_heads, group;
+  int32_t pages, kv_heads;
+  int32_t tile_nodes;  // nodes of a row tile
   int32_t units;       // key/value heads, or pairs of them
   int32_t half_rows;   // rows of a copy that one head takes
   uint32_t over_group; // ceil(2^16 / group)
@@ -219,92 +200,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// ---- the line of work ------------------------------------------------------------------------------
-// A request's part: its cache tiles are [0, sink_tiles) and [near_tile, ...).
-struct Request {
-  int64_t first;       // its first query row
-  int32_t len, nodes;
-  int32_t sink_tiles, near_tile, tiles;  // tiles = cache tiles that some node sees
-  int32_t mtiles;      // row tiles per key/value head
-  uint32_t bad;        // SV_DEV_* bits
-};
-__device__ __forceinline__ Request request_of(const Line& a, int i) {
-  Request r = {};
-  const int64_t first = a.node_offsets[i], last = a.node_offsets[i + 1];
-  const int64_t len = a.seq_len[i], nodes = last - first;
-  r.first = first;
-  if (first < 0 || nodes < 0 || nodes > a.Nmax || last > a.n_rows) {
-    r.bad = SV_DEV_BAD_NODES;
-    return r;
-  }
-  if (nodes == 0) return r;
-  if (len < 0 || len + nodes > (static_cast<int64_t>(a.width) << a.shift)) {
-    r.bad = SV_DEV_BAD_SEQ;
-    return r;
-  }
-  r.len = static_cast<int32_t>(len);
-  r.nodes = static_cast<int32_t>(nodes);
-  const int all = static_cast<int>((len + nodes + kTile - 1) / kTile);
-  if (a.window > 0) {
-    const int lo = max(0, r.len - a.window + 1);
-    r.near_tile = lo / kTile;
-    r.sink_tiles = min(static_cast<int>((static_cast<int64_t>(min(a.sinks, lo)) + kTile - 1) / kTile), r.near_tile);
-  }
-  r.tiles = r.sink_tiles + all - r.near_tile;
-  r.mtiles = (r.nodes + a.tile_nodes - 1) / a.tile_nodes;
-  return r;
-}
-
-// A stretch of cache tiles [kv0, kv1) of one row tile.
-struct Segment {
-  Request r;
-  int32_t request, head, mtile, kv0, kv1;
-  uint32_t begin, next;  // places of the line: the row tile's first, and the one after this stretch
-};
-// (a: in shared memory; a kernel parameter passed by reference is read through global memory, 0.3 us a field)
-__device__ __noinline__ Segment segment_at(const Line& a, const uint32_t* before, uint32_t t, uint32_t end) {
-  int lo = 0, hi = a.B;  // the last request whose tiles begin at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (before[mid] <= t) lo = mid; else hi = mid;
-  }
-  Segment s;
-  s.request = lo;
-  s.r = request_of(a, lo);
-  const uint32_t places = s.r.tiles + a.extra, local = t - before[lo], unit = local / places, at = local - unit * places;
-  const uint32_t to = min(places, at + (end - t));
-  s.begin = t - at;
-  s.next = s.begin + to;
-  s.kv0 = max(static_cast<int>(at) - a.extra, 0);
-  s.kv1 = max(static_cast<int>(to) - a.extra, 0);  // (kv0: the part ends among the places before the tiles)
-  s.head = static_cast<int>(unit / s.r.mtiles);   // a head's row tiles are neighbours: they share its tiles in L2
-  s.mtile = static_cast<int>(unit - static_cast<uint32_t>(s.head) * s.r.mtiles);
-  return s;
-}
-__device__ __forceinline__ int tile_slot(const Request& r, int j) {
-  return (j < r.sink_tiles ? j : r.near_tile + (j - r.sink_tiles)) * kTile;
-}
-// The line in n parts as equal as can be: the first `longer` have a place more.  (32-bit arithmetic: a 64-bit division is
-// a page of code, and at a call's start code comes from behind the instruction cache.)
-struct Parts {
-  uint32_t length, longer;
-  __device__ __forceinline__ Parts(uint32_t total, uint32_t n) : length(total / n), longer(total - length * n) {}
-  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * length + min(c, longer); }
-  // the part that holds place `at`
-  __device__ __forceinline__ int of(uint32_t at) const {
-    const uint32_t first = longer * (length + 1);
-    return static_cast<int>(at < first ? at / (length + 1) : longer + (at - first) / length);
-  }
-};
 // row / group for row < 128, group <= 128: over = ceil(2^16 / group).
 __device__ __forceinline__ int over_group(int row, uint32_t over) { return static_cast<int>((row * over) >> 16); }
-
-// Bits [lo, hi) of a 32-bit word whose bit 0 stands for position `at`.
-__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int at) {
-  const int a = max(lo - at, 0), b = min(hi - at, 32);
-  if (b <= a) return 0u;
-  return (b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u) & ~((1u << a) - 1u);
-}
 
 // The part of shared memory with a fixed size; then come the tiles before each request [B], the parents of two segments'
 // trees [2][Nmax] and, 1024-byte aligned, Q and the ring.
@@ -324,39 +221,6 @@ struct Smem {
   uint32_t tmem;
   volatile int32_t dead;       // a wait ran out: everyone leaves
 };
-
-// Bounded wait (about 2 s), polling: the waits between products and softmax are a fraction of a microsecond each, and
-// a suspended try_wait oversleeps them.  The loop is not inlined: with it at every wait the kernel's code does not
-// stay in the instruction cache.
-__device__ __noinline__ bool still_waiting(uint64_t* began, volatile int32_t* dead, uint32_t* status) {
-  const uint64_t now = globaltimer_ns();
-  if (*began == 0) *began = now;
-  if (!*dead && now - *began <= kWaitLimitNs) return true;
-  atomicOr(status, SV_DEV_TIMEOUT);
-  *dead = 1;
-  return false;
-}
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
-  uint64_t began = 0;
-  for (uint32_t it = 1;; ++it) {
-    if (it >= 16) __nanosleep(40);
-    if (mbar_test_wait(bar, parity)) return true;
-    if ((it & 255u) == 0 && !still_waiting(&began, dead, status)) return false;
-  }
-}
-__device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
-  return mbar_test_wait(bar, parity) || wait_slow(bar, parity, dead, status);
-}
-// The same by a whole warp: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, wait_or_leave(bar, parity, dead, status));
-}
-
-__device__ __forceinline__ void mark_bad(const AttendParams& a, int request, uint32_t bits) {
-  a.bad[request] = 1;
-  *a.any_bad = 1;
-  atomicOr(a.status, bits);
-}
 
 // A place in the ring of stages and the parity of its present round.
 struct Ring {
@@ -1031,36 +895,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) join_kernel(const AttendPar
     *reinterpret_cast<uint2*>(a.out + row * a.out_row_stride + head * a.out_head_stride + piece * 4) = w;
     if (piece == 0 && a.lse != nullptr) a.lse[row * a.q_heads + head] = (M + log2f(L)) * 0.693147180559945309f;
   }
-  if (*a.any_bad != 0) {
-    const int blocks = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
-    for (int i = me; i < a.B; i += blocks) {
-      if (!a.bad[i]) continue;
-      const int64_t first = max(int64_t(0), static_cast<int64_t>(a.node_offsets[i]));
-      const int64_t last = min(a.n_rows, static_cast<int64_t>(a.node_offsets[i + 1]));
-      for (int64_t row = first; row < last; ++row) {
-        for (int x = threadIdx.x; x < a.q_heads * (D / 8); x += kJoinThreads)
-          *reinterpret_cast<uint4*>(a.out + row * a.out_row_stride + (x / (D / 8)) * a.out_head_stride + (x % (D / 8)) * 8) =
-              make_uint4(0, 0, 0, 0);
-        if (a.lse != nullptr)
-          for (int x = threadIdx.x; x < a.q_heads; x += kJoinThreads) a.lse[row * a.q_heads + x] = -INFINITY;
-      }
-    }
-    // the last CTA clears the marks for the next call
-    __shared__ int last_one;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      last_one = atomicAdd(a.any_bad + 1, 1) == blocks - 1;
-    }
-    __syncthreads();
-    if (last_one) {
-      for (int i = threadIdx.x; i < a.B; i += kJoinThreads) a.bad[i] = 0;
-      if (threadIdx.x == 0) {
-        a.any_bad[0] = 0;
-        a.any_bad[1] = 0;
-      }
-    }
-  }
+  clear_bad<D, kJoinThreads>(a, a, a);
 }
 
 // ---- host --------------------------------------------------------------------------------------------
@@ -1220,6 +1055,7 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   a.units = pair ? c->kv_heads / 2 : c->kv_heads;
   a.group = group;
   a.tile_nodes = tile_nodes;
+  a.tile_rows = tile_nodes * group;
   a.over_group = (65536 + group - 1) / group;
   a.window = window;
   a.sinks = sinks;

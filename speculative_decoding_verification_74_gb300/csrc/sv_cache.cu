@@ -15,6 +15,7 @@
 
 #include "sv_device.cuh"
 #include "sv_ops.h"
+#include "sv_pages.cuh"
 
 namespace sv {
 
@@ -45,102 +46,6 @@ sv_status check_table(const int32_t* page_table, int table_width, const int32_t*
 }
 
 namespace {
-
-constexpr int kPageThreads = 1024;
-constexpr int kRowThreads = 256;
-constexpr int kPerThread = SV_MAX_BATCH / kPageThreads;  // rows per thread of the bookkeeping CTA
-
-struct Pool {
-  int32_t* refs;
-  int32_t pages, shift;  // page_size = 1 << shift
-};
-
-// Sum over the CTA before this thread (exclusive), and the total.  buf: 33 ints of shared memory.
-__device__ __forceinline__ int block_scan(int v, int* buf, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();  // buf may still be read from a scan before
-  if (lane == 31) buf[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    const int n = blockDim.x >> 5;
-    int w = lane < n ? buf[lane] : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, w, d);
-      if (lane >= d) w += y;
-    }
-    if (lane < n) buf[lane] = w;
-    if (lane == 31) buf[32] = w;
-  }
-  __syncthreads();
-  *total = buf[32];
-  return x - v + (warp > 0 ? buf[warp - 1] : 0);
-}
-
-// Thread t owns pages [t n, (t + 1) n), n a multiple of 4: one scan gives every free page its
-// rank in page order.  16-byte loads, four in flight.
-__device__ __forceinline__ int pages_per_thread(int pages) {
-  return ((pages + kPageThreads - 1) / kPageThreads + 3) & ~3;
-}
-__device__ __forceinline__ int count_free(const Pool& p) {
-  const int n = pages_per_thread(p.pages);
-  const int64_t first = static_cast<int64_t>(threadIdx.x) * n;
-  const int64_t last = min(first + n, static_cast<int64_t>(p.pages));
-  int free_pages = 0;
-  if ((reinterpret_cast<uintptr_t>(p.refs) & 15u) == 0) {
-#pragma unroll 4
-    for (int64_t g = first; g < last; g += 4) {
-      if (g + 4 <= last) {
-        const int4 r = *reinterpret_cast<const int4*>(p.refs + g);
-        free_pages += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-      } else {
-        for (int64_t h = g; h < last; ++h) free_pages += p.refs[h] == 0;
-      }
-    }
-  } else {
-    for (int64_t g = first; g < last; ++g) free_pages += p.refs[g] == 0;
-  }
-  return free_pages;
-}
-
-// Calls take(rank, page) for this thread's free pages of rank < wanted, in page order.
-template <typename F>
-__device__ __forceinline__ void take_free(const Pool& p, int rank, int wanted, F take) {
-  const int n = pages_per_thread(p.pages);
-  const int64_t first = static_cast<int64_t>(threadIdx.x) * n;
-  const int64_t last = min(first + n, static_cast<int64_t>(p.pages));
-  for (int64_t g = first; g < last && rank < wanted; ++g)
-    if (p.refs[g] == 0) {
-      take(rank, static_cast<int>(g));
-      ++rank;
-    }
-}
-
-// Gives back one reference of a page; a page that nothing holds is reported and left at 0.
-__device__ __forceinline__ void give_back(const Pool& p, int page, uint32_t* status) {
-  if (page >= p.pages || atomicSub(p.refs + page, 1) <= 0) {
-    if (page < p.pages) atomicAdd(p.refs + page, 1);
-    atomicOr(status, SV_DEV_BAD_PAGE);
-  }
-}
-
-// Entries of one row from `from` on that hold a page, given back by one warp (the held entries of a
-// row come first, so the row is read up to the first entry that holds none).
-__device__ __forceinline__ void release_entries(const Pool& p, int32_t* row, int from, int width, uint32_t* status) {
-  const int lane = threadIdx.x & 31;
-  for (int e0 = from; e0 < width; e0 += 32) {
-    const int e = e0 + lane;
-    const int page = e < width ? row[e] : -1;
-    if (page >= 0 && atomicExch(row + e, -1) >= 0) give_back(p, page, status);
-    if (__any_sync(0xFFFFFFFFu, page < 0)) break;
-  }
-}
 
 // ---- reserve ---------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPageThreads) reserve_kernel(Pool p, int32_t* table, int width, const int32_t* seq_len,
@@ -336,6 +241,159 @@ __global__ void __launch_bounds__(kPageThreads) release_kernel(Pool p, int32_t* 
   }
 }
 
+// ---- reorder ---------------------------------------------------------------------------------
+// marks after plan_kernel: the free page that row j gets for its partly filled last page (>= 0), or
+constexpr int32_t kKeeps = -1;    // row j takes its source row's entries as they are
+constexpr int32_t kShares = -2;   // it shares the full pages, there is nothing else
+constexpr int32_t kEmpties = -3;  // it names no source
+constexpr int32_t kFailed = -4;   // in marks[0 .. rows): nothing changes
+
+// What becomes of every row, and the pages: one CTA.  Shared memory: four ints per row.
+__global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_t* table, int width, int rows, int32_t* seq_len,
+                                                            const int32_t* src, int32_t* out_ok, int32_t* marks,
+                                                            uint32_t* status) {
+  extern __shared__ int32_t per_row[];
+  int32_t *from = per_row, *len = per_row + rows, *first = per_row + 2 * rows, *pair_of = per_row + 3 * rows;
+  __shared__ int buf[33];
+  __shared__ uint32_t wrong;
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) wrong = 0;
+  for (int j = threadIdx.x; j < rows; j += kPageThreads) {
+    from[j] = src[j];
+    len[j] = seq_len[j];
+    first[j] = INT_MAX;  // the first row that names row j: INT_MAX = none
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < rows; j += kPageThreads) {
+    const int s = from[j];
+    if (s < -1 || s >= rows) atomicOr(&wrong, SV_DEV_BAD_SEQ);
+    else if (s >= 0) atomicMin(first + s, s == j ? -1 : j);  // the row itself comes before all others
+  }
+  __syncthreads();
+  for (int j = warp; j < rows; j += kPageThreads / 32) {
+    if (first[j] == INT_MAX) continue;
+    const int64_t held = (static_cast<int64_t>(len[j]) + (1 << p.shift) - 1) >> p.shift;
+    if (len[j] < 0 || held > width) {
+      if (lane == 0) atomicOr(&wrong, SV_DEV_BAD_SEQ);
+      continue;
+    }
+    const int32_t* row = table + static_cast<int64_t>(j) * width;
+    bool lacks = false;
+#pragma unroll 4
+    for (int e = lane; e < held; e += 32) lacks |= static_cast<uint32_t>(row[e]) >= static_cast<uint32_t>(p.pages);
+    if (__any_sync(0xFFFFFFFFu, lacks) && lane == 0) atomicOr(&wrong, SV_DEV_BAD_PAGE);
+  }
+  __syncthreads();
+  uint32_t problem = wrong;
+  int total = 0;
+  int split[kPerThread], at = 0;
+  if (problem == 0) {
+    // the pages of rows that no row names are given back first (their table rows are rewritten later)
+    auto each_entry = [&](auto f) {
+      for (int j = warp; j < rows; j += kPageThreads / 32) {
+        if (first[j] != INT_MAX) continue;
+        const int32_t* row = table + static_cast<int64_t>(j) * width;
+        for (int e0 = 0; e0 < width; e0 += 32) {
+          const int page = e0 + lane < width ? row[e0 + lane] : -1;
+          if (page >= 0) f(page);
+          if (__any_sync(0xFFFFFFFFu, page < 0)) break;
+        }
+      }
+    };
+    each_entry([&](int page) { give_back(p, page, status); });
+    const int part_mask = (1 << p.shift) - 1;
+    int sum = 0;
+#pragma unroll
+    for (int x = 0; x < kPerThread; ++x) {
+      const int j = threadIdx.x * kPerThread + x;
+      const int s = j < rows ? from[j] : -1;
+      split[x] = s >= 0 && first[s] != (s == j ? -1 : j) && (len[s] & part_mask) != 0;
+      sum += split[x];
+    }
+    at = block_scan(sum, buf, &total);
+    __threadfence_block();
+    __syncthreads();
+    int found;
+    const int rank = block_scan(count_free(p), buf, &found);
+    if (total > found) {
+      problem = SV_DEV_OUT_OF_PAGES;
+      __syncthreads();
+      each_entry([&](int page) {
+        if (page < p.pages) atomicAdd(p.refs + page, 1);
+      });
+    } else {
+#pragma unroll
+      for (int x = 0; x < kPerThread; ++x)
+        if (split[x]) pair_of[at++] = threadIdx.x * kPerThread + x;
+      __syncthreads();
+      take_free(p, rank, total, [&](int r, int page) {
+        marks[pair_of[r]] = page;
+        p.refs[page] = 1;
+      });
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kPerThread; ++x) {
+    const int j = threadIdx.x * kPerThread + x;
+    if (j >= rows) continue;
+    const int s = from[j];
+    if (problem != 0) {
+      marks[j] = kFailed;
+    } else {
+      if (s < 0) marks[j] = kEmpties;
+      else if (!split[x]) marks[j] = first[s] == (s == j ? -1 : j) ? kKeeps : kShares;
+      seq_len[j] = s < 0 ? 0 : len[s];
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (problem != 0) atomicOr(status, problem);
+    if (out_ok != nullptr) out_ok[0] = problem == 0;
+  }
+}
+
+// The table rows, `columns` entries of every row to a CTA: all are read before any is written.
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(Pool p, int32_t* table, int width, int rows,
+                                                             const int32_t* seq_len, const int32_t* src, int32_t* marks,
+                                                             int columns) {
+  extern __shared__ int32_t old[];  // [rows][columns]
+  pdl_wait();
+  if (marks[0] == kFailed) return;
+  const int c0 = blockIdx.x * columns, n = min(columns, width - c0);
+  const int items = rows * columns;
+  bool some = false;
+  for (int x = threadIdx.x; x < items; x += kRowThreads) {
+    const int j = x / columns, c = x - j * columns;
+    const int32_t page = c < n ? table[static_cast<int64_t>(j) * width + c0 + c] : -1;
+    some |= page >= 0;
+    old[x] = page;
+  }
+  if (__syncthreads_or(some) == 0) return;  // (a row's held entries come first: past the longest row there are none)
+  for (int x = threadIdx.x; x < items; x += kRowThreads) {
+    const int j = x / columns, c = x - j * columns, e = c0 + c;
+    if (c >= n) continue;
+    const int mark = marks[j];
+    int32_t page = -1;
+    if (mark != kEmpties) {
+      const int s = src[j], full = seq_len[j] >> p.shift;
+      page = old[s * columns + c];
+      if (mark != kKeeps) {
+        if (e < full) {
+          atomicAdd(p.refs + page, 1);
+        } else if (e == full && mark >= 0) {
+          // rows of this CTA alone look at this mark from here on: a partly filled page lies in one column
+          const int32_t source = page;
+          page = mark;
+          marks[j] = source;
+        } else {
+          page = -1;
+        }
+      }
+    }
+    table[static_cast<int64_t>(j) * width + e] = page;
+  }
+}
+
 // ---- rows ------------------------------------------------------------------------------------
 // Where the 16-byte piece `e` of a token's keys (or values) lies within its slot.
 struct RowShape {
@@ -501,8 +559,8 @@ struct CopyParams {
   __nv_bfloat16* k;
   __nv_bfloat16* v;
   const int32_t *table, *seq_len, *src, *dst;
-  int32_t width, rows, layers;
-  const int32_t* done;  // [n] pairs that were forked
+  int32_t width, layers;
+  const int32_t* done;  // [n] pairs that were forked; after a reorder (src NULL), the pages to copy from
 };
 
 // grid (pieces of [layer][k, v][slot][piece], pairs): the used slots of each forked pair's last page.  I: an unsigned type
@@ -511,13 +569,9 @@ constexpr int kInFlight = 4;
 template <typename I>
 __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(CopyParams a) {
   pdl_wait();
-  const int j = blockIdx.y;
-  if (a.done[j] == 0) return;
-  const int from_row = a.src[j], to_row = a.dst[j];
-  const int len = a.seq_len[to_row], part = len & ((1 << a.r.shift) - 1), e0 = len >> a.r.shift;
+  int32_t from, to;
+  const int part = copied_slots(a.src, a.dst, a.done, a.table, a.width, a.seq_len, a.r.shift, blockIdx.y, &from, &to);
   if (part == 0) return;
-  const int32_t from = a.table[static_cast<int64_t>(from_row) * a.width + e0];
-  const int32_t to = a.table[static_cast<int64_t>(to_row) * a.width + e0];  // (both name pages: fork_kernel has seen to it)
   const I pieces = static_cast<I>(a.r.pieces), per_side = part * pieces, items = static_cast<I>(a.layers) * 2 * per_side;
   const I step = static_cast<I>(gridDim.x) * kRowThreads;
   for (I x0 = static_cast<I>(blockIdx.x) * kRowThreads + threadIdx.x; x0 < items; x0 += kInFlight * step) {
@@ -539,10 +593,13 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(CopyParams a) {
   }
 }
 
-int log2_of(int v) {
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
+// Copies of `items` pieces per pair, in one wave of eight CTAs an SM (half as many again 73.5 us against 72.0 for 16 prompts to 48 beams).
+cudaError_t copy_rows(const CopyParams& a, int page_size, int n, void* stream) {
+  const int64_t items = static_cast<int64_t>(a.layers) * 2 * page_size * a.r.pieces;
+  const int64_t groups = std::min<int64_t>(std::max(1, 8 * 152 / n), (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
+  const auto kernel = items <= INT_MAX ? fork_rows_kernel<uint32_t> : fork_rows_kernel<uint64_t>;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, groups)), n), kRowThreads, 0, stream,
+                          SV_KERNEL_CACHE_ROWS, 1, a);
 }
 
 RowShape row_shape(const sv_cache* c) {
@@ -558,14 +615,54 @@ RowShape row_shape(const sv_cache* c) {
   return r;
 }
 
+CopyParams copy_params(const sv_cache* c, const int32_t* table, int width, const int32_t* seq_len) {
+  CopyParams a = {};
+  a.r = row_shape(c);
+  a.k = static_cast<__nv_bfloat16*>(c->k);
+  a.v = static_cast<__nv_bfloat16*>(c->v);
+  a.table = table;
+  a.seq_len = seq_len;
+  a.width = width;
+  a.layers = c->layers;
+  return a;
+}
+
 Pool pool_of(const sv_cache* c) { return Pool{c->page_refs, c->pages, log2_of(c->page_size)}; }
 
-uint32_t* status_of(void* ws) { return static_cast<uint32_t*>(ws); }
-// commit's arrival counters (zero between calls), and fork's marks
-int32_t* arrived_of(void* ws) { return reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + SV_STATUS_BYTES); }
-int32_t* marks_of(void* ws) { return arrived_of(ws) + SV_MAX_BATCH; }
-
 }  // namespace
+
+cudaError_t reserve_pages(const Pool& p, int32_t* table, int width, const int32_t* seq_len, const int32_t* extra, int B,
+                          int32_t* out_ok, void* ws, void* stream) {
+  return launch_dependent(reserve_kernel, dim3(1), kPageThreads, 0, stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, seq_len,
+                          extra, B, out_ok, status_of(ws));
+}
+cudaError_t fork_pages(const Pool& p, int32_t* table, int width, int rows, int32_t* seq_len, const int32_t* src,
+                       const int32_t* dst, int n, int32_t* done, void* ws, void* stream) {
+  return launch_dependent(fork_kernel, dim3(1), kPageThreads, 0, stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows,
+                          seq_len, src, dst, n, done, status_of(ws));
+}
+cudaError_t release_pages(const Pool& p, int32_t* table, int width, int rows, int32_t* seq_len, const int32_t* seqs, int n,
+                          void* ws, void* stream) {
+  return launch_dependent(release_kernel, dim3(1), kPageThreads, 0, stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows,
+                          seq_len, seqs, n, status_of(ws));
+}
+cudaError_t reorder_pages(const Pool& p, int32_t* table, int width, int rows, int32_t* seq_len, const int32_t* src,
+                          int32_t* out_ok, void* ws, void* stream) {
+  const size_t per_row = sizeof(int32_t) * 4 * rows;
+  cudaError_t e = allow_smem<plan_kernel>(sizeof(int32_t) * 4 * SV_MAX_BATCH);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(plan_kernel, dim3(1), kPageThreads, per_row, stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows,
+                       seq_len, src, out_ok, marks_of(ws), status_of(ws));
+  if (e != cudaSuccess) return e;
+  // a CTA holds its columns of every row in at most 32 KB (64 KB for 4096 rows)
+  const int columns = std::min(std::max(4, 8192 / rows), std::max(width, 1));
+  const size_t bytes = sizeof(int32_t) * columns * rows;
+  e = allow_smem<gather_kernel>(sizeof(int32_t) * 4 * SV_MAX_BATCH);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(gather_kernel, dim3((width + columns - 1) / columns), kRowThreads, bytes, stream,
+                          SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows, seq_len, src, marks_of(ws), columns);
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -581,9 +678,7 @@ sv_status sv_cache_reserve(const sv_cache* c, int32_t* page_table, int table_wid
   if (static_cast<int64_t>(B) * table_width > INT_MAX)
     return set_error(SV_ERR_INVALID_ARG, "B * table_width = %lld exceeds 2^31 - 1", (long long)B * table_width);
   if ((s = check_workspace(ws, ws_bytes, SV_CACHE_WORKSPACE_BYTES)) != SV_OK) return s;
-  return launch_status(launch_dependent(reserve_kernel, dim3(1), kPageThreads, 0, stream, SV_KERNEL_CACHE_PAGES, 1,
-                                        pool_of(c), page_table, table_width, seq_len, extra, B, out_ok, status_of(ws)),
-                       "reserve");
+  return launch_status(reserve_pages(pool_of(c), page_table, table_width, seq_len, extra, B, out_ok, ws, stream), "reserve");
 }
 
 sv_status sv_cache_append(const sv_cache* c, int layer, int layers, const int32_t* page_table, int table_width,
@@ -670,28 +765,13 @@ sv_status sv_cache_fork(const sv_cache* c, int32_t* page_table, int table_width,
   if (rows == 0 || src == nullptr || dst == nullptr) return set_error(SV_ERR_INVALID_ARG, "rows, src or dst is missing");
   if ((s = check_workspace(ws, ws_bytes, SV_CACHE_WORKSPACE_BYTES)) != SV_OK) return s;
   int32_t* done = out_ok != nullptr ? out_ok : marks_of(ws);
-  cudaError_t e = launch_dependent(fork_kernel, dim3(1), kPageThreads, 0, stream, SV_KERNEL_CACHE_PAGES, 1, pool_of(c),
-                                   page_table, table_width, rows, seq_len, src, dst, n, done, status_of(ws));
+  const cudaError_t e = fork_pages(pool_of(c), page_table, table_width, rows, seq_len, src, dst, n, done, ws, stream);
   if (e != cudaSuccess) return launch_status(e, "fork");
-  CopyParams a = {};
-  a.r = row_shape(c);
-  a.k = static_cast<__nv_bfloat16*>(c->k);
-  a.v = static_cast<__nv_bfloat16*>(c->v);
-  a.table = page_table;
-  a.seq_len = seq_len;
+  CopyParams a = copy_params(c, page_table, table_width, seq_len);
   a.src = src;
   a.dst = dst;
-  a.width = table_width;
-  a.rows = rows;
-  a.layers = c->layers;
   a.done = done;
-  const int64_t items = static_cast<int64_t>(c->layers) * 2 * c->page_size * a.r.pieces;
-  // one wave of eight CTAs an SM (half as many again 73.5 us against 72.0 for 16 prompts to 48 beams)
-  const int64_t groups = std::min<int64_t>(std::max(1, 8 * 152 / n), (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
-  const auto kernel = items <= INT_MAX ? fork_rows_kernel<uint32_t> : fork_rows_kernel<uint64_t>;
-  return launch_status(launch_dependent(kernel, dim3(static_cast<unsigned>(std::max<int64_t>(1, groups)), n),
-                                        kRowThreads, 0, stream, SV_KERNEL_CACHE_ROWS, 1, a),
-                       "fork rows");
+  return launch_status(copy_rows(a, c->page_size, n, stream), "fork rows");
 }
 
 sv_status sv_cache_release(const sv_cache* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
@@ -702,9 +782,21 @@ sv_status sv_cache_release(const sv_cache* c, int32_t* page_table, int table_wid
   if (n == 0) return SV_OK;
   if (rows == 0 || seqs == nullptr) return set_error(SV_ERR_INVALID_ARG, "rows or seqs is missing");
   if ((s = check_workspace(ws, ws_bytes, SV_CACHE_WORKSPACE_BYTES)) != SV_OK) return s;
-  return launch_status(launch_dependent(release_kernel, dim3(1), kPageThreads, 0, stream, SV_KERNEL_CACHE_PAGES, 1,
-                                        pool_of(c), page_table, table_width, rows, seq_len, seqs, n, status_of(ws)),
-                       "release");
+  return launch_status(release_pages(pool_of(c), page_table, table_width, rows, seq_len, seqs, n, ws, stream), "release");
+}
+
+sv_status sv_cache_reorder(const sv_cache* c, int32_t* page_table, int table_width, int rows, int32_t* seq_len,
+                           const int32_t* src, int32_t* out_ok, void* ws, size_t ws_bytes, void* stream) {
+  sv_status s;
+  if ((s = check_cache(c)) != SV_OK || (s = check_table(page_table, table_width, seq_len, rows)) != SV_OK) return s;
+  if (rows == 0) return SV_OK;
+  if (src == nullptr) return set_error(SV_ERR_INVALID_ARG, "src is NULL");
+  if ((s = check_workspace(ws, ws_bytes, SV_CACHE_WORKSPACE_BYTES)) != SV_OK) return s;
+  const cudaError_t e = reorder_pages(pool_of(c), page_table, table_width, rows, seq_len, src, out_ok, ws, stream);
+  if (e != cudaSuccess) return launch_status(e, "reorder");
+  CopyParams a = copy_params(c, page_table, table_width, seq_len);
+  a.done = marks_of(ws);
+  return launch_status(copy_rows(a, c->page_size, rows, stream), "reorder rows");
 }
 
 }  // extern "C"

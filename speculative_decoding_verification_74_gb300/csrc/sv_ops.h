@@ -23,6 +23,7 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // The pool's description (sv_cache.cu).
 sv_status check_cache(const sv_cache* c);
+sv_status check_cache4(const sv_cache4* c);  // (sv_cache4.cu)
 sv_status check_table(const int32_t* page_table, int table_width, const int32_t* seq_len, int B);
 
 inline sv_status launch_status(cudaError_t e, const char* what) {

@@ -52,6 +52,7 @@
 namespace sv {
 namespace {
 
+constexpr int kTile = 128;                 // rows of Q, and slots of the cache, in a tile
 constexpr int kGroupThreads = 128;
 constexpr int kSoftThreads = 2 * kGroupThreads;
 constexpr int kThreads = 128 + kSoftThreads;
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i0 = min(a.B, tid * per), i1 = min(a.B, i0 + per);
     uint32_t sum = 0;
     for (int i = i0; i < i1; ++i) {
-      const Request r = request_of(a, i);
+      const Request r = request_of<kTile>(a, i);
       if (r.bad != 0 && blockIdx.x == 0) mark_bad(a, i, r.bad);
       before[i] = sum;
       sum += static_cast<uint32_t>(r.tiles + a.extra) * r.mtiles * a.units;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Parts parts(total, max(1u, min(gridDim.x, total)));
   const uint32_t t0 = min(parts.begin(blockIdx.x), total), t1 = min(parts.begin(blockIdx.x + 1), total);
   Segment opening = {};
-  if (t0 < t1) opening = segment_at(sm.line, before, t0, t1);
+  if (t0 < t1) opening = segment_at<kTile>(sm.line, before, t0, t1);
   const bool some = opening.kv0 < opening.kv1;
   // a part's stretches but the first begin a row tile; the last may hold none of its cache tiles
   auto stretch_at = [&](uint32_t t) { return t == t0 ? some : t + a.extra < t1; };
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int block = 0, page_now = -1, page_next = -1, next_block = 0, next_now = -1;
     if (some) {
       s = opening;
-      block = tile_slot(s.r, s.kv0) >> (box_shift + 5);
+      block = tile_slot<kTile>(s.r, s.kv0) >> (box_shift + 5);
       page_now = pages_of(s, block);
     }
     for (uint32_t t = t0; stretch_at(t) && go;) {
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t after = s.next;
       page_next = pages_of(s, block + 1);
       for (int j = s.kv0; j < s.kv1 && go; ++j) {
-        const int s0 = tile_slot(s.r, j);
+        const int s0 = tile_slot<kTile>(s.r, j);
         const int need = s0 >> (box_shift + 5);
         if (need != block) {
           page_now = need == block + 1 ? page_next : pages_of(s, need);
@@ -381,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.step(stages);
         at.step(stages);
         if (j == max(s.kv0, s.kv1 - 2) && stretch_at(after)) {
-          next = segment_at(sm.line, before, after, t1);
-          next_block = tile_slot(next.r, next.kv0) >> (box_shift + 5);
+          next = segment_at<kTile>(sm.line, before, after, t1);
+          next_block = tile_slot<kTile>(next.r, next.kv0) >> (box_shift + 5);
           next_now = pages_of(next, next_block);
         }
       }
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- segments: description, parents, Q --------------------------------------------------------
     constexpr int rows_apart = kTile / kCopies;
     for (uint32_t t = t0; stretch_at(t); ++segments) {
-      const Segment s = t == t0 ? opening : segment_at(sm.line, before, t, t1);
+      const Segment s = t == t0 ? opening : segment_at<kTile>(sm.line, before, t, t1);
       const int b = segments & 1;
       if (segments >= 2 && !warp_wait(&sm.seg_free[b], ((segments >> 1) - 1) & 1, &sm.dead, a.status)) break;
       if (a.parent != nullptr)
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t n = n0 + j;
         if (left = !warp_wait(&sm.s_full[group], (n >> 1) & 1, &sm.dead, a.status); left) break;
         tc_after_sync();
-        const int s0 = tile_slot(s.r, s.kv0 + j);
+        const int s0 = tile_slot<kTile>(s.r, s.kv0 + j);
         const bool whole = s0 + kTile <= len && (a.window <= 0 || s0 + kTile <= a.sinks || s0 >= len + s.r.nodes - a.window);
         if (!whole && (s0 + kTile > end || (a.window > 0 && s0 < lo && s0 + kTile > a.sinks))) {
           // slots that no node sees may hold anything: 0 times it has to be 0

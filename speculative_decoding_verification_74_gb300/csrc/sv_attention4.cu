@@ -1,10 +1,10 @@
 // sv_tree_attention4: a token tree's queries against a paged cache held in 4 bits.
 //
-// A warp holds a row tile: 16 rows (query heads that share a key/value head, times nodes) as fragments of the 16 x 8 x 16
-// products of two-byte floats, and goes over its share of the cache in chunks of 32 slots.  With c = scale k_scale log2(e) and
-// running maximum m:
-//   S = Q K^T [16 x 32];  P = 2^(c S - m) in float16;  O = O + P V [16 x D], all sums in float32
-// and at the end o = v_scale O / sum P, lse = (m + log2 sum P) ln 2.
+// A warp holds a row tile of 8 or 16 rows (query heads that share a key/value head, times nodes) and goes over its share of the
+// cache in chunks of 32 slots.  With c = scale k_scale log2(e) and running maximum m:
+//   S' = K Q' [32 x rows];  P' = 2^(c S' - m) in float16;  O' = O' + V' P' [D x rows], all sums in float32
+// (' = transposed) and at the end o = v_scale O / sum P, lse = (m + log2 sum P) ln 2.  The cache is the 16-row operand of the
+// 16 x 8 x 16 products and the queries the 8-column one, so few rows waste little: one decoded token has 4 or 8.
 //
 // Exactness.  A code times its e4m3 scale has at most six significant bits and lies in [2^-10, 2688]: it is a float16 without
 // rounding.  A query row is scaled by a power of two so that its largest element lies in [2^14, 2^15); elements down to 2^-28
@@ -15,11 +15,13 @@
 // is shared between warps.  In a group of eight slots a lane's codes are 16 (8 for D = 64) neighbouring bytes, in lane order: for K
 // the slot lane / 4 and a quarter of its dimensions, whose order in the product is free as long as Q's is the same; for V two
 // neighbouring slots and an eighth of the dimensions.  So codes go from shared memory to the fragments through registers
-// only: per pair of elements a conversion and a multiplication by the scales.
+// only: per pair of elements a conversion and a multiplication by the scales.  P' comes out of the first product with a slot's
+// rows in a lane and goes into the second with a row's slots: 8 x 8 blocks are transposed by movmatrix.
 //
-// Work split.  All (row tile, cache tile of 128 slots) pairs lie on one line, cut into equal parts, one per CTA; a part's
-// stretches of row tiles are shared by the CTA's warps chunk by chunk, whose partial results are added in shared memory; a
-// row tile that crosses CTAs leaves partial results in the workspace, which join4_kernel adds.
+// Work split.  All (row tile, chunk) pairs of the batch lie on one line, and before each row tile a few places for what
+// beginning and ending it costs; every warp of the grid takes an equal part of the line, in segments: stretches of one row
+// tile.  Warps share nothing but the SM, so one's loads of Q and results run beside another's products.  A row tile that
+// crosses warps leaves partial results in the workspace, which join4_kernel adds.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,14 +36,19 @@
 namespace sv {
 namespace {
 
-constexpr int kRows = 16;                 // rows of a row tile
 constexpr int kChunk = 32;                // slots that a warp takes at a time
-constexpr int kWarps = 8;
-constexpr int kThreads4 = 32 * kWarps;
+// Row tiles of N columns of eight.  Warps: as many as the registers leave room for, so that their latencies overlap.
+template <int N>
+struct Tile4 {
+  static constexpr int kRows = 8 * N;
+  static constexpr int kWarps = N == 1 ? 16 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+};
+constexpr int kMaxWarps = 16;
 constexpr float kLazyGrowth4 = 8.0f;      // log2 units by which a maximum may grow without a rescale of O
 constexpr float kBias = 4.0f;             // P is 2^kBias at the maximum that it is scaled to
-constexpr int kExtra4 = 2;                // places of the line for a row tile's beginning and end
-constexpr int kMaxStages4 = 8;
+constexpr int kExtra4 = 2;                // places of the line for a row tile's beginning and end, in chunks
+constexpr int kMaxStages4 = 4;
 
 struct Attend4Params : Line, Marks, Outputs {
   const __nv_bfloat16* q;
@@ -49,22 +56,25 @@ struct Attend4Params : Line, Marks, Outputs {
   const unsigned char* pool;     // of the layer
   int64_t page_stride, head_stride;
   const int32_t *table, *parent;
-  Job* jobs;          // [grid]
-  float* parts;       // [2 grid] partial results
+  int32_t* n_jobs;    // [2] row tiles to join; CTAs of the join that are done (both zero between calls)
+  Job* jobs;          // [warps of the grid]
+  float* parts;       // [2 warps of the grid] partial results
   int32_t pages, kv_heads, stages;
   float scale;        // with k_scale
   float v_scale;
 };
 
-// Floats of one partial result: O [16][D], then m and the sum per row.
-template <int D>
-constexpr int part4_floats() { return kRows * D + 2 * kRows; }
+// Floats of one partial result: O [rows][D], then m and the sum per row.
+template <int D, int N>
+constexpr int part4_floats() { return 8 * N * (D + 2); }
+
+constexpr int kQueue = kMaxStages4 + 2;   // segments between a warp's copies and its products: one per chunk in flight, and the ends
 
 struct Smem4 {
   Line line;
-  uint64_t full[kWarps][kMaxStages4];
-  float m[kWarps][kRows], l[kWarps][kRows];
-  uint32_t scan[kWarps];
+  uint64_t full[kMaxWarps][kMaxStages4];
+  Segment queue[kMaxWarps][kQueue];
+  uint32_t scan[kMaxWarps];
   volatile int32_t dead;       // a wait ran out: the launch finishes on what it holds
 };
 
@@ -106,45 +116,39 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The transpose of an 8 x 8 block: lane 4 i + j has elements 2 j and 2 j + 1 of row i.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-  return x + __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+// Over the lanes of the same lane % 4.
+__device__ __forceinline__ float column_max(float x) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+  return x;
+}
+__device__ __forceinline__ float column_sum(float x) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+  return x;
 }
 
-// First slot of the segment's x-th chunk.
-__device__ __forceinline__ int chunk_slot(const Segment& s, int x) {
-  constexpr int per = kTile / kChunk;
-  return tile_slot(s.r, s.kv0 + x / per) + (x % per) * kChunk;
-}
-// Whether some node sees a slot of [slot, slot + n).
-__device__ __forceinline__ bool seen_by_some(const Line& a, const Request& r, int slot, int n) {
-  const int lo = a.window > 0 ? max(0, r.len - a.window + 1) : 0;
-  return slot < r.len + r.nodes && (a.window <= 0 || slot < a.sinks || slot + n > lo);
-}
-
-// A warp's chunks in the order of the line: its place, and where the next one is.
-struct Walk {
-  Segment s;
-  uint32_t t;      // place of the line where the segment begins
-  int x, n;        // chunk, chunks of the segment
-};
-
-template <int D>
-__global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const Attend4Params a) {
+template <int D, int N>
+__global__ void __launch_bounds__(Tile4<N>::kThreads, 1) attend4_kernel(const Attend4Params a) {
+  constexpr int kRows = Tile4<N>::kRows, kWarps = Tile4<N>::kWarps, kThreads4 = Tile4<N>::kThreads;
   constexpr int kGroupBytes = 9 * D;                       // eight slots
   constexpr int kChunkBytes = kChunk / 8 * kGroupBytes;
   constexpr int kSteps = D / 16;                           // products over the dimensions
   constexpr int kWords = D / 32;                           // words of a lane's codes in a group: 4 or 2
-  constexpr int kEighth = D / 8;                           // 8-column tiles of O
+  constexpr int kDimTiles = D / 16;                        // 16-row tiles of O'
   extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ Smem4 sm;
-  float* mix = reinterpret_cast<float*>(dyn);                                  // [kWarps][kRows][D + 4]
-  unsigned char* rings = dyn + sizeof(float) * kWarps * kRows * (D + 4);
-  uint32_t* before = reinterpret_cast<uint32_t*>(rings + static_cast<size_t>(kWarps) * a.stages * kChunkBytes);  // [B]
+  uint32_t* before = reinterpret_cast<uint32_t*>(dyn + static_cast<size_t>(kWarps) * a.stages * kChunkBytes);  // [B]
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int g = lane >> 2, t4 = lane & 3;
   if (tid == 0) {
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const Attend4Para
     const int i0 = min(a.B, tid * per), i1 = min(a.B, i0 + per);
     uint32_t sum = 0;
     for (int i = i0; i < i1; ++i) {
-      const Request r = request_of(a, i);
+      const Request r = request_of<kChunk>(a, i);
       if (r.bad != 0 && blockIdx.x == 0) mark_bad(a, i, r.bad);
       before[i] = sum;
       sum += static_cast<uint32_t>(r.tiles + a.extra) * r.mtiles * a.kv_heads;
@@ -186,90 +190,87 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const Attend4Para
     for (int i = i0; i < i1; ++i) before[i] += at;
     __syncthreads();
   }
-  // with fewer places than CTAs the last CTAs have none
-  const Parts parts(total, max(1u, min(gridDim.x, total)));
-  const uint32_t t0 = min(parts.begin(blockIdx.x), total), t1 = min(parts.begin(blockIdx.x + 1), total);
-  if (tid == 0) a.jobs[blockIdx.x].valid = 0;
+  // parts are dealt out CTA by CTA: with fewer places than warps every SM has some
+  const uint32_t me = warp * gridDim.x + blockIdx.x;
+  const Parts parts(total, max(1u, min(gridDim.x * kWarps, total)));
+  const uint32_t t0 = min(parts.begin(me), total), t1 = min(parts.begin(me + 1), total);
 
-  // ---- copies ---------------------------------------------------------------------------------------
-  unsigned char* ring = rings + static_cast<size_t>(warp) * a.stages * kChunkBytes;
-  const int piece_shift = min(5, a.shift), piece = 1 << piece_shift;  // slots per copy: a page, or 32 slots of one
-  // The next chunk of this warp that some node sees, from w.x on; false = there is none in this CTA's part.
-  auto settle = [&](Walk& w) {
-    for (;;) {
-      while (w.x < w.n && !seen_by_some(sm.line, w.s.r, chunk_slot(w.s, w.x), kChunk)) w.x += kWarps;
-      if (w.x < w.n) return true;
-      if (w.s.next >= t1) return false;
-      w.t = w.s.next;
-      w.s = segment_at(sm.line, before, w.t, t1);
-      w.n = (w.s.kv1 - w.s.kv0) * (kTile / kChunk);
-      w.x = warp;
+  // ---- copies: this warp's chunks in the order of the line -------------------------------------------
+  unsigned char* ring = dyn + static_cast<size_t>(warp) * a.stages * kChunkBytes;
+  const int piece_shift = min(5, a.shift);                   // slots per copy: a page, or 32 slots of one
+  const bool copies = lane < (kChunk >> piece_shift);        // this lane copies the lane-th piece
+  uint32_t asked = 0, used = 0;                              // chunks that were asked for, and used
+  uint32_t ask_stage = 0, use_stage = 0, use_parity = 0;
+  uint32_t ask_t = t0, found = 0;                            // place of the next segment to look for, segments found
+  Segment load = {};
+  int load_j = 0, load_end = 0, block = -1, page_now = -1;   // pages of 32 entries at a time
+  // Finds the next chunk to ask for: false = there is none in this part.
+  auto settle = [&]() {
+    if (load_j < load_end) return true;
+    while (ask_t < t1) {
+      load = segment_at<kChunk>(sm.line, before, ask_t, t1);
+      ask_t = load.next;
+      if (load.kv0 >= load.kv1) continue;                    // (only places before a row tile's chunks)
+      if (lane == 0) sm.queue[warp][found % kQueue] = load;
+      ++found;
+      load_j = load.kv0;
+      load_end = load.kv1;
+      block = -1;
+      return true;
     }
+    return false;
   };
-  uint32_t asked = 0, used = 0;      // chunks that were asked for, and used
-  Walk load = {};
-  bool more = t0 < t1;
-  if (more) {
-    load.t = t0;
-    load.s = segment_at(sm.line, before, t0, t1);
-    load.n = (load.s.kv1 - load.s.kv0) * (kTile / kChunk);
-    load.x = warp;
-  }
-  auto page_of = [&](const Walk& w) {  // lane x < 32 / piece: the page of the chunk's x-th piece
-    const int64_t slot = chunk_slot(w.s, w.x) + (lane << piece_shift);
-    return lane < (kChunk >> piece_shift) && seen_by_some(sm.line, w.s.r, static_cast<int>(slot), piece)
-               ? a.table[static_cast<int64_t>(w.s.request) * a.width + (slot >> a.shift)]
-               : INT_MIN;              // (left out)
-  };
-  int page_now = INT_MIN;
-  if (more) more = settle(load);
-  if (more) page_now = page_of(load);
+  bool more = settle();
   auto ask = [&]() {
-    const uint32_t stage = asked % a.stages;
-    const int slot = chunk_slot(load.s, load.x) + (lane << piece_shift);
-    int page = page_now;
-    bool wanted = page != INT_MIN;
+    const int s0 = tile_slot<kChunk>(load.r, load_j), slot = s0 + (lane << piece_shift);
+    const int entry = s0 >> a.shift;
+    const int end = load.r.len + load.r.nodes;
+    if ((entry >> 5) != block) {
+      block = entry >> 5;
+      const int e = 32 * block + lane;
+      page_now = (static_cast<int64_t>(e) << a.shift) < end ? a.table[static_cast<int64_t>(load.request) * a.width + e] : -1;
+    }
+    const int page = __shfl_sync(0xFFFFFFFFu, page_now, (entry + (a.shift < 5 ? lane : 0)) & 31);
+    bool wanted = copies && slot < end;
+    if (a.window > 0) wanted = wanted && (slot < a.sinks || slot + (1 << piece_shift) > load.r.len - a.window + 1);
     if (wanted && (page < 0 || page >= a.pages)) {
-      mark_bad(a, load.s.request, SV_DEV_BAD_PAGE);
+      mark_bad(a, load.request, SV_DEV_BAD_PAGE);
       wanted = false;
     }
-    const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, wanted)) * (piece >> 3) * kGroupBytes;
-    if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][stage], bytes);
+    constexpr int kUnit = kGroupBytes / 8;                    // bytes of a slot
+    uint64_t* bar = &sm.full[warp][ask_stage];
+    const int bytes = (__popc(__ballot_sync(0xFFFFFFFFu, wanted)) << piece_shift) * kUnit;
+    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
     __syncwarp();
     if (wanted)
-      bulk_g2s(ring + stage * kChunkBytes + (lane << piece_shift >> 3) * kGroupBytes,
-               a.pool + page * a.page_stride + load.s.head * a.head_stride + ((slot & ((1 << a.shift) - 1)) >> 3) * kGroupBytes,
-               (piece >> 3) * kGroupBytes, &sm.full[warp][stage]);
+      bulk_g2s(ring + ask_stage * kChunkBytes + (lane << piece_shift) * kUnit,
+               a.pool + page * a.page_stride + load.head * a.head_stride + (slot & ((1 << a.shift) - 1)) * kUnit,
+               kUnit << piece_shift, bar);
+    ask_stage = ask_stage + 1 == static_cast<uint32_t>(a.stages) ? 0 : ask_stage + 1;
     ++asked;
-    load.x += kWarps;
-    more = settle(load);
-    if (more) page_now = page_of(load);
+    ++load_j;
+    more = settle();
   };
   while (more && asked < static_cast<uint32_t>(a.stages)) ask();
 
   // ---- row tiles --------------------------------------------------------------------------------------
-  for (uint32_t t = t0; t < t1;) {
-    const Segment s = segment_at(sm.line, before, t, t1);
-    const uint32_t after = s.next;
-    if (s.kv0 >= s.kv1) {  // the part begins or ends among the places before a row tile's cache tiles
-      t = after;
-      continue;
-    }
+  for (uint32_t seg = 0; seg < found; ++seg) {  // (a segment is found before the one before it ends)
+    __syncwarp();
+    const Segment s = sm.queue[warp][seg % kQueue];
     const int len = s.r.len, end = len + s.r.nodes;
     const int first_row = s.mtile * kRows, rows = min(kRows, s.r.nodes * a.group - first_row);
-    // this lane's rows: g and g + 8
-    int node[2], head[2], depth[2] = {0, 0}, near[2] = {0, 0};
-    float c[2];
-    uint32_t q[kSteps][4];
+    // Q': this lane has a quarter of row g of each column of eight, scaled by a power of two
+    uint32_t q[N][kSteps][2];
+    float c[N][2];                     // from here on this lane has rows 2 t4 and 2 t4 + 1 of each column of eight
+    int node[N][2], depth[N][2], near[N][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int local = g + 8 * h, row = first_row + local;
-      const bool exists = local < rows;
-      node[h] = exists ? row / a.group : -1;
-      head[h] = exists ? s.head * a.group + row - node[h] * a.group : 0;
+    for (int n = 0; n < N; ++n) {
+      const int local = 8 * n + g, row = first_row + local;
       uint4 w[D / 32];
-      if (exists) {
-        const uint4* from = reinterpret_cast<const uint4*>(a.q + (s.r.first + node[h]) * a.q_row_stride + head[h] * a.q_head_stride + t4 * (D / 4));
+      if (local < rows) {
+        const int its_node = row / a.group;
+        const uint4* from = reinterpret_cast<const uint4*>(a.q + (s.r.first + its_node) * a.q_row_stride +
+                                                           (s.head * a.group + row - its_node * a.group) * a.q_head_stride + t4 * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) w[i] = __ldg(from + i);
       } else {
@@ -285,70 +286,88 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const Attend4Para
       const int up = 14 - max(static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127, -100);
       const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
       // (not 0, however small the scale: masked scores are -inf)
-      c[h] = fmaxf(a.scale * 1.44269504088896341f * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1e-37f);
+      const float its_c = fmaxf(a.scale * 1.44269504088896341f * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1e-37f);
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        q[k][h] = pack_f16(bf16_lo(p[2 * k]) * by, bf16_hi(p[2 * k]) * by);
-        q[k][2 + h] = pack_f16(bf16_lo(p[2 * k + 1]) * by, bf16_hi(p[2 * k + 1]) * by);
-      }
-      if (a.window > 0 && exists) {
-        if (a.parent == nullptr) depth[h] = node[h];
-        else
-          for (int x = node[h]; x > 0; ++depth[h]) {
-            const int up_node = a.parent[s.r.first + x];
-            if (up_node < 0 || up_node >= x) break;  // reported where the node's own chunk is masked
-            x = up_node;
-          }
-        near[h] = len + depth[h] - a.window + 1;
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) q[n][k][i] = pack_f16(bf16_lo(p[2 * k + i]) * by, bf16_hi(p[2 * k + i]) * by);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        c[n][e] = __shfl_sync(0xFFFFFFFFu, its_c, 4 * (2 * t4 + e));
+        const int other = 8 * n + 2 * t4 + e;
+        node[n][e] = other < rows ? (first_row + other) / a.group : -1;
+        depth[n][e] = near[n][e] = 0;
+        if (a.window > 0 && other < rows) {
+          if (a.parent == nullptr) depth[n][e] = node[n][e];
+          else
+            for (int x = node[n][e]; x > 0; ++depth[n][e]) {
+              const int up_node = a.parent[s.r.first + x];
+              if (up_node < 0 || up_node >= x) break;  // reported where the node's own chunk is masked
+              x = up_node;
+            }
+          near[n][e] = len + depth[n][e] - a.window + 1;
+        }
       }
     }
-    float o[kEighth][4];
+    float o[kDimTiles][N][4];
 #pragma unroll
-    for (int i = 0; i < kEighth; ++i)
+    for (int i = 0; i < kDimTiles; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    const int chunks = (s.kv1 - s.kv0) * (kTile / kChunk);
-    for (int x = warp; x < chunks; x += kWarps) {
-      const int s0 = chunk_slot(s, x);
-      if (!seen_by_some(sm.line, s.r, s0, kChunk)) continue;
-      const uint32_t stage = used % a.stages;
-      warp_wait(&sm.full[warp][stage], (used / a.stages) & 1, &sm.dead, a.status);
-      const unsigned char* chunk = ring + stage * kChunkBytes;
-      float p[4][4];
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {  // eight slots: this lane has slot g's quarter t4
-        const unsigned char* group = chunk + u * kGroupBytes;
-        uint32_t w[kWords];
-        if constexpr (D == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(group + lane * 16);
-          w[0] = v.x;
-          w[1] = v.y;
-          w[2] = v.z;
-          w[3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(group + lane * 8);
-          w[0] = v.x;
-          w[1] = v.y;
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
+    float m[N][2], l[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = -INFINITY;
+        l[n][e] = 0.0f;
+      }
+    for (int j = s.kv0; j < s.kv1; ++j) {
+      const int s0 = tile_slot<kChunk>(s.r, j);
+      warp_wait(&sm.full[warp][use_stage], use_parity, &sm.dead, a.status);
+      const unsigned char* chunk = ring + use_stage * kChunkBytes;
+      float p[2][N][4];  // sixteen slots each: this lane has slots g and g + 8 of them
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[h][n][e] = 0.0f;
+        uint32_t w[2][kWords], sc[2][2];  // of both groups of eight: codes and scales of slot g's quarter t4
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const unsigned char* group = chunk + (2 * h + u) * kGroupBytes;
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(group + lane * 16);
+            w[u][0] = v.x;
+            w[u][1] = v.y;
+            w[u][2] = v.z;
+            w[u][3] = v.w;
+            const uint32_t two = decode_scales(*reinterpret_cast<const uint16_t*>(group + 4 * D + lane * 2));
+            sc[u][0] = __byte_perm(two, two, 0x1010);
+            sc[u][1] = __byte_perm(two, two, 0x3232);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(group + lane * 8);
+            w[u][0] = v.x;
+            w[u][1] = v.y;
+            const uint32_t one = decode_scales(group[4 * D + lane]);
+            sc[u][0] = sc[u][1] = __byte_perm(one, one, 0x1010);
+          }
         }
-        uint32_t sc[2];  // of the quarter's first and last sixteen dimensions (D = 64: of all its sixteen)
-        if constexpr (D == 128) {
-          const uint32_t two = decode_scales(*reinterpret_cast<const uint16_t*>(group + 4 * D + lane * 2));
-          sc[0] = __byte_perm(two, two, 0x1010);
-          sc[1] = __byte_perm(two, two, 0x3232);
-        } else {
-          const uint32_t one = decode_scales(group[4 * D + lane]);
-          sc[0] = sc[1] = __byte_perm(one, one, 0x1010);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[u][e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-          uint32_t h[4];
-          decode8(w[i], h);
-          const uint32_t by = sc[i / 2];
-          mma16(p[u], q[2 * i], mul_f16x2(h[0], by), mul_f16x2(h[1], by));
-          mma16(p[u], q[2 * i + 1], mul_f16x2(h[2], by), mul_f16x2(h[3], by));
+          uint32_t x0[4], x1[4];
+          decode8(w[0][i], x0);
+          decode8(w[1][i], x1);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t ka[4] = {mul_f16x2(x0[2 * k], sc[0][i / 2]), mul_f16x2(x1[2 * k], sc[1][i / 2]),
+                                    mul_f16x2(x0[2 * k + 1], sc[0][i / 2]), mul_f16x2(x1[2 * k + 1], sc[1][i / 2])};
+#pragma unroll
+            for (int n = 0; n < N; ++n) mma16(p[h][n], ka, q[n][2 * i + k][0], q[n][2 * i + k][1]);
+          }
         }
       }
       const bool whole = s0 + kChunk <= len && (a.window <= 0 || s0 + kChunk <= a.sinks || s0 >= end - a.window);
@@ -357,216 +376,229 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const Attend4Para
         const int lo = a.window > 0 ? max(0, len - a.window + 1) : 0;
         live = range_bits(lo, end, s0) | (a.window > 0 ? range_bits(0, min(a.sinks, end), s0) : 0u);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t see = 0;
-          if (node[h] >= 0) {
-            see = range_bits(near[h], len, s0) | (a.window > 0 ? range_bits(0, min(a.sinks, len), s0) : 0u);
-            if (s0 + kChunk > len) {
-              int d = depth[h];
-              for (int at = node[h];; --d) {
-                const int bit = len + at - s0;
-                if (bit >= 0 && bit < kChunk && (a.window <= 0 || len + d >= near[h] || len + d < a.sinks)) see |= 1u << bit;
-                if (at <= 0 || bit < 0) break;
-                const int up_node = a.parent != nullptr ? a.parent[s.r.first + at] : at - 1;
-                if (up_node < 0 || up_node >= at) {
-                  mark_bad(a, s.request, SV_DEV_BAD_PARENT);
-                  break;
-                }
-                at = up_node;
-              }
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!((see >> (8 * u + 2 * t4 + e)) & 1u)) p[u][2 * h + e] = -INFINITY;
-        }
-      }
-      float top[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(fmaxf(fmaxf(p[0][2 * h], p[0][2 * h + 1]), fmaxf(p[1][2 * h], p[1][2 * h + 1])),
-                       fmaxf(fmaxf(p[2][2 * h], p[2][2 * h + 1]), fmaxf(p[3][2 * h], p[3][2 * h + 1]))) * c[h];  // c > 0
-      }
-      if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kLazyGrowth4 || top[1] > m[1] + kLazyGrowth4)) {  // (m = -inf: some slot is seen)
-        float keep[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float now = fmaxf(m[h], quad_max(top[h]));
-          keep[h] = m[h] == -INFINITY ? 0.0f : ex2_approx(m[h] - now);
-          m[h] = now;
-          l[h] *= keep[h];
-        }
-#pragma unroll
-        for (int i = 0; i < kEighth; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= keep[e >> 1];
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float off = m[h] == -INFINITY ? 0.0f : kBias - m[h];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int n = 0; n < N; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            p[u][2 * h + e] = ex2_approx(fmaf(p[u][2 * h + e], c[h], off));
-            l[h] += p[u][2 * h + e];
+            uint32_t see = 0;
+            if (node[n][e] >= 0) {
+              see = range_bits(near[n][e], len, s0) | (a.window > 0 ? range_bits(0, min(a.sinks, len), s0) : 0u);
+              if (s0 + kChunk > len) {
+                int d = depth[n][e];
+                for (int at = node[n][e];; --d) {
+                  const int bit = len + at - s0;
+                  if (bit >= 0 && bit < kChunk && (a.window <= 0 || len + d >= near[n][e] || len + d < a.sinks)) see |= 1u << bit;
+                  if (at <= 0 || bit < 0) break;
+                  const int up_node = a.parent != nullptr ? a.parent[s.r.first + at] : at - 1;
+                  if (up_node < 0 || up_node >= at) {
+                    mark_bad(a, s.request, SV_DEV_BAD_PARENT);
+                    break;
+                  }
+                  at = up_node;
+                }
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                if (!((see >> (16 * h + 8 * u + g)) & 1u)) p[h][n][2 * u + e] = -INFINITY;
           }
       }
+      float top[N][2];
+      bool grows = false;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {  // sixteen slots: this lane has pair t4 of both groups, and eighth g of the dimensions
-        const uint32_t pa[4] = {pack_f16(p[2 * k][0], p[2 * k][1]), pack_f16(p[2 * k][2], p[2 * k][3]),
-                                pack_f16(p[2 * k + 1][0], p[2 * k + 1][1]), pack_f16(p[2 * k + 1][2], p[2 * k + 1][3])};
-        uint32_t b[2][kEighth];
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[n][e] = fmaxf(fmaxf(p[0][n][e], p[0][n][2 + e]), fmaxf(p[1][n][e], p[1][n][2 + e])) * c[n][e];  // c > 0
+          grows |= top[n][e] > m[n][e] + kLazyGrowth4;  // (m = -inf: some slot is seen)
+        }
+      if (__any_sync(0xFFFFFFFFu, grows)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float now = fmaxf(m[n][e], column_max(top[n][e]));
+            const float keep = m[n][e] == -INFINITY ? 0.0f : ex2_approx(m[n][e] - now);
+            m[n][e] = now;
+            l[n][e] *= keep;
+#pragma unroll
+            for (int i = 0; i < kDimTiles; ++i) {
+              o[i][n][e] *= keep;
+              o[i][n][2 + e] *= keep;
+            }
+          }
+      }
+      uint32_t pb[2][N][2];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float off[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) off[e] = m[n][e] == -INFINITY ? 0.0f : kBias - m[n][e];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[h][n][e] = ex2_approx(fmaf(p[h][n][e], c[n][e & 1], off[e & 1]));
+            l[n][e & 1] += p[h][n][e];
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) pb[h][n][u] = transpose8(pack_f16(p[h][n][2 * u], p[h][n][2 * u + 1]));
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // sixteen slots: this lane has pair t4 of both groups, and eighth g of the dimensions
+        uint32_t even[2][kWords / 2], odd[2][kWords / 2], by[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const unsigned char* group = chunk + (2 * k + u) * kGroupBytes + 4 * D + D / 2;
-          uint32_t even[kWords / 2], odd[kWords / 2];
+          const unsigned char* group = chunk + (2 * h + u) * kGroupBytes + 4 * D + D / 2;
           if constexpr (D == 128) {
             const uint4 v = *reinterpret_cast<const uint4*>(group + lane * 16);
-            even[0] = v.x;
-            even[1] = v.y;
-            odd[0] = v.z;
-            odd[1] = v.w;
+            even[u][0] = v.x;
+            even[u][1] = v.y;
+            odd[u][0] = v.z;
+            odd[u][1] = v.w;
           } else {
             const uint2 v = *reinterpret_cast<const uint2*>(group + lane * 8);
-            even[0] = v.x;
-            odd[0] = v.y;
+            even[u][0] = v.x;
+            odd[u][0] = v.y;
           }
-          uint32_t by = decode_scales(*reinterpret_cast<const uint16_t*>(group + 4 * D + (D == 128 ? lane * 2 : (g >> 1) * 8 + t4 * 2)));
+          by[u] = decode_scales(*reinterpret_cast<const uint16_t*>(group + 4 * D + (D == 128 ? lane * 2 : (g >> 1) * 8 + t4 * 2)));
           if (!whole) {  // 0 times what an unseen slot holds has to be 0
-            const uint32_t bits = live >> (8 * (2 * k + u) + 2 * t4);
-            by &= ((bits & 1u) ? 0xFFFFu : 0u) | ((bits & 2u) ? 0xFFFF0000u : 0u);
-          }
-#pragma unroll
-          for (int i = 0; i < kWords / 2; ++i) {
-            uint32_t h[4];
-            decode8((even[i] & 0x0F0F0F0Fu) | ((odd[i] << 4) & 0xF0F0F0F0u), h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b[u][8 * i + 2 * e] = mul_f16x2(h[e], by);
-            decode8(((even[i] >> 4) & 0x0F0F0F0Fu) | (odd[i] & 0xF0F0F0F0u), h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b[u][8 * i + 2 * e + 1] = mul_f16x2(h[e], by);
+            const uint32_t bits = live >> (16 * h + 8 * u + 2 * t4);
+            by[u] &= ((bits & 1u) ? 0xFFFFu : 0u) | ((bits & 2u) ? 0xFFFF0000u : 0u);
           }
         }
 #pragma unroll
-        for (int i = 0; i < kEighth; ++i) mma16(o[i], pa, b[0][i], b[1][i]);
+        for (int i = 0; i < kWords / 2; ++i) {
+          uint32_t v[2][2][4];  // [group][dimension's parity]: pairs of slots
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            decode8((even[u][i] & 0x0F0F0F0Fu) | ((odd[u][i] << 4) & 0xF0F0F0F0u), v[u][0]);
+            decode8(((even[u][i] >> 4) & 0x0F0F0F0Fu) | (odd[u][i] & 0xF0F0F0F0u), v[u][1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // dimensions 8 i + 2 e in the tile's rows g, and the next ones in its rows g + 8
+            const uint32_t va[4] = {mul_f16x2(v[0][0][e], by[0]), mul_f16x2(v[0][1][e], by[0]), mul_f16x2(v[1][0][e], by[1]),
+                                    mul_f16x2(v[1][1][e], by[1])};
+#pragma unroll
+            for (int n = 0; n < N; ++n) mma16(o[4 * i + e][n], va, pb[h][n][0], pb[h][n][1]);
+          }
+        }
       }
       ++used;
+      use_stage = use_stage + 1 == static_cast<uint32_t>(a.stages) ? 0 : use_stage + 1;
+      use_parity ^= use_stage == 0;
       __syncwarp();  // every lane has read the stage
       if (more) ask();
     }
-    // ---- the segment's end: the warps' results together ----------------------------------------------
+    // ---- the segment's end -----------------------------------------------------------------------------
+    const bool complete = s.kv0 == 0 && s.kv1 == s.r.tiles;
+    float* part = a.parts + static_cast<int64_t>(2 * me + (s.kv0 == 0)) * part4_floats<D, N>();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] = quad_sum(l[h]);
-      if (t4 == 0) {
-        sm.m[warp][g + 8 * h] = m[h];
-        sm.l[warp][g + 8 * h] = l[h];
-      }
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int col = 0; col < 2; ++col)  // columns i of eighths 2 t4 and 2 t4 + 1
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] = column_sum(l[n][e]);
+        const int r = 8 * n + 2 * t4 + e;
+        if (r >= rows) continue;
+        const int head = s.head * a.group + (first_row + r - node[n][e] * a.group);
+        // this lane's eighth of the dimensions
+        if (complete) {
+          // Every row sees its own node's slot, so a sum that is not above 0 is that of a row without a softmax (NaN among its
+          // scores, or nothing but -inf): its outputs are NaN.
+          const float inv = l[n][e] > 0.0f ? a.v_scale / l[n][e] : NAN;
+          uint4* to = reinterpret_cast<uint4*>(a.out + (s.r.first + node[n][e]) * a.out_row_stride + head * a.out_head_stride + g * (D / 8));
 #pragma unroll
-        for (int i = 0; i < kEighth; i += 4)
-          *reinterpret_cast<float4*>(mix + (warp * kRows + g + 8 * h) * (D + 4) + (2 * t4 + col) * kEighth + i) =
-              make_float4(o[i][2 * h + col], o[i + 1][2 * h + col], o[i + 2][2 * h + col], o[i + 3][2 * h + col]);
-    }
-    __syncthreads();
-    {
-      constexpr int kPer = kThreads4 / kRows;  // threads of a row
-      const int r = tid / kPer, at = tid % kPer;
-      const bool complete = s.kv0 == 0 && s.kv1 == s.r.tiles;
-      float top = -INFINITY, sum = 0.0f, w[kWarps];
+          for (int i = 0; i < kDimTiles; i += 4)
+            to[i / 4] = make_uint4(pack_bf16x2(o[i][n][e] * inv, o[i][n][2 + e] * inv), pack_bf16x2(o[i + 1][n][e] * inv, o[i + 1][n][2 + e] * inv),
+                                   pack_bf16x2(o[i + 2][n][e] * inv, o[i + 2][n][2 + e] * inv), pack_bf16x2(o[i + 3][n][e] * inv, o[i + 3][n][2 + e] * inv));
+          if (g == 0 && a.lse != nullptr)
+            a.lse[(s.r.first + node[n][e]) * a.q_heads + head] = (m[n][e] - kBias + log2f(l[n][e])) * 0.693147180559945309f;
+        } else {
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sm.m[x][r]);
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) {
-        // (a warp that saw nothing of the row has m = -inf and sums of 0; one whose scores are NaN has NaN sums)
-        w[x] = sm.m[x][r] == -INFINITY ? (sm.l[x][r] == 0.0f ? 0.0f : NAN) : ex2_approx(sm.m[x][r] - top);
-        sum += w[x] == 0.0f ? 0.0f : w[x] * sm.l[x][r];
-      }
-      const int row = first_row + r, its_node = row / a.group, its_head = s.head * a.group + row - its_node * a.group;
-      // Every row sees its own node's slot, so a sum that is not above 0 is that of a row without a softmax: its outputs are NaN.
-      const float inv = complete ? (sum > 0.0f ? a.v_scale / sum : NAN) : 1.0f;
-      if (r < rows) {
-        float* part = a.parts + static_cast<int64_t>(2 * blockIdx.x + (s.kv0 == 0)) * part4_floats<D>();
-#pragma unroll
-        for (int i = 4 * at; i < D; i += 4 * kPer) {
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int x = 0; x < kWarps; ++x) {
-            const float4 y = *reinterpret_cast<const float4*>(mix + (x * kRows + r) * (D + 4) + i);
-            if (w[x] == 0.0f) continue;
-            v.x += w[x] * y.x;
-            v.y += w[x] * y.y;
-            v.z += w[x] * y.z;
-            v.w += w[x] * y.w;
-          }
-          if (complete)
-            *reinterpret_cast<uint2*>(a.out + (s.r.first + its_node) * a.out_row_stride + its_head * a.out_head_stride + i) =
-                make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-          else
-            *reinterpret_cast<float4*>(part + r * D + i) = v;
-        }
-        if (at == 0) {
-          if (!complete) {
-            part[kRows * D + r] = top;
-            part[kRows * D + kRows + r] = sum;
-          } else if (a.lse != nullptr) {
-            a.lse[(s.r.first + its_node) * a.q_heads + its_head] = (top - kBias + log2f(sum)) * 0.693147180559945309f;
+          for (int i = 0; i < kDimTiles; i += 2)
+            *reinterpret_cast<float4*>(part + r * D + g * (D / 8) + 2 * i) =
+                make_float4(o[i][n][e], o[i][n][2 + e], o[i + 1][n][e], o[i + 1][n][2 + e]);
+          if (g == 0) {
+            part[kRows * D + r] = m[n][e];
+            part[kRows * D + kRows + r] = l[n][e];
           }
         }
       }
-      if (tid == 0 && s.kv0 == 0 && !complete) {
-        const uint32_t ends = s.begin + a.extra + s.r.tiles - 1;  // the CTA in which the row tile ends
-        const Job job = {1, s.request, s.head, s.mtile, rows, static_cast<int32_t>(blockIdx.x), parts.of(ends), 0};
-        a.jobs[blockIdx.x] = job;
-      }
+    if (lane == 0 && s.kv0 == 0 && !complete) {
+      const uint32_t ends = s.begin + a.extra + s.r.tiles - 1;  // the part in which the row tile ends
+      const Job job = {1, s.request, s.head, s.mtile, rows, static_cast<int32_t>(me), parts.of(ends), 0};
+      a.jobs[atomicAdd(a.n_jobs, 1)] = job;
     }
-    __syncthreads();
-    t = after;
   }
   // (after a wait that ran out: no copy may be in flight when the CTA leaves)
-  for (; used < asked; ++used) mbar_wait(&sm.full[warp][used % a.stages], (used / a.stages) & 1, a.status);
+  for (; used < asked; ++used) {
+    mbar_wait(&sm.full[warp][use_stage], use_parity, a.status);
+    use_stage = use_stage + 1 == static_cast<uint32_t>(a.stages) ? 0 : use_stage + 1;
+    use_parity ^= use_stage == 0;
+  }
 }
 
-// Adds the partial results of row tile `jobs[x]`: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i; a thread
-// has four columns of a row.  Then the outputs of bad requests become 0.
-template <int D>
-__global__ void __launch_bounds__(kRows * D / 4) join4_kernel(const Attend4Params a) {
+// Adds the partial results of row tile `jobs[x]`: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  A thread
+// has four columns of a row and every kJoinGroups-th part (long contexts over few row tiles leave dozens).  Then the outputs
+// of bad requests become 0.
+constexpr int kJoinGroups = 2;
+template <int D, int N>
+__global__ void __launch_bounds__(kJoinGroups * 8 * N * D / 4) join4_kernel(const Attend4Params a) {
+  constexpr int kRows = Tile4<N>::kRows, kPieces = kRows * D / 4;
+  __shared__ float4 other_o[kPieces];
+  __shared__ float other_l[kRows];
   pdl_wait();
-  const Job job = a.jobs[blockIdx.x];
-  const int r = threadIdx.x / (D / 4), i = threadIdx.x % (D / 4) * 4;
-  if (job.valid != 0 && r < job.rows && !a.bad[job.request]) {
+  const int n_jobs = *a.n_jobs;
+  for (int x = blockIdx.x; x < n_jobs; x += gridDim.x) {
+    const Job job = a.jobs[x];
+    const int half = threadIdx.x / kPieces, at = threadIdx.x - half * kPieces, r = at / (D / 4), i = at % (D / 4) * 4;
+    const bool mine = r < job.rows && !a.bad[job.request];
     const int n = job.last - job.first + 1;
-    // part x > 0 is its CTA's first, part 0 its CTA's second
-    auto part_of = [&](int x) { return a.parts + static_cast<int64_t>(2 * (job.first + x) + (x == 0)) * part4_floats<D>(); };
+    // part x > 0 is its warp's first, part 0 its warp's second
+    auto part_of = [&](int y) { return a.parts + static_cast<int64_t>(2 * (job.first + y) + (y == 0)) * part4_floats<D, N>(); };
     float M = -INFINITY, L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (mine) {
+#pragma unroll 8
+      for (int y = 0; y < n; ++y) M = fmaxf(M, part_of(y)[kRows * D + r]);
 #pragma unroll 4
-    for (int x = 0; x < n; ++x) M = fmaxf(M, part_of(x)[kRows * D + r]);
-#pragma unroll 4
-    for (int x = 0; x < n; ++x) {
-      const float* part = part_of(x);
-      const float m = part[kRows * D + r], l = part[kRows * D + kRows + r];
-      const float w = m == -INFINITY ? (l == 0.0f ? 0.0f : NAN) : ex2_approx(m - M);
-      if (w == 0.0f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(part + r * D + i);
-      L += w * l;
-      o.x += w * v.x;
-      o.y += w * v.y;
-      o.z += w * v.z;
-      o.w += w * v.w;
+      for (int y = half; y < n; y += kJoinGroups) {
+        const float* part = part_of(y);
+        const float m = part[kRows * D + r], l = part[kRows * D + kRows + r];
+        const float4 v = *reinterpret_cast<const float4*>(part + r * D + i);
+        // (a part that saw nothing of the row has m = -inf and sums of 0; one whose scores are NaN has NaN sums)
+        const float w = m == -INFINITY ? (l == 0.0f ? 0.0f : NAN) : ex2_approx(m - M);
+        L += w * l;
+        o.x += w * v.x;
+        o.y += w * v.y;
+        o.z += w * v.z;
+        o.w += w * v.w;
+      }
     }
-    const float inv = L > 0.0f ? a.v_scale / L : NAN;
-    const int row = job.mtile * kRows + r, node = row / a.group, head = job.head * a.group + row - node * a.group;
-    const int64_t at = a.node_offsets[job.request] + node;
-    *reinterpret_cast<uint2*>(a.out + at * a.out_row_stride + head * a.out_head_stride + i) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (i == 0 && a.lse != nullptr) a.lse[at * a.q_heads + head] = (M - kBias + log2f(L)) * 0.693147180559945309f;
+    if (half == 1) {
+      other_o[at] = o;
+      if (i == 0) other_l[r] = L;
+    }
+    __syncthreads();
+    if (half == 0 && mine) {
+      const float4 v = other_o[at];
+      L += other_l[r];
+      const float inv = L > 0.0f ? a.v_scale / L : NAN;
+      const int row = job.mtile * kRows + r, node = row / a.group, head = job.head * a.group + row - node * a.group;
+      const int64_t to = a.node_offsets[job.request] + node;
+      *reinterpret_cast<uint2*>(a.out + to * a.out_row_stride + head * a.out_head_stride + i) =
+          make_uint2(pack_bf16x2((o.x + v.x) * inv, (o.y + v.y) * inv), pack_bf16x2((o.z + v.z) * inv, (o.w + v.w) * inv));
+      if (i == 0 && a.lse != nullptr) a.lse[to * a.q_heads + head] = (M - kBias + log2f(L)) * 0.693147180559945309f;
+    }
+    __syncthreads();
   }
-  clear_bad<D, kRows * D / 4>(a, a, a);
+  if (threadIdx.x == 0 && atomicAdd(a.n_jobs + 1, 1) == static_cast<int>(gridDim.x) - 1) {  // every CTA has read the count
+    a.n_jobs[0] = 0;
+    a.n_jobs[1] = 0;
+  }
+  clear_bad<D, kJoinGroups * kPieces>(a, a, a);
 }
 
 // ---- host --------------------------------------------------------------------------------------------
@@ -574,26 +606,31 @@ struct Layout4 {
   size_t bad, jobs, parts, total;
 };
 Layout4 layout4_of(int head_dim) {
+  // 16 warps of 8 rows, or 8 of 16: the same floats
+  static_assert(Tile4<1>::kWarps * part4_floats<128, 1>() == Tile4<2>::kWarps * part4_floats<128, 2>(), "parts");
   Layout4 L;
   L.bad = SV_STATUS_BYTES;
   L.jobs = L.bad + SV_MAX_BATCH;
-  L.parts = (L.jobs + sizeof(Job) * kMaxCtas + 255) & ~size_t(255);
-  L.total = L.parts + sizeof(float) * (head_dim == 128 ? part4_floats<128>() : part4_floats<64>()) * 2 * kMaxCtas;
+  L.parts = (L.jobs + sizeof(Job) * kMaxWarps * kMaxCtas + 255) & ~size_t(255);
+  L.total = L.parts + sizeof(float) * (head_dim == 128 ? part4_floats<128, 1>() : part4_floats<64, 1>()) * 2 * Tile4<1>::kWarps * kMaxCtas;
   return L;
 }
 
-template <int D>
+template <int D, int N>
 cudaError_t launch_attention4(Attend4Params& a, int ctas, void* stream) {
+  using T = Tile4<N>;
   constexpr int kChunkBytes = kChunk / 8 * 9 * D;
-  const int fixed = static_cast<int>(sizeof(float)) * kWarps * kRows * (D + 4) + 4 * a.B;
-  const int room = kSmemMax - static_cast<int>(sizeof(Smem4)) - 128 - fixed;
-  a.stages = std::min(kMaxStages4, room / (kWarps * kChunkBytes));  // at least 3
-  const size_t dyn = static_cast<size_t>(fixed) + static_cast<size_t>(kWarps) * a.stages * kChunkBytes;
-  cudaError_t e = allow_smem<attend4_kernel<D>>(kSmemMax - sizeof(Smem4) - 128);
+  const int room = kSmemMax - static_cast<int>(sizeof(Smem4)) - 128 - 4 * a.B;
+  a.stages = std::min(kMaxStages4, room / (T::kWarps * kChunkBytes));  // at least 2
+  const size_t dyn = 4 * static_cast<size_t>(a.B) + static_cast<size_t>(T::kWarps) * a.stages * kChunkBytes;
+  cudaError_t e = allow_smem<attend4_kernel<D, N>>(kSmemMax - sizeof(Smem4) - 128);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attend4_kernel<D>, dim3(ctas), kThreads4, dyn, stream, SV_KERNEL_ATTENTION, 1, a);
+  e = launch_dependent(attend4_kernel<D, N>, dim3(ctas), T::kThreads, dyn, stream, SV_KERNEL_ATTENTION, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(join4_kernel<D>, dim3(ctas), kRows * D / 4, 0, stream, SV_KERNEL_ATTENTION_JOIN, 1, a);
+  // row tiles to join: at most all, and at most a part's worth each
+  const int64_t row_tiles = static_cast<int64_t>(a.B) * a.kv_heads * ((static_cast<int64_t>(a.Nmax) * a.group + T::kRows - 1) / T::kRows);
+  const int joins = static_cast<int>(std::min<int64_t>(row_tiles, 8 * ctas));
+  return launch_dependent(join4_kernel<D, N>, dim3(joins), kJoinGroups * T::kRows * D / 4, 0, stream, SV_KERNEL_ATTENTION_JOIN, 1, a);
 }
 
 }  // namespace
@@ -637,8 +674,9 @@ sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64
   if ((s = check_workspace(ws, ws_bytes, sv_attention4_workspace_size(c, q_heads))) != SV_OK) return s;
   const int group = q_heads / c->kv_heads;
   // the line of work is counted in 32 bits
-  const int64_t tiles = ((static_cast<int64_t>(table_width) * c->page_size + kTile - 1) / kTile + 1 + kExtra4) *
-                        ((static_cast<int64_t>(Nmax) * group + kRows - 1) / kRows);
+  const int rows = Nmax * group <= 8 ? 8 : 16;
+  const int64_t tiles = ((static_cast<int64_t>(table_width) * c->page_size + kChunk - 1) / kChunk + 1 + kExtra4) *
+                        ((static_cast<int64_t>(Nmax) * group + rows - 1) / rows);
   if (tiles > INT_MAX || tiles * c->kv_heads > INT_MAX || tiles * c->kv_heads * B > INT_MAX)
     return set_error(SV_ERR_INVALID_ARG, "B=%d requests of up to %lld tiles a head are too many for one call", B, (long long)tiles);
   int sms = 0;
@@ -664,6 +702,7 @@ sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64
   a.head_stride = c->head_stride;
   a.status = reinterpret_cast<uint32_t*>(w);
   a.any_bad = reinterpret_cast<int32_t*>(w) + 1;
+  a.n_jobs = reinterpret_cast<int32_t*>(w) + 3;
   a.bad = w + L.bad;
   a.jobs = reinterpret_cast<Job*>(w + L.jobs);
   a.parts = reinterpret_cast<float*>(w + L.parts);
@@ -676,13 +715,15 @@ sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64
   a.q_heads = q_heads;
   a.kv_heads = c->kv_heads;
   a.group = group;
-  a.tile_rows = kRows;
+  a.tile_rows = rows;
   a.window = window;
   a.sinks = sinks;
   a.scale = scale * c->k_scale;
   a.v_scale = c->v_scale;
   a.extra = kExtra4;
-  return launch_status(c->head_dim == 128 ? launch_attention4<128>(a, ctas, stream) : launch_attention4<64>(a, ctas, stream), "attention");
+  const auto launch = c->head_dim == 128 ? (rows == 8 ? launch_attention4<128, 1> : launch_attention4<128, 2>)
+                                         : (rows == 8 ? launch_attention4<64, 1> : launch_attention4<64, 2>);
+  return launch_status(launch(a, ctas, stream), "attention");
 }
 
 }  // extern "C"

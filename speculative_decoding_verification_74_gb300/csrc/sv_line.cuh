@@ -10,7 +10,6 @@
 namespace sv {
 namespace {
 
-constexpr int kTile = 128;                 // slots of the cache in a tile
 constexpr int kMaxCtas = 152;              // SMs of the GPU: one CTA each
 constexpr int kSmemMax = 232448;           // shared memory that a CTA can have
 
@@ -39,7 +38,7 @@ struct Outputs {
 };
 
 // ---- the line of work ------------------------------------------------------------------------------
-// A request's part: its cache tiles are [0, sink_tiles) and [near_tile, ...).
+// T: slots of a cache tile.  A request's part: its cache tiles are [0, sink_tiles) and [near_tile, ...).
 struct Request {
   int64_t first;       // its first query row
   int32_t len, nodes;
@@ -47,6 +46,7 @@ struct Request {
   int32_t mtiles;      // row tiles per key/value head
   uint32_t bad;        // SV_DEV_* bits
 };
+template <int T>
 __device__ __forceinline__ Request request_of(const Line& a, int i) {
   Request r = {};
   const int64_t first = a.node_offsets[i], last = a.node_offsets[i + 1];
@@ -63,11 +63,11 @@ __device__ __forceinline__ Request request_of(const Line& a, int i) {
   }
   r.len = static_cast<int32_t>(len);
   r.nodes = static_cast<int32_t>(nodes);
-  const int all = static_cast<int>((len + nodes + kTile - 1) / kTile);
+  const int all = static_cast<int>((len + nodes + T - 1) / T);
   if (a.window > 0) {
     const int lo = max(0, r.len - a.window + 1);
-    r.near_tile = lo / kTile;
-    r.sink_tiles = min(static_cast<int>((static_cast<int64_t>(min(a.sinks, lo)) + kTile - 1) / kTile), r.near_tile);
+    r.near_tile = lo / T;
+    r.sink_tiles = min(static_cast<int>((static_cast<int64_t>(min(a.sinks, lo)) + T - 1) / T), r.near_tile);
   }
   r.tiles = r.sink_tiles + all - r.near_tile;
   r.mtiles = (r.nodes * a.group + a.tile_rows - 1) / a.tile_rows;
@@ -81,6 +81,7 @@ struct Segment {
   uint32_t begin, next;  // places of the line: the row tile's first, and the one after this stretch
 };
 // (a: in shared memory; a kernel parameter passed by reference is read through global memory, 0.3 us a field)
+template <int T>
 __device__ __noinline__ Segment segment_at(const Line& a, const uint32_t* before, uint32_t t, uint32_t end) {
   int lo = 0, hi = a.B;  // the last request whose tiles begin at or before t
   while (hi - lo > 1) {
@@ -89,7 +90,7 @@ __device__ __noinline__ Segment segment_at(const Line& a, const uint32_t* before
   }
   Segment s;
   s.request = lo;
-  s.r = request_of(a, lo);
+  s.r = request_of<T>(a, lo);
   const uint32_t places = s.r.tiles + a.extra, local = t - before[lo], unit = local / places, at = local - unit * places;
   const uint32_t to = min(places, at + (end - t));
   s.begin = t - at;
@@ -100,8 +101,9 @@ __device__ __noinline__ Segment segment_at(const Line& a, const uint32_t* before
   s.mtile = static_cast<int>(unit - static_cast<uint32_t>(s.head) * s.r.mtiles);
   return s;
 }
+template <int T>
 __device__ __forceinline__ int tile_slot(const Request& r, int j) {
-  return (j < r.sink_tiles ? j : r.near_tile + (j - r.sink_tiles)) * kTile;
+  return (j < r.sink_tiles ? j : r.near_tile + (j - r.sink_tiles)) * T;
 }
 // The line in n parts as equal as can be: the first `longer` have a place more.  (32-bit arithmetic: a 64-bit division is
 // a page of code, and at a call's start code comes from behind the instruction cache.)

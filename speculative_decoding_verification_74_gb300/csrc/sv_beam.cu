@@ -1,19 +1,20 @@
 // sv_beam_select: one step of beam search, the K best of all beams' continuations.
 //
-// rows_kernel reads every row of logits once.  A row is cut into parts, one CTA each; a CTA takes its part in pieces of 16 KB
-// held in registers, the next one in flight, and keeps
+// rows_kernel reads every row of logits once; a row is cut into parts, a CTA each.  A warp takes every eighth piece of its CTA's
+// part, 2 KB held in registers, the next ones in flight, and keeps
 //   the sum of exp(x - ref) for a reference near the part's maximum: float32 terms, compensated sums;
-//   a list of candidates for the part's K largest logits.  A bound below the K-th largest lets few of them in: at first the
-//   smallest of G >= K groups' largest logits (a group is some threads' logits: K groups have a logit at or above it),
-//   later the K-th largest so far, and then only logits above it (an equal one further on comes after it).
-// Candidates are ranked by counting.  Pieces with more candidates than the list takes (long runs of equals) are worked off by
-// K rounds of a maximum.
+//   each lane's largest logit of each piece, in shared memory.
+// Then the CTA finds a bound that at least K of its threads' largest logits, and few more, are at or above (bisection, a barrier
+// that counts per step): the part's K best logits are at or above it too.  The pieces' lanes that reach it are read again (64 bytes each), and their logits
+// at or above the bound are ranked by counting.  Parts with too many of those (long runs of equals, or too few finite maxima for a
+// bound) are scanned in order instead, by one warp with a sorted list into which batches of candidates are merged.
 //
-// merge_kernel, a CTA per request, merges a row's parts, gives each row A = score - log sum exp(x - m), m its largest logit, and merges the
-// beams by A + (x - m), all in 64 bits (m apart: next to a large one the rest would be lost), best first.  The float32 terms leave A uncertain by up to about 2^-19 (each term by 2^-22 of ex2
-// and a few 2^-24 |y|, y its exponent; of E|y| <= log2 V; compensated sums add next to nothing).  So where the best two beams' totals
-// lie within kNear of each other, their rows are summed again with terms in pairs of floats (about 2^-30), and the
-// merge starts over: with this the order is that of the exact totals, down to 2^-29.
+// merge_kernel, a CTA per request, gives each row A = score - log sum exp(x - m), m its largest logit, so that a candidate's total
+// is A + (x - m) (m apart: next to a large one the rest would be lost).  A bisection on totals in float32 leaves little more
+// than K candidates, which are ranked by counting on totals in 64 bits.  The float32 terms leave A uncertain by up to about 2^-19
+// (each term by 2^-22 of ex2 and a few 2^-24 |y|, y its exponent, of E|y| <= log2 V; compensated sums add next to nothing).  So
+// where neighbours of different beams in the order lie within kNear of each other, their rows are summed again with terms in
+// pairs of floats (about 2^-30), and the ranking is repeated: with this the order is that of the exact totals, down to 2^-29.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,11 +28,11 @@ namespace sv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRowCtas = 3;                    // CTAs of the rows' kernel on an SM (1024 rows bf16 61 us; with 4 64, with 2 75)
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;                       // 16-byte vectors of a piece per thread
-constexpr int kPiece = kThreads * kVecs;       // vectors of a piece
-constexpr int kList = 1024;                    // candidates of a part
-constexpr int kKeep = 256;                     // listed candidates above which the list is cut to the K best
+constexpr int kVecs = 4;                       // 16-byte vectors of a piece per lane
+constexpr int kPiece = 32 * kVecs;             // vectors of a piece
+constexpr int kBatch = 64;                     // candidates that wait for the list
 constexpr int kMaxParts = 32;                  // parts of a row: a lane each in the merge
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kRefSlack = 30.0f;             // how far a logit may lie above a sum's reference
@@ -59,7 +60,7 @@ struct BeamParams {
   Part* parts;       // [rows][P]
   Entry* entries;    // [rows][P][K]
   uint32_t* status;
-  int32_t W, V, K, P, pad, groups;
+  int32_t W, V, K, P, pad, rows;
 };
 
 template <int DT>
@@ -79,6 +80,79 @@ __device__ __forceinline__ float element(const uint4 (&w)[kVecs], int i, int j) 
   const uint32_t* p = reinterpret_cast<const uint32_t*>(&w[i]);
   if constexpr (DT == SV_BF16) return (j & 1) ? bf16_hi(p[j >> 1]) : bf16_lo(p[j >> 1]);
   else return __uint_as_float(p[j]);
+}
+
+// One of a vector's elements, j known at run time only.
+template <int DT>
+__device__ __forceinline__ float element_at(const uint4& w, int j) {
+  if constexpr (DT == SV_BF16) {
+    const uint32_t pair = j < 4 ? (j < 2 ? w.x : w.y) : (j < 6 ? w.z : w.w);
+    return (j & 1) ? bf16_hi(pair) : bf16_lo(pair);
+  } else {
+    return __uint_as_float(j < 2 ? (j < 1 ? w.x : w.y) : (j < 3 ? w.z : w.w));
+  }
+}
+// Its largest element (NaN passed over).
+template <int DT>
+__device__ __forceinline__ float vec_max(const uint4& w) {
+  if constexpr (DT == SV_BF16) {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return fmaxf(bf16_lo(a), bf16_hi(a));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+}
+// The largest of a lane's elements of a piece.
+template <int DT>
+__device__ __forceinline__ float piece_max(const uint4 (&w)[kVecs]) {
+  if constexpr (DT == SV_BF16) {
+    uint32_t m[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int i = 1; i < kVecs; ++i) {
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(m[0]) : "r"(w[i].x));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(m[1]) : "r"(w[i].y));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(m[2]) : "r"(w[i].z));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(m[3]) : "r"(w[i].w));
+    }
+    return vec_max<DT>(make_uint4(m[0], m[1], m[2], m[3]));
+  } else {
+    float m = vec_max<DT>(w[0]);
+#pragma unroll
+    for (int i = 1; i < kVecs; ++i) m = fmaxf(m, vec_max<DT>(w[i]));
+    return m;
+  }
+}
+
+// At least K of a piece's logits are at or above it: every lane's vectors are groups, and at least K groups' largest logits are.
+// Found by bisection between the smallest and the largest of them, until little more than K are.
+__device__ __forceinline__ float group_bound(const float (&high)[kVecs], float mine, int K) {
+  float low = mine, top = mine;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) low = fminf(low, high[i]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, d));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  }
+  low = fmaxf(low, -FLT_MAX);          // (all groups are at or above it, or it is no bound at all)
+  float over = top;
+#pragma unroll 1
+  for (int step = 0; step < 10; ++step) {
+    const float mid = 0.5f * low + 0.5f * over;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) n += __popc(__ballot_sync(0xFFFFFFFFu, high[i] >= mid));
+    if (n >= K) {
+      low = mid;
+      if (n <= K + (K >> 2)) break;
+    } else {
+      over = mid;
+    }
+  }
+  return fmaxf(low, -FLT_MAX);         // (a piece of nothing but -inf)
 }
 
 // A row as 16-byte vectors: `lead` elements of the first lie before the row.
@@ -117,33 +191,57 @@ __device__ __noinline__ uint4 edge_vec(const Row& r, int vec) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <int DT>
-__device__ __forceinline__ void load_piece(const Row& r, int piece, uint4 (&w)[kVecs]) {
+__device__ __forceinline__ uint4 load_vec(const Row& r, int vec) {
   using E = Elem<DT>;
   const int last = (r.lead + r.V) % E::kPerVec != 0 ? r.vecs - 1 : r.vecs;  // vectors from here on are not whole
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int vec = piece * kPiece + i * kThreads + static_cast<int>(threadIdx.x);
-    if (vec >= (r.lead != 0 ? 1 : 0) && vec < last) {
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                   : "l"(r.base + static_cast<int64_t>(vec) * 16));
-    } else {
-      w[i] = vec < r.vecs ? edge_vec<DT>(r, vec) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
-    }
+  uint4 w;
+  if (vec >= (r.lead != 0 ? 1 : 0) && vec < last) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "l"(r.base + static_cast<int64_t>(vec) * 16));
+  } else {
+    w = vec < r.vecs ? edge_vec<DT>(r, vec) : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
   }
+  return w;
+}
+template <int DT>
+__device__ __forceinline__ void load_piece(const Row& r, int piece, uint4 (&w)[kVecs]) {
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) w[i] = load_vec<DT>(r, piece * kPiece + i * 32 + static_cast<int>(threadIdx.x & 31));
 }
 
+// Floats as integers in their order; 0 is below them all.
+__device__ __forceinline__ uint32_t float_key(float t) {
+  const uint32_t b = __float_as_uint(t + 0.0f);  // (-0 equals 0)
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float float_of_key(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k); }
+// A key that at least `want` threads' keys are at or above, at most `enough` where they differ; `least` where fewer are above that.
+// Every thread of the CTA calls it; most: the largest key; guess: where to look first.
+template <int kThreadsOfCta>
+__device__ __forceinline__ uint32_t lower_bound_of(uint32_t key, uint32_t least, uint32_t most, uint32_t guess, int want, int enough) {
+  static_assert(kThreadsOfCta >= SV_MAX_BEAM_CANDIDATES + 1, "a thread for each");
+  if (most <= least) return least;
+  uint32_t low = least, over = most + 1;
+  for (uint32_t mid = guess;;) {
+    if (mid <= low || mid >= over) mid = low + ((over - low) >> 1);
+    const int n = __syncthreads_count(key >= mid);
+    if (n >= want) {
+      low = mid;
+      if (n <= enough) return low;
+    } else {
+      over = mid;
+    }
+    if (over - low <= 1) return low;
+    mid = 0;
+  }
+}
 // Order of candidates as an integer: larger x first, then the lower token.
 __device__ __forceinline__ uint64_t order_key(float x, int token) {
-  const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 equals 0)
-  const uint32_t k = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  return (static_cast<uint64_t>(k) << 32) | ~static_cast<uint32_t>(token);
+  return (static_cast<uint64_t>(float_key(x)) << 32) | ~static_cast<uint32_t>(token);
 }
-__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
-  const uint32_t hi = static_cast<uint32_t>(k >> 32), top = __reduce_max_sync(0xFFFFFFFFu, hi);
-  const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, hi == top ? static_cast<uint32_t>(k) : 0u);
-  return (static_cast<uint64_t>(top) << 32) | lo;
-}
+__device__ __forceinline__ float logit_of(uint64_t key) { return float_of_key(static_cast<uint32_t>(key >> 32)); }
+__device__ __forceinline__ Entry entry_of(uint64_t key) { return Entry{logit_of(key), static_cast<int32_t>(~static_cast<uint32_t>(key))}; }
 // The next float above x (x finite or -inf).
 __device__ __forceinline__ float above(float x) {
   if (x == 0.0f) return __uint_as_float(1u);
@@ -151,201 +249,266 @@ __device__ __forceinline__ float above(float x) {
   return __uint_as_float((b & 0x80000000u) ? b - 1 : b + 1);
 }
 
-struct Shared {
-  Entry list[2][kList];
-  float lowest[kWarps], top[kWarps];
-  uint64_t best[kWarps];
-  unsigned long long sum;
-  int n;
+// Shared memory of a scan.
+struct Scan {
+  uint4 piece[kPiece];                       // a piece whose candidates are looked for
+  uint64_t list[2][SV_MAX_BEAM_CANDIDATES];  // keys, best first; the halves in turn
+  uint64_t batch[kBatch], sorted[32];
+  int32_t from, listed, waiting;             // the list's half and length, the batch's length
 };
 
-// The K best of list[from][0 .. n), in order, into the other half; fewer than K are followed by none.
-__device__ __forceinline__ void rank_list(Shared& sh, int from, int n, int K) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Entry e = sh.list[from][i];
-    const uint64_t key = order_key(e.x, e.token);
-    int rank = 0;
-    for (int j = 0; j < n; ++j) {
-      const Entry o = sh.list[from][j];
-      rank += order_key(o.x, o.token) > key;
-    }
-    if (rank < K) sh.list[from ^ 1][rank] = e;
+// How many of keys[0 .. n) (best first) are better than `key`.
+__device__ __forceinline__ int better(const uint64_t* keys, int n, uint64_t key) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (keys[mid] > key) lo = mid + 1; else hi = mid;
   }
-  for (int i = n + threadIdx.x; i < K; i += kThreads) sh.list[from ^ 1][i] = Entry{-INFINITY, -1};
+  return lo;
+}
+// Merges the batch's first n <= 32 keys into list[from][0 .. listed); returns the list's new length, in the other half.
+__device__ __noinline__ int merge_batch(Scan& sh, int from, int listed, int n, int K) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  const uint64_t key = lane < n ? sh.batch[lane] : 0;
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < n; ++j) rank += sh.batch[j] > key;
+  if (lane < n) sh.sorted[rank] = key;
+  __syncwarp();
+  uint64_t* to = sh.list[from ^ 1];
+  for (int i = lane; i < listed; i += 32) {
+    const uint64_t k = sh.list[from][i];
+    const int at = i + better(sh.sorted, n, k);
+    if (at < K) to[at] = k;
+  }
+  if (lane < n) {
+    const int at = rank + better(sh.list[from], listed, key);
+    if (at < K) to[at] = key;
+  }
+  __syncwarp();
+  return min(K, listed + n);
+}
+// The batch's first 32 into the list.
+__device__ __noinline__ void flush_batch(Scan& sh, int K) {
+  const int lane = threadIdx.x & 31, n = min(sh.waiting, 32), left = sh.waiting - n;
+  const int listed = merge_batch(sh, sh.from, sh.listed, n, K);
+  const uint64_t later = lane < left ? sh.batch[32 + lane] : 0;
+  __syncwarp();
+  if (lane < left) sh.batch[lane] = later;
+  if (lane == 0) {
+    sh.from ^= 1;
+    sh.listed = listed;
+    sh.waiting = left;
+  }
+  __syncwarp();
+}
+// The candidates of the piece in shared memory, whose vector v is at row vector first_vec + v: those at or above `bound` (until K
+// are listed also at or above the piece's own bound).  Returns the bound of the pieces after it.
+template <int DT>
+__device__ __noinline__ float scan_piece(Scan& sh, int first_vec, int lead, float bound, int K) {
+  using E = Elem<DT>;
+  const int lane = threadIdx.x & 31;
+  float high[kVecs], mine = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    high[i] = vec_max<DT>(sh.piece[i * 32 + lane]);
+    mine = fmaxf(mine, high[i]);
+  }
+  float least = sh.listed < K ? fmaxf(bound, group_bound(high, mine, K)) : bound;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    // the lanes whose vectors reach it, one by one: its elements go to as many lanes
+    uint32_t lanes = __ballot_sync(0xFFFFFFFFu, high[i] >= least);
+    while (lanes != 0) {
+      const int vec = i * 32 + __ffs(lanes) - 1;
+      lanes &= lanes - 1;
+      const float x = element_at<DT>(sh.piece[vec], lane & (E::kPerVec - 1));
+      const bool takes = lane < E::kPerVec && x >= least;
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, takes);
+      const int waiting = sh.waiting;
+      if (takes) sh.batch[waiting + __popc(who & ((1u << lane) - 1u))] = order_key(x, (first_vec + vec) * E::kPerVec + lane - lead);
+      __syncwarp();
+      if (lane == 0) sh.waiting = waiting + __popc(who);
+      __syncwarp();
+      if (waiting + __popc(who) >= 32) {
+        flush_batch(sh, K);
+        if (sh.listed == K) least = fmaxf(least, logit_of(sh.list[sh.from][K - 1]));  // no logit below the K-th counts
+      }
+    }
+  }
+  if (sh.waiting > 0 && sh.listed < K) flush_batch(sh, K);
+  return sh.listed == K ? above(logit_of(sh.list[sh.from][K - 1])) : -FLT_MAX;  // an equal logit further on comes after it
 }
 
+// A sum of exp(x - ref): terms 2^(k x - k ref), the product with k = log2 e exact but for one rounding; Kahan's sum.
+struct Sum {
+  float ref = 0.0f, sum = 0.0f, lost = 0.0f;
+  bool begun = false;                  // ref is a logit's
+};
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 3) rows_kernel(const BeamParams a) {
+__device__ __forceinline__ void add_piece(Sum& a, const uint4 (&w)[kVecs], float mine) {
   using E = Elem<DT>;
-  __shared__ Shared sh;
+  if (mine > (a.begun ? a.ref + kRefSlack : -INFINITY)) {
+    const float by = a.begun ? exp2f((a.ref - mine) * kLog2e) : 0.0f;
+    a.sum *= by;
+    a.lost *= by;
+    a.ref = mine;
+    a.begun = true;
+  }
+  float terms;
+  if (__any_sync(0xFFFFFFFFu, fabsf(a.ref) > 0x1p100f)) {  // k ref might overflow
+    terms = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < kVecs; ++i) {
+      const uint4 v = i < 2 ? (i < 1 ? w[0] : w[1]) : (i < 3 ? w[2] : w[3]);
+#pragma unroll 1
+      for (int j = 0; j < E::kPerVec; ++j) terms += ex2_approx((element_at<DT>(v, j) - a.ref) * kLog2e);
+    }
+  } else {
+    const float off = -a.ref * kLog2e, rest = fmaf(-a.ref, kLog2e, -off);  // off + rest = -k ref
+    const f32x2 k2 = f2_pack(kLog2e, kLog2e), off2 = f2_pack(off, off);
+    f32x2 s[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < E::kPerVec; j += 2)
+        s[(j >> 1) & 1] = f2_add(s[(j >> 1) & 1], f2_exp2_offset(f2_pack(element<DT>(w, i, j), element<DT>(w, i, j + 1)), k2, off2));
+    float s0, s1;
+    f2_unpack(f2_add(s[0], s[1]), s0, s1);
+    terms = fmaf(s0 + s1, rest * 0.693147181f, s0 + s1);  // 2^rest = 1 + rest ln 2
+  }
+  const float y = terms - a.lost, now = a.sum + y;
+  a.lost = (now - a.sum) - y;
+  a.sum = now;
+}
+
+constexpr int kGroups = 512;                   // lanes of pieces that are read again (of K = 128 about 250)
+constexpr int kFound = 1024;                   // their logits that are ranked
+// Shared memory of a CTA; then the maxima [pieces of the part][32].
+struct Shared {
+  union {
+    Scan scan;
+    struct {
+      uint64_t key[kFound];
+      int32_t group[kGroups];
+    } few;
+  };
+  unsigned long long sum;
+  float top[kWarps];
+  int n_groups, n_found;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, kRowCtas) rows_kernel(const BeamParams a) {
+  using E = Elem<DT>;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  Shared& sh = *reinterpret_cast<Shared*>(dyn);
+  float* maxima = reinterpret_cast<float*>(dyn + sizeof(Shared));
   pdl_wait();
   pdl_trigger();
-  const int64_t row = blockIdx.x / a.P;
-  const int part = static_cast<int>(blockIdx.x - row * a.P), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t id = blockIdx.x, row = id / a.P;
+  const int part = static_cast<int>(id - row * a.P), K = a.K;
   const float score = a.scores[row];
   if (!(fabsf(score) <= FLT_MAX) || (a.finished != nullptr && a.finished[row] != 0)) return;  // (the merge looks at neither)
   const Row r = row_of<DT>(a, row);
   const int pieces = (r.vecs + kPiece - 1) / kPiece;
   const int p0 = static_cast<int>(static_cast<int64_t>(pieces) * part / a.P), p1 = static_cast<int>(static_cast<int64_t>(pieces) * (part + 1) / a.P);
-  const int K = a.K;
   if (tid == 0) {
-    sh.n = 0;
     sh.sum = 0;
+    sh.n_groups = sh.n_found = 0;
   }
-  uint4 w[kVecs], next[kVecs];
-  if (p0 < p1) load_piece<DT>(r, p0, w);
-  float bound = 0.0f;                  // candidates are at or above it
-  float ref = -INFINITY, sum = 0.0f, lost = 0.0f, top = -INFINITY;
-  int from = 0, listed = 0;            // the list's half, and its length before this piece
-  bool first = true;
-  for (int piece = p0; piece < p1; ++piece) {
-    if (piece + 1 < p1) load_piece<DT>(r, piece + 1, next);
-    float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < E::kPerVec; j += 2) {
-        t0 = fmaxf(t0, element<DT>(w, i, j));
-        t1 = fmaxf(t1, element<DT>(w, i, j + 1));
-      }
-    const float mine = fmaxf(t0, t1);
-    top = fmaxf(top, mine);
-    auto group_bound = [&]() {  // at least K of this piece's logits are at or above it
-      float g = mine;
-      for (int d = 1; d < kThreads / a.groups; d <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
-      float low = g, high = g;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, d));
-        high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
-      }
-      if (lane == 0) {
-        sh.lowest[warp] = low;
-        sh.top[warp] = high;
-      }
-      __syncthreads();
-      low = sh.lowest[0];
-      high = sh.top[0];
-      for (int x = 1; x < kWarps; ++x) {
-        low = fminf(low, sh.lowest[x]);
-        high = fmaxf(high, sh.top[x]);
-      }
-      __syncthreads();
-      ref = ref == -INFINITY ? high : ref;
-      return fmaxf(low, -FLT_MAX);  // (-inf is no candidate)
+  float top = -INFINITY;
+  Sum total;
+  {
+    uint4 w[kVecs], next[kVecs];
+    auto step = [&](const uint4 (&x)[kVecs], int piece) {
+      const float mine = piece_max<DT>(x);
+      top = fmaxf(top, mine);
+      maxima[(piece - p0) * 32 + lane] = mine;
+      add_piece<DT>(total, x, mine);
     };
-    if (first) bound = group_bound();
-    // the sum
-    if (mine > ref + kRefSlack || (ref == -INFINITY && mine > -INFINITY)) {
-      const float by = ref == -INFINITY ? 0.0f : exp2f((ref - mine) * kLog2e);
-      sum *= by;
-      lost *= by;
-      ref = mine;
+    int piece = p0 + warp;
+    if (piece < p1) load_piece<DT>(r, piece, w);
+    for (; piece < p1; piece += 2 * kWarps) {
+      if (piece + kWarps < p1) load_piece<DT>(r, piece + kWarps, next);
+      step(w, piece);
+      if (piece + kWarps >= p1) break;
+      if (piece + 2 * kWarps < p1) load_piece<DT>(r, piece + 2 * kWarps, w);
+      step(next, piece + kWarps);
     }
-    {
-      const float at = ref == -INFINITY ? 0.0f : ref;  // (nothing but -inf so far: terms of 0)
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int j = 0; j < E::kPerVec; ++j) s[j & 3] += ex2_approx((element<DT>(w, i, j) - at) * kLog2e);
-      const float y = ((s[0] + s[1]) + (s[2] + s[3])) - lost, now = sum + y;  // Kahan's compensated sum
-      lost = (now - sum) - y;
-      sum = now;
-    }
-    // the candidates
-    auto collect = [&]() {
-      if (!(mine >= bound)) return;
-      int n = 0;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int j = 0; j < E::kPerVec; ++j) n += element<DT>(w, i, j) >= bound;
-      int at = atomicAdd(&sh.n, n);
-      if (at + n > kList) return;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int j = 0; j < E::kPerVec; ++j) {
-          const float x = element<DT>(w, i, j);
-          if (x >= bound) sh.list[from][at++] = Entry{x, (piece * kPiece + i * kThreads + tid) * E::kPerVec + j - r.lead};
-        }
-    };
-    collect();
-    int n = 0;
-    if (__syncthreads_or(mine >= bound)) {
-      n = sh.n;
-      if (n > kList && !first) {  // a bound from this piece's own groups
-        __syncthreads();
-        if (tid == 0) sh.n = listed;
-        bound = fmaxf(bound, group_bound());
-        collect();
-        __syncthreads();
-        n = sh.n;
-      }
-      if (n > kList) {  // the piece's K best, one by one
-        uint64_t before = ~uint64_t(0);
-        n = listed;
-        for (int k = 0; k < K; ++k) {
-          uint64_t best = 0;
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int j = 0; j < E::kPerVec; ++j) {
-              const float x = element<DT>(w, i, j);
-              const uint64_t key = order_key(x, (piece * kPiece + i * kThreads + tid) * E::kPerVec + j - r.lead);
-              if (x >= bound && key < before && key > best) best = key;
-            }
-          best = warp_max(best);
-          __syncthreads();
-          if (lane == 0) sh.best[warp] = best;
-          __syncthreads();
-          for (int x = 0; x < kWarps; ++x) best = max(best, sh.best[x]);
-          if (best == 0) break;
-          before = best;
-          if (tid == 0) {
-            const uint32_t b = static_cast<uint32_t>(best >> 32);
-            sh.list[from][n] = Entry{__uint_as_float((b & 0x80000000u) ? b & 0x7FFFFFFFu : ~b), static_cast<int32_t>(~static_cast<uint32_t>(best))};
-          }
-          ++n;
-        }
-        __syncthreads();
-      }
-      if (n > kKeep || (n >= K && (first || n >= 2 * K))) {
-        rank_list(sh, from, n, K);
-        from ^= 1;
-        n = K;
-        __syncthreads();
-        bound = above(sh.list[from][K - 1].x);
-      }
-      if (tid == 0) sh.n = n;
-      listed = n;
-      __syncthreads();
-    }
-    first = first && listed < K;   // (until K are listed every logit counts: the bound is -FLT_MAX or this piece's own)
-    if (first) bound = -FLT_MAX;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) w[i] = next[i];
   }
-  __syncthreads();
-  rank_list(sh, from, listed, K);
-  // the sum, relative to the part's largest logit
+  // the sum, relative to the part's largest logit; a NaN or +inf logit leaves one that is not finite
   float high = top;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
   if (lane == 0) sh.top[warp] = high;
+  const bool bad = __syncthreads_or(!(fabsf(total.sum) <= FLT_MAX) || high == INFINITY);
+#pragma unroll
+  for (int x = 0; x < kWarps; ++x) high = fmaxf(high, sh.top[x]);
+  uint64_t units = 0;
+  if (!bad && total.begun)
+    units = __float2ull_rn((total.sum - total.lost) * exp2f((total.ref - high) * kLog2e) * static_cast<float>(1ull << kFraction));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) units += __shfl_xor_sync(0xFFFFFFFFu, units, d);
+  if (lane == 0 && units != 0) atomicAdd(&sh.sum, static_cast<unsigned long long>(units));
+  // the bound: at least K threads' largest logits are at or above it, or it is the lowest there is
+  const float bound = float_of_key(lower_bound_of<kThreads>(float_key(top), float_key(-FLT_MAX), float_key(high), float_key(high - 8.0f), K, K + (K >> 2)));
+  const int groups = (p1 - p0) * 32;
+  for (int x = tid; x < groups; x += kThreads)
+    if (maxima[x] >= bound) {
+      const int at = atomicAdd(&sh.n_groups, 1);
+      if (at < kGroups) sh.few.group[at] = x;
+    }
   __syncthreads();
-  high = sh.top[0];
-  for (int x = 1; x < kWarps; ++x) high = fmaxf(high, sh.top[x]);
-  // a NaN or +inf logit leaves a sum that is not finite
-  const bool bad = __syncthreads_or(!(fabsf(sum) <= FLT_MAX) || high == INFINITY);
-  if (!bad && ref > -INFINITY) {
-    atomicAdd(&sh.sum, __float2ull_rn((sum - lost) * exp2f((ref - high) * kLog2e) * static_cast<float>(1ull << kFraction)));
+  const int n_groups = sh.n_groups;
+  if (n_groups <= kGroups) {
+    for (int x = tid; x < n_groups * kVecs; x += kThreads) {
+      const int g = sh.few.group[x / kVecs], vec = (p0 + (g >> 5)) * kPiece + (x % kVecs) * 32 + (g & 31);
+      const uint4 v = load_vec<DT>(r, vec);
+      if (vec_max<DT>(v) >= bound)
+#pragma unroll
+        for (int j = 0; j < E::kPerVec; ++j) {
+          const float e = element_at<DT>(v, j);
+          if (e >= bound) {
+            const int at = atomicAdd(&sh.n_found, 1);
+            if (at < kFound) sh.few.key[at] = order_key(e, vec * E::kPerVec + j - r.lead);
+          }
+        }
+    }
   }
   __syncthreads();
-  const int64_t at = row * a.P + part;
-  if (tid == 0) a.parts[at] = Part{sh.sum, high, bad};
-  for (int i = tid; i < K; i += kThreads) a.entries[at * K + i] = sh.list[from ^ 1][i];
+  const int n = n_groups <= kGroups ? sh.n_found : INT_MAX;
+  Entry* out = a.entries + id * K;
+  if (n <= kFound) {
+    for (int x = tid; x < n; x += kThreads) {
+      const uint64_t key = sh.few.key[x];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) rank += sh.few.key[j] > key;
+      if (rank < K) out[rank] = entry_of(key);
+    }
+    for (int x = n + tid; x < K; x += kThreads) out[x] = Entry{-INFINITY, -1};
+  } else if (warp == 0) {
+    Scan& scan = sh.scan;
+    if (lane == 0) scan.from = scan.listed = scan.waiting = 0;
+    __syncwarp();
+    float least = bound;
+    for (int piece = p0; piece < p1; ++piece) {
+      if (!__any_sync(0xFFFFFFFFu, maxima[(piece - p0) * 32 + lane] >= least)) continue;
+      uint4 w[kVecs];
+      load_piece<DT>(r, piece, w);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) scan.piece[i * 32 + lane] = w[i];
+      __syncwarp();
+      least = fmaxf(bound, scan_piece<DT>(scan, piece * kPiece, r.lead, least, K));
+      __syncwarp();
+    }
+    while (scan.waiting > 0) flush_batch(scan, K);
+    for (int i = lane; i < K; i += 32) out[i] = i < scan.listed ? entry_of(scan.list[scan.from][i]) : Entry{-INFINITY, -1};
+  }
+  if (tid == 0) a.parts[id] = Part{sh.sum, high, bad};
 }
 
 // ---- merge -----------------------------------------------------------------------------------------
@@ -372,17 +535,23 @@ __device__ __forceinline__ uint64_t exact_weight(float x, float m) {
   return __float2ull_rn(d * unit) + static_cast<uint64_t>(__float2ll_rn(low * unit));
 }
 
+constexpr int kRanked = 512;      // candidates that are ranked by counting: one a thread,
+constexpr int kFew = 128;         // or with a quarter of the others to a thread
 struct MergeShared {
   double A[SV_MAX_BEAMS];         // what is added to a beam's x - m
-  float m[SV_MAX_BEAMS];
+  float m[SV_MAX_BEAMS], high[SV_MAX_BEAMS], low[SV_MAX_BEAMS];  // and A as a pair of floats
   uint8_t exact[SV_MAX_BEAMS];    // A is not to be summed again
+  uint8_t live[SV_MAX_BEAMS];     // the beam's logits count
   uint8_t asked[SV_MAX_BEAMS];
+  uint64_t key[kRanked], out_key[SV_MAX_BEAM_CANDIDATES + 1];
+  uint32_t what[kRanked], out_what[SV_MAX_BEAM_CANDIDATES + 1];
   unsigned long long sum;
   uint32_t bad;
-  int again;
+  int again, n, counts[32], rank[kFew];
+  uint32_t tops[32];
 };
 
-// Totals as integers in their order.
+// Totals as integers in their order; 0 is below them all.
 __device__ __forceinline__ uint64_t total_key(double t) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(t + 0.0));
   return (b >> 63) ? ~b : b | (uint64_t(1) << 63);
@@ -391,71 +560,50 @@ __device__ __forceinline__ double total_of_key(uint64_t k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? k & ~(uint64_t(1) << 63) : ~k));
 }
 
+// high + low + (x - m), rounded once or twice: the rounding of each sum is kept (Knuth's exact sum).
+__device__ __forceinline__ float about_total(float high, float low, float x, float m) {
+  const float d = x - m, b = d - x, d_low = (x - (d - b)) - (m + b);
+  const float t = high + d, c = t - high;
+  return t + (((high - (t - c)) + (d - c)) + (low + d_low));
+}
+
+// What stands for a candidate: beam << kTokenBits | token, in the order of equal totals; kPad: the token is `pad`.
+constexpr int kTokenBits = 18;
+constexpr uint32_t kPad = 1u << 31, kTokenMask = (1u << kTokenBits) - 1u;
+
 template <int DT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a) {
   using E = Elem<DT>;
-  extern __shared__ Entry lists[];  // [W][K]
+  extern __shared__ uint32_t about[];  // [W][P][K] the totals in float32, as integers (0 = none)
   __shared__ MergeShared sh;
   pdl_wait();
   const int request = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = static_cast<int64_t>(request) * a.W;
-  const int K = a.K, W = a.W, P = a.P;
+  const int K = a.K, W = a.W, P = a.P, per_beam = P * K, N = W * per_beam;
+  static_assert(SV_MAX_SAMPLE_VOCAB <= 1 << kTokenBits && int64_t(SV_MAX_BEAMS) << kTokenBits <= int64_t(kPad), "what stands for a candidate");
   if (tid == 0) sh.bad = 0;
   __syncthreads();
-  // a row's parts: one list, one sum
-  for (int w = warp; w < W; w += kMergeThreads / 32) {
-    const int64_t row = row0 + w;
-    const float score = a.scores[row];
-    const bool done = a.finished != nullptr && a.finished[row] != 0;
-    Entry* list = lists + w * K;
-    if (!(score < INFINITY)) {
-      if (lane == 0) atomicOr(&sh.bad, 1u);
-    }
-    if (done || !(fabsf(score) <= FLT_MAX)) {
-      for (int i = lane; i < K; i += 32) list[i] = i == 0 && done && score > -INFINITY ? Entry{0.0f, a.pad} : Entry{-INFINITY, -1};
-      if (lane == 0) {
-        sh.A[w] = score;
-        sh.m[w] = 0.0f;
-        sh.exact[w] = 1;
-      }
-      continue;
-    }
-    Part part = lane < P ? a.parts[row * P + lane] : Part{0, -INFINITY, 0};
+  for (int w = warp; w < W; w += kMergeThreads / 32) {  // one sum of the parts'
+    const float score = a.scores[row0 + w];
+    if (!(score < INFINITY) && lane == 0) atomicOr(&sh.bad, 1u);
+    const bool lives = fabsf(score) <= FLT_MAX && (a.finished == nullptr || a.finished[row0 + w] == 0);
+    const Part part = lives && lane < P ? a.parts[(row0 + w) * P + lane] : Part{0, -INFINITY, 0};
     if (__any_sync(0xFFFFFFFFu, part.bad != 0) && lane == 0) atomicOr(&sh.bad, 1u);
     float m = part.m;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    double sum = part.m == -INFINITY ? 0.0 : static_cast<double>(part.sum) * exp2f((part.m - m) * kLog2e);
+    float sum = part.m == -INFINITY ? 0.0f : __ull2float_rn(part.sum) * exp2f((part.m - m) * kLog2e);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (lane == 0) {
-      sh.A[w] = static_cast<double>(score) - log(sum * (1.0 / static_cast<double>(1ull << kFraction)));
-      sh.m[w] = m;
-      sh.exact[w] = m == -INFINITY;  // (no candidates)
-    }
-    const Entry* from = a.entries + row * P * K;
-    if (P == 1) {
-      for (int i = lane; i < K; i += 32) list[i] = from[i];
-      continue;
-    }
-    // heads of the parts' lists; the one after is on its way
-    from += static_cast<int64_t>(lane) * K;
-    const Entry none = {-INFINITY, -1};
-    Entry head = lane < P ? from[0] : none, after = lane < P && K > 1 ? from[1] : none;
-    int taken = 0;
-    for (int k = 0; k < K; ++k) {
-      const uint64_t key = head.token < 0 ? 0 : order_key(head.x, head.token);
-      const uint64_t best = warp_max(key);
-      if (best == 0) {
-        for (int i = k + lane; i < K; i += 32) list[i] = none;
-        break;
-      }
-      if (key == best) {
-        list[k] = head;
-        head = after;
-        ++taken;
-        after = taken + 1 < K ? from[taken + 1] : none;
-      }
+      // log of the sum: its exponent's share exact, the fraction's to float32
+      const int e = (__float_as_int(sum) >> 23) - 127;
+      const float fraction = __int_as_float((__float_as_int(sum) & 0x7FFFFF) | 0x3F800000);
+      sh.A[w] = !lives || m == -INFINITY ? static_cast<double>(score)
+                                         : static_cast<double>(score) - ((e - kFraction) * 0.69314718055994530942 + static_cast<double>(logf(fraction)));
+      sh.m[w] = lives ? m : 0.0f;
+      sh.live[w] = lives;
+      sh.exact[w] = !lives || m == -INFINITY;  // (a finished beam's total is its score; the others have no candidates)
     }
   }
   __syncthreads();
@@ -468,51 +616,156 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     if (tid == 0) atomicOr(a.status, SV_DEV_BAD_LOGIT);
     return;
   }
+  // A candidate: its total, and what stands for it (false = none)
+  auto candidate = [&](int x, uint64_t* key, uint32_t* what) {
+    const int w = x / per_beam;
+    const double A = sh.A[w];
+    if (sh.live[w]) {
+      const Entry e = a.entries[row0 * per_beam + x];
+      if (e.token < 0) return false;
+      *key = total_key(A + (static_cast<double>(e.x) - sh.m[w]));
+      *what = static_cast<uint32_t>(w) << kTokenBits | static_cast<uint32_t>(e.token);
+      return true;
+    }
+    if (x != w * per_beam || !(A > -INFINITY)) return false;
+    *key = total_key(A);
+    *what = static_cast<uint32_t>(w) << kTokenBits | kPad;
+    return true;
+  };
   for (;;) {
     if (tid < SV_MAX_BEAMS) sh.asked[tid] = 0;
-    if (tid == 0) sh.again = 0;
+    if (tid == 0) {
+      sh.again = 0;
+      sh.n = 0;
+    }
+    if (tid < W) {
+      sh.high[tid] = static_cast<float>(sh.A[tid]);
+      sh.low[tid] = fabsf(sh.high[tid]) <= FLT_MAX ? static_cast<float>(sh.A[tid] - sh.high[tid]) : 0.0f;
+    }
     __syncthreads();
-    if (warp == 0) {  // lane l has the lists of beams l and l + 32
-      int taken[2] = {0, 0};
-      uint64_t key[2];
-      auto fetch = [&](int h) {
-        const int w = lane + 32 * h;
-        const Entry e = w < W && taken[h] < K ? lists[w * K + taken[h]] : Entry{-INFINITY, -1};
-        key[h] = e.token < 0 ? 0 : total_key(sh.A[w] + (static_cast<double>(e.x) - sh.m[w]));
-      };
-      fetch(0);
-      fetch(1);
-      for (int k = 0; k < K; ++k) {
-        const uint64_t mine = max(key[0], key[1]), best = warp_max(mine);
-        int beam = -1;
-        if (best != 0) {
-          beam = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, key[0] == best ? lane : key[1] == best ? lane + 32 : INT_MAX));
-          // the best of the other beams
-          const uint64_t rest = warp_max(max(beam == lane ? 0 : key[0], beam == lane + 32 ? 0 : key[1]));
-          if (rest != 0 && total_of_key(best) - total_of_key(rest) < kNear) {
-            const double least = total_of_key(best) - kNear;
-            bool ask = false;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (key[h] != 0 && total_of_key(key[h]) > least && !sh.exact[lane + 32 * h]) {
-                sh.asked[lane + 32 * h] = 1;
-                ask = true;
-              }
-            if (__any_sync(0xFFFFFFFFu, ask) && lane == 0) sh.again = 1;
+    // totals in float32: off by a step or so, which the bound leaves room for
+    uint32_t top = 0;
+    int mine = 0;
+#pragma unroll 2
+    for (int x = tid; x < N; x += kMergeThreads) {
+      const int w = x / per_beam;
+      uint32_t key = 0;
+      if (sh.live[w]) {
+        const Entry e = a.entries[row0 * per_beam + x];
+        if (e.token >= 0) key = float_key(about_total(sh.high[w], sh.low[w], e.x, sh.m[w]));
+      } else if (x == w * per_beam && sh.A[w] > -INFINITY) {
+        key = float_key(sh.high[w]);
+      }
+      about[x] = key;
+      top = max(top, key);
+      mine += key != 0;
+    }
+    const uint32_t top_of_warp = __reduce_max_sync(0xFFFFFFFFu, top);
+    const int there_of_warp = __reduce_add_sync(0xFFFFFFFFu, mine);
+    if (lane == 0) {
+      sh.tops[warp] = top_of_warp;
+      sh.counts[warp] = there_of_warp;
+    }
+    __syncthreads();
+    const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, lane < kMergeThreads / 32 ? sh.tops[lane] : 0u);
+    const int there = __reduce_add_sync(0xFFFFFFFFu, lane < kMergeThreads / 32 ? sh.counts[lane] : 0);
+    const int want = min(K + 1, there);
+    // the bound: `want` threads' best totals are at or above it, and few more where totals differ; a few steps of float32 below
+    uint32_t low = there <= kFew ? 1 : lower_bound_of<kMergeThreads>(top, 1, best, float_key(float_of_key(best) - 8.0f), K + 1, K + 1 + (K >> 2));
+    low = low > 16 ? low - 16 : 1;
+    for (int x = tid; x < N; x += kMergeThreads) {
+      uint64_t key;
+      uint32_t what;
+      if (about[x] >= low && candidate(x, &key, &what)) {
+        const int at = atomicAdd(&sh.n, 1);
+        if (at < kRanked) {
+          sh.key[at] = key;
+          sh.what[at] = what;
+        }
+      }
+    }
+    __syncthreads();
+    const int n = sh.n;
+    if (n <= kFew) {
+      const int i = tid & (kFew - 1), part = tid / kFew;
+      if (tid < kFew) sh.rank[tid] = 0;
+      __syncthreads();
+      if (i < n) {
+        const uint64_t key = sh.key[i];
+        const uint32_t what = sh.what[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = part; j < n; j += kMergeThreads / kFew) rank += sh.key[j] > key || (sh.key[j] == key && sh.what[j] < what);
+        atomicAdd(&sh.rank[i], rank);
+      }
+      __syncthreads();
+      if (tid < n && sh.rank[tid] <= K) {
+        sh.out_key[sh.rank[tid]] = sh.key[tid];
+        sh.out_what[sh.rank[tid]] = sh.what[tid];
+      }
+    } else if (n <= kRanked) {
+      if (tid < n) {
+        const uint64_t key = sh.key[tid];
+        const uint32_t what = sh.what[tid];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += sh.key[j] > key || (sh.key[j] == key && sh.what[j] < what);
+        if (rank <= K) {
+          sh.out_key[rank] = key;
+          sh.out_what[rank] = what;
+        }
+      }
+    } else {  // long runs of equals: one by one
+      uint64_t before = ~uint64_t(0);
+      uint32_t before_what = 0;
+      for (int k = 0; k < want; ++k) {
+        uint64_t best_key = 0;
+        uint32_t best_what = 0;
+        for (int x = tid; x < N; x += kMergeThreads) {
+          uint64_t key;
+          uint32_t what;
+          if (about[x] >= low && candidate(x, &key, &what) && (key < before || (key == before && what > before_what)) &&
+              (key > best_key || (key == best_key && what < best_what))) {
+            best_key = key;
+            best_what = what;
           }
         }
-        if (lane == (beam & 31) || (beam < 0 && lane == 0)) {
-          const int64_t at = static_cast<int64_t>(request) * K + k;
-          a.out_scores[at] = beam < 0 ? -INFINITY : static_cast<float>(total_of_key(best));
-          a.out_rows[at] = beam < 0 ? -1 : static_cast<int32_t>(row0) + beam;
-          a.out_tokens[at] = beam < 0 ? -1 : lists[beam * K + taken[beam >> 5]].token;
-          if (beam >= 0) {
-            ++taken[beam >> 5];
-            if (beam < 32) fetch(0);
-            else fetch(1);
+        sh.key[tid] = best_key;
+        sh.what[tid] = best_what;
+        for (int d = kMergeThreads / 2; d > 0; d >>= 1) {
+          __syncthreads();
+          if (tid < d && (sh.key[tid + d] > sh.key[tid] || (sh.key[tid + d] == sh.key[tid] && sh.what[tid + d] < sh.what[tid]))) {
+            sh.key[tid] = sh.key[tid + d];
+            sh.what[tid] = sh.what[tid + d];
           }
         }
-        __syncwarp();
+        __syncthreads();
+        before = sh.key[0];
+        before_what = sh.what[0];
+        if (tid == 0) {
+          sh.out_key[k] = before;
+          sh.out_what[k] = before_what;
+        }
+        __syncthreads();
+      }
+    }
+    __syncthreads();
+    for (int k = tid; k < K; k += kMergeThreads) {
+      const bool some = k < want;
+      const uint64_t key = some ? sh.out_key[k] : 0;
+      const uint32_t what = some ? sh.out_what[k] : 0;
+      const int beam = static_cast<int>((what & ~kPad) >> kTokenBits);
+      const int64_t at = static_cast<int64_t>(request) * K + k;
+      a.out_scores[at] = some ? static_cast<float>(total_of_key(key)) : -INFINITY;
+      a.out_rows[at] = some ? static_cast<int32_t>(row0) + beam : -1;
+      a.out_tokens[at] = !some ? -1 : (what & kPad) ? a.pad : static_cast<int32_t>(what & kTokenMask);
+      if (k + 1 < want) {
+        const int next = static_cast<int>((sh.out_what[k + 1] & ~kPad) >> kTokenBits);
+        if (next != beam && total_of_key(key) - total_of_key(sh.out_key[k + 1]) < kNear && !(sh.exact[beam] && sh.exact[next])) {
+          if (!sh.exact[beam]) sh.asked[beam] = 1;
+          if (!sh.exact[next]) sh.asked[next] = 1;
+          sh.again = 1;
+        }
       }
     }
     __syncthreads();
@@ -541,11 +794,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
 }
 
 // ---- host --------------------------------------------------------------------------------------------
-// Parts of a row: as many as give every CTA that fits on the GPU one, each of a piece at least.
+// Parts of a row: as many as give every CTA that fits on the GPU one, each of a piece per warp at least.
 int parts_of(int rows, int V) {
   const int pieces = (V + 7 + kPiece * 4 - 1) / (kPiece * 4);  // (of float32: the most there are)
-  return std::max(1, std::min({kMaxParts, pieces, (2 * 152 + rows - 1) / rows}));
+  return std::max(1, std::min({kMaxParts, pieces / kWarps, kRowCtas * 152 / rows}));
 }
+// ... and as many as the merge's shared memory has room for.
+constexpr int kMerged = 40960;    // candidates of a request's beams and parts
+int parts_of(int rows, int V, int W, int K) { return std::max(1, std::min(parts_of(rows, V), kMerged / (W * K))); }
 struct BeamLayout {
   size_t parts, entries, total;
 };
@@ -563,11 +819,18 @@ bool valid_sizes(int rows, int V, int K) {
 
 template <int DT>
 cudaError_t launch_beam(const BeamParams& a, int B, void* stream) {
-  cudaError_t e = launch_dependent(rows_kernel<DT>, dim3(static_cast<unsigned>(B) * a.W * a.P), kThreads, 0, stream, SV_KERNEL_BEAM, 1, a);
+  constexpr int kPerPiece = kPiece * Elem<DT>::kPerVec;
+  auto bytes = [](int V, int P) {  // a part's pieces, rounded up
+    const int pieces = (V + Elem<DT>::kPerVec - 1 + kPerPiece - 1) / kPerPiece;
+    return sizeof(Shared) + sizeof(float) * 32 * ((pieces + P - 1) / P);
+  };
+  cudaError_t e = allow_smem<rows_kernel<DT>>(bytes(SV_MAX_SAMPLE_VOCAB, 1));
   if (e != cudaSuccess) return e;
-  e = allow_smem<merge_kernel<DT>>(sizeof(Entry) * SV_MAX_BEAMS * SV_MAX_BEAM_CANDIDATES);
+  e = launch_dependent(rows_kernel<DT>, dim3(static_cast<unsigned>(a.rows) * a.P), kThreads, bytes(a.V, a.P), stream, SV_KERNEL_BEAM, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(merge_kernel<DT>, dim3(B), kMergeThreads, sizeof(Entry) * a.W * a.K, stream, SV_KERNEL_BEAM_MERGE, 1, a);
+  e = allow_smem<merge_kernel<DT>>(4 * kMerged);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(merge_kernel<DT>, dim3(B), kMergeThreads, 4 * static_cast<size_t>(a.W) * a.P * a.K, stream, SV_KERNEL_BEAM_MERGE, 1, a);
 }
 
 }  // namespace
@@ -612,10 +875,9 @@ sv_status sv_beam_select(const void* logits, int64_t row_stride, sv_dtype dt, in
   a.W = W;
   a.V = V;
   a.K = K;
-  a.P = parts_of(B * W, V);
+  a.P = parts_of(B * W, V, W, K);
   a.pad = pad;
-  a.groups = 8;  // a power of two, at least K (at most a group to two threads)
-  while (a.groups < K) a.groups *= 2;
+  a.rows = B * W;
   return launch_status(dt == SV_BF16 ? launch_beam<SV_BF16>(a, B, stream) : launch_beam<SV_F32>(a, B, stream), "beam select");
 }
 

@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
   pdl_wait();
   const int request = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = static_cast<int64_t>(request) * a.W;
-  const int K = a.K, W = a.W, P = a.P, per_beam = P * K, N = W * per_beam;
+  const int K = a.K, W = a.W, P = a.P, lists = W * P;
   static_assert(SV_MAX_SAMPLE_VOCAB <= 1 << kTokenBits && int64_t(SV_MAX_BEAMS) << kTokenBits <= int64_t(kPad), "what stands for a candidate");
   if (tid == 0) sh.bad = 0;
   __syncthreads();
@@ -616,21 +616,28 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     if (tid == 0) atomicOr(a.status, SV_DEV_BAD_LOGIT);
     return;
   }
-  // A candidate: its total, and what stands for it (false = none)
-  auto candidate = [&](int x, uint64_t* key, uint32_t* what) {
-    const int w = x / per_beam;
+  const Entry* entries = a.entries + row0 * P * K;
+  // f(list, place, beam) for this thread's candidates: a warp takes a list, or as many short ones as it has lanes for
+  const int places = min(32, 1 << (32 - __clz(K - 1))), per_warp = 32 / places;  // (K = 1: 1)
+  auto each = [&](auto f) {
+#pragma unroll 4
+    for (int l0 = warp * per_warp; l0 < lists; l0 += kMergeThreads / 32 * per_warp) {
+      const int l = l0 + lane / places;
+      if (l < lists)
+        for (int i = lane & (places - 1); i < K; i += places) f(l, i, l / P);
+    }
+  };
+  // A candidate: its total, and what stands for it
+  auto candidate = [&](int l, int i, int w, uint64_t* key, uint32_t* what) {
     const double A = sh.A[w];
     if (sh.live[w]) {
-      const Entry e = a.entries[row0 * per_beam + x];
-      if (e.token < 0) return false;
+      const Entry e = entries[l * K + i];
       *key = total_key(A + (static_cast<double>(e.x) - sh.m[w]));
       *what = static_cast<uint32_t>(w) << kTokenBits | static_cast<uint32_t>(e.token);
-      return true;
+    } else {
+      *key = total_key(A);
+      *what = static_cast<uint32_t>(w) << kTokenBits | kPad;
     }
-    if (x != w * per_beam || !(A > -INFINITY)) return false;
-    *key = total_key(A);
-    *what = static_cast<uint32_t>(w) << kTokenBits | kPad;
-    return true;
   };
   for (;;) {
     if (tid < SV_MAX_BEAMS) sh.asked[tid] = 0;
@@ -646,20 +653,20 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     // totals in float32: off by a step or so, which the bound leaves room for
     uint32_t top = 0;
     int mine = 0;
-#pragma unroll 2
-    for (int x = tid; x < N; x += kMergeThreads) {
-      const int w = x / per_beam;
+    each([&](int l, int i, int w) {
       uint32_t key = 0;
       if (sh.live[w]) {
-        const Entry e = a.entries[row0 * per_beam + x];
-        if (e.token >= 0) key = float_key(about_total(sh.high[w], sh.low[w], e.x, sh.m[w]));
-      } else if (x == w * per_beam && sh.A[w] > -INFINITY) {
+        const Entry e = entries[l * K + i];
+        // a part whose part before has K logits at or above this one adds none: they come first
+        const bool late = l != w * P && entries[l * K - 1].x >= e.x;
+        if (e.token >= 0 && !late) key = float_key(about_total(sh.high[w], sh.low[w], e.x, sh.m[w]));
+      } else if (l == w * P && i == 0 && sh.A[w] > -INFINITY) {
         key = float_key(sh.high[w]);
       }
-      about[x] = key;
+      about[l * K + i] = key;
       top = max(top, key);
       mine += key != 0;
-    }
+    });
     const uint32_t top_of_warp = __reduce_max_sync(0xFFFFFFFFu, top);
     const int there_of_warp = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0) {
@@ -672,18 +679,36 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     const int want = min(K + 1, there);
     // the bound: `want` threads' best totals are at or above it, and few more where totals differ; a few steps of float32 below
     uint32_t low = there <= kFew ? 1 : lower_bound_of<kMergeThreads>(top, 1, best, float_key(float_of_key(best) - 8.0f), K + 1, K + 1 + (K >> 2));
-    low = low > 16 ? low - 16 : 1;
-    for (int x = tid; x < N; x += kMergeThreads) {
-      uint64_t key;
-      uint32_t what;
-      if (about[x] >= low && candidate(x, &key, &what)) {
-        const int at = atomicAdd(&sh.n, 1);
-        if (at < kRanked) {
-          sh.key[at] = key;
-          sh.what[at] = what;
+    // a thread may have several: further by counting all
+    auto count_from = [&](uint32_t bound) {
+      int n = 0;
+      each([&](int l, int i, int) { n += about[l * K + i] >= bound; });
+      n = __reduce_add_sync(0xFFFFFFFFu, n);
+      __syncthreads();
+      if (lane == 0) sh.counts[warp] = n;
+      __syncthreads();
+      return __reduce_add_sync(0xFFFFFFFFu, lane < kMergeThreads / 32 ? sh.counts[lane] : 0);
+    };
+    if (there > kFew) {
+      uint32_t over = best + 1;
+      for (int n = count_from(low); n > kFew - 16 && over - low > 1;) {
+        const uint32_t mid = low + ((over - low) >> 1);
+        const int at_mid = count_from(mid);
+        if (at_mid >= want) {
+          low = mid;
+          n = at_mid;
+        } else {
+          over = mid;
         }
       }
     }
+    low = low > 16 ? low - 16 : 1;  // (steps of float32 that its totals may be off by)
+    __syncthreads();
+    each([&](int l, int i, int w) {
+      if (about[l * K + i] < low) return;
+      const int at = atomicAdd(&sh.n, 1);
+      if (at < kRanked) candidate(l, i, w, &sh.key[at], &sh.what[at]);
+    });
     __syncthreads();
     const int n = sh.n;
     if (n <= kFew) {
@@ -721,15 +746,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
       for (int k = 0; k < want; ++k) {
         uint64_t best_key = 0;
         uint32_t best_what = 0;
-        for (int x = tid; x < N; x += kMergeThreads) {
+        each([&](int l, int i, int w) {
+          if (about[l * K + i] < low) return;
           uint64_t key;
           uint32_t what;
-          if (about[x] >= low && candidate(x, &key, &what) && (key < before || (key == before && what > before_what)) &&
-              (key > best_key || (key == best_key && what < best_what))) {
+          candidate(l, i, w, &key, &what);
+          if ((key < before || (key == before && what > before_what)) && (key > best_key || (key == best_key && what < best_what))) {
             best_key = key;
             best_what = what;
           }
-        }
+        });
         sh.key[tid] = best_key;
         sh.what[tid] = best_what;
         for (int d = kMergeThreads / 2; d > 0; d >>= 1) {
@@ -800,7 +826,7 @@ int parts_of(int rows, int V) {
   return std::max(1, std::min({kMaxParts, pieces / kWarps, kRowCtas * 152 / rows}));
 }
 // ... and as many as the merge's shared memory has room for.
-constexpr int kMerged = 40960;    // candidates of a request's beams and parts
+constexpr int kMerged = 8192;     // candidates of a request's beams and parts: more take longer to merge than a row's further parts save
 int parts_of(int rows, int V, int W, int K) { return std::max(1, std::min(parts_of(rows, V), kMerged / (W * K))); }
 struct BeamLayout {
   size_t parts, entries, total;

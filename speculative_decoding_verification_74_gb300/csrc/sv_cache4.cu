@@ -74,6 +74,11 @@ __device__ __forceinline__ uint32_t codes_of(const float* r) {
       : "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]));
   return w;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // The e4m3 nearest to v >= 0, at most 448.
 __device__ __forceinline__ uint8_t scale_of(float v) {
   uint16_t w;
@@ -121,15 +126,13 @@ __global__ void __launch_bounds__(kRowThreads) append4_kernel(Append4Params a) {
   }
   __syncthreads();
   if (where < 0) return;
-  const int scales = a.r.dim >> 4, per_layer = 2 * a.r.heads * scales;
-  const int64_t items = static_cast<int64_t>(a.layers) * per_layer;
+  const int scales_shift = a.r.dim == 128 ? 3 : 2;         // sixteens of a head
+  const uint32_t per_side = a.r.heads << scales_shift, items = 2 * a.layers * per_side;
   bool wrong = false;
-  for (int64_t x = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; x < items; x += static_cast<int64_t>(gridDim.y) * kRowThreads) {
-    const int layer = static_cast<int>(x / per_layer);
-    int e = static_cast<int>(x - static_cast<int64_t>(layer) * per_layer);
-    const bool value = e >= per_layer / 2;
-    e -= value ? per_layer / 2 : 0;
-    const int head = e / scales, part = e - head * scales;
+  for (uint32_t x = blockIdx.y * kRowThreads + threadIdx.x; x < items; x += gridDim.y * kRowThreads) {
+    const uint32_t side = x / per_side, e = x - side * per_side, layer = side >> 1;
+    const bool value = side & 1;
+    const int head = e >> scales_shift, part = e & ((1 << scales_shift) - 1);
     const uint4* from = reinterpret_cast<const uint4*>((value ? a.v_new : a.k_new) + layer * a.new_layer_stride + row * a.new_row_stride) + 2 * e;
     const uint4 w[2] = {__ldg(from), __ldg(from + 1)};
     float t[16], top = 0.0f;
@@ -137,22 +140,31 @@ __global__ void __launch_bounds__(kRowThreads) append4_kernel(Append4Params a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t pair = reinterpret_cast<const uint32_t*>(w)[i];
-      t[2 * i] = bf16_lo(pair) * inverse;
-      t[2 * i + 1] = bf16_hi(pair) * inverse;
+      t[2 * i] = __fmul_rn(bf16_lo(pair), inverse);
+      t[2 * i + 1] = __fmul_rn(bf16_hi(pair), inverse);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      wrong |= !(fabsf(t[i]) <= 3.402823466e38f);
-      top = fmaxf(top, fabsf(t[i]));
-    }
-    const uint8_t scale = scale_of(fminf(top * (1.0f / 6.0f), 448.0f));
-    const float by = scale_value(scale);
+    for (int i = 0; i < 16; ++i) top = max_nan(top, fabsf(t[i]));
+    wrong |= !(top <= 3.402823466e38f);
+    const uint8_t scale = scale_of(fminf(__fmul_rn(top, 1.0f / 6.0f), 448.0f));
+    // t / s, s known to four bits: with 1 / s as a pair of floats, fma(t, high, t low) is the correctly rounded quotient
+    // (Brisebarre, Muller and Raina 2004; checked for all significands of s and t)
+    const float by = scale_value(scale), high = by > 0.0f ? 1.0f / by : 0.0f, low = __fmul_rn(fmaf(-high, by, 1.0f), high);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = by > 0.0f ? __fdiv_rn(t[i], by) : 0.0f;
+    for (int i = 0; i < 16; ++i) t[i] = fmaf(t[i], high, __fmul_rn(t[i], low));
+    if (by == 0.0f) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t[i] = 0.0f;
+    }
     unsigned char* group = a.pool + layer * a.r.layer_stride + where + head * a.r.head_stride;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint32_t*>(group + code_place(a.r.dim, value, place, 2 * part + h)) = codes_of(t + 8 * h);
+    const uint32_t codes[2] = {codes_of(t), codes_of(t + 8)};
+    unsigned char* to = group + code_place(a.r.dim, value, place, 2 * part);
+    if (value && a.r.dim == 64) {  // (two eighths of the dimensions)
+      *reinterpret_cast<uint32_t*>(to) = codes[0];
+      *reinterpret_cast<uint32_t*>(group + code_place(a.r.dim, value, place, 2 * part + 1)) = codes[1];
+    } else {
+      *reinterpret_cast<uint2*>(to) = make_uint2(codes[0], codes[1]);
+    }
     group[scale_place(a.r.dim, value, place, 2 * part)] = scale;
   }
   if (wrong) atomicOr(a.status, SV_DEV_BAD_VALUE);
@@ -376,6 +388,7 @@ sv_status sv_cache4_append(const sv_cache4* c, int layer, int layers, const int3
   a.v_inverse = 1.0f / c->v_scale;
   a.status = status_of(ws);
   const int64_t items = static_cast<int64_t>(layers) * 2 * c->kv_heads * (c->head_dim / 16);
+  if (items > INT_MAX) return set_error(SV_ERR_INVALID_ARG, "layers=%d: too many for one call", layers);
   const int64_t groups = std::min<int64_t>(64, (items + kRowThreads - 1) / kRowThreads);
   return launch_status(launch_dependent(append4_kernel, dim3(static_cast<unsigned>(n_rows), static_cast<unsigned>(groups)),
                                         kRowThreads, 0, stream, SV_KERNEL_CACHE_ROWS, 1, a),

@@ -170,3 +170,17 @@ def test_other_stream_and_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_equals_over_many_parts_and_beams(dtype):
+    """Rows long enough for many parts: constant ones, equal beams, and a step between parts."""
+    V = 150000
+    x = torch.zeros((8, V))
+    x[2:4] = torch.arange(V)[None, :] // 30000.0
+    x[4:6, 70000:] = 1.0
+    x[6:8] = torch.randn((1, V), generator=torch.Generator().manual_seed(1))
+    x = x.to(dtype)
+    for K in (1, 33, 128):
+        check(x, torch.full((1, 8), -3.0), K)
+        check(x, torch.tensor([[-3.0, -3.5], [-3.0, -2.0], [-1.0, -1.0], [-4.0, -4.25]]), K)

@@ -45,6 +45,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "sv_decode4.cuh"
 #include "sv_device.cuh"
 #include "sv_line.cuh"
 #include "sv_ops.h"
@@ -55,18 +56,26 @@ namespace {
 constexpr int kTile = 128;                 // rows of Q, and slots of the cache, in a tile
 constexpr int kGroupThreads = 128;
 constexpr int kSoftThreads = 2 * kGroupThreads;
-constexpr int kThreads = 128 + kSoftThreads;
-constexpr int kWarpK = 0, kWarpMma = 1, kWarpQ = 10, kWarpV = 11;  // 2 to 9: the two groups
+// Warps: the two groups of the softmax are four consecutive ones each.
+template <bool kFour>
+struct Warps {  // a cache in bf16
+  static constexpr int kThreads = 128 + kSoftThreads, kSoft = 2, kK = 0, kMma = 1, kQ = 10, kV = 11, kDecode = 99;
+};
+template <>
+struct Warps<true> {  // in 4 bits: whole warpgroups, which share out the registers
+  static constexpr int kThreads = 256 + kSoftThreads, kSoft = 4, kK = 2, kMma = 0, kQ = 1, kV = 99, kDecode = 12;
+};
 constexpr int kHalfBytes = kTile * 128;    // 128 slots of 64 bf16: one swizzled column block
 constexpr int kTmemColumns = 512;
-// Tensor memory by group: S at columns 0 and 128, O from 256 on.  With 128 dimensions P lies over S, so a group's next
-// S waits for its product P V; with 64 there is room for P, and S only waits until the softmax has read it.
+// Tensor memory by group: S at columns 0 and 128, O from 256 on.  With 128 dimensions P lies over the upper half of S (which is
+// read first), so a group's next S waits for its product P V; with 64 there is room for P, and S only waits until the softmax
+// has read it.
 template <int D>
 struct Columns {
   static constexpr bool kOwnP = D == 64;
   static __device__ __forceinline__ constexpr uint32_t s(uint32_t g) { return g * 128; }
   static __device__ __forceinline__ constexpr uint32_t o(uint32_t g) { return 256 + g * D; }
-  static __device__ __forceinline__ constexpr uint32_t p(uint32_t g) { return kOwnP ? 384 + g * 64 : g * 128; }
+  static __device__ __forceinline__ constexpr uint32_t p(uint32_t g) { return kOwnP ? 384 + g * 64 : g * 128 + 64; }
 };
 constexpr float kLazyGrowth = 8.0f;        // log2 units by which a maximum may grow without a rescale of O
 constexpr int kJoinRows = 16;              // rows per CTA of the join
@@ -74,6 +83,11 @@ constexpr int kJoinRows = 16;              // rows per CTA of the join
 // (64 trees over 512 to 4096 slots 126 us at 0, 114 at 2, 3 and 4; the window's 33 trees 55.5, 40.7, 40.6 and 41.2).
 constexpr int kExtra = 3;
 constexpr int kMixFloat4 = 768;            // (a fifth stage still fits)
+constexpr int kMixFloat4Of4 = 512;         // in 4 bits: at most two copies
+// A cache in 4 bits: one warp copies a tile's codes into a ring of their own, and four decode them, each a quarter of its slots,
+// sixteen at a time.
+constexpr int kRawSlots = 16;
+constexpr int kMaxRaw = 2;                 // (with 3, and a stage less: four chains over 131k 330 us against 283)
 constexpr int kMaxStages = 12;
 struct AttendParams : Line, Marks, Outputs {
   const int32_t *table, *parent;
@@ -85,7 +99,12 @@ struct AttendParams : Line, Marks, Outputs {
   int32_t half_rows;   // rows of a copy that one head takes
   uint32_t over_group; // ceil(2^16 / group)
   int32_t stages;
-  float scale;
+  float scale;         // with the cache's k_scale
+  float v_scale;
+  // a cache in 4 bits: the layer's pool, and the places of the codes' ring
+  const unsigned char* pool;
+  int64_t page_stride, head_stride;
+  int32_t raw_stages;
 };
 
 // Floats of one partial result: O as [D / 4][128 rows][4], then m and the two sums per row.
@@ -125,9 +144,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
   return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
          (static_cast<uint64_t>(stride >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-// Instruction descriptor: float32 accumulator, bf16 operands, M = 128.
-constexpr uint32_t instr_desc(int n, bool b_rows_are_k) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows_are_k ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+// Instruction descriptor: float32 accumulator, bf16 (or float16) operands, M = 128.
+constexpr uint32_t instr_desc(int n, bool b_rows_are_k, bool f16 = false) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_rows_are_k ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kTile >> 4) << 24);
 }
 
@@ -195,6 +214,16 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Registers of this warpgroup's threads from here on.
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -206,10 +235,13 @@ __device__ __forceinline__ int over_group(int row, uint32_t over) { return stati
 
 // The part of shared memory with a fixed size; then come the tiles before each request [B], the parents of two segments'
 // trees [2][Nmax] and, 1024-byte aligned, Q and the ring.
+template <bool kFour>
 struct Smem {
   Line line;
   Segment seg[2];              // by the segment's parity
   uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t raw_full[kFour ? kMaxRaw : 1], raw_empty[kFour ? kMaxRaw : 1];  // a tile's codes are there, are decoded
+  uint64_t q_raw[2];           // in 4 bits, by the segment's parity: its Q is there in bf16
   uint64_t q_full[2];          // by the segment's parity: its Q and description are there
   uint64_t q_free;             // once per segment: its last S is complete
   uint64_t seg_free[2];        // every softmax thread is done with a description
@@ -217,8 +249,9 @@ struct Smem {
   uint64_t sums_full, o_free;  // once per segment: the groups' sums are there; every thread has read O
   uint64_t mix_full[2], mix_free[2];  // by group: copies' columns written, read
   float m[2][2][kTile], l[2][2][kTile], lr[2][2][kTile];  // by the segment's parity and group
-  float4 mix[2][kMixFloat4];   // by group: columns that the copies exchange, four columns of all rows together
-  uint32_t scan[kThreads / 32];
+  float q_size[kFour ? 2 : 1][kFour ? kTile : 1];  // by the segment's parity: what a row of Q was divided by
+  float4 mix[2][kFour ? kMixFloat4Of4 : kMixFloat4];   // by group: columns that the copies exchange, four columns of all rows together
+  uint32_t scan[Warps<kFour>::kThreads / 32];
   uint32_t tmem;
   volatile int32_t dead;       // a wait ran out: everyone leaves
 };
@@ -234,17 +267,19 @@ struct Ring {
   }
 };
 
-template <int D, bool kPair, int kCopies>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kPair, int kCopies, bool kFour>
+__global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
     attend_kernel(const AttendParams a, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map) {
   constexpr int W = kPair ? 2 * D : D;  // dimensions of a tile
   using Col = Columns<W>;
+  using Role = Warps<kFour>;
+  constexpr int kThreads = Role::kThreads;
   constexpr int kHalves = W / 64;
   constexpr int kHalfRows = kTile / kCopies / (kPair ? 2 : 1);
   constexpr int kStageBytes = kHalves * kHalfBytes;
   extern __shared__ unsigned char dyn[];
-  __shared__ Smem sm;
+  __shared__ Smem<kFour> sm;
   uint32_t* before = reinterpret_cast<uint32_t*>(dyn);           // [B]
   int32_t* parents = reinterpret_cast<int32_t*>(dyn) + a.B;      // [2][Nmax]
   unsigned char* q_buf = dyn + 4 * (a.B + 2 * a.Nmax);
@@ -254,12 +289,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (known to be the same in all lanes)
   if (tid == 0) {
     for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.full[i], kFour ? 128 : 1);
       mbar_init(&sm.empty[i], 1);
     }
+    if constexpr (kFour)
+      for (int i = 0; i < kMaxRaw; ++i) {
+        mbar_init(&sm.raw_full[i], 1);
+        mbar_init(&sm.raw_empty[i], 4);
+      }
     mbar_init(&sm.q_free, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_raw[i], 1);
+      mbar_init(&sm.q_full[i], kFour ? 128 : 1);
       mbar_init(&sm.seg_free[i], kSoftThreads);
       mbar_init(&sm.mix_full[i], kGroupThreads);
       mbar_init(&sm.mix_free[i], kGroupThreads);
@@ -278,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = tid; i < kHalves * kHalfBytes / 16; i += kThreads) reinterpret_cast<uint4*>(q_buf)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
-  if (warp == kWarpMma) tmem_alloc(&sm.tmem);
+  if (warp == Role::kMma) tmem_alloc(&sm.tmem);
   pdl_wait();
   pdl_trigger();
   // tiles before each request
@@ -317,20 +358,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Parts parts(total, max(1u, min(gridDim.x, total)));
   const uint32_t t0 = min(parts.begin(blockIdx.x), total), t1 = min(parts.begin(blockIdx.x + 1), total);
   Segment opening = {};
-  if (t0 < t1) opening = segment_at<kTile>(sm.line, before, t0, t1);
+  if (t0 < t1) opening = segment_at<kTile, kFour>(sm.line, before, t0, t1);
   const bool some = opening.kv0 < opening.kv1;
   // a part's stretches but the first begin a row tile; the last may hold none of its cache tiles
   auto stretch_at = [&](uint32_t t) { return t == t0 ? some : t + a.extra < t1; };
   const uint32_t stages = a.stages;
   uint32_t loaded = 0, segments = 0;  // stages and Q's that were asked for
 
-  if (warp == kWarpK || warp == kWarpV) {
+  [[maybe_unused]] auto copies = [&]() {
     // ---- copies -----------------------------------------------------------------------------------
     const int box_shift = min(7, a.shift), box = 1 << box_shift;  // slots per copy: a page, or 128 slots of one
     const int chunks = kTile >> box_shift;
     bool go = true;
-    const uint32_t second = warp == kWarpV;  // K's and V's stages alternate
+    const uint32_t second = warp == Role::kV;  // K's and V's stages alternate (in 4 bits they come together)
     const CUtensorMap* map = second ? &v_map : &k_map;
+    const uint32_t places = kFour ? a.raw_stages : stages;
     Ring at;
     if (second) at.step(stages);
     loaded = second;
@@ -366,8 +408,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           mark_bad(a, s.request, SV_DEV_BAD_PAGE);
           page = a.pages;  // outside the tensor: the copy fills zeros
         }
+        if constexpr (kFour) {
+          constexpr int kHeads = kPair ? 2 : 1, kSlotBytes = 9 * D / 8;
+          const bool there = wanted && page < a.pages;
+          const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, there)) * kHeads * box * kSlotBytes;
+          if (loaded >= places) go = warp_wait<kFour>(&sm.raw_empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
+          if (!go) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[at.stage], bytes);
+          __syncwarp();
+          if (there) {
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h)
+              bulk_g2s(ring + stages * kStageBytes + (at.stage * kHeads + h) * kTile * kSlotBytes + (lane << box_shift) * kSlotBytes,
+                       a.pool + page * a.page_stride + (kHeads * s.head + h) * a.head_stride + (slot & ((1 << a.shift) - 1)) * kSlotBytes,
+                       box * kSlotBytes, &sm.raw_full[at.stage]);
+          }
+          ++loaded;
+          at.step(places);
+        } else {
         const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, wanted)) * kHalves * box * 128;
-        if (loaded >= stages) go = warp_wait(&sm.empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
+        if (loaded >= stages) go = warp_wait<kFour>(&sm.empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
         if (!go) break;
         if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.stage], bytes);
         __syncwarp();
@@ -381,8 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         loaded += 2;
         at.step(stages);
         at.step(stages);
+        }
         if (j == max(s.kv0, s.kv1 - 2) && stretch_at(after)) {
-          next = segment_at<kTile>(sm.line, before, after, t1);
+          next = segment_at<kTile, kFour>(sm.line, before, after, t1);
           next_block = tile_slot<kTile>(next.r, next.kv0) >> (box_shift + 5);
           next_now = pages_of(next, next_block);
         }
@@ -392,37 +453,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       block = next_block;
       page_now = next_now;
     }
-  } else if (warp == kWarpQ) {
+  };
+  auto queries = [&]() {
     // ---- segments: description, parents, Q --------------------------------------------------------
     constexpr int rows_apart = kTile / kCopies;
     for (uint32_t t = t0; stretch_at(t); ++segments) {
-      const Segment s = t == t0 ? opening : segment_at<kTile>(sm.line, before, t, t1);
+      const Segment s = t == t0 ? opening : segment_at<kTile, kFour>(sm.line, before, t, t1);
       const int b = segments & 1;
-      if (segments >= 2 && !warp_wait(&sm.seg_free[b], ((segments >> 1) - 1) & 1, &sm.dead, a.status)) break;
+      if (segments >= 2 && !warp_wait<kFour>(&sm.seg_free[b], ((segments >> 1) - 1) & 1, &sm.dead, a.status)) break;
       if (a.parent != nullptr)
         for (int x = lane; x < s.r.nodes; x += 32) parents[b * a.Nmax + x] = a.parent[s.r.first + x];
       if (lane == 0) sm.seg[b] = s;
-      if (segments >= 1 && !warp_wait(&sm.q_free, (segments - 1) & 1, &sm.dead, a.status)) break;
+      if (segments >= 1 && !warp_wait<kFour>(&sm.q_free, (segments - 1) & 1, &sm.dead, a.status)) break;
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_expect_tx(&sm.q_full[b], kCopies * kHalves * a.tile_nodes * a.group * 128);
+        uint64_t* there = kFour ? &sm.q_raw[b] : &sm.q_full[b];
+        mbar_arrive_expect_tx(there, kCopies * kHalves * a.tile_nodes * a.group * 128);
         for (int copy = 0; copy < kCopies; ++copy)
 #pragma unroll
           for (int h = 0; h < kHalves; ++h)
             tma_load_3d(q_buf + h * kHalfBytes + (copy * rows_apart + (kPair ? h * kHalfRows : 0)) * 128, &q_map,
                         kPair ? 0 : h * 64, (kPair ? 2 * s.head + h : s.head) * a.group,
-                        static_cast<int>(s.r.first) + s.mtile * a.tile_nodes, &sm.q_full[b]);
+                        static_cast<int>(s.r.first) + s.mtile * a.tile_nodes, there);
       }
       t = s.next;
     }
-  } else if (warp == kWarpMma) {
+  };
+  auto products = [&]() {
     // ---- products ---------------------------------------------------------------------------------
     // The whole warp runs the loop, so counters and descriptors stay in uniform registers, which tcgen05.mma takes its
     // operands from; one elected thread issues.
     if (some) {
       const bool elected = elect_one();
       auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
-      constexpr uint32_t kDescS = instr_desc(kTile, false), kDescO = instr_desc(W, true);
+      constexpr uint32_t kDescS = instr_desc(kTile, false, kFour), kDescO = instr_desc(W, true, kFour);
       bool more = true;                   // S's are left
       // descriptors by addition: their low words count 16-byte units of shared memory
       const uint64_t q_desc0 = smem_desc(smem_u32(q_buf), 16, 1024), k_desc0 = smem_desc(smem_u32(ring), 16, 1024),
@@ -492,14 +556,164 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         idle = issued ? 0 : idle + 1;
-        if ((idle & 1023u) == 1023u && !__all_sync(0xFFFFFFFFu, still_waiting(&began, &sm.dead, a.status))) break;
+        if ((idle & 1023u) == 1023u && !__all_sync(0xFFFFFFFFu, still_waiting<kFour>(&began, &sm.dead, a.status))) break;
         if (issued) began = 0;
       }
     }
     __syncwarp();
-  } else {
+  };
+  [[maybe_unused]] auto decode = [&]() {
+    // ---- decoding: codes times scales into the stages, as float16 (exact: six bits) -----------------------
+    // And Q: each row is scaled by a power of two so that its largest element lies in [2^14, 2^15), where elements down to
+    // 2^-28 of it keep all bits of their bf16.
+    if constexpr (kFour) {
+      constexpr int kHeads = kPair ? 2 : 1, kGroupBytes = 9 * D, kHeadBytes = kTile / 8 * kGroupBytes;
+      constexpr int kWords = D / 32;   // words of a lane's codes in a group of eight slots
+      constexpr int kAll = kHeads * (kRawSlots / 8);  // groups of a chunk: [head][group]
+      const int quarter = warp - Role::kDecode, chunk0 = quarter * 32, g = lane >> 2, t4 = lane & 3;
+      const unsigned char* raw = ring + stages * kStageBytes + chunk0 / 8 * kGroupBytes;
+      Ring codes;
+      Ring at;
+      uint32_t filled = 0, seg = 0;
+      bool go = true;
+      auto convert = [&](int b) {
+        constexpr int kLanes = W / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at once
+#pragma unroll 2
+        for (int x = 0; x < 32; x += kAtOnce) {
+          const int row = chunk0 + x + lane / kLanes, y = lane & (kLanes - 1);
+          uint4* at = reinterpret_cast<uint4*>(q_buf + (y >> 3) * kHalfBytes + row * 128 + ((y ^ row) & 7) * 16);
+          const uint4 v = *at;
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(in[i])), fabsf(bf16_hi(in[i]))));
+#pragma unroll
+          for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          const int up = 14 - max(static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127, -100);
+          const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+          if (y == 0) sm.q_size[b][row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          uint32_t out[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = pack_f16(bf16_lo(in[i]) * by, bf16_hi(in[i]) * by);
+          *at = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.q_full[b]);
+      };
+      for (uint32_t t = t0; stretch_at(t) && go;) {
+        const Segment s = t == t0 ? opening : segment_at<kTile, kFour>(sm.line, before, t, t1);
+        const int end = s.r.len + s.r.nodes, lo = a.window > 0 ? max(0, s.r.len - a.window + 1) : 0;
+        for (int j = s.kv0; j < s.kv1 && go; ++j) {
+          const int s0 = tile_slot<kTile>(s.r, j) + chunk0;
+          uint32_t live = 0xFFFFFFFFu;  // this quarter's slots that some node may see: the others may hold anything
+          if (s0 + 32 > end || (a.window > 0 && s0 < lo && s0 + 32 > a.sinks))
+            live = range_bits(lo, end, s0) | (a.window > 0 ? range_bits(0, min(a.sinks, end), s0) : 0u);
+#pragma unroll
+          for (int value = 0; value < 2; ++value) {
+            if (filled >= stages) go = warp_wait<kFour>(&sm.empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
+            if (!go) break;
+            unsigned char* stage = ring + at.stage * kStageBytes;
+            if (value == 0) go = warp_wait<kFour>(&sm.raw_full[codes.stage], codes.parity, &sm.dead, a.status);
+            // a chunk's codes and scales are read before the one before it is stored: loads do not pass stores by themselves
+            uint32_t w[kAll][kWords], two[kAll], next_w[kAll][kWords], next_two[kAll];
+            auto fetch = [&](int c) {
+#pragma unroll
+              for (int x = 0; x < kAll; ++x) {
+                const int head = x / (kRawSlots / 8), u = x % (kRawSlots / 8);
+                const unsigned char* group = raw + (codes.stage * kHeads + head) * kHeadBytes + (c * (kRawSlots / 8) + u) * kGroupBytes + (value ? 4 * D + D / 2 : 0);
+                if constexpr (D == 128) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(group + lane * 16);
+                  next_w[x][0] = v.x;
+                  next_w[x][1] = v.y;
+                  next_w[x][2] = v.z;
+                  next_w[x][3] = v.w;
+                  next_two[x] = *reinterpret_cast<const uint16_t*>(group + 4 * D + lane * 2);
+                } else {
+                  const uint2 v = *reinterpret_cast<const uint2*>(group + lane * 8);
+                  next_w[x][0] = v.x;
+                  next_w[x][1] = v.y;
+                  next_two[x] = value ? *reinterpret_cast<const uint16_t*>(group + 4 * D + (g >> 1) * 8 + t4 * 2) : group[4 * D + lane];
+                }
+              }
+            };
+            fetch(0);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int x = 0; x < kAll; ++x) {
+              two[x] = next_two[x];
+#pragma unroll
+              for (int i = 0; i < kWords; ++i) w[x][i] = next_w[x][i];
+            }
+            if (c == 0) fetch(1);
+#pragma unroll
+            for (int x = 0; x < kAll; ++x) {
+              const int head = x / (kRawSlots / 8) % kHeads, u = x % (kRawSlots / 8);
+              const int row0 = chunk0 + c * kRawSlots + u * 8;
+              // 16 bytes: eight dimensions of a slot, piece y of its row
+              auto put = [&](int slot_in, int y, const uint32_t (&o)[4]) {
+                *reinterpret_cast<uint4*>(stage + (head + (y >> 3)) * kHalfBytes + (row0 + slot_in) * 128 + ((y ^ slot_in) & 7) * 16) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+              };
+              uint32_t by = decode_scales(static_cast<uint16_t>(two[x]));
+              if (value == 0) {  // slot g, a quarter of its dimensions
+                const uint32_t low = __byte_perm(by, by, 0x1010), high = D == 128 ? __byte_perm(by, by, 0x3232) : low;
+                // (for neighbouring lanes' pieces in different banks the upper quarters go in another order)
+                const bool flip = D == 128 && (t4 & 2) != 0;
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                  const uint32_t word = D == 128 && flip ? w[x][i ^ 2] : w[x][i];
+                  const uint32_t scale = D == 128 ? (((i & 2) != 0) != flip ? high : low) : low;
+                  uint32_t h[4];
+                  decode8(word, h);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(scale));
+                  put(g, t4 * kWords + (D == 128 && flip ? i ^ 2 : i), h);
+                }
+              } else {           // slots 2 t4 and 2 t4 + 1, an eighth of their dimensions
+                const uint32_t bits = live >> (c * kRawSlots + u * 8 + 2 * t4);
+                by &= ((bits & 1u) ? 0xFFFFu : 0u) | ((bits & 2u) ? 0xFFFF0000u : 0u);
+                const bool flip = D == 128 && (g & 1) != 0;  // (as above: the odd slot first)
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                  const uint32_t its = __byte_perm(by, by, (o == 1) != flip ? 0x3232 : 0x1010);
+#pragma unroll
+                  for (int i = 0; i < kWords / 2; ++i) {
+                    const uint32_t word = flip ? w[x][(o ^ 1) * (kWords / 2) + i] : w[x][o * (kWords / 2) + i];
+                    uint32_t h[4];
+                    decode8(word, h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(its));
+                    put(2 * t4 + (flip ? o ^ 1 : o), g * (kWords / 2) + i, h);
+                  }
+                }
+              }
+            }
+            }
+            if (value == 1) {  // the codes are done with
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.raw_empty[codes.stage]);
+              codes.step(a.raw_stages);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.full[at.stage]);
+            ++filled;
+            at.step(stages);
+          }
+          // (behind the segment's first stages: Q comes when the segment before has had its last S)
+          if (j == s.kv0 && go) {
+            go = warp_wait<kFour>(&sm.q_raw[seg & 1], (seg >> 1) & 1, &sm.dead, a.status);
+            convert(seg & 1);
+          }
+        }
+        ++seg;
+        t = s.next;
+      }
+    }
+  };
+  auto softmax = [&]() {
     // ---- softmax: thread r of a group has row r of the tile: row `row_in` of copy `copy` -----------
-    const int group = (warp - 2) >> 2;
+    const int group = (warp - Role::kSoft) >> 2;
     const int r = (warp & 3) * 32 + lane;
     constexpr int rows_apart = kTile / kCopies;
     const int row_in = r & (rows_apart - 1), copy = r / rows_apart;
@@ -510,12 +724,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = my + Col::s(group), o_addr = my + Col::o(group), p_addr = my + Col::p(group);
     float4* mix = sm.mix[group];
-    const float c = a.scale * 1.44269504088896341f;
-    if (tid == 64) a.jobs[blockIdx.x].valid = 0;
+    float c = a.scale * 1.44269504088896341f;
+    if (tid == 32 * Role::kSoft) a.jobs[blockIdx.x].valid = 0;
     uint32_t n0 = 0, seg = 0, mixes = 0, frees = 0;  // the segment's first tile in this CTA's count
     for (uint32_t t = t0; stretch_at(t); ++seg) {
       const int b = seg & 1;
-      if (!warp_wait(&sm.q_full[b], (seg >> 1) & 1, &sm.dead, a.status)) break;
+      if (!warp_wait<kFour>(&sm.q_full[b], (seg >> 1) & 1, &sm.dead, a.status)) break;
+      if constexpr (kFour) c = fmaxf(a.scale * 1.44269504088896341f * sm.q_size[b][r], 1e-37f);  // (not 0: masked scores are -inf)
       const Segment& s = sm.seg[b];
       const int32_t* tree = parents + b * a.Nmax;
       auto parent_of = [&](int node) { return a.parent != nullptr ? tree[node] : node - 1; };
@@ -541,14 +756,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool left = false;
       for (int j = (group + n0) & 1; j < tiles; j += 2) {
         const uint32_t n = n0 + j;
-        if (left = !warp_wait(&sm.s_full[group], (n >> 1) & 1, &sm.dead, a.status); left) break;
+        if (left = !warp_wait<kFour>(&sm.s_full[group], (n >> 1) & 1, &sm.dead, a.status); left) break;
         tc_after_sync();
         const int s0 = tile_slot<kTile>(s.r, s.kv0 + j);
         const bool whole = s0 + kTile <= len && (a.window <= 0 || s0 + kTile <= a.sinks || s0 >= len + s.r.nodes - a.window);
-        if (!whole && (s0 + kTile > end || (a.window > 0 && s0 < lo && s0 + kTile > a.sinks))) {
+        if (!kFour && !whole && (s0 + kTile > end || (a.window > 0 && s0 < lo && s0 + kTile > a.sinks))) {
           // slots that no node sees may hold anything: 0 times it has to be 0
           const uint32_t v = 2 * n + 1, st = v % stages;
-          if (left = !warp_wait(&sm.full[st], (v / stages) & 1, &sm.dead, a.status); left) break;
+          if (left = !warp_wait<kFour>(&sm.full[st], (v / stages) & 1, &sm.dead, a.status); left) break;
           const int slot = s0 + r;
           if (slot >= end || (slot < lo && slot >= a.sinks)) {
 #pragma unroll 4
@@ -559,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (active) {
           // With one copy S is read in two halves, the first half twice (for the maximum and for P); P's columns
-          // lie over columns that were read before.
+          // lie over the second half.
           uint32_t x[kWide];
           float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
@@ -618,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               l *= keep;
               lr *= keep;
               // the group's O is complete up to its tile before
-              if (left = !warp_wait(&sm.pv_done[group], ((n - 2) >> 1) & 1, &sm.dead, a.status); left) break;
+              if (left = !warp_wait<kFour>(&sm.pv_done[group], ((n - 2) >> 1) & 1, &sm.dead, a.status); left) break;
               tc_after_sync();
 #pragma unroll 1
               for (int i = 0; i < W; i += 16) {
@@ -632,13 +847,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (Col::kOwnP && j >= 2) {  // the product of the group's tile before has read P
-            if (left = !warp_wait(&sm.pv_done[group], ((n - 2) >> 1) & 1, &sm.dead, a.status); left) break;
+            if (left = !warp_wait<kFour>(&sm.pv_done[group], ((n - 2) >> 1) & 1, &sm.dead, a.status); left) break;
             tc_after_sync();
           }
           const float off = m == -INFINITY ? 0.0f : -m;
           const f32x2 c2 = f2_pack(c, c), off2 = f2_pack(off, off);
           f32x2 sum[2] = {0, 0}, sumr[2] = {0, 0};
-          [[maybe_unused]] uint32_t later[kSteps > 1 ? 32 : 1];
 #pragma unroll 1
           for (int k = kSteps - 1; k >= 0; --k) {  // the last step's scores are still there
             const int col = slot0 + k * kWide;
@@ -653,20 +867,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, off2), e0, e1);
               e0 = ex2_approx(e0);
               e1 = ex2_approx(e1);
-              const uint32_t w = pack_bf16(e0, e1);
+              // (a float16 is off by 2^-12 at most: its weights are divided by the sum before rounding)
+              const uint32_t w = kFour ? pack_f16(e0, e1) : pack_bf16(e0, e1);
               sum[(i >> 1) & 1] = f2_add(sum[(i >> 1) & 1], f2_pack(e0, e1));
-              sumr[(i >> 1) & 1] = f2_add(sumr[(i >> 1) & 1], f2_pack(bf16_lo(w), bf16_hi(w)));
+              if (!kFour) sumr[(i >> 1) & 1] = f2_add(sumr[(i >> 1) & 1], f2_pack(bf16_lo(w), bf16_hi(w)));
               x[i >> 1] = w;
             }
-            if constexpr (kSteps > 1) {
-              if (k > 0) {  // this half's P lies over the half of S that is still to be read
-#pragma unroll
-                for (int i = 0; i < 32; ++i) later[i] = x[i];
-              } else {
-                tmem_store32(p_addr, x);
-                tmem_store32(p_addr + 32, later);
-              }
-            } else if constexpr (kWide == 64) {
+            if constexpr (kWide == 64) {
               tmem_store32(p_addr + col / 2, x);
             } else {
               tmem_store16(p_addr + col / 2, x);
@@ -683,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float e0, e1;
           f2_unpack(f2_add(sum[0], sum[1]), e0, e1);
           l += e0 + e1;
-          f2_unpack(f2_add(sumr[0], sumr[1]), e0, e1);
+          if (!kFour) f2_unpack(f2_add(sumr[0], sumr[1]), e0, e1);
           lr += e0 + e1;
           tmem_wait_store();
         }
@@ -696,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.l[b][group][r] = l;
       sm.lr[b][group][r] = lr;
       mbar_arrive(&sm.sums_full);
-      if (!warp_wait(&sm.sums_full, seg & 1, &sm.dead, a.status)) break;
+      if (!warp_wait<kFour>(&sm.sums_full, seg & 1, &sm.dead, a.status)) break;
       float top = -INFINITY, sum = 0.0f, sumr = 0.0f;
       for (int x = row_in; x < kTile; x += rows_apart) top = fmaxf(top, fmaxf(sm.m[b][0][x], sm.m[b][1][x]));
       for (int x = row_in; x < kTile; x += rows_apart)
@@ -709,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool complete = s.kv0 == 0 && s.kv1 == s.r.tiles;
       // Every row sees its own node's slot, so a sum that is not above 0 is that of a row without a softmax: NaN among its
       // scores (which the maximum passes over), or nothing but -inf.  Its outputs are NaN; the parts' sums tell the join.
-      const float inv = !complete ? 1.0f : sumr > 0.0f ? 1.0f / sumr : NAN;
+      const float inv = !complete ? 1.0f : sumr > 0.0f ? a.v_scale / sumr : NAN;
       // (a group without a tile in the segment has m = -inf: its O is not used, whatever it holds)
       const float w0 = (sm.m[b][0][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][0][r] - top)) * inv;
       const float w1 = (sm.m[b][1][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[b][1][r] - top)) * inv;
@@ -732,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[(s.r.first + node) * a.q_heads + head] = (top + log2f(sum)) * 0.693147180559945309f;
         }
       }
-      if (tid == 64 && s.kv0 == 0 && !complete) {
+      if (tid == 32 * Role::kSoft && s.kv0 == 0 && !complete) {
         // the CTA in which the row tile ends
         const uint32_t ends = s.begin + a.extra + s.r.tiles - 1;
         const Job job = {1, s.request, s.head, s.mtile, rows, static_cast<int32_t>(blockIdx.x), parts.of(ends), 0};
@@ -740,8 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // the last tile of each parity: its product is the last into that group's O
       const uint32_t last = n0 + tiles - 1;
-      bool ok = warp_wait(&sm.pv_done[last & 1], (last >> 1) & 1, &sm.dead, a.status);
-      if (ok && tiles > 1) ok = warp_wait(&sm.pv_done[(last - 1) & 1], ((last - 1) >> 1) & 1, &sm.dead, a.status);
+      bool ok = warp_wait<kFour>(&sm.pv_done[last & 1], (last >> 1) & 1, &sm.dead, a.status);
+      if (ok && tiles > 1) ok = warp_wait<kFour>(&sm.pv_done[(last - 1) & 1], ((last - 1) >> 1) & 1, &sm.dead, a.status);
       if (!ok) break;
       tc_after_sync();
       // P of this thread's columns from `column` on, both groups' O's together
@@ -799,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               read_o(i0 + copy * P, f);
             }
             mbar_arrive(&sm.mix_full[group]);
-            if (!warp_wait(&sm.mix_full[group], mixes & 1, &sm.dead, a.status)) return false;
+            if (!warp_wait<kFour>(&sm.mix_full[group], mixes & 1, &sm.dead, a.status)) return false;
             ++mixes;
             if (writes) {
               const float4* from = mix + copy * (kCopies - 1) * (P / 4) * kept_rows + local;
@@ -819,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (i0 + kCopies * P < col1) {  // the buffer is written again
               mbar_arrive(&sm.mix_free[group]);
-              if (!warp_wait(&sm.mix_free[group], frees & 1, &sm.dead, a.status)) return false;
+              if (!warp_wait<kFour>(&sm.mix_free[group], frees & 1, &sm.dead, a.status)) return false;
               ++frees;
             }
           }
@@ -827,6 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // (kept_rows copies (copies - 1) P floats; a half of 32 columns goes over four copies by 8)
         static_assert(64 * 2 * 16 <= 4 * kMixFloat4 && 16 * 4 * 3 * 16 <= 4 * kMixFloat4 && 32 * 4 * 3 * 8 <= 4 * kMixFloat4, "mix");
+        static_assert(!kFour || (kCopies <= 2 && 64 * 2 * 16 <= 4 * kMixFloat4Of4), "mix");
         using Sixteen = std::integral_constant<int, 16>;
         using Eight = std::integral_constant<int, 8>;
         if constexpr (kCopies == 2) left = !mixed(Sixteen());
@@ -840,18 +1048,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&sm.seg_free[b]);
       n0 += tiles;
     }
+  };
+  if constexpr (kFour) {
+    if (warp < Role::kSoft) {  // 128 registers a thread at launch: 4 * 128 >= 72 + 2 * 168 + 104
+      fewer_registers<72>();
+      if (warp == Role::kMma) products();
+      else if (warp == Role::kQ) queries();
+      else if (warp == Role::kK) copies();
+    } else if (warp < Role::kDecode) {
+      more_registers<168>();
+      softmax();
+    } else {
+      fewer_registers<104>();
+      decode();
+    }
+  } else {
+    if (warp == Role::kK || warp == Role::kV) copies();
+    else if (warp == Role::kQ) queries();
+    else if (warp == Role::kMma) products();
+    else softmax();
   }
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
   if (sm.dead) {  // copies in flight land before the CTA leaves
-    if (warp == kWarpK || warp == kWarpV)  // its last fills: every second place of the ring's line
-      for (uint32_t x = loaded > stages + 1 ? loaded - ((stages + 1) & ~1u) : (warp == kWarpV); x < loaded; x += 2)
+    if (kFour && warp == Role::kK)
+      for (uint32_t x = loaded > static_cast<uint32_t>(a.raw_stages) ? loaded - a.raw_stages : 0; x < loaded; ++x)
+        mbar_wait(&sm.raw_full[x % a.raw_stages], (x / a.raw_stages) & 1, a.status);
+    if (!kFour && (warp == Role::kK || warp == Role::kV))  // its last fills: every second place of the ring's line
+      for (uint32_t x = loaded > stages + 1 ? loaded - ((stages + 1) & ~1u) : (warp == Role::kV); x < loaded; x += 2)
         mbar_wait(&sm.full[x % stages], (x / stages) & 1, a.status);
-    if (warp == kWarpQ && segments > 0) mbar_wait(&sm.q_full[(segments - 1) & 1], ((segments - 1) >> 1) & 1, a.status);
+    if (warp == Role::kQ && segments > 0)
+      mbar_wait(kFour ? &sm.q_raw[(segments - 1) & 1] : &sm.q_full[(segments - 1) & 1], ((segments - 1) >> 1) & 1, a.status);
     __syncthreads();
   }
-  if (warp == kWarpMma) tmem_free(tmem);
+  if (warp == Role::kMma) tmem_free(tmem);
 }
 
 // Adds the partial results of row tile `jobs[x]`: with M = max m_i, o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
@@ -887,7 +1118,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) join_kernel(const AttendPar
       o[2] += w * v.z;
       o[3] += w * v.w;
     }
-    const float inv = R > 0.0f ? 1.0f / R : NAN;  // (not above 0: NaN among the row's scores, or nothing but -inf)
+    const float inv = R > 0.0f ? a.v_scale / R : NAN;  // (not above 0: NaN among the row's scores, or nothing but -inf)
     const int node = job.mtile * a.tile_nodes + local / a.group, head = (heads * job.head + half) * a.group + local % a.group;
     const int64_t row = a.node_offsets[job.request] + node;
     uint2 w;
@@ -956,24 +1187,92 @@ bool encode_queries(CUtensorMap* map, const void* q, int64_t row_stride, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kPair, int kCopies>
+template <int D, bool kPair, int kCopies, bool kFour>
 cudaError_t launch_attention(AttendParams& a, const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
                              int ctas, void* stream) {
-  // the ring gets what Q, the tables and the fixed part leave of the shared memory: at least 4 stages
+  // the ring gets what Q, the tables and the fixed part leave of the shared memory: at least 4 stages (in 4 bits 3, behind
+  // the codes' rings)
   constexpr int kStageBytes = (kPair ? 2 : 1) * D / 64 * kHalfBytes;
-  const int fixed = 4 * (a.B + 2 * a.Nmax) + 1024 + kStageBytes;
-  const int room = kSmemMax - static_cast<int>(sizeof(Smem)) - 64 - fixed;
-  a.stages = std::min(kMaxStages, room / kStageBytes);
+  constexpr int kRawBytes = kFour ? (kPair ? 2 : 1) * kTile / 8 * 9 * D : 0;
+  constexpr int kStatic = sizeof(Smem<kFour>) + 64;
+  int fixed = 4 * (a.B + 2 * a.Nmax) + 1024 + kStageBytes;
+  if (kFour) {
+    a.raw_stages = std::min(kMaxRaw, (kSmemMax - kStatic - fixed - 3 * kStageBytes) / std::max(kRawBytes, 1));
+    fixed += a.raw_stages * kRawBytes;
+  }
+  a.stages = std::min(kMaxStages, (kSmemMax - kStatic - fixed) / kStageBytes);
   const size_t dyn = static_cast<size_t>(fixed) + static_cast<size_t>(a.stages) * kStageBytes;
-  cudaError_t e = allow_smem<attend_kernel<D, kPair, kCopies>>(kSmemMax - sizeof(Smem) - 64);
+  cudaError_t e = allow_smem<attend_kernel<D, kPair, kCopies, kFour>>(kSmemMax - kStatic);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attend_kernel<D, kPair, kCopies>, dim3(ctas), kThreads, dyn, stream, SV_KERNEL_ATTENTION, 1, a, q_map, k_map, v_map);
+  e = launch_dependent(attend_kernel<D, kPair, kCopies, kFour>, dim3(ctas), Warps<kFour>::kThreads, dyn, stream,
+                       SV_KERNEL_ATTENTION, 1, a, q_map, k_map, v_map);
   if (e != cudaSuccess) return e;
   const int groups = ((kPair ? 2 : 1) * a.tile_nodes * a.group + kJoinRows - 1) / kJoinRows;
   return launch_dependent(join_kernel<D>, dim3(ctas, groups), kJoinRows * D / 4, 0, stream, SV_KERNEL_ATTENTION_JOIN, 1, a);
 }
 
 }  // namespace
+
+size_t attention4_tiles_workspace(int head_dim) { return layout_of(kMaxCtas, head_dim).total; }
+sv_status attention4_tiles(const sv_cache4* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                           const int32_t* page_table, int table_width, const int32_t* seq_len, const int32_t* node_offsets,
+                           int64_t n_rows, const int32_t* parent, int B, int Nmax, float scale, int window, int sinks, void* out,
+                           int64_t out_row_stride, int64_t out_head_stride, float* out_lse, void* ws, void* stream) {
+  const int group = q_heads / c->kv_heads;
+  const bool pair = c->head_dim == 64 && c->kv_heads % 2 == 0 && 2 * Nmax * group <= kTile;
+  const int tile_nodes = std::min(kTile / group, Nmax);
+  CUtensorMap q_map;
+  if (!encode_queries(&q_map, q, q_row_stride, q_head_stride, c->head_dim, q_heads, n_rows, group, tile_nodes))
+    return set_error(SV_ERR_CUDA, "the query rows' strides or sizes cannot be described to the copy engine");
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return launch_status(e, "device");
+  const int ctas = std::min(sms, kMaxCtas);
+  const Layout L = layout_of(kMaxCtas, c->head_dim);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  AttendParams a = {};
+  a.out_row_stride = out_row_stride;
+  a.out_head_stride = out_head_stride;
+  a.table = page_table;
+  a.seq_len = seq_len;
+  a.node_offsets = node_offsets;
+  a.parent = parent;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = out_lse;
+  a.status = reinterpret_cast<uint32_t*>(w);
+  a.any_bad = reinterpret_cast<int32_t*>(w) + 1;
+  a.bad = w + L.bad;
+  a.jobs = reinterpret_cast<Job*>(w + L.jobs);
+  a.parts = reinterpret_cast<float*>(w + L.parts);
+  a.n_rows = n_rows;
+  a.width = table_width;
+  a.B = B;
+  a.Nmax = Nmax;
+  a.pages = c->pages;
+  while ((1 << a.shift) < c->page_size) ++a.shift;
+  a.q_heads = q_heads;
+  a.kv_heads = c->kv_heads;
+  a.units = pair ? c->kv_heads / 2 : c->kv_heads;
+  a.group = group;
+  a.tile_nodes = tile_nodes;
+  a.tile_rows = tile_nodes * group;
+  a.over_group = (65536 + group - 1) / group;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale = scale * c->k_scale;
+  a.v_scale = c->v_scale;
+  a.pool = static_cast<const unsigned char*>(c->pool) + layer * c->layer_stride;
+  a.page_stride = c->page_stride;
+  a.head_stride = c->head_stride;
+  const int copies = tile_nodes * group * (pair ? 2 : 1) <= 64 ? 2 : 1;
+  a.half_rows = kTile / copies / (pair ? 2 : 1);
+  a.extra = kExtra;
+  const auto launch = pair                 ? (copies == 2 ? launch_attention<64, true, 2, true> : launch_attention<64, true, 1, true>)
+                      : c->head_dim == 128 ? (copies == 2 ? launch_attention<128, false, 2, true> : launch_attention<128, false, 1, true>)
+                                           : (copies == 2 ? launch_attention<64, false, 2, true> : launch_attention<64, false, 1, true>);
+  return launch_status(launch(a, q_map, q_map, q_map, ctas, stream), "attention");
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -1061,20 +1360,21 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
   a.window = window;
   a.sinks = sinks;
   a.scale = scale;
+  a.v_scale = 1.0f;
   // as many copies of a row tile as its height leaves room for (window's 33 trees, 32 rows: 41 us with four, 43 with two, 45
   // with one; 64 trees of 64 rows: 114 with two, 121 with one; 64 contexts of 1000, 4 rows: 57, 58, 60)
   const int tile_rows = tile_nodes * group * (pair ? 2 : 1), copies = tile_rows <= 32 ? 4 : tile_rows <= 64 ? 2 : 1;
   a.half_rows = kTile / copies / (pair ? 2 : 1);
   a.extra = kExtra;
-  const auto launch = pair                 ? (copies == 4   ? launch_attention<64, true, 4>
-                                              : copies == 2 ? launch_attention<64, true, 2>
-                                                            : launch_attention<64, true, 1>)
-                      : c->head_dim == 128 ? (copies == 4   ? launch_attention<128, false, 4>
-                                              : copies == 2 ? launch_attention<128, false, 2>
-                                                            : launch_attention<128, false, 1>)
-                                           : (copies == 4   ? launch_attention<64, false, 4>
-                                              : copies == 2 ? launch_attention<64, false, 2>
-                                                            : launch_attention<64, false, 1>);
+  const auto launch = pair                 ? (copies == 4   ? launch_attention<64, true, 4, false>
+                                              : copies == 2 ? launch_attention<64, true, 2, false>
+                                                            : launch_attention<64, true, 1, false>)
+                      : c->head_dim == 128 ? (copies == 4   ? launch_attention<128, false, 4, false>
+                                              : copies == 2 ? launch_attention<128, false, 2, false>
+                                                            : launch_attention<128, false, 1, false>)
+                                           : (copies == 4   ? launch_attention<64, false, 4, false>
+                                              : copies == 2 ? launch_attention<64, false, 2, false>
+                                                            : launch_attention<64, false, 1, false>);
   return launch_status(launch(a, q_map, k_map, v_map, ctas, stream), "attention");
 }
 

@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "sv_decode4.cuh"
 #include "sv_device.cuh"
 #include "sv_line.cuh"
 #include "sv_ops.h"
@@ -49,6 +50,10 @@ constexpr float kLazyGrowth4 = 8.0f;      // log2 units by which a maximum may g
 constexpr float kBias = 4.0f;             // P is 2^kBias at the maximum that it is scaled to
 constexpr int kExtra4 = 2;                // places of the line for a row tile's beginning and end, in chunks
 constexpr int kMaxStages4 = 4;
+#ifndef SVX_FROM
+#define SVX_FROM 16
+#endif
+constexpr int kTilesFrom = SVX_FROM;            // rows above which tiles of 128 rows take the call
 
 struct Attend4Params : Line, Marks, Outputs {
   const __nv_bfloat16* q;
@@ -84,27 +89,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Four bytes of two codes each: pairs of float16, the low half's code first.
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t decode_scales(uint16_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-  return h;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -646,7 +630,7 @@ size_t sv_attention4_workspace_size(const sv_cache4* c, int q_heads) {
     set_error(SV_ERR_INVALID_ARG, "q_heads=%d: 1 to 128 times kv_heads=%d are needed", q_heads, c->kv_heads);
     return 0;
   }
-  return layout4_of(c->head_dim).total;
+  return std::max(layout4_of(c->head_dim).total, attention4_tiles_workspace(c->head_dim));
 }
 
 sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride,
@@ -679,6 +663,10 @@ sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64
                         ((static_cast<int64_t>(Nmax) * group + rows - 1) / rows);
   if (tiles > INT_MAX || tiles * c->kv_heads > INT_MAX || tiles * c->kv_heads * B > INT_MAX)
     return set_error(SV_ERR_INVALID_ARG, "B=%d requests of up to %lld tiles a head are too many for one call", B, (long long)tiles);
+  // more rows than a warp's tile holds: decoding once for up to 128 rows
+  if (Nmax * group > kTilesFrom)
+    return attention4_tiles(c, layer, q, q_row_stride, q_head_stride, q_heads, page_table, table_width, seq_len, node_offsets, n_rows,
+                            parent, B, Nmax, scale, window, sinks, out, out_row_stride, out_head_stride, out_lse, ws, stream);
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return launch_status(e, "device");

@@ -82,7 +82,7 @@ struct Segment {
 };
 // (a: in shared memory; a kernel parameter passed by reference is read through global memory, 0.3 us a field)
 template <int T>
-__device__ __noinline__ Segment segment_at(const Line& a, const uint32_t* before, uint32_t t, uint32_t end) {
+__device__ __forceinline__ Segment segment_at_here(const Line& a, const uint32_t* before, uint32_t t, uint32_t end) {
   int lo = 0, hi = a.B;  // the last request whose tiles begin at or before t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -100,6 +100,17 @@ __device__ __noinline__ Segment segment_at(const Line& a, const uint32_t* before
   s.head = static_cast<int>(unit / s.r.mtiles);   // a head's row tiles are neighbours: they share its tiles in L2
   s.mtile = static_cast<int>(unit - static_cast<uint32_t>(s.head) * s.r.mtiles);
   return s;
+}
+template <int T>
+__device__ __noinline__ Segment segment_at_call(const Line& a, const uint32_t* before, uint32_t t, uint32_t end) {
+  return segment_at_here<T>(a, before, t, end);
+}
+// kHere: in line, for kernels whose warpgroups share out their registers (those may call nothing); otherwise a function, as code
+// that runs once in a while keeps the rest out of the instruction cache.
+template <int T, bool kHere = false>
+__device__ __forceinline__ Segment segment_at(const Line& a, const uint32_t* before, uint32_t t, uint32_t end) {
+  if constexpr (kHere) return segment_at_here<T>(a, before, t, end);
+  else return segment_at_call<T>(a, before, t, end);
 }
 template <int T>
 __device__ __forceinline__ int tile_slot(const Request& r, int j) {
@@ -127,7 +138,7 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int at) {
 // Bounded wait (about 2 s), polling: the waits between products and softmax are a fraction of a microsecond each, and
 // a suspended try_wait oversleeps them.  The loop is not inlined: with it at every wait the kernel's code does not
 // stay in the instruction cache.
-__device__ __noinline__ bool still_waiting(uint64_t* began, volatile int32_t* dead, uint32_t* status) {
+__device__ __forceinline__ bool still_waiting_here(uint64_t* began, volatile int32_t* dead, uint32_t* status) {
   const uint64_t now = globaltimer_ns();
   if (*began == 0) *began = now;
   if (!*dead && now - *began <= kWaitLimitNs) return true;
@@ -135,20 +146,37 @@ __device__ __noinline__ bool still_waiting(uint64_t* began, volatile int32_t* de
   *dead = 1;
   return false;
 }
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
+__device__ __noinline__ bool still_waiting_call(uint64_t* began, volatile int32_t* dead, uint32_t* status) {
+  return still_waiting_here(began, dead, status);
+}
+template <bool kHere = false>
+__device__ __forceinline__ bool still_waiting(uint64_t* began, volatile int32_t* dead, uint32_t* status) {
+  if constexpr (kHere) return still_waiting_here(began, dead, status);
+  else return still_waiting_call(began, dead, status);
+}
+template <bool kHere>
+__device__ __forceinline__ bool wait_slow_here(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
   uint64_t began = 0;
+#pragma unroll 1
   for (uint32_t it = 1;; ++it) {
     if (it >= 16) __nanosleep(40);
     if (mbar_test_wait(bar, parity)) return true;
-    if ((it & 255u) == 0 && !still_waiting(&began, dead, status)) return false;
+    if ((it & 255u) == 0 && !still_waiting<kHere>(&began, dead, status)) return false;
   }
 }
+__device__ __noinline__ bool wait_slow_call(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
+  return wait_slow_here<false>(bar, parity, dead, status);
+}
+template <bool kHere = false>
 __device__ __forceinline__ bool wait_or_leave(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
-  return mbar_test_wait(bar, parity) || wait_slow(bar, parity, dead, status);
+  if (mbar_test_wait(bar, parity)) return true;
+  if constexpr (kHere) return wait_slow_here<true>(bar, parity, dead, status);
+  else return wait_slow_call(bar, parity, dead, status);
 }
 // The same by a whole warp: every lane gets the same answer.
+template <bool kHere = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* dead, uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, wait_or_leave(bar, parity, dead, status));
+  return __all_sync(0xFFFFFFFFu, wait_or_leave<kHere>(bar, parity, dead, status));
 }
 
 __device__ __forceinline__ void mark_bad(const Marks& a, int request, uint32_t bits) {

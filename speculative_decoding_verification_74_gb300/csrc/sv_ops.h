@@ -26,6 +26,13 @@ sv_status check_cache(const sv_cache* c);
 sv_status check_cache4(const sv_cache4* c);  // (sv_cache4.cu)
 sv_status check_table(const int32_t* page_table, int table_width, const int32_t* seq_len, int B);
 
+// sv_tree_attention4 by tiles of 128 rows (sv_attention.cu): arguments as in sv.h, checked by the caller.
+size_t attention4_tiles_workspace(int head_dim);
+sv_status attention4_tiles(const sv_cache4* c, int layer, const void* q, int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                           const int32_t* page_table, int table_width, const int32_t* seq_len, const int32_t* node_offsets,
+                           int64_t n_rows, const int32_t* parent, int B, int Nmax, float scale, int window, int sinks, void* out,
+                           int64_t out_row_stride, int64_t out_head_stride, float* out_lse, void* ws, void* stream);
+
 inline sv_status launch_status(cudaError_t e, const char* what) {
   return e == cudaSuccess ? SV_OK : set_error(SV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }

@@ -219,6 +219,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ void lds64(uint32_t at, uint32_t& a, uint32_t& b) {
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
 // Registers of this warpgroup's threads from here on.
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -571,7 +584,18 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
       constexpr int kWords = D / 32;   // words of a lane's codes in a group of eight slots
       constexpr int kAll = kHeads * (kRawSlots / 8);  // groups of a chunk: [head][group]
       const int quarter = warp - Role::kDecode, chunk0 = quarter * 32, g = lane >> 2, t4 = lane & 3;
-      const unsigned char* raw = ring + stages * kStageBytes + chunk0 / 8 * kGroupBytes;
+      const uint32_t raw = smem_u32(ring) + stages * kStageBytes + chunk0 / 8 * kGroupBytes;
+      // Where this lane's codes lie in a group, and where its 16-byte pieces (eight dimensions of a slot) go: piece i of a lane at
+      // `to` ^ 16 i.  Half of the lanes take their two 8-byte halves the other way round, so that eight neighbouring lanes' pieces
+      // lie in different banks.
+      // keys: slot g, a quarter of its dimensions; values: slots 2 t4 and 2 t4 + 1, an eighth of the dimensions
+      const uint32_t k_flip = D == 128 && (t4 & 2) ? 1u : 0u, v_flip = D == 128 && (g & 1) ? 1u : 0u;
+      const uint32_t k_piece = t4 * kWords, v_piece = g * (kWords / 2);
+      const uint32_t k_to = (k_piece >> 3) * kHalfBytes + (chunk0 + g) * 128 + (((k_piece ^ g) & 7) ^ (2 * k_flip)) * 16;
+      const uint32_t v_to = (v_piece >> 3) * kHalfBytes + (chunk0 + 2 * t4 + v_flip) * 128 + ((v_piece ^ (2 * t4 + v_flip)) & 7) * 16;
+      const uint32_t v_to2 = (v_piece >> 3) * kHalfBytes + (chunk0 + 2 * t4 + (v_flip ^ 1)) * 128 + ((v_piece ^ (2 * t4 + (v_flip ^ 1))) & 7) * 16;
+      const uint32_t k_low = k_flip ? 0x3232 : 0x1010, k_high = k_flip ? 0x1010 : 0x3232;  // selectors of the scales
+      const uint32_t v_low = v_flip ? 0x3232 : 0x1010, v_high = v_flip ? 0x1010 : 0x3232;
       Ring codes;
       Ring at;
       uint32_t filled = 0, seg = 0;
@@ -612,7 +636,7 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
           for (int value = 0; value < 2; ++value) {
             if (filled >= stages) go = warp_wait<kFour>(&sm.empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
             if (!go) break;
-            unsigned char* stage = ring + at.stage * kStageBytes;
+            const uint32_t stage = smem_u32(ring) + at.stage * kStageBytes;
             if (value == 0) go = warp_wait<kFour>(&sm.raw_full[codes.stage], codes.parity, &sm.dead, a.status);
             // a chunk's codes and scales are read before the one before it is stored: loads do not pass stores by themselves
             uint32_t w[kAll][kWords], two[kAll], next_w[kAll][kWords], next_two[kAll];
@@ -620,19 +644,15 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
 #pragma unroll
               for (int x = 0; x < kAll; ++x) {
                 const int head = x / (kRawSlots / 8), u = x % (kRawSlots / 8);
-                const unsigned char* group = raw + (codes.stage * kHeads + head) * kHeadBytes + (c * (kRawSlots / 8) + u) * kGroupBytes + (value ? 4 * D + D / 2 : 0);
+                const uint32_t group = raw + (codes.stage * kHeads + head) * kHeadBytes + (c * (kRawSlots / 8) + u) * kGroupBytes + (value ? 4 * D + D / 2 : 0);
                 if constexpr (D == 128) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(group + lane * 16);
-                  next_w[x][0] = v.x;
-                  next_w[x][1] = v.y;
-                  next_w[x][2] = v.z;
-                  next_w[x][3] = v.w;
-                  next_two[x] = *reinterpret_cast<const uint16_t*>(group + 4 * D + lane * 2);
+                  const uint32_t at_codes = group + lane * 16 + (value ? v_flip : k_flip) * 8;
+                  lds64(at_codes, next_w[x][0], next_w[x][1]);
+                  lds64(at_codes ^ 8, next_w[x][2], next_w[x][3]);
+                  next_two[x] = lds16(group + 4 * D + lane * 2);
                 } else {
-                  const uint2 v = *reinterpret_cast<const uint2*>(group + lane * 8);
-                  next_w[x][0] = v.x;
-                  next_w[x][1] = v.y;
-                  next_two[x] = value ? *reinterpret_cast<const uint16_t*>(group + 4 * D + (g >> 1) * 8 + t4 * 2) : group[4 * D + lane];
+                  lds64(group + lane * 8, next_w[x][0], next_w[x][1]);
+                  next_two[x] = value ? lds16(group + 4 * D + (g >> 1) * 8 + t4 * 2) : lds8(group + 4 * D + lane);
                 }
               }
             };
@@ -640,55 +660,34 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
-            for (int x = 0; x < kAll; ++x) {
-              two[x] = next_two[x];
+              for (int x = 0; x < kAll; ++x) {
+                two[x] = next_two[x];
 #pragma unroll
-              for (int i = 0; i < kWords; ++i) w[x][i] = next_w[x][i];
-            }
-            if (c == 0) fetch(1);
+                for (int i = 0; i < kWords; ++i) w[x][i] = next_w[x][i];
+              }
+              if (c == 0) fetch(1);
 #pragma unroll
-            for (int x = 0; x < kAll; ++x) {
-              const int head = x / (kRawSlots / 8) % kHeads, u = x % (kRawSlots / 8);
-              const int row0 = chunk0 + c * kRawSlots + u * 8;
-              // 16 bytes: eight dimensions of a slot, piece y of its row
-              auto put = [&](int slot_in, int y, const uint32_t (&o)[4]) {
-                *reinterpret_cast<uint4*>(stage + (head + (y >> 3)) * kHalfBytes + (row0 + slot_in) * 128 + ((y ^ slot_in) & 7) * 16) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-              };
-              uint32_t by = decode_scales(static_cast<uint16_t>(two[x]));
-              if (value == 0) {  // slot g, a quarter of its dimensions
-                const uint32_t low = __byte_perm(by, by, 0x1010), high = D == 128 ? __byte_perm(by, by, 0x3232) : low;
-                // (for neighbouring lanes' pieces in different banks the upper quarters go in another order)
-                const bool flip = D == 128 && (t4 & 2) != 0;
+              for (int x = 0; x < kAll; ++x) {
+                const int head = x / (kRawSlots / 8), u = x % (kRawSlots / 8);
+                const uint32_t to = stage + head * kHalfBytes + (c * kRawSlots + u * 8) * 128;
+                uint32_t by = decode_scales(static_cast<uint16_t>(two[x]));
+                if (value == 1 && live != 0xFFFFFFFFu) {
+                  const uint32_t bits = live >> (c * kRawSlots + u * 8 + 2 * t4);
+                  by &= ((bits & 1u) ? 0xFFFFu : 0u) | ((bits & 2u) ? 0xFFFF0000u : 0u);
+                }
+                const uint32_t low = __byte_perm(by, by, D == 64 && value == 0 ? 0x1010 : value ? v_low : k_low);
+                const uint32_t high = D == 64 && value == 0 ? low : __byte_perm(by, by, value ? v_high : k_high);
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) {
-                  const uint32_t word = D == 128 && flip ? w[x][i ^ 2] : w[x][i];
-                  const uint32_t scale = D == 128 ? (((i & 2) != 0) != flip ? high : low) : low;
                   uint32_t h[4];
-                  decode8(word, h);
+                  decode8(w[x][i], h);
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(scale));
-                  put(g, t4 * kWords + (D == 128 && flip ? i ^ 2 : i), h);
-                }
-              } else {           // slots 2 t4 and 2 t4 + 1, an eighth of their dimensions
-                const uint32_t bits = live >> (c * kRawSlots + u * 8 + 2 * t4);
-                by &= ((bits & 1u) ? 0xFFFFu : 0u) | ((bits & 2u) ? 0xFFFF0000u : 0u);
-                const bool flip = D == 128 && (g & 1) != 0;  // (as above: the odd slot first)
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                  const uint32_t its = __byte_perm(by, by, (o == 1) != flip ? 0x3232 : 0x1010);
-#pragma unroll
-                  for (int i = 0; i < kWords / 2; ++i) {
-                    const uint32_t word = flip ? w[x][(o ^ 1) * (kWords / 2) + i] : w[x][o * (kWords / 2) + i];
-                    uint32_t h[4];
-                    decode8(word, h);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(its));
-                    put(2 * t4 + (flip ? o ^ 1 : o), g * (kWords / 2) + i, h);
-                  }
+                  for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(2 * i < kWords ? low : high));
+                  constexpr int kHalf = kWords / 2;
+                  const uint32_t place = value == 0 ? to + (k_to ^ (16 * i)) : i < kHalf ? to + (v_to ^ (16 * i)) : to + (v_to2 ^ (16 * (i - kHalf)));
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(place), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
                 }
               }
-            }
             }
             if (value == 1) {  // the codes are done with
               __syncwarp();

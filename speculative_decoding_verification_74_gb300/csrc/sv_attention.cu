@@ -248,6 +248,7 @@ __device__ __forceinline__ int over_group(int row, uint32_t over) { return stati
 
 // The part of shared memory with a fixed size; then come the tiles before each request [B], the parents of two segments'
 // trees [2][Nmax] and, 1024-byte aligned, Q and the ring.
+static_assert(kMaxRaw == 2 && kMaxStages <= 32, "the barriers' threads");
 template <bool kFour>
 struct Smem {
   Line line;
@@ -300,33 +301,38 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
   unsigned char* ring = q_buf + kHalves * kHalfBytes;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (known to be the same in all lanes)
-  if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&sm.full[i], kFour ? 128 : 1);
-      mbar_init(&sm.empty[i], 1);
+  // (a few barriers a thread: by one thread they take 1 to 2 us)
+  if (tid < a.stages) {
+    mbar_init(&sm.full[tid], kFour ? 128 : 1);
+    mbar_init(&sm.empty[tid], 1);
+  } else if (tid >= 32 && tid < 34) {
+    const int i = tid - 32;
+    mbar_init(&sm.q_raw[i], 1);
+    mbar_init(&sm.q_full[i], kFour ? 128 : 1);
+    mbar_init(&sm.seg_free[i], kSoftThreads);
+    mbar_init(&sm.mix_full[i], kGroupThreads);
+    mbar_init(&sm.mix_free[i], kGroupThreads);
+  } else if (tid >= 64 && tid < 66) {
+    const int i = tid - 64;
+    mbar_init(&sm.s_full[i], 1);
+    mbar_init(&sm.p_full[i], kGroupThreads);
+    mbar_init(&sm.pv_done[i], 1);
+    if constexpr (kFour) {
+      mbar_init(&sm.raw_full[i], 1);
+      mbar_init(&sm.raw_empty[i], 4);
     }
-    if constexpr (kFour)
-      for (int i = 0; i < kMaxRaw; ++i) {
-        mbar_init(&sm.raw_full[i], 1);
-        mbar_init(&sm.raw_empty[i], 4);
-      }
+  } else if (tid == 96) {
     mbar_init(&sm.q_free, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.q_raw[i], 1);
-      mbar_init(&sm.q_full[i], kFour ? 128 : 1);
-      mbar_init(&sm.seg_free[i], kSoftThreads);
-      mbar_init(&sm.mix_full[i], kGroupThreads);
-      mbar_init(&sm.mix_free[i], kGroupThreads);
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kGroupThreads);
-      mbar_init(&sm.pv_done[i], 1);
-    }
     mbar_init(&sm.sums_full, kSoftThreads);
     mbar_init(&sm.o_free, kSoftThreads);
-    sm.dead = 0;
-    sm.line = a;
+  }
+  if (tid < 128) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
+  }
+  if (tid == 0) {
+    sm.dead = 0;
+    sm.line = a;
   }
   if constexpr (kPair) {  // the other head's dimensions: never written again
     for (int i = tid; i < kHalves * kHalfBytes / 16; i += kThreads) reinterpret_cast<uint4*>(q_buf)[i] = make_uint4(0, 0, 0, 0);

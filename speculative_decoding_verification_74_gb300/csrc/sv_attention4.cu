@@ -135,13 +135,13 @@ __global__ void __launch_bounds__(Tile4<N>::kThreads, 1) attend4_kernel(const At
   uint32_t* before = reinterpret_cast<uint32_t*>(dyn + static_cast<size_t>(kWarps) * a.stages * kChunkBytes);  // [B]
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int g = lane >> 2, t4 = lane & 3;
+  // (a barrier a thread: by one thread they take 2 us)
+  for (int i = tid; i < kWarps * kMaxStages4; i += kThreads4) mbar_init(&sm.full[i / kMaxStages4][i % kMaxStages4], 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  fence_proxy_async_smem();
   if (tid == 0) {
-    for (int w = 0; w < kWarps; ++w)
-      for (int i = 0; i < a.stages; ++i) mbar_init(&sm.full[w][i], 1);
     sm.dead = 0;
     sm.line = a;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    fence_proxy_async_smem();
   }
   pdl_wait();
   pdl_trigger();
@@ -197,6 +197,16 @@ __global__ void __launch_bounds__(Tile4<N>::kThreads, 1) attend4_kernel(const At
       if (load.kv0 >= load.kv1) continue;                    // (only places before a row tile's chunks)
       if (lane == 0) sm.queue[warp][found % kQueue] = load;
       ++found;
+      // its rows of Q, before its chunks: loads behind a ring's copies wait for all of them
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int row = load.mtile * kRows + 8 * n + g;
+        if (row < load.r.nodes * a.group) {
+          const int node = row / a.group;
+          const __nv_bfloat16* q = a.q + (load.r.first + node) * a.q_row_stride + (load.head * a.group + row - node * a.group) * a.q_head_stride + t4 * (D / 4);
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
+        }
+      }
       load_j = load.kv0;
       load_end = load.kv1;
       block = -1;

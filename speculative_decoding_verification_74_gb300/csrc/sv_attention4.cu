@@ -215,31 +215,52 @@ __global__ void __launch_bounds__(Tile4<N>::kThreads, 1) attend4_kernel(const At
     return false;
   };
   bool more = settle();
+  bool page_there = false;
+  const unsigned char* page_at = nullptr;
+  // page numbers of 32 entries from a multiple of 32 on
+  auto pages_from = [&](int entry) {
+    if ((entry >> 5) == block) return;
+    block = entry >> 5;
+    const int e = 32 * block + lane;
+    page_now = (static_cast<int64_t>(e) << a.shift) < load.r.len + load.r.nodes ? a.table[static_cast<int64_t>(load.request) * a.width + e] : -1;
+  };
   auto ask = [&]() {
-    const int s0 = tile_slot<kChunk>(load.r, load_j), slot = s0 + (lane << piece_shift);
-    const int entry = s0 >> a.shift;
-    const int end = load.r.len + load.r.nodes;
-    if ((entry >> 5) != block) {
-      block = entry >> 5;
-      const int e = 32 * block + lane;
-      page_now = (static_cast<int64_t>(e) << a.shift) < end ? a.table[static_cast<int64_t>(load.request) * a.width + e] : -1;
-    }
-    const int page = __shfl_sync(0xFFFFFFFFu, page_now, (entry + (a.shift < 5 ? lane : 0)) & 31);
-    bool wanted = copies && slot < end;
-    if (a.window > 0) wanted = wanted && (slot < a.sinks || slot + (1 << piece_shift) > load.r.len - a.window + 1);
-    if (wanted && (page < 0 || page >= a.pages)) {
-      mark_bad(a, load.request, SV_DEV_BAD_PAGE);
-      wanted = false;
-    }
+    const int s0 = tile_slot<kChunk>(load.r, load_j);
     constexpr int kUnit = kGroupBytes / 8;                    // bytes of a slot
     uint64_t* bar = &sm.full[warp][ask_stage];
-    const int bytes = (__popc(__ballot_sync(0xFFFFFFFFu, wanted)) << piece_shift) * kUnit;
-    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-    __syncwarp();
-    if (wanted)
-      bulk_g2s(ring + ask_stage * kChunkBytes + (lane << piece_shift) * kUnit,
-               a.pool + page * a.page_stride + load.head * a.head_stride + (slot & ((1 << a.shift) - 1)) * kUnit,
-               kUnit << piece_shift, bar);
+    if (a.shift >= 5) {                                       // one copy, of a page that is looked up where it begins
+      const int in_page = s0 & ((1 << a.shift) - 1);
+      if (in_page == 0 || block < 0) {
+        const int entry = s0 >> a.shift;
+        pages_from(entry);
+        const int page = __shfl_sync(0xFFFFFFFFu, page_now, entry & 31);
+        page_there = page >= 0 && page < a.pages;
+        if (!page_there) mark_bad(a, load.request, SV_DEV_BAD_PAGE);
+        page_at = a.pool + page * a.page_stride + load.head * a.head_stride;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, page_there ? kChunkBytes : 0);
+        if (page_there) bulk_g2s(ring + ask_stage * kChunkBytes, page_at + in_page * kUnit, kChunkBytes, bar);
+      }
+      __syncwarp();
+    } else {
+      const int entry = s0 >> a.shift, slot = s0 + (lane << piece_shift);
+      pages_from(entry);
+      const int page = __shfl_sync(0xFFFFFFFFu, page_now, (entry + lane) & 31);
+      bool wanted = copies && slot < load.r.len + load.r.nodes;
+      if (a.window > 0) wanted = wanted && (slot < a.sinks || slot + (1 << piece_shift) > load.r.len - a.window + 1);
+      if (wanted && (page < 0 || page >= a.pages)) {
+        mark_bad(a, load.request, SV_DEV_BAD_PAGE);
+        wanted = false;
+      }
+      const int bytes = (__popc(__ballot_sync(0xFFFFFFFFu, wanted)) << piece_shift) * kUnit;
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      if (wanted)
+        bulk_g2s(ring + ask_stage * kChunkBytes + (lane << piece_shift) * kUnit,
+                 a.pool + page * a.page_stride + load.head * a.head_stride + (slot & ((1 << a.shift) - 1)) * kUnit,
+                 kUnit << piece_shift, bar);
+    }
     ask_stage = ask_stage + 1 == static_cast<uint32_t>(a.stages) ? 0 : ask_stage + 1;
     ++asked;
     ++load_j;

@@ -248,12 +248,15 @@ constexpr int32_t kShares = -2;   // it shares the full pages, there is nothing 
 constexpr int32_t kEmpties = -3;  // it names no source
 constexpr int32_t kFailed = -4;   // in marks[0 .. rows): nothing changes
 
-// What becomes of every row, and the pages: one CTA.  Shared memory: four ints per row.
-__global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_t* table, int width, int rows, int32_t* seq_len,
+// What becomes of every row, and the pages: one CTA.  Shared memory: five ints per row, and with kWhole the table, which is then
+// rewritten here too (without it by gather_kernel).
+template <bool kWhole>
+__global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, int32_t* table, int width, int rows, int32_t* seq_len,
                                                             const int32_t* src, int32_t* out_ok, int32_t* marks,
                                                             uint32_t* status) {
   extern __shared__ int32_t per_row[];
-  int32_t *from = per_row, *len = per_row + rows, *first = per_row + 2 * rows, *pair_of = per_row + 3 * rows;
+  int32_t *from = per_row, *len = per_row + rows, *first = per_row + 2 * rows, *pair_of = per_row + 3 * rows, *mark = per_row + 4 * rows;
+  int32_t* old = per_row + 5 * rows;
   __shared__ int buf[33];
   __shared__ uint32_t wrong;
   pdl_wait();
@@ -264,6 +267,10 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_
     len[j] = seq_len[j];
     first[j] = INT_MAX;  // the first row that names row j: INT_MAX = none
   }
+  if constexpr (kWhole)
+    for (int x = threadIdx.x; x < rows * width; x += kPageThreads) old[x] = table[x];
+  const int32_t* entries = kWhole ? old : table;
+  const int free_pages = count_free(p);
   __syncthreads();
   for (int j = threadIdx.x; j < rows; j += kPageThreads) {
     const int s = from[j];
@@ -271,20 +278,24 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_
     else if (s >= 0) atomicMin(first + s, s == j ? -1 : j);  // the row itself comes before all others
   }
   __syncthreads();
+  bool drops = false;  // some row's pages are given back
   for (int j = warp; j < rows; j += kPageThreads / 32) {
-    if (first[j] == INT_MAX) continue;
+    const int32_t* row = entries + static_cast<int64_t>(j) * width;
+    if (first[j] == INT_MAX) {
+      drops |= row[0] >= 0;
+      continue;
+    }
     const int64_t held = (static_cast<int64_t>(len[j]) + (1 << p.shift) - 1) >> p.shift;
     if (len[j] < 0 || held > width) {
       if (lane == 0) atomicOr(&wrong, SV_DEV_BAD_SEQ);
       continue;
     }
-    const int32_t* row = table + static_cast<int64_t>(j) * width;
     bool lacks = false;
 #pragma unroll 4
     for (int e = lane; e < held; e += 32) lacks |= static_cast<uint32_t>(row[e]) >= static_cast<uint32_t>(p.pages);
     if (__any_sync(0xFFFFFFFFu, lacks) && lane == 0) atomicOr(&wrong, SV_DEV_BAD_PAGE);
   }
-  __syncthreads();
+  drops = __syncthreads_or(drops);
   uint32_t problem = wrong;
   int total = 0;
   int split[kPerThread], at = 0;
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_
     auto each_entry = [&](auto f) {
       for (int j = warp; j < rows; j += kPageThreads / 32) {
         if (first[j] != INT_MAX) continue;
-        const int32_t* row = table + static_cast<int64_t>(j) * width;
+        const int32_t* row = entries + static_cast<int64_t>(j) * width;
         for (int e0 = 0; e0 < width; e0 += 32) {
           const int page = e0 + lane < width ? row[e0 + lane] : -1;
           if (page >= 0) f(page);
@@ -301,7 +312,7 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_
         }
       }
     };
-    each_entry([&](int page) { give_back(p, page, status); });
+    if (drops) each_entry([&](int page) { give_back(p, page, status); });
     const int part_mask = (1 << p.shift) - 1;
     int sum = 0;
 #pragma unroll
@@ -312,23 +323,28 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_
       sum += split[x];
     }
     at = block_scan(sum, buf, &total);
-    __threadfence_block();
-    __syncthreads();
-    int found;
-    const int rank = block_scan(count_free(p), buf, &found);
+    int found, rank = 0;
+    if (total == 0) {
+      found = 0;
+    } else {
+      __threadfence_block();
+      __syncthreads();
+      rank = block_scan(drops ? count_free(p) : free_pages, buf, &found);
+    }
     if (total > found) {
       problem = SV_DEV_OUT_OF_PAGES;
       __syncthreads();
-      each_entry([&](int page) {
-        if (page < p.pages) atomicAdd(p.refs + page, 1);
-      });
-    } else {
+      if (drops)
+        each_entry([&](int page) {
+          if (page < p.pages) atomicAdd(p.refs + page, 1);
+        });
+    } else if (total > 0) {
 #pragma unroll
       for (int x = 0; x < kPerThread; ++x)
         if (split[x]) pair_of[at++] = threadIdx.x * kPerThread + x;
       __syncthreads();
       take_free(p, rank, total, [&](int r, int page) {
-        marks[pair_of[r]] = page;
+        (kWhole ? mark : marks)[pair_of[r]] = page;
         p.refs[page] = 1;
       });
     }
@@ -338,17 +354,38 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, const int32_
     const int j = threadIdx.x * kPerThread + x;
     if (j >= rows) continue;
     const int s = from[j];
+    int32_t* its = (kWhole ? mark : marks) + j;
     if (problem != 0) {
-      marks[j] = kFailed;
+      *its = kFailed;
     } else {
-      if (s < 0) marks[j] = kEmpties;
-      else if (!split[x]) marks[j] = first[s] == (s == j ? -1 : j) ? kKeeps : kShares;
+      if (s < 0) *its = kEmpties;
+      else if (!split[x]) *its = first[s] == (s == j ? -1 : j) ? kKeeps : kShares;
       seq_len[j] = s < 0 ? 0 : len[s];
     }
   }
   if (threadIdx.x == 0) {
     if (problem != 0) atomicOr(status, problem);
     if (out_ok != nullptr) out_ok[0] = problem == 0;
+  }
+  if constexpr (kWhole) {
+    __syncthreads();
+    for (int j = warp; j < rows; j += kPageThreads / 32) {
+      const int what = mark[j], s = from[j], full = what == kFailed || what == kEmpties ? 0 : len[s] >> p.shift;
+      if (lane == 0) marks[j] = what >= 0 ? old[s * width + full] : what;
+      if (what == kFailed || (what == kKeeps && s == j)) continue;
+      for (int e = lane; e < width; e += 32) {
+        int32_t page = -1;
+        if (what == kKeeps) {
+          page = old[s * width + e];
+        } else if (what != kEmpties && e < full) {
+          page = old[s * width + e];
+          atomicAdd(p.refs + page, 1);
+        } else if (what >= 0 && e == full) {
+          page = what;
+        }
+        table[static_cast<int64_t>(j) * width + e] = page;
+      }
+    }
   }
 }
 
@@ -648,12 +685,15 @@ cudaError_t release_pages(const Pool& p, int32_t* table, int width, int rows, in
 }
 cudaError_t reorder_pages(const Pool& p, int32_t* table, int width, int rows, int32_t* seq_len, const int32_t* src,
                           int32_t* out_ok, void* ws, void* stream) {
-  const size_t per_row = sizeof(int32_t) * 4 * rows;
-  cudaError_t e = allow_smem<plan_kernel>(sizeof(int32_t) * 4 * SV_MAX_BATCH);
+  const size_t per_row = sizeof(int32_t) * 5 * rows;
+  // a table of up to 16384 entries is rewritten by the CTA that plans (16 requests of four beams 22 us with it, 25 without)
+  const bool whole = static_cast<int64_t>(rows) * width <= 16384;
+  cudaError_t e = whole ? allow_smem<plan_kernel<true>>(sizeof(int32_t) * (5 * SV_MAX_BATCH + 16384)) : allow_smem<plan_kernel<false>>(sizeof(int32_t) * 5 * SV_MAX_BATCH);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(plan_kernel, dim3(1), kPageThreads, per_row, stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows,
+  e = launch_dependent(whole ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPageThreads,
+                       per_row + (whole ? sizeof(int32_t) * rows * width : 0), stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows,
                        seq_len, src, out_ok, marks_of(ws), status_of(ws));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole) return e;
   // a CTA holds its columns of every row in at most 32 KB (64 KB for 4096 rows)
   const int columns = std::min(std::max(4, 8192 / rows), std::max(width, 1));
   const size_t bytes = sizeof(int32_t) * columns * rows;

@@ -102,10 +102,22 @@ struct Append4Params {
   uint32_t* status;
 };
 
-// One CTA per (new row, part of the layers): a thread quantises sixteen dimensions of [layer][k, v][head] at a time.
+// One CTA per (new row, part of the layers): a thread quantises sixteen dimensions of [layer][k, v][head] at a time, about four
+// times, the next ones' loads in flight; the first are asked for before the row's place is known.
 __global__ void __launch_bounds__(kRowThreads) append4_kernel(Append4Params a) {
   pdl_wait();
   const int64_t row = blockIdx.x;
+  const int scales_shift = a.r.dim == 128 ? 3 : 2;         // sixteens of a head
+  const uint32_t per_side = a.r.heads << scales_shift, items = 2 * a.layers * per_side, step = gridDim.y * kRowThreads;
+  auto fetch = [&](uint32_t x, uint4 (&w)[2]) {
+    const uint32_t side = x / per_side, e = x - side * per_side, layer = side >> 1;
+    const uint4* from = reinterpret_cast<const uint4*>(((side & 1) ? a.v_new : a.k_new) + layer * a.new_layer_stride + row * a.new_row_stride) + 2 * e;
+    w[0] = __ldg(from);
+    w[1] = __ldg(from + 1);
+  };
+  uint32_t x = blockIdx.y * kRowThreads + threadIdx.x;
+  uint4 next[2] = {};
+  if (x < items) fetch(x, next);
   __shared__ int64_t where;
   __shared__ int place;
   if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -120,21 +132,19 @@ __global__ void __launch_bounds__(kRowThreads) append4_kernel(Append4Params a) {
       if (first >= 0 && last <= a.n_rows && row >= first && row < last) {
         where = len < 0 ? -1 : group_offset(a.r, a.table + static_cast<int64_t>(lo) * a.width, a.width, len + (row - first));
         place = static_cast<int>((len + (row - first)) & 7);
-        if (where < 0) atomicOr(a.status, len < 0 ? SV_DEV_BAD_SEQ : SV_DEV_BAD_PAGE);
+        if (where < 0 && blockIdx.y == 0) atomicOr(a.status, len < 0 ? SV_DEV_BAD_SEQ : SV_DEV_BAD_PAGE);
       }
     }
   }
   __syncthreads();
   if (where < 0) return;
-  const int scales_shift = a.r.dim == 128 ? 3 : 2;         // sixteens of a head
-  const uint32_t per_side = a.r.heads << scales_shift, items = 2 * a.layers * per_side;
   bool wrong = false;
-  for (uint32_t x = blockIdx.y * kRowThreads + threadIdx.x; x < items; x += gridDim.y * kRowThreads) {
+  for (; x < items; x += step) {
+    const uint4 w[2] = {next[0], next[1]};
+    if (x + step < items) fetch(x + step, next);
     const uint32_t side = x / per_side, e = x - side * per_side, layer = side >> 1;
     const bool value = side & 1;
     const int head = e >> scales_shift, part = e & ((1 << scales_shift) - 1);
-    const uint4* from = reinterpret_cast<const uint4*>((value ? a.v_new : a.k_new) + layer * a.new_layer_stride + row * a.new_row_stride) + 2 * e;
-    const uint4 w[2] = {__ldg(from), __ldg(from + 1)};
     float t[16], top = 0.0f;
     const float inverse = value ? a.v_inverse : a.k_inverse;
 #pragma unroll
@@ -389,7 +399,7 @@ sv_status sv_cache4_append(const sv_cache4* c, int layer, int layers, const int3
   a.status = status_of(ws);
   const int64_t items = static_cast<int64_t>(layers) * 2 * c->kv_heads * (c->head_dim / 16);
   if (items > INT_MAX) return set_error(SV_ERR_INVALID_ARG, "layers=%d: too many for one call", layers);
-  const int64_t groups = std::min<int64_t>(64, (items + kRowThreads - 1) / kRowThreads);
+  const int64_t groups = std::min<int64_t>(64, (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
   return launch_status(launch_dependent(append4_kernel, dim3(static_cast<unsigned>(n_rows), static_cast<unsigned>(groups)),
                                         kRowThreads, 0, stream, SV_KERNEL_CACHE_ROWS, 1, a),
                        "append");
@@ -422,7 +432,7 @@ sv_status sv_cache4_commit(const sv_cache4* c, int32_t* page_table, int table_wi
   a.status = status_of(ws);
   a.arrived = arrived_of(ws);
   const int64_t items = static_cast<int64_t>(c->layers) * 2 * c->kv_heads * (c->head_dim / 8);
-  const int64_t groups = std::min<int64_t>(64, (items + kRowThreads - 1) / kRowThreads);
+  const int64_t groups = std::min<int64_t>(64, (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
   return launch_status(launch_dependent(commit4_kernel, dim3(static_cast<unsigned>(groups), B), kRowThreads,
                                         sizeof(int64_t) * 2 * Nmax, stream, SV_KERNEL_CACHE_ROWS, 1, a),
                        "commit");

@@ -144,3 +144,23 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         assert int(ok) == oracle.reorder(lens, s) == 1
         same(cache, oracle, d_len, lens)
+
+
+def test_wide_tables():
+    """Tables too wide for one CTA, with pages in their first entries only."""
+    rng = np.random.default_rng(7)
+    lens = rng.integers(0, 60, 30)
+    cache, oracle, d_len, lens = make(list(lens), [0] * 30, 400, layers=1, width=2000)
+    for _ in range(3):
+        src = rng.integers(-1, 30, 30)
+        assert int(cache.reorder(d_len, i32(src))) == oracle.reorder(lens, src) == 1
+        same(cache, oracle, d_len, lens)
+    cache, oracle, d_len, lens = make([30, 30, 40], [0] * 3, 14, width=9000)    # 4 + 4 + 5 pages: one is free
+    assert int(cache.reorder(d_len, i32([0, 0, 0]))) == oracle.reorder(lens, [0, 0, 0]) == 1
+    same(cache, oracle, d_len, lens)
+    cache, oracle, d_len, lens = make([30, 30, 40], [0] * 3, 13, width=9000)    # none
+    assert int(cache.reorder(d_len, i32([0, 1, 0]))) == oracle.reorder(lens, [0, 1, 0]) == 1
+    cache, oracle, d_len, lens = make([30, 30, 32, 0], [0] * 4, 12, width=9000)
+    assert int(cache.reorder(d_len, i32([0, 1, 2, 1]))) == oracle.reorder(lens, [0, 1, 2, 1]) == 0
+    same(cache, oracle, d_len, lens)
+    assert sv.sv_query_status(cache.ws)[1] == sv.SV_DEV_OUT_OF_PAGES

@@ -52,13 +52,15 @@ __device__ __forceinline__ int64_t group_offset(const Shape4& r, const int32_t* 
   return page * r.page_stride + ((slot & ((1 << r.shift) - 1)) >> 3) * (9 * r.dim);
 }
 // Places in a group: the eight dimensions from 8 x on of slot i, and their scale.
-__device__ __forceinline__ int code_place(int dim, bool value, int i, int x) {
-  if (!value) return i * (dim >> 1) + 4 * x;
-  const int eighth = dim >> 3, e = 8 * x / eighth;  // (8 or 16 dimensions)
-  return 4 * dim + (dim >> 1) + (4 * e + (i >> 1)) * eighth + (i & 1) * (eighth >> 1) + ((8 * x) & (eighth - 1)) / 2;
+template <int D>
+__device__ __forceinline__ int code_place(bool value, int i, int x) {
+  constexpr int kEighth = D / 8;  // dimensions: 8 or 16
+  const int e = 8 * x / kEighth;
+  return value ? 4 * D + D / 2 + (4 * e + (i >> 1)) * kEighth + (i & 1) * (kEighth / 2) + (8 * x) % kEighth / 2 : i * (D / 2) + 4 * x;
 }
-__device__ __forceinline__ int scale_place(int dim, bool value, int i, int x) {
-  return value ? 8 * dim + (dim >> 1) + (x >> 1) * 8 + i : 4 * dim + i * (dim >> 4) + (x >> 1);
+template <int D>
+__device__ __forceinline__ int scale_place(bool value, int i, int x) {
+  return value ? 8 * D + D / 2 + (x >> 1) * 8 + i : 4 * D + i * (D / 16) + (x >> 1);
 }
 
 // t / s of eight values as e2m1, the first in the low half of the first byte.
@@ -104,20 +106,22 @@ struct Append4Params {
 
 // One CTA per (new row, part of the layers): a thread quantises sixteen dimensions of [layer][k, v][head] at a time, about four
 // times, the next ones' loads in flight; the first are asked for before the row's place is known.
+template <int D>
 __global__ void __launch_bounds__(kRowThreads) append4_kernel(Append4Params a) {
   pdl_wait();
   const int64_t row = blockIdx.x;
-  const int scales_shift = a.r.dim == 128 ? 3 : 2;         // sixteens of a head
-  const uint32_t per_side = a.r.heads << scales_shift, items = 2 * a.layers * per_side, step = gridDim.y * kRowThreads;
-  auto fetch = [&](uint32_t x, uint4 (&w)[2]) {
-    const uint32_t side = x / per_side, e = x - side * per_side, layer = side >> 1;
-    const uint4* from = reinterpret_cast<const uint4*>(((side & 1) ? a.v_new : a.k_new) + layer * a.new_layer_stride + row * a.new_row_stride) + 2 * e;
-    w[0] = __ldg(from);
-    w[1] = __ldg(from + 1);
-  };
-  uint32_t x = blockIdx.y * kRowThreads + threadIdx.x;
+  constexpr int kScales = D / 16;                          // sixteens of a head
+  const uint32_t per_side = a.r.heads * kScales, items = 2 * a.layers * per_side, step = gridDim.y * kRowThreads;
+  // item x is sixteen e of side (layer; k or v)
+  uint32_t x = blockIdx.y * kRowThreads + threadIdx.x, side = x / per_side, e = x - side * per_side;
+  const uint32_t step_side = step / per_side, step_e = step - step_side * per_side;
   uint4 next[2] = {};
-  if (x < items) fetch(x, next);
+  auto fetch = [&](uint32_t its_side, uint32_t its_e) {
+    const uint4* from = reinterpret_cast<const uint4*>(((its_side & 1) ? a.v_new : a.k_new) + (its_side >> 1) * a.new_layer_stride + row * a.new_row_stride) + 2 * its_e;
+    next[0] = __ldg(from);
+    next[1] = __ldg(from + 1);
+  };
+  if (x < items) fetch(side, e);
   __shared__ int64_t where;
   __shared__ int place;
   if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -141,10 +145,16 @@ __global__ void __launch_bounds__(kRowThreads) append4_kernel(Append4Params a) {
   bool wrong = false;
   for (; x < items; x += step) {
     const uint4 w[2] = {next[0], next[1]};
-    if (x + step < items) fetch(x + step, next);
-    const uint32_t side = x / per_side, e = x - side * per_side, layer = side >> 1;
+    const uint32_t layer = side >> 1;
     const bool value = side & 1;
-    const int head = e >> scales_shift, part = e & ((1 << scales_shift) - 1);
+    const int head = e / kScales, part = e % kScales;
+    side += step_side;
+    e += step_e;
+    if (e >= per_side) {
+      e -= per_side;
+      ++side;
+    }
+    if (x + step < items) fetch(side, e);
     float t[16], top = 0.0f;
     const float inverse = value ? a.v_inverse : a.k_inverse;
 #pragma unroll
@@ -168,14 +178,14 @@ __global__ void __launch_bounds__(kRowThreads) append4_kernel(Append4Params a) {
     }
     unsigned char* group = a.pool + layer * a.r.layer_stride + where + head * a.r.head_stride;
     const uint32_t codes[2] = {codes_of(t), codes_of(t + 8)};
-    unsigned char* to = group + code_place(a.r.dim, value, place, 2 * part);
-    if (value && a.r.dim == 64) {  // (two eighths of the dimensions)
+    unsigned char* to = group + code_place<D>(value, place, 2 * part);
+    if (D == 64 && value) {  // (two eighths of the dimensions)
       *reinterpret_cast<uint32_t*>(to) = codes[0];
-      *reinterpret_cast<uint32_t*>(group + code_place(a.r.dim, value, place, 2 * part + 1)) = codes[1];
+      *reinterpret_cast<uint32_t*>(group + code_place<D>(value, place, 2 * part + 1)) = codes[1];
     } else {
       *reinterpret_cast<uint2*>(to) = make_uint2(codes[0], codes[1]);
     }
-    group[scale_place(a.r.dim, value, place, 2 * part)] = scale;
+    group[scale_place<D>(value, place, 2 * part)] = scale;
   }
   if (wrong) atomicOr(a.status, SV_DEV_BAD_VALUE);
 }
@@ -197,6 +207,7 @@ constexpr int kMoveBatch = 8;  // nodes whose pieces a thread holds at once
 // grid (parts of the layers, B).  A thread moves eight dimensions of every accepted node, and with the first eight of sixteen
 // their scale, in path order: node path[j] >= j + 1, so a slot that is written was read before, or is never read.  The
 // request's CTA that finishes last gives back the pages past the new length.
+template <int D>
 __global__ void __launch_bounds__(kRowThreads) commit4_kernel(Commit4Params a) {
   extern __shared__ int64_t moves[];  // [2 * Nmax]: 8 * group offset + place of source and destination (-1 = stays)
   __shared__ int bad, last_one;
@@ -231,7 +242,8 @@ __global__ void __launch_bounds__(kRowThreads) commit4_kernel(Commit4Params a) {
   const bool invalid = wrong || bad != 0;
   if (invalid && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, SV_DEV_BAD_SEQ);
   if (!invalid) {
-    const int parts = a.r.dim >> 3, per_layer = 2 * a.r.heads * parts;
+    constexpr int parts = D / 8;
+    const int per_layer = 2 * a.r.heads * parts;
     const int64_t items = static_cast<int64_t>(a.layers) * per_layer;
     for (int64_t x = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; x < items;
          x += static_cast<int64_t>(gridDim.x) * kRowThreads) {
@@ -250,16 +262,16 @@ __global__ void __launch_bounds__(kRowThreads) commit4_kernel(Commit4Params a) {
           if (j0 + j < keep && moves[2 * (j0 + j)] >= 0) {
             const int64_t m = moves[2 * (j0 + j)];
             const unsigned char* group = base + (m >> 3);
-            codes[j] = *reinterpret_cast<const uint32_t*>(group + code_place(a.r.dim, value, m & 7, part));
-            if (scales) scale[j] = group[scale_place(a.r.dim, value, m & 7, part)];
+            codes[j] = *reinterpret_cast<const uint32_t*>(group + code_place<D>(value, m & 7, part));
+            if (scales) scale[j] = group[scale_place<D>(value, m & 7, part)];
           }
 #pragma unroll
         for (int j = 0; j < kMoveBatch; ++j)
           if (j0 + j < keep && moves[2 * (j0 + j)] >= 0) {
             const int64_t m = moves[2 * (j0 + j) + 1];
             unsigned char* group = base + (m >> 3);
-            *reinterpret_cast<uint32_t*>(group + code_place(a.r.dim, value, m & 7, part)) = codes[j];
-            if (scales) group[scale_place(a.r.dim, value, m & 7, part)] = scale[j];
+            *reinterpret_cast<uint32_t*>(group + code_place<D>(value, m & 7, part)) = codes[j];
+            if (scales) group[scale_place<D>(value, m & 7, part)] = scale[j];
           }
       }
     }
@@ -400,7 +412,7 @@ sv_status sv_cache4_append(const sv_cache4* c, int layer, int layers, const int3
   const int64_t items = static_cast<int64_t>(layers) * 2 * c->kv_heads * (c->head_dim / 16);
   if (items > INT_MAX) return set_error(SV_ERR_INVALID_ARG, "layers=%d: too many for one call", layers);
   const int64_t groups = std::min<int64_t>(64, (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
-  return launch_status(launch_dependent(append4_kernel, dim3(static_cast<unsigned>(n_rows), static_cast<unsigned>(groups)),
+  return launch_status(launch_dependent(c->head_dim == 128 ? append4_kernel<128> : append4_kernel<64>, dim3(static_cast<unsigned>(n_rows), static_cast<unsigned>(groups)),
                                         kRowThreads, 0, stream, SV_KERNEL_CACHE_ROWS, 1, a),
                        "append");
 }
@@ -433,7 +445,7 @@ sv_status sv_cache4_commit(const sv_cache4* c, int32_t* page_table, int table_wi
   a.arrived = arrived_of(ws);
   const int64_t items = static_cast<int64_t>(c->layers) * 2 * c->kv_heads * (c->head_dim / 8);
   const int64_t groups = std::min<int64_t>(64, (items + 4 * kRowThreads - 1) / (4 * kRowThreads));
-  return launch_status(launch_dependent(commit4_kernel, dim3(static_cast<unsigned>(groups), B), kRowThreads,
+  return launch_status(launch_dependent(c->head_dim == 128 ? commit4_kernel<128> : commit4_kernel<64>, dim3(static_cast<unsigned>(groups), B), kRowThreads,
                                         sizeof(int64_t) * 2 * Nmax, stream, SV_KERNEL_CACHE_ROWS, 1, a),
                        "commit");
 }

@@ -8,7 +8,7 @@
 
 The drafter is the target's first layer.  With temperature 0 the text is the target's own greedy text.
 
-    python examples/tree_round.py [--requests 8] [--new-tokens 64] [--temperature 0.8]
+    python examples/tree_round.py [--requests 8] [--new-tokens 64] [--temperature 0.8] [--cache-bits 4]
 """
 from __future__ import annotations
 
@@ -44,9 +44,10 @@ class Model:
         m.__dict__.update(self.__dict__, layers=self.layers[:1])
         return m
 
-    def cache(self, requests, longest, page_size=16):
+    def cache(self, requests, longest, page_size=16, bits=16):
         entries = -(-longest // page_size)
-        return sv.PagedCache.empty(len(self.layers), requests * entries, page_size, self.kv_heads, self.head_dim, requests, entries)
+        kind = sv.PagedCache4 if bits == 4 else sv.PagedCache
+        return kind.empty(len(self.layers), requests * entries, page_size, self.kv_heads, self.head_dim, requests, entries)
 
     def _rotate(self, x, position):
         half = self.head_dim // 2
@@ -70,8 +71,8 @@ class Model:
 class Side:
     """A model with its cache and workspaces: the drafter's or the target's side of a round."""
 
-    def __init__(self, model, requests, longest):
-        self.model, self.cache = model, model.cache(requests, longest)
+    def __init__(self, model, requests, longest, bits=16):
+        self.model, self.cache = model, model.cache(requests, longest, bits=bits)
         self.ws = sv.attention_workspace(self.cache, model.q_heads)
 
     def run(self, tokens, depth, seq_len, offsets, parent, nmax):
@@ -98,13 +99,14 @@ def tree_of(branching):
     return parent, depth, levels
 
 
-def generate(model, prompts, new_tokens, temperature, *, top_k=0, top_p=1.0, branching=BRANCHING, seed=0):
-    """Continues the prompts (lists of token ids) by at least new_tokens tokens each.  Returns (texts, rounds)."""
+def generate(model, prompts, new_tokens, temperature, *, top_k=0, top_p=1.0, branching=BRANCHING, seed=0, bits=16):
+    """Continues the prompts (lists of token ids) by at least new_tokens tokens each, with caches held in 16 or 4
+    bits.  Returns (texts, rounds)."""
     B = len(prompts)
     parents, depths, levels = tree_of(branching)
     N = len(parents)
     longest = max(map(len, prompts)) + new_tokens + 2 * N
-    target, drafter = Side(model, B, longest), Side(model.first_layer(), B, longest)
+    target, drafter = Side(model, B, longest, bits), Side(model.first_layer(), B, longest, bits)
     gpu = lambda x, dtype=I32: torch.tensor(x, dtype=dtype, device="cuda")  # noqa: E731
     # the prompts but their last tokens: chains over empty sequences
     seq_len, counts = gpu([0] * B), [len(p) - 1 for p in prompts]
@@ -167,14 +169,15 @@ def main():
     a.add_argument("--requests", type=int, default=8)
     a.add_argument("--new-tokens", type=int, default=64)
     a.add_argument("--temperature", type=float, default=0.8)
+    a.add_argument("--cache-bits", type=int, choices=(16, 4), default=16)
     a = a.parse_args()
     model = Model()
     g = torch.Generator().manual_seed(1)
     prompts = [torch.randint(model.vocab, (int(n),), generator=g).tolist() for n in torch.randint(1, 40, (a.requests,), generator=g)]
-    generate(model, prompts, 4, a.temperature)  # warm-up
+    generate(model, prompts, 4, a.temperature, bits=a.cache_bits)  # warm-up
     torch.cuda.synchronize()
     began = time.time()
-    texts, rounds = generate(model, prompts, a.new_tokens, a.temperature, top_k=50, top_p=0.95)
+    texts, rounds = generate(model, prompts, a.new_tokens, a.temperature, top_k=50, top_p=0.95, bits=a.cache_bits)
     new = sum(len(t) - len(p) for t, p in zip(texts, prompts))
     print(f"{a.requests} requests, {new} tokens in {rounds} rounds: {new / rounds / a.requests:.2f} tokens a request and round, "
           f"{(time.time() - began) / rounds * 1e3:.2f} ms a round")

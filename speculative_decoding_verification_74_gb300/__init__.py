@@ -1013,14 +1013,14 @@ def beam_select(logits, scores, candidates, *, finished=None, pad=0, out=None, w
     if finished is not None and finished.shape != scores.shape:
         raise ValueError("finished must have the shape of scores")
     f32, i32 = torch.float32, torch.int32
-    dt = _dt(logits)
+    dt, row_stride = _dt(logits), _row_stride(logits)
     if out is None:
         out = (_empty((B, K), f32, dev, stream), _empty((B, K), i32, dev, stream), _empty((B, K), i32, dev, stream))
     if ws is None:
         ws = _workspace(sv_beam_workspace_size(B * W, V, K), dev, stream)
     n = B * K
     _check((_lib or lib()).sv_beam_select(
-        _p(logits), _row_stride(logits), dt, B, W, V, _array(scores, "scores", f32, B * W),
+        _p(logits), row_stride, dt, B, W, V, _array(scores, "scores", f32, B * W),
         _array(finished, "finished", i32, B * W), pad, K, _array(out[0], "scores", f32, n), _array(out[1], "rows", i32, n),
         _array(out[2], "tokens", i32, n), _p(ws), _ws_bytes(ws), _stream(stream)))
     return out

@@ -523,8 +523,9 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
         if (more) {
           if (s_left == 0 && ready(&sm.q_full[s_seg & 1], (s_seg >> 1) & 1))
             s_left = __shfl_sync(0xFFFFFFFFu, sm.seg[s_seg & 1].kv1 - sm.seg[s_seg & 1].kv0, 0);
-          // the group's S was last read by the softmax, or by the product P V, of tile n - 2
-          if (s_left > 0 && ready(&sm.full[ks.stage], ks.parity) &&
+          // The group's S was last read by the softmax, or by the product P V, of tile n - 2.  Parities tell a stage's fills apart
+          // only while the one before has been seen: with an odd number of stages that is a tile's V, whose product comes first.
+          if (s_left > 0 && 2 * i + stages > 2 * n && ready(&sm.full[ks.stage], ks.parity) &&
               (n < 2 || ready(Col::kOwnP ? &sm.p_full[n & 1] : &sm.pv_done[n & 1], ((n - 2) >> 1) & 1))) {
             tc_after_sync();
             const uint64_t k_desc = k_desc0 + ks.stage * (kStageBytes >> 4);

@@ -1005,7 +1005,7 @@ def beam_select(logits, scores, candidates, *, finished=None, pad=0, out=None, w
     `pad`.  Returns (scores [requests, candidates] float32, rows [requests, candidates] int32: the row of logits that a
     candidate goes on from, tokens [requests, candidates] int32), best first; places without a candidate hold -inf, -1, -1.
     With candidates = beams, rows.flatten() is what PagedCache.reorder takes.  out = (scores, rows, tokens) takes the place of
-    new tensors."""
+    new tensors; with candidates = beams its scores may be `scores` itself."""
     if logits.dim() != 2 or scores.dim() != 2 or scores.numel() != logits.shape[0]:
         raise ValueError("beam_select() takes logits [requests * beams, V] and scores [requests, beams]")
     B, W = scores.shape

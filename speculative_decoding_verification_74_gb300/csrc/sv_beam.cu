@@ -539,6 +539,7 @@ constexpr int kRanked = 512;      // candidates that are ranked by counting: one
 constexpr int kFew = 128;         // or with a quarter of the others to a thread
 struct MergeShared {
   double A[SV_MAX_BEAMS];         // what is added to a beam's x - m
+  float score[SV_MAX_BEAMS];      // (out_scores may lie over the scores)
   float m[SV_MAX_BEAMS], high[SV_MAX_BEAMS], low[SV_MAX_BEAMS];  // and A as a pair of floats
   uint8_t exact[SV_MAX_BEAMS];    // A is not to be summed again
   uint8_t live[SV_MAX_BEAMS];     // the beam's logits count
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (lane == 0) {
+      sh.score[w] = score;
       // log of the sum: its exponent's share exact, the fraction's to float32
       const int e = (__float_as_int(sum) >> 23) - 127;
       const float fraction = __int_as_float((__float_as_int(sum) & 0x7FFFFF) | 0x3F800000);
@@ -811,7 +813,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
       if (lane == 0) atomicAdd(&sh.sum, static_cast<unsigned long long>(sum));
       __syncthreads();
       if (tid == 0) {
-        sh.A[w] = static_cast<double>(a.scores[row0 + w]) - log(static_cast<double>(sh.sum) * 0x1p-44);
+        sh.A[w] = static_cast<double>(sh.score[w]) - log(static_cast<double>(sh.sum) * 0x1p-44);
         sh.exact[w] = 1;
       }
       __syncthreads();

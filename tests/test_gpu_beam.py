@@ -72,6 +72,20 @@ def test_runs_of_equals(dtype, K):
     check(x.to(dtype), torch.linspace(-3, -1, 8)[None, :].contiguous(), K)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_scores_in_place(dtype):
+    """The new scores over the old ones, also where equal totals of two beams have their rows summed again."""
+    x, scores = made(3, 4, 5000, dtype, 5)
+    x[1], x[6] = x[0], x[5]
+    scores[0, 1], scores[1, 2] = scores[0, 0], scores[1, 1]
+    want = sv.beam_select(x.cuda(), scores.cuda(), 4)
+    place, ints = scores.cuda(), torch.empty((2, 3, 4), dtype=torch.int32, device="cuda")
+    got = sv.beam_select(x.cuda(), place, 4, out=(place, ints[0], ints[1]))
+    assert got[0] is place
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_equal_beams():
     """Beams with the same logits and scores: every total occurs twice or more, the lower beam first."""
     x, scores = made(2, 4, 5000, torch.float32, 1)

@@ -248,6 +248,8 @@ constexpr int32_t kShares = -2;   // it shares the full pages, there is nothing 
 constexpr int32_t kEmpties = -3;  // it names no source
 constexpr int32_t kFailed = -4;   // in marks[0 .. rows): nothing changes
 
+constexpr size_t kPlanSmem = 200 << 10;  // shared memory that a plan may take
+
 // What becomes of every row, and the pages: one CTA.  Shared memory: five ints per row, and with kWhole the table, which is then
 // rewritten here too (without it by gather_kernel).
 template <bool kWhole>
@@ -685,13 +687,14 @@ cudaError_t release_pages(const Pool& p, int32_t* table, int width, int rows, in
 }
 cudaError_t reorder_pages(const Pool& p, int32_t* table, int width, int rows, int32_t* seq_len, const int32_t* src,
                           int32_t* out_ok, void* ws, void* stream) {
-  const size_t per_row = sizeof(int32_t) * 5 * rows;
-  // a table of up to 16384 entries is rewritten by the CTA that plans (16 requests of four beams 22 us with it, 25 without)
-  const bool whole = static_cast<int64_t>(rows) * width <= 16384;
-  cudaError_t e = whole ? allow_smem<plan_kernel<true>>(sizeof(int32_t) * (5 * SV_MAX_BATCH + 16384)) : allow_smem<plan_kernel<false>>(sizeof(int32_t) * 5 * SV_MAX_BATCH);
+  // a table that fits into shared memory is rewritten by the CTA that plans (256 rows of up to 58 pages 27 us
+  // with it, 46 without; up to 127 pages 39 and 56; four of 9 8.2 and 10.2)
+  const size_t per_row = sizeof(int32_t) * 5 * rows, table_bytes = sizeof(int32_t) * rows * static_cast<size_t>(width);
+  const bool whole = per_row + table_bytes <= kPlanSmem;
+  cudaError_t e = whole ? allow_smem<plan_kernel<true>>(kPlanSmem) : allow_smem<plan_kernel<false>>(sizeof(int32_t) * 5 * SV_MAX_BATCH);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(whole ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPageThreads,
-                       per_row + (whole ? sizeof(int32_t) * rows * width : 0), stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows,
+  e = launch_dependent(whole ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPageThreads, per_row + (whole ? table_bytes : 0),
+                       stream, SV_KERNEL_CACHE_PAGES, 1, p, table, width, rows,
                        seq_len, src, out_ok, marks_of(ws), status_of(ws));
   if (e != cudaSuccess || whole) return e;
   // a CTA holds its columns of every row in at most 32 KB (64 KB for 4096 rows)

@@ -164,3 +164,14 @@ def test_wide_tables():
     assert int(cache.reorder(d_len, i32([0, 1, 2, 1]))) == oracle.reorder(lens, [0, 1, 2, 1]) == 0
     same(cache, oracle, d_len, lens)
     assert sv.sv_query_status(cache.ws)[1] == sv.SV_DEV_OUT_OF_PAGES
+
+
+def test_wider_tables():
+    """The same past what one CTA's shared memory holds."""
+    cache, oracle, d_len, lens = make([30, 30, 40], [0] * 3, 14, width=20000)   # 4 + 4 + 5 pages: one is free
+    assert int(cache.reorder(d_len, i32([0, 0, 0]))) == oracle.reorder(lens, [0, 0, 0]) == 1
+    same(cache, oracle, d_len, lens)
+    cache, oracle, d_len, lens = make([30, 30, 32, 0], [0] * 4, 12, width=20000)
+    assert int(cache.reorder(d_len, i32([0, 1, 2, 1]))) == oracle.reorder(lens, [0, 1, 2, 1]) == 0
+    same(cache, oracle, d_len, lens)
+    assert sv.sv_query_status(cache.ws)[1] == sv.SV_DEV_OUT_OF_PAGES

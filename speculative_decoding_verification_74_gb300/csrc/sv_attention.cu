@@ -36,6 +36,13 @@
 // Q; two groups of four warps take the tiles in turn (a thread has a row), each with its own S and O, so one group's
 // exponentials run beside the other's products.  P is rounded to bf16, the products' type; o is divided by the sum of
 // the rounded P, so its weights add up to 1, and lse takes the sum before rounding.
+//
+// A cache in 4 bits (kFour) with more rows than sv_attention4.cu's tiles: one warp copies a tile's codes into a ring of their
+// own, and four more warps turn them into the stages' K and V, as float16 (exact: a code times its scale has six bits), and Q
+// into float16 rows scaled by powers of two.  The rest is the same, with P in float16.  Whole warpgroups share out the registers.
+// Measured (as above, bytes in 4 bits in brackets): 64 trees 114 us (28), four chains 260 us (78; their products padded to 128
+// rows 126).  A tile takes 1.3 to 1.4 us however few its bytes: S, softmax and P V follow each other through barriers, on four
+// stages of 32 KB; decoding waits for them.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -87,7 +94,7 @@ constexpr int kMixFloat4Of4 = 512;         // in 4 bits: at most two copies
 // A cache in 4 bits: one warp copies a tile's codes into a ring of their own, and four decode them, each a quarter of its slots,
 // sixteen at a time.
 constexpr int kRawSlots = 16;
-constexpr int kMaxRaw = 2;                 // (with 3, and a stage less: four chains over 131k 330 us against 283)
+constexpr int kMaxRaw = 2;                 // (beside four stages four chains over 131k take 260 us; with 1 323, with 2 and three stages 313, 3 and three 330)
 constexpr int kMaxStages = 12;
 struct AttendParams : Line, Marks, Outputs {
   const int32_t *table, *parent;
@@ -445,21 +452,21 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
           ++loaded;
           at.step(places);
         } else {
-        const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, wanted)) * kHalves * box * 128;
-        if (loaded >= stages) go = warp_wait<kFour>(&sm.empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
-        if (!go) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.stage], bytes);
-        __syncwarp();
-        if (wanted) {
+          const int bytes = __popc(__ballot_sync(0xFFFFFFFFu, wanted)) * kHalves * box * 128;
+          if (loaded >= stages) go = warp_wait<kFour>(&sm.empty[at.stage], at.parity ^ 1, &sm.dead, a.status);
+          if (!go) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.stage], bytes);
+          __syncwarp();
+          if (wanted) {
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-            tma_load_4d(ring + at.stage * kStageBytes + h * kHalfBytes + (lane << box_shift) * 128, map, kPair ? 0 : h * 64,
-                        kPair ? 2 * s.head + h : s.head,
-                        slot & ((1 << a.shift) - 1), page, &sm.full[at.stage]);
-        }
-        loaded += 2;
-        at.step(stages);
-        at.step(stages);
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_4d(ring + at.stage * kStageBytes + h * kHalfBytes + (lane << box_shift) * 128, map, kPair ? 0 : h * 64,
+                          kPair ? 2 * s.head + h : s.head,
+                          slot & ((1 << a.shift) - 1), page, &sm.full[at.stage]);
+          }
+          loaded += 2;
+          at.step(stages);
+          at.step(stages);
         }
         if (j == max(s.kv0, s.kv1 - 2) && stretch_at(after)) {
           next = segment_at<kTile, kFour>(sm.line, before, after, t1);

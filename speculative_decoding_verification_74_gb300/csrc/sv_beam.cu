@@ -15,6 +15,10 @@
 // (each term by 2^-22 of ex2 and a few 2^-24 |y|, y its exponent, of E|y| <= log2 V; compensated sums add next to nothing).  So
 // where neighbours of different beams in the order lie within kNear of each other, their rows are summed again with terms in
 // pairs of floats (about 2^-30), and the ranking is repeated: with this the order is that of the exact totals, down to 2^-29.
+//
+// Measured (GB300, graph replay; a copy of the logits in brackets): 1024 rows of 151936, K = 8 float32 93 us (92), K = 32 bf16 61
+// us (46), where the stream's instructions count: half the bytes for as many exponentials and maxima; 64 rows float32 19 us (6),
+// four rows of 32000 bf16 14 us: the latency of a part, 10 us, and of the merge, 7.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

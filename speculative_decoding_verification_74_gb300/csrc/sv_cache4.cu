@@ -3,6 +3,10 @@
 //
 // A head's page lies in groups of eight slots, 9 D bytes each: key codes, key scales, value codes, value scales, in the order
 // in which a warp of the attention reads them (see sv.h).  So 32 slots of one head are one contiguous copy of 36 D bytes.
+//
+// Measured (GB300, graph replay; a copy of the bytes in brackets): a turn of 64 trees of up to 16 nodes in 32 layers (8 heads of
+// 128) 59 us (26): append 40, which quantising's 200 instructions for sixteen elements and the lookup of each row's place bound,
+// commit 10, reserve 4; 64 rows reordered in 32 layers 16 us (4): the plan 8, the copies 6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

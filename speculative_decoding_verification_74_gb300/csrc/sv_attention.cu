@@ -66,11 +66,13 @@ constexpr int kSoftThreads = 2 * kGroupThreads;
 // Warps: the two groups of the softmax are four consecutive ones each.
 template <bool kFour>
 struct Warps {  // a cache in bf16
-  static constexpr int kThreads = 128 + kSoftThreads, kSoft = 2, kK = 0, kMma = 1, kQ = 10, kV = 11, kDecode = 99;
+  static constexpr int kThreads = 128 + kSoftThreads, kSoft = 2, kK = 0, kMma = 1, kQ = 10, kV = 11, kDecode = 99, kPv = 99;
+  static constexpr int kSegments = 2;      // descriptions held at once
 };
 template <>
 struct Warps<true> {  // in 4 bits: whole warpgroups, which share out the registers
-  static constexpr int kThreads = 256 + kSoftThreads, kSoft = 4, kK = 2, kMma = 0, kQ = 1, kV = 99, kDecode = 12;
+  static constexpr int kThreads = 256 + kSoftThreads, kSoft = 4, kK = 2, kMma = 0, kQ = 1, kV = 99, kDecode = 12, kPv = 3;
+  static constexpr int kSegments = 4;
 };
 constexpr int kHalfBytes = kTile * 128;    // 128 slots of 64 bf16: one swizzled column block
 constexpr int kTmemColumns = 512;
@@ -92,8 +94,8 @@ constexpr int kExtra = 3;
 constexpr int kMixFloat4 = 768;            // (a fifth stage still fits)
 constexpr int kMixFloat4Of4 = 512;         // in 4 bits: at most two copies
 // A cache in 4 bits: one warp copies a tile's codes into a ring of their own, and four decode them, each a quarter of its slots,
-// sixteen at a time.
-constexpr int kRawSlots = 16;
+// eight at a time.  (Sixteen: 64 trees 123 us against 113; the roles' code together has to fit into the instruction cache.)
+constexpr int kRawSlots = 8;
 constexpr int kMaxRaw = 2;                 // (beside four stages four chains over 131k take 260 us; with 1 323, with 2 and three stages 313, 3 and three 330)
 constexpr int kMaxStages = 12;
 struct AttendParams : Line, Marks, Outputs {
@@ -253,19 +255,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // row / group for row < 128, group <= 128: over = ceil(2^16 / group).
 __device__ __forceinline__ int over_group(int row, uint32_t over) { return static_cast<int>((row * over) >> 16); }
 
-// The part of shared memory with a fixed size; then come the tiles before each request [B], the parents of two segments'
-// trees [2][Nmax] and, 1024-byte aligned, Q and the ring.
+// The part of shared memory with a fixed size; then come the tiles before each request [B], the parents of some segments'
+// trees [kSegments][Nmax] and, 1024-byte aligned, Q and the ring.
 static_assert(kMaxRaw == 2 && kMaxStages <= 32, "the barriers' threads");
 template <bool kFour>
 struct Smem {
   Line line;
-  Segment seg[2];              // by the segment's parity
+  Segment seg[Warps<kFour>::kSegments];             // segments' descriptions in turn
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t raw_full[kFour ? kMaxRaw : 1], raw_empty[kFour ? kMaxRaw : 1];  // a tile's codes are there, are decoded
   uint64_t q_raw[2];           // in 4 bits, by the segment's parity: its Q is there in bf16
   uint64_t q_full[2];          // by the segment's parity: its Q and description are there
   uint64_t q_free;             // once per segment: its last S is complete
-  uint64_t seg_free[2];        // every softmax thread is done with a description
+  uint64_t seg_there[kFour ? Warps<kFour>::kSegments : 1];  // in 4 bits: a description is there
+  uint64_t seg_free[Warps<kFour>::kSegments];  // every softmax thread is done with a description
   uint64_t s_full[2], p_full[2], pv_done[2];  // by group
   uint64_t sums_full, o_free;  // once per segment: the groups' sums are there; every thread has read O
   uint64_t mix_full[2], mix_free[2];  // by group: copies' columns written, read
@@ -302,8 +305,8 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
   extern __shared__ unsigned char dyn[];
   __shared__ Smem<kFour> sm;
   uint32_t* before = reinterpret_cast<uint32_t*>(dyn);           // [B]
-  int32_t* parents = reinterpret_cast<int32_t*>(dyn) + a.B;      // [2][Nmax]
-  unsigned char* q_buf = dyn + 4 * (a.B + 2 * a.Nmax);
+  int32_t* parents = reinterpret_cast<int32_t*>(dyn) + a.B;      // [segments' descriptions][Nmax]
+  unsigned char* q_buf = dyn + 4 * (a.B + Role::kSegments * a.Nmax);
   q_buf += (1024u - (smem_u32(q_buf) & 1023u)) & 1023u;
   unsigned char* ring = q_buf + kHalves * kHalfBytes;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -316,7 +319,6 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
     const int i = tid - 32;
     mbar_init(&sm.q_raw[i], 1);
     mbar_init(&sm.q_full[i], kFour ? 128 : 1);
-    mbar_init(&sm.seg_free[i], kSoftThreads);
     mbar_init(&sm.mix_full[i], kGroupThreads);
     mbar_init(&sm.mix_free[i], kGroupThreads);
   } else if (tid >= 64 && tid < 66) {
@@ -332,6 +334,9 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
     mbar_init(&sm.q_free, 1);
     mbar_init(&sm.sums_full, kSoftThreads);
     mbar_init(&sm.o_free, kSoftThreads);
+  } else if (tid >= 97 && tid < 97 + Role::kSegments) {
+    mbar_init(&sm.seg_free[tid - 97], kSoftThreads);
+    if constexpr (kFour) mbar_init(&sm.seg_there[tid - 97], 1);
   }
   if (tid < 128) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -391,6 +396,19 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
   const uint32_t stages = a.stages;
   uint32_t loaded = 0, segments = 0;  // stages and Q's that were asked for
 
+  // In 4 bits only one warp finds the segments, and the others read its descriptions (code that is in line for every role does
+  // not fit into the instruction cache).  k: the segment's number in this CTA.
+  constexpr int kSegMask = Role::kSegments - 1;
+  [[maybe_unused]] auto described = [&](uint32_t k, Segment* s) {
+    if (k == 0) {
+      *s = opening;
+      return true;
+    }
+    if (!warp_wait<kFour>(&sm.seg_there[k & kSegMask], (k / Role::kSegments) & 1, &sm.dead, a.status)) return false;
+    *s = sm.seg[k & kSegMask];
+    return true;
+  };
+
   [[maybe_unused]] auto copies = [&]() {
     // ---- copies -----------------------------------------------------------------------------------
     const int box_shift = min(7, a.shift), box = 1 << box_shift;  // slots per copy: a page, or 128 slots of one
@@ -409,6 +427,7 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
     };
     Segment s = {}, next = {};  // the next segment and its first pages are looked up while the ring is full
     int block = 0, page_now = -1, page_next = -1, next_block = 0, next_now = -1;
+    [[maybe_unused]] uint32_t segment = 0;
     if (some) {
       s = opening;
       block = tile_slot<kTile>(s.r, s.kv0) >> (box_shift + 5);
@@ -469,7 +488,11 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
           at.step(stages);
         }
         if (j == max(s.kv0, s.kv1 - 2) && stretch_at(after)) {
-          next = segment_at<kTile, kFour>(sm.line, before, after, t1);
+          if constexpr (kFour) {
+            if (go = described(++segment, &next); !go) break;
+          } else {
+            next = segment_at<kTile>(sm.line, before, after, t1);
+          }
           next_block = tile_slot<kTile>(next.r, next.kv0) >> (box_shift + 5);
           next_now = pages_of(next, next_block);
         }
@@ -483,17 +506,38 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
   auto queries = [&]() {
     // ---- segments: description, parents, Q --------------------------------------------------------
     constexpr int rows_apart = kTile / kCopies;
-    for (uint32_t t = t0; stretch_at(t); ++segments) {
-      const Segment s = t == t0 ? opening : segment_at<kTile, kFour>(sm.line, before, t, t1);
-      const int b = segments & 1;
-      if (segments >= 2 && !warp_wait<kFour>(&sm.seg_free[b], ((segments >> 1) - 1) & 1, &sm.dead, a.status)) break;
+    // the k-th segment's description, once the softmax is done with the one that lay there
+    auto describe = [&](uint32_t k, const Segment& s) {
+      const uint32_t slot = k & kSegMask;
+      if (k >= Role::kSegments && !warp_wait<kFour>(&sm.seg_free[slot], (k / Role::kSegments - 1) & 1, &sm.dead, a.status)) return false;
       if (a.parent != nullptr)
-        for (int x = lane; x < s.r.nodes; x += 32) parents[b * a.Nmax + x] = a.parent[s.r.first + x];
-      if (lane == 0) sm.seg[b] = s;
+        for (int x = lane; x < s.r.nodes; x += 32) parents[slot * a.Nmax + x] = a.parent[s.r.first + x];
+      if (lane == 0) sm.seg[slot] = s;
+      return true;
+    };
+    [[maybe_unused]] uint32_t told = 0, tell_t = t0;
+    for (uint32_t t = t0; stretch_at(t); ++segments) {
+      Segment s;
+      if constexpr (kFour) {  // descriptions run one ahead of Q, but for the first
+        bool go = true;
+        while (go && told < segments + (segments > 0 ? 2 : 1) && stretch_at(tell_t)) {
+          const Segment one = told == 0 ? opening : segment_at<kTile, kFour>(sm.line, before, tell_t, t1);
+          go = describe(told, one);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.seg_there[told & kSegMask]);
+          ++told;
+          tell_t = one.next;
+        }
+        if (!go) break;
+        s = sm.seg[segments & kSegMask];
+      } else {
+        s = t == t0 ? opening : segment_at<kTile>(sm.line, before, t, t1);
+        if (!describe(segments, s)) break;
+      }
       if (segments >= 1 && !warp_wait<kFour>(&sm.q_free, (segments - 1) & 1, &sm.dead, a.status)) break;
       __syncwarp();
       if (lane == 0) {
-        uint64_t* there = kFour ? &sm.q_raw[b] : &sm.q_full[b];
+        uint64_t* there = kFour ? &sm.q_raw[segments & 1] : &sm.q_full[segments & 1];
         mbar_arrive_expect_tx(there, kCopies * kHalves * a.tile_nodes * a.group * 128);
         for (int copy = 0; copy < kCopies; ++copy)
 #pragma unroll
@@ -505,18 +549,46 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
       t = s.next;
     }
   };
-  auto products = [&]() {
-    // ---- products ---------------------------------------------------------------------------------
-    // The whole warp runs the loop, so counters and descriptors stay in uniform registers, which tcgen05.mma takes its
-    // operands from; one elected thread issues.
+  // ---- products -----------------------------------------------------------------------------------
+  // The whole warp runs these loops, so counters and descriptors stay in uniform registers, which tcgen05.mma takes its
+  // operands from; one elected thread issues.  Descriptors go by addition: their low words count 16-byte units of shared memory.
+  constexpr uint32_t kDescS = instr_desc(kTile, false, kFour), kDescO = instr_desc(W, true, kFour);
+  const uint64_t q_desc0 = smem_desc(smem_u32(q_buf), 16, 1024), k_desc0 = smem_desc(smem_u32(ring), 16, 1024),
+                 v_desc0 = smem_desc(smem_u32(ring), kHalfBytes, 1024);
+  // S of tile n from a stage of K; the segment's last one frees Q
+  auto issue_s = [&](bool elected, uint32_t n, uint32_t stage, bool last) {
+    tc_after_sync();
+    const uint64_t k_desc = k_desc0 + stage * (kStageBytes >> 4);
+    const uint32_t d = tmem + Col::s(n & 1);
+    if (elected) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(d, q_desc0 + h * (kHalfBytes >> 4) + 2 * k, k_desc + h * (kHalfBytes >> 4) + 2 * k, kDescS, h + k > 0);
+      tc_commit(&sm.s_full[n & 1]);
+      tc_commit(&sm.empty[stage]);
+      if (last) tc_commit(&sm.q_free);
+    }
+  };
+  // P V of tile i, the segment's j-th, from a stage of V
+  auto issue_pv = [&](bool elected, uint32_t i, uint32_t stage, int j) {
+    tc_after_sync();
+    const uint64_t v_desc = v_desc0 + stage * (kStageBytes >> 4);
+    const uint32_t d = tmem + Col::o(i & 1), p = tmem + Col::p(i & 1);
+    const uint32_t more = j > 1;
+    if (elected) {
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k) mma_ts(d, p + 8 * k, v_desc + k * (2048 >> 4), kDescO, k > 0 ? 1u : more);
+      tc_commit(&sm.pv_done[i & 1]);
+      tc_commit(&sm.empty[stage]);
+    }
+  };
+  auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
+  [[maybe_unused]] auto products = [&]() {
     if (some) {
       const bool elected = elect_one();
-      auto ready = [](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)); };
-      constexpr uint32_t kDescS = instr_desc(kTile, false, kFour), kDescO = instr_desc(W, true, kFour);
       bool more = true;                   // S's are left
-      // descriptors by addition: their low words count 16-byte units of shared memory
-      const uint64_t q_desc0 = smem_desc(smem_u32(q_buf), 16, 1024), k_desc0 = smem_desc(smem_u32(ring), 16, 1024),
-                     v_desc0 = smem_desc(smem_u32(ring), kHalfBytes, 1024);
       Ring ks, vs;  // K's and V's stages alternate
       vs.step(stages);
       uint32_t s_seg = 0, p_seg = 0;      // segments of the next S and the next P V
@@ -534,20 +606,8 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
           // only while the one before has been seen: with an odd number of stages that is a tile's V, whose product comes first.
           if (s_left > 0 && 2 * i + stages > 2 * n && ready(&sm.full[ks.stage], ks.parity) &&
               (n < 2 || ready(Col::kOwnP ? &sm.p_full[n & 1] : &sm.pv_done[n & 1], ((n - 2) >> 1) & 1))) {
-            tc_after_sync();
-            const uint64_t k_desc = k_desc0 + ks.stage * (kStageBytes >> 4);
-            const uint32_t d = tmem + Col::s(n & 1);
             --s_left;
-            if (elected) {
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ss(d, q_desc0 + h * (kHalfBytes >> 4) + 2 * k, k_desc + h * (kHalfBytes >> 4) + 2 * k, kDescS, h + k > 0);
-              tc_commit(&sm.s_full[n & 1]);
-              tc_commit(&sm.empty[ks.stage]);
-              if (s_left == 0) tc_commit(&sm.q_free);
-            }
+            issue_s(elected, n, ks.stage, s_left == 0);
             ks.step(stages);
             ks.step(stages);
             if (s_left == 0) more = stretch_at(__shfl_sync(0xFFFFFFFFu, sm.seg[s_seg & 1].next, 0));
@@ -565,16 +625,7 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
           // (at a segment's first tile both groups' O of the segment before have been read)
           if (ready(&sm.p_full[i & 1], (i >> 1) & 1) && ready(&sm.full[vs.stage], vs.parity) &&
               (p_j > 0 || p_seg < 2 || ready(&sm.o_free, (p_seg - 2) & 1))) {
-            tc_after_sync();
-            const uint64_t v_desc = v_desc0 + vs.stage * (kStageBytes >> 4);
-            const uint32_t d = tmem + Col::o(i & 1), p = tmem + Col::p(i & 1);
-            const uint32_t more = p_j > 1;
-            if (elected) {
-#pragma unroll
-              for (int k = 0; k < kTile / 16; ++k) mma_ts(d, p + 8 * k, v_desc + k * (2048 >> 4), kDescO, k > 0 ? 1u : more);
-              tc_commit(&sm.pv_done[i & 1]);
-              tc_commit(&sm.empty[vs.stage]);
-            }
+            issue_pv(elected, i, vs.stage, p_j);
             vs.step(stages);
             vs.step(stages);
             ++p_j;
@@ -585,6 +636,44 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
         idle = issued ? 0 : idle + 1;
         if ((idle & 1023u) == 1023u && !__all_sync(0xFFFFFFFFu, still_waiting<kFour>(&began, &sm.dead, a.status))) break;
         if (issued) began = 0;
+      }
+    }
+    __syncwarp();
+  };
+  // In 4 bits two warps issue, one S and one P V, each behind its own barriers (four chains 260 us by one warp, 250 by two).  With
+  // an odd ring S waits for the product of two tiles before even where S itself could go: its stage may have held that tile's V.
+  [[maybe_unused]] auto half_of_products = [&](auto of_values) {
+    constexpr bool kPv = decltype(of_values)::value;
+    if (some) {
+      const bool elected = elect_one();
+      // (by polling: a sleeping warp wakes late)
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        uint64_t began = 0;
+        bool there = true;
+        for (uint32_t it = 1; there && !mbar_test_wait(bar, parity); ++it)
+          if ((it & 1023u) == 0) there = still_waiting<kFour>(&began, &sm.dead, a.status);
+        return __all_sync(0xFFFFFFFFu, there) != 0;
+      };
+      Ring at;
+      if (kPv) at.step(stages);
+      uint32_t n = 0, seg = 0;
+      bool go = true;
+      for (uint32_t t = t0; go && stretch_at(t); ++seg) {
+        if (go = wait(&sm.q_full[seg & 1], (seg >> 1) & 1); !go) break;
+        const Segment& s = sm.seg[seg & kSegMask];
+        const int tiles = __shfl_sync(0xFFFFFFFFu, s.kv1 - s.kv0, 0);
+        t = __shfl_sync(0xFFFFFFFFu, s.next, 0);
+        for (int j = 0; j < tiles && go; ++j, ++n) {
+          if constexpr (kPv) {  // (at a segment's first tile both groups' O of the segment before have been read)
+            go = (j > 0 || seg == 0 || wait(&sm.o_free, (seg - 1) & 1)) && wait(&sm.p_full[n & 1], (n >> 1) & 1) && wait(&sm.full[at.stage], at.parity);
+            if (go) issue_pv(elected, n, at.stage, j);
+          } else {
+            go = (n < 2 || wait(Col::kOwnP && (stages & 1) == 0 ? &sm.p_full[n & 1] : &sm.pv_done[n & 1], ((n - 2) >> 1) & 1)) && wait(&sm.full[at.stage], at.parity);
+            if (go) issue_s(elected, n, at.stage, j + 1 == tiles);
+          }
+          at.step(stages);
+          at.step(stages);
+        }
       }
     }
     __syncwarp();
@@ -639,7 +728,8 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
         mbar_arrive(&sm.q_full[b]);
       };
       for (uint32_t t = t0; stretch_at(t) && go;) {
-        const Segment s = t == t0 ? opening : segment_at<kTile, kFour>(sm.line, before, t, t1);
+        Segment s;
+        if (go = described(seg, &s); !go) break;
         const int end = s.r.len + s.r.nodes, lo = a.window > 0 ? max(0, s.r.len - a.window + 1) : 0;
         for (int j = s.kv0; j < s.kv1 && go; ++j) {
           const int s0 = tile_slot<kTile>(s.r, j) + chunk0;
@@ -672,14 +762,14 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
             };
             fetch(0);
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 32 / kRawSlots; ++c) {
 #pragma unroll
               for (int x = 0; x < kAll; ++x) {
                 two[x] = next_two[x];
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) w[x][i] = next_w[x][i];
               }
-              if (c == 0) fetch(1);
+              if (c + 1 < 32 / kRawSlots) fetch(c + 1);
 #pragma unroll
               for (int x = 0; x < kAll; ++x) {
                 const int head = x / (kRawSlots / 8), u = x % (kRawSlots / 8);
@@ -731,8 +821,10 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
     constexpr int rows_apart = kTile / kCopies;
     const int row_in = r & (rows_apart - 1), copy = r / rows_apart;
     const int half = kPair ? row_in / kHalfRows : 0, local = row_in & (kHalfRows - 1);  // its head of the pair, its row there
-    constexpr int kWide = kCopies == 4 ? 32 : 64;           // slots whose scores are in registers at once
-    constexpr int kSteps = kTile / kCopies / kWide;          // of a copy's slots: 2 with one copy, else 1
+    // slots whose scores are in registers at once (in 4 bits with two copies 64 trees 113 us with 64, 109 with 32: less code; four
+    // chains, one copy, 250 and 264)
+    constexpr int kWide = kCopies == 4 || (kFour && kCopies == 2) ? 32 : 64;
+    constexpr int kSteps = kTile / kCopies / kWide;          // of a copy's slots
     const int slot0 = copy * (kTile / kCopies);              // first slot of a tile that this thread's copy takes
     const uint32_t my = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = my + Col::s(group), o_addr = my + Col::o(group), p_addr = my + Col::p(group);
@@ -744,8 +836,8 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
       const int b = seg & 1;
       if (!warp_wait<kFour>(&sm.q_full[b], (seg >> 1) & 1, &sm.dead, a.status)) break;
       if constexpr (kFour) c = fmaxf(a.scale * 1.44269504088896341f * sm.q_size[b][r], 1e-37f);  // (not 0: masked scores are -inf)
-      const Segment& s = sm.seg[b];
-      const int32_t* tree = parents + b * a.Nmax;
+      const Segment& s = sm.seg[seg & kSegMask];
+      const int32_t* tree = parents + (seg & kSegMask) * a.Nmax;
       auto parent_of = [&](int node) { return a.parent != nullptr ? tree[node] : node - 1; };
       const int rows = min(a.tile_nodes, s.r.nodes - s.mtile * a.tile_nodes) * a.group;
       const bool active = (((warp & 3) * 32) & (kHalfRows - 1)) < rows;  // some row of this warp exists
@@ -823,7 +915,7 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < kWide; ++i)
                 if (!((see[i >> 5] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
-              if (kSteps > 1 && k == 0) {  // masked, for the second reading
+              if (k + 1 < kSteps) {  // masked, for the second reading
 #pragma unroll
                 for (int i = 0; i < kWide; i += 32) tmem_store32(s_addr + col + i, x + i);
               }
@@ -1058,14 +1150,15 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
       tc_before_sync();
       t = s.next;
       mbar_arrive(&sm.o_free);
-      mbar_arrive(&sm.seg_free[b]);
+      mbar_arrive(&sm.seg_free[seg & kSegMask]);
       n0 += tiles;
     }
   };
   if constexpr (kFour) {
     if (warp < Role::kSoft) {  // 128 registers a thread at launch: 4 * 128 >= 72 + 2 * 168 + 104
       fewer_registers<72>();
-      if (warp == Role::kMma) products();
+      if (warp == Role::kMma) half_of_products(std::false_type());
+      else if (warp == Role::kPv) half_of_products(std::true_type());
       else if (warp == Role::kQ) queries();
       else if (warp == Role::kK) copies();
     } else if (warp < Role::kDecode) {
@@ -1208,7 +1301,7 @@ cudaError_t launch_attention(AttendParams& a, const CUtensorMap& q_map, const CU
   constexpr int kStageBytes = (kPair ? 2 : 1) * D / 64 * kHalfBytes;
   constexpr int kRawBytes = kFour ? (kPair ? 2 : 1) * kTile / 8 * 9 * D : 0;
   constexpr int kStatic = sizeof(Smem<kFour>) + 64;
-  int fixed = 4 * (a.B + 2 * a.Nmax) + 1024 + kStageBytes;
+  int fixed = 4 * (a.B + Warps<kFour>::kSegments * a.Nmax) + 1024 + kStageBytes;
   if (kFour) {
     a.raw_stages = std::min(kMaxRaw, (kSmemMax - kStatic - fixed - 3 * kStageBytes) / std::max(kRawBytes, 1));
     fixed += a.raw_stages * kRawBytes;
@@ -1216,7 +1309,7 @@ cudaError_t launch_attention(AttendParams& a, const CUtensorMap& q_map, const CU
   a.stages = std::min(kMaxStages, (kSmemMax - kStatic - fixed) / kStageBytes);
   // With an even number of stages K and V keep to their own.  Where S does not wait for the product P V of two tiles before, the V
   // warp could otherwise take an earlier emptying of a stage for its K's.  (33 trees, window 1024: 42.5 us with 4, 43.0 with 5.)
-  if (!kFour && Columns<D>::kOwnP) a.stages &= ~1;
+  if (Columns<D>::kOwnP && a.stages > 3) a.stages &= ~1;
   const size_t dyn = static_cast<size_t>(fixed) + static_cast<size_t>(a.stages) * kStageBytes;
   cudaError_t e = allow_smem<attend_kernel<D, kPair, kCopies, kFour>>(kSmemMax - kStatic);
   if (e != cudaSuccess) return e;

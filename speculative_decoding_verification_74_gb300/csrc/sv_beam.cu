@@ -16,9 +16,11 @@
 // where neighbours of different beams in the order lie within kNear of each other, their rows are summed again with terms in
 // pairs of floats (about 2^-30), and the ranking is repeated: with this the order is that of the exact totals, down to 2^-29.
 //
-// Measured (GB300, graph replay; a copy of the logits in brackets): 1024 rows of 151936, K = 8 float32 93 us (92), K = 32 bf16 61
-// us (46), where the stream's instructions count: half the bytes for as many exponentials and maxima; 64 rows float32 19 us (6),
-// four rows of 32000 bf16 14 us: the latency of a part, 10 us, and of the merge, 7.
+// Measured (GB300, graph replay; a copy of the logits in brackets): 1024 rows of 151936, K = 8, float32 125 us (92), bf16 79 (46);
+// of 64 requests of 16 beams a quarter with one beam only, K = 32, bf16 61 (35: rows of missing beams are not read); 64 rows
+// float32 19 us (6), four rows of 32000 bf16 14 us.  Of the 79, the stream takes 55, looking for candidates 13, all CTAs at about
+// the same time, and the merge 10.  Where two beams' totals lie near each other (one request of 32 candidates in 300), summing
+// their rows again takes another 80 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,7 +34,7 @@ namespace sv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowCtas = 3;                    // CTAs of the rows' kernel on an SM (1024 rows bf16 61 us; with 4 64, with 2 75)
+constexpr int kRowCtas = 3;                    // CTAs of the rows' kernel on an SM (784 rows bf16 61 us; with 4 64, with 2 75)
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;                       // 16-byte vectors of a piece per lane
 constexpr int kPiece = 32 * kVecs;             // vectors of a piece
@@ -516,28 +518,56 @@ __global__ void __launch_bounds__(kThreads, kRowCtas) rows_kernel(const BeamPara
 }
 
 // ---- merge -----------------------------------------------------------------------------------------
-// 2^((x - m) log2 e) in units of 2^-44, from pairs of floats (Dekker's and Knuth's exact sums and products): off by about
-// 2^-30 of itself and half a unit.
-__device__ __forceinline__ uint64_t exact_weight(float x, float m) {
-  const float s = x - m, b = s - x, err = (x - (s - b)) - (m + b);            // x - m = s + err
-  const float p = s * kLog2e;
-  const float e = fmaf(err, kLog2e, fmaf(s, 1.92596299e-8f, fmaf(s, kLog2e, -p)));  // (x - m) log2 e = p + e
-  if (!(p > -45.0f)) return 0;
-  const float n = rintf(p), f = p - n;
-  const float t = f * 0.693147182f;                                           // the exponent's fraction times ln 2: t + u
-  const float u = fmaf(e, 0.693147182f, fmaf(f, -1.90465421e-9f, fmaf(f, 0.693147182f, -t)));
-  const float q = t * t, q_low = fmaf(2.0f * t, u, fmaf(t, t, -q));
-  float rest = fmaf(t, 1.0f / 40320.0f, 1.0f / 5040.0f);                      // Taylor's series from t^3 / 6 on
-  rest = fmaf(t, rest, 1.0f / 720.0f);
-  rest = fmaf(t, rest, 1.0f / 120.0f);
-  rest = fmaf(t, rest, 1.0f / 24.0f);
-  rest = fmaf(t, rest, 1.0f / 6.0f) * q * t;
-  const float c = 1.0f + t, c_low = t - (c - 1.0f);
-  const float d = c + 0.5f * q, d_low = 0.5f * q - (d - c);
-  const float low = (c_low + d_low) + (fmaf(0.5f, q_low, u) + rest);
-  const float unit = __uint_as_float(static_cast<uint32_t>(127 + 44 + static_cast<int>(n)) << 23);
-  return __float2ull_rn(d * unit) + static_cast<uint64_t>(__float2ll_rn(low * unit));
-}
+__device__ __forceinline__ f32x2 f2_all(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ f32x2 f2_less(f32x2 a, f32x2 b) { return f2_fma(b, f2_all(-1.0f), a); }  // a - b
+
+// A sum of 2^((x - m) log2 e), x <= m, in units of 2^-44: each term from pairs of floats (Dekker's and Knuth's exact sums and
+// products), off by about 2^-30 of itself and half a unit, and then rounded to whole units, so that the sum does not depend on
+// its order.  Two logits at a time in packed arithmetic (two rows
+// of 151936 by one CTA 78 us; one logit at a time, converted to integers by instructions, 158).
+struct ExactSum {
+  static constexpr float kHigh = 3.0f, kLow = 1.5f * 0x1p-21f;  // a sum with these is a multiple of 2^-22, of 2^-44
+  uint32_t high = 0, low = 0;                                   // their bits added up
+  uint32_t pairs = 0;
+  __device__ __forceinline__ void add(f32x2 x, f32x2 m) {
+    constexpr float k = kLog2e, k_low = 1.92596299e-8f, ln2 = 0.693147182f, ln2_low = -1.90465421e-9f, whole = 0x1.8p23f;
+    const f32x2 s = f2_less(x, m), b = f2_less(s, x), err = f2_less(f2_less(x, f2_less(s, b)), f2_add(m, b));  // x - m = s + err
+    const f32x2 np = f2_mul(s, f2_all(-k));
+    const f32x2 e = f2_fma(err, f2_all(k), f2_fma(s, f2_all(k_low), f2_fma(s, f2_all(k), np)));  // (x - m) log2 e = e - np
+    const f32x2 nm = f2_less(f2_all(whole), np);                 // its whole part n above `whole`
+    const f32x2 f = f2_less(f2_less(f2_all(whole), nm), np);     // and the rest
+    // the exponent's fraction times ln 2: t + u
+    const f32x2 t = f2_mul(f, f2_all(ln2)), nt = f2_mul(f, f2_all(-ln2));
+    const f32x2 u = f2_fma(e, f2_all(ln2), f2_fma(f, f2_all(ln2_low), f2_fma(f, f2_all(ln2), nt)));
+    const f32x2 q = f2_mul(t, t), q_low = f2_fma(f2_add(t, t), u, f2_fma(t, t, f2_mul(t, nt)));
+    f32x2 rest = f2_fma(t, f2_all(1.0f / 40320.0f), f2_all(1.0f / 5040.0f));  // Taylor's series from t^3 / 6 on
+    rest = f2_fma(t, rest, f2_all(1.0f / 720.0f));
+    rest = f2_fma(t, rest, f2_all(1.0f / 120.0f));
+    rest = f2_fma(t, rest, f2_all(1.0f / 24.0f));
+    rest = f2_mul(f2_mul(f2_fma(t, rest, f2_all(1.0f / 6.0f)), q), t);
+    const f32x2 c = f2_add(t, f2_all(1.0f)), c_low = f2_less(t, f2_add(c, f2_all(-1.0f)));
+    const f32x2 half = f2_mul(q, f2_all(0.5f)), d = f2_add(c, half), d_low = f2_less(half, f2_less(d, c));
+    // (u times e^t: 1 and t, which is in q_low, and t^2 / 2 and the rest)
+    const f32x2 parts = f2_add(f2_add(c_low, d_low), f2_add(f2_fma(f2_all(0.5f), q_low, f2_fma(u, f2_add(half, rest), u)), rest));
+    const f32x2 main = f2_add(d, parts), l = f2_less(parts, f2_less(main, d));
+    float n0, n1, p0, p1, d0, d1, l0, l1;
+    f2_unpack(nm, n0, n1);
+    f2_unpack(np, p0, p1);
+    const f32x2 unit = f2_pack(__uint_as_float((__float_as_uint(n0) << 23) + 0x3F800000u), __uint_as_float((__float_as_uint(n1) << 23) + 0x3F800000u));
+    f2_unpack(f2_mul(main, unit), d0, d1);
+    f2_unpack(f2_mul(l, unit), l0, l1);
+    const f32x2 v = f2_pack(p0 < 45.0f ? d0 : 0.0f, p1 < 45.0f ? d1 : 0.0f), v_low = f2_pack(p0 < 45.0f ? l0 : 0.0f, p1 < 45.0f ? l1 : 0.0f);
+    const f32x2 at_high = f2_add(v, f2_all(kHigh));
+    const f32x2 at_low = f2_add(f2_add(f2_less(v, f2_add(at_high, f2_all(-kHigh))), v_low), f2_all(kLow));
+    high += static_cast<uint32_t>(at_high) + static_cast<uint32_t>(at_high >> 32);
+    low += static_cast<uint32_t>(at_low) + static_cast<uint32_t>(at_low >> 32);
+    ++pairs;
+  }
+  __device__ __forceinline__ uint64_t units() const {
+    const uint32_t h = high - 2 * pairs * __float_as_uint(kHigh), l = low - 2 * pairs * __float_as_uint(kLow);
+    return (static_cast<uint64_t>(h) << 22) + static_cast<int64_t>(static_cast<int32_t>(l));
+  }
+};
 
 constexpr int kRanked = 512;      // candidates that are ranked by counting: one a thread,
 constexpr int kFew = 128;         // or with a quarter of the others to a thread
@@ -809,10 +839,18 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
       __syncthreads();
       const Row r = row_of<DT>(a, row0 + w);
       const float m = sh.m[w];
-      uint64_t sum = 0;
-      const unsigned char* x = r.base + r.lead * E::kBytes;
-#pragma unroll 4
-      for (int v = tid; v < a.V; v += kMergeThreads) sum += exact_weight(load_logit<DT>(x, v), m);
+      ExactSum exact;
+      uint4 next = tid < r.vecs ? load_vec<DT>(r, tid) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+      for (int v = tid; v < r.vecs; v += kMergeThreads) {
+        const uint4 x = next;
+        if (v + kMergeThreads < r.vecs) next = load_vec<DT>(r, v + kMergeThreads);
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+        for (int j = 0; j < 4; j += DT == SV_BF16 ? 1 : 2)
+          exact.add(DT == SV_BF16 ? f2_pack(bf16_lo(p[j]), bf16_hi(p[j])) : f2_pack(__uint_as_float(p[j]), __uint_as_float(p[j + 1])), f2_all(m));
+      }
+      uint64_t sum = exact.units();
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
       if (lane == 0) atomicAdd(&sh.sum, static_cast<unsigned long long>(sum));
       __syncthreads();

@@ -39,10 +39,11 @@
 //
 // A cache in 4 bits (kFour) with more rows than sv_attention4.cu's tiles: one warp copies a tile's codes into a ring of their
 // own, and four more warps turn them into the stages' K and V, as float16 (exact: a code times its scale has six bits), and Q
-// into float16 rows scaled by powers of two.  The rest is the same, with P in float16.  Whole warpgroups share out the registers.
-// Measured (as above, bytes in 4 bits in brackets): 64 trees 114 us (28), four chains 260 us (78; their products padded to 128
-// rows 126).  A tile takes 1.3 to 1.4 us however few its bytes: S, softmax and P V follow each other through barriers, on four
-// stages of 32 KB; decoding waits for them.
+// into float16 rows scaled by powers of two.  S and P V are issued by two warps; the one that brings Q finds the segments for all.
+// The rest is the same, with P in float16.  Whole warpgroups share out the registers.
+// Measured (as above, bytes in 4 bits in brackets): 64 trees 108.5 us (28), four chains 250 us (78; their products padded to 128
+// rows 126).  A tile takes 1.2 us however few its bytes: a warp's decoding 2100 clocks of 2300, the softmax of a group 1900, the
+// products 1100, and half of the issue slots are used; a row tile's beginning and end 6 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -217,3 +217,66 @@ def test_other_stream_and_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("Hq,Hk", [(16, 4), (18, 3)])
+def test_many_tiles_of_64_dimensions(Hq, Hk):
+    """Pairs of heads and single ones, row tiles over many cache tiles."""
+    check(case([5000, 2100, 900], ["mixed", "wide", "chain"], Hq, Hk, 64, 32, seed=Hq))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_requests_than_leave_room_for_four_stages(D):
+    lens = [(37 * i) % 300 for i in range(1700)]
+    c = case(lens, ["wide" if i % 8 == 0 else "one" for i in range(1700)], 4, 2, D, 16, seed=D)
+    check(c)
+
+
+def test_one_workspace_for_few_and_many_rows():
+    few, many = case([300, 40], ["one", "one"], 8, 2, 128, 16, seed=1), case([300, 40], ["big", "mixed"], 8, 2, 128, 16, seed=2)
+    ws = sv.attention_workspace(few["cache"], 8)
+    for _ in range(2):
+        check(few, ws=ws)
+        check(many, ws=ws)
+
+
+@pytest.mark.parametrize("tree", ["one", "mixed"])
+def test_rows_behind_the_last_request_stay(tree):
+    c = case([100, 30], [tree] * 2, 8, 2, 64, 16, seed=3)
+    n = c["q"].shape[0]
+    q = torch.cat([c["q"], torch.full((5, 8, 64), float("nan"), dtype=torch.bfloat16, device="cuda")])
+    out, lse = torch.full((n + 5, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((n + 5, 8), 9.0, device="cuda")
+    parent = torch.cat([c["parent"], i32([-1] * 5)])
+    sv.tree_attention(q, c["cache"], 0, c["lens"], c["offs"], parent, c["nmax"], out=out, lse=lse)
+    want, want_lse = sv.tree_attention(c["q"], c["cache"], 0, c["lens"], c["offs"], c["parent"], c["nmax"])
+    assert torch.equal(out[:n], want) and torch.equal(lse[:n], want_lse)
+    assert (out[n:] == 7).all() and (lse[n:] == 9).all()
+
+
+@pytest.mark.parametrize("tree", ["one", "mixed"])
+def test_pages_past_four_gigabytes(tree):
+    """The same sequences in a small pool and in pages whose bytes lie behind 2^32."""
+    pages, ps, D, Hk = 60000, 64, 128, 8
+    outs = []
+    for count, first in ((40, 0), (pages, pages - 40)):
+        table = i32([[first + 7, first + 30, first + 2, first + 39], [first + 11, first + 1, -1, -1], [-1] * 4])
+        refs = torch.zeros(count, dtype=torch.int32, device="cuda")
+        refs[table[table >= 0].long()] = 1
+        refs[:first] = 1
+        cache = sv.PagedCache4(torch.empty((1, count, Hk, ps * 9 * D // 8), dtype=torch.uint8, device="cuda"), refs, table, ps, D)
+        g = torch.Generator(device="cuda").manual_seed(4)
+        parent = TREES[tree]
+        N = len(parent)
+        k, v = (torch.randn((1, 330 + 2 * N, Hk, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        q = torch.randn((2 * N, 32, D), generator=g, device="cuda").to(torch.bfloat16)
+        cache.append(k, v, i32([0, 0, 0]), i32([0, 230 + N, 330 + 2 * N, 330 + 2 * N]))
+        args = (i32([0, N, 2 * N, 2 * N]), i32(parent * 2), N)
+        lens = i32([230, 100, 0])
+        one = sv.tree_attention(q, cache, 0, lens, *args)
+        assert int(cache.reorder(lens, i32([1, 0, 0]))) == 1
+        two = sv.tree_attention(q[:N], cache, 0, lens, i32([0, 0, 0, N]), i32(parent), N)  # the copied row, without its tree's slots
+        outs.append((*one, lens))
+        assert cache.page_table[2, 3] != cache.page_table[1, 3] and cache.page_table[2, 0] == cache.page_table[1, 0]
+        assert two[0].shape == (N, 32, D)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)

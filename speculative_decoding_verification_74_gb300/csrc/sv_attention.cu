@@ -531,6 +531,8 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
         }
         if (!go) break;
         s = sm.seg[segments & kSegMask];
+        // what belongs to Q is there twice: every softmax thread has to be done with the segment before the last one
+        if (segments >= 2 && !warp_wait<kFour>(&sm.seg_free[(segments - 2) & kSegMask], ((segments - 2) / Role::kSegments) & 1, &sm.dead, a.status)) break;
       } else {
         s = t == t0 ? opening : segment_at<kTile>(sm.line, before, t, t1);
         if (!describe(segments, s)) break;

@@ -29,7 +29,7 @@ def i32(a):
 
 TREES = {"one": [-1], "none": [], "chain": list(tree_shape([1] * 16, 17)), "mixed": list(tree_shape([3, 2, 1, 1], 16)),
          "wide": list(tree_shape([7, 1], 15)), "big": list(tree_shape([4, 3, 3, 2], 77)),
-         "deep": list(tree_shape([2] + [1] * 80, 150))}
+         "deep": list(tree_shape([2] + [1] * 80, 150)), "longest": list(range(-1, 1023))}
 
 
 def case(lens, trees, Hq, Hk, D, ps, seed=0, layers=1, stride=0):
@@ -280,3 +280,13 @@ def test_pages_past_four_gigabytes(tree):
         assert two[0].shape == (N, 32, D)
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_longest_chain_and_the_most_requests(D):
+    c = case([100, 5], ["longest", "one"], 4, 2, D, 64, seed=D)
+    check(c)
+    check(c, parent=None)
+    check(c, window=700, sinks=3)
+    c = case([i % 40 for i in range(4096)], ["wide" if i % 300 == 0 else "one" for i in range(4096)], 4, 2, D, 16, seed=D)
+    check(c)

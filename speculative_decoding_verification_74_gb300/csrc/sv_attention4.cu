@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(Tile4<N>::kThreads, 1) attend4_kernel(const At
     const int s0 = tile_slot<kChunk>(load.r, load_j);
     constexpr int kUnit = kGroupBytes / 8;                    // bytes of a slot
     uint64_t* bar = &sm.full[warp][ask_stage];
-    if (a.shift >= 5) {                                       // one copy, of a page that is looked up where it begins
+    if (a.shift >= 5) {  // one copy, of a page that is looked up where it begins, or where the chunk does not follow the last one
       const int in_page = s0 & ((1 << a.shift) - 1);
-      if (in_page == 0 || block < 0) {
+      if (in_page == 0 || block < 0 || load_j == load.r.sink_tiles) {
         const int entry = s0 >> a.shift;
         pages_from(entry);
         const int page = __shfl_sync(0xFFFFFFFFu, page_now, entry & 31);

@@ -42,6 +42,7 @@ constexpr int kBatch = 64;                     // candidates that wait for the l
 constexpr int kMaxParts = 32;                  // parts of a row: a lane each in the merge
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kRefSlack = 30.0f;             // how far a logit may lie above a sum's reference
+constexpr float kFarRef = 0x1p12f;             // references past this are subtracted from the logits themselves
 constexpr int kFraction = 40;                  // fractional bits of a part's sum
 constexpr int kMergeThreads = 512;
 constexpr double kNear = 0x1p-18;              // totals of two beams nearer than this are told apart by exact sums
@@ -362,28 +363,29 @@ __device__ __forceinline__ void add_piece(Sum& a, const uint4 (&w)[kVecs], float
     a.ref = mine;
     a.begun = true;
   }
-  float terms;
-  if (__any_sync(0xFFFFFFFFu, fabsf(a.ref) > 0x1p100f)) {  // k ref might overflow
-    terms = 0.0f;
-#pragma unroll 1
-    for (int i = 0; i < kVecs; ++i) {
-      const uint4 v = i < 2 ? (i < 1 ? w[0] : w[1]) : (i < 3 ? w[2] : w[3]);
-#pragma unroll 1
-      for (int j = 0; j < E::kPerVec; ++j) terms += ex2_approx((element_at<DT>(v, j) - a.ref) * kLog2e);
-    }
+  // Up to kFarRef, k ref is off by 2^-12 at most, and 2^rest = 1 + rest ln 2 to 2^-26.  Past it (masks of large numbers, logits far
+  // from 0) the difference comes first, rounded once more; nothing of k ref is left then.
+  const bool far = __any_sync(0xFFFFFFFFu, fabsf(a.ref) > kFarRef);
+  const float off = far ? 0.0f : -a.ref * kLog2e, rest = far ? 0.0f : fmaf(-a.ref, kLog2e, -off);  // off + rest = -k ref
+  const f32x2 k2 = f2_pack(kLog2e, kLog2e), off2 = f2_pack(off, off);
+  f32x2 s[2] = {0, 0};
+  if (far) {
+    const f32x2 less = f2_pack(-a.ref, -a.ref);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < E::kPerVec; j += 2)
+        s[(j >> 1) & 1] = f2_add(s[(j >> 1) & 1], f2_exp2_offset(f2_add(f2_pack(element<DT>(w, i, j), element<DT>(w, i, j + 1)), less), k2, off2));
   } else {
-    const float off = -a.ref * kLog2e, rest = fmaf(-a.ref, kLog2e, -off);  // off + rest = -k ref
-    const f32x2 k2 = f2_pack(kLog2e, kLog2e), off2 = f2_pack(off, off);
-    f32x2 s[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
 #pragma unroll
       for (int j = 0; j < E::kPerVec; j += 2)
         s[(j >> 1) & 1] = f2_add(s[(j >> 1) & 1], f2_exp2_offset(f2_pack(element<DT>(w, i, j), element<DT>(w, i, j + 1)), k2, off2));
-    float s0, s1;
-    f2_unpack(f2_add(s[0], s[1]), s0, s1);
-    terms = fmaf(s0 + s1, rest * 0.693147181f, s0 + s1);  // 2^rest = 1 + rest ln 2
   }
+  float s0, s1;
+  f2_unpack(f2_add(s[0], s[1]), s0, s1);
+  const float terms = fmaf(s0 + s1, rest * 0.693147181f, s0 + s1);
   const float y = terms - a.lost, now = a.sum + y;
   a.lost = (now - a.sum) - y;
   a.sum = now;

@@ -14,9 +14,10 @@
 // than K candidates, which are ranked by counting on totals in 64 bits.  The float32 terms leave A uncertain by up to 2^-19: 2^-22
 // of ex2, the roundings of a term's exponent and of its lane's reference (half a step of numbers below 8, or of up to log2 V for
 // terms that are as many as they are small, times ln 2: 2^-21 each), a piece's plain sum (ten steps of 2^-24), logf and exp2f
-// (2^-23 each); the pieces' compensated sums add next to nothing.  So
-// where neighbours of different beams in the order lie within kNear of each other, their rows are summed again with terms in
-// pairs of floats (about 2^-30), and the ranking is repeated: with this the order is that of the exact totals, down to 2^-29.
+// (2^-23 each); the pieces' compensated sums add next to nothing.  So where neighbours of different beams in the order lie within
+// kNear of each other, or the K-th and any candidate past the cut do, their rows are summed again with terms in pairs of floats,
+// and the ranking is repeated.  With this the order is that of the exact totals where those of two beams differ by 2^-25 (each
+// term is off by 2^-30 of itself and 2^-45, V of them by 2^-27), and that of beams where they are equal.
 //
 // Measured (GB300, graph replay; a copy of the logits in brackets): 1024 rows of 151936, K = 8, float32 125 us (92), bf16 79 (46);
 // of 64 requests of 16 beams a quarter with one beam only, K = 32, bf16 61 (35: rows of missing beams are not read); 64 rows
@@ -681,6 +682,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
       *what = static_cast<uint32_t>(w) << kTokenBits | kPad;
     }
   };
+  auto beam_of = [](uint32_t what) { return static_cast<int>((what & ~kPad) >> kTokenBits); };
+  // two beams whose totals nearly agree: their rows are to be summed again, unless that is done
+  auto settled = [&](int beam, int other) { return beam == other || (sh.exact[beam] && sh.exact[other]); };
+  auto ask = [&](int beam, int other) {
+    if (settled(beam, other)) return;
+    if (!sh.exact[beam]) sh.asked[beam] = 1;
+    if (!sh.exact[other]) sh.asked[other] = 1;
+    sh.again = 1;
+  };
   for (;;) {
     if (tid < SV_MAX_BEAMS) sh.asked[tid] = 0;
     if (tid == 0) {
@@ -744,7 +754,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
         }
       }
     }
-    low = low > 16 ? low - 16 : 1;  // (steps of float32 that its totals may be off by)
+    // totals in float32 may be off by a few steps, and whatever may come before the K-th once its row is summed again counts too
+    if (low > float_key(-FLT_MAX)) low = float_key(float_of_key(low) - static_cast<float>(2.0 * kNear));
+    low = low > 16 ? low - 16 : 1;
     __syncthreads();
     each([&](int l, int i, int w) {
       if (about[l * K + i] < low) return;
@@ -782,14 +794,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
           sh.out_what[rank] = what;
         }
       }
-    } else {  // long runs of equals: one by one
+    } else {  // long runs of equals: one by one, the (K + 1)-th of another beam than the K-th
       uint64_t before = ~uint64_t(0);
       uint32_t before_what = 0;
       for (int k = 0; k < want; ++k) {
         uint64_t best_key = 0;
         uint32_t best_what = 0;
+        const int last = k == K ? beam_of(before_what) : -1;  // past the cut: the best of a beam that the K-th's is to be told from
         each([&](int l, int i, int w) {
-          if (about[l * K + i] < low) return;
+          if (about[l * K + i] < low || (last >= 0 && settled(last, w))) return;
           uint64_t key;
           uint32_t what;
           candidate(l, i, w, &key, &what);
@@ -818,23 +831,23 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
       }
     }
     __syncthreads();
+    // candidates past the cut, of other beams than the K-th's (more than kRanked: found one by one)
+    if (want > K && n <= kRanked && tid < n) {
+      const uint64_t key = sh.key[tid], last_key = sh.out_key[K - 1];
+      const uint32_t what = sh.what[tid], last_what = sh.out_what[K - 1];
+      if ((key < last_key || (key == last_key && what > last_what)) && total_of_key(last_key) - total_of_key(key) < kNear)
+        ask(beam_of(last_what), beam_of(what));
+    }
     for (int k = tid; k < K; k += kMergeThreads) {
       const bool some = k < want;
       const uint64_t key = some ? sh.out_key[k] : 0;
       const uint32_t what = some ? sh.out_what[k] : 0;
-      const int beam = static_cast<int>((what & ~kPad) >> kTokenBits);
+      const int beam = beam_of(what);
       const int64_t at = static_cast<int64_t>(request) * K + k;
       a.out_scores[at] = some ? static_cast<float>(total_of_key(key)) : -INFINITY;
       a.out_rows[at] = some ? static_cast<int32_t>(row0) + beam : -1;
       a.out_tokens[at] = !some ? -1 : (what & kPad) ? a.pad : static_cast<int32_t>(what & kTokenMask);
-      if (k + 1 < want) {
-        const int next = static_cast<int>((sh.out_what[k + 1] & ~kPad) >> kTokenBits);
-        if (next != beam && total_of_key(key) - total_of_key(sh.out_key[k + 1]) < kNear && !(sh.exact[beam] && sh.exact[next])) {
-          if (!sh.exact[beam]) sh.asked[beam] = 1;
-          if (!sh.exact[next]) sh.asked[next] = 1;
-          sh.again = 1;
-        }
-      }
+      if (k + 1 < want && total_of_key(key) - total_of_key(sh.out_key[k + 1]) < kNear) ask(beam, beam_of(sh.out_what[k + 1]));
     }
     __syncthreads();
     if (sh.again == 0) return;

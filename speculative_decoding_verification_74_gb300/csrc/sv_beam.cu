@@ -609,9 +609,9 @@ __device__ __forceinline__ float about_total(float high, float low, float x, flo
   return t + (((high - (t - c)) + (d - c)) + (low + d_low));
 }
 
-// What stands for a candidate: beam << kTokenBits | token, in the order of equal totals; kPad: the token is `pad`.
-constexpr int kTokenBits = 18;
-constexpr uint32_t kPad = 1u << 31, kTokenMask = (1u << kTokenBits) - 1u;
+// What stands for a candidate: beam << kBeamAt | token, in the order of equal totals; kPad (below the beam's bits): the token is `pad`.
+constexpr int kBeamAt = 19;
+constexpr uint32_t kPad = 1u << (kBeamAt - 1), kTokenMask = kPad - 1u;
 
 template <int DT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a) {
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
   const int request = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = static_cast<int64_t>(request) * a.W;
   const int K = a.K, W = a.W, P = a.P, lists = W * P;
-  static_assert(SV_MAX_SAMPLE_VOCAB <= 1 << kTokenBits && int64_t(SV_MAX_BEAMS) << kTokenBits <= int64_t(kPad), "what stands for a candidate");
+  static_assert(SV_MAX_SAMPLE_VOCAB <= int64_t(kPad) && int64_t(SV_MAX_BEAMS) << kBeamAt <= int64_t(UINT32_MAX), "what stands for a candidate");
   if (tid == 0) sh.bad = 0;
   __syncthreads();
   for (int w = warp; w < W; w += kMergeThreads / 32) {  // one sum of the parts'
@@ -676,13 +676,13 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     if (sh.live[w]) {
       const Entry e = entries[l * K + i];
       *key = total_key(A + (static_cast<double>(e.x) - sh.m[w]));
-      *what = static_cast<uint32_t>(w) << kTokenBits | static_cast<uint32_t>(e.token);
+      *what = static_cast<uint32_t>(w) << kBeamAt | static_cast<uint32_t>(e.token);
     } else {
       *key = total_key(A);
-      *what = static_cast<uint32_t>(w) << kTokenBits | kPad;
+      *what = static_cast<uint32_t>(w) << kBeamAt | kPad;
     }
   };
-  auto beam_of = [](uint32_t what) { return static_cast<int>((what & ~kPad) >> kTokenBits); };
+  auto beam_of = [](uint32_t what) { return static_cast<int>(what >> kBeamAt); };
   // two beams whose totals nearly agree: their rows are to be summed again, unless that is done
   auto settled = [&](int beam, int other) { return beam == other || (sh.exact[beam] && sh.exact[other]); };
   auto ask = [&](int beam, int other) {

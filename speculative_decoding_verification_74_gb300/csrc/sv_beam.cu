@@ -586,7 +586,7 @@ struct MergeShared {
   uint8_t live[SV_MAX_BEAMS];     // the beam's logits count
   uint8_t asked[SV_MAX_BEAMS];
   uint64_t key[kRanked], out_key[SV_MAX_BEAM_CANDIDATES + 1];
-  uint32_t what[kRanked], out_what[SV_MAX_BEAM_CANDIDATES + 1];
+  uint64_t what[kRanked], out_what[SV_MAX_BEAM_CANDIDATES + 1];
   unsigned long long sum;
   uint32_t bad;
   int again, n, counts[32], rank[kFew];
@@ -609,9 +609,15 @@ __device__ __forceinline__ float about_total(float high, float low, float x, flo
   return t + (((high - (t - c)) + (d - c)) + (low + d_low));
 }
 
-// What stands for a candidate: beam << kBeamAt | token, in the order of equal totals; kPad (below the beam's bits): the token is `pad`.
-constexpr int kBeamAt = 19;
-constexpr uint32_t kPad = 1u << (kBeamAt - 1), kTokenMask = kPad - 1u;
+// What stands for a candidate, in the order of equal totals, the larger first: the lower beam, of its candidates the larger logit
+// (a total may have lost what tells two of a beam's logits apart), then the lower token.
+constexpr int kTokenBits = 18, kBeamAt = kTokenBits + 32;
+constexpr uint32_t kTokenMask = (1u << kTokenBits) - 1u;
+__device__ __forceinline__ uint64_t standing(int beam, float x, int token) {
+  return static_cast<uint64_t>(SV_MAX_BEAMS - 1 - beam) << kBeamAt | static_cast<uint64_t>(float_key(x)) << kTokenBits | (kTokenMask - static_cast<uint32_t>(token));
+}
+__device__ __forceinline__ int beam_of(uint64_t what) { return SV_MAX_BEAMS - 1 - static_cast<int>(what >> kBeamAt); }
+__device__ __forceinline__ int token_of(uint64_t what) { return static_cast<int>(kTokenMask - (static_cast<uint32_t>(what) & kTokenMask)); }
 
 template <int DT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a) {
@@ -622,7 +628,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
   const int request = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = static_cast<int64_t>(request) * a.W;
   const int K = a.K, W = a.W, P = a.P, lists = W * P;
-  static_assert(SV_MAX_SAMPLE_VOCAB <= int64_t(kPad) && int64_t(SV_MAX_BEAMS) << kBeamAt <= int64_t(UINT32_MAX), "what stands for a candidate");
+  static_assert(SV_MAX_SAMPLE_VOCAB <= 1 << kTokenBits && SV_MAX_BEAMS <= 1 << (64 - kBeamAt), "what stands for a candidate");
   if (tid == 0) sh.bad = 0;
   __syncthreads();
   for (int w = warp; w < W; w += kMergeThreads / 32) {  // one sum of the parts'
@@ -671,18 +677,17 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     }
   };
   // A candidate: its total, and what stands for it
-  auto candidate = [&](int l, int i, int w, uint64_t* key, uint32_t* what) {
+  auto candidate = [&](int l, int i, int w, uint64_t* key, uint64_t* what) {
     const double A = sh.A[w];
     if (sh.live[w]) {
       const Entry e = entries[l * K + i];
       *key = total_key(A + (static_cast<double>(e.x) - sh.m[w]));
-      *what = static_cast<uint32_t>(w) << kBeamAt | static_cast<uint32_t>(e.token);
+      *what = standing(w, e.x, e.token);
     } else {
       *key = total_key(A);
-      *what = static_cast<uint32_t>(w) << kBeamAt | kPad;
+      *what = standing(w, 0.0f, 0);
     }
   };
-  auto beam_of = [](uint32_t what) { return static_cast<int>(what >> kBeamAt); };
   // two beams whose totals nearly agree: their rows are to be summed again, unless that is done
   auto settled = [&](int beam, int other) { return beam == other || (sh.exact[beam] && sh.exact[other]); };
   auto ask = [&](int beam, int other) {
@@ -771,10 +776,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
       __syncthreads();
       if (i < n) {
         const uint64_t key = sh.key[i];
-        const uint32_t what = sh.what[i];
+        const uint64_t what = sh.what[i];
         int rank = 0;
 #pragma unroll 4
-        for (int j = part; j < n; j += kMergeThreads / kFew) rank += sh.key[j] > key || (sh.key[j] == key && sh.what[j] < what);
+        for (int j = part; j < n; j += kMergeThreads / kFew) rank += sh.key[j] > key || (sh.key[j] == key && sh.what[j] > what);
         atomicAdd(&sh.rank[i], rank);
       }
       __syncthreads();
@@ -785,10 +790,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     } else if (n <= kRanked) {
       if (tid < n) {
         const uint64_t key = sh.key[tid];
-        const uint32_t what = sh.what[tid];
+        const uint64_t what = sh.what[tid];
         int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) rank += sh.key[j] > key || (sh.key[j] == key && sh.what[j] < what);
+        for (int j = 0; j < n; ++j) rank += sh.key[j] > key || (sh.key[j] == key && sh.what[j] > what);
         if (rank <= K) {
           sh.out_key[rank] = key;
           sh.out_what[rank] = what;
@@ -796,17 +801,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
       }
     } else {  // long runs of equals: one by one, the (K + 1)-th of another beam than the K-th
       uint64_t before = ~uint64_t(0);
-      uint32_t before_what = 0;
+      uint64_t before_what = 0;
       for (int k = 0; k < want; ++k) {
         uint64_t best_key = 0;
-        uint32_t best_what = 0;
+        uint64_t best_what = 0;
         const int last = k == K ? beam_of(before_what) : -1;  // past the cut: the best of a beam that the K-th's is to be told from
         each([&](int l, int i, int w) {
           if (about[l * K + i] < low || (last >= 0 && settled(last, w))) return;
-          uint64_t key;
-          uint32_t what;
+          uint64_t key, what;
           candidate(l, i, w, &key, &what);
-          if ((key < before || (key == before && what > before_what)) && (key > best_key || (key == best_key && what < best_what))) {
+          if ((key < before || (key == before && what < before_what)) && (key > best_key || (key == best_key && what > best_what))) {
             best_key = key;
             best_what = what;
           }
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
         sh.what[tid] = best_what;
         for (int d = kMergeThreads / 2; d > 0; d >>= 1) {
           __syncthreads();
-          if (tid < d && (sh.key[tid + d] > sh.key[tid] || (sh.key[tid + d] == sh.key[tid] && sh.what[tid + d] < sh.what[tid]))) {
+          if (tid < d && (sh.key[tid + d] > sh.key[tid] || (sh.key[tid + d] == sh.key[tid] && sh.what[tid + d] > sh.what[tid]))) {
             sh.key[tid] = sh.key[tid + d];
             sh.what[tid] = sh.what[tid + d];
           }
@@ -833,20 +837,19 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
     __syncthreads();
     // candidates past the cut, of other beams than the K-th's (more than kRanked: found one by one)
     if (want > K && n <= kRanked && tid < n) {
-      const uint64_t key = sh.key[tid], last_key = sh.out_key[K - 1];
-      const uint32_t what = sh.what[tid], last_what = sh.out_what[K - 1];
-      if ((key < last_key || (key == last_key && what > last_what)) && total_of_key(last_key) - total_of_key(key) < kNear)
+      const uint64_t key = sh.key[tid], last_key = sh.out_key[K - 1], what = sh.what[tid], last_what = sh.out_what[K - 1];
+      if ((key < last_key || (key == last_key && what < last_what)) && total_of_key(last_key) - total_of_key(key) < kNear)
         ask(beam_of(last_what), beam_of(what));
     }
     for (int k = tid; k < K; k += kMergeThreads) {
       const bool some = k < want;
       const uint64_t key = some ? sh.out_key[k] : 0;
-      const uint32_t what = some ? sh.out_what[k] : 0;
+      const uint64_t what = some ? sh.out_what[k] : 0;
       const int beam = beam_of(what);
       const int64_t at = static_cast<int64_t>(request) * K + k;
       a.out_scores[at] = some ? static_cast<float>(total_of_key(key)) : -INFINITY;
       a.out_rows[at] = some ? static_cast<int32_t>(row0) + beam : -1;
-      a.out_tokens[at] = !some ? -1 : (what & kPad) ? a.pad : static_cast<int32_t>(what & kTokenMask);
+      a.out_tokens[at] = !some ? -1 : sh.live[beam] ? token_of(what) : a.pad;
       if (k + 1 < want && total_of_key(key) - total_of_key(sh.out_key[k + 1]) < kNear) ask(beam, beam_of(sh.out_what[k + 1]));
     }
     __syncthreads();

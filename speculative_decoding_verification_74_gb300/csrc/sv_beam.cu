@@ -602,11 +602,13 @@ __device__ __forceinline__ double total_of_key(uint64_t k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? k & ~(uint64_t(1) << 63) : ~k));
 }
 
-// high + low + (x - m), rounded once or twice: the rounding of each sum is kept (Knuth's exact sum).
+// high + low + (x - m), rounded once or twice: the rounding of each sum is kept (Knuth's exact sum).  Sums below float32's range
+// are its lowest number.
 __device__ __forceinline__ float about_total(float high, float low, float x, float m) {
   const float d = x - m, b = d - x, d_low = (x - (d - b)) - (m + b);
   const float t = high + d, c = t - high;
-  return t + (((high - (t - c)) + (d - c)) + (low + d_low));
+  const float total = t + (((high - (t - c)) + (d - c)) + (low + d_low));
+  return total >= -FLT_MAX ? total : -FLT_MAX;  // (what was lost of an infinite sum is NaN)
 }
 
 // What stands for a candidate, in the order of equal totals, the larger first: the lower beam, of its candidates the larger logit

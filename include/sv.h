@@ -610,7 +610,8 @@ sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64
  * candidate get -inf, -1, -1.  With K = W out_scores may be scores.  A NaN or +inf among the scores of a request, or the logits of a beam that is not finished and whose
  * score is not -inf: the request's outputs are NaN, -1, -1 (SV_DEV_BAD_LOGIT).
  * Limits: 0 <= B, 1 <= W <= SV_MAX_BEAMS, B W <= SV_MAX_BEAM_ROWS, 1 <= V <= SV_MAX_SAMPLE_VOCAB, 1 <= K <= SV_MAX_BEAM_CANDIDATES,
- * 0 <= pad.  Workspace: sv_beam_workspace_size(B W, V, K), its first SV_STATUS_BYTES zero-filled before its first use.
+ * 0 <= pad.  Workspace: sv_beam_workspace_size(B W, V, K), its first SV_STATUS_BYTES zero-filled before its first use; the size
+ * grows with each argument, so one made for the largest call serves smaller ones.
  */
 #define SV_MAX_BEAMS 64
 #define SV_MAX_BEAM_ROWS (1 << 16)

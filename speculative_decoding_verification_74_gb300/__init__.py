@@ -991,7 +991,7 @@ class PagedCache4(PagedCache):
 
 
 def beam_workspace(rows: int, vocab: int, candidates: int, device="cuda") -> torch.Tensor:
-    """Workspace of beam_select() for that many rows of logits (its first word is the device status word)."""
+    """Workspace of beam_select() for up to that many rows of logits (its first word is the device status word)."""
     n = sv_beam_workspace_size(rows, vocab, candidates)
     if n == 0:
         raise ValueError("invalid sizes for sv_beam_workspace_size")

@@ -889,18 +889,22 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamParams a
 
 // ---- host --------------------------------------------------------------------------------------------
 // Parts of a row: as many as give every CTA that fits on the GPU one, each of a piece per warp at least.
-int parts_of(int rows, int V) {
+constexpr int kCtas = kRowCtas * 152;
+int most_parts(int V) {
   const int pieces = (V + 7 + kPiece * 4 - 1) / (kPiece * 4);  // (of float32: the most there are)
-  return std::max(1, std::min({kMaxParts, pieces / kWarps, kRowCtas * 152 / rows}));
+  return std::max(1, std::min(kMaxParts, pieces / kWarps));
 }
+int parts_of(int rows, int V) { return std::max(1, std::min(most_parts(V), kCtas / rows)); }
 // ... and as many as the merge's shared memory has room for.
 constexpr int kMerged = 8192;     // candidates of a request's beams and parts: more take longer to merge than a row's further parts save
 int parts_of(int rows, int V, int W, int K) { return std::max(1, std::min(parts_of(rows, V), kMerged / (W * K))); }
 struct BeamLayout {
   size_t parts, entries, total;
 };
+// Sizes for the most parts that any number of rows up to this one has: a workspace serves every call of no more rows, vocabulary
+// and candidates.
 BeamLayout layout_of(int rows, int V, int K) {
-  const size_t n = static_cast<size_t>(rows) * parts_of(rows, V);
+  const size_t n = std::max(static_cast<size_t>(rows), std::min<size_t>(kCtas, static_cast<size_t>(rows) * most_parts(V)));
   BeamLayout L;
   L.parts = SV_STATUS_BYTES;
   L.entries = L.parts + ((sizeof(Part) * n + 255) & ~size_t(255));

@@ -314,7 +314,12 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, int32_t* tab
         }
       }
     };
-    if (drops) each_entry([&](int page) { give_back(p, page, status); });
+    // (counts may fall below 0 here, where a page is named more often than it is counted: so that all can be taken back)
+    bool too_often = false;
+    if (drops) {
+      each_entry([&](int page) { too_often |= page >= p.pages || atomicSub(p.refs + page, 1) <= 0; });
+      too_often = __syncthreads_or(too_often);
+    }
     const int part_mask = (1 << p.shift) - 1;
     int sum = 0;
 #pragma unroll
@@ -329,18 +334,22 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, int32_t* tab
     if (total == 0) {
       found = 0;
     } else {
-      __threadfence_block();
-      __syncthreads();
-      rank = block_scan(drops ? count_free(p) : free_pages, buf, &found);
+      rank = block_scan(drops ? count_free<true>(p) : free_pages, buf, &found);
     }
     if (total > found) {
       problem = SV_DEV_OUT_OF_PAGES;
-      __syncthreads();
       if (drops)
         each_entry([&](int page) {
           if (page < p.pages) atomicAdd(p.refs + page, 1);
         });
-    } else if (total > 0) {
+    } else if (too_often) {
+      each_entry([&](int page) {
+        if (page < p.pages) atomicMax(p.refs + page, 0);
+      });
+      if (threadIdx.x == 0) atomicOr(status, SV_DEV_BAD_PAGE);
+      __syncthreads();
+    }
+    if (problem == 0 && total > 0) {
 #pragma unroll
       for (int x = 0; x < kPerThread; ++x)
         if (split[x]) pair_of[at++] = threadIdx.x * kPerThread + x;

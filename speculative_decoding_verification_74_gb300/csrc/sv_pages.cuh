@@ -73,7 +73,10 @@ __device__ __forceinline__ int block_scan(int v, int* buf, int* total) {
 __device__ __forceinline__ int pages_per_thread(int pages) {
   return ((pages + kPageThreads - 1) / kPageThreads + 3) & ~3;
 }
+// kBelow: while pages are given back tentatively, counts below 0 are those of free pages too.
+template <bool kBelow = false>
 __device__ __forceinline__ int count_free(const Pool& p) {
+  auto is_free = [](int refs) { return kBelow ? refs <= 0 : refs == 0; };
   const int n = pages_per_thread(p.pages);
   const int64_t first = static_cast<int64_t>(threadIdx.x) * n;
   const int64_t last = min(first + n, static_cast<int64_t>(p.pages));
@@ -83,13 +86,13 @@ __device__ __forceinline__ int count_free(const Pool& p) {
     for (int64_t g = first; g < last; g += 4) {
       if (g + 4 <= last) {
         const int4 r = *reinterpret_cast<const int4*>(p.refs + g);
-        free_pages += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+        free_pages += is_free(r.x) + is_free(r.y) + is_free(r.z) + is_free(r.w);
       } else {
-        for (int64_t h = g; h < last; ++h) free_pages += p.refs[h] == 0;
+        for (int64_t h = g; h < last; ++h) free_pages += is_free(p.refs[h]);
       }
     }
   } else {
-    for (int64_t g = first; g < last; ++g) free_pages += p.refs[g] == 0;
+    for (int64_t g = first; g < last; ++g) free_pages += is_free(p.refs[g]);
   }
   return free_pages;
 }

@@ -1392,7 +1392,11 @@ using namespace sv;
 extern "C" {
 
 size_t sv_attention_workspace_size(const sv_cache* c, int q_heads) {
-  if (check_cache(c) != SV_OK || q_heads < 1 || q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > kTile) return 0;
+  if (check_cache(c) != SV_OK) return 0;
+  if (q_heads < 1 || q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > kTile) {
+    set_error(SV_ERR_INVALID_ARG, "q_heads=%d: 1 to %d times kv_heads=%d are needed", q_heads, kTile, c->kv_heads);
+    return 0;
+  }
   return layout_of(kMaxCtas, c->head_dim).total;
 }
 

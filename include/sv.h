@@ -588,7 +588,8 @@ sv_status sv_tree_attention(const sv_cache* c, int layer, const void* q, int64_t
 /*
  * sv_tree_attention4 -- sv_tree_attention over a cache held in 4 bits: the same arguments, masks, errors and outputs, with the
  * values that the pool's codes stand for as keys and values (they have at most six significant bits, and enter the products
- * exactly).  Slots past a sequence's length, or outside every node's window, may hold anything, scales that are NaN included.
+ * exactly).  Softmax weights are rounded to float16 for the product with v, by 2^-12 of themselves or 2^-29 of the row's largest at
+ * most, and o is divided by their sum before rounding.  Slots past a sequence's length, or outside every node's window, may hold anything, scales that are NaN included.
  * Workspace: sv_attention4_workspace_size(c, q_heads), zero-filled once before its first use.
  */
 size_t sv_attention4_workspace_size(const sv_cache4* c, int q_heads);

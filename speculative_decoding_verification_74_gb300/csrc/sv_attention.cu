@@ -40,7 +40,7 @@
 // A cache in 4 bits (kFour) with more rows than sv_attention4.cu's tiles: one warp copies a tile's codes into a ring of their
 // own, and four more warps turn them into the stages' K and V, as float16 (exact: a code times its scale has six bits), and Q
 // into float16 rows scaled by powers of two.  S and P V are issued by two warps; the one that brings Q finds the segments for all.
-// The rest is the same, with P in float16.  Whole warpgroups share out the registers.
+// The rest is the same, with P in float16, 2^7 to 2^15 at a row's maximum.  Whole warpgroups share out the registers.
 // Measured (as above, bytes in 4 bits in brackets): 64 trees 108.5 us (28), four chains 250 us (78; their products padded to 128
 // rows 126).  A tile takes 1.2 us however few its bytes: a warp's decoding 2100 clocks of 2300, the softmax of a group 1900, the
 // products 1100, and half of the issue slots are used; a row tile's beginning and end 6 us.
@@ -88,6 +88,9 @@ struct Columns {
   static __device__ __forceinline__ constexpr uint32_t p(uint32_t g) { return kOwnP ? 384 + g * 64 : g * 128 + 64; }
 };
 constexpr float kLazyGrowth = 8.0f;        // log2 units by which a maximum may grow without a rescale of O
+// In 4 bits P is float16: m lies this far below the maximum, so P is 2^kBias there, 2^(kBias + kLazyGrowth) at most (float16 ends
+// at 2^16), and the many small weights beside a large one, which float16 has no bits for below 2^-25, are kept down to 2^-32 of it.
+constexpr float kBias = 7.0f;
 constexpr int kJoinRows = 16;              // rows per CTA of the join
 // What a row tile costs besides its cache tiles, in those: its masked tiles and its end, about 4 us against 1.5 a tile
 // (64 trees over 512 to 4096 slots 126 us at 0, 114 at 2, 3 and 4; the window's 33 trees 55.5, 40.7, 40.6 and 41.2).
@@ -931,13 +934,14 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
           }
           if (!whole) tmem_wait_store();
           const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * c;  // c > 0
+          const float now = kFour ? top - kBias : top;
           if (j < 2) {
-            m = top;
+            m = now;
           } else {
-            const bool grow = top > m + kLazyGrowth || (m == -INFINITY && top > -INFINITY);
+            const bool grow = now > m + kLazyGrowth || (m == -INFINITY && now > -INFINITY);
             if (__any_sync(0xFFFFFFFFu, grow)) {
-              const float keep = grow ? (m == -INFINITY ? 0.0f : ex2_approx(m - top)) : 1.0f;
-              if (grow) m = top;
+              const float keep = grow ? (m == -INFINITY ? 0.0f : ex2_approx(m - now)) : 1.0f;
+              if (grow) m = now;
               l *= keep;
               lr *= keep;
               // the group's O is complete up to its tile before
@@ -975,7 +979,7 @@ __global__ void __launch_bounds__(Warps<kFour>::kThreads, 1)
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, off2), e0, e1);
               e0 = ex2_approx(e0);
               e1 = ex2_approx(e1);
-              // (a float16 is off by 2^-12 at most: its weights are divided by the sum before rounding)
+              // (a float16 is off by 2^-12 of itself, below 2^-14 by 2^-25: o is divided by the sum before rounding)
               const uint32_t w = kFour ? pack_f16(e0, e1) : pack_bf16(e0, e1);
               sum[(i >> 1) & 1] = f2_add(sum[(i >> 1) & 1], f2_pack(e0, e1));
               if (!kFour) sumr[(i >> 1) & 1] = f2_add(sumr[(i >> 1) & 1], f2_pack(bf16_lo(w), bf16_hi(w)));

@@ -336,17 +336,14 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(Pool p, int32_t* tab
     } else {
       rank = block_scan(drops ? count_free<true>(p) : free_pages, buf, &found);
     }
-    if (total > found) {
-      problem = SV_DEV_OUT_OF_PAGES;
-      if (drops)
-        each_entry([&](int page) {
-          if (page < p.pages) atomicAdd(p.refs + page, 1);
-        });
-    } else if (too_often) {
+    if (total > found) problem = SV_DEV_OUT_OF_PAGES;
+    if (too_often || (problem != 0 && drops)) {
       each_entry([&](int page) {
-        if (page < p.pages) atomicMax(p.refs + page, 0);
+        if (page >= p.pages) return;
+        if (problem != 0) atomicAdd(p.refs + page, 1);
+        else atomicMax(p.refs + page, 0);
       });
-      if (threadIdx.x == 0) atomicOr(status, SV_DEV_BAD_PAGE);
+      if (threadIdx.x == 0 && too_often) atomicOr(status, SV_DEV_BAD_PAGE);
       __syncthreads();
     }
     if (problem == 0 && total > 0) {

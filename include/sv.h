@@ -606,7 +606,8 @@ sv_status sv_tree_attention4(const sv_cache4* c, int layer, const void* q, int64
  *   total(w, v) = scores[w] + (x_wv - log sum_u exp x_wu);  a beam with finished[i W + w] != 0 (finished nullable) has one
  *   candidate instead, the token `pad` at total = scores[w] (its logits are not looked at)
  * Totals of -inf are no candidates.  Outputs, K per request, in the order (total desc, beam asc, token asc), as if in exact
- * arithmetic but for totals that 64 bits cannot tell apart; within a beam the order is that of the logits:
+ * arithmetic but for totals of different beams that lie within 2^-25 of each other without being equal, or that 64 bits cannot tell
+ * apart; beams with equal scores and logits tie, wherever the logits lie; within a beam the order is that of the logits:
  * out_scores float32, out_rows int32 (i W + w, what sv_cache_reorder takes for K = W), out_tokens int32.  Places past the last
  * candidate get -inf, -1, -1.  With K = W out_scores may be scores.  A NaN or +inf among the scores of a request, or the logits of a beam that is not finished and whose
  * score is not -inf: the request's outputs are NaN, -1, -1 (SV_DEV_BAD_LOGIT).

@@ -24,10 +24,11 @@
 // of the first in the lower half of the (copy's) rows and the lower 64 dimensions, those of the second in the upper ones,
 // zeros elsewhere; of O each row's own 64 columns count.  The products do the work of 128 dimensions on as many bytes.
 //
-// Measured (GB300, 32 query and 8 key/value heads of 128, graph replay; a copy of the cache's bytes in brackets): 64 requests
-// of one token over 6k to 8k slots 281 to 287 us (275), 64 trees of up to 16 nodes over 512 to 4096 slots 113 us (92), four
-// chains of 17 over 99k to 131k slots 286 to 293 us (278); a window of 1024 with 16 heads of 64, 33 trees 38 us (19); four
-// requests of one token and up to 130 slots 10.9 us.  Long contexts are bound by memory.  A row tile's masked tiles and
+// Measured (GB300, 32 query and 8 key/value heads of 128; a copy of the cache's bytes in brackets; one call after the other, and a
+// graph of one call replayed, whose start takes some 4 us): 64 requests of one token over 6k to 8k slots 279 and 289 us (275), 64
+// trees of up to 16 nodes over 512 to 4096 slots 112 and 117 us (92), four chains of 17 over 99k to 131k slots 283 and 295 us
+// (278); a window of 1024 with 16 heads of 64, 33 trees 39 and 43 us (19); four requests of one token and up to 130 slots 11.8 and
+// 14.4 us.  Long contexts are bound by memory.  A row tile's masked tiles and
 // end cost about 4 us besides its tiles (1.5 us each), which short contexts feel; a call's launches, first tile and join
 // about 11 us.
 //
@@ -41,7 +42,7 @@
 // own, and four more warps turn them into the stages' K and V, as float16 (exact: a code times its scale has six bits), and Q
 // into float16 rows scaled by powers of two.  S and P V are issued by two warps; the one that brings Q finds the segments for all.
 // The rest is the same, with P in float16, 2^7 to 2^15 at a row's maximum.  Whole warpgroups share out the registers.
-// Measured (as above, bytes in 4 bits in brackets): 64 trees 108.5 us (28), four chains 250 us (78; their products padded to 128
+// Measured (graph replay, bytes in 4 bits in brackets): 64 trees 108 us (28), four chains 250 us (78; their products padded to 128
 // rows 126).  A tile takes 1.2 us however few its bytes: a warp's decoding 2100 clocks of 2300, the softmax of a group 1900, the
 // products 1100, and half of the issue slots are used; a row tile's beginning and end 6 us.
 #include <cuda.h>
@@ -95,7 +96,7 @@ constexpr int kJoinRows = 16;              // rows per CTA of the join
 // What a row tile costs besides its cache tiles, in those: its masked tiles and its end, about 4 us against 1.5 a tile
 // (64 trees over 512 to 4096 slots 126 us at 0, 114 at 2, 3 and 4; the window's 33 trees 55.5, 40.7, 40.6 and 41.2).
 constexpr int kExtra = 3;
-constexpr int kMixFloat4 = 768;            // (a fifth stage still fits)
+constexpr int kMixFloat4 = 768;            // (a fifth stage of 128 dimensions still fits)
 constexpr int kMixFloat4Of4 = 512;         // in 4 bits: at most two copies
 // A cache in 4 bits: one warp copies a tile's codes into a ring of their own, and four decode them, each a quarter of its slots,
 // eight at a time.  (Sixteen: 64 trees 123 us against 113; the roles' code together has to fit into the instruction cache.)
@@ -1314,8 +1315,9 @@ cudaError_t launch_attention(AttendParams& a, const CUtensorMap& q_map, const CU
     fixed += a.raw_stages * kRawBytes;
   }
   a.stages = std::min(kMaxStages, (kSmemMax - kStatic - fixed) / kStageBytes);
-  // With an even number of stages K and V keep to their own.  Where S does not wait for the product P V of two tiles before, the V
-  // warp could otherwise take an earlier emptying of a stage for its K's.  (33 trees, window 1024: 42.5 us with 4, 43.0 with 5.)
+  // With an even number of stages K and V keep to their own.  Where S does not wait for the product P V of two tiles before (tiles
+  // of 64 dimensions), the V warp could otherwise take an earlier emptying of a stage for its K's.  Pairs of heads, whose S waits,
+  // go by it too: a fifth stage is no gain there (33 trees, window 1024: 42.5 us with 4, 43.0 with 5).
   if (Columns<D>::kOwnP && a.stages > 3) a.stages &= ~1;
   const size_t dyn = static_cast<size_t>(fixed) + static_cast<size_t>(a.stages) * kStageBytes;
   cudaError_t e = allow_smem<attend_kernel<D, kPair, kCopies, kFour>>(kSmemMax - kStatic);

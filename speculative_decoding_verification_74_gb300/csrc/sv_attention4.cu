@@ -25,7 +25,7 @@
 //
 // Measured (GB300, 32 query and 8 key/value heads of 128, graph replay; a copy of the bytes read in brackets): 64 requests of one
 // token over 6k to 8k slots 110 us (77), four of up to 130 slots 14.4 us; a window of 1024 with 16 heads of 64, 33 trees of up to
-// 16 nodes 43 us (6).  A chunk takes 640 instructions, of them 256 that turn codes into products' operands; with 16 warps of 128
+// 16 nodes 44 us (6).  A chunk takes 640 instructions, of them 256 that turn codes into products' operands; with 16 warps of 128
 // registers 62% of the issue slots are used and as much of the memory's pace.  Short calls are latency: two launches, the line's
 // scan, a row tile's chain.
 #include <cuda_bf16.h>

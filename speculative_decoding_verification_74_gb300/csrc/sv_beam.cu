@@ -19,11 +19,11 @@
 // and the ranking is repeated.  With this the order is that of the exact totals where those of two beams differ by 2^-25 (each
 // term is off by 2^-30 of itself and 2^-45, V of them by 2^-27), and that of beams where they are equal.
 //
-// Measured (GB300, graph replay; a copy of the logits in brackets): 1024 rows of 151936, K = 8, float32 125 us (92), bf16 79 (46);
-// of 64 requests of 16 beams a quarter with one beam only, K = 32, bf16 61 (35: rows of missing beams are not read); 64 rows
-// float32 19 us (6), four rows of 32000 bf16 14 us.  Of the 79, the stream takes 55, looking for candidates 13, all CTAs at about
-// the same time, and the merge 10.  Where two beams' totals lie near each other (one request of 32 candidates in 300), summing
-// their rows again takes another 80 us.
+// Measured (GB300, graph replay; a copy of the logits in brackets): 256 requests of four rows of 151936, K = 8, float32 123 us (92),
+// bf16 77 (46); of 64 requests of 16 beams a quarter with one beam only, K = 32, bf16 62 (35: rows of missing beams are not read);
+// 64 rows float32 20 us (6), four rows of 32000 bf16 14 to 16 us.  Of the 77, the stream takes 55, looking for candidates 12, all
+// CTAs at about the same time, and the merge 10.  Where two beams' totals lie near each other (one request of 32 candidates in
+// 300), summing their rows again takes another 55 to 80 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
